@@ -54,7 +54,16 @@ typedef enum pkv_status {
     PKV_ESTALE = -5         /* descriptors that do not describe the same cache shape */
 } pkv_status;
 
-typedef enum pkv_dtype { PKV_BF16 = 0, PKV_F32 = 1 } pkv_dtype;
+/*
+ * PKV_FP4 is a cache format: K and V values are e2m1 numbers times a scale
+ * shared by 16 consecutive head_dim columns of a token and kv head, 4.5 bits
+ * a value.  The scale is an unsigned 8-bit float s of 5 exponent (bias 15)
+ * and 3 mantissa bits, the nearest one to max|x| / 6 (ties to even, at most
+ * 10240); the code is the nearest e2m1 number to x / s (ties to even, 0 where
+ * s is 0, the sign kept).  A group that holds a NaN reads back as NaN, an
+ * infinity as its scale's largest value.  Rows (q, k_new, v_new) are bf16.
+ */
+typedef enum pkv_dtype { PKV_BF16 = 0, PKV_F32 = 1, PKV_FP4 = 2 } pkv_dtype;
 
 /* Device-side error bits, OR-ed into *err_flags. */
 #define PKV_ERR_SEGMENT  (1u << 0)  /* q_start/q_len/col/kv_end out of range, or kv_end < q_len */
@@ -70,6 +79,7 @@ typedef enum pkv_dtype { PKV_BF16 = 0, PKV_F32 = 1 } pkv_dtype;
 #define PKV_FLAG_PDL   (1u << 1)  /* launch with programmatic dependent launch; see pkv_attend_varlen */
 #define PKV_FLAG_PREFETCH_NEXT (1u << 2)  /* warm L2 with layer + 1's pages; see pkv_attend_varlen */
 #define PKV_FLAG_MMA_SYNC (1u << 3)  /* bf16, head_dim 128, > 8 rows per kv head: mma.sync tile instead of tcgen05 */
+#define PKV_FLAG_OUT_BF16 (1u << 4)  /* PKV_FP4 caches: out is bf16 (it is fp32 otherwise) */
 
 /*
  * One paged K/V cache: per layer, a K pool and a V pool, each
@@ -85,6 +95,18 @@ typedef enum pkv_dtype { PKV_BF16 = 0, PKV_F32 = 1 } pkv_dtype;
  * attention: position p lives at slot p % R ([ExecuTorch #24074]), and a
  * window of W keys with steps of up to q_len rows needs
  * R >= W + q_len - 1 ([ExecuTorch #24073]).
+ *
+ * A PKV_FP4 cache has head_dim 64, 128 or 256 (D below), and pools of bytes,
+ * (num_blocks, kv_heads, 9 * D): 8 * D bytes of codes of the page's 16 tokens,
+ * then D bytes of scales.  In a K block the code of (token, column) is in byte
+ * token * D / 2 + column / 2 (even columns in the low nibble) and its scale at
+ * 8 * D + token * D / 16 + column / 16.  In a V block, with token = 8 * hi +
+ * 2 * t + n and column = g * D / 8 + 8 * p + i, it is in byte 512 * p +
+ * 16 * (4 * g + t) + 2 * i + hi, nibble n, and its scale at 8 * D +
+ * 4 * (4 * (column / 16) + t) + 2 * hi + n.  The append and attention calls,
+ * pkv_rewind, pkv_advance and pkv_seqinfo_from_seqused take such caches; the
+ * copying calls (pkv_seq_clone, pkv_resize_bucket, pkv_load_prefix,
+ * pkv_to_contiguous) return PKV_EUNSUPPORTED for them.
  *
  * The descriptor is host memory owned by the caller; k and v are host arrays
  * of num_layers device pointers (16-byte aligned).  bucket is the token
@@ -152,11 +174,104 @@ const char *pkv_status_str(int status);
  * PKV_ERR_* bit is set.  Rows no segment covers are not written.  Two
  * segments that write the same slot race (unspecified result).
  * err_flags: device uint32, OR-ed, never cleared by the library.
+ *
+ * On a PKV_FP4 cache the rows are bf16 and are quantised on the way (this is
+ * pkv_norm_rope_append without a pkv_rope and without q).
  */
 int pkv_append(const pkv_cache *cache, int32_t layer,
                const void *k_new, const void *v_new, int32_t total_rows,
                const int32_t *seq_info, int32_t num_segments, int32_t window,
                uint32_t *err_flags, void *stream);
+
+/* Frequency scalings of pkv_rope_inv_freq. */
+enum {
+    PKV_ROPE_PLAIN = 0,   /* theta^(-2 i / rot_dim) */
+    PKV_ROPE_LINEAR = 1,  /* positions divided by factor */
+    PKV_ROPE_NTK = 2,     /* theta * factor^(rot_dim / (rot_dim - 2)) in place of theta */
+    PKV_ROPE_YARN = 3     /* YaRN: fast pairs kept, slow ones divided by factor, a linear ramp between */
+};
+
+/*
+ * Rotary frequencies (radians a position) of rot_dim / 2 column pairs, in
+ * inv_freq[rot_dim / 2], and the factor on the sines and cosines that goes with them
+ * in *mscale (1, or 0.1 ln(factor) + 1 with YaRN).  factor >= 1;
+ * trained_len (the context the model was trained on), beta_fast > beta_slow >
+ * 0 (turns in that context above which a pair is kept and below which it is
+ * stretched; 32 and 1 are usual) are read with YaRN only.  Host only.
+ */
+int pkv_rope_inv_freq(int32_t rot_dim, double theta, int32_t scaling, double factor, double trained_len,
+                      double beta_fast, double beta_slow, double *inv_freq, double *mscale);
+
+/*
+ * turns[i] = inv_freq[i] / (2 pi) as a fraction of a turn, in units of 2^-64:
+ * the form the kernels read (position * turns, modulo 2^64, is the angle at
+ * any position).  Host only; the caller copies the array to the device.
+ */
+int pkv_rope_turns(const double *inv_freq, int32_t n, uint64_t *turns);
+
+/*
+ * What is done to a q or k head: y = x * rsqrt(mean(x^2) + eps) * weight
+ * where there is a weight, then the first rot_dim columns are rotated by
+ * angle a_i = position * frequency i:
+ *   (u, w) -> mscale * (u cos a_i - w sin a_i, w cos a_i + u sin a_i)
+ * for column pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved.
+ * All in fp32, rounded once at the end.  Host struct, device pointers.
+ */
+typedef struct pkv_rope {
+    const uint64_t *turns;      /* device [rot_dim / 2], from pkv_rope_turns; unread if rot_dim is 0 */
+    int32_t rot_dim;            /* even, 0 (no rotation) .. head_dim */
+    int32_t interleaved;        /* 0 or 1 */
+    float mscale;               /* on the rotated columns */
+    float eps;
+    const void *q_weight;       /* device [head_dim] of the rows' type (16-byte aligned), or NULL: q is not normalised */
+    const void *k_weight;       /* the same for k */
+} pkv_rope;
+
+/*
+ * This step's rows.  Strides are in elements from one row to the next (at
+ * least heads * head_dim, a multiple of 16 bytes), heads of a row are
+ * contiguous; q, k and v may be slices of one projection output.  Pointers are
+ * 16-byte aligned device memory.  An output may be its own input (same
+ * pointer and stride); no other overlap.
+ */
+typedef struct pkv_rows {
+    const void *q, *k, *v;
+    void *q_out, *k_out, *v_out;
+    int64_t q_stride, k_stride, v_stride;
+    int64_t q_out_stride, k_out_stride, v_out_stride;
+    int32_t q_heads;
+    int32_t total_rows;
+    const int32_t *positions;   /* device [total_rows], the angles' positions, or NULL */
+} pkv_rows;
+
+/*
+ * Norm and rotation of rows that go to no cache: q to q_out and k to k_out
+ * (either pair may be NULL with q_heads or kv_heads 0), rows of dtype
+ * PKV_BF16 or PKV_F32.  v and v_out must be NULL; positions may be NULL only
+ * with rot_dim 0.  head_dim: a multiple of 8, at most 256.
+ */
+int pkv_norm_rope(const pkv_rope *rope, int32_t dtype, int32_t head_dim, int32_t kv_heads,
+                  const pkv_rows *rows, void *stream);
+
+/*
+ * Norm, rotation and append in one pass: for each row of a segment, q goes to
+ * q_out (q NULL with q_heads 0: no queries), k after norm and rotation and v
+ * as it is go to the row's cache slot, as pkv_append places and checks them.
+ * rope NULL: rows as they are.  The angles' positions are positions[row], or the
+ * row's position in the cache (kv_end - q_len + i).  k_out and v_out
+ * (optional) get the rows as the cache now holds them; with a PKV_FP4 cache
+ * those are the quantised values (k is rounded to bf16 before it is
+ * quantised).  Rows are of the cache's dtype (PKV_FP4: bf16).
+ *
+ * A row belongs to one segment at most (in two it is unspecified which of
+ * them places it).  Rows no segment covers, and rows of segments that
+ * pkv_append would refuse (the same PKV_ERR_* bits), are not written, in
+ * none of the outputs.  A later attention call may be launched with
+ * PKV_FLAG_PDL behind this one.
+ */
+int pkv_norm_rope_append(const pkv_cache *cache, int32_t layer, const pkv_rope *rope, const pkv_rows *rows,
+                         const int32_t *seq_info, int32_t num_segments, int32_t window,
+                         uint32_t *err_flags, void *stream);
 
 /*
  * Decode attention over the paged cache ([ExecuTorch #24072]
@@ -211,7 +326,17 @@ int pkv_append(const pkv_cache *cache, int32_t layer,
  * segments (one decode step): a hint only, it changes no result.  The
  * prefetch is capped at about 48 MB per call.
  *
- * Device pointers must be 16-byte aligned (out and lse: 4-byte).
+ * On a PKV_FP4 cache q is bf16 and out is fp32, or bf16 with
+ * PKV_FLAG_OUT_BF16.  Scores are those of the stored values to fp32; the
+ * softmax weights are rounded to fp16 for the product with V.  A NaN in V
+ * reaches only the rows that see its key.  The splits always form a cluster
+ * (num_splits 0..16, workspace ignored); PKV_FLAG_SIMT, PKV_FLAG_MMA_SYNC and
+ * PKV_FLAG_PREFETCH_NEXT have no effect.  PKV_FLAG_PDL: pages wholly below
+ * position kv_end - q_len may be read before the previous kernel has
+ * finished, so it may be the append of this step.
+ *
+ * Device pointers must be 16-byte aligned (out and lse: 4-byte; with a
+ * PKV_FP4 cache out: 16-byte).
  */
 int pkv_attend_varlen(const pkv_cache *cache, int32_t layer,
                       const void *q, int32_t num_q_heads, int32_t total_rows,
@@ -227,7 +352,8 @@ int pkv_attend_varlen(const pkv_cache *cache, int32_t layer,
  * step are written into the cache and attended to from k_new / v_new
  * directly.  Same arguments and results as the two calls in sequence, with
  * one extra condition: no two segments of the call may name the same `col`
- * (the two-call sequence has no such limit).
+ * (the two-call sequence has no such limit).  On a PKV_FP4 cache it is the two
+ * calls, one launch each.
  */
 int pkv_append_attend(const pkv_cache *cache, int32_t layer,
                       const void *q, const void *k_new, const void *v_new,
@@ -241,7 +367,7 @@ int pkv_append_attend(const pkv_cache *cache, int32_t layer,
 
 /*
  * Bytes of workspace the two calls above need for these launch bounds when
- * given one (0: the launch never uses it).  With a workspace, the decode
+ * given one (0: the launch never uses it; always so with a PKV_FP4 cache).  With a workspace, the decode
  * kernel (at most 8 query rows per segment and kv head: G * max_q_len <= 8,
  * bf16, tensor-core path) splits a key range over independent CTAs (up to 64
  * per range, num_splits 0..64) that merge through it: each writes its

@@ -15,11 +15,13 @@ LIB_PATH = os.path.join(HERE, "libpkv.so")
 OK, EMPTY, SAME_BUCKET = 0, 1, 2
 EINVAL, EUNSUPPORTED, ECUDA, ECAPACITY, ESTALE = -1, -2, -3, -4, -5
 # pkv_dtype
-BF16, F32 = 0, 1
+BF16, F32, FP4 = 0, 1, 2
+# frequency scalings
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 # device error bits
 ERR_SEGMENT, ERR_CAPACITY, ERR_RING, ERR_BLOCK, ERR_QLEN, ERR_OVERLAP, ERR_TIMEOUT = 1, 2, 4, 8, 16, 32, 64
 # attention flags
-FLAG_SIMT, FLAG_PDL, FLAG_PREFETCH_NEXT, FLAG_MMA_SYNC = 1, 2, 4, 8
+FLAG_SIMT, FLAG_PDL, FLAG_PREFETCH_NEXT, FLAG_MMA_SYNC, FLAG_OUT_BF16 = 1, 2, 4, 8, 16
 BLOCK_SIZE = 16
 
 
@@ -45,10 +47,48 @@ class CacheDesc(ctypes.Structure):
     ]
 
 
+class RopeDesc(ctypes.Structure):
+    """Mirror of ``struct pkv_rope`` in include/pkv.h."""
+
+    _fields_ = [
+        ("turns", ctypes.c_void_p),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("mscale", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+    ]
+
+
+class RowsDesc(ctypes.Structure):
+    """Mirror of ``struct pkv_rows`` in include/pkv.h."""
+
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p),
+        ("v_out", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64),
+        ("k_out_stride", ctypes.c_int64),
+        ("v_out_stride", ctypes.c_int64),
+        ("q_heads", ctypes.c_int32),
+        ("total_rows", ctypes.c_int32),
+        ("positions", ctypes.c_void_p),
+    ]
+
+
 def _declare(lib):
     i32, i64, u32, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
     p = ctypes.c_void_p
+    f64 = ctypes.c_double
     cp = ctypes.POINTER(CacheDesc)
+    rp, wp = ctypes.POINTER(RopeDesc), ctypes.POINTER(RowsDesc)
     sigs = {
         "pkv_bucket_for": (i64, [i64]),
         "pkv_status_str": (ctypes.c_char_p, [ctypes.c_int]),
@@ -57,6 +97,10 @@ def _declare(lib):
                                              p, p, p, i64, p, u32, p]),
         "pkv_append_attend": (ctypes.c_int, [cp, i32, p, p, p, i32, i32, p, i32, i32, i64, i32, f32, i32,
                                              i32, p, p, p, i64, p, u32, p]),
+        "pkv_rope_inv_freq": (ctypes.c_int, [i32, f64, i32, f64, f64, f64, f64, p, p]),
+        "pkv_rope_turns": (ctypes.c_int, [p, i32, p]),
+        "pkv_norm_rope": (ctypes.c_int, [rp, i32, i32, i32, wp, p]),
+        "pkv_norm_rope_append": (ctypes.c_int, [cp, i32, rp, wp, p, i32, i32, p, p]),
         "pkv_attend_workspace_bytes": (i64, [cp, i32, i32, i32, i64, i32, u32]),
         "pkv_append_attend_noalloc": (ctypes.c_int, [cp, i32, p, p, p, i32, i32, p, i32, i32, i64, i32, f32, i32,
                                                      i32, p, p, p, u32, p]),

@@ -6,15 +6,16 @@ CUDA kernels; torch supplies device memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
-from typing import List, Optional, Sequence
+from typing import List, Optional, Sequence, Tuple
 
 import torch
 
 from . import _lib
 from ._lib import lib
 
-_DTYPES = {torch.bfloat16: _lib.BF16, torch.float32: _lib.F32}
+_DTYPES = {torch.bfloat16: _lib.BF16, torch.float32: _lib.F32, torch.uint8: _lib.FP4}
 
 
 def _stream(stream=None) -> ctypes.c_void_p:
@@ -38,7 +39,9 @@ class PagedKVCache:
     """Per-layer paged K/V pools plus one block table, and their descriptor.
 
     Pools are (num_blocks, 16, kv_heads, head_dim) tensors of bf16 or fp32
-    (the layout of vLLM-Omni's SenseNova-U1 PagedDecodeCache); the block
+    (the layout of vLLM-Omni's SenseNova-U1 PagedDecodeCache), or, for a cache
+    held in 4 bits, uint8 (num_blocks, kv_heads, 9 * head_dim) with head_dim
+    64, 128 or 256 (the page format is in include/pkv.h); the block
     table is int32 (max_seqs, max_blocks_per_seq).  first_valid, optional
     int32 (max_seqs,), is each sequence's first non-padding position for
     left-padded batches (tiny-llm kv_cache.py, SlotKVCache): the attention
@@ -57,8 +60,14 @@ class PagedKVCache:
         for t in list(k) + list(v):
             if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError("every pool must be contiguous with the same shape and dtype")
-        if len(shape) != 4 or shape[1] != _lib.BLOCK_SIZE:
-            raise ValueError("pools are (num_blocks, 16, kv_heads, head_dim)")
+        if dtype == torch.uint8:
+            if len(shape) != 3 or shape[2] % 9:
+                raise ValueError("4-bit pools are uint8 (num_blocks, kv_heads, 9 * head_dim)")
+            kv_heads, head_dim = int(shape[1]), int(shape[2]) // 9
+        else:
+            if len(shape) != 4 or shape[1] != _lib.BLOCK_SIZE:
+                raise ValueError("pools are (num_blocks, 16, kv_heads, head_dim)")
+            kv_heads, head_dim = int(shape[2]), int(shape[3])
         if block_table.dtype != torch.int32 or block_table.dim() != 2:
             raise ValueError("block_table is int32 (max_seqs, max_blocks_per_seq)")
         self.k: List[torch.Tensor] = list(k)
@@ -75,7 +84,7 @@ class PagedKVCache:
         self._kp = (ctypes.c_void_p * len(k))(*[t.data_ptr() for t in self.k])
         self._vp = (ctypes.c_void_p * len(v))(*[t.data_ptr() for t in self.v])
         self.desc = _lib.CacheDesc(
-            num_layers=len(k), kv_heads=shape[2], head_dim=shape[3], dtype=_DTYPES[dtype], num_blocks=nb,
+            num_layers=len(k), kv_heads=kv_heads, head_dim=head_dim, dtype=_DTYPES[dtype], num_blocks=nb,
             max_seqs=block_table.shape[0], max_blocks_per_seq=block_table.shape[1], ring_rows=self.ring_rows,
             reserved0=0, k=ctypes.cast(self._kp, ctypes.c_void_p), v=ctypes.cast(self._vp, ctypes.c_void_p),
             block_table=block_table.data_ptr(), bucket=self.bucket, generation=self.generation,
@@ -84,9 +93,9 @@ class PagedKVCache:
     @classmethod
     def allocate(cls, num_layers: int, kv_heads: int, head_dim: int, bucket: int, dtype=torch.bfloat16,
                  device="cuda", generation: int = 0) -> "PagedKVCache":
-        """Zeroed single-sequence cache behind an identity table (one bucket)."""
+        """Zeroed single-sequence cache behind an identity table (one bucket); dtype torch.uint8: held in 4 bits."""
         nb = (bucket + _lib.BLOCK_SIZE - 1) // _lib.BLOCK_SIZE
-        shape = (nb, _lib.BLOCK_SIZE, kv_heads, head_dim)
+        shape = (nb, kv_heads, 9 * head_dim) if dtype == torch.uint8 else (nb, _lib.BLOCK_SIZE, kv_heads, head_dim)
         k = [torch.zeros(shape, dtype=dtype, device=device) for _ in range(num_layers)]
         v = [torch.zeros(shape, dtype=dtype, device=device) for _ in range(num_layers)]
         bt = torch.arange(nb, dtype=torch.int32, device=device).unsqueeze(0)
@@ -98,15 +107,20 @@ class PagedKVCache:
 
     @property
     def kv_heads(self) -> int:
-        return int(self.k[0].shape[2])
+        return int(self.desc.kv_heads)
 
     @property
     def head_dim(self) -> int:
-        return int(self.k[0].shape[3])
+        return int(self.desc.head_dim)
 
     @property
     def dtype(self) -> torch.dtype:
         return self.k[0].dtype
+
+    @property
+    def row_dtype(self) -> torch.dtype:
+        """The type of q, k_new and v_new rows: the cache's, bf16 for a 4-bit cache."""
+        return torch.bfloat16 if self.dtype == torch.uint8 else self.dtype
 
     def ref(self):
         return ctypes.byref(self.desc)
@@ -125,6 +139,154 @@ def new_err_flags(device="cuda") -> torch.Tensor:
     return torch.zeros(1, dtype=torch.int32, device=device)
 
 
+@contextlib.contextmanager
+def _on(device: torch.device):
+    """Launches go to the tensors' device, whichever is current."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        yield
+    else:
+        with torch.cuda.device(device):
+            yield
+
+
+def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                  trained_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0) -> Tuple[torch.Tensor, float]:
+    """pkv_rope_inv_freq: (float64 frequencies on the host, factor on the sines and cosines).
+
+    scaling: "none", "linear" (positions / factor), "ntk" (a larger theta) or
+    "yarn" (by parts, from the trained context length).
+    """
+    kinds = {"none": _lib.ROPE_PLAIN, "linear": _lib.ROPE_LINEAR, "ntk": _lib.ROPE_NTK, "yarn": _lib.ROPE_YARN}
+    if scaling not in kinds:
+        raise ValueError(f"scaling is one of {sorted(kinds)}")
+    freq = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64)
+    mscale = ctypes.c_double()
+    _lib.check("pkv_rope_inv_freq", lib.pkv_rope_inv_freq(int(rot_dim), float(theta), kinds[scaling], float(factor),
+                                                          float(trained_len), float(beta_fast), float(beta_slow),
+                                                          _ptr(freq), ctypes.addressof(mscale)))
+    return freq, float(mscale.value)
+
+
+class Rope:
+    """What norm_rope and norm_rope_append do to a head: RMSNorm by a weight, then a rotation.
+
+    inv_freq: radians a position of each column pair (rot_dim = 2 *
+    len(inv_freq), at most head_dim), from rope_inv_freq or a model's own;
+    None for no rotation.  interleaved: pairs (2i, 2i + 1) instead of (i, i +
+    rot_dim / 2).  mscale multiplies the rotated columns.  q_weight /
+    k_weight: (head_dim,) of the rows' type, or None for no norm of that
+    side.  Made once per model or layer; it keeps its tensors.
+    """
+
+    def __init__(self, inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False, mscale: float = 1.0,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 device=None):
+        self.turns = None
+        n = 0
+        if inv_freq is not None:
+            if inv_freq.dim() != 1 or inv_freq.numel() == 0:
+                raise ValueError("inv_freq is (rot_dim / 2,)")
+            n = int(inv_freq.numel())
+            host = inv_freq.detach().to("cpu", torch.float64).contiguous()
+            turns = torch.empty(n, dtype=torch.int64)
+            _lib.check("pkv_rope_turns", lib.pkv_rope_turns(_ptr(host), n, _ptr(turns)))
+            if device is None:
+                device = inv_freq.device if inv_freq.is_cuda else "cuda"
+            self.turns = turns.to(device)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None and (w.dim() != 1 or w.dtype not in (torch.bfloat16, torch.float32)):
+                raise ValueError(f"{name} is (head_dim,) of bf16 or fp32")
+        self.q_weight = None if q_weight is None else _contig(q_weight, "q_weight")
+        self.k_weight = None if k_weight is None else _contig(k_weight, "k_weight")
+        self.rot_dim, self.interleaved, self.mscale, self.eps = 2 * n, bool(interleaved), float(mscale), float(eps)
+        self.desc = _lib.RopeDesc(turns=_ptr(self.turns), rot_dim=self.rot_dim, interleaved=int(self.interleaved),
+                                  mscale=self.mscale, eps=self.eps, q_weight=_ptr(self.q_weight),
+                                  k_weight=_ptr(self.k_weight))
+
+    def check(self, dtype: torch.dtype, head_dim: int, device: torch.device) -> None:
+        if self.rot_dim > head_dim:
+            raise ValueError(f"rot_dim {self.rot_dim} is above head_dim {head_dim}")
+        if self.turns is not None and self.turns.device != device:
+            raise ValueError("the frequencies are on another device than the rows")
+        for w in (self.q_weight, self.k_weight):
+            if w is not None and (w.dtype != dtype or w.numel() != head_dim or w.device != device):
+                raise ValueError("norm weights are (head_dim,) of the rows' type, on their device")
+
+
+def _row_stride(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dtype, device) -> int:
+    """Elements between the rows of (rows, heads, dim); heads and columns contiguous, rows apart as they like."""
+    if t.shape != (rows, heads, dim) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} is ({rows}, {heads}, {dim}) of {dtype} on {device}")
+    s0, s1, s2 = t.stride()
+    if (dim > 1 and s2 != 1) or (heads > 1 and s1 != dim):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return s0 if rows > 1 else max(s0, heads * dim)
+
+
+def _rows_desc(q, k, v, q_out, k_out, v_out, positions, kv_heads, head_dim, dtype, device) -> _lib.RowsDesc:
+    some = q if q is not None else k
+    rows = int(some.shape[0])
+    hq = int(q.shape[1]) if q is not None and q.dim() == 3 else 0
+    d = _lib.RowsDesc(q_heads=hq, total_rows=rows)
+    for name, t, heads in (("q", q, hq), ("k", k, kv_heads), ("v", v, kv_heads), ("q_out", q_out, hq),
+                           ("k_out", k_out, kv_heads), ("v_out", v_out, kv_heads)):
+        if t is not None:
+            setattr(d, name + "_stride", _row_stride(t, name, rows, heads, head_dim, dtype, device))
+            setattr(d, name, t.data_ptr())
+    if positions is not None:
+        if positions.shape != (rows,) or positions.dtype != torch.int32 or positions.device != device:
+            raise ValueError(f"positions is int32 ({rows},) on {device}")
+        d.positions = _contig(positions, "positions").data_ptr()
+    return d
+
+
+def norm_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+              q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pkv_norm_rope: norm and rotation of rows that go to no cache.
+
+    q (rows, q_heads, head_dim) and k (rows, kv_heads, head_dim), bf16 or fp32,
+    either may be None; rows may be strided (a slice of a projection's output).
+    Without q_out / k_out the rows are changed in place.
+    """
+    some = q if q is not None else k
+    if some is None or some.dim() != 3:
+        raise ValueError("q or k is (rows, heads, head_dim)")
+    if some.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"unsupported dtype {some.dtype}")
+    dim, dtype, dev = int(some.shape[2]), some.dtype, some.device
+    rope.check(dtype, dim, dev)
+    kv = int(k.shape[1]) if k is not None and k.dim() == 3 else 0
+    d = _rows_desc(q, k, None, q_out if q_out is not None else q, k_out if k_out is not None else k, None, positions, kv, dim,
+                   dtype, dev)
+    with _on(dev):
+        _lib.check("pkv_norm_rope", lib.pkv_norm_rope(ctypes.byref(rope.desc), _DTYPES[dtype], dim, kv, ctypes.byref(d),
+                                                      _stream(stream)))
+
+
+def norm_rope_append(cache: PagedKVCache, layer: int, rope: Optional[Rope], q: Optional[torch.Tensor], k_new: torch.Tensor,
+                     v_new: torch.Tensor, seq_info: torch.Tensor, q_out: Optional[torch.Tensor], err: torch.Tensor,
+                     window: int = 0, positions: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                     v_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """pkv_norm_rope_append: norm and rotation of q and k, and the append of k and v, in one pass.
+
+    q goes to q_out (None: in place).  positions (rows,) int32 overrides the
+    angles' positions; by default a row's position in the cache.  k_out / v_out
+    get the rows as the cache holds them.  Rows may be strided.
+    """
+    dev = cache.k[0].device
+    if rope is not None:
+        rope.check(cache.row_dtype, cache.head_dim, dev)
+    if q is not None and q_out is None:
+        q_out = q
+    if seq_info.dtype != torch.int32 or seq_info.dim() != 2 or seq_info.shape[1] != 4 or seq_info.device != dev:
+        raise ValueError(f"seq_info is int32 (segments, 4) on {dev}")
+    d = _rows_desc(q, k_new, v_new, q_out, k_out, v_out, positions, cache.kv_heads, cache.head_dim, cache.row_dtype, dev)
+    with _on(dev):
+        _lib.check("pkv_norm_rope_append", lib.pkv_norm_rope_append(
+            cache.ref(), int(layer), None if rope is None else ctypes.byref(rope.desc), ctypes.byref(d),
+            _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(window), _ptr(err), _stream(stream)))
+
+
 def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, seq_info: torch.Tensor,
            err: torch.Tensor, window: int = 0, stream=None) -> None:
     rows = int(k_new.shape[0])
@@ -136,6 +298,8 @@ def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Te
 def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max_q_len, max_kv, scale, causal,
             window, num_splits, flags, stream, workspace):
     rows, hq = int(q.shape[0]), int(q.shape[1])
+    if out.dtype == torch.bfloat16:
+        flags |= _lib.FLAG_OUT_BF16
     args = [cache.ref(), layer, _ptr(_contig(q, "q"))]
     if fn_name == "pkv_append_attend":
         args += [_ptr(_contig(k_new, "k_new")), _ptr(_contig(v_new, "v_new"))]
@@ -169,6 +333,8 @@ def append_attend_noalloc(cache: PagedKVCache, layer: int, q: torch.Tensor, k_ne
                           stream=None) -> None:
     """pkv_append_attend_noalloc: append_attend merging its splits in the library's fixed scratch."""
     rows, hq = int(q.shape[0]), int(q.shape[1])
+    if out.dtype == torch.bfloat16:
+        flags |= _lib.FLAG_OUT_BF16
     _lib.check("pkv_append_attend_noalloc", lib.pkv_append_attend_noalloc(
         cache.ref(), layer, _ptr(_contig(q, "q")), _ptr(_contig(k_new, "k_new")), _ptr(_contig(v_new, "v_new")),
         hq, rows, _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(max_q_len), int(max_kv),

@@ -1,7 +1,8 @@
 """Build libpkv.so in-tree with nvcc for sm_103a.
 
 Nine attention translation units (three compute variants x three padded
-head_dims) and the C-ABI unit compile in parallel, then link into one shared
+head_dims), three of the 4-bit attention (one per head_dim), the norm + rotary
++ append unit and the C-ABI unit compile in parallel, then link into one shared
 library next to this file.  Objects go to ``_build/`` (git-ignored).
 """
 from __future__ import annotations
@@ -35,6 +36,9 @@ def _sources():
         for dp in (64, 128, 256):
             units.append((os.path.join(CSRC, "attend_inst.cu"), f"attend_{variant}_{dp}.o",
                           [f"-DPKV_INST_VARIANT={variant}", f"-DPKV_INST_DP={dp}"]))
+    for d in (64, 128, 256):
+        units.append((os.path.join(CSRC, "attend4_inst.cu"), f"attend4_{d}.o", [f"-DPKV_INST_D={d}"]))
+    units.append((os.path.join(CSRC, "rope.cu"), "rope.o", []))
     units.append((os.path.join(CSRC, "api.cu"), "api.o", []))
     return units
 

@@ -9,8 +9,12 @@
 #include <algorithm>
 #include <mutex>
 
+#include <math.h>
+
+#include "attend4_launch.h"
 #include "launch.h"
 #include "misc_kernels.cuh"
+#include "rope_launch.h"
 
 using namespace pkv;
 
@@ -24,11 +28,15 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int elem_bytes(int dtype) { return dtype == PKV_BF16 ? 2 : dtype == PKV_F32 ? 4 : 0; }
 
-int check_cache(const pkv_cache *c) {
+bool is_fp4(const pkv_cache *c) { return c && c->dtype == PKV_FP4; }
+
+// fp4: whether the call takes 4-bit caches.
+int check_cache(const pkv_cache *c, bool fp4 = false) {
     if (!c) return PKV_EINVAL;
-    if (c->dtype != PKV_BF16 && c->dtype != PKV_F32) return PKV_EUNSUPPORTED;
+    if (c->dtype != PKV_BF16 && c->dtype != PKV_F32 && !(fp4 && is_fp4(c))) return PKV_EUNSUPPORTED;
     // vLLM-Omni paged_decode_supported: head_dim a multiple of 8, at most 256.
     if (c->head_dim <= 0 || c->head_dim % 8 != 0 || c->head_dim > 256) return PKV_EUNSUPPORTED;
+    if (is_fp4(c) && c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return PKV_EUNSUPPORTED;
     if (c->num_layers <= 0 || c->kv_heads <= 0 || c->num_blocks <= 0) return PKV_EINVAL;
     if (c->num_blocks > INT32_MAX || c->kv_heads > 65535) return PKV_EINVAL;
     if (c->max_seqs <= 0 || c->max_blocks_per_seq <= 0) return PKV_EINVAL;
@@ -341,11 +349,170 @@ int encode_pool_pages(CUtensorMap *map, const void *pool, const pkv_cache *c) {
     return r == CUDA_SUCCESS ? PKV_OK : PKV_ECUDA;
 }
 
+// ---- 4-bit caches
+
+struct Plan4 {
+    Attend4Kernel k4;
+    AttnKernel k;  // the same kernel for the shared cluster queries
+    int G, row_tiles, ncta;
+    long long units;
+};
+
+int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_kv, int num_splits, Plan4 *pl) {
+    const int st = check_cache(c, true);
+    if (st) return st;
+    if (Hq <= 0 || Hq % c->kv_heads != 0) return PKV_EINVAL;
+    if (S < 0 || S > 65535 || max_q_len <= 0 || max_kv <= 0 || num_splits < 0 || num_splits > kMaxCluster) return PKV_EINVAL;
+    pl->G = Hq / c->kv_heads;
+    const long long rows = (long long)pl->G * max_q_len;
+    if (rows > (1 << 20)) return PKV_EINVAL;
+    pl->k4 = c->head_dim == 64 ? pick4_64((int)rows) : c->head_dim == 128 ? pick4_128((int)rows) : pick4_256((int)rows);
+    pl->k = AttnKernel{pl->k4.fn, pl->k4.threads, pl->k4.smem, pl->k4.rows, c->head_dim, true, false};
+    pl->row_tiles = (int)((rows + pl->k4.rows - 1) / pl->k4.rows);
+    if ((long long)c->kv_heads * pl->row_tiles > 65535) return PKV_EINVAL;
+    pl->units = (long long)std::max(S, 1) * c->kv_heads * pl->row_tiles;
+    const long long max_pages = (max_kv + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE + 1;
+    long long n = num_splits;
+    if (n == 0) {
+        const long long want = ((long long)kTargetWaves * device_sms() * pl->k4.ctas + pl->units - 1) / pl->units;
+        n = 1;
+        while (n < want && n < kMaxCluster) n *= 2;
+        // no more CTAs than leave each warp a few pages
+        while (n > 1 && n * pl->k4.warps * 2 > max_pages) n /= 2;
+    }
+    pl->ncta = (int)std::max<long long>(1, std::min<long long>(n, max_pages));
+    return PKV_OK;
+}
+
+int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows, const int *seq_info, int S, int max_q_len,
+            long long max_kv, int num_splits, float scale, int causal, int window, void *out, float *lse, unsigned *err,
+            unsigned flags, void *stream) {
+    Plan4 pl;
+    int st = make_plan4(c, Hq, S, max_q_len, max_kv, num_splits, &pl);
+    if (st) return st;
+    if ((st = check_layer(c, layer))) return st;
+    if (total_rows < 0 || window < 0 || (causal != 0 && causal != 1)) return PKV_EINVAL;
+    if (!err || !out || !aligned16(out) || (total_rows > 0 && (!q || !aligned16(q)))) return PKV_EINVAL;
+    if (S > 0 && (!seq_info || !aligned16(seq_info))) return PKV_EINVAL;
+    if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return PKV_EINVAL;
+    if (S == 0 && total_rows == 0) return PKV_OK;
+    if ((st = prepare_kernel(pl.k))) return st;
+    int ncta = S == 0 ? 1 : schedulable_cluster(pl.k, pl.ncta);
+    if (S > 0 && num_splits == 0) ncta = wave_cluster(pl.k, pl.units, ncta);
+    Attend4Params p;
+    p.k = reinterpret_cast<const unsigned char *>(c->k[layer]);
+    p.v = reinterpret_cast<const unsigned char *>(c->v[layer]);
+    p.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    p.block_table = c->block_table;
+    p.seq_info = reinterpret_cast<const int4 *>(seq_info);
+    p.first_valid = c->first_valid;
+    p.out = out;
+    p.lse = lse;
+    p.err = err;
+    p.num_blocks = c->num_blocks;
+    p.Hq = Hq;
+    p.Hkv = c->kv_heads;
+    p.G = pl.G;
+    p.total_rows = total_rows;
+    p.S = S;
+    p.max_seqs = c->max_seqs;
+    p.mbps = c->max_blocks_per_seq;
+    p.ring_rows = c->ring_rows;
+    p.max_q_len = max_q_len;
+    p.row_tiles = pl.row_tiles;
+    p.causal = causal;
+    p.window = window;
+    p.out_bf16 = (flags & PKV_FLAG_OUT_BF16) ? 1 : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = S == 0 ? dim3(1, 1, 1) : dim3((unsigned)ncta, (unsigned)(c->kv_heads * pl.row_tiles), (unsigned)S);
+    cfg.blockDim = dim3((unsigned)pl.k.threads);
+    cfg.dynamicSmemBytes = pl.k.smem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (ncta > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = (unsigned)ncta;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    if (flags & PKV_FLAG_PDL) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
+    cfg.attrs = na ? attr : nullptr;
+    cfg.numAttrs = (unsigned)na;
+    void *args[] = {&p};
+    return launch_status(cudaLaunchKernelExC(&cfg, pl.k.fn, args));
+}
+
+// ---- norm + rotary + append
+
+// A row argument: 16-byte aligned, rows a multiple of 16 bytes apart and at least `need` elements.
+bool rows_ok(const void *ptr, long long stride, long long need, int eb) {
+    return ptr && aligned16(ptr) && stride >= need && stride * eb % 16 == 0;
+}
+
+// Fields of the row warps, after their checks.  stored: whether v rows come too (append).
+int rope_params(const pkv_rope *rope, const pkv_rows *r, int dtype, int head_dim, int kv_heads, bool append, RopeParams *p) {
+    const int eb = dtype == PKV_F32 ? 4 : 2;
+    if (!r || r->total_rows < 0 || r->q_heads < 0 || r->q_heads > 65535) return PKV_EINVAL;
+    const long long nq = (long long)r->q_heads * head_dim, nk = (long long)kv_heads * head_dim;
+    const bool q = r->q != nullptr, k = r->k != nullptr;
+    if (r->total_rows > 0) {
+        if (q != (r->q_heads > 0) || q != (r->q_out != nullptr)) return PKV_EINVAL;
+        if (q && (!rows_ok(r->q, r->q_stride, nq, eb) || !rows_ok(r->q_out, r->q_out_stride, nq, eb))) return PKV_EINVAL;
+        if (append ? !k || !r->v : k != (r->k_out != nullptr) || r->v || r->v_out || (!q && !k)) return PKV_EINVAL;
+        if (k && !rows_ok(r->k, r->k_stride, nk, eb)) return PKV_EINVAL;
+        if (r->k_out && !rows_ok(r->k_out, r->k_out_stride, nk, eb)) return PKV_EINVAL;
+        if (append && !rows_ok(r->v, r->v_stride, nk, eb)) return PKV_EINVAL;
+        if (r->v_out && !rows_ok(r->v_out, r->v_out_stride, nk, eb)) return PKV_EINVAL;
+        if (reinterpret_cast<uintptr_t>(r->positions) & 3u) return PKV_EINVAL;
+    }
+    *p = RopeParams{};
+    if (rope) {
+        if (rope->rot_dim < 0 || rope->rot_dim > head_dim || rope->rot_dim % 2 || (rope->interleaved != 0 && rope->interleaved != 1))
+            return PKV_EINVAL;
+        if (rope->rot_dim > 0 && (!rope->turns || (reinterpret_cast<uintptr_t>(rope->turns) & 7u))) return PKV_EINVAL;
+        if (!aligned16(rope->q_weight) || !aligned16(rope->k_weight)) return PKV_EINVAL;
+        if (!append && rope->rot_dim > 0 && r->total_rows > 0 && !r->positions) return PKV_EINVAL;
+        p->turns = reinterpret_cast<const unsigned long long *>(rope->turns);
+        p->rot_dim = rope->rot_dim;
+        p->interleaved = rope->interleaved;
+        p->mscale = rope->mscale;
+        p->eps = rope->eps;
+        p->q_weight = rope->q_weight;
+        p->k_weight = rope->k_weight;
+    }
+    p->q = r->q;
+    p->k = r->k;
+    p->v = r->v;
+    p->q_out = r->q_out;
+    p->k_out = r->k_out;
+    p->v_out = r->v_out;
+    p->q_stride = r->q_stride;
+    p->k_stride = r->k_stride;
+    p->v_stride = r->v_stride;
+    p->q_out_stride = r->q_out_stride;
+    p->k_out_stride = r->k_out_stride;
+    p->v_out_stride = r->v_out_stride;
+    p->positions = r->positions;
+    p->rows = r->total_rows;
+    p->Hq = r->q_heads;
+    p->Hkv = kv_heads;
+    p->D = head_dim;
+    return PKV_OK;
+}
+
 int attend_common(const pkv_cache *c, int layer, const void *q, const void *k_new, const void *v_new,
                   int Hq, int total_rows, const int *seq_info, int S, int max_q_len, long long max_kv,
                   int num_splits, float scale, int causal, int window, float *out, float *lse,
                   void *workspace, long long workspace_bytes, unsigned *err, unsigned flags, void *stream,
                   int *counters = nullptr) {
+    if (flags & PKV_FLAG_OUT_BF16) return PKV_EUNSUPPORTED;  // 4-bit caches only
     Plan pl;
     int st = make_plan(c, Hq, S, max_q_len, max_kv, num_splits, flags, workspace != nullptr, &pl);
     if (st) return st;
@@ -522,8 +689,17 @@ const char *pkv_status_str(int s) {
 
 int pkv_append(const pkv_cache *c, int32_t layer, const void *k_new, const void *v_new, int32_t total_rows,
                const int32_t *seq_info, int32_t S, int32_t window, uint32_t *err, void *stream) {
-    int st = check_cache(c);
+    int st = check_cache(c, true);
     if (st) return st;
+    if (is_fp4(c)) {
+        const int64_t n = (int64_t)c->kv_heads * c->head_dim;
+        pkv_rows r = {};
+        r.k = k_new;
+        r.v = v_new;
+        r.k_stride = r.v_stride = n;
+        r.total_rows = total_rows;
+        return pkv_norm_rope_append(c, layer, nullptr, &r, seq_info, S, window, err, stream);
+    }
     if ((st = check_layer(c, layer))) return st;
     if (S < 0 || total_rows < 0 || window < 0 || !err) return PKV_EINVAL;
     if (S == 0) return PKV_OK;
@@ -549,10 +725,94 @@ int pkv_append(const pkv_cache *c, int32_t layer, const void *k_new, const void 
     return launch_status(cudaSuccess);
 }
 
+int pkv_rope_turns(const double *inv_freq, int32_t n, uint64_t *turns) {
+    if (n < 0 || (n > 0 && (!inv_freq || !turns))) return PKV_EINVAL;
+    for (int i = 0; i < n; ++i)
+        if (!isfinite(inv_freq[i])) return PKV_EINVAL;
+    for (int i = 0; i < n; ++i) {
+        // the fraction of a turn a position, in units of 2^-64: whole turns do not matter
+        const double t = inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
+        const double f = t - floor(t);
+        turns[i] = f >= 1.0 ? 0 : (uint64_t)ldexp(f, 32) << 32 | (uint64_t)ldexp(ldexp(f, 32) - floor(ldexp(f, 32)), 32);
+    }
+    return PKV_OK;
+}
+
+int pkv_rope_inv_freq(int32_t rot_dim, double theta, int32_t scaling, double factor, double trained_len, double beta_fast,
+                      double beta_slow, double *inv_freq, double *mscale) {
+    if (rot_dim <= 0 || rot_dim % 2 || !(theta > 1.0) || !isfinite(theta) || !inv_freq || !mscale) return PKV_EINVAL;
+    if (scaling < PKV_ROPE_PLAIN || scaling > PKV_ROPE_YARN) return PKV_EINVAL;
+    if (scaling != PKV_ROPE_PLAIN && !(factor >= 1.0 && isfinite(factor))) return PKV_EINVAL;
+    if (scaling == PKV_ROPE_NTK && rot_dim == 2) return PKV_EINVAL;
+    const double two_pi = 6.283185307179586;
+    double lo = 0.0, hi = 1.0;
+    if (scaling == PKV_ROPE_YARN) {
+        if (!(trained_len > 0.0 && isfinite(trained_len)) || !(beta_fast > beta_slow) || !(beta_slow > 0.0) || !isfinite(beta_fast))
+            return PKV_EINVAL;
+        // the pair index whose wave turns `beta` times in the trained context
+        auto pair = [&](double beta) { return rot_dim * log(trained_len / (beta * two_pi)) / (2.0 * log(theta)); };
+        lo = fmax(floor(pair(beta_fast)), 0.0);
+        hi = fmin(ceil(pair(beta_slow)), rot_dim - 1.0);
+        if (!(hi > lo)) hi = lo + 0.001;
+    }
+    const double base = scaling == PKV_ROPE_NTK ? theta * pow(factor, rot_dim / (rot_dim - 2.0)) : theta;
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        const double f = pow(base, -2.0 * i / rot_dim);
+        if (scaling == PKV_ROPE_LINEAR) inv_freq[i] = f / factor;
+        else if (scaling == PKV_ROPE_YARN) {
+            const double slow = fmin(fmax((i - lo) / (hi - lo), 0.0), 1.0);  // 1: stretched by the whole factor
+            inv_freq[i] = f / factor * slow + f * (1.0 - slow);
+        } else {
+            inv_freq[i] = f;
+        }
+    }
+    *mscale = scaling == PKV_ROPE_YARN ? 0.1 * log(factor) + 1.0 : 1.0;
+    return PKV_OK;
+}
+
+int pkv_norm_rope(const pkv_rope *rope, int32_t dtype, int32_t head_dim, int32_t kv_heads, const pkv_rows *rows, void *stream) {
+    if (dtype != PKV_BF16 && dtype != PKV_F32) return PKV_EUNSUPPORTED;
+    if (head_dim <= 0 || head_dim % 8 != 0 || head_dim > 256) return PKV_EUNSUPPORTED;
+    if (kv_heads < 0 || kv_heads > 65535 || !rope) return PKV_EINVAL;
+    RopeParams p;
+    const int st = rope_params(rope, rows, dtype, head_dim, kv_heads, false, &p);
+    if (st) return st;
+    if (p.rows == 0) return PKV_OK;
+    return launch_status(launch_rope(p, kNoCache, dtype == PKV_F32, device_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int pkv_norm_rope_append(const pkv_cache *c, int32_t layer, const pkv_rope *rope, const pkv_rows *rows, const int32_t *seq_info,
+                         int32_t S, int32_t window, uint32_t *err, void *stream) {
+    int st = check_cache(c, true);
+    if (st) return st;
+    if ((st = check_layer(c, layer))) return st;
+    if (S < 0 || window < 0 || !err) return PKV_EINVAL;
+    if (S > 0 && (!seq_info || !aligned16(seq_info))) return PKV_EINVAL;
+    RopeParams p;
+    if ((st = rope_params(rope, rows, c->dtype, c->head_dim, c->kv_heads, true, &p))) return st;
+    if (S == 0) return PKV_OK;
+    p.k_pool = c->k[layer];
+    p.v_pool = c->v[layer];
+    p.block_table = c->block_table;
+    p.seq_info = reinterpret_cast<const int4 *>(seq_info);
+    p.err = err;
+    p.num_blocks = c->num_blocks;
+    p.S = S;
+    p.max_seqs = c->max_seqs;
+    p.mbps = c->max_blocks_per_seq;
+    p.ring_rows = c->ring_rows;
+    p.window = window;
+    return launch_status(launch_rope(p, is_fp4(c) ? kFp4 : kSameType, c->dtype == PKV_F32, device_sms(),
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int pkv_attend_varlen(const pkv_cache *c, int32_t layer, const void *q, int32_t Hq, int32_t total_rows,
                       const int32_t *seq_info, int32_t S, int32_t max_q_len, int64_t max_kv, int32_t num_splits,
                       float scale, int32_t causal, int32_t window, float *out, float *lse, void *workspace,
                       int64_t workspace_bytes, uint32_t *err, uint32_t flags, void *stream) {
+    if (is_fp4(c))
+        return attend4(c, layer, q, Hq, total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale, causal, window, out, lse,
+                       err, flags, stream);
     return attend_common(c, layer, q, nullptr, nullptr, Hq, total_rows, seq_info, S, max_q_len, max_kv,
                          num_splits, scale, causal, window, out, lse, workspace, workspace_bytes, err, flags,
                          stream);
@@ -564,6 +824,20 @@ int pkv_append_attend(const pkv_cache *c, int32_t layer, const void *q, const vo
                       float *out, float *lse, void *workspace, int64_t workspace_bytes, uint32_t *err,
                       uint32_t flags, void *stream) {
     if (total_rows > 0 && (!k_new || !v_new)) return PKV_EINVAL;
+    if (is_fp4(c)) {
+        // Two launches.  The attention is checked first (a call with no rows of
+        // work launches nothing), so a refused call writes nothing.
+        Plan4 pl;
+        int st = make_plan4(c, Hq, S, max_q_len, max_kv, num_splits, &pl);
+        if (st) return st;
+        if ((st = check_layer(c, layer))) return st;
+        if (total_rows < 0 || window < 0 || (causal != 0 && causal != 1) || !err || !out || !aligned16(out) ||
+            (total_rows > 0 && (!q || !aligned16(q))) || (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)))
+            return PKV_EINVAL;
+        if ((st = pkv_append(c, layer, k_new, v_new, total_rows, seq_info, S, window, err, stream))) return st;
+        return attend4(c, layer, q, Hq, total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale, causal, window, out, lse,
+                       err, flags, stream);
+    }
     return attend_common(c, layer, q, total_rows > 0 ? k_new : nullptr, total_rows > 0 ? v_new : nullptr, Hq,
                          total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale, causal, window, out, lse,
                          workspace, workspace_bytes, err, flags, stream);
@@ -573,6 +847,9 @@ int pkv_append_attend_noalloc(const pkv_cache *c, int32_t layer, const void *q, 
                               const void *v_new, int32_t Hq, int32_t total_rows, const int32_t *seq_info, int32_t S,
                               int32_t max_q_len, int64_t max_kv, int32_t num_splits, float scale, int32_t causal,
                               int32_t window, float *out, float *lse, uint32_t *err, uint32_t flags, void *stream) {
+    if (is_fp4(c))  // needs no scratch
+        return pkv_append_attend(c, layer, q, k_new, v_new, Hq, total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale,
+                                 causal, window, out, lse, nullptr, 0, err, flags, stream);
     const int64_t need = pkv_attend_workspace_bytes(c, Hq, S, max_q_len, max_kv, num_splits, flags);
     if (need < 0) return (int)need;
     if (need > 0) {
@@ -595,6 +872,10 @@ int pkv_append_attend_noalloc(const pkv_cache *c, int32_t layer, const void *q, 
 
 int64_t pkv_attend_workspace_bytes(const pkv_cache *c, int32_t Hq, int32_t S, int32_t max_q_len, int64_t max_kv,
                                    int32_t num_splits, uint32_t flags) {
+    if (is_fp4(c)) {  // 4-bit caches merge in the cluster
+        Plan4 pl4;
+        return make_plan4(c, Hq, S, max_q_len, max_kv, num_splits, &pl4);
+    }
     Plan pl;
     const int st = make_plan(c, Hq, S, max_q_len, max_kv, num_splits, flags, true, &pl);
     if (st) return st;
@@ -641,7 +922,7 @@ int pkv_seq_clone(const pkv_cache *c, int32_t src_col, int32_t dst_col, int64_t 
 
 int pkv_rewind(const pkv_cache *c, int32_t *seq_info, int32_t n, const int32_t *amount, int32_t window,
                uint32_t *err, void *stream) {
-    int st = check_cache(c);
+    int st = check_cache(c, true);
     if (st) return st;
     if (n < 0 || window < 0 || !err) return PKV_EINVAL;
     if (n == 0) return PKV_OK;

@@ -1,0 +1,46 @@
+// Host-side view of the 4-bit attention kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stddef.h>
+
+#include "common.cuh"
+
+namespace pkv {
+
+// Key ranges of at most this many pages a warp run on one CTA of the cluster.
+constexpr int kSolo4 = 4;
+
+// Everything one launch reads; passed by value as a grid constant.
+struct Attend4Params {
+    const unsigned char *k, *v;   // this layer's pools, [num_blocks][Hkv][9 D]
+    const __nv_bfloat16 *q;       // [rows][Hq][D]
+    const int *block_table;       // [max_seqs][mbps]
+    const int4 *seq_info;         // [S]
+    const int *first_valid;       // [max_seqs] or null
+    void *out;                    // [rows][Hq][D], fp32 or bf16
+    float *lse;                   // [rows][Hq] or null
+    unsigned *err;
+    long long num_blocks;
+    int Hq, Hkv, G;
+    int total_rows, S, max_seqs, mbps, ring_rows, max_q_len;
+    int row_tiles;                // CTAs along the rows of one (segment, kv head)
+    int causal, window, out_bf16;
+    float scale_log2;             // softmax scale * log2(e)
+};
+
+struct Attend4Kernel {
+    const void *fn;
+    int threads;
+    size_t smem;
+    int rows;   // query rows of a CTA
+    int warps;
+    int ctas;   // CTAs an SM holds
+};
+
+// The kernel for head_dim D and at most `rows` query rows a (segment, kv head).
+Attend4Kernel pick4_64(int rows);
+Attend4Kernel pick4_128(int rows);
+Attend4Kernel pick4_256(int rows);
+
+}  // namespace pkv

@@ -1,0 +1,438 @@
+// Per-head norm, rotary position and append of this step's rows (sm_103a).
+//
+// One pass over q, k and v: y = R(pos) (x * rsqrt(mean(x^2) + eps) * w) for q
+// and k heads, q to its output rows, k and v to their cache slots.  Every value
+// is read once and written once, about a dozen flops each, so long calls are
+// bound by HBM and short ones by the launch.
+//
+// A warp takes one row (token) and a slice of its heads: lanes own 8 columns
+// of a head, D / 8 lanes (rounded up to a power of two) a head, 32 / that many
+// heads at once.  The row's angles are then the same for every head the warp
+// takes: each lane forms the sines and cosines of its 8 columns once and keeps
+// them, with the head weights folded in, in registers.  No shared memory, no
+// barrier; the norm's sum and the rotation partner come by shuffles.
+//
+// Angles: turn_i = frequency / 2 pi as a 64-bit fraction of a turn.  position *
+// turn_i, taken modulo 2^64, is the exact fractional turn to 2^-33 at any
+// 32-bit position; sinpif / cospif of its top 32 bits need no range reduction.
+// (A float product pos * freq is off by 0.008 rad at position 131072.)
+//
+// The 4-bit cache stores V by token pairs, two tokens to a byte, so its V pages
+// are written by page: a warp takes one (segment, kv head, page), gathers the
+// page's new rows and merges their nibbles into the old ones.  K needs no
+// merge (a byte is two columns of one token) and is quantised by the row warps.
+#pragma once
+
+#include "fp4.cuh"
+
+namespace pkv {
+
+constexpr int kRopeWarps = 4;    // warps of a CTA
+constexpr int kRopeUnroll = 4;   // head loads in flight per lane
+
+enum RopeCache { kNoCache = 0, kSameType = 1, kFp4 = 2 };
+enum RopePair { kInLane = 0, kByShuffle = 1, kByShared = 2 };
+
+struct RopeParams {
+    const void *q, *k, *v;            // rows; q may be null (no query heads), k and v null without a cache or k rows
+    void *q_out, *k_out, *v_out;      // q_out null without q; k_out / v_out optional with a cache
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride, v_out_stride;  // elements between rows
+    const int *positions;             // [rows] or null: the row's cache position
+    const unsigned long long *turns;  // [rot_dim / 2]
+    const void *q_weight, *k_weight;  // [D] or null
+    float eps, mscale;
+    int rot_dim, interleaved;
+    int rows, Hq, Hkv, D;
+    int lanes_log2;                   // lanes of a head
+    int slices;                       // warps of a row
+    int row_ctas;                     // CTAs of row warps; the rest write 4-bit V pages
+    // cache
+    void *k_pool, *v_pool;
+    const int *block_table;
+    const int4 *seq_info;
+    unsigned *err;
+    long long num_blocks;
+    int S, max_seqs, mbps, ring_rows, window;
+    int page_warps;                   // 4-bit cache: warps that share one (segment, kv head)'s new pages
+};
+
+// Every page the segment's new rows go to is inside the pool (the whole warp asks).
+__device__ __forceinline__ bool new_pages_ok(const RopeParams &p, const Segment &sg, int lane) {
+    const int *bt = p.block_table + (long long)sg.col * p.mbps;
+    const int p0 = (sg.kend - sg.ql) / kPage, p1 = (sg.kend + kPage - 1) / kPage;
+    bool ok = true;
+    if (sg.ql > 0)
+        for (int pb = p0 + lane; pb < p1; pb += 32) {
+            const int b = bt[table_page(pb, p.ring_rows)];
+            ok &= b >= 0 && (long long)b < p.num_blocks;
+        }
+    return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ bool holds_row(const RopeParams &p, const Segment &sg, int row) {
+    return sg.q0 <= row && (long long)row < (long long)sg.q0 + sg.ql &&
+           !segment_fault(sg, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
+}
+
+// Lowest valid segment that holds `row`, or -1 (the whole warp asks).  A decode
+// step's table has segment i at row i: looked at first.
+__device__ __forceinline__ int segment_of_row(const RopeParams &p, int row, int lane) {
+    if (row < p.S && holds_row(p, load_segment(p.seq_info, row), row)) return row;
+    for (int s0 = 0; s0 < p.S; s0 += 32) {
+        const int s = s0 + lane;
+        const bool hit = s < p.S && holds_row(p, load_segment(p.seq_info, min(s, p.S - 1)), row);
+        const unsigned m = __ballot_sync(0xffffffffu, hit);
+        if (m) return s0 + __ffs(m) - 1;
+    }
+    return -1;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(float (&o)[8], const T *src) {
+    if constexpr (sizeof(T) == 2) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(src);
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = __uint_as_float(w[i] << 16);
+            o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
+        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *dst, const float (&x)[8]) {
+    if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                     pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    } else {
+        *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+}
+
+// Quantise 8 columns of a row (half a scale group: lanes 2j and 2j + 1 hold
+// one); x holds bf16 numbers.  Returns the codes, leaves the stored values in x.
+__device__ __forceinline__ unsigned quantise8(float (&x)[8], unsigned &scale) {
+    unsigned amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    scale = scale4_of(amax);
+    const float s = scale4_value(scale);
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = code4_arg(x[i], s);
+    const unsigned codes = pack_e2m1x8(r);
+    unsigned h[4];
+    unpack_e2m1x8(h, codes);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+        x[2 * i] = f.x * s;
+        x[2 * i + 1] = f.y * s;
+    }
+    return codes;
+}
+
+// One row warp's cache slot.
+struct RopeSlot {
+    long long block;  // page id
+    int token;        // slot in the page
+};
+
+// The heads [h0, h1) of one kind (q, k or v) of a row.
+//   ca, sb: this lane's factors of its own and its partner's columns.
+template <typename T, int CACHE, int PAIR, bool NORM, bool ROPE>
+__device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T *dst, unsigned char *pool,
+                                           const RopeSlot &slot, int h0, int h1, const float (&ca)[8],
+                                           const float (&sb)[8], int partner, float *stage, int lane) {
+    const int per = 1 << p.lanes_log2, sub = lane >> p.lanes_log2, c = lane & (per - 1), heads = 32 >> p.lanes_log2;
+    const bool col_ok = c * 8 < p.D;
+    for (int hb = h0; hb < h1; hb += heads * kRopeUnroll) {
+        float x[kRopeUnroll][8];
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+            const int h = hb + u * heads + sub;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
+            if (col_ok && h < h1) load8<T>(x[u], src + (long long)h * p.D + c * 8);
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+            if (hb + u * heads >= h1) break;  // uniform
+            const int h = hb + u * heads + sub;
+            const bool mine = col_ok && h < h1;
+            float y[8];
+            float rinv = 1.f;
+            if constexpr (NORM) {
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(x[u][e], x[u][e], ss);
+                for (int o = 1; o < per; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                rinv = rsqrtf(ss / (float)p.D + p.eps);
+            }
+            if constexpr (ROPE) {
+                float z[8];  // the partner columns' values (0 where the column is not rotated)
+                if constexpr (PAIR == kInLane) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] = x[u][e ^ 1];
+                } else if constexpr (PAIR == kByShuffle) {
+                    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {  // bf16 pairs travel in one word
+                            const unsigned w = __byte_perm(__float_as_uint(x[u][e]), __float_as_uint(x[u][e + 1]), 0x7632);
+                            const unsigned o = __shfl_sync(0xffffffffu, w, partner);
+                            z[e] = __uint_as_float(o << 16);
+                            z[e + 1] = __uint_as_float(o & 0xffff0000u);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) z[e] = __shfl_sync(0xffffffffu, x[u][e], partner);
+                    }
+                } else {
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) stage[e * 32 + lane] = x[u][e];
+                    __syncwarp();
+                    const int half = p.rot_dim / 2;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int d = c * 8 + e, o = d < half ? d + half : d - half;
+                        z[e] = d < p.rot_dim ? stage[(o & 7) * 32 + (sub << p.lanes_log2) + (o >> 3)] : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool turned = c * 8 + e < p.rot_dim;
+                    y[e] = rinv * (turned ? fmaf(z[e], sb[e], x[u][e] * ca[e]) : x[u][e] * ca[e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = NORM ? rinv * x[u][e] * ca[e] : x[u][e];
+            }
+            if (CACHE == kFp4 && pool) {
+                // the row as it would be handed on (bf16), then quantised
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = __bfloat162float(__float2bfloat16_rn(y[e]));
+                unsigned scale;
+                const unsigned codes = quantise8(y, scale);
+                if (mine) {
+                    unsigned char *b = pool + (slot.block * p.Hkv + h) * block4_bytes(p.D);
+                    *reinterpret_cast<unsigned *>(b + slot.token * (p.D / 2) + c * 4) = codes;
+                    if ((c & 1) == 0) b[8 * p.D + slot.token * (p.D / 16) + c / 2] = (unsigned char)scale;
+                }
+            } else if (CACHE == kSameType && pool && mine) {
+                store8<T>(reinterpret_cast<T *>(pool) + ((slot.block * kPage + slot.token) * p.Hkv + h) * p.D + c * 8, y);
+            }
+            if (dst && mine) store8<T>(dst + (long long)h * p.D + c * 8, y);
+        }
+    }
+}
+
+// Write the 4-bit V page `pb` of kv head h from the segment's new rows.
+template <int D>
+__device__ __forceinline__ void write_v4_page(const RopeParams &p, const Segment &sg, int h, int pb, unsigned char *codes,
+                                              unsigned char *scales, int lane) {
+    constexpr int L = D / 8, TPI = 32 / L;  // lanes a row, rows at once
+    const int start = sg.kend - sg.ql, sub = lane / L, c = lane % L;
+    const int a = max(start - pb * kPage, 0), b = min(sg.kend - pb * kPage, kPage);  // new tokens of the page
+    const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(p.v);
+    __syncwarp();
+#pragma unroll 4
+    for (int t0 = 0; t0 < kPage; t0 += TPI) {
+        if (t0 + TPI <= a || t0 >= b) continue;  // uniform
+        const int tok = t0 + sub;
+        const bool mine = tok >= a && tok < b;
+        const long long row = (long long)sg.q0 + (pb * kPage + tok - start);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        if (mine) load8<__nv_bfloat16>(x, v + row * p.v_stride + h * D + c * 8);
+        unsigned scale;
+        const unsigned w = quantise8(x, scale);
+        if (mine) {
+            // one code a byte, for the exchange below
+            const unsigned lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
+            *reinterpret_cast<uint2 *>(codes + tok * D + c * 8) =
+                make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
+            if ((c & 1) == 0) scales[tok * (D / 16) + c / 2] = (unsigned char)scale;
+            if (p.v_out) store8<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16 *>(p.v_out) + row * p.v_out_stride + h * D + c * 8, x);
+        }
+    }
+    __syncwarp();
+    const long long blk = p.block_table[(long long)sg.col * p.mbps + table_page(pb, p.ring_rows)];
+    unsigned char *out = reinterpret_cast<unsigned char *>(p.v_pool) + (blk * p.Hkv + h) * block4_bytes(D);
+    const int g = lane >> 2, t = lane & 3;
+    auto fresh = [&](int tok) { return tok >= a && tok < b; };
+    const unsigned m0 = (fresh(2 * t) ? 0x0fu : 0u) | (fresh(2 * t + 1) ? 0xf0u : 0u);
+    const unsigned m1 = (fresh(2 * t + 8) ? 0x0fu : 0u) | (fresh(2 * t + 9) ? 0xf0u : 0u);
+    const unsigned mask = (m0 | m1 << 8) * 0x10001u;
+    if (mask) {
+#pragma unroll
+        for (int pl = 0; pl < D / 64; ++pl) {
+            auto pair = [&](int tok) {  // tokens tok and tok + 1 of 8 columns, one byte a column
+                const unsigned char *s = codes + tok * D + g * (D / 8) + pl * 8;
+                const uint2 lo = *reinterpret_cast<const uint2 *>(s), hi = *reinterpret_cast<const uint2 *>(s + D);
+                return make_uint2((lo.x & 0x0f0f0f0fu) | (hi.x & 0x0f0f0f0fu) << 4, (lo.y & 0x0f0f0f0fu) | (hi.y & 0x0f0f0f0fu) << 4);
+            };
+            const uint2 x = pair(2 * t), y = pair(2 * t + 8);
+            uint4 w = make_uint4(__byte_perm(x.x, y.x, 0x5140), __byte_perm(x.x, y.x, 0x7362),
+                                 __byte_perm(x.y, y.y, 0x5140), __byte_perm(x.y, y.y, 0x7362));
+            uint4 *d = reinterpret_cast<uint4 *>(out + pl * 512 + lane * 16);
+            if (mask != 0xffffffffu) {
+                const uint4 o = *d;
+                w = make_uint4((w.x & mask) | (o.x & ~mask), (w.y & mask) | (o.y & ~mask), (w.z & mask) | (o.z & ~mask),
+                               (w.w & mask) | (o.w & ~mask));
+            }
+            *d = w;
+        }
+    }
+    for (int i = lane; i < (b - a) * (D / 16); i += 32) {
+        const int tok = a + i / (D / 16), G = i % (D / 16);
+        out[8 * D + (G * 4 + (tok % 8) / 2) * 4 + (tok / 8) * 2 + (tok & 1)] = scales[tok * (D / 16) + G];
+    }
+}
+
+template <typename T, int CACHE, int PAIR>
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeParams p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_trigger();
+    if (CACHE == kFp4 && (int)blockIdx.x >= p.row_ctas) {
+        // V pages: units (segment, kv head, page warp), page warps fastest
+        const long long unit = (long long)(blockIdx.x - p.row_ctas) * kRopeWarps + warp;
+        const int pw = (int)(unit % p.page_warps), h = (int)(unit / p.page_warps % p.Hkv);
+        const long long s = unit / p.page_warps / p.Hkv;
+        if (s >= p.S) return;
+        const Segment sg = load_segment(p.seq_info, (int)s);
+        if (segment_fault(sg, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window) || sg.ql == 0) return;
+        if (!new_pages_ok(p, sg, lane)) return;
+        unsigned char *codes = smem + (size_t)warp * kPage * (p.D + p.D / 16), *scales = codes + kPage * p.D;
+        const int p1 = (sg.kend + kPage - 1) / kPage;
+        for (int pb = (sg.kend - sg.ql) / kPage + pw; pb < p1; pb += p.page_warps) {
+            if (p.D == 64) write_v4_page<64>(p, sg, h, pb, codes, scales, lane);
+            else if (p.D == 128) write_v4_page<128>(p, sg, h, pb, codes, scales, lane);
+            else write_v4_page<256>(p, sg, h, pb, codes, scales, lane);
+        }
+        return;
+    }
+    if (CACHE != kNoCache && blockIdx.x == 0)  // the refused segments
+        for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
+            const unsigned f = segment_fault(load_segment(p.seq_info, s), p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
+            if (f) atomicOr(p.err, f);
+        }
+    const long long w = (long long)blockIdx.x * kRopeWarps + warp;
+    const int row = (int)(w / p.slices), slice = (int)(w - (long long)row * p.slices);
+    if (w >= (long long)p.rows * p.slices) return;
+    RopeSlot slot{0, 0};
+    long long place = 0;
+    if (CACHE != kNoCache) {
+        const int s = segment_of_row(p, row, lane);
+        if (s < 0) return;
+        const Segment sg = load_segment(p.seq_info, s);
+        if (!new_pages_ok(p, sg, lane)) {
+            if (lane == 0) atomicOr(p.err, PKV_ERR_BLOCK);
+            return;
+        }
+        place = (long long)sg.kend - sg.ql + (row - sg.q0);
+        slot.block = p.block_table[(long long)sg.col * p.mbps + table_page((int)(place / kPage), p.ring_rows)];
+        slot.token = (int)(place % kPage);
+    }
+    // This lane's columns: cosine and signed sine of each.
+    const int per = 1 << p.lanes_log2, c = lane & (per - 1), half = p.rot_dim / 2;
+    float cs[8], sn[8];
+    int partner = lane;
+    if (p.rot_dim) {
+        const unsigned pos = (unsigned)(p.positions ? p.positions[row] : (int)place);
+        auto angle = [&](int i, float &co, float &si) {
+            const unsigned long long turn = p.turns[i];
+            const unsigned f = pos * (unsigned)(turn >> 32) + __umulhi(pos, (unsigned)turn) -
+                               ((int)pos < 0 ? (unsigned)turn : 0u);  // (pos mod 2^64) * turn, bits 32..63
+            const float x = (float)(int)f * 4.656612873077393e-10f;   // 2^-31: half turns in [-1, 1]
+            sincospif(x, &si, &co);
+            co *= p.mscale;
+            si *= p.mscale;
+        };
+        if (PAIR == kInLane) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const int i = (c * 8 + e) / 2;
+                float co = 1.f, si = 0.f;
+                if (i < half) angle(i, co, si);
+                cs[e] = cs[e + 1] = co;
+                sn[e] = -si;
+                sn[e + 1] = si;
+            }
+        } else {
+            const int hc = half / 8;  // by shuffle: the halves are whole lanes
+            if (PAIR == kByShuffle && c < 2 * hc) partner = lane + (c < hc ? hc : -hc);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int d = c * 8 + e;
+                float co = 1.f, si = 0.f;
+                if (d < p.rot_dim) angle(d < half ? d : d - half, co, si);
+                cs[e] = co;
+                sn[e] = d < half ? -si : si;
+            }
+        }
+    }
+    float *stage = reinterpret_cast<float *>(smem) + warp * 256;
+    const int heads = 32 >> p.lanes_log2;
+    // The row's groups of `heads` heads, q then k then v, cut evenly into the slices.
+    const int nq = p.q ? (p.Hq + heads - 1) / heads : 0, nk = p.k ? (p.Hkv + heads - 1) / heads : 0;
+    const int all = nq + nk + (CACHE == kSameType ? (p.Hkv + heads - 1) / heads : 0);
+    const int f0 = (int)((long long)all * slice / p.slices), f1 = (int)((long long)all * (slice + 1) / p.slices);
+    auto part = [&](int first, int H, int &h0, int &h1) {
+        h0 = max(f0 - first, 0) * heads;
+        h1 = min(max(f1 - first, 0) * heads, H);
+    };
+    auto kind = [&](const T *src, T *dst, unsigned char *pool, const T *weight, int first, int H) {
+        int h0, h1;
+        part(first, H, h0, h1);
+        if (h0 >= h1) return;
+        float ca[8], sb[8], wt[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wt[e] = 1.f;
+        if (weight && c * 8 < p.D) load8<T>(wt, weight + c * 8);
+        if (p.rot_dim) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float wz = 1.f;  // the partner column's weight
+                if (weight) {
+                    const int d = c * 8 + e;
+                    const int o = PAIR == kInLane ? d ^ 1 : d < half ? d + half : d - half;
+                    if (d < p.rot_dim) {
+                        if constexpr (sizeof(T) == 2) wz = __bfloat162float(weight[o]);
+                        else wz = weight[o];
+                    }
+                }
+                ca[e] = cs[e] * wt[e];
+                sb[e] = sn[e] * wz;
+            }
+            if (weight) rope_heads<T, CACHE, PAIR, true, true>(p, src, dst, pool, slot, h0, h1, ca, sb, partner, stage, lane);
+            else rope_heads<T, CACHE, PAIR, false, true>(p, src, dst, pool, slot, h0, h1, ca, sb, partner, stage, lane);
+        } else {
+            if (weight) rope_heads<T, CACHE, PAIR, true, false>(p, src, dst, pool, slot, h0, h1, wt, wt, partner, stage, lane);
+            else rope_heads<T, CACHE, PAIR, false, false>(p, src, dst, pool, slot, h0, h1, wt, wt, partner, stage, lane);
+        }
+    };
+    if (p.q) kind(reinterpret_cast<const T *>(p.q) + row * p.q_stride, reinterpret_cast<T *>(p.q_out) + row * p.q_out_stride, nullptr,
+                  reinterpret_cast<const T *>(p.q_weight), 0, p.Hq);
+    if (p.k) kind(reinterpret_cast<const T *>(p.k) + row * p.k_stride, p.k_out ? reinterpret_cast<T *>(p.k_out) + row * p.k_out_stride : nullptr,
+                  reinterpret_cast<unsigned char *>(p.k_pool), reinterpret_cast<const T *>(p.k_weight), nq, p.Hkv);
+    if (CACHE == kSameType) {
+        int h0, h1;
+        part(nq + nk, p.Hkv, h0, h1);
+        const float one[8] = {};
+        if (h0 < h1) rope_heads<T, CACHE, PAIR, false, false>(p, reinterpret_cast<const T *>(p.v) + row * p.v_stride,
+                                                 p.v_out ? reinterpret_cast<T *>(p.v_out) + row * p.v_out_stride : nullptr,
+                                                 reinterpret_cast<unsigned char *>(p.v_pool), slot, h0, h1, one, one, partner, stage, lane);
+    }
+}
+
+}  // namespace pkv

@@ -1,0 +1,15 @@
+// Host-side view of the norm + rotary + append kernel.
+#pragma once
+
+#include "rope.cuh"
+
+namespace pkv {
+
+// Warps an SM is given before a warp takes more than one group of heads.
+constexpr int kRopeFill = 24;
+
+// Picks the instantiation and the split (fills the fields the split decides).
+// cache: RopeCache; f32: the rows' type (bf16 otherwise; 4-bit caches take bf16 rows).
+cudaError_t launch_rope(RopeParams &p, int cache, bool f32, int sms, cudaStream_t stream);
+
+}  // namespace pkv
