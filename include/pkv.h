@@ -329,8 +329,9 @@ int pkv_norm_rope_append(const pkv_cache *cache, int32_t layer, const pkv_rope *
  * On a PKV_FP4 cache q is bf16 and out is fp32, or bf16 with
  * PKV_FLAG_OUT_BF16.  Scores are those of the stored values to fp32; the
  * softmax weights are rounded to fp16 for the product with V.  A NaN in V
- * reaches only the rows that see its key.  The splits always form a cluster
- * (num_splits 0..16, workspace ignored); PKV_FLAG_SIMT, PKV_FLAG_MMA_SYNC and
+ * reaches only the rows that see its key.  Without a workspace the splits form
+ * a cluster (num_splits 0..16); large launches are faster with one (see
+ * pkv_attend_workspace_bytes).  PKV_FLAG_SIMT, PKV_FLAG_MMA_SYNC and
  * PKV_FLAG_PREFETCH_NEXT have no effect.  PKV_FLAG_PDL: pages wholly below
  * position kv_end - q_len may be read before the previous kernel has
  * finished, so it may be the append of this step.
@@ -367,7 +368,7 @@ int pkv_append_attend(const pkv_cache *cache, int32_t layer,
 
 /*
  * Bytes of workspace the two calls above need for these launch bounds when
- * given one (0: the launch never uses it; always so with a PKV_FP4 cache).  With a workspace, the decode
+ * given one (0: the launch never uses it).  With a workspace, the decode
  * kernel (at most 8 query rows per segment and kv head: G * max_q_len <= 8,
  * bf16, tensor-core path) splits a key range over independent CTAs (up to 64
  * per range, num_splits 0..64) that merge through it: each writes its
@@ -381,6 +382,13 @@ int pkv_append_attend(const pkv_cache *cache, int32_t layer,
  * heads) than before, it must be zero-filled again.  Calls that may run
  * concurrently need their own.  A workspace smaller than this size is rejected with
  * PKV_EINVAL.  Returns a negative pkv_status for invalid bounds.
+ *
+ * With a PKV_FP4 cache: launches with num_splits 0, at most 8 query rows per
+ * kv head, at most 512 segments and bounds of about 100,000 (key, kv head)
+ * pairs or more.  Given a workspace, they run as one wave of CTAs with equal shares of all
+ * key ranges and a second launch that merges the shared ones, instead of as a
+ * cluster per range.  It need not be zeroed, and may be shared by calls that
+ * follow one another on one stream.
  */
 int64_t pkv_attend_workspace_bytes(const pkv_cache *cache, int32_t num_q_heads,
                                    int32_t num_segments, int32_t max_q_len,

@@ -6,7 +6,6 @@ CUDA kernels; torch supplies device memory and streams.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import List, Optional, Sequence, Tuple
 
@@ -18,9 +17,11 @@ from ._lib import lib
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float32: _lib.F32, torch.uint8: _lib.FP4}
 
 
-def _stream(stream=None) -> ctypes.c_void_p:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream=None) -> int:
+    """The handle of `stream`, or of the current stream of the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -89,6 +90,11 @@ class PagedKVCache:
             reserved0=0, k=ctypes.cast(self._kp, ctypes.c_void_p), v=ctypes.cast(self._vp, ctypes.c_void_p),
             block_table=block_table.data_ptr(), bucket=self.bucket, generation=self.generation,
             first_valid=_ptr(self.first_valid))
+        self._ref = ctypes.byref(self.desc)
+        self._fp4 = dtype == torch.uint8
+        self._kv_heads, self._head_dim, self._device = kv_heads, head_dim, k[0].get_device()
+        # the type of q, k_new and v_new rows: the cache's, bf16 for a 4-bit cache
+        self.row_dtype = torch.bfloat16 if self._fp4 else dtype
 
     @classmethod
     def allocate(cls, num_layers: int, kv_heads: int, head_dim: int, bucket: int, dtype=torch.bfloat16,
@@ -107,23 +113,18 @@ class PagedKVCache:
 
     @property
     def kv_heads(self) -> int:
-        return int(self.desc.kv_heads)
+        return self._kv_heads
 
     @property
     def head_dim(self) -> int:
-        return int(self.desc.head_dim)
+        return self._head_dim
 
     @property
     def dtype(self) -> torch.dtype:
         return self.k[0].dtype
 
-    @property
-    def row_dtype(self) -> torch.dtype:
-        """The type of q, k_new and v_new rows: the cache's, bf16 for a 4-bit cache."""
-        return torch.bfloat16 if self.dtype == torch.uint8 else self.dtype
-
     def ref(self):
-        return ctypes.byref(self.desc)
+        return self._ref
 
     def reusable_for(self, num_layers, kv_heads, head_dim, dtype, length) -> bool:
         """Same shape and the length fits the current bucket (PagedDecodeCache.reusable_for)."""
@@ -137,16 +138,6 @@ def bucket_for(length: int) -> int:
 
 def new_err_flags(device="cuda") -> torch.Tensor:
     return torch.zeros(1, dtype=torch.int32, device=device)
-
-
-@contextlib.contextmanager
-def _on(device: torch.device):
-    """Launches go to the tensors' device, whichever is current."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        yield
-    else:
-        with torch.cuda.device(device):
-            yield
 
 
 def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -203,41 +194,74 @@ class Rope:
                                   mscale=self.mscale, eps=self.eps, q_weight=_ptr(self.q_weight),
                                   k_weight=_ptr(self.k_weight))
 
-    def check(self, dtype: torch.dtype, head_dim: int, device: torch.device) -> None:
+        given = [t for t in (self.turns, self.q_weight, self.k_weight) if t is not None]
+        weights = [w for w in (self.q_weight, self.k_weight) if w is not None]
+        if any(t.get_device() != given[0].get_device() for t in given) or any(
+                w.dtype != weights[0].dtype or w.numel() != weights[0].numel() for w in weights):
+            raise ValueError("the norm weights and frequencies are on one device, the weights of one type and size")
+        self._device = given[0].get_device() if given else None
+        self._dtype, self._dim = (weights[0].dtype, weights[0].numel()) if weights else (None, None)
+        self._ref = ctypes.byref(self.desc)
+
+    def check(self, dtype: torch.dtype, head_dim: int, device: int) -> None:
+        """Raises unless this applies to rows of dtype and head_dim on CUDA device `device`."""
         if self.rot_dim > head_dim:
             raise ValueError(f"rot_dim {self.rot_dim} is above head_dim {head_dim}")
-        if self.turns is not None and self.turns.device != device:
-            raise ValueError("the frequencies are on another device than the rows")
-        for w in (self.q_weight, self.k_weight):
-            if w is not None and (w.dtype != dtype or w.numel() != head_dim or w.device != device):
-                raise ValueError("norm weights are (head_dim,) of the rows' type, on their device")
+        if self._device is not None and self._device != device:
+            raise ValueError("the frequencies and norm weights are on another device than the rows")
+        if self._dtype is not None and (self._dtype is not dtype or self._dim != head_dim):
+            raise ValueError("norm weights are (head_dim,) of the rows' type")
 
 
-def _row_stride(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dtype, device) -> int:
-    """Elements between the rows of (rows, heads, dim); heads and columns contiguous, rows apart as they like."""
-    if t.shape != (rows, heads, dim) or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} is ({rows}, {heads}, {dim}) of {dtype} on {device}")
+def _row_stride(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: int) -> int:
+    """Elements between the rows of t, whose heads and columns are contiguous and whose rows are apart as they like."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} is {tuple(shape)} of {dtype} on device {device}")
     s0, s1, s2 = t.stride()
-    if (dim > 1 and s2 != 1) or (heads > 1 and s1 != dim):
+    rows, heads, dim = shape
+    if (s2 != 1 and dim > 1) or (s1 != dim and heads > 1):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return s0 if rows > 1 else max(s0, heads * dim)
+    return s0 if rows > 1 else heads * dim
 
 
 def _rows_desc(q, k, v, q_out, k_out, v_out, positions, kv_heads, head_dim, dtype, device) -> _lib.RowsDesc:
     some = q if q is not None else k
-    rows = int(some.shape[0])
-    hq = int(q.shape[1]) if q is not None and q.dim() == 3 else 0
-    d = _lib.RowsDesc(q_heads=hq, total_rows=rows)
-    for name, t, heads in (("q", q, hq), ("k", k, kv_heads), ("v", v, kv_heads), ("q_out", q_out, hq),
-                           ("k_out", k_out, kv_heads), ("v_out", v_out, kv_heads)):
-        if t is not None:
-            setattr(d, name + "_stride", _row_stride(t, name, rows, heads, head_dim, dtype, device))
-            setattr(d, name, t.data_ptr())
+    if some.dim() != 3:
+        raise ValueError("rows are (rows, heads, head_dim)")
+    rows, hq, _ = some.shape
+    kv = (rows, kv_heads, head_dim)
+    qp = kp = vp = qop = kop = vop = pos = None
+    qs = ks = vs = qos = kos = vos = 0
+    if q is not None:
+        qs, qp = _row_stride(q, "q", (rows, hq, head_dim), dtype, device), q.data_ptr()
+        qos, qop = (qs, qp) if q_out is q else (_row_stride(q_out, "q_out", (rows, hq, head_dim), dtype, device), q_out.data_ptr())
+    else:
+        hq = 0
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    if k is not None:
+        ks, kp = _row_stride(k, "k", kv, dtype, device), k.data_ptr()
+    if v is not None:
+        vs, vp = _row_stride(v, "v", kv, dtype, device), v.data_ptr()
+    if k_out is not None:
+        kos, kop = _row_stride(k_out, "k_out", kv, dtype, device), k_out.data_ptr()
+    if v_out is not None:
+        vos, vop = _row_stride(v_out, "v_out", kv, dtype, device), v_out.data_ptr()
     if positions is not None:
-        if positions.shape != (rows,) or positions.dtype != torch.int32 or positions.device != device:
-            raise ValueError(f"positions is int32 ({rows},) on {device}")
-        d.positions = _contig(positions, "positions").data_ptr()
-    return d
+        if positions.shape != (rows,) or positions.dtype is not torch.int32 or positions.get_device() != device:
+            raise ValueError(f"positions is int32 ({rows},) on device {device}")
+        pos = _contig(positions, "positions").data_ptr()
+    return _lib.RowsDesc(qp, kp, vp, qop, kop, vop, qs, ks, vs, qos, kos, vos, hq, rows, pos)
+
+
+def _on_device(device: int, fn, stream) -> int:
+    """fn(stream handle) with `device` current, whichever is."""
+    if device < 0:
+        raise ValueError("the tensors are not on a CUDA device")
+    if device != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return fn(_stream(stream))
+    return fn(stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device))
 
 
 def norm_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -251,16 +275,17 @@ def norm_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
     some = q if q is not None else k
     if some is None or some.dim() != 3:
         raise ValueError("q or k is (rows, heads, head_dim)")
-    if some.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"unsupported dtype {some.dtype}")
-    dim, dtype, dev = int(some.shape[2]), some.dtype, some.device
+    dim, dtype, dev = int(some.shape[2]), some.dtype, some.get_device()
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
     rope.check(dtype, dim, dev)
     kv = int(k.shape[1]) if k is not None and k.dim() == 3 else 0
     d = _rows_desc(q, k, None, q_out if q_out is not None else q, k_out if k_out is not None else k, None, positions, kv, dim,
                    dtype, dev)
-    with _on(dev):
-        _lib.check("pkv_norm_rope", lib.pkv_norm_rope(ctypes.byref(rope.desc), _DTYPES[dtype], dim, kv, ctypes.byref(d),
-                                                      _stream(stream)))
+    _lib.check("pkv_norm_rope", _on_device(dev, lambda st: lib.pkv_norm_rope(rope._ref, _DTYPES[dtype], dim, kv, ctypes.byref(d), st),
+                                           stream))
 
 
 def norm_rope_append(cache: PagedKVCache, layer: int, rope: Optional[Rope], q: Optional[torch.Tensor], k_new: torch.Tensor,
@@ -273,18 +298,18 @@ def norm_rope_append(cache: PagedKVCache, layer: int, rope: Optional[Rope], q: O
     angles' positions; by default a row's position in the cache.  k_out / v_out
     get the rows as the cache holds them.  Rows may be strided.
     """
-    dev = cache.k[0].device
+    dev, dtype, dim = cache._device, cache.row_dtype, cache._head_dim
     if rope is not None:
-        rope.check(cache.row_dtype, cache.head_dim, dev)
-    if q is not None and q_out is None:
-        q_out = q
-    if seq_info.dtype != torch.int32 or seq_info.dim() != 2 or seq_info.shape[1] != 4 or seq_info.device != dev:
-        raise ValueError(f"seq_info is int32 (segments, 4) on {dev}")
-    d = _rows_desc(q, k_new, v_new, q_out, k_out, v_out, positions, cache.kv_heads, cache.head_dim, cache.row_dtype, dev)
-    with _on(dev):
-        _lib.check("pkv_norm_rope_append", lib.pkv_norm_rope_append(
-            cache.ref(), int(layer), None if rope is None else ctypes.byref(rope.desc), ctypes.byref(d),
-            _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(window), _ptr(err), _stream(stream)))
+        rope.check(dtype, dim, dev)
+    si = seq_info.shape
+    if seq_info.dtype is not torch.int32 or len(si) != 2 or si[1] != 4 or seq_info.get_device() != dev:
+        raise ValueError(f"seq_info is int32 (segments, 4) on device {dev}")
+    d = _rows_desc(q, k_new, v_new, q if q_out is None else q_out, k_out, v_out, positions, cache._kv_heads, dim, dtype, dev)
+    table = _contig(seq_info, "seq_info").data_ptr()
+    st = _on_device(dev, lambda st: lib.pkv_norm_rope_append(cache._ref, layer, None if rope is None else rope._ref, ctypes.byref(d), table,
+                                                             si[0], window, err.data_ptr(), st), stream)
+    if st:
+        _lib.check("pkv_norm_rope_append", st)
 
 
 def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, seq_info: torch.Tensor,
@@ -295,19 +320,47 @@ def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Te
         _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(window), _ptr(err), _stream(stream)))
 
 
+# Bounds (segments x kv heads x keys) from which a launch over a 4-bit cache
+# may use a workspace; pkv_attend_workspace_bytes decides.
+_FP4_WORKSPACE_FROM = 16 * 6144
+
+
+def _fp4_workspace(cache, hq, segments, max_q_len, max_kv, window, flags, stream):
+    """A workspace for one call over a 4-bit cache, or None: a large launch merges its shared ranges through it.
+
+    Each call takes its own from torch's allocator, so calls on several
+    streams, and captured graphs, share nothing.
+    """
+    keys = min(max_kv, window + max_q_len) if window > 0 else max_kv
+    if segments * cache._kv_heads * keys < _FP4_WORKSPACE_FROM:
+        return None
+    n = attend_workspace_bytes(cache, hq, segments, max_q_len, max_kv, 0, flags)
+    if n <= 0:
+        return None
+    ws = torch.empty(n, dtype=torch.uint8, device=cache.k[0].device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
 def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max_q_len, max_kv, scale, causal,
             window, num_splits, flags, stream, workspace):
-    rows, hq = int(q.shape[0]), int(q.shape[1])
-    if out.dtype == torch.bfloat16:
+    shape, segments = q.shape, seq_info.shape[0]
+    max_q_len, max_kv, window = int(max_q_len), int(max_kv), int(window)
+    if out.dtype is torch.bfloat16:
         flags |= _lib.FLAG_OUT_BF16
-    args = [cache.ref(), layer, _ptr(_contig(q, "q"))]
+    if cache._fp4 and workspace is None and num_splits == 0:
+        workspace = _fp4_workspace(cache, shape[1], segments, max_q_len, max_kv, window, flags, stream)
+    new = ()
     if fn_name == "pkv_append_attend":
-        args += [_ptr(_contig(k_new, "k_new")), _ptr(_contig(v_new, "v_new"))]
-    ws_bytes = int(workspace.numel() * workspace.element_size()) if workspace is not None else 0
-    args += [hq, rows, _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(max_q_len), int(max_kv),
-             int(num_splits), float(scale), int(bool(causal)), int(window), _ptr(_contig(out, "out")),
-             _ptr(lse), _ptr(workspace), ws_bytes, _ptr(err), int(flags), _stream(stream)]
-    _lib.check(fn_name, getattr(lib, fn_name)(*args))
+        new = (_contig(k_new, "k_new").data_ptr(), _contig(v_new, "v_new").data_ptr())
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    st = getattr(lib, fn_name)(
+        cache._ref, layer, _contig(q, "q").data_ptr(), *new, shape[1], shape[0], _contig(seq_info, "seq_info").data_ptr(), segments,
+        max_q_len, max_kv, int(num_splits), float(scale), 1 if causal else 0, window, _contig(out, "out").data_ptr(),
+        None if lse is None else lse.data_ptr(), ws, ws_bytes, err.data_ptr(), int(flags), _stream(stream))
+    if st:
+        _lib.check(fn_name, st)
 
 
 def attend_varlen(cache: PagedKVCache, layer: int, q: torch.Tensor, seq_info: torch.Tensor, out: torch.Tensor,

@@ -356,9 +356,31 @@ struct Plan4 {
     AttnKernel k;  // the same kernel for the shared cluster queries
     int G, row_tiles, ncta;
     long long units;
+    int shares;    // CTAs of the equal-shares kernel, 0: not for these bounds
 };
 
-int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_kv, int num_splits, Plan4 *pl) {
+// Equal shares cost a second launch (about 3 us) and balance the SMs: worth
+// it from about this many 16-token pages of one kv head on (about 8 us of
+// reading at head_dim 128; one sequence of 8192 keys and 8 heads, 4096 pages, is
+// faster in clusters).  Every CTA sums the segment table's pages, so the
+// table has to be short; long ones have ranges enough for one CTA each.
+constexpr long long kSharesFrom = 6144;
+constexpr int kSharesSegments = 512;
+
+struct Ws4Layout {
+    size_t head, stat, part, total;
+};
+Ws4Layout ws4_layout(int shares, int rows, int head_dim) {
+    auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
+    Ws4Layout w;
+    w.head = 0;
+    w.stat = al((size_t)2 * shares * 16);
+    w.part = al(w.stat + (size_t)2 * shares * rows * 8);
+    w.total = al(w.part + (size_t)2 * shares * rows * head_dim * 4);
+    return w;
+}
+
+int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_kv, int window, int num_splits, Plan4 *pl) {
     const int st = check_cache(c, true);
     if (st) return st;
     if (Hq <= 0 || Hq % c->kv_heads != 0) return PKV_EINVAL;
@@ -381,14 +403,20 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
         while (n > 1 && n * pl->k4.warps * 2 > max_pages) n /= 2;
     }
     pl->ncta = (int)std::max<long long>(1, std::min<long long>(n, max_pages));
+    pl->shares = 0;
+    if (pl->k4.balance && pl->row_tiles == 1 && num_splits == 0 && S > 0 && S <= kSharesSegments) {
+        const long long keys = window > 0 ? std::min<long long>(max_kv, (long long)window + max_q_len) : max_kv;
+        if ((long long)S * c->kv_heads * ((keys + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE) >= kSharesFrom)
+            pl->shares = std::min(device_sms() * pl->k4.ctas, kMerge4Slots);
+    }
     return PKV_OK;
 }
 
 int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows, const int *seq_info, int S, int max_q_len,
-            long long max_kv, int num_splits, float scale, int causal, int window, void *out, float *lse, unsigned *err,
-            unsigned flags, void *stream) {
+            long long max_kv, int num_splits, float scale, int causal, int window, void *out, float *lse, void *workspace,
+            long long workspace_bytes, unsigned *err, unsigned flags, void *stream, bool check_only = false) {
     Plan4 pl;
-    int st = make_plan4(c, Hq, S, max_q_len, max_kv, num_splits, &pl);
+    int st = make_plan4(c, Hq, S, max_q_len, max_kv, window, num_splits, &pl);
     if (st) return st;
     if ((st = check_layer(c, layer))) return st;
     if (total_rows < 0 || window < 0 || (causal != 0 && causal != 1)) return PKV_EINVAL;
@@ -396,9 +424,15 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     if (S > 0 && (!seq_info || !aligned16(seq_info))) return PKV_EINVAL;
     if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return PKV_EINVAL;
     if (S == 0 && total_rows == 0) return PKV_OK;
+    if (workspace && (!aligned16(workspace) || workspace_bytes < 0)) return PKV_EINVAL;
+    const bool shares = pl.shares > 0 && workspace;
+    const Ws4Layout wl = ws4_layout(pl.shares, pl.k4.rows, c->head_dim);
+    if (shares && workspace_bytes < (long long)wl.total) return PKV_EINVAL;
+    if (check_only) return PKV_OK;
+    if (shares) pl.k.fn = pl.k4.balance;
     if ((st = prepare_kernel(pl.k))) return st;
-    int ncta = S == 0 ? 1 : schedulable_cluster(pl.k, pl.ncta);
-    if (S > 0 && num_splits == 0) ncta = wave_cluster(pl.k, pl.units, ncta);
+    int ncta = S == 0 || shares ? 1 : schedulable_cluster(pl.k, pl.ncta);
+    if (S > 0 && !shares && num_splits == 0) ncta = wave_cluster(pl.k, pl.units, ncta);
     Attend4Params p;
     p.k = reinterpret_cast<const unsigned char *>(c->k[layer]);
     p.v = reinterpret_cast<const unsigned char *>(c->v[layer]);
@@ -420,12 +454,23 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     p.ring_rows = c->ring_rows;
     p.max_q_len = max_q_len;
     p.row_tiles = pl.row_tiles;
+    p.min_pages = 4 * pl.k4.warps;  // four a warp
     p.causal = causal;
     p.window = window;
     p.out_bf16 = (flags & PKV_FLAG_OUT_BF16) ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.ws_head = nullptr;
+    p.ws_stat = nullptr;
+    p.ws_part = nullptr;
+    if (shares) {
+        char *base = reinterpret_cast<char *>(workspace);
+        p.ws_head = reinterpret_cast<int4 *>(base + wl.head);
+        p.ws_stat = reinterpret_cast<float2 *>(base + wl.stat);
+        p.ws_part = reinterpret_cast<float *>(base + wl.part);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = S == 0 ? dim3(1, 1, 1) : dim3((unsigned)ncta, (unsigned)(c->kv_heads * pl.row_tiles), (unsigned)S);
+    if (shares) cfg.gridDim = dim3((unsigned)pl.shares, 1, 1);
     cfg.blockDim = dim3((unsigned)pl.k.threads);
     cfg.dynamicSmemBytes = pl.k.smem;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
@@ -446,7 +491,17 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     cfg.attrs = na ? attr : nullptr;
     cfg.numAttrs = (unsigned)na;
     void *args[] = {&p};
-    return launch_status(cudaLaunchKernelExC(&cfg, pl.k.fn, args));
+    if ((st = launch_status(cudaLaunchKernelExC(&cfg, pl.k.fn, args))) || !shares) return st;
+    cudaLaunchConfig_t mc = {};
+    mc.gridDim = dim3((unsigned)pl.shares, (unsigned)(pl.G * max_q_len), 1);
+    mc.blockDim = dim3(kMerge4Threads);
+    mc.stream = cfg.stream;
+    cudaLaunchAttribute after;
+    after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    after.val.programmaticStreamSerializationAllowed = 1;
+    mc.attrs = &after;
+    mc.numAttrs = 1;
+    return launch_status(cudaLaunchKernelExC(&mc, pl.k4.merge, args));
 }
 
 // ---- norm + rotary + append
@@ -812,7 +867,7 @@ int pkv_attend_varlen(const pkv_cache *c, int32_t layer, const void *q, int32_t 
                       int64_t workspace_bytes, uint32_t *err, uint32_t flags, void *stream) {
     if (is_fp4(c))
         return attend4(c, layer, q, Hq, total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale, causal, window, out, lse,
-                       err, flags, stream);
+                       workspace, workspace_bytes, err, flags, stream);
     return attend_common(c, layer, q, nullptr, nullptr, Hq, total_rows, seq_info, S, max_q_len, max_kv,
                          num_splits, scale, causal, window, out, lse, workspace, workspace_bytes, err, flags,
                          stream);
@@ -825,18 +880,15 @@ int pkv_append_attend(const pkv_cache *c, int32_t layer, const void *q, const vo
                       uint32_t flags, void *stream) {
     if (total_rows > 0 && (!k_new || !v_new)) return PKV_EINVAL;
     if (is_fp4(c)) {
-        // Two launches.  The attention is checked first (a call with no rows of
-        // work launches nothing), so a refused call writes nothing.
-        Plan4 pl;
-        int st = make_plan4(c, Hq, S, max_q_len, max_kv, num_splits, &pl);
+        // The attention's arguments are checked first, so that a refused call writes nothing.
+        auto attend = [&](bool check_only) {
+            return attend4(c, layer, q, Hq, total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale, causal, window, out, lse,
+                           workspace, workspace_bytes, err, flags, stream, check_only);
+        };
+        int st = attend(true);
         if (st) return st;
-        if ((st = check_layer(c, layer))) return st;
-        if (total_rows < 0 || window < 0 || (causal != 0 && causal != 1) || !err || !out || !aligned16(out) ||
-            (total_rows > 0 && (!q || !aligned16(q))) || (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)))
-            return PKV_EINVAL;
         if ((st = pkv_append(c, layer, k_new, v_new, total_rows, seq_info, S, window, err, stream))) return st;
-        return attend4(c, layer, q, Hq, total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale, causal, window, out, lse,
-                       err, flags, stream);
+        return attend(false);
     }
     return attend_common(c, layer, q, total_rows > 0 ? k_new : nullptr, total_rows > 0 ? v_new : nullptr, Hq,
                          total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale, causal, window, out, lse,
@@ -874,7 +926,8 @@ int64_t pkv_attend_workspace_bytes(const pkv_cache *c, int32_t Hq, int32_t S, in
                                    int32_t num_splits, uint32_t flags) {
     if (is_fp4(c)) {  // 4-bit caches merge in the cluster
         Plan4 pl4;
-        return make_plan4(c, Hq, S, max_q_len, max_kv, num_splits, &pl4);
+        const int st = make_plan4(c, Hq, S, max_q_len, max_kv, 0, num_splits, &pl4);
+        return st ? st : pl4.shares ? (int64_t)ws4_layout(pl4.shares, pl4.k4.rows, c->head_dim).total : 0;
     }
     Plan pl;
     const int st = make_plan(c, Hq, S, max_q_len, max_kv, num_splits, flags, true, &pl);

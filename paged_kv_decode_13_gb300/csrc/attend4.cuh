@@ -31,17 +31,20 @@
 namespace pkv {
 
 constexpr int kWaitProbes4 = 1 << 20;  // probes of one barrier phase before PKV_ERR_TIMEOUT
+constexpr float kNoMax = -1e30f;       // reference maximum of a row that has seen no key
 constexpr float kLazy4 = 8.f;          // a row's reference maximum moves when a score passes it by 2^8
 
-template <int D_, int NT_, int KW_, int NST_, int CTAS_>
+template <int D_, int NT_, int KW_, int NST_, int PP_, int CTAS_, bool QSH_>
 struct Cfg4 {
     static constexpr int D = D_, NT = NT_, KW = KW_, NST = NST_, kCtas = CTAS_;
+    static constexpr int PP = PP_;                   // pages of a stage
     static constexpr int kThreads = KW * 32;
     static constexpr int R = 8 * NT;                 // query rows of a CTA
     static constexpr int kBlock = block4_bytes(D);   // K or V bytes of a page
-    static constexpr int kStage = 2 * kBlock;
+    static constexpr int kPageBytes = 2 * kBlock;    // a page's K block, then its V block
+    static constexpr int kStage = PP * kPageBytes;
     static constexpr int KS = D / 16;                // 16-wide steps of S, 16-row tiles of O
-    static constexpr bool kQShared = NT > 1;         // Q fragments in shared memory (else in registers)
+    static constexpr bool kQShared = QSH_;           // Q fragments in shared memory (else in registers)
     static constexpr int LD = D + 4;                 // padded row of a warp's partial
     static constexpr size_t kPartFloats = (size_t)R * LD + 2 * R;
     static constexpr size_t kPipe = (size_t)KW * NST * kStage;
@@ -54,6 +57,7 @@ struct Cfg4 {
     static constexpr size_t kRow = (size_t)R * 3 * 4;
     static constexpr size_t kBars = (size_t)KW * NST * 8;
     static constexpr size_t kSmem = 128 + kBody + kQBytes + kRecv + kStat + kWeight + kRow + kBars + 128;
+    static_assert(NT == 1 || kQShared, "wider tiles keep Q in shared memory");
     static_assert(kSmem <= 232448, "exceeds the per-CTA shared memory limit");
 };
 
@@ -69,6 +73,12 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], unsigned a0, unsign
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 2^x for x <= about 8; results below fp32's normal range are zero.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ unsigned transpose8x8(unsigned x) {
     unsigned y;
@@ -125,137 +135,141 @@ __device__ __noinline__ void coverage4(const Attend4Params &p) {
     }
 }
 
+// A piece of work: 8 NT rows of one (segment, kv head) against pages of its range.
+struct Piece4 {
+    Segment sg;
+    int h, row0, rows;           // kv head, first row of the tile, rows of it
+    int lo_u, hi_u;              // keys some row sees
+    int lo_in, hi_in;            // keys every row sees
+    int page0, pages;            // the piece's pages
+};
+
+// Shared memory of a CTA.
 template <class C>
-__global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __grid_constant__ Attend4Params p) {
-    namespace cg = cooperative_groups;
-    constexpr int D = C::D, NT = C::NT, KW = C::KW, NST = C::NST, KS = C::KS, R = C::R, LD = C::LD, NTHR = C::kThreads;
-    constexpr float kLn2 = 0.6931471805599453f;
+struct Smem4 {
+    unsigned char *pipe;         // the warps' stages; then their partials, [KW][R][LD] and (max, sum)
+    uint2 *q;                    // [NT][KS][32] Q fragments
+    float *recv;                 // partials pushed by the cluster
+    float2 *stat;                // [16][R]
+    float *w;                    // [R][16]
+    float *scale;                // [R]
+    int *lo, *hi;                // [R] key bounds of the rows
+    uint64_t *bars;              // [KW][NST]
+    int *flag, *all_flags;       // own flags (1 bad page, 2 timeout), the cluster's [16]
+    __device__ explicit Smem4(unsigned char *raw) {
+        pipe = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
+        q = reinterpret_cast<uint2 *>(pipe + C::kBody);
+        recv = reinterpret_cast<float *>(pipe + C::kBody + C::kQBytes);
+        stat = reinterpret_cast<float2 *>(reinterpret_cast<unsigned char *>(recv) + C::kRecv);
+        w = reinterpret_cast<float *>(stat + 16 * C::R);
+        scale = w + C::R * 16;
+        lo = reinterpret_cast<int *>(scale + C::R);
+        hi = lo + C::R;
+        bars = reinterpret_cast<uint64_t *>(hi + C::R);
+        flag = reinterpret_cast<int *>(bars + C::KW * C::NST);
+        all_flags = flag + 1;
+    }
+};
 
-    extern __shared__ unsigned char smem_raw[];
-    unsigned char *pipe = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    uint2 *sQ = reinterpret_cast<uint2 *>(pipe + C::kBody);                         // [NT][KS][32]
-    float *sRecv = reinterpret_cast<float *>(pipe + C::kBody + C::kQBytes);         // [ncl][per4] float4
-    float2 *sStat = reinterpret_cast<float2 *>(reinterpret_cast<unsigned char *>(sRecv) + C::kRecv);  // [16][R]
-    float *sW = reinterpret_cast<float *>(sStat + 16 * R);                          // [R][16]
-    float *sScale = sW + R * 16;                                                    // [R]
-    int *sLo = reinterpret_cast<int *>(sScale + R), *sHi = sLo + R;                 // [R]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sHi + R);                         // [KW][NST]
-    int *sFlag = reinterpret_cast<int *>(bars + KW * NST);                          // own flags: 1 bad page, 2 timeout
-    int *sAllF = sFlag + 1;                                                         // [16] flags of the cluster
+// The tile's key range: bounds grow with the row, so it is [lo of the first
+// row, hi of the last), and every row sees all of [lo of the last, hi of the first).
+__device__ __forceinline__ void piece_bounds(const Attend4Params &p, Piece4 &w) {
+    const int start = w.sg.kend - w.sg.ql, first = first_valid_of(p.first_valid, w.sg.col);
+    row_key_bounds(start + w.row0 / p.G, w.sg.kend, p.causal, p.window, first, w.lo_u, w.hi_in);
+    row_key_bounds(start + (w.row0 + w.rows - 1) / p.G, w.sg.kend, p.causal, p.window, first, w.lo_in, w.hi_u);
+    w.page0 = w.lo_u / kPage;
+    w.pages = (w.hi_u + kPage - 1) / kPage - w.page0;
+}
+__device__ __forceinline__ unsigned fault4(const Attend4Params &p, const Segment &sg) {
+    const unsigned f = segment_fault(sg, p.total_rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
+    return f ? f : sg.ql > p.max_q_len ? PKV_ERR_QLEN : 0u;
+}
+// A refused segment: its error, and zero rows of kv heads [h0, h1).
+template <int D>
+__device__ __forceinline__ void refuse4(const Attend4Params &p, const Segment &sg, unsigned fault, int h0, int h1) {
+    if (threadIdx.x == 0) atomicOr(p.err, fault);
+    if (sg.q0 >= 0)  // a negative q_start covers nothing
+        for (long long r = sg.q0; r < min((long long)sg.q0 + sg.ql, (long long)p.total_rows); ++r)
+            zero_row4(p, r, h0 * p.G, (h1 - h0) * p.G, D, threadIdx.x, blockDim.x);
+}
 
+// Attend one piece: every warp takes every KW-th of its pages and leaves its
+// partial rows and (max, sum) in shared memory.  ring: stages this warp has
+// used so far.  dep: the dependency wait happens in here, after the first
+// copies.  Returns the CTA's flags.
+template <class C>
+__device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<C> &sm, const Piece4 &w, int &ring, bool dep) {
+    constexpr int D = C::D, NT = C::NT, KW = C::KW, NST = C::NST, KS = C::KS, R = C::R, LD = C::LD, PP = C::PP;
     const int tid = threadIdx.x, kw = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
-    const int rank = blockIdx.x, ncta = gridDim.x;
-    const int tile = blockIdx.y % p.row_tiles, h = blockIdx.y / p.row_tiles, s = blockIdx.z;
-
-    if (p.S == 0) {
-        pdl_wait();
-        pdl_trigger();
-        coverage4<D>(p);
-        return;
-    }
-    // ---- the segment and this tile's key range (read before the dependency wait)
-    const Segment sg = load_segment(p.seq_info, s);
-    unsigned fault = segment_fault(sg, p.total_rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
-    if (!fault && sg.ql > p.max_q_len) fault = PKV_ERR_QLEN;
-    const int row0 = tile * R;
-    const int rows_here = fault ? 0 : min(R, sg.ql * p.G - row0);
-    if (rows_here <= 0) {  // uniform across the cluster
-        pdl_wait();
-        pdl_trigger();
-        if (fault && rank == 0) {
-            if (tid == 0) atomicOr(p.err, fault);
-            if (tile == 0 && sg.q0 >= 0)  // a negative q_start covers nothing
-                for (long long r = sg.q0; r < min((long long)sg.q0 + sg.ql, (long long)p.total_rows); ++r)
-                    zero_row4(p, r, h * p.G, p.G, D, tid, NTHR);
-        }
-        coverage4<D>(p);
-        return;
-    }
-    const int kend = sg.kend, new_start = kend - sg.ql;
-    const int first = first_valid_of(p.first_valid, sg.col);
-    // Bounds grow with the row: the tile's keys are [lo of its first row, hi of
-    // its last), and every row sees all of [lo of the last, hi of the first).
-    int lo_u, hi_u, lo_in, hi_in;
-    row_key_bounds(new_start + row0 / p.G, kend, p.causal, p.window, first, lo_u, hi_in);
-    row_key_bounds(new_start + (row0 + rows_here - 1) / p.G, kend, p.causal, p.window, first, lo_in, hi_u);
-    const int pb_begin = lo_u / kPage, pb_end = (hi_u + kPage - 1) / kPage, nblk = pb_end - pb_begin;
-    // A range of a few pages a warp runs on one CTA, without the cluster's merge.
-    const bool solo = nblk <= kSolo4 * KW;
-    const int ncl = solo ? 1 : ncta;
-    if (rank >= ncl) {
-        pdl_wait();
-        pdl_trigger();
-        coverage4<D>(p);
-        return;
-    }
-    const int bps = (nblk + ncl - 1) / ncl;
-    const int cb0 = pb_begin + rank * bps;
-    const int nb = max(0, min(bps, pb_end - cb0));
+    const Segment &sg = w.sg;
+    const int h = w.h, row0 = w.row0, rows_here = w.rows, kend = sg.kend, new_start = kend - sg.ql;
+    const int lo_u = w.lo_u, hi_u = w.hi_u, lo_in = w.lo_in, hi_in = w.hi_in, cb0 = w.page0, nb = w.pages;
     const int n_mine = nb > kw ? (nb - kw + KW - 1) / KW : 0;
-    if (ncl > 1)  // announce this CTA to the cluster; waited on before any remote store
-        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
-
-    const int *bt_row = p.block_table + (long long)sg.col * p.mbps;
-    uint64_t *wbars = bars + kw * NST;
+    uint2 *sQ = sm.q;
+    float *sScale = sm.scale;
+    int *sLo = sm.lo, *sHi = sm.hi, *sFlag = sm.flag;
+    unsigned char *pipe = sm.pipe;
+    uint64_t *wbars = sm.bars + kw * NST;
     unsigned char *wstage = pipe + (size_t)kw * NST * C::kStage;
-    if (lane == 0) {
-#pragma unroll 1
-        for (int i = 0; i < NST; ++i) mbar_init(wbars + i, 1);
-        fence_barrier_init();
-    }
+    const int *bt_row = p.block_table + (long long)sg.col * p.mbps;
     if (tid == 0) sFlag[0] = 0;
     if (tid < R) {
         int lo = 0, hi = 0;  // padding rows see no key
-        if (tid < rows_here) row_key_bounds(new_start + (row0 + tid) / p.G, kend, p.causal, p.window, first, lo, hi);
+        if (tid < rows_here)
+            row_key_bounds(new_start + (row0 + tid) / p.G, kend, p.causal, p.window, first_valid_of(p.first_valid, sg.col), lo, hi);
         sLo[tid] = lo;
         sHi[tid] = hi;
     }
     __syncthreads();
 
-    // ---- page ids and copies (lane l holds the id of the warp's page window + l)
+    // ---- page ids and copies.  The warp's j-th stage is its pages j PP .. (j + 1) PP - 1;
+    // lane l holds the id of its page window + l.
+    const int stages = (n_mine + PP - 1) / PP, base = ring;
     int id_reg = -1, id_window = -1;
     bool bad = false, timed_out = false;
+    const unsigned char *copy_base = ((lane & 1) ? p.v : p.k) + (size_t)h * C::kBlock;
+    const size_t block_stride = (size_t)p.Hkv * C::kBlock;
+    auto slot = [&](int j) { return (base + j) % NST; };
     auto issue = [&](int j) {
-        if ((j & ~31) != id_window) {
-            id_window = j & ~31;
+        const int j0 = j * PP;
+        if ((j0 & ~31) != id_window) {
+            id_window = j0 & ~31;
             const int li = kw + (id_window + lane) * KW;
             id_reg = li < nb ? bt_row[table_page(cb0 + li, p.ring_rows)] : -1;
         }
-        const int bid = __shfl_sync(0xffffffffu, id_reg, j & 31);
-        const bool ok = bid >= 0 && (long long)bid < p.num_blocks;
-        bad |= !ok;
-        if (lane == 0) {
-            uint64_t *bar = wbars + j % NST;
-            unsigned char *st = wstage + (size_t)(j % NST) * C::kStage;
-            if (ok) {
-                const size_t at = ((size_t)bid * p.Hkv + h) * C::kBlock;
-                fence_proxy_async();  // the stage was read through the generic proxy
-                mbar_expect_tx(bar, C::kStage);
-                bulk_load(st, p.k + at, C::kBlock, bar);
-                bulk_load(st + C::kBlock, p.v + at, C::kBlock, bar);
+        // lane 2 e copies the stage's e-th K block, lane 2 e + 1 its V block
+        const int bid = __shfl_sync(0xffffffffu, id_reg, (j0 + (lane >> 1)) & 31);
+        if (lane < 2 * PP) {
+            const bool some = j0 + (lane >> 1) < n_mine, ok = (unsigned)bid < (unsigned)p.num_blocks;
+            bad |= some && !ok;
+            uint64_t *bar = wbars + slot(j);
+            if (some && ok) {
+                mbar_expect_tx(bar, C::kBlock);
+                bulk_load(wstage + (size_t)slot(j) * C::kStage + lane * C::kBlock, copy_base + (unsigned)bid * block_stride, C::kBlock, bar);
             } else {
-                mbar_arrive(bar);  // nothing to fetch: the result is discarded
+                mbar_arrive(bar);  // nothing to fetch; after a bad page the result is discarded
             }
         }
     };
-    auto wait_page = [&](int j) {
-        if (timed_out) return;
-        bool done = false;
+    auto wait_stage = [&](int j) {
+        const unsigned parity = ((base + j) / NST) & 1;
+        if (mbar_try_wait(wbars + slot(j), parity)) return;
+        bool done = timed_out;
 #pragma unroll 1
-        for (int it = 0; it < kWaitProbes4 && !done; ++it) done = mbar_try_wait(wbars + j % NST, (j / NST) & 1);
-        if (!__all_sync(0xffffffffu, done)) timed_out = true;
+        for (int it = 0; it < kWaitProbes4 && !done; ++it) done = mbar_try_wait(wbars + slot(j), parity);
+        timed_out |= !done;
     };
-    // Pages wholly below this step's rows are in the cache already, whatever
-    // the kernel before this one still writes.
     int issued = 0;
+    if (dep) {
+        // Pages wholly below this step's rows are in the cache already, whatever
+        // the kernel before this one still writes.
 #pragma unroll 1
-    for (; issued < NST && issued < n_mine && (cb0 + kw + issued * KW + 1) * kPage <= new_start; ++issued) issue(issued);
-
-    pdl_wait();
-    pdl_trigger();
-
+        for (; issued < NST && issued < stages && (cb0 + kw + (issued * PP + PP - 1) * KW + 1) * kPage <= new_start; ++issued) issue(issued);
+        pdl_wait();
+        pdl_trigger();
+    }
 #pragma unroll 1
-    for (; issued < NST && issued < n_mine; ++issued) issue(issued);
+    for (; issued < NST && issued < stages; ++issued) issue(issued);
 
     // ---- Q^T fragments of one 8-row tile: lane (g, t) holds row g, columns t D/4 ..
     auto load_q = [&](int nt, unsigned (&f)[KS][2]) {
@@ -310,49 +324,45 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
     float m_r[NT][2], l_r[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        m_r[nt][0] = m_r[nt][1] = -CUDART_INF_F;
+        m_r[nt][0] = m_r[nt][1] = kNoMax;
         l_r[nt][0] = l_r[nt][1] = 0.f;
 #pragma unroll
         for (int i = 0; i < KS; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
     }
 #pragma unroll 1
-    for (int j = 0; j < n_mine; ++j) {
-        const unsigned char *st = wstage + (size_t)(j % NST) * C::kStage;
-        const int pos0 = (cb0 + kw + j * KW) * kPage;
-        wait_page(j);
-        // S^T: lane (g, t) holds tokens g and g + 8, columns t D/4 ..
-        float sa[NT][4], sb[NT][4];
+    for (int j = 0; j < stages; ++j) {
+        const unsigned char *stage = wstage + (size_t)slot(j) * C::kStage;
+        const int pos_first = (cb0 + kw + j * PP * KW) * kPage;  // position of the stage's first page; the next ones follow KW pages on
+        const int pages = min(PP, n_mine - j * PP);
+        wait_stage(j);
+        // S^T: lane (g, t) holds tokens g and g + 8, columns t D/4 ..  (A stage's
+        // missing last page holds whatever was there: its scores and scales are masked.)
+        float sa[PP][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int e = 0; e < PP; ++e) {
+            const unsigned char *st = stage + e * C::kPageBytes;
+            // One accumulation chain a page and tile; a lone one is split in two.
+            constexpr bool kTwo = PP * NT == 1;
+            float sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sa[nt][e] = sb[nt][e] = 0.f;
-        {
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sa[e][nt][i] = 0.f;
             constexpr int W = D / 32;  // code words of a token and lane
             unsigned ka[W], kb[W];
             lds_words<W>(ka, st + gq * (D / 2) + tq * (D / 8));
             lds_words<W>(kb, st + (gq + 8) * (D / 2) + tq * (D / 8));
-            unsigned wa, wb;  // scale bytes of the two tokens
-            const unsigned char *ss = st + 8 * D + gq * (D / 16) + tq * (D / 64);
-            if constexpr (D == 64) {
-                wa = ss[0];
-                wb = ss[8 * (D / 16)];
-            } else if constexpr (D == 128) {
-                wa = *reinterpret_cast<const unsigned short *>(ss);
-                wb = *reinterpret_cast<const unsigned short *>(ss + 8 * (D / 16));
-            } else {
-                wa = *reinterpret_cast<const unsigned *>(ss);
-                wb = *reinterpret_cast<const unsigned *>(ss + 8 * (D / 16));
-            }
+            const unsigned char *ss = st + 8 * D + gq * (D / 16) + tq * (D / 64);  // scale bytes of the two tokens
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                const unsigned fa = scale4_both(wa, w / 2), fb = scale4_both(wb, w / 2);
+                const unsigned fa = scale4_both(ss[w / 2]), fb = scale4_both(ss[w / 2 + D / 2]);
                 unsigned a[4], b[4];
                 unpack_e2m1x8(a, ka[w]);
                 unpack_e2m1x8(b, kb[w]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    a[e] = hmul2(a[e], fa);
-                    b[e] = hmul2(b[e], fb);
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = hmul2(a[i], fa);
+                    b[i] = hmul2(b[i], fb);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -364,57 +374,78 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
                         q0 = make_uint2(qf[2 * w][0], qf[2 * w][1]);
                         q1 = make_uint2(qf[2 * w + 1][0], qf[2 * w + 1][1]);
                     }
-                    mma_f16_16816(sa[nt], a[0], b[0], a[1], b[1], q0.x, q0.y);
-                    mma_f16_16816(sb[nt], a[2], b[2], a[3], b[3], q1.x, q1.y);
+                    mma_f16_16816(sa[e][nt], a[0], b[0], a[1], b[1], q0.x, q0.y);
+                    if constexpr (kTwo) mma_f16_16816(sb, a[2], b[2], a[3], b[3], q1.x, q1.y);
+                    else mma_f16_16816(sa[e][nt], a[2], b[2], a[3], b[3], q1.x, q1.y);
                 }
             }
+            if constexpr (kTwo)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sa[e][0][i] += sb[i];
         }
         // Online softmax (base 2) with a lazy maximum: this lane has tokens g,
-        // g + 8 of rows 2t, 2t + 1.
-        const bool inside = pos0 >= lo_in && pos0 + kPage <= hi_in;
-        unsigned pb[NT][2];
+        // g + 8 of rows 2t, 2t + 1.  x = score - reference; the reference moves
+        // only when some x passes 2^kLazy4.
+        const bool inside = pages == PP && pos_first >= lo_in && pos_first + (PP - 1) * KW * kPage + kPage <= hi_in;
+        unsigned pb[PP][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float v[4];
+            float x[PP][4], top = -CUDART_INF_F;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = (sa[nt][e] + sb[nt][e]) * sc[nt][e & 1];
+            for (int e = 0; e < PP; ++e)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[e][i] = fmaf(sa[e][nt][i], sc[nt][i & 1], -m_r[nt][i & 1]);
             if (!inside) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int key = pos0 + gq + (e >> 1) * 8, r = nt * 8 + 2 * tq + (e & 1);
-                    if (key < sLo[r] || key >= sHi[r]) v[e] = -CUDART_INF_F;
+                for (int e = 0; e < PP; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = pos_first + e * KW * kPage + gq + (i >> 1) * 8, r = nt * 8 + 2 * tq + (i & 1);
+                        if (e >= pages || key < sLo[r] || key >= sHi[r]) x[e][i] = -CUDART_INF_F;
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < PP; ++e) top = fmaxf(top, fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3])));
+            if (__any_sync(0xffffffffu, top > kLazy4)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float mx = m_r[nt][i];
+#pragma unroll
+                    for (int e = 0; e < PP; ++e)
+#pragma unroll
+                        for (int o = 0; o < 4; o += 2)
+                            if (x[e][i + o] != -CUDART_INF_F) mx = fmaxf(mx, sa[e][nt][i + o] * sc[nt][i]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    const float al = ex2(m_r[nt][i] - mx);
+                    m_r[nt][i] = mx;
+                    l_r[nt][i] *= al;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        acc[nt][k][i] *= al;
+                        acc[nt][k][i + 2] *= al;
+                    }
+#pragma unroll
+                    for (int e = 0; e < PP; ++e)
+#pragma unroll
+                        for (int o = 0; o < 4; o += 2)
+                            if (x[e][i + o] != -CUDART_INF_F) x[e][i + o] = fmaf(sa[e][nt][i + o], sc[nt][i], -mx);
                 }
             }
-            float mx0 = fmaxf(v[0], v[2]), mx1 = fmaxf(v[1], v[3]);
-            if (__any_sync(0xffffffffu, mx0 > m_r[nt][0] + kLazy4 || mx1 > m_r[nt][1] + kLazy4)) {
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-                }
-                const float mn0 = fmaxf(m_r[nt][0], mx0), mn1 = fmaxf(m_r[nt][1], mx1);
-                const float al0 = mn0 == -CUDART_INF_F ? 1.f : exp2f(m_r[nt][0] - mn0);
-                const float al1 = mn1 == -CUDART_INF_F ? 1.f : exp2f(m_r[nt][1] - mn1);
-                m_r[nt][0] = mn0;
-                m_r[nt][1] = mn1;
-                l_r[nt][0] *= al0;
-                l_r[nt][1] *= al1;
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    acc[nt][i][0] *= al0; acc[nt][i][1] *= al1;
-                    acc[nt][i][2] *= al0; acc[nt][i][3] *= al1;
-                }
+            for (int e = 0; e < PP; ++e) {
+                const float p00 = ex2(x[e][0]), p01 = ex2(x[e][1]), p10 = ex2(x[e][2]), p11 = ex2(x[e][3]);
+                l_r[nt][0] += p00 + p10;
+                l_r[nt][1] += p01 + p11;
+                pb[e][nt][0] = transpose8x8(pack_f16x2(p00, p01));
+                pb[e][nt][1] = transpose8x8(pack_f16x2(p10, p11));
             }
-            const float mu0 = m_r[nt][0] == -CUDART_INF_F ? 0.f : m_r[nt][0], mu1 = m_r[nt][1] == -CUDART_INF_F ? 0.f : m_r[nt][1];
-            const float p00 = exp2f(v[0] - mu0), p01 = exp2f(v[1] - mu1), p10 = exp2f(v[2] - mu0), p11 = exp2f(v[3] - mu1);
-            l_r[nt][0] += p00 + p10;
-            l_r[nt][1] += p01 + p11;
-            pb[nt][0] = transpose8x8(pack_f16x2(p00, p01));
-            pb[nt][1] = transpose8x8(pack_f16x2(p10, p11));
         }
         // O^T += V^T P^T: lane (g, t) holds columns g D/8 .., tokens 2t, 2t + 1, 2t + 8, 2t + 9
-        {
-            const unsigned char *sv = st + C::kBlock;
+#pragma unroll
+        for (int e = 0; e < PP; ++e) {
+            const int pos0 = pos_first + e * KW * kPage;
+            const unsigned char *sv = stage + e * C::kPageBytes + C::kBlock;
             unsigned fa = 0, fb = 0;
 #pragma unroll
             for (int pl = 0; pl < D / 64; ++pl) {
@@ -427,11 +458,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
                         // see it are set to NaN in the columns it scales.
                         unsigned keep = 0, nan = 0;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = pos0 + 2 * tq + (e >> 1) * 8 + (e & 1);
-                            const unsigned m = 0xffu << (8 * e);
-                            if (key >= lo_u && key < hi_u) {
-                                if ((w & m) >= (0xf8u << (8 * e))) nan |= m;
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = pos0 + 2 * tq + (i >> 1) * 8 + (i & 1);
+                            const unsigned m = 0xffu << (8 * i);
+                            if (e < pages && key >= lo_u && key < hi_u) {
+                                if ((w & m) >= (0xf8u << (8 * i))) nan |= m;
                                 else keep |= m;
                             }
                         }
@@ -444,12 +475,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const int r = nt * 8 + 2 * tq + e;
+                                    for (int i = 0; i < 2; ++i) {
+                                        const int r = nt * 8 + 2 * tq + i;
                                         if (pos0 + o >= sLo[r] && pos0 + o < sHi[r])
 #pragma unroll
                                             for (int k = pl * 4; k < (pl + 2 < D / 64 ? pl + 2 : D / 64) * 4; ++k)
-                                                acc[nt][k][e] = acc[nt][k][e + 2] = CUDART_NAN_F;
+                                                acc[nt][k][i] = acc[nt][k][i + 2] = CUDART_NAN_F;
                                     }
                             }
                         }
@@ -465,19 +496,21 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
                     unpack_e2m1x8(x, vw[k]);  // (column 0: tokens 2t.., 2t+8..), (column 1: ..)
                     const unsigned a0 = hmul2(x[0], fa), a2 = hmul2(x[1], fb), a1 = hmul2(x[2], fa), a3 = hmul2(x[3], fb);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[nt][pl * 4 + k], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[nt][pl * 4 + k], a0, a1, a2, a3, pb[e][nt][0], pb[e][nt][1]);
                 }
             }
         }
         __syncwarp();  // every lane is done with the stage
-        if (j + NST < n_mine) issue(j + NST);
+        if (j + NST < stages) issue(j + NST);
     }
+    timed_out = __any_sync(0xffffffffu, timed_out);
+    bad = __any_sync(0xffffffffu, bad);
     if (timed_out && lane == 0) {
         // copies still in flight get a bounded chance to land before the stages are reused
 #pragma unroll 1
-        for (int j = max(0, n_mine - NST); j < n_mine; ++j)
+        for (int j = max(0, stages - NST); j < stages; ++j)
 #pragma unroll 1
-            for (int it = 0; it < kWaitProbes4 && !mbar_try_wait(wbars + j % NST, (j / NST) & 1); ++it) {
+            for (int it = 0; it < kWaitProbes4 && !mbar_try_wait(wbars + slot(j), ((base + j) / NST) & 1); ++it) {
             }
     }
     if ((bad || timed_out) && lane == 0) atomicOr(sFlag, (bad ? 1 : 0) | (timed_out ? 2 : 0));
@@ -494,7 +527,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-            if (m_r[nt][e] == -CUDART_INF_F && l_r[nt][e] != l_r[nt][e]) m_r[nt][e] = 0.f;
+            if (m_r[nt][e] == kNoMax) m_r[nt][e] = l_r[nt][e] != l_r[nt][e] ? 0.f : -CUDART_INF_F;
     // ---- the warps' partials, over the idle stages of all of them
     __syncthreads();
     {
@@ -516,93 +549,378 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
             }
         }
     }
+    ring = base + stages;
     __syncthreads();
-    const int flags = sFlag[0];
-    if (tid == 0 && flags) atomicOr(p.err, ((flags & 1) ? PKV_ERR_BLOCK : 0u) | ((flags & 2) ? PKV_ERR_TIMEOUT : 0u));
-    auto out_row = [&](int r) {
-        const int i = (row0 + r) / p.G, jh = (row0 + r) % p.G;
-        return ((long long)sg.q0 + i) * p.Hq + (long long)h * p.G + jh;
-    };
-    cg::cluster_group cluster = cg::this_cluster();
-    const int items = rows_here * (D / 4), per4 = (items + ncl - 1) / ncl;
-    if (ncl > 1) {
-        asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");  // every CTA of the cluster runs
-        if (tid < ncl) *cluster.map_shared_rank(sAllF + rank, tid) = flags;
+    return sFlag[0];
+}
+
+// The warps' partials of row r, columns 4 c4 .. + 3, merged: unnormalised sum, max and sum of weights.
+template <class C>
+__device__ __forceinline__ float4 merge_warps(const Smem4<C> &sm, int r, int c4, float &M, float &L) {
+    constexpr int KW = C::KW, R = C::R, LD = C::LD;
+    const float *base = reinterpret_cast<const float *>(sm.pipe);
+    float mk[KW];
+    M = -CUDART_INF_F;
+#pragma unroll
+    for (int k = 0; k < KW; ++k) {
+        mk[k] = base[k * C::kPartFloats + R * LD + r];
+        M = fmaxf(M, mk[k]);
     }
+    L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < KW; ++k) {
+        // a warp that saw no key of the row has weight 0 and a zero accumulator
+        const float w = mk[k] == -CUDART_INF_F ? 0.f : ex2(mk[k] - M);
+        const float4 v = *reinterpret_cast<const float4 *>(base + k * C::kPartFloats + r * LD + 4 * c4);
+        L = fmaf(w, base[k * C::kPartFloats + R * LD + R + r], L);
+        o.x = fmaf(w, v.x, o.x);
+        o.y = fmaf(w, v.y, o.y);
+        o.z = fmaf(w, v.z, o.z);
+        o.w = fmaf(w, v.w, o.w);
+    }
+    return o;
+}
+__device__ __forceinline__ long long out_row4(const Attend4Params &p, const Piece4 &w, int r) {
+    const int i = (w.row0 + r) / p.G, jh = (w.row0 + r) % p.G;
+    return ((long long)w.sg.q0 + i) * p.Hq + (long long)w.h * p.G + jh;
+}
+// One CTA held the whole range: its rows are final.
+template <class C>
+__device__ __forceinline__ void write_rows4(const Attend4Params &p, const Smem4<C> &sm, const Piece4 &w, int flags) {
+    constexpr int D = C::D;
+#pragma unroll 1
+    for (int e = threadIdx.x; e < w.rows * (D / 4); e += C::kThreads) {
+        const int r = e / (D / 4), c4 = e % (D / 4);
+        float M, L;
+        const float4 o = merge_warps<C>(sm, r, c4, M, L);
+        const bool zero = flags || L == 0.f;  // a NaN sum stays: the row holds a NaN
+        const float inv = 1.f / L;
+        const long long row = out_row4(p, w, r);
+        store_out4(p, row * D + 4 * c4, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        if (c4 == 0 && p.lse) p.lse[row] = zero ? -CUDART_INF_F : (M + log2f(L)) * 0.6931471805599453f;
+    }
+}
+__device__ __forceinline__ void report4(const Attend4Params &p, int flags) {
+    if (threadIdx.x == 0 && flags) atomicOr(p.err, ((flags & 1) ? PKV_ERR_BLOCK : 0u) | ((flags & 2) ? PKV_ERR_TIMEOUT : 0u));
+}
+template <class C>
+__device__ __forceinline__ void init_bars4(const Smem4<C> &sm) {
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll 1
+        for (int i = 0; i < C::NST; ++i) mbar_init(sm.bars + (threadIdx.x >> 5) * C::NST + i, 2 * C::PP);  // one arrival a copy
+        fence_barrier_init();
+    }
+}
+
+// ---------------------------------------------------------------- one cluster per range
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __grid_constant__ Attend4Params p) {
+    namespace cg = cooperative_groups;
+    constexpr int D = C::D, R = C::R, NTHR = C::kThreads;
+    extern __shared__ unsigned char smem_raw[];
+    const Smem4<C> sm(smem_raw);
+    const int tid = threadIdx.x, rank = blockIdx.x, ncta = gridDim.x;
+    const int tile = blockIdx.y % p.row_tiles, s = blockIdx.z;
+    auto leave = [&] {
+        pdl_wait();
+        pdl_trigger();
+        coverage4<D>(p);
+    };
+    if (p.S == 0) return leave();
+    // the segment and this tile's key range are read before the dependency wait
+    Piece4 w;
+    w.h = blockIdx.y / p.row_tiles;
+    w.sg = load_segment(p.seq_info, s);
+    const unsigned fault = fault4(p, w.sg);
+    w.row0 = tile * R;
+    w.rows = fault ? 0 : min(R, w.sg.ql * p.G - w.row0);
+    if (w.rows <= 0) {  // uniform across the cluster
+        pdl_wait();
+        pdl_trigger();
+        if (fault && rank == 0 && tile == 0) refuse4<D>(p, w.sg, fault, w.h, w.h + 1);
+        coverage4<D>(p);
+        return;
+    }
+    piece_bounds(p, w);
+    // Short ranges take fewer CTAs than the cluster has: each gets a number of
+    // pages that is worth its share of the merge.
+    const int nblk = w.pages, ncl = min(ncta, max(1, (nblk + p.min_pages / 2) / p.min_pages));
+    if (rank >= ncl) return leave();
+    const int bps = (nblk + ncl - 1) / ncl;
+    w.page0 += rank * bps;
+    w.pages = max(0, min(bps, nblk - rank * bps));
+    if (ncl > 1)  // announce this CTA to the cluster; waited on before any remote store
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
+    init_bars4<C>(sm);
+    int ring = 0;
+    const int flags = attend_piece<C>(p, sm, w, ring, true);
+    report4(p, flags);
+    if (ncl == 1) {
+        write_rows4<C>(p, sm, w, flags);
+        coverage4<D>(p);
+        return;
+    }
+    // ---- merge across the cluster: every CTA pushes its merged partial of each
+    // output slice to the CTA that finishes it
+    cg::cluster_group cluster = cg::this_cluster();
+    const int items = w.rows * (D / 4), per4 = (items + ncl - 1) / ncl;
+    asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");  // every CTA of the cluster runs
+    if (tid < ncl) *cluster.map_shared_rank(sm.all_flags + rank, tid) = flags;
 #pragma unroll 1
     for (int e = tid; e < items; e += NTHR) {
-        const int r = e / (D / 4), c4 = e % (D / 4);
-        const float *base = reinterpret_cast<const float *>(pipe);
-        float mk[KW], M = -CUDART_INF_F;
-#pragma unroll
-        for (int k = 0; k < KW; ++k) {
-            mk[k] = base[k * C::kPartFloats + R * LD + r];
-            M = fmaxf(M, mk[k]);
-        }
-        float L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < KW; ++k) {
-            // a warp that saw no key of the row has weight 0 and a zero accumulator
-            const float w = mk[k] == -CUDART_INF_F ? 0.f : exp2f(mk[k] - M);
-            const float4 v = *reinterpret_cast<const float4 *>(base + k * C::kPartFloats + r * LD + 4 * c4);
-            L = fmaf(w, base[k * C::kPartFloats + R * LD + R + r], L);
-            o.x = fmaf(w, v.x, o.x);
-            o.y = fmaf(w, v.y, o.y);
-            o.z = fmaf(w, v.z, o.z);
-            o.w = fmaf(w, v.w, o.w);
-        }
-        if (ncl == 1) {
-            const bool zero = flags || L == 0.f;  // a NaN sum stays: the row holds a NaN
-            const float inv = 1.f / L;
-            const long long row = out_row(r);
-            store_out4(p, row * D + 4 * c4, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-            if (c4 == 0 && p.lse) p.lse[row] = zero ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
-        } else {
-            const int owner = e / per4;
-            *cluster.map_shared_rank(reinterpret_cast<float4 *>(sRecv) + rank * per4 + (e - owner * per4), owner) = o;
-            if (c4 < ncl) *cluster.map_shared_rank(sStat + rank * R + r, c4) = make_float2(M, L);
-        }
+        const int r = e / (D / 4), c4 = e % (D / 4), owner = e / per4;
+        float M, L;
+        const float4 o = merge_warps<C>(sm, r, c4, M, L);
+        *cluster.map_shared_rank(reinterpret_cast<float4 *>(sm.recv) + rank * per4 + (e - owner * per4), owner) = o;
+        if (c4 < ncl) *cluster.map_shared_rank(sm.stat + rank * R + r, c4) = make_float2(M, L);
     }
-    if (ncl > 1) {
-        cluster.sync();  // publishes every CTA's partials
-        int poison = 0;
+    cluster.sync();  // publishes every CTA's partials
+    int poison = 0;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) poison |= c < ncl ? sAllF[c] : 0;
+    for (int c = 0; c < 16; ++c) poison |= c < ncl ? sm.all_flags[c] : 0;
 #pragma unroll 1
-        for (int b = 0; b < R * 16; b += NTHR) {  // row, source CTA: normalised weights by 16-lane shuffles
-            const int r = (b + tid) >> 4, c = tid & 15;
-            const float2 stt = c < ncl && r < rows_here ? sStat[c * R + r] : make_float2(-CUDART_INF_F, 0.f);
-            float M = stt.x;
+    for (int b = 0; b < R * 16; b += NTHR) {  // row, source CTA: normalised weights by 16-lane shuffles
+        const int r = (b + tid) >> 4, c = tid & 15;
+        const float2 stt = c < ncl && r < w.rows ? sm.stat[c * R + r] : make_float2(-CUDART_INF_F, 0.f);
+        float M = stt.x;
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            const float w = stt.x == -CUDART_INF_F ? 0.f : exp2f(stt.x - M);
-            float W = w * stt.y;
+        for (int o = 1; o < 16; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float wt = stt.x == -CUDART_INF_F ? 0.f : ex2(stt.x - M);
+        float W = wt * stt.y;
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
-            const bool zero = poison || W == 0.f;
-            if (b + tid < R * 16) sW[r * 16 + c] = zero ? 0.f : w / W;
-            if (c == 0 && r < rows_here && rank == 0 && p.lse) p.lse[out_row(r)] = zero ? -CUDART_INF_F : (M + log2f(W)) * kLn2;
-        }
-        __syncthreads();
+        for (int o = 1; o < 16; o <<= 1) W += __shfl_xor_sync(0xffffffffu, W, o);
+        const bool zero = poison || W == 0.f;
+        if (b + tid < R * 16) sm.w[r * 16 + c] = zero ? 0.f : wt / W;
+        if (c == 0 && r < w.rows && rank == 0 && p.lse) p.lse[out_row4(p, w, r)] = zero ? -CUDART_INF_F : (M + log2f(W)) * 0.6931471805599453f;
+    }
+    __syncthreads();
 #pragma unroll 1
-        for (int e = tid; e < per4 && rank * per4 + e < items; e += NTHR) {
-            const int r = (rank * per4 + e) / (D / 4), c4 = (rank * per4 + e) % (D / 4);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = 0; c < ncl; ++c) {
-                const float w = sW[r * 16 + c];
-                const float4 v = reinterpret_cast<const float4 *>(sRecv)[c * per4 + e];
-                if (w != 0.f) {  // a zero weight must not touch its partial: a poisoned one may hold NaN
-                    o.x = fmaf(w, v.x, o.x);
-                    o.y = fmaf(w, v.y, o.y);
-                    o.z = fmaf(w, v.z, o.z);
-                    o.w = fmaf(w, v.w, o.w);
-                }
+    for (int e = tid; e < per4 && rank * per4 + e < items; e += NTHR) {
+        const int r = (rank * per4 + e) / (D / 4), c4 = (rank * per4 + e) % (D / 4);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < ncl; ++c) {
+            const float wt = sm.w[r * 16 + c];
+            const float4 v = reinterpret_cast<const float4 *>(sm.recv)[c * per4 + e];
+            if (wt != 0.f) {  // a zero weight must not touch its partial: a poisoned one may hold NaN
+                o.x = fmaf(wt, v.x, o.x);
+                o.y = fmaf(wt, v.y, o.y);
+                o.z = fmaf(wt, v.z, o.z);
+                o.w = fmaf(wt, v.w, o.w);
             }
-            store_out4(p, out_row(r) * D + 4 * c4, o);
         }
+        store_out4(p, out_row4(p, w, r) * D + 4 * c4, o);
     }
     coverage4<D>(p);
+}
+
+// ---------------------------------------------------------------- equal shares of all ranges
+
+// With a workspace the ranges (one row tile each) are laid end to end, T
+// pages in all, and the one wave of CTAs the device holds takes equal shares:
+// CTA i pages [i T / N, (i + 1) T / N).  A range that one CTA holds whole is
+// written at once; of a range that several share, each leaves its rows and
+// (max, sum) in the workspace, slot 2 i + 1 where the range begins in CTA i and
+// slot 2 i where it continues, and a second launch merges them.  Clusters
+// need their CTAs free at the same time in one GPC, and a fixed number of
+// them splits long and short ranges alike; shares have neither limit.
+__device__ __forceinline__ long long share_begin(long long i, long long T, int N) { return i * T / N; }
+
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, C::kCtas) balance4_kernel(const __grid_constant__ Attend4Params p) {
+    constexpr int D = C::D, R = C::R, NTHR = C::kThreads;
+    extern __shared__ unsigned char smem_raw[];
+    const Smem4<C> sm(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x;
+    init_bars4<C>(sm);
+    // ---- prefix sum of the segments' pages; thread t holds segments t per ..
+    auto piece_of = [&](int s, Piece4 &w) {
+        w.sg = load_segment(p.seq_info, s);
+        w.row0 = 0;
+        w.rows = fault4(p, w.sg) ? 0 : w.sg.ql * p.G;
+        w.pages = 0;
+        if (w.rows > 0) piece_bounds(p, w);
+    };
+    const int per = (p.S + NTHR - 1) / NTHR, s_lo = min(tid * per, p.S), s_hi = min(s_lo + per, p.S);
+    long long mine = 0;
+#pragma unroll 4
+    for (int s = s_lo; s < s_hi; ++s) {
+        Piece4 w;
+        piece_of(s, w);
+        mine += (long long)w.pages * p.Hkv;
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    long long *sSum = reinterpret_cast<long long *>(sm.recv);
+    if (lane == 31) sSum[tid >> 5] = upto;
+    __syncthreads();
+    long long T = 0;
+#pragma unroll
+    for (int k = 0; k < C::KW; ++k) {
+        if (k < tid >> 5) upto += sSum[k];
+        T += sSum[k];
+    }
+    const int N = (int)max(1ll, min((long long)gridDim.x, T / p.min_pages));
+    const long long a = share_begin(cta, T, N), b = cta < N ? share_begin(cta + 1, T, N) : a;
+    int *sFind = reinterpret_cast<int *>(sSum + C::KW);  // the segment that holds page a, and where it begins
+    long long *sBegin = sSum + C::KW + 1;
+    if (cta < N && upto - mine <= a && a < upto) {
+        long long at = upto - mine;
+        int s = s_lo;
+#pragma unroll 1
+        for (; s < s_hi; ++s) {
+            Piece4 w;
+            piece_of(s, w);
+            const long long n = (long long)w.pages * p.Hkv;
+            if (a < at + n) break;
+            at += n;
+        }
+        sFind[0] = s;
+        *sBegin = at;
+    }
+    __syncthreads();
+    int s = sFind[0], ring = 0;
+    long long begin = *sBegin;
+    bool waited = false;
+    int left = 0;  // bit i: a piece in slot 2 cta + i
+    __syncthreads();  // sm.recv is free again
+#pragma unroll 1
+    for (long long at = a; at < b;) {
+        Piece4 w;
+        piece_of(s, w);
+        const int nblk = w.pages;
+        if (at >= begin + (long long)nblk * p.Hkv) {  // past this segment (or it has no pages)
+            begin += (long long)nblk * p.Hkv;
+            ++s;
+            continue;
+        }
+        const int off = (int)(at - begin);
+        w.h = off / nblk;
+        const int from = off - w.h * nblk, n = (int)min((long long)(nblk - from), b - at);
+        w.page0 += from;
+        w.pages = n;
+        const int flags = attend_piece<C>(p, sm, w, ring, !waited);
+        waited = true;
+        report4(p, flags);
+        if (n == nblk) {
+            write_rows4<C>(p, sm, w, flags);
+        } else {
+            const int slot = 2 * cta + (from == 0);
+            left |= 1 << (from == 0);
+            float *part = p.ws_part + (size_t)slot * R * D;
+#pragma unroll 1
+            for (int e = tid; e < w.rows * (D / 4); e += NTHR) {
+                const int r = e / (D / 4), c4 = e % (D / 4);
+                float M, L;
+                reinterpret_cast<float4 *>(part)[e] = merge_warps<C>(sm, r, c4, M, L);
+                if (c4 == 0) p.ws_stat[slot * R + r] = make_float2(M, L);
+            }
+            if (tid == 0) {
+                // the range's last CTA is the one whose share holds its last page
+                const long long last = ((begin + (long long)(w.h + 1) * nblk) * N - 1) / T;
+                p.ws_head[slot] = make_int4(s, w.h, (int)last, 1 | flags << 1);
+            }
+        }
+        at += n;
+        __syncthreads();          // the partials are read
+        fence_proxy_async();      // and the next copies may write over them
+    }
+    if (!waited) {
+        pdl_wait();
+        pdl_trigger();
+    }
+    // (only after the dependency wait: the kernel before may be the last call's merge)
+    if (tid < 2 && !(left >> tid & 1)) p.ws_head[2 * cta + tid].w = 0;
+    // the refused segments, in turn
+#pragma unroll 1
+    for (int i = cta; i < p.S; i += gridDim.x) {
+        const Segment sg = load_segment(p.seq_info, i);
+        const unsigned fault = fault4(p, sg);
+        if (fault) refuse4<D>(p, sg, fault, 0, p.Hkv);
+    }
+    coverage4<D>(p);
+}
+
+// Merge of the shared ranges: CTA (i, r) finishes row r of the range that
+// begins in slot 2 i + 1, from that slot and slots 2 (i + 1), .., 2 last.
+template <int D, int R>
+__global__ void __launch_bounds__(kMerge4Threads) merge4_kernel(const __grid_constant__ Attend4Params p) {
+    constexpr int Q = D / 4, GR = kMerge4Threads / Q;  // column quads; groups that share the slots
+    __shared__ float sWt[kMerge4Slots];
+    __shared__ float sRed[kMerge4Threads / 32][2];
+    __shared__ float4 sAcc[kMerge4Threads];
+    const int tid = threadIdx.x, cta = blockIdx.x, r = blockIdx.y;
+    pdl_wait();
+    pdl_trigger();
+    const int4 hd = p.ws_head[2 * cta + 1];
+    if (!(hd.w & 1)) return;
+    Piece4 w;
+    w.sg = load_segment(p.seq_info, hd.x);
+    w.h = hd.y;
+    w.row0 = 0;
+    if (r >= w.sg.ql * p.G) return;
+    const int n = hd.z - cta + 1;  // slots, at most kMerge4Slots
+    auto slot_of = [&](int k) { return k == 0 ? 2 * cta + 1 : 2 * (cta + k); };
+    // max over the slots, then weights and their sum
+    float M = -CUDART_INF_F;
+    int poison = 0;
+    for (int k = tid; k < n; k += kMerge4Threads) {
+        M = fmaxf(M, p.ws_stat[slot_of(k) * R + r].x);
+        poison |= p.ws_head[slot_of(k)].w >> 1;
+    }
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if ((tid & 31) == 0) sRed[tid >> 5][0] = M;
+    poison = __syncthreads_or(poison);
+#pragma unroll
+    for (int k = 0; k < kMerge4Threads / 32; ++k) M = fmaxf(M, sRed[k][0]);
+    float L = 0.f;
+    for (int k = tid; k < n; k += kMerge4Threads) {
+        const float2 st = p.ws_stat[slot_of(k) * R + r];
+        const float wt = st.x == -CUDART_INF_F ? 0.f : ex2(st.x - M);
+        sWt[k] = wt;
+        L = fmaf(wt, st.y, L);
+    }
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if ((tid & 31) == 0) sRed[tid >> 5][1] = L;
+    __syncthreads();
+    L = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMerge4Threads / 32; ++k) L += sRed[k][1];
+    const int c4 = tid % Q, g = tid / Q;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = g; k < n; k += GR) {
+        const float wt = sWt[k];
+        const float4 v = reinterpret_cast<const float4 *>(p.ws_part)[(size_t)(slot_of(k) * R + r) * Q + c4];
+        if (wt != 0.f) {
+            o.x = fmaf(wt, v.x, o.x);
+            o.y = fmaf(wt, v.y, o.y);
+            o.z = fmaf(wt, v.z, o.z);
+            o.w = fmaf(wt, v.w, o.w);
+        }
+    }
+    sAcc[tid] = o;
+    __syncthreads();
+    if (g == 0) {
+#pragma unroll
+        for (int k = 1; k < GR; ++k) {
+            const float4 v = sAcc[k * Q + c4];
+            o.x += v.x;
+            o.y += v.y;
+            o.z += v.z;
+            o.w += v.w;
+        }
+        const bool zero = poison || L == 0.f;
+        const float inv = 1.f / L;
+        const long long row = out_row4(p, w, r);
+        store_out4(p, row * D + 4 * c4, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        if (c4 == 0 && p.lse) p.lse[row] = zero ? -CUDART_INF_F : (M + log2f(L)) * 0.6931471805599453f;
+    }
 }
 
 }  // namespace pkv

@@ -9,7 +9,12 @@ namespace pkv {
 
 template <class C>
 static Attend4Kernel info4() {
-    return Attend4Kernel{reinterpret_cast<const void *>(&attend4_kernel<C>), C::kThreads, C::kSmem, C::R, C::KW, C::kCtas};
+    Attend4Kernel k{reinterpret_cast<const void *>(&attend4_kernel<C>), nullptr, nullptr, C::kThreads, C::kSmem, C::R, C::KW, C::kCtas};
+    if constexpr (C::NT == 1) {
+        k.balance = reinterpret_cast<const void *>(&balance4_kernel<C>);
+        k.merge = reinterpret_cast<const void *>(&merge4_kernel<C::D, C::R>);
+    }
+    return k;
 }
 
 #define PICK4_NAME2(D) pick4_##D
@@ -17,16 +22,16 @@ static Attend4Kernel info4() {
 
 Attend4Kernel PICK4_NAME(PKV_INST_D)(int rows) {
 #if PKV_INST_D == 64
-    if (rows <= 8) return info4<Cfg4<64, 1, 8, 6, 2>>();
-    if (rows <= 16) return info4<Cfg4<64, 2, 8, 6, 2>>();
-    return info4<Cfg4<64, 4, 8, 6, 2>>();
+    if (rows <= 8) return info4<Cfg4<64, 1, 4, 4, 2, 4, false>>();
+    if (rows <= 16) return info4<Cfg4<64, 2, 8, 4, 1, 2, true>>();
+    return info4<Cfg4<64, 4, 8, 4, 1, 1, true>>();
 #elif PKV_INST_D == 128
-    if (rows <= 8) return info4<Cfg4<128, 1, 8, 4, 2>>();
-    if (rows <= 16) return info4<Cfg4<128, 2, 8, 4, 1>>();
-    return info4<Cfg4<128, 4, 8, 4, 1>>();
+    if (rows <= 8) return info4<Cfg4<128, 1, 4, 2, 2, 4, false>>();
+    if (rows <= 16) return info4<Cfg4<128, 2, 8, 4, 1, 1, true>>();
+    return info4<Cfg4<128, 4, 8, 4, 1, 1, true>>();
 #else
-    if (rows <= 8) return info4<Cfg4<256, 1, 8, 3, 1>>();
-    return info4<Cfg4<256, 2, 8, 3, 1>>();
+    if (rows <= 8) return info4<Cfg4<256, 1, 4, 3, 1, 3, true>>();
+    return info4<Cfg4<256, 2, 8, 3, 1, 1, true>>();
 #endif
 }
 

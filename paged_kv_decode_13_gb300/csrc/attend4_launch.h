@@ -8,9 +8,6 @@
 
 namespace pkv {
 
-// Key ranges of at most this many pages a warp run on one CTA of the cluster.
-constexpr int kSolo4 = 4;
-
 // Everything one launch reads; passed by value as a grid constant.
 struct Attend4Params {
     const unsigned char *k, *v;   // this layer's pools, [num_blocks][Hkv][9 D]
@@ -25,12 +22,21 @@ struct Attend4Params {
     int Hq, Hkv, G;
     int total_rows, S, max_seqs, mbps, ring_rows, max_q_len;
     int row_tiles;                // CTAs along the rows of one (segment, kv head)
+    int min_pages;                // pages of a range worth a CTA of the cluster
     int causal, window, out_bf16;
     float scale_log2;             // softmax scale * log2(e)
+    // equal shares (balance4_kernel): what shared ranges leave for the merge
+    int4 *ws_head;                // [2 N] (segment, kv head, last CTA, 1 | flags << 1); w = 0: no piece
+    float2 *ws_stat;              // [2 N][R] (max, sum)
+    float *ws_part;               // [2 N][R][D]
 };
+
+constexpr int kMerge4Threads = 256;
+constexpr int kMerge4Slots = 2048;  // CTAs of a wave, at most
 
 struct Attend4Kernel {
     const void *fn;
+    const void *balance, *merge;  // equal shares and their merge; null where the kernel has none
     int threads;
     size_t smem;
     int rows;   // query rows of a CTA

@@ -48,11 +48,6 @@ __device__ __forceinline__ unsigned scale4_of(unsigned amax) {
 __device__ __forceinline__ float scale4_value(unsigned byte) {
     return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
 }
-// x / s for the code, |x| <= about 6 s.  A bf16 x over a 4-bit s never rounds
-// across a border between two codes in fp32, so the code is the nearest one
-// to the exact quotient.
-__device__ __forceinline__ float code4_arg(float x, float s) { return s > 0.f ? __fdiv_rn(x, s) : copysignf(0.f, x); }
-
 // Eight floats to eight e2m1 codes, x[0] in the low nibble (nearest, ties to
 // even, saturating at 6).
 __device__ __forceinline__ unsigned pack_e2m1x8(const float (&x)[8]) {
@@ -79,10 +74,8 @@ __device__ __forceinline__ unsigned hmul2(unsigned a, unsigned b) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const unsigned *>(&r);
 }
-// Scale byte `i` of a word, in both halves of an fp16 pair.
-__device__ __forceinline__ unsigned scale4_both(unsigned w, int i) {
-    return __byte_perm(w, 0u, 0x4040u | (unsigned)(i | (i << 8))) << 7;
-}
+// A scale byte in both halves of an fp16 pair.
+__device__ __forceinline__ unsigned scale4_both(unsigned byte) { return byte * 0x00800080u; }
 // Scale bytes i and i + 1 of a word as an fp16 pair.
 __device__ __forceinline__ unsigned scale4_pair(unsigned w, int i) {
     return __byte_perm(w, 0u, 0x4040u | (unsigned)(i | ((i + 1) << 8))) << 7;

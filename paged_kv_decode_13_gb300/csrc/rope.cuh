@@ -87,53 +87,76 @@ __device__ __forceinline__ int segment_of_row(const RopeParams &p, int row, int 
     return -1;
 }
 
+// Eight elements of a row as they are in memory.
 template <typename T>
-__device__ __forceinline__ void load8(float (&o)[8], const T *src) {
-    if constexpr (sizeof(T) == 2) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(src);
-        const unsigned w[4] = {v.x, v.y, v.z, v.w};
+struct Raw8 {
+    unsigned w[2 * sizeof(T)];
+    __device__ __forceinline__ void load(const T *src) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[2 * i] = __uint_as_float(w[i] << 16);
-            o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint4 v = reinterpret_cast<const uint4 *>(src)[i];
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
         }
-    } else {
-        const float4 a = *reinterpret_cast<const float4 *>(src), b = *reinterpret_cast<const float4 *>(src + 4);
-        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
     }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T *dst, const float (&x)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                     pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-    } else {
-        *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-        *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    __device__ __forceinline__ void store(T *dst) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     }
-}
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[i] = 0u;
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 2) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+            else x[i] = __uint_as_float(w[i]);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                if (i & 1) w[i / 2] = pack_bf16x2(x[i - 1], x[i]);
+            } else {
+                w[i] = __float_as_uint(x[i]);
+            }
+        }
+    }
+};
 
-// Quantise 8 columns of a row (half a scale group: lanes 2j and 2j + 1 hold
-// one); x holds bf16 numbers.  Returns the codes, leaves the stored values in x.
-__device__ __forceinline__ unsigned quantise8(float (&x)[8], unsigned &scale) {
+// Quantise 8 columns of a bf16 row (half a scale group: lanes 2j and 2j + 1
+// hold one).  Returns the codes; kStored: x becomes the stored values.
+//
+// x / s: s has 4 significant bits and x 8, so the quotient is either exactly
+// on a border between two codes (a multiple of 1/4) or at least 2^-8 of it
+// away.  x * (1 / s), whose error is below 2^-22, rounded to a multiple of
+// 2^-11 by adding and taking off 3 * 2^11, is therefore on the same side, and
+// exactly on the border where x / s is: the code is that of the exact quotient.
+template <bool kStored>
+__device__ __forceinline__ unsigned quantise8(Raw8<__nv_bfloat16> &x, unsigned &scale) {
     unsigned amax = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 0; i < 4; ++i) amax = max(amax, max(x.w[i] & 0x7fff0000u, (x.w[i] << 16) & 0x7fffffffu));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     scale = scale4_of(amax);
-    const float s = scale4_value(scale);
-    float r[8];
+    const float inv = scale ? __frcp_rn(scale4_value(scale)) : 0.f;  // a zero scale: codes 0 with the signs of x
+    float v[8];
+    x.get(v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = code4_arg(x[i], s);
-    const unsigned codes = pack_e2m1x8(r);
-    unsigned h[4];
-    unpack_e2m1x8(h, codes);
+    for (int i = 0; i < 8; ++i) v[i] = copysignf((fmaf(fabsf(v[i]), inv, 6144.f) - 6144.f), v[i]);
+    const unsigned codes = pack_e2m1x8(v);
+    if constexpr (kStored) {
+        unsigned h[4];
+        unpack_e2m1x8(h, codes);
+        const unsigned s2 = scale4_both(scale);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-        x[2 * i] = f.x * s;
-        x[2 * i + 1] = f.y * s;
+        for (int i = 0; i < 4; ++i) {  // exact in fp16, and in bf16
+            const unsigned m = hmul2(h[i], s2);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&m));
+            x.w[i] = pack_bf16x2(f.x, f.y);
+        }
     }
     return codes;
 }
@@ -144,92 +167,108 @@ struct RopeSlot {
     int token;        // slot in the page
 };
 
-// The heads [h0, h1) of one kind (q, k or v) of a row.
-//   ca, sb: this lane's factors of its own and its partner's columns.
+// The heads [h0, h1) of one kind (q, k or v) of a row.  ca, sb: this lane's
+// factors of its own and its partner's columns; turned: bit e set where column
+// e of the lane is rotated.
 template <typename T, int CACHE, int PAIR, bool NORM, bool ROPE>
 __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T *dst, unsigned char *pool,
                                            const RopeSlot &slot, int h0, int h1, const float (&ca)[8],
-                                           const float (&sb)[8], int partner, float *stage, int lane) {
+                                           const float (&sb)[8], unsigned turned, int partner, float *stage, int lane) {
     const int per = 1 << p.lanes_log2, sub = lane >> p.lanes_log2, c = lane & (per - 1), heads = 32 >> p.lanes_log2;
     const bool col_ok = c * 8 < p.D;
-    for (int hb = h0; hb < h1; hb += heads * kRopeUnroll) {
-        float x[kRopeUnroll][8];
+    const bool whole = (p.rot_dim & 7) == 0;  // a lane's columns are all rotated or none
+    const float inv_d = 1.f / (float)p.D;
+    src += (h0 + sub) * p.D + c * 8;
+    if (dst) dst += (h0 + sub) * p.D + c * 8;
+    const int step = heads * p.D;
+    if (CACHE == kSameType && pool)
+        pool += (((slot.block * kPage + slot.token) * p.Hkv + h0 + sub) * p.D + c * 8) * (long long)sizeof(T);
+    if (CACHE == kFp4 && pool) pool += (slot.block * p.Hkv + h0 + sub) * block4_bytes(p.D);
+    const int pool_step = CACHE == kFp4 ? heads * block4_bytes(p.D) : step * (int)sizeof(T);
+#pragma unroll 1
+    for (int hb = h0 + sub; hb - sub < h1; hb += heads * kRopeUnroll) {
+        Raw8<T> raw[kRopeUnroll];
 #pragma unroll
         for (int u = 0; u < kRopeUnroll; ++u) {
-            const int h = hb + u * heads + sub;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
-            if (col_ok && h < h1) load8<T>(x[u], src + (long long)h * p.D + c * 8);
+            raw[u].clear();
+            if (col_ok && hb + u * heads < h1) raw[u].load(src + u * step);
         }
 #pragma unroll
         for (int u = 0; u < kRopeUnroll; ++u) {
-            if (hb + u * heads >= h1) break;  // uniform
-            const int h = hb + u * heads + sub;
-            const bool mine = col_ok && h < h1;
-            float y[8];
-            float rinv = 1.f;
-            if constexpr (NORM) {
-                float ss = 0.f;
+            if (hb - sub + u * heads >= h1) break;  // uniform
+            const bool mine = col_ok && hb + u * heads < h1;
+            if constexpr (NORM || ROPE) {
+                float x[8], y[8];
+                raw[u].get(x);
+                float rinv = 1.f;
+                if constexpr (NORM) {
+                    float ss = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[u][e], x[u][e], ss);
-                for (int o = 1; o < per; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                rinv = rsqrtf(ss / (float)p.D + p.eps);
-            }
-            if constexpr (ROPE) {
-                float z[8];  // the partner columns' values (0 where the column is not rotated)
-                if constexpr (PAIR == kInLane) {
+                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] = x[u][e ^ 1];
-                } else if constexpr (PAIR == kByShuffle) {
-                    if constexpr (sizeof(T) == 2) {
+                    for (int o = 1; o < 32; o <<= 1)
+                        if (o < per) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    rinv = rsqrtf(fmaf(ss, inv_d, p.eps));
+                }
 #pragma unroll
-                        for (int e = 0; e < 8; e += 2) {  // bf16 pairs travel in one word
-                            const unsigned w = __byte_perm(__float_as_uint(x[u][e]), __float_as_uint(x[u][e + 1]), 0x7632);
-                            const unsigned o = __shfl_sync(0xffffffffu, w, partner);
-                            z[e] = __uint_as_float(o << 16);
-                            z[e + 1] = __uint_as_float(o & 0xffff0000u);
+                for (int e = 0; e < 8; ++e) y[e] = x[e] * ca[e];
+                if constexpr (ROPE) {
+                    float z[8];  // the partner columns' values
+                    if constexpr (PAIR == kInLane) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) z[e] = x[e ^ 1];
+                    } else if constexpr (PAIR == kByShuffle) {
+                        Raw8<T> o;
+#pragma unroll
+                        for (int e = 0; e < 2 * (int)sizeof(T); ++e) o.w[e] = __shfl_sync(0xffffffffu, raw[u].w[e], partner);
+                        o.get(z);
+                    } else {
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) stage[e * 32 + lane] = x[e];
+                        __syncwarp();
+                        const int half = p.rot_dim / 2;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int d = c * 8 + e, o = d < half ? d + half : d - half;
+                            z[e] = d < p.rot_dim ? stage[(o & 7) * 32 + (sub << p.lanes_log2) + (o >> 3)] : 0.f;
                         }
+                    }
+                    // Columns that are not rotated never meet a partner's infinity.
+                    if (whole) {
+                        if (turned)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], sb[e], y[e]);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) z[e] = __shfl_sync(0xffffffffu, x[u][e], partner);
-                    }
-                } else {
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) stage[e * 32 + lane] = x[u][e];
-                    __syncwarp();
-                    const int half = p.rot_dim / 2;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int d = c * 8 + e, o = d < half ? d + half : d - half;
-                        z[e] = d < p.rot_dim ? stage[(o & 7) * 32 + (sub << p.lanes_log2) + (o >> 3)] : 0.f;
+                        for (int e = 0; e < 8; ++e)
+                            if (turned >> e & 1u) y[e] = fmaf(z[e], sb[e], y[e]);
                     }
                 }
+                if constexpr (NORM)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const bool turned = c * 8 + e < p.rot_dim;
-                    y[e] = rinv * (turned ? fmaf(z[e], sb[e], x[u][e] * ca[e]) : x[u][e] * ca[e]);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = NORM ? rinv * x[u][e] * ca[e] : x[u][e];
+                    for (int e = 0; e < 8; ++e) y[e] *= rinv;
+                raw[u].set(y);
             }
-            if (CACHE == kFp4 && pool) {
-                // the row as it would be handed on (bf16), then quantised
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = __bfloat162float(__float2bfloat16_rn(y[e]));
-                unsigned scale;
-                const unsigned codes = quantise8(y, scale);
-                if (mine) {
-                    unsigned char *b = pool + (slot.block * p.Hkv + h) * block4_bytes(p.D);
-                    *reinterpret_cast<unsigned *>(b + slot.token * (p.D / 2) + c * 4) = codes;
-                    if ((c & 1) == 0) b[8 * p.D + slot.token * (p.D / 16) + c / 2] = (unsigned char)scale;
+            if constexpr (CACHE == kFp4) {
+                if (pool) {  // the row as it would be handed on (bf16), quantised
+                    unsigned scale, codes;
+                    if (dst) codes = quantise8<true>(raw[u], scale);
+                    else codes = quantise8<false>(raw[u], scale);
+                    if (mine) {
+                        unsigned char *b = pool + u * pool_step;
+                        *reinterpret_cast<unsigned *>(b + slot.token * (p.D / 2) + c * 4) = codes;
+                        if ((c & 1) == 0) b[8 * p.D + slot.token * (p.D / 16) + c / 2] = (unsigned char)scale;
+                    }
                 }
             } else if (CACHE == kSameType && pool && mine) {
-                store8<T>(reinterpret_cast<T *>(pool) + ((slot.block * kPage + slot.token) * p.Hkv + h) * p.D + c * 8, y);
+                raw[u].store(reinterpret_cast<T *>(pool + u * pool_step));
             }
-            if (dst && mine) store8<T>(dst + (long long)h * p.D + c * 8, y);
+            if (dst && mine) raw[u].store(dst + u * step);
         }
+        src += kRopeUnroll * step;
+        if (dst) dst += kRopeUnroll * step;
+        if (CACHE != kNoCache && pool) pool += kRopeUnroll * pool_step;
     }
 }
 
@@ -248,19 +287,19 @@ __device__ __forceinline__ void write_v4_page(const RopeParams &p, const Segment
         const int tok = t0 + sub;
         const bool mine = tok >= a && tok < b;
         const long long row = (long long)sg.q0 + (pb * kPage + tok - start);
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        if (mine) load8<__nv_bfloat16>(x, v + row * p.v_stride + h * D + c * 8);
-        unsigned scale;
-        const unsigned w = quantise8(x, scale);
+        Raw8<__nv_bfloat16> x;
+        x.clear();
+        if (mine) x.load(v + row * p.v_stride + h * D + c * 8);
+        unsigned scale, w;
+        if (p.v_out) w = quantise8<true>(x, scale);
+        else w = quantise8<false>(x, scale);
         if (mine) {
             // one code a byte, for the exchange below
             const unsigned lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
             *reinterpret_cast<uint2 *>(codes + tok * D + c * 8) =
                 make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
             if ((c & 1) == 0) scales[tok * (D / 16) + c / 2] = (unsigned char)scale;
-            if (p.v_out) store8<__nv_bfloat16>(reinterpret_cast<__nv_bfloat16 *>(p.v_out) + row * p.v_out_stride + h * D + c * 8, x);
+            if (p.v_out) x.store(reinterpret_cast<__nv_bfloat16 *>(p.v_out) + row * p.v_out_stride + h * D + c * 8);
         }
     }
     __syncwarp();
@@ -347,6 +386,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
     const int per = 1 << p.lanes_log2, c = lane & (per - 1), half = p.rot_dim / 2;
     float cs[8], sn[8];
     int partner = lane;
+    const int left = p.rot_dim - c * 8;  // rotated columns from this lane's first on
+    const unsigned turned = left >= 8 ? 0xffu : left <= 0 ? 0u : (1u << left) - 1u;
     if (p.rot_dim) {
         const unsigned pos = (unsigned)(p.positions ? p.positions[row] : (int)place);
         auto angle = [&](int i, float &co, float &si) {
@@ -398,7 +439,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
         float ca[8], sb[8], wt[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) wt[e] = 1.f;
-        if (weight && c * 8 < p.D) load8<T>(wt, weight + c * 8);
+        if (weight && c * 8 < p.D) {
+            Raw8<T> r;
+            r.load(weight + c * 8);
+            r.get(wt);
+        }
         if (p.rot_dim) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -414,11 +459,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
                 ca[e] = cs[e] * wt[e];
                 sb[e] = sn[e] * wz;
             }
-            if (weight) rope_heads<T, CACHE, PAIR, true, true>(p, src, dst, pool, slot, h0, h1, ca, sb, partner, stage, lane);
-            else rope_heads<T, CACHE, PAIR, false, true>(p, src, dst, pool, slot, h0, h1, ca, sb, partner, stage, lane);
+            if (weight) rope_heads<T, CACHE, PAIR, true, true>(p, src, dst, pool, slot, h0, h1, ca, sb, turned, partner, stage, lane);
+            else rope_heads<T, CACHE, PAIR, false, true>(p, src, dst, pool, slot, h0, h1, ca, sb, turned, partner, stage, lane);
         } else {
-            if (weight) rope_heads<T, CACHE, PAIR, true, false>(p, src, dst, pool, slot, h0, h1, wt, wt, partner, stage, lane);
-            else rope_heads<T, CACHE, PAIR, false, false>(p, src, dst, pool, slot, h0, h1, wt, wt, partner, stage, lane);
+            if (weight) rope_heads<T, CACHE, PAIR, true, false>(p, src, dst, pool, slot, h0, h1, wt, wt, 0u, partner, stage, lane);
+            else rope_heads<T, CACHE, PAIR, false, false>(p, src, dst, pool, slot, h0, h1, wt, wt, 0u, partner, stage, lane);
         }
     };
     if (p.q) kind(reinterpret_cast<const T *>(p.q) + row * p.q_stride, reinterpret_cast<T *>(p.q_out) + row * p.q_out_stride, nullptr,
@@ -431,7 +476,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
         const float one[8] = {};
         if (h0 < h1) rope_heads<T, CACHE, PAIR, false, false>(p, reinterpret_cast<const T *>(p.v) + row * p.v_stride,
                                                  p.v_out ? reinterpret_cast<T *>(p.v_out) + row * p.v_out_stride : nullptr,
-                                                 reinterpret_cast<unsigned char *>(p.v_pool), slot, h0, h1, one, one, partner, stage, lane);
+                                                 reinterpret_cast<unsigned char *>(p.v_pool), slot, h0, h1, one, one, 0u, partner, stage, lane);
     }
 }
 

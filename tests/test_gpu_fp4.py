@@ -453,3 +453,140 @@ def test_side_stream_and_graph(pkv):
         torch.cuda.synchronize()
         assert torch.equal(got[0], out) and torch.equal(got[1], lse) and int(err.item()) == 0
         check(f, out, lse, q=qo.cpu())
+
+
+# ---------------------------------------------------------------- equal shares: launches whose bounds are large
+#
+# The launch bounds decide (max_kv is one), so a large max_kv runs small cases there.
+
+BIG = 1 << 20
+
+
+def shares(pkv, f, max_q):
+    w = f.w
+    return pkv.attend_workspace_bytes(f.cache, w.q_heads, w.num_segments, max_q, BIG) > 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lengths", [[1], [16], [17, 1, 5000], [3000, 0, 40, 2999, 1], [9000]])
+def test_shares(pkv, D, lengths):
+    w = U.nan_tails(workloads.batched(S=len(lengths), max_len=max(lengths), seed=D, lengths=lengths, q_heads=8, kv_heads=2, head_dim=D))
+    w.seq_info[:, 1] = (w.seq_info[:, 3] > 0).int()
+    f = Fp4(pkv, w)
+    assert shares(pkv, f, 1)
+    for dt in (torch.float32, torch.bfloat16):
+        out, lse, err = attend(pkv, f, out_dtype=dt, max_kv=BIG)
+        assert err == 0
+        check(f, out, lse)
+    again, lse2, _ = attend(pkv, f, out_dtype=dt, max_kv=BIG)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,max_q", [(1, 1, 1), (8, 1, 1), (12, 3, 2), (4, 4, 8), (7, 1, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [0, 33, 700])
+def test_shares_groups_and_windows(pkv, q_heads, kv_heads, max_q, causal, window):
+    w = U.nan_tails(workloads.spec_verify(S=9, max_q=max_q, len_lo=max_q, len_hi=2000, seed=q_heads, q_heads=q_heads, kv_heads=kv_heads, causal=causal))
+    f = Fp4(pkv, w)
+    assert shares(pkv, f, max_q)
+    ws = pkv.new_workspace(f.cache, q_heads, 9, max_q, BIG)
+    out, lse, err = torch.empty(w.q[0].shape, device="cuda"), torch.empty(w.q[0].shape[:2], device="cuda"), pkv.new_err_flags()
+    buf = torch.full((ws.numel() + 4096,), 0xA5, dtype=torch.uint8, device="cuda")   # garbage in it, a guard behind it
+    pkv.attend_varlen(f.cache, 0, w.q[0].cuda(), w.seq_info.cuda(), out, err, max_q, BIG, w.scale, causal, window, lse=lse, workspace=buf[:ws.numel()])
+    assert int(err.item()) == 0 and bool((buf[ws.numel():] == 0xA5).all())
+    check(f, out, lse, window=window)
+
+
+def test_shares_many_segments(pkv):
+    g = torch.Generator().manual_seed(1)
+    lengths = torch.randint(1, 400, (512,), generator=g).tolist()
+    w = workloads.batched(S=512, max_len=400, lengths=lengths, q_heads=2, kv_heads=1, head_dim=64)
+    f = Fp4(pkv, w)
+    assert shares(pkv, f, 1)
+    out, lse, err = attend(pkv, f, max_kv=BIG)
+    assert err == 0
+    check(f, out, lse)
+
+
+@pytest.mark.parametrize("D,window,ring,kv", [(128, 1000, 1008, 5000), (64, 333, 352, 5000), (256, 512, 512, 3001)])
+def test_shares_rings_and_padding(pkv, D, window, ring, kv):
+    w = workloads.long_context(S=3, kv_len=kv, window=window, ring_rows=ring, q_heads=8, kv_heads=2, head_dim=D)
+    f = Fp4(pkv, w, garbage=False, first_valid=np.array([0, kv - 100, kv + 5], np.int32))
+    assert shares(pkv, f, 1)
+    ws = pkv.new_workspace(f.cache, 8, 3, 1, BIG)
+    out, lse, err = torch.empty(w.q[0].shape, device="cuda"), torch.empty(w.q[0].shape[:2], device="cuda"), pkv.new_err_flags()
+    # (with a window the bound is the window's: enough kv heads and segments, or an ample window)
+    pkv.attend_varlen(f.cache, 0, w.q[0].cuda(), w.seq_info.cuda(), out, err, 1, BIG, w.scale, w.causal, window, lse=lse, workspace=ws)
+    assert int(err.item()) == 0
+    check(f, out, lse)
+    w = U.nan_tails(workloads.batched(S=5, max_len=3000, seed=2, q_heads=8, kv_heads=2, head_dim=D))
+    fv = np.array([0, 5, 2999, 4000, 17], np.int32)
+    f = Fp4(pkv, w, first_valid=fv)
+    out, lse, err = attend(pkv, f, max_kv=BIG)
+    assert err == 0
+    check(f, out, lse)
+
+
+@pytest.mark.parametrize("seg,bit", [((2, 1, 9, 5), 1), ((-1, 2, 0, 9), 1), ((2, 9, 0, 9), 1), ((2, 1, 0, 99999), 2),
+                                     ((2, 2, 1, 33), 8), ((2, 2, 1, 5990), 8), ((2, 2, 1, 17), 8), ((2, 4, 0, 9), 16)])
+def test_shares_bad_segments_read_zero(pkv, seg, bit):
+    w = workloads.batched(S=2, max_len=6000, seed=4, lengths=[6000, 5990], q_heads=4, kv_heads=2)
+    w.block_table[1, 1] = 4000
+    w.q = [torch.randn(6, 4, 128).bfloat16()]
+    f = Fp4(pkv, w)
+    w.seq_info = torch.tensor([seg, [0, 2, 0, 5900]], dtype=torch.int32)
+    assert shares(pkv, f, 3)
+    out, lse, err = attend(pkv, f, causal=True, max_q=3, max_kv=BIG)
+    assert err == bit
+    assert (out[2:] == 0).all() and torch.isinf(lse[2:]).all()
+    w.seq_info = w.seq_info[1:]
+    check(f, out, lse, causal=True, rows=np.arange(6) < 2)
+    w.seq_info = torch.tensor([[0, 3, 0, 40], [2, 3, 0, 30]], dtype=torch.int32)
+    assert attend(pkv, f, causal=True, max_q=3, max_kv=BIG)[2] == 32
+    w.seq_info = torch.tensor([[7, 1, 0, 40]], dtype=torch.int32)   # past the rows: nothing is left to attend
+    out, lse, err = attend(pkv, f, max_q=1, max_kv=BIG)
+    assert err == 1 and (out == 0).all()
+
+
+def test_shares_nan(pkv):
+    w = workloads.spec_verify(S=1, max_q=4, len_lo=5000, len_hi=5000, seed=6, q_heads=4, kv_heads=2)
+    w.seq_info = torch.tensor([[0, 4, 0, 5000]], dtype=torch.int32)
+    w.q = [torch.randn(4, 4, 128).bfloat16()]
+    f = Fp4(pkv, w)
+    for at, see in ((4998, np.arange(4996, 5000) >= 4998), (1234, np.ones(4, bool))):
+        pool = f.cache.v[0]
+        keep = pool.clone()
+        c, s = R.unpack(pool.cpu().numpy(), True)
+        s[int(w.block_table[0, at // 16]), at % 16, 1, 2] = 0xFF
+        pool.copy_(torch.from_numpy(R.pack(c, s, True)))
+        out, lse, err = attend(pkv, f, causal=True, max_q=4, max_kv=BIG)
+        want = np.zeros((4, 4, 128), bool)
+        want[see, 2:, 32:48] = True
+        assert err == 0 and (out.isnan().cpu().numpy() == want).all() and not lse.isnan().any()
+        pool.copy_(keep)
+
+
+def test_shares_in_graphs(pkv):
+    """Two captured graphs, each with its own workspace from the allocator, replayed on two streams."""
+    w = workloads.batched(S=4, max_len=4000, seed=3, q_heads=16, kv_heads=4)
+    f = Fp4(pkv, w)
+    q, si, err = w.q[0].cuda(), w.seq_info.cuda(), pkv.new_err_flags()
+    want, want_lse, _ = attend(pkv, f, max_kv=BIG)
+    made = []
+    for _ in range(2):
+        out, lse = torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(3):
+                pkv.attend_varlen(f.cache, 0, q, si, out, err, 1, BIG, w.scale, lse=lse, flags=pkv.FLAG_PDL)
+        made.append((g, st, out, lse))
+    for _ in range(20):
+        for g, st, _, _ in made:
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, _, out, lse in made:
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert int(err.item()) == 0
