@@ -320,7 +320,7 @@ def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Te
         _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(window), _ptr(err), _stream(stream)))
 
 
-# Bounds (segments x kv heads x keys) from which a launch over a 4-bit cache
+# Bounds (segments x kv heads x row tiles x keys) from which a launch over a 4-bit cache
 # may use a workspace; pkv_attend_workspace_bytes decides.
 _FP4_WORKSPACE_FROM = 16 * 6144
 
@@ -332,7 +332,8 @@ def _fp4_workspace(cache, hq, segments, max_q_len, max_kv, window, flags, stream
     streams, and captured graphs, share nothing.
     """
     keys = min(max_kv, window + max_q_len) if window > 0 else max_kv
-    if segments * cache._kv_heads * keys < _FP4_WORKSPACE_FROM:
+    tiles = -(-hq * max_q_len // (8 * cache._kv_heads))  # of 8 query rows, at most
+    if segments * cache._kv_heads * tiles * keys < _FP4_WORKSPACE_FROM:
         return None
     n = attend_workspace_bytes(cache, hq, segments, max_q_len, max_kv, 0, flags)
     if n <= 0:

@@ -356,7 +356,8 @@ struct Plan4 {
     AttnKernel k;  // the same kernel for the shared cluster queries
     int G, row_tiles, ncta;
     long long units;
-    int shares;    // CTAs of the equal-shares kernel, 0: not for these bounds
+    Attend4Kernel ks;  // the kernel of equal shares
+    int shares;        // its CTAs, 0: not for these bounds
 };
 
 // Equal shares cost a second launch (about 3 us) and balance the SMs: worth
@@ -366,6 +367,11 @@ struct Plan4 {
 // table has to be short; long ones have ranges enough for one CTA each.
 constexpr long long kSharesFrom = 6144;
 constexpr int kSharesSegments = 512;
+constexpr int kSharesTiles = 16;  // each tile's range is taken as long as its segment's: not for long causal chunks
+constexpr int kPieceWide = 40;  // the same for the tcgen05 kernel, in pages
+// Rows a kv head from which the tcgen05 kernel (tiles of 128) is faster than mma.sync tiles of 32.
+constexpr int kWideFrom = 17;
+constexpr int kPieceBytes = 56 << 10;  // what a piece costs, as bytes that one CTA reads meanwhile
 
 struct Ws4Layout {
     size_t head, stat, part, total;
@@ -404,10 +410,13 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     }
     pl->ncta = (int)std::max<long long>(1, std::min<long long>(n, max_pages));
     pl->shares = 0;
-    if (pl->k4.balance && pl->row_tiles == 1 && num_splits == 0 && S > 0 && S <= kSharesSegments) {
+    if (num_splits == 0 && S > 0 && S <= kSharesSegments) {
+        pl->ks = c->head_dim == 128 && rows >= kWideFrom ? pick4_wide() : pl->k4;
+        const long long tiles = (rows + pl->ks.rows - 1) / pl->ks.rows;
         const long long keys = window > 0 ? std::min<long long>(max_kv, (long long)window + max_q_len) : max_kv;
-        if ((long long)S * c->kv_heads * ((keys + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE) >= kSharesFrom)
-            pl->shares = std::min(device_sms() * pl->k4.ctas, kMerge4Slots);
+        const long long pages = (long long)S * c->kv_heads * tiles * ((keys + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE);
+        if (tiles <= kSharesTiles && pages >= (pl->ks.rows == 8 ? kSharesFrom : pl->ks.rows == 128 ? kSharesFrom / 6 : kSharesFrom / 2))
+            pl->shares = std::min(device_sms() * pl->ks.ctas, kMerge4Slots);
     }
     return PKV_OK;
 }
@@ -426,10 +435,10 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     if (S == 0 && total_rows == 0) return PKV_OK;
     if (workspace && (!aligned16(workspace) || workspace_bytes < 0)) return PKV_EINVAL;
     const bool shares = pl.shares > 0 && workspace;
-    const Ws4Layout wl = ws4_layout(pl.shares, pl.k4.rows, c->head_dim);
+    const Ws4Layout wl = ws4_layout(pl.shares, pl.ks.rows, c->head_dim);
     if (shares && workspace_bytes < (long long)wl.total) return PKV_EINVAL;
     if (check_only) return PKV_OK;
-    if (shares) pl.k.fn = pl.k4.balance;
+    if (shares) pl.k = AttnKernel{pl.ks.balance, pl.ks.threads, pl.ks.smem, pl.ks.rows, c->head_dim, true, pl.ks.rows == 128};
     if ((st = prepare_kernel(pl.k))) return st;
     int ncta = S == 0 || shares ? 1 : schedulable_cluster(pl.k, pl.ncta);
     if (S > 0 && !shares && num_splits == 0) ncta = wave_cluster(pl.k, pl.units, ncta);
@@ -454,11 +463,12 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     p.ring_rows = c->ring_rows;
     p.max_q_len = max_q_len;
     p.row_tiles = pl.row_tiles;
-    p.min_pages = 4 * pl.k4.warps;  // four a warp
+    p.min_pages = 4 * (shares ? pl.ks.warps : pl.k4.warps);  // four a warp
     p.causal = causal;
     p.window = window;
     p.out_bf16 = (flags & PKV_FLAG_OUT_BF16) ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.piece_pages = shares && pl.ks.rows == 128 ? kPieceWide : kPieceBytes / (2 * block4_bytes(c->head_dim));
     p.ws_head = nullptr;
     p.ws_stat = nullptr;
     p.ws_part = nullptr;
@@ -493,7 +503,8 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     void *args[] = {&p};
     if ((st = launch_status(cudaLaunchKernelExC(&cfg, pl.k.fn, args))) || !shares) return st;
     cudaLaunchConfig_t mc = {};
-    mc.gridDim = dim3((unsigned)pl.shares, (unsigned)(pl.G * max_q_len), 1);
+    const int merge_rows = pl.ks.rows == 8 ? 1 : kMerge4Threads / 32;  // a CTA's
+    mc.gridDim = dim3((unsigned)pl.shares, (unsigned)((std::min(pl.ks.rows, pl.G * max_q_len) + merge_rows - 1) / merge_rows), 1);
     mc.blockDim = dim3(kMerge4Threads);
     mc.stream = cfg.stream;
     cudaLaunchAttribute after;
@@ -501,7 +512,7 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     after.val.programmaticStreamSerializationAllowed = 1;
     mc.attrs = &after;
     mc.numAttrs = 1;
-    return launch_status(cudaLaunchKernelExC(&mc, pl.k4.merge, args));
+    return launch_status(cudaLaunchKernelExC(&mc, pl.ks.merge, args));
 }
 
 // ---- norm + rotary + append
@@ -927,7 +938,7 @@ int64_t pkv_attend_workspace_bytes(const pkv_cache *c, int32_t Hq, int32_t S, in
     if (is_fp4(c)) {  // 4-bit caches merge in the cluster
         Plan4 pl4;
         const int st = make_plan4(c, Hq, S, max_q_len, max_kv, 0, num_splits, &pl4);
-        return st ? st : pl4.shares ? (int64_t)ws4_layout(pl4.shares, pl4.k4.rows, c->head_dim).total : 0;
+        return st ? st : pl4.shares ? (int64_t)ws4_layout(pl4.shares, pl4.ks.rows, c->head_dim).total : 0;
     }
     Plan pl;
     const int st = make_plan(c, Hq, S, max_q_len, max_kv, num_splits, flags, true, &pl);

@@ -717,97 +717,148 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
 
 // ---------------------------------------------------------------- equal shares of all ranges
 
-// With a workspace the ranges (one row tile each) are laid end to end, T
-// pages in all, and the one wave of CTAs the device holds takes equal shares:
-// CTA i pages [i T / N, (i + 1) T / N).  A range that one CTA holds whole is
+// With a workspace the ranges (one (kv head, row tile) each) are laid end to end, each
+// as long as its pages and a few more for what a piece costs besides them (its
+// first loads and its merge, about 4 us: short ranges would else make the
+// CTAs that hold many of them late, 73 us against 50 on 32 sequences of up to
+// 16384 keys).  The one wave of CTAs the device holds takes equal shares of
+// the total T: CTA i [i T / N, (i + 1) T / N).  A range that one CTA holds whole is
 // written at once; of a range that several share, each leaves its rows and
 // (max, sum) in the workspace, slot 2 i + 1 where the range begins in CTA i and
 // slot 2 i where it continues, and a second launch merges them.  Clusters
 // need their CTAs free at the same time in one GPC, and a fixed number of
 // them splits long and short ranges alike; shares have neither limit.
-__device__ __forceinline__ long long share_begin(long long i, long long T, int N) { return i * T / N; }
+
+// A CTA's share, and a walk over its pieces.
+struct Share4 {
+    long long T;       // length of all ranges
+    int N;             // CTAs that share them
+    long long at, b;   // what is left of this CTA's share
+    int s;             // the segment that holds `at`, and where it begins
+    long long begin;
+
+    // All rows of segment s.
+    __device__ __forceinline__ static void segment(const Attend4Params &p, int s, Piece4 &w) {
+        w.sg = load_segment(p.seq_info, s);
+        w.row0 = 0;
+        w.rows = fault4(p, w.sg) ? 0 : w.sg.ql * p.G;
+        w.pages = 0;
+        if (w.rows > 0) piece_bounds(p, w);
+    }
+    // Its (kv head, row tile) ranges, each as long as all its rows' range.
+    __device__ __forceinline__ static long long length(const Attend4Params &p, const Piece4 &w, int R) {
+        return w.pages ? (long long)(w.pages + p.piece_pages) * p.Hkv * ((w.rows + R - 1) / R) : 0ll;
+    }
+    // Every thread of the CTA calls it; NTHR threads, scratch of NTHR / 32 + 2 words of 8 bytes.
+    template <int NTHR>
+    __device__ __forceinline__ void find(const Attend4Params &p, int R, long long *scratch) {
+        // prefix sum of the segments' lengths; thread t holds segments t per ..
+        const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x;
+        const int per = (p.S + NTHR - 1) / NTHR, s_lo = min(tid * per, p.S), s_hi = min(s_lo + per, p.S);
+        long long mine = 0;
+#pragma unroll 4
+        for (int i = s_lo; i < s_hi; ++i) {
+            Piece4 w;
+            segment(p, i, w);
+            mine += length(p, w, R);
+        }
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        if (lane == 31) scratch[tid >> 5] = upto;
+        __syncthreads();
+        T = 0;
+#pragma unroll
+        for (int k = 0; k < NTHR / 32; ++k) {
+            if (k < tid >> 5) upto += scratch[k];
+            T += scratch[k];
+        }
+        N = (int)max(1ll, min((long long)gridDim.x, T / p.min_pages));
+        at = cta * T / N;
+        b = cta < N ? (cta + 1) * T / N : at;
+        if (at < b && upto - mine <= at && at < upto) {
+            long long x = upto - mine;
+            int i = s_lo;
+#pragma unroll 1
+            for (; i < s_hi; ++i) {
+                Piece4 w;
+                segment(p, i, w);
+                const long long n = length(p, w, R);
+                if (at < x + n) break;
+                x += n;
+            }
+            scratch[NTHR / 32] = i;
+            scratch[NTHR / 32 + 1] = x;
+        }
+        __syncthreads();
+        s = (int)scratch[NTHR / 32];
+        begin = scratch[NTHR / 32 + 1];
+        __syncthreads();  // the scratch is free again
+    }
+    // The next piece: its rows, bounds and pages; from: pages of its range
+    // before it, whole: it is all of the range.  last: the CTA that holds the
+    // range's last page.  False when the share is done.
+    __device__ __forceinline__ bool next(const Attend4Params &p, int R, Piece4 &w, int &tile, int &from, bool &whole, int &last) {
+#pragma unroll 1
+        while (at < b) {
+            segment(p, s, w);
+            const int nblk = w.pages, len = nblk + p.piece_pages;
+            const long long n_seg = length(p, w, R);
+            if (at >= begin + n_seg) {  // past this segment (or it has no pages)
+                begin += n_seg;
+                ++s;
+                continue;
+            }
+            const int range = (int)((at - begin) / len), tiles = (w.rows + R - 1) / R;
+            tile = range % tiles;
+            const long long first = begin + (long long)range * len, end = min(b, first + len);
+            // the pages come after the piece's cost
+            from = max(0, (int)(at - first) - p.piece_pages);
+            const int n = max(0, (int)(end - first) - p.piece_pages) - from;
+            at = end;
+            if (n == 0) continue;
+            const int page = w.page0 + from;
+            w.h = range / tiles;
+            w.row0 = tile * R;
+            w.rows = min(R, w.rows - w.row0);
+            if (tiles > 1) piece_bounds(p, w);  // the tile's own bounds: keys outside them are masked
+            w.page0 = page;
+            w.pages = n;
+            whole = n == nblk;
+            last = (int)(((first + len) * N - 1) / T);
+            return true;
+        }
+        return false;
+    }
+};
+// What a piece of a shared range leaves for the merge.
+__device__ __forceinline__ int4 head4(const Piece4 &w, int tile, int last, int flags) {
+    return make_int4(w.sg.q0, w.h | tile << 16, last, 1 | flags << 1 | w.rows << 4);
+}
 
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas) balance4_kernel(const __grid_constant__ Attend4Params p) {
     constexpr int D = C::D, R = C::R, NTHR = C::kThreads;
     extern __shared__ unsigned char smem_raw[];
     const Smem4<C> sm(smem_raw);
-    const int tid = threadIdx.x, lane = tid & 31, cta = blockIdx.x;
+    const int tid = threadIdx.x, cta = blockIdx.x;
     init_bars4<C>(sm);
-    // ---- prefix sum of the segments' pages; thread t holds segments t per ..
-    auto piece_of = [&](int s, Piece4 &w) {
-        w.sg = load_segment(p.seq_info, s);
-        w.row0 = 0;
-        w.rows = fault4(p, w.sg) ? 0 : w.sg.ql * p.G;
-        w.pages = 0;
-        if (w.rows > 0) piece_bounds(p, w);
-    };
-    const int per = (p.S + NTHR - 1) / NTHR, s_lo = min(tid * per, p.S), s_hi = min(s_lo + per, p.S);
-    long long mine = 0;
-#pragma unroll 4
-    for (int s = s_lo; s < s_hi; ++s) {
-        Piece4 w;
-        piece_of(s, w);
-        mine += (long long)w.pages * p.Hkv;
-    }
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += x;
-    }
-    long long *sSum = reinterpret_cast<long long *>(sm.recv);
-    if (lane == 31) sSum[tid >> 5] = upto;
-    __syncthreads();
-    long long T = 0;
-#pragma unroll
-    for (int k = 0; k < C::KW; ++k) {
-        if (k < tid >> 5) upto += sSum[k];
-        T += sSum[k];
-    }
-    const int N = (int)max(1ll, min((long long)gridDim.x, T / p.min_pages));
-    const long long a = share_begin(cta, T, N), b = cta < N ? share_begin(cta + 1, T, N) : a;
-    int *sFind = reinterpret_cast<int *>(sSum + C::KW);  // the segment that holds page a, and where it begins
-    long long *sBegin = sSum + C::KW + 1;
-    if (cta < N && upto - mine <= a && a < upto) {
-        long long at = upto - mine;
-        int s = s_lo;
-#pragma unroll 1
-        for (; s < s_hi; ++s) {
-            Piece4 w;
-            piece_of(s, w);
-            const long long n = (long long)w.pages * p.Hkv;
-            if (a < at + n) break;
-            at += n;
-        }
-        sFind[0] = s;
-        *sBegin = at;
-    }
-    __syncthreads();
-    int s = sFind[0], ring = 0;
-    long long begin = *sBegin;
+    Share4 share;
+    share.find<NTHR>(p, R, reinterpret_cast<long long *>(sm.recv));
+    int ring = 0, left = 0;  // left: bit i, a piece in slot 2 cta + i
     bool waited = false;
-    int left = 0;  // bit i: a piece in slot 2 cta + i
-    __syncthreads();  // sm.recv is free again
+    Piece4 w;
+    int tile, from, last;
+    bool whole;
 #pragma unroll 1
-    for (long long at = a; at < b;) {
-        Piece4 w;
-        piece_of(s, w);
-        const int nblk = w.pages;
-        if (at >= begin + (long long)nblk * p.Hkv) {  // past this segment (or it has no pages)
-            begin += (long long)nblk * p.Hkv;
-            ++s;
-            continue;
-        }
-        const int off = (int)(at - begin);
-        w.h = off / nblk;
-        const int from = off - w.h * nblk, n = (int)min((long long)(nblk - from), b - at);
-        w.page0 += from;
-        w.pages = n;
+    while (share.next(p, R, w, tile, from, whole, last)) {
         const int flags = attend_piece<C>(p, sm, w, ring, !waited);
         waited = true;
         report4(p, flags);
-        if (n == nblk) {
+        if (whole) {
             write_rows4<C>(p, sm, w, flags);
         } else {
             const int slot = 2 * cta + (from == 0);
@@ -820,13 +871,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) balance4_kernel(const _
                 reinterpret_cast<float4 *>(part)[e] = merge_warps<C>(sm, r, c4, M, L);
                 if (c4 == 0) p.ws_stat[slot * R + r] = make_float2(M, L);
             }
-            if (tid == 0) {
-                // the range's last CTA is the one whose share holds its last page
-                const long long last = ((begin + (long long)(w.h + 1) * nblk) * N - 1) / T;
-                p.ws_head[slot] = make_int4(s, w.h, (int)last, 1 | flags << 1);
-            }
+            if (tid == 0) p.ws_head[slot] = head4(w, tile, last, flags);
         }
-        at += n;
         __syncthreads();          // the partials are read
         fence_proxy_async();      // and the next copies may write over them
     }
@@ -846,81 +892,102 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) balance4_kernel(const _
     coverage4<D>(p);
 }
 
-// Merge of the shared ranges: CTA (i, r) finishes row r of the range that
-// begins in slot 2 i + 1, from that slot and slots 2 (i + 1), .., 2 last.
-template <int D, int R>
+// Merge of the shared ranges: CTA (i, y) finishes rows y .. of the range that
+// begins in slot 2 i + 1, from that slot and slots 2 (i + 1), .., 2 last.  TPR
+// threads a row: a whole CTA where few rows have many slots, a warp where
+// many rows have few.
+template <int D, int R, int TPR>
 __global__ void __launch_bounds__(kMerge4Threads) merge4_kernel(const __grid_constant__ Attend4Params p) {
-    constexpr int Q = D / 4, GR = kMerge4Threads / Q;  // column quads; groups that share the slots
-    __shared__ float sWt[kMerge4Slots];
+    constexpr int Q = D / 4, GR = TPR > Q ? TPR / Q : 1, QL = TPR > Q ? 1 : Q / TPR;  // column quads; groups that share the slots; quads a thread
+    constexpr int ROWS = kMerge4Threads / TPR;
+    __shared__ float sWt[TPR == 32 ? 1 : kMerge4Slots];
     __shared__ float sRed[kMerge4Threads / 32][2];
-    __shared__ float4 sAcc[kMerge4Threads];
-    const int tid = threadIdx.x, cta = blockIdx.x, r = blockIdx.y;
+    __shared__ float4 sAcc[TPR == 32 ? 1 : kMerge4Threads];
+    const int tid = threadIdx.x, t = tid % TPR, cta = blockIdx.x, r = blockIdx.y * ROWS + tid / TPR;
     pdl_wait();
     pdl_trigger();
     const int4 hd = p.ws_head[2 * cta + 1];
     if (!(hd.w & 1)) return;
     Piece4 w;
-    w.sg = load_segment(p.seq_info, hd.x);
-    w.h = hd.y;
-    w.row0 = 0;
-    if (r >= w.sg.ql * p.G) return;
+    w.sg.q0 = hd.x;
+    w.h = hd.y & 0xffff;
+    w.row0 = (hd.y >> 16) * R;
+    if (r >= hd.w >> 4) return;    // whole CTAs (TPR = CTA) or warps leave
     const int n = hd.z - cta + 1;  // slots, at most kMerge4Slots
     auto slot_of = [&](int k) { return k == 0 ? 2 * cta + 1 : 2 * (cta + k); };
     // max over the slots, then weights and their sum
     float M = -CUDART_INF_F;
     int poison = 0;
-    for (int k = tid; k < n; k += kMerge4Threads) {
-        M = fmaxf(M, p.ws_stat[slot_of(k) * R + r].x);
-        poison |= p.ws_head[slot_of(k)].w >> 1;
+    for (int k = t; k < n; k += TPR) {
+        M = fmaxf(M, p.ws_stat[(size_t)slot_of(k) * R + r].x);
+        poison |= p.ws_head[slot_of(k)].w >> 1 & 3;
     }
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if ((tid & 31) == 0) sRed[tid >> 5][0] = M;
-    poison = __syncthreads_or(poison);
+    if constexpr (TPR == 32) {
+        poison = __any_sync(0xffffffffu, poison);
+    } else {
+        if ((tid & 31) == 0) sRed[tid >> 5][0] = M;
+        poison = __syncthreads_or(poison);
 #pragma unroll
-    for (int k = 0; k < kMerge4Threads / 32; ++k) M = fmaxf(M, sRed[k][0]);
+        for (int k = 0; k < kMerge4Threads / 32; ++k) M = fmaxf(M, sRed[k][0]);
+    }
     float L = 0.f;
-    for (int k = tid; k < n; k += kMerge4Threads) {
-        const float2 st = p.ws_stat[slot_of(k) * R + r];
+    for (int k = t; k < n; k += TPR) {
+        const float2 st = p.ws_stat[(size_t)slot_of(k) * R + r];
         const float wt = st.x == -CUDART_INF_F ? 0.f : ex2(st.x - M);
-        sWt[k] = wt;
+        if constexpr (TPR != 32) sWt[k] = wt;
         L = fmaf(wt, st.y, L);
     }
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if ((tid & 31) == 0) sRed[tid >> 5][1] = L;
-    __syncthreads();
-    L = 0.f;
+    if constexpr (TPR != 32) {
+        if ((tid & 31) == 0) sRed[tid >> 5][1] = L;
+        __syncthreads();
+        L = 0.f;
 #pragma unroll
-    for (int k = 0; k < kMerge4Threads / 32; ++k) L += sRed[k][1];
-    const int c4 = tid % Q, g = tid / Q;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = g; k < n; k += GR) {
-        const float wt = sWt[k];
-        const float4 v = reinterpret_cast<const float4 *>(p.ws_part)[(size_t)(slot_of(k) * R + r) * Q + c4];
-        if (wt != 0.f) {
+        for (int k = 0; k < kMerge4Threads / 32; ++k) L += sRed[k][1];
+    }
+    const bool zero = poison || L == 0.f;
+    const float inv = 1.f / L;
+    const long long row = out_row4(p, w, r);
+    const int c4 = t % Q, g = TPR > Q ? t / Q : 0;
+    auto add = [](float4 &o, float wt, float4 v) {
+        if (wt != 0.f) {  // a zero weight must not touch its partial: a poisoned one may hold NaN
             o.x = fmaf(wt, v.x, o.x);
             o.y = fmaf(wt, v.y, o.y);
             o.z = fmaf(wt, v.z, o.z);
             o.w = fmaf(wt, v.w, o.w);
         }
-    }
-    sAcc[tid] = o;
-    __syncthreads();
-    if (g == 0) {
+    };
+    auto part = [&](int k, int q) { return reinterpret_cast<const float4 *>(p.ws_part)[((size_t)slot_of(k) * R + r) * Q + q]; };
+    auto put = [&](int q, float4 o) {
+        store_out4(p, row * D + 4 * q, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    };
+    float4 o[QL];
 #pragma unroll
-        for (int k = 1; k < GR; ++k) {
-            const float4 v = sAcc[k * Q + c4];
-            o.x += v.x;
-            o.y += v.y;
-            o.z += v.z;
-            o.w += v.w;
+    for (int q = 0; q < QL; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if constexpr (TPR == 32) {
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float x = p.ws_stat[(size_t)slot_of(k) * R + r].x, wt = x == -CUDART_INF_F ? 0.f : ex2(x - M);
+#pragma unroll
+            for (int q = 0; q < QL; ++q)
+                if (t + q * TPR < Q) add(o[q], wt, part(k, t + q * TPR));
         }
-        const bool zero = poison || L == 0.f;
-        const float inv = 1.f / L;
-        const long long row = out_row4(p, w, r);
-        store_out4(p, row * D + 4 * c4, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (c4 == 0 && p.lse) p.lse[row] = zero ? -CUDART_INF_F : (M + log2f(L)) * 0.6931471805599453f;
+#pragma unroll
+        for (int q = 0; q < QL; ++q)
+            if (t + q * TPR < Q) put(t + q * TPR, o[q]);
+    } else {
+#pragma unroll 4
+        for (int k = g; k < n; k += GR) add(o[0], sWt[k], part(k, c4));
+        sAcc[tid] = o[0];
+        __syncthreads();
+        if (g == 0) {
+#pragma unroll
+            for (int k = 1; k < GR; ++k) add(o[0], 1.f, sAcc[k * Q + c4]);
+            put(c4, o[0]);
+        }
     }
+    if (t == 0 && p.lse) p.lse[row] = zero ? -CUDART_INF_F : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 }  // namespace pkv

@@ -1,5 +1,6 @@
 // Instantiates the 4-bit attention kernel for one head_dim (-DPKV_INST_D=<64|128|256>).
 #include "attend4.cuh"
+#include "wide4.cuh"
 
 #ifndef PKV_INST_D
 #error "PKV_INST_D not set"
@@ -9,12 +10,8 @@ namespace pkv {
 
 template <class C>
 static Attend4Kernel info4() {
-    Attend4Kernel k{reinterpret_cast<const void *>(&attend4_kernel<C>), nullptr, nullptr, C::kThreads, C::kSmem, C::R, C::KW, C::kCtas};
-    if constexpr (C::NT == 1) {
-        k.balance = reinterpret_cast<const void *>(&balance4_kernel<C>);
-        k.merge = reinterpret_cast<const void *>(&merge4_kernel<C::D, C::R>);
-    }
-    return k;
+    return Attend4Kernel{reinterpret_cast<const void *>(&attend4_kernel<C>), reinterpret_cast<const void *>(&balance4_kernel<C>),
+                         reinterpret_cast<const void *>(&merge4_kernel<C::D, C::R, C::R == 8 ? kMerge4Threads : 32>), C::kThreads, C::kSmem, C::R, C::KW, C::kCtas};
 }
 
 #define PICK4_NAME2(D) pick4_##D
@@ -28,11 +25,18 @@ Attend4Kernel PICK4_NAME(PKV_INST_D)(int rows) {
 #elif PKV_INST_D == 128
     if (rows <= 8) return info4<Cfg4<128, 1, 4, 2, 2, 4, false>>();
     if (rows <= 16) return info4<Cfg4<128, 2, 8, 4, 1, 1, true>>();
-    return info4<Cfg4<128, 4, 8, 4, 1, 1, true>>();
+    return info4<Cfg4<128, 4, 4, 4, 1, 2, true>>();
 #else
     if (rows <= 8) return info4<Cfg4<256, 1, 4, 3, 1, 3, true>>();
     return info4<Cfg4<256, 2, 8, 3, 1, 1, true>>();
 #endif
 }
+
+#if PKV_INST_D == 128
+Attend4Kernel pick4_wide() {
+    return Attend4Kernel{nullptr, reinterpret_cast<const void *>(&wide4_kernel), reinterpret_cast<const void *>(&merge4_kernel<128, 128, 32>),
+                         Wide4::kThreads, Wide4::kSmem, Wide4::R, Wide4::kThreads / 32, 1};
+}
+#endif
 
 }  // namespace pkv

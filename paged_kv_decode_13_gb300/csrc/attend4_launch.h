@@ -25,8 +25,10 @@ struct Attend4Params {
     int min_pages;                // pages of a range worth a CTA of the cluster
     int causal, window, out_bf16;
     float scale_log2;             // softmax scale * log2(e)
-    // equal shares (balance4_kernel): what shared ranges leave for the merge
-    int4 *ws_head;                // [2 N] (segment, kv head, last CTA, 1 | flags << 1); w = 0: no piece
+    // equal shares (balance4_kernel)
+    int piece_pages;              // what a piece of a range costs besides its pages, in pages
+    // what shared ranges leave for the merge
+    int4 *ws_head;                // [2 N] (first row, kv head | tile << 16, last CTA, 1 | flags << 1 | rows << 4); w = 0: no piece
     float2 *ws_stat;              // [2 N][R] (max, sum)
     float *ws_part;               // [2 N][R][D]
 };
@@ -36,7 +38,7 @@ constexpr int kMerge4Slots = 2048;  // CTAs of a wave, at most
 
 struct Attend4Kernel {
     const void *fn;
-    const void *balance, *merge;  // equal shares and their merge; null where the kernel has none
+    const void *balance, *merge;  // equal shares and their merge
     int threads;
     size_t smem;
     int rows;   // query rows of a CTA
@@ -48,5 +50,7 @@ struct Attend4Kernel {
 Attend4Kernel pick4_64(int rows);
 Attend4Kernel pick4_128(int rows);
 Attend4Kernel pick4_256(int rows);
+// The tcgen05 kernel of wide groups (head_dim 128, equal shares only: fn is null).
+Attend4Kernel pick4_wide();
 
 }  // namespace pkv

@@ -26,19 +26,19 @@ cudaError_t launch_rope(RopeParams &p, int cache, bool f32, int sms, cudaStream_
     const auto groups = [&](int H) { return (H + heads - 1) / heads; };
     const int all = std::max(1, (p.q ? groups(p.Hq) : 0) + (p.k ? groups(p.Hkv) : 0) + (cache == kSameType ? groups(p.Hkv) : 0));
     // Few rows: a row's heads are spread over warps until there are about
-    // kRopeFill warps an SM.  Many rows: one warp keeps the row's angles for all its heads.
-    const long long want = ((long long)kRopeFill * sms + std::max(p.rows, 1) - 1) / std::max(p.rows, 1);
+    // kRopeFill warps an SM.  Many rows: about kRopeFill warps an SM take them
+    // in turn, each keeping a row's angles for all its heads.
+    const long long fill = (long long)kRopeFill * sms, want = (fill + std::max(p.rows, 1) - 1) / std::max(p.rows, 1);
     p.slices = (int)std::max<long long>(1, std::min<long long>(want, all));
-    p.row_ctas = (int)(((long long)p.rows * p.slices + kRopeWarps - 1) / kRopeWarps);
-    if (cache != kNoCache) p.row_ctas = std::max(p.row_ctas, 1);  // the first looks at segments that hold no row
+    p.row_ctas = (int)((std::min<long long>(p.rows, std::max<long long>(fill, 1)) * p.slices + kRopeWarps - 1) / kRopeWarps);
+    if (cache != kNoCache) p.row_ctas = std::max(p.row_ctas, 1);  // the first looks at the refused segments
     long long ctas = p.row_ctas;
-    size_t smem = pair == kByShared ? (size_t)kRopeWarps * 256 * sizeof(float) : 0;
+    size_t smem = (size_t)kRopeWarps * 2048;  // angles, exchange
     p.page_warps = 1;
     if (cache == kFp4) {
         // V pages of one (segment, kv head): no more warps than it can have new pages
         const long long units = (long long)p.S * p.Hkv, pages = (p.rows + kPage - 2) / kPage + 1;
-        const long long fill = ((long long)kRopeFill * sms + units - 1) / units;
-        p.page_warps = (int)std::max<long long>(1, std::min(fill, pages));
+        p.page_warps = (int)std::max<long long>(1, std::min((fill + units - 1) / units, pages));
         ctas += (units * p.page_warps + kRopeWarps - 1) / kRopeWarps;
         smem = std::max(smem, (size_t)kRopeWarps * kPage * (p.D + p.D / 16));
     }

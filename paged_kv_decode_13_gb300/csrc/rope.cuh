@@ -127,18 +127,19 @@ struct Raw8 {
 };
 
 // Quantise 8 columns of a bf16 row (half a scale group: lanes 2j and 2j + 1
-// hold one).  Returns the codes; kStored: x becomes the stored values.
+// hold one).  Returns the codes; stored: x becomes the stored values.
 //
 // x / s: s has 4 significant bits and x 8, so the quotient is either exactly
 // on a border between two codes (a multiple of 1/4) or at least 2^-8 of it
 // away.  x * (1 / s), whose error is below 2^-22, rounded to a multiple of
 // 2^-11 by adding and taking off 3 * 2^11, is therefore on the same side, and
 // exactly on the border where x / s is: the code is that of the exact quotient.
-template <bool kStored>
-__device__ __forceinline__ unsigned quantise8(Raw8<__nv_bfloat16> &x, unsigned &scale) {
-    unsigned amax = 0;
+__device__ __forceinline__ unsigned quantise8(Raw8<__nv_bfloat16> &x, unsigned &scale, bool stored) {
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&x.w[0]));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) amax = max(amax, max(x.w[i] & 0x7fff0000u, (x.w[i] << 16) & 0x7fffffffu));
+    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&x.w[i])));
+    unsigned amax = *reinterpret_cast<const unsigned *>(&m);
+    amax = max(amax << 16, amax & 0xffff0000u);  // a NaN's bits are above all others
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     scale = scale4_of(amax);
     const float inv = scale ? __frcp_rn(scale4_value(scale)) : 0.f;  // a zero scale: codes 0 with the signs of x
@@ -147,14 +148,14 @@ __device__ __forceinline__ unsigned quantise8(Raw8<__nv_bfloat16> &x, unsigned &
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = copysignf((fmaf(fabsf(v[i]), inv, 6144.f) - 6144.f), v[i]);
     const unsigned codes = pack_e2m1x8(v);
-    if constexpr (kStored) {
+    if (stored) {
         unsigned h[4];
         unpack_e2m1x8(h, codes);
         const unsigned s2 = scale4_both(scale);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // exact in fp16, and in bf16
-            const unsigned m = hmul2(h[i], s2);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&m));
+            const unsigned y = hmul2(h[i], s2);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&y));
             x.w[i] = pack_bf16x2(f.x, f.y);
         }
     }
@@ -168,12 +169,12 @@ struct RopeSlot {
 };
 
 // The heads [h0, h1) of one kind (q, k or v) of a row.  ca, sb: this lane's
-// factors of its own and its partner's columns; turned: bit e set where column
-// e of the lane is rotated.
-template <typename T, int CACHE, int PAIR, bool NORM, bool ROPE>
+// factors of its own and its partner's columns; norm, turn: what is done to
+// them; turned: bit e set where column e of the lane is rotated.
+template <typename T, int CACHE, int PAIR>
 __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T *dst, unsigned char *pool,
                                            const RopeSlot &slot, int h0, int h1, const float (&ca)[8],
-                                           const float (&sb)[8], unsigned turned, int partner, float *stage, int lane) {
+                                           const float (&sb)[8], bool norm, bool turn, unsigned turned, int partner, float *stage, int lane) {
     const int per = 1 << p.lanes_log2, sub = lane >> p.lanes_log2, c = lane & (per - 1), heads = 32 >> p.lanes_log2;
     const bool col_ok = c * 8 < p.D;
     const bool whole = (p.rot_dim & 7) == 0;  // a lane's columns are all rotated or none
@@ -197,11 +198,11 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T 
         for (int u = 0; u < kRopeUnroll; ++u) {
             if (hb - sub + u * heads >= h1) break;  // uniform
             const bool mine = col_ok && hb + u * heads < h1;
-            if constexpr (NORM || ROPE) {
+            if (norm || turn) {
                 float x[8], y[8];
                 raw[u].get(x);
                 float rinv = 1.f;
-                if constexpr (NORM) {
+                if (norm) {
                     float ss = 0.f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
@@ -212,7 +213,7 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T 
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = x[e] * ca[e];
-                if constexpr (ROPE) {
+                if (turn) {
                     float z[8];  // the partner columns' values
                     if constexpr (PAIR == kInLane) {
 #pragma unroll
@@ -245,16 +246,15 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T 
                             if (turned >> e & 1u) y[e] = fmaf(z[e], sb[e], y[e]);
                     }
                 }
-                if constexpr (NORM)
+                if (norm)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) y[e] *= rinv;
                 raw[u].set(y);
             }
             if constexpr (CACHE == kFp4) {
                 if (pool) {  // the row as it would be handed on (bf16), quantised
-                    unsigned scale, codes;
-                    if (dst) codes = quantise8<true>(raw[u], scale);
-                    else codes = quantise8<false>(raw[u], scale);
+                    unsigned scale;
+                    const unsigned codes = quantise8(raw[u], scale, dst != nullptr);
                     if (mine) {
                         unsigned char *b = pool + u * pool_step;
                         *reinterpret_cast<unsigned *>(b + slot.token * (p.D / 2) + c * 4) = codes;
@@ -290,9 +290,8 @@ __device__ __forceinline__ void write_v4_page(const RopeParams &p, const Segment
         Raw8<__nv_bfloat16> x;
         x.clear();
         if (mine) x.load(v + row * p.v_stride + h * D + c * 8);
-        unsigned scale, w;
-        if (p.v_out) w = quantise8<true>(x, scale);
-        else w = quantise8<false>(x, scale);
+        unsigned scale;
+        const unsigned w = quantise8(x, scale, p.v_out != nullptr);
         if (mine) {
             // one code a byte, for the exchange below
             const unsigned lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
@@ -337,7 +336,7 @@ __device__ __forceinline__ void write_v4_page(const RopeParams &p, const Segment
 }
 
 template <typename T, int CACHE, int PAIR>
-__global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, sizeof(T) == 2 ? 5 : 4) rope_kernel(const __grid_constant__ RopeParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
@@ -365,118 +364,110 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const __grid_cons
             const unsigned f = segment_fault(load_segment(p.seq_info, s), p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
             if (f) atomicOr(p.err, f);
         }
+    // Few rows: `slices` warps share a row's heads.  Many: a warp takes rows of
+    // its own, one after the other, and looks their segment up once.
     const long long w = (long long)blockIdx.x * kRopeWarps + warp;
-    const int row = (int)(w / p.slices), slice = (int)(w - (long long)row * p.slices);
-    if (w >= (long long)p.rows * p.slices) return;
-    RopeSlot slot{0, 0};
-    long long place = 0;
-    if (CACHE != kNoCache) {
-        const int s = segment_of_row(p, row, lane);
-        if (s < 0) return;
-        const Segment sg = load_segment(p.seq_info, s);
-        if (!new_pages_ok(p, sg, lane)) {
-            if (lane == 0) atomicOr(p.err, PKV_ERR_BLOCK);
-            return;
-        }
-        place = (long long)sg.kend - sg.ql + (row - sg.q0);
-        slot.block = p.block_table[(long long)sg.col * p.mbps + table_page((int)(place / kPage), p.ring_rows)];
-        slot.token = (int)(place % kPage);
-    }
-    // This lane's columns: cosine and signed sine of each.
-    const int per = 1 << p.lanes_log2, c = lane & (per - 1), half = p.rot_dim / 2;
-    float cs[8], sn[8];
+    const int slice = (int)(w % p.slices);
+    const long long warps = (long long)p.row_ctas * kRopeWarps / p.slices, wr = w / p.slices;
+    if (wr >= warps) return;
+    const int row0 = (int)(wr * p.rows / warps), row1 = (int)((wr + 1) * p.rows / warps);
+    const int per = 1 << p.lanes_log2, c = lane & (per - 1), half = p.rot_dim / 2, heads = 32 >> p.lanes_log2;
+    float2 *angles = reinterpret_cast<float2 *>(smem) + warp * 128;                       // cosine and sine of each pair
+    float *stage = reinterpret_cast<float *>(smem) + kRopeWarps * 256 + warp * 256;
     int partner = lane;
+    if (PAIR == kByShuffle && c < half / 4) partner = lane + (c < half / 8 ? half / 8 : -(half / 8));  // the halves are whole lanes
     const int left = p.rot_dim - c * 8;  // rotated columns from this lane's first on
     const unsigned turned = left >= 8 ? 0xffu : left <= 0 ? 0u : (1u << left) - 1u;
-    if (p.rot_dim) {
-        const unsigned pos = (unsigned)(p.positions ? p.positions[row] : (int)place);
-        auto angle = [&](int i, float &co, float &si) {
-            const unsigned long long turn = p.turns[i];
-            const unsigned f = pos * (unsigned)(turn >> 32) + __umulhi(pos, (unsigned)turn) -
-                               ((int)pos < 0 ? (unsigned)turn : 0u);  // (pos mod 2^64) * turn, bits 32..63
-            const float x = (float)(int)f * 4.656612873077393e-10f;   // 2^-31: half turns in [-1, 1]
-            sincospif(x, &si, &co);
-            co *= p.mscale;
-            si *= p.mscale;
-        };
-        if (PAIR == kInLane) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const int i = (c * 8 + e) / 2;
-                float co = 1.f, si = 0.f;
-                if (i < half) angle(i, co, si);
-                cs[e] = cs[e + 1] = co;
-                sn[e] = -si;
-                sn[e + 1] = si;
-            }
-        } else {
-            const int hc = half / 8;  // by shuffle: the halves are whole lanes
-            if (PAIR == kByShuffle && c < 2 * hc) partner = lane + (c < hc ? hc : -hc);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int d = c * 8 + e;
-                float co = 1.f, si = 0.f;
-                if (d < p.rot_dim) angle(d < half ? d : d - half, co, si);
-                cs[e] = co;
-                sn[e] = d < half ? -si : si;
-            }
-        }
-    }
-    float *stage = reinterpret_cast<float *>(smem) + warp * 256;
-    const int heads = 32 >> p.lanes_log2;
     // The row's groups of `heads` heads, q then k then v, cut evenly into the slices.
     const int nq = p.q ? (p.Hq + heads - 1) / heads : 0, nk = p.k ? (p.Hkv + heads - 1) / heads : 0;
     const int all = nq + nk + (CACHE == kSameType ? (p.Hkv + heads - 1) / heads : 0);
     const int f0 = (int)((long long)all * slice / p.slices), f1 = (int)((long long)all * (slice + 1) / p.slices);
-    auto part = [&](int first, int H, int &h0, int &h1) {
-        h0 = max(f0 - first, 0) * heads;
-        h1 = min(max(f1 - first, 0) * heads, H);
-    };
-    auto kind = [&](const T *src, T *dst, unsigned char *pool, const T *weight, int first, int H) {
-        int h0, h1;
-        part(first, H, h0, h1);
-        if (h0 >= h1) return;
-        float ca[8], sb[8], wt[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) wt[e] = 1.f;
-        if (weight && c * 8 < p.D) {
-            Raw8<T> r;
-            r.load(weight + c * 8);
-            r.get(wt);
+    Segment sg{0, 0, 0, 0};
+    bool pages_ok = false;
+#pragma unroll 1
+    for (int row = row0; row < row1; ++row) {
+        RopeSlot slot{0, 0};
+        long long place = 0;
+        if (CACHE != kNoCache) {
+            if (!(sg.q0 <= row && (long long)row < (long long)sg.q0 + sg.ql)) {
+                const int s = segment_of_row(p, row, lane);
+                if (s < 0) {
+                    sg.ql = 0;
+                    continue;
+                }
+                sg = load_segment(p.seq_info, s);
+                pages_ok = new_pages_ok(p, sg, lane);
+                if (!pages_ok && lane == 0) atomicOr(p.err, PKV_ERR_BLOCK);
+            }
+            if (!pages_ok) continue;
+            place = (long long)sg.kend - sg.ql + (row - sg.q0);
+            slot.block = p.block_table[(long long)sg.col * p.mbps + table_page((int)(place / kPage), p.ring_rows)];
+            slot.token = (int)(place % kPage);
         }
-        if (p.rot_dim) {
+        if (p.rot_dim) {  // the row's angles, each once
+            const unsigned pos = (unsigned)(p.positions ? p.positions[row] : (int)place);
+            __syncwarp();
+            for (int i = lane; i < half; i += 32) {
+                const unsigned long long turn = p.turns[i];
+                const unsigned f = pos * (unsigned)(turn >> 32) + __umulhi(pos, (unsigned)turn) -
+                                   ((int)pos < 0 ? (unsigned)turn : 0u);  // (pos mod 2^64) * turn, bits 32..63
+                float si, co;
+                sincospif((float)(int)f * 4.656612873077393e-10f, &si, &co);  // 2^-31: half turns in [-1, 1]
+                angles[i] = make_float2(co * p.mscale, si * p.mscale);
+            }
+            __syncwarp();
+        }
+        int first = 0;
+#pragma unroll 1
+        for (int kind = 0; kind < (CACHE == kSameType ? 3 : 2); ++kind) {  // q, k, v
+            const int H = kind == 0 ? p.Hq : p.Hkv, groups = kind == 0 ? nq : kind == 1 ? nk : all - nq - nk;
+            const int h0 = max(f0 - first, 0) * heads, h1 = min(max(f1 - first, 0) * heads, H);
+            first += groups;
+            if (groups == 0 || h0 >= h1) continue;
+            const T *src = reinterpret_cast<const T *>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
+                           row * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride);
+            T *dst = reinterpret_cast<T *>(kind == 0 ? p.q_out : kind == 1 ? p.k_out : p.v_out);
+            if (dst) dst += row * (kind == 0 ? p.q_out_stride : kind == 1 ? p.k_out_stride : p.v_out_stride);
+            unsigned char *pool = reinterpret_cast<unsigned char *>(kind == 0 ? nullptr : kind == 1 ? p.k_pool : p.v_pool);
+            const T *weight = reinterpret_cast<const T *>(kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr);
+            // this lane's columns: cosine and signed sine, then the head weights
+            const bool turn = kind < 2 && p.rot_dim > 0;
+            float ca[8], sb[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float wz = 1.f;  // the partner column's weight
-                if (weight) {
-                    const int d = c * 8 + e;
-                    const int o = PAIR == kInLane ? d ^ 1 : d < half ? d + half : d - half;
-                    if (d < p.rot_dim) {
-                        if constexpr (sizeof(T) == 2) wz = __bfloat162float(weight[o]);
-                        else wz = weight[o];
+                ca[e] = 1.f;
+                sb[e] = 0.f;
+            }
+            if (turn) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int d = c * 8 + e, i = PAIR == kInLane ? d / 2 : d < half ? d : d - half;
+                    if (turned >> e & 1u) {
+                        const float2 t = angles[i];
+                        ca[e] = t.x;
+                        sb[e] = (PAIR == kInLane ? e & 1 : d >= half) ? t.y : -t.y;
                     }
                 }
-                ca[e] = cs[e] * wt[e];
-                sb[e] = sn[e] * wz;
             }
-            if (weight) rope_heads<T, CACHE, PAIR, true, true>(p, src, dst, pool, slot, h0, h1, ca, sb, turned, partner, stage, lane);
-            else rope_heads<T, CACHE, PAIR, false, true>(p, src, dst, pool, slot, h0, h1, ca, sb, turned, partner, stage, lane);
-        } else {
-            if (weight) rope_heads<T, CACHE, PAIR, true, false>(p, src, dst, pool, slot, h0, h1, wt, wt, 0u, partner, stage, lane);
-            else rope_heads<T, CACHE, PAIR, false, false>(p, src, dst, pool, slot, h0, h1, wt, wt, 0u, partner, stage, lane);
+            if (weight && c * 8 < p.D) {
+                Raw8<T> r;
+                r.load(weight + c * 8);
+                float wt[8];
+                r.get(wt);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    ca[e] *= wt[e];
+                    const int d = c * 8 + e, o = PAIR == kInLane ? d ^ 1 : d < half ? d + half : d - half;
+                    if (turned >> e & 1u) {  // the partner column's weight
+                        if constexpr (PAIR == kInLane) sb[e] *= wt[e ^ 1];
+                        else if constexpr (sizeof(T) == 2) sb[e] *= __bfloat162float(weight[o]);
+                        else sb[e] *= weight[o];
+                    }
+                }
+            }
+            rope_heads<T, CACHE, PAIR>(p, src, dst, pool, slot, h0, h1, ca, sb, weight != nullptr, turn, turned, partner,
+                                       stage, lane);
         }
-    };
-    if (p.q) kind(reinterpret_cast<const T *>(p.q) + row * p.q_stride, reinterpret_cast<T *>(p.q_out) + row * p.q_out_stride, nullptr,
-                  reinterpret_cast<const T *>(p.q_weight), 0, p.Hq);
-    if (p.k) kind(reinterpret_cast<const T *>(p.k) + row * p.k_stride, p.k_out ? reinterpret_cast<T *>(p.k_out) + row * p.k_out_stride : nullptr,
-                  reinterpret_cast<unsigned char *>(p.k_pool), reinterpret_cast<const T *>(p.k_weight), nq, p.Hkv);
-    if (CACHE == kSameType) {
-        int h0, h1;
-        part(nq + nk, p.Hkv, h0, h1);
-        const float one[8] = {};
-        if (h0 < h1) rope_heads<T, CACHE, PAIR, false, false>(p, reinterpret_cast<const T *>(p.v) + row * p.v_stride,
-                                                 p.v_out ? reinterpret_cast<T *>(p.v_out) + row * p.v_out_stride : nullptr,
-                                                 reinterpret_cast<unsigned char *>(p.v_pool), slot, h0, h1, one, one, 0u, partner, stage, lane);
     }
 }
 

@@ -6,7 +6,7 @@
 namespace pkv {
 
 // Warps an SM is given before a warp takes more than one group of heads.
-constexpr int kRopeFill = 24;
+constexpr int kRopeFill = 20;
 
 // Picks the instantiation and the split (fills the fields the split decides).
 // cache: RopeCache; f32: the rows' type (bf16 otherwise; 4-bit caches take bf16 rows).

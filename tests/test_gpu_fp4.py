@@ -590,3 +590,113 @@ def test_shares_in_graphs(pkv):
     for _, _, out, lse in made:
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
     assert int(err.item()) == 0
+
+
+# ---------------------------------------------------------------- equal shares of wide groups (head_dim 128: the tcgen05 kernel)
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_heads,kv_heads,max_q", [(16, 1, 1), (17, 1, 1), (8, 2, 5), (64, 8, 16), (8, 1, 16), (16, 2, 40)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_shares_wide(pkv, D, q_heads, kv_heads, max_q, causal):
+    w = U.nan_tails(workloads.spec_verify(S=5, max_q=max_q, len_lo=max_q, len_hi=1500, seed=max_q + q_heads, q_heads=q_heads, kv_heads=kv_heads,
+                                          head_dim=D, causal=causal))
+    f = Fp4(pkv, w)
+    assert shares(pkv, f, max_q) == (D != 256 or q_heads // kv_heads * max_q <= 256)   # at most 16 row tiles
+    for dt in (torch.float32, torch.bfloat16):
+        out, lse, err = attend(pkv, f, out_dtype=dt, max_kv=BIG, max_q=max_q)
+        assert err == 0
+        check(f, out, lse)
+    again, lse2, _ = attend(pkv, f, out_dtype=dt, max_kv=BIG, max_q=max_q)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("window", [1, 17, 64, 333, 5000])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("padded", [False, True])
+def test_shares_wide_windows_and_padding(pkv, window, causal, padded):
+    w = U.nan_tails(workloads.spec_verify(S=6, max_q=9, len_lo=20, len_hi=900, seed=window, q_heads=16, kv_heads=2, causal=causal))
+    ends = w.seq_info[:, 3].tolist()
+    fv = np.array([0, 17, ends[2] - 1, ends[3] + 5, max(ends[4] - 5, 0), 3], np.int32) if padded else None
+    f = Fp4(pkv, w, first_valid=fv)
+    ws = pkv.new_workspace(f.cache, 16, 6, 9, BIG)
+    assert ws is not None
+    out, lse, err = torch.empty(w.q[0].shape, device="cuda"), torch.empty(w.q[0].shape[:2], device="cuda"), pkv.new_err_flags()
+    pkv.attend_varlen(f.cache, 0, w.q[0].cuda(), w.seq_info.cuda(), out, err, 9, BIG, w.scale, causal, window if window < 5000 else 0, lse=lse, workspace=ws)
+    assert int(err.item()) == 0
+    check(f, out, lse, window=window if window < 5000 else 0)
+
+
+def test_shares_wide_ring(pkv):
+    w = workloads.long_context(S=3, kv_len=5000, window=2000, ring_rows=2016, q_heads=16, kv_heads=2, head_dim=128)
+    g = torch.Generator().manual_seed(3)
+    w.q = [torch.randn(30, 16, 128, generator=g).bfloat16()]
+    w.seq_info = torch.tensor([[0, 10, 0, 5000], [10, 3, 1, 2100], [13, 17, 2, 40]], dtype=torch.int32)
+    w.max_q_len = 17
+    f = Fp4(pkv, w, garbage=False)
+    assert shares(pkv, f, 17)
+    out, lse, err = attend(pkv, f, max_kv=BIG)
+    assert err == 0
+    check(f, out, lse)
+
+
+@pytest.mark.parametrize("seg,bit", [((2, 1, 9, 5), 1), ((-1, 2, 0, 9), 1), ((2, 9, 0, 9), 1), ((2, 1, 0, 99999), 2),
+                                     ((2, 2, 1, 33), 8), ((2, 2, 1, 5990), 8), ((2, 2, 1, 17), 8), ((2, 4, 0, 9), 16)])
+def test_shares_wide_bad_segments_read_zero(pkv, seg, bit):
+    w = workloads.batched(S=2, max_len=6000, seed=4, lengths=[6000, 5990], q_heads=48, kv_heads=2)
+    w.block_table[1, 1] = 4000
+    w.q = [torch.randn(6, 48, 128).bfloat16()]
+    f = Fp4(pkv, w)
+    w.seq_info = torch.tensor([seg, [0, 2, 0, 5900]], dtype=torch.int32)
+    assert shares(pkv, f, 3)
+    out, lse, err = attend(pkv, f, causal=True, max_q=3, max_kv=BIG)
+    assert err == bit
+    assert (out[2:] == 0).all() and torch.isinf(lse[2:]).all()
+    w.seq_info = w.seq_info[1:]
+    check(f, out, lse, causal=True, rows=np.arange(6) < 2)
+
+
+def test_shares_wide_nan(pkv):
+    w = workloads.spec_verify(S=1, max_q=8, len_lo=5000, len_hi=5000, seed=6, q_heads=16, kv_heads=2)
+    w.seq_info = torch.tensor([[0, 8, 0, 5000]], dtype=torch.int32)
+    w.q = [torch.randn(8, 16, 128).bfloat16()]
+    f = Fp4(pkv, w)
+    for which, at in ((1, 4997), (1, 1234), (1, 4992), (0, 4997), (0, 777)):
+        pool = (f.cache.k if which == 0 else f.cache.v)[0]
+        keep = pool.clone()
+        c, s = R.unpack(pool.cpu().numpy(), bool(which))
+        s[int(w.block_table[0, at // 16]), at % 16, 1, 2] = 0xFF
+        pool.copy_(torch.from_numpy(R.pack(c, s, bool(which))))
+        out, lse, err = attend(pkv, f, causal=True, max_q=8, max_kv=BIG)
+        see = np.arange(4992, 5000) >= at
+        want = np.zeros((8, 16, 128), bool)
+        want[see, 8:, (32 if which else 0):(48 if which else 128)] = True
+        assert err == 0 and (out.isnan().cpu().numpy() == want).all()
+        assert (lse.isnan().cpu().numpy() == (want.all(-1))).all()
+        pool.copy_(keep)
+    q = w.q[0].clone()
+    q[3, 2, 7] = float("nan")
+    out, lse, _ = attend(pkv, f, q=q, causal=True, max_q=8, max_kv=BIG)
+    assert out[3, 2].isnan().all() and lse[3, 2].isnan() and int(out.isnan().any(-1).sum()) == 1
+
+
+@pytest.mark.parametrize("q_heads", [4, 64])
+def test_shares_scales_and_magnitudes(pkv, q_heads):
+    """A negative and a zero softmax scale, and queries far from fp16's range."""
+    w = workloads.batched(S=4, max_len=900, seed=5, q_heads=q_heads, kv_heads=2)
+    f = Fp4(pkv, w)
+    base = w.q[0].clone()
+
+    def go(q, scale):
+        out, lse, err = torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:2], device="cuda"), pkv.new_err_flags()
+        pkv.attend_varlen(f.cache, 0, q.cuda(), w.seq_info.cuda(), out, err, 1, BIG, scale, lse=lse)
+        assert int(err.item()) == 0
+        return out, lse
+    out, lse = go(base, w.scale)
+    for e in (-100, -40, 40, 100):
+        got, l2 = go((base.float() * 2.0 ** e).bfloat16(), w.scale * 2.0 ** -e)
+        assert torch.equal(got, out) and torch.equal(l2, lse)
+    got, l2 = go(-base, -w.scale)
+    assert torch.allclose(got, out, rtol=0, atol=1e-6) and torch.allclose(l2, lse, rtol=1e-6)
+    got, l2 = go(base, 0.0)
+    for s, (_, _, col, kend) in enumerate(w.seq_info.tolist()):
+        assert torch.allclose(l2[s], torch.full_like(l2[s], float(np.log(kend))), rtol=1e-5)
