@@ -368,10 +368,30 @@ struct Plan4 {
 constexpr long long kSharesFrom = 6144;
 constexpr int kSharesSegments = 512;
 constexpr int kSharesTiles = 16;  // each tile's range is taken as long as its segment's: not for long causal chunks
-constexpr int kPieceWide = 40;  // the same for the tcgen05 kernel, in pages
+constexpr int kPieceWide = 24;  // the same for the tcgen05 kernel, in pages
 // Rows a kv head from which the tcgen05 kernel (tiles of 128) is faster than mma.sync tiles of 32.
 constexpr int kWideFrom = 17;
 constexpr int kPieceBytes = 56 << 10;  // what a piece costs, as bytes that one CTA reads meanwhile
+
+// Whether the kernel was compiled to the register count its warps hand around
+// (setmaxnreg waits for registers the launch must have brought).
+bool regs_ok(const Attend4Kernel &k) {
+    static std::mutex mu;
+    static const void *fn = nullptr;
+    static bool ok = false;
+    if (!k.regs) return true;
+    std::lock_guard<std::mutex> lock(mu);
+    if (fn != k.balance) {
+        cudaFuncAttributes a;
+        if (cudaFuncGetAttributes(&a, k.balance) != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        ok = a.numRegs == k.regs;
+        fn = k.balance;
+    }
+    return ok;
+}
 
 struct Ws4Layout {
     size_t head, stat, part, total;
@@ -411,7 +431,8 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     pl->ncta = (int)std::max<long long>(1, std::min<long long>(n, max_pages));
     pl->shares = 0;
     if (num_splits == 0 && S > 0 && S <= kSharesSegments) {
-        pl->ks = c->head_dim == 128 && rows >= kWideFrom ? pick4_wide() : pl->k4;
+        pl->ks = pl->k4;
+        if (c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide())) pl->ks = pick4_wide();
         const long long tiles = (rows + pl->ks.rows - 1) / pl->ks.rows;
         const long long keys = window > 0 ? std::min<long long>(max_kv, (long long)window + max_q_len) : max_kv;
         const long long pages = (long long)S * c->kv_heads * tiles * ((keys + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE);

@@ -157,7 +157,7 @@ struct Smem4 {
     uint64_t *bars;              // [KW][NST]
     int *flag, *all_flags;       // own flags (1 bad page, 2 timeout), the cluster's [16]
     __device__ explicit Smem4(unsigned char *raw) {
-        pipe = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 127) & ~uintptr_t(127));
+        pipe = raw + (-smem_u32(raw) & 127u);  // pointer arithmetic keeps the shared address space (a cast would lose it)
         q = reinterpret_cast<uint2 *>(pipe + C::kBody);
         recv = reinterpret_cast<float *>(pipe + C::kBody + C::kQBytes);
         stat = reinterpret_cast<float2 *>(reinterpret_cast<unsigned char *>(recv) + C::kRecv);

@@ -1,9 +1,11 @@
 // Instantiates the 4-bit attention kernel for one head_dim (-DPKV_INST_D=<64|128|256>).
 #include "attend4.cuh"
-#include "wide4.cuh"
 
 #ifndef PKV_INST_D
 #error "PKV_INST_D not set"
+#endif
+#if PKV_INST_D == 128
+#include "wide4.cuh"
 #endif
 
 namespace pkv {
@@ -11,7 +13,7 @@ namespace pkv {
 template <class C>
 static Attend4Kernel info4() {
     return Attend4Kernel{reinterpret_cast<const void *>(&attend4_kernel<C>), reinterpret_cast<const void *>(&balance4_kernel<C>),
-                         reinterpret_cast<const void *>(&merge4_kernel<C::D, C::R, C::R == 8 ? kMerge4Threads : 32>), C::kThreads, C::kSmem, C::R, C::KW, C::kCtas};
+                         reinterpret_cast<const void *>(&merge4_kernel<C::D, C::R, C::R == 8 ? kMerge4Threads : 32>), C::kThreads, C::kSmem, C::R, C::KW, C::kCtas, 0};
 }
 
 #define PICK4_NAME2(D) pick4_##D
@@ -35,7 +37,7 @@ Attend4Kernel PICK4_NAME(PKV_INST_D)(int rows) {
 #if PKV_INST_D == 128
 Attend4Kernel pick4_wide() {
     return Attend4Kernel{nullptr, reinterpret_cast<const void *>(&wide4_kernel), reinterpret_cast<const void *>(&merge4_kernel<128, 128, 32>),
-                         Wide4::kThreads, Wide4::kSmem, Wide4::R, Wide4::kThreads / 32, 1};
+                         Wide4::kThreads, Wide4::kSmem, Wide4::R, 8, 1, Wide4::kRegs};
 }
 #endif
 

@@ -44,6 +44,7 @@ struct Attend4Kernel {
     int rows;   // query rows of a CTA
     int warps;
     int ctas;   // CTAs an SM holds
+    int regs;   // registers a thread the kernel has to be launched with (it hands them between its warps), or 0
 };
 
 // The kernel for head_dim D and at most `rows` query rows a (segment, kv head).
