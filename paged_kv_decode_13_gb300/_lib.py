@@ -88,7 +88,7 @@ def _declare(lib):
     p = ctypes.c_void_p
     f64 = ctypes.c_double
     cp = ctypes.POINTER(CacheDesc)
-    rp, wp = ctypes.POINTER(RopeDesc), ctypes.POINTER(RowsDesc)
+    rp, wp = ctypes.POINTER(RopeDesc), ctypes.c_void_p  # pkv_rows: a RowsDesc by reference, or its bytes
     sigs = {
         "pkv_bucket_for": (i64, [i64]),
         "pkv_status_str": (ctypes.c_char_p, [ctypes.c_int]),

@@ -7,6 +7,7 @@ CUDA kernels; torch supplies device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -213,6 +214,11 @@ class Rope:
             raise ValueError("norm weights are (head_dim,) of the rows' type")
 
 
+# struct pkv_rows as bytes (native sizes and alignment): cheaper to make than a ctypes structure
+_ROWS = struct.Struct("6Q6q2iQ")
+assert _ROWS.size == ctypes.sizeof(_lib.RowsDesc)
+
+
 def _row_stride(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: int) -> int:
     """Elements between the rows of t, whose heads and columns are contiguous and whose rows are apart as they like."""
     if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
@@ -224,21 +230,21 @@ def _row_stride(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: i
     return s0 if rows > 1 else heads * dim
 
 
-def _rows_desc(q, k, v, q_out, k_out, v_out, positions, kv_heads, head_dim, dtype, device) -> _lib.RowsDesc:
-    some = q if q is not None else k
-    if some.dim() != 3:
+def _rows_desc(q, k, v, q_out, k_out, v_out, positions, kv_heads, head_dim, dtype, device) -> bytes:
+    shape = (q if q is not None else k).shape
+    if len(shape) != 3:
         raise ValueError("rows are (rows, heads, head_dim)")
-    rows, hq, _ = some.shape
+    rows, hq = shape[0], 0
     kv = (rows, kv_heads, head_dim)
-    qp = kp = vp = qop = kop = vop = pos = None
+    qp = kp = vp = qop = kop = vop = pos = 0
     qs = ks = vs = qos = kos = vos = 0
     if q is not None:
-        qs, qp = _row_stride(q, "q", (rows, hq, head_dim), dtype, device), q.data_ptr()
-        qos, qop = (qs, qp) if q_out is q else (_row_stride(q_out, "q_out", (rows, hq, head_dim), dtype, device), q_out.data_ptr())
-    else:
-        hq = 0
-        if q_out is not None:
-            raise ValueError("q_out without q")
+        hq = shape[1]
+        heads = (rows, hq, head_dim)
+        qs, qp = _row_stride(q, "q", heads, dtype, device), q.data_ptr()
+        qos, qop = (qs, qp) if q_out is q else (_row_stride(q_out, "q_out", heads, dtype, device), q_out.data_ptr())
+    elif q_out is not None:
+        raise ValueError("q_out without q")
     if k is not None:
         ks, kp = _row_stride(k, "k", kv, dtype, device), k.data_ptr()
     if v is not None:
@@ -251,17 +257,26 @@ def _rows_desc(q, k, v, q_out, k_out, v_out, positions, kv_heads, head_dim, dtyp
         if positions.shape != (rows,) or positions.dtype is not torch.int32 or positions.get_device() != device:
             raise ValueError(f"positions is int32 ({rows},) on device {device}")
         pos = _contig(positions, "positions").data_ptr()
-    return _lib.RowsDesc(qp, kp, vp, qop, kop, vop, qs, ks, vs, qos, kos, vos, hq, rows, pos)
+    return _ROWS.pack(qp, kp, vp, qop, kop, vop, qs, ks, vs, qos, kos, vos, hq, rows, pos)
 
 
-def _on_device(device: int, fn, stream) -> int:
-    """fn(stream handle) with `device` current, whichever is."""
+def _raw_stream(device: int, stream) -> int:
+    """The handle of `stream` or of the device's current stream, for a launch on it as the current device."""
     if device < 0:
         raise ValueError("the tensors are not on a CUDA device")
-    if device != torch._C._cuda_getDevice():
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+
+
+def _launch(name: str, fn, args, device: int, stream) -> None:
+    """fn(*args, stream) with `device` current, whichever is."""
+    handle = _raw_stream(device, stream)
+    if device == torch._C._cuda_getDevice():
+        st = fn(*args, handle)
+    else:
         with torch.cuda.device(device):
-            return fn(_stream(stream))
-    return fn(stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device))
+            st = fn(*args, handle)
+    if st:
+        _lib.check(name, st)
 
 
 def norm_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
@@ -284,8 +299,7 @@ def norm_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
     kv = int(k.shape[1]) if k is not None and k.dim() == 3 else 0
     d = _rows_desc(q, k, None, q_out if q_out is not None else q, k_out if k_out is not None else k, None, positions, kv, dim,
                    dtype, dev)
-    _lib.check("pkv_norm_rope", _on_device(dev, lambda st: lib.pkv_norm_rope(rope._ref, _DTYPES[dtype], dim, kv, ctypes.byref(d), st),
-                                           stream))
+    _launch("pkv_norm_rope", lib.pkv_norm_rope, (rope._ref, _DTYPES[dtype], dim, kv, d), dev, stream)
 
 
 def norm_rope_append(cache: PagedKVCache, layer: int, rope: Optional[Rope], q: Optional[torch.Tensor], k_new: torch.Tensor,
@@ -305,11 +319,9 @@ def norm_rope_append(cache: PagedKVCache, layer: int, rope: Optional[Rope], q: O
     if seq_info.dtype is not torch.int32 or len(si) != 2 or si[1] != 4 or seq_info.get_device() != dev:
         raise ValueError(f"seq_info is int32 (segments, 4) on device {dev}")
     d = _rows_desc(q, k_new, v_new, q if q_out is None else q_out, k_out, v_out, positions, cache._kv_heads, dim, dtype, dev)
-    table = _contig(seq_info, "seq_info").data_ptr()
-    st = _on_device(dev, lambda st: lib.pkv_norm_rope_append(cache._ref, layer, None if rope is None else rope._ref, ctypes.byref(d), table,
-                                                             si[0], window, err.data_ptr(), st), stream)
-    if st:
-        _lib.check("pkv_norm_rope_append", st)
+    _launch("pkv_norm_rope_append", lib.pkv_norm_rope_append,
+            (cache._ref, layer, None if rope is None else rope._ref, d, _contig(seq_info, "seq_info").data_ptr(), si[0], window, err.data_ptr()),
+            dev, stream)
 
 
 def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, seq_info: torch.Tensor,

@@ -414,7 +414,13 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     pl->G = Hq / c->kv_heads;
     const long long rows = (long long)pl->G * max_q_len;
     if (rows > (1 << 20)) return PKV_EINVAL;
-    pl->k4 = c->head_dim == 64 ? pick4_64((int)rows) : c->head_dim == 128 ? pick4_128((int)rows) : pick4_256((int)rows);
+    auto pick4 = [&](bool few) {
+        return c->head_dim == 64 ? pick4_64((int)rows, few) : c->head_dim == 128 ? pick4_128((int)rows, few) : pick4_256((int)rows, few);
+    };
+    pl->k4 = pick4(false);
+    const Attend4Kernel small = pl->k4;  // of equal shares
+    // Few ranges: CTAs of eight warps, each with fewer pages to wait for.
+    if ((long long)std::max(S, 1) * c->kv_heads * 8 <= device_sms()) pl->k4 = pick4(true);
     pl->k = AttnKernel{pl->k4.fn, pl->k4.threads, pl->k4.smem, pl->k4.rows, c->head_dim, true, false};
     pl->row_tiles = (int)((rows + pl->k4.rows - 1) / pl->k4.rows);
     if ((long long)c->kv_heads * pl->row_tiles > 65535) return PKV_EINVAL;
@@ -431,7 +437,7 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     pl->ncta = (int)std::max<long long>(1, std::min<long long>(n, max_pages));
     pl->shares = 0;
     if (num_splits == 0 && S > 0 && S <= kSharesSegments) {
-        pl->ks = pl->k4;
+        pl->ks = small;
         if (c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide())) pl->ks = pick4_wide();
         const long long tiles = (rows + pl->ks.rows - 1) / pl->ks.rows;
         const long long keys = window > 0 ? std::min<long long>(max_kv, (long long)window + max_q_len) : max_kv;

@@ -196,7 +196,7 @@ __device__ __forceinline__ void refuse4(const Attend4Params &p, const Segment &s
 // Attend one piece: every warp takes every KW-th of its pages and leaves its
 // partial rows and (max, sum) in shared memory.  ring: stages this warp has
 // used so far.  dep: the dependency wait happens in here, after the first
-// copies.  Returns the CTA's flags.
+// copies, and with it the rows no segment covers.  Returns the CTA's flags.
 template <class C>
 __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<C> &sm, const Piece4 &w, int &ring, bool dep) {
     constexpr int D = C::D, NT = C::NT, KW = C::KW, NST = C::NST, KS = C::KS, R = C::R, LD = C::LD, PP = C::PP;
@@ -270,6 +270,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
     }
 #pragma unroll 1
     for (; issued < NST && issued < stages; ++issued) issue(issued);
+    if (dep) coverage4<D>(p);  // while the copies are on their way
 
     // ---- Q^T fragments of one 8-row tile: lane (g, t) holds row g, columns t D/4 ..
     auto load_q = [&](int nt, unsigned (&f)[KS][2]) {
@@ -659,7 +660,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
     report4(p, flags);
     if (ncl == 1) {
         write_rows4<C>(p, sm, w, flags);
-        coverage4<D>(p);
         return;
     }
     // ---- merge across the cluster: every CTA pushes its merged partial of each
@@ -712,7 +712,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
         }
         store_out4(p, out_row4(p, w, r) * D + 4 * c4, o);
     }
-    coverage4<D>(p);
 }
 
 // ---------------------------------------------------------------- equal shares of all ranges
@@ -879,6 +878,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) balance4_kernel(const _
     if (!waited) {
         pdl_wait();
         pdl_trigger();
+        coverage4<D>(p);
     }
     // (only after the dependency wait: the kernel before may be the last call's merge)
     if (tid < 2 && !(left >> tid & 1)) p.ws_head[2 * cta + tid].w = 0;
@@ -889,7 +889,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) balance4_kernel(const _
         const unsigned fault = fault4(p, sg);
         if (fault) refuse4<D>(p, sg, fault, 0, p.Hkv);
     }
-    coverage4<D>(p);
 }
 
 // Merge of the shared ranges: CTA (i, y) finishes rows y .. of the range that

@@ -19,16 +19,19 @@ static Attend4Kernel info4() {
 #define PICK4_NAME2(D) pick4_##D
 #define PICK4_NAME(D) PICK4_NAME2(D)
 
-Attend4Kernel PICK4_NAME(PKV_INST_D)(int rows) {
+Attend4Kernel PICK4_NAME(PKV_INST_D)(int rows, bool few) {
 #if PKV_INST_D == 64
+    if (rows <= 8 && few) return info4<Cfg4<64, 1, 8, 2, 2, 2, false>>();
     if (rows <= 8) return info4<Cfg4<64, 1, 4, 4, 2, 4, false>>();
     if (rows <= 16) return info4<Cfg4<64, 2, 8, 4, 1, 2, true>>();
     return info4<Cfg4<64, 4, 8, 4, 1, 1, true>>();
 #elif PKV_INST_D == 128
+    if (rows <= 8 && few) return info4<Cfg4<128, 1, 8, 2, 2, 2, false>>();
     if (rows <= 8) return info4<Cfg4<128, 1, 4, 2, 2, 4, false>>();
     if (rows <= 16) return info4<Cfg4<128, 2, 8, 4, 1, 1, true>>();
     return info4<Cfg4<128, 4, 4, 4, 1, 2, true>>();
 #else
+    if (rows <= 8 && few) return info4<Cfg4<256, 1, 8, 3, 1, 1, true>>();
     if (rows <= 8) return info4<Cfg4<256, 1, 4, 3, 1, 3, true>>();
     return info4<Cfg4<256, 2, 8, 3, 1, 1, true>>();
 #endif

@@ -47,10 +47,11 @@ struct Attend4Kernel {
     int regs;   // registers a thread the kernel has to be launched with (it hands them between its warps), or 0
 };
 
-// The kernel for head_dim D and at most `rows` query rows a (segment, kv head).
-Attend4Kernel pick4_64(int rows);
-Attend4Kernel pick4_128(int rows);
-Attend4Kernel pick4_256(int rows);
+// The kernel for head_dim D and at most `rows` query rows a (segment, kv head);
+// few: there are few ranges, and a CTA has twice the warps.
+Attend4Kernel pick4_64(int rows, bool few);
+Attend4Kernel pick4_128(int rows, bool few);
+Attend4Kernel pick4_256(int rows, bool few);
 // The tcgen05 kernel of wide groups (head_dim 128, equal shares only: fn is null).
 Attend4Kernel pick4_wide();
 
