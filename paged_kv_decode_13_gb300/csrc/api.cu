@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include <math.h>
@@ -65,11 +66,18 @@ constexpr int kMaxSplitsGm = 64;  // splits per key range when merging through g
 
 // SMs of the current device (GB300's count when no device answers).
 int device_sms() {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
         return kDefaultSms;
     }
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return kDefaultSms;
+    }
+    if (dev >= 0 && dev < 64 && n > 0) known[dev].store(n, std::memory_order_relaxed);
     return n > 0 ? n : kDefaultSms;
 }
 
@@ -368,7 +376,7 @@ struct Plan4 {
 constexpr long long kSharesFrom = 6144;
 constexpr int kSharesSegments = 512;
 constexpr int kSharesTiles = 16;  // each tile's range is taken as long as its segment's: not for long causal chunks
-constexpr int kPieceWide = 24;  // the same for the tcgen05 kernel, in pages
+constexpr int kPieceWide = 36;  // the same for the tcgen05 kernel, in pages
 // Rows a kv head from which the tcgen05 kernel (tiles of 128) is faster than mma.sync tiles of 32.
 constexpr int kWideFrom = 17;
 constexpr int kPieceBytes = 56 << 10;  // what a piece costs, as bytes that one CTA reads meanwhile
@@ -494,6 +502,7 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     p.causal = causal;
     p.window = window;
     p.out_bf16 = (flags & PKV_FLAG_OUT_BF16) ? 1 : 0;
+    p.early = (flags & PKV_FLAG_PDL) ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.piece_pages = shares && pl.ks.rows == 128 ? kPieceWide : kPieceBytes / (2 * block4_bytes(c->head_dim));
     p.ws_head = nullptr;
@@ -520,7 +529,7 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
         attr[na].val.clusterDim.z = 1;
         ++na;
     }
-    if (flags & PKV_FLAG_PDL) {
+    if (!shares || (flags & PKV_FLAG_PDL)) {  // (an early start gains a long launch nothing, and takes room from the merge before it)
         attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[na].val.programmaticStreamSerializationAllowed = 1;
         ++na;

@@ -61,11 +61,6 @@ struct Cfg4 {
     static_assert(kSmem <= 232448, "exceeds the per-CTA shared memory limit");
 };
 
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, unsigned bytes, uint64_t *bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(smem_u32(dst)),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
 // D = A(16x16 fp16, row) * B(16x8 fp16, col) + D, fp32 accumulate.
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
                                               unsigned b1) {
@@ -132,6 +127,17 @@ __device__ __noinline__ void coverage4(const Attend4Params &p) {
         n = __reduce_add_sync(0xffffffffu, n);
         if (n == 0) zero_row4(p, row, 0, p.Hq, D, lane, 32);
         if (n > 1 && lane == 0) atomicOr(p.err, PKV_ERR_OVERLAP);
+    }
+}
+
+// The dependency wait.  Every launch is a programmatic dependent one, so that
+// its start overlaps the kernel before it; with PKV_FLAG_PDL (p.early) the
+// segment table, the block table and old pages are read before the wait
+// (second call), otherwise nothing is (first call).
+__device__ __forceinline__ void depend4(const Attend4Params &p, bool second) {
+    if ((p.early != 0) == second) {
+        pdl_wait();
+        pdl_trigger();
     }
 }
 
@@ -265,8 +271,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
         // the kernel before this one still writes.
 #pragma unroll 1
         for (; issued < NST && issued < stages && (cb0 + kw + (issued * PP + PP - 1) * KW + 1) * kPage <= new_start; ++issued) issue(issued);
-        pdl_wait();
-        pdl_trigger();
+        depend4(p, true);
     }
 #pragma unroll 1
     for (; issued < NST && issued < stages; ++issued) issue(issued);
@@ -624,13 +629,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
     const Smem4<C> sm(smem_raw);
     const int tid = threadIdx.x, rank = blockIdx.x, ncta = gridDim.x;
     const int tile = blockIdx.y % p.row_tiles, s = blockIdx.z;
+    depend4(p, false);
     auto leave = [&] {
-        pdl_wait();
-        pdl_trigger();
+        depend4(p, true);
         coverage4<D>(p);
     };
     if (p.S == 0) return leave();
-    // the segment and this tile's key range are read before the dependency wait
     Piece4 w;
     w.h = blockIdx.y / p.row_tiles;
     w.sg = load_segment(p.seq_info, s);
@@ -638,8 +642,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
     w.row0 = tile * R;
     w.rows = fault ? 0 : min(R, w.sg.ql * p.G - w.row0);
     if (w.rows <= 0) {  // uniform across the cluster
-        pdl_wait();
-        pdl_trigger();
+        depend4(p, true);
         if (fault && rank == 0 && tile == 0) refuse4<D>(p, w.sg, fault, w.h, w.h + 1);
         coverage4<D>(p);
         return;
@@ -845,6 +848,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) balance4_kernel(const _
     const Smem4<C> sm(smem_raw);
     const int tid = threadIdx.x, cta = blockIdx.x;
     init_bars4<C>(sm);
+    depend4(p, false);
     Share4 share;
     share.find<NTHR>(p, R, reinterpret_cast<long long *>(sm.recv));
     int ring = 0, left = 0;  // left: bit i, a piece in slot 2 cta + i
@@ -876,8 +880,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) balance4_kernel(const _
         fence_proxy_async();      // and the next copies may write over them
     }
     if (!waited) {
-        pdl_wait();
-        pdl_trigger();
+        depend4(p, true);
         coverage4<D>(p);
     }
     // (only after the dependency wait: the kernel before may be the last call's merge)

@@ -24,6 +24,7 @@ struct Attend4Params {
     int row_tiles;                // CTAs along the rows of one (segment, kv head)
     int min_pages;                // pages of a range worth a CTA of the cluster
     int causal, window, out_bf16;
+    int early;                    // PKV_FLAG_PDL: the tables and old pages may be read before the dependency wait
     float scale_log2;             // softmax scale * log2(e)
     // equal shares (balance4_kernel)
     int piece_pages;              // what a piece of a range costs besides its pages, in pages

@@ -37,16 +37,22 @@ constexpr unsigned kScaleNan = 0xFF;  // an fp16 NaN: a group with a NaN reads b
 __host__ __device__ constexpr int block4_bytes(int head_dim) { return 9 * head_dim; }
 
 // Scale byte of a group whose largest magnitude has the float bits `amax`
-// (NaN payloads compare above infinity): nearest e5m3 to max / 6, ties to even.
+// (NaN payloads compare above infinity; a bf16 number): nearest e5m3 to max / 6,
+// ties to even.  max / 6 is on a border between two scales (a number of at most
+// 5 significant bits) or at least 2^-10 of it away, and max * (1 / 6) is within
+// 2^-23 of it: rounded to 16 significant bits it is on the same side, or on the
+// border exactly.
 __device__ __forceinline__ unsigned scale4_of(unsigned amax) {
     if (amax > 0x7f800000u) return kScaleNan;
-    const float a = __fdiv_rn(__uint_as_float(amax), 6.f);
-    if (a < 6.103515625e-05f) return (unsigned)__float2int_rn(a * 131072.f);  // steps of 2^-17 below 2^-14
-    const unsigned u = __float_as_uint(a);
+    const unsigned u = (__float_as_uint(__uint_as_float(amax) * 0.16666667f) + 0x80u) & ~0xffu;
+    if (u < 0x38800000u) return (unsigned)__float2int_rn(__uint_as_float(u) * 131072.f);  // steps of 2^-17 below 2^-14
     return min(((u + 0x7ffffu + ((u >> 20) & 1u)) >> 20) - (112u << 3), kScaleMax);
 }
-__device__ __forceinline__ float scale4_value(unsigned byte) {
-    return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
+// 1 / scale to within 2^-22 (0 for a zero scale, whose codes are all 0).
+__device__ __forceinline__ float scale4_inverse(unsigned byte) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(__half2float(__ushort_as_half((unsigned short)(byte << 7)))));
+    return byte ? r : 0.f;
 }
 // Eight floats to eight e2m1 codes, x[0] in the low nibble (nearest, ties to
 // even, saturating at 6).

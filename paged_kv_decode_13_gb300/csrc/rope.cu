@@ -28,7 +28,7 @@ cudaError_t launch_rope(RopeParams &p, int cache, bool f32, int sms, cudaStream_
     // Few rows: a row's heads are spread over warps until there are about
     // kRopeFill warps an SM.  Many rows: about kRopeFill warps an SM take them
     // in turn, each keeping a row's angles for all its heads.
-    const long long fill = (long long)kRopeFill * sms, want = (fill + std::max(p.rows, 1) - 1) / std::max(p.rows, 1);
+    const long long fill = (long long)kRopeFill * sms, want = (long long)kRopeSpread * sms / std::max(p.rows, 1);
     p.slices = (int)std::max<long long>(1, std::min<long long>(want, all));
     p.row_ctas = (int)((std::min<long long>(p.rows, std::max<long long>(fill, 1)) * p.slices + kRopeWarps - 1) / kRopeWarps);
     if (cache != kNoCache) p.row_ctas = std::max(p.row_ctas, 1);  // the first looks at the refused segments
@@ -38,16 +38,28 @@ cudaError_t launch_rope(RopeParams &p, int cache, bool f32, int sms, cudaStream_
     if (cache == kFp4) {
         // V pages of one (segment, kv head): no more warps than it can have new pages
         const long long units = (long long)p.S * p.Hkv, pages = (p.rows + kPage - 2) / kPage + 1;
-        p.page_warps = (int)std::max<long long>(1, std::min((fill + units - 1) / units, pages));
+        p.page_warps = (int)std::max<long long>(1, std::min(fill / units, pages));
         ctas += (units * p.page_warps + kRopeWarps - 1) / kRopeWarps;
         smem = std::max(smem, (size_t)kRopeWarps * kPage * (p.D + p.D / 16));
     }
     if (ctas == 0) return cudaSuccess;
-    const void *fn = cache == kFp4         ? pick_pair<__nv_bfloat16, kFp4>(pair)
-                     : cache == kSameType  ? (f32 ? pick_pair<float, kSameType>(pair) : pick_pair<__nv_bfloat16, kSameType>(pair))
-                                           : (f32 ? pick_pair<float, kNoCache>(pair) : pick_pair<__nv_bfloat16, kNoCache>(pair));
+    const void *fn = cache == kFp4        ? pick_pair<__nv_bfloat16, kFp4>(pair)
+                     : cache == kSameType ? (f32 ? pick_pair<float, kSameType>(pair) : pick_pair<__nv_bfloat16, kSameType>(pair))
+                                          : (f32 ? pick_pair<float, kNoCache>(pair) : pick_pair<__nv_bfloat16, kNoCache>(pair));
     void *args[] = {&p};
-    return cudaLaunchKernel(fn, dim3((unsigned)ctas), dim3(kRopeWarps * 32), args, smem, stream);
+    // Programmatic dependent launch: the kernel waits for the one before it
+    // first thing, and only its start overlaps that one's end.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kRopeWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute after;
+    after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    after.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &after;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 }  // namespace pkv

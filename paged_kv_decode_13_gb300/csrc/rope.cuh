@@ -131,7 +131,7 @@ struct Raw8 {
 //
 // x / s: s has 4 significant bits and x 8, so the quotient is either exactly
 // on a border between two codes (a multiple of 1/4) or at least 2^-8 of it
-// away.  x * (1 / s), whose error is below 2^-22, rounded to a multiple of
+// away.  x * (1 / s), whose error is below 2^-21, rounded to a multiple of
 // 2^-11 by adding and taking off 3 * 2^11, is therefore on the same side, and
 // exactly on the border where x / s is: the code is that of the exact quotient.
 __device__ __forceinline__ unsigned quantise8(Raw8<__nv_bfloat16> &x, unsigned &scale, bool stored) {
@@ -142,11 +142,16 @@ __device__ __forceinline__ unsigned quantise8(Raw8<__nv_bfloat16> &x, unsigned &
     amax = max(amax << 16, amax & 0xffff0000u);  // a NaN's bits are above all others
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     scale = scale4_of(amax);
-    const float inv = scale ? __frcp_rn(scale4_value(scale)) : 0.f;  // a zero scale: codes 0 with the signs of x
+    const float inv = scale4_inverse(scale);  // a zero scale: codes 0 with the signs of x
     float v[8];
     x.get(v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = copysignf((fmaf(fabsf(v[i]), inv, 6144.f) - 6144.f), v[i]);
+    for (int i = 0; i < 8; i += 2) {
+        float a, b;
+        f32x2_split(add_f32x2(fma_f32x2(f32x2(v[i], v[i + 1]), f32x2(inv, inv), f32x2(6144.f, 6144.f)), f32x2(-6144.f, -6144.f)), a, b);
+        v[i] = copysignf(a, v[i]);
+        v[i + 1] = copysignf(b, v[i + 1]);
+    }
     const unsigned codes = pack_e2m1x8(v);
     if (stored) {
         unsigned h[4];
@@ -203,16 +208,18 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T 
                 raw[u].get(x);
                 float rinv = 1.f;
                 if (norm) {
-                    float ss = 0.f;
+                    uint64_t s2 = 0;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1)
-                        if (o < per) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    for (int e = 0; e < 8; e += 2) s2 = fma_f32x2(f32x2(x[e], x[e + 1]), f32x2(x[e], x[e + 1]), s2);
+                    float ss, st;
+                    f32x2_split(s2, ss, st);
+                    ss += st;
+                    for (int o = per >> 1; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                     rinv = rsqrtf(fmaf(ss, inv_d, p.eps));
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = x[e] * ca[e];
+                for (int e = 0; e < 8; e += 2)
+                    f32x2_split(mul_f32x2(f32x2(x[e], x[e + 1]), f32x2(ca[e], ca[e + 1])), y[e], y[e + 1]);
                 if (turn) {
                     float z[8];  // the partner columns' values
                     if constexpr (PAIR == kInLane) {
@@ -239,7 +246,8 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T 
                     if (whole) {
                         if (turned)
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) y[e] = fmaf(z[e], sb[e], y[e]);
+                            for (int e = 0; e < 8; e += 2)
+                                f32x2_split(fma_f32x2(f32x2(z[e], z[e + 1]), f32x2(sb[e], sb[e + 1]), f32x2(y[e], y[e + 1])), y[e], y[e + 1]);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
@@ -248,7 +256,7 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T 
                 }
                 if (norm)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] *= rinv;
+                    for (int e = 0; e < 8; e += 2) f32x2_split(mul_f32x2(f32x2(y[e], y[e + 1]), f32x2(rinv, rinv)), y[e], y[e + 1]);
                 raw[u].set(y);
             }
             if constexpr (CACHE == kFp4) {
@@ -272,6 +280,129 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T 
     }
 }
 
+// Where a row goes; false where it goes nowhere (no valid segment, or a bad
+// page).  sg: the segment of the row before, looked up again when the row is
+// past it.  The whole warp asks.
+__device__ __forceinline__ bool place_row(const RopeParams &p, int row, Segment &sg, bool &pages_ok, RopeSlot &slot, long long &place, int lane) {
+    if (!(sg.q0 <= row && (long long)row < (long long)sg.q0 + sg.ql)) {
+        const int s = segment_of_row(p, row, lane);
+        if (s < 0) {
+            sg.ql = 0;
+            return false;
+        }
+        sg = load_segment(p.seq_info, s);
+        pages_ok = new_pages_ok(p, sg, lane);
+        if (!pages_ok && lane == 0) atomicOr(p.err, PKV_ERR_BLOCK);
+    }
+    if (!pages_ok) return false;
+    place = (long long)sg.kend - sg.ql + (row - sg.q0);
+    slot.block = p.block_table[(long long)sg.col * p.mbps + table_page((int)(place / kPage), p.ring_rows)];
+    slot.token = (int)(place % kPage);
+    return true;
+}
+
+// Cosine and sine (times mscale) of position `pos` at a pair of `turn`.
+__device__ __forceinline__ float2 angle_of(unsigned pos, unsigned long long turn, float mscale) {
+    const unsigned f = pos * (unsigned)(turn >> 32) + __umulhi(pos, (unsigned)turn) -
+                       ((int)pos < 0 ? (unsigned)turn : 0u);  // (pos mod 2^64) * turn, bits 32..63
+    float si, co;
+    sincospif((float)(int)f * 4.656612873077393e-10f, &si, &co);  // 2^-31: half turns in [-1, 1]
+    return make_float2(co * mscale, si * mscale);
+}
+
+// The heads of one row that groups [f0, f1) name (q, then k, then v), from
+// `rows[kind]` (global or shared memory); angles: the row's pairs.
+struct RopeWork {
+    int f0, f1, nq, nk, all;   // groups of heads: this warp's, and of each kind
+    unsigned turned;           // columns of this lane that are rotated
+    int partner;               // lane of the partner columns (by shuffle)
+};
+template <typename T, int CACHE, int PAIR>
+__device__ __forceinline__ void rope_row(const RopeParams &p, int row, const RopeSlot &slot, const float2 *angles, const T *const (&rows)[3],
+                                         const RopeWork &w, float *stage, int lane) {
+    const int per = 1 << p.lanes_log2, c = lane & (per - 1), half = p.rot_dim / 2, heads = 32 >> p.lanes_log2;
+    int first = 0;
+#pragma unroll 1
+    for (int kind = 0; kind < (CACHE == kSameType ? 3 : 2); ++kind) {  // q, k, v
+        const int H = kind == 0 ? p.Hq : p.Hkv, groups = kind == 0 ? w.nq : kind == 1 ? w.nk : w.all - w.nq - w.nk;
+        const int h0 = max(w.f0 - first, 0) * heads, h1 = min(max(w.f1 - first, 0) * heads, H);
+        first += groups;
+        if (groups == 0 || h0 >= h1) continue;
+        const T *src = kind == 0 ? rows[0] : kind == 1 ? rows[1] : rows[2];
+        T *dst = reinterpret_cast<T *>(kind == 0 ? p.q_out : kind == 1 ? p.k_out : p.v_out);
+        if (dst) dst += row * (kind == 0 ? p.q_out_stride : kind == 1 ? p.k_out_stride : p.v_out_stride);
+        unsigned char *pool = reinterpret_cast<unsigned char *>(kind == 0 ? nullptr : kind == 1 ? p.k_pool : p.v_pool);
+        const T *weight = reinterpret_cast<const T *>(kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr);
+        // this lane's columns: cosine and signed sine, then the head weights
+        const bool turn = kind < 2 && p.rot_dim > 0;
+        float ca[8], sb[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ca[e] = 1.f;
+            sb[e] = 0.f;
+        }
+        if (turn) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int d = c * 8 + e, i = PAIR == kInLane ? d / 2 : d < half ? d : d - half;
+                if (w.turned >> e & 1u) {
+                    const float2 t = angles[i];
+                    ca[e] = t.x;
+                    sb[e] = (PAIR == kInLane ? e & 1 : d >= half) ? t.y : -t.y;
+                }
+            }
+        }
+        if (weight) {
+            Raw8<T> r;
+            r.clear();
+            if (c * 8 < p.D) r.load(weight + c * 8);
+            float wt[8], wz[8];  // the columns' weights, and their partners'
+            r.get(wt);
+            if constexpr (PAIR == kInLane) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) wz[e] = wt[e ^ 1];
+            } else if constexpr (PAIR == kByShuffle) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) wz[e] = __shfl_sync(0xffffffffu, wt[e], w.partner);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int d = c * 8 + e, o = d < half ? d + half : d - half;
+                    wz[e] = 1.f;
+                    if (w.turned >> e & 1u) {
+                        if constexpr (sizeof(T) == 2) wz[e] = __bfloat162float(weight[o]);
+                        else wz[e] = weight[o];
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ca[e] *= wt[e];
+                sb[e] *= wz[e];
+            }
+        }
+        rope_heads<T, CACHE, PAIR>(p, src, dst, pool, slot, h0, h1, ca, sb, weight != nullptr, turn, w.turned, w.partner,
+                                   stage, lane);
+    }
+}
+
+// Part `slice` of `slices` of a row's groups of heads (q, then k, then v, cut evenly).
+template <int CACHE, int PAIR>
+__device__ __forceinline__ RopeWork rope_work(const RopeParams &p, int slice, int slices, int lane) {
+    const int per = 1 << p.lanes_log2, c = lane & (per - 1), half = p.rot_dim / 2, heads = 32 >> p.lanes_log2;
+    RopeWork w;
+    w.partner = lane;
+    if (PAIR == kByShuffle && c < half / 4) w.partner = lane + (c < half / 8 ? half / 8 : -(half / 8));  // the halves are whole lanes
+    const int left = p.rot_dim - c * 8;  // rotated columns from this lane's first on
+    w.turned = left >= 8 ? 0xffu : left <= 0 ? 0u : (1u << left) - 1u;
+    w.nq = p.q ? (p.Hq + heads - 1) / heads : 0;
+    w.nk = p.k ? (p.Hkv + heads - 1) / heads : 0;
+    w.all = w.nq + w.nk + (CACHE == kSameType ? (p.Hkv + heads - 1) / heads : 0);
+    w.f0 = (int)((long long)w.all * slice / slices);
+    w.f1 = (int)((long long)w.all * (slice + 1) / slices);
+    return w;
+}
+
 // Write the 4-bit V page `pb` of kv head h from the segment's new rows.
 template <int D>
 __device__ __forceinline__ void write_v4_page(const RopeParams &p, const Segment &sg, int h, int pb, unsigned char *codes,
@@ -281,24 +412,32 @@ __device__ __forceinline__ void write_v4_page(const RopeParams &p, const Segment
     const int a = max(start - pb * kPage, 0), b = min(sg.kend - pb * kPage, kPage);  // new tokens of the page
     const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(p.v);
     __syncwarp();
-#pragma unroll 4
-    for (int t0 = 0; t0 < kPage; t0 += TPI) {
-        if (t0 + TPI <= a || t0 >= b) continue;  // uniform
-        const int tok = t0 + sub;
-        const bool mine = tok >= a && tok < b;
-        const long long row = (long long)sg.q0 + (pb * kPage + tok - start);
-        Raw8<__nv_bfloat16> x;
-        x.clear();
-        if (mine) x.load(v + row * p.v_stride + h * D + c * 8);
-        unsigned scale;
-        const unsigned w = quantise8(x, scale, p.v_out != nullptr);
-        if (mine) {
-            // one code a byte, for the exchange below
-            const unsigned lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
-            *reinterpret_cast<uint2 *>(codes + tok * D + c * 8) =
-                make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
-            if ((c & 1) == 0) scales[tok * (D / 16) + c / 2] = (unsigned char)scale;
-            if (p.v_out) x.store(reinterpret_cast<__nv_bfloat16 *>(p.v_out) + row * p.v_out_stride + h * D + c * 8);
+    constexpr int B = 16 / TPI < 8 ? 16 / TPI : 8;  // rows of the lane that are loaded together
+#pragma unroll 1
+    for (int tb = 0; tb < kPage; tb += B * TPI) {
+        Raw8<__nv_bfloat16> x[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int tok = tb + i * TPI + sub;
+            x[i].clear();
+            if (tok >= a && tok < b) x[i].load(v + ((long long)sg.q0 + (pb * kPage + tok - start)) * p.v_stride + h * D + c * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+            const int t0 = tb + i * TPI, tok = t0 + sub;
+            if (t0 + TPI <= a || t0 >= b) continue;  // uniform
+            const bool mine = tok >= a && tok < b;
+            unsigned scale;
+            const unsigned w = quantise8(x[i], scale, p.v_out != nullptr);
+            if (mine) {
+                // one code a byte, for the exchange below
+                const unsigned lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
+                *reinterpret_cast<uint2 *>(codes + tok * D + c * 8) =
+                    make_uint2(__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362));
+                if ((c & 1) == 0) scales[tok * (D / 16) + c / 2] = (unsigned char)scale;
+                if (p.v_out)
+                    x[i].store(reinterpret_cast<__nv_bfloat16 *>(p.v_out) + ((long long)sg.q0 + (pb * kPage + tok - start)) * p.v_out_stride + h * D + c * 8);
+            }
         }
     }
     __syncwarp();
@@ -335,6 +474,30 @@ __device__ __forceinline__ void write_v4_page(const RopeParams &p, const Segment
     }
 }
 
+// The V pages of one (segment, kv head, page warp) unit, page warps fastest.
+__device__ __forceinline__ void write_v4_pages(const RopeParams &p, long long unit, unsigned char *codes, int lane) {
+    const int pw = (int)(unit % p.page_warps), h = (int)(unit / p.page_warps % p.Hkv);
+    const long long s = unit / p.page_warps / p.Hkv;
+    if (s >= p.S) return;
+    const Segment sg = load_segment(p.seq_info, (int)s);
+    if (segment_fault(sg, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window) || sg.ql == 0) return;
+    if (!new_pages_ok(p, sg, lane)) return;
+    unsigned char *scales = codes + kPage * p.D;
+    const int p1 = (sg.kend + kPage - 1) / kPage;
+    for (int pb = (sg.kend - sg.ql) / kPage + pw; pb < p1; pb += p.page_warps) {
+        if (p.D == 64) write_v4_page<64>(p, sg, h, pb, codes, scales, lane);
+        else if (p.D == 128) write_v4_page<128>(p, sg, h, pb, codes, scales, lane);
+        else write_v4_page<256>(p, sg, h, pb, codes, scales, lane);
+    }
+}
+// The errors of the refused segments (one CTA).
+__device__ __forceinline__ void report_segments(const RopeParams &p) {
+    for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
+        const unsigned f = segment_fault(load_segment(p.seq_info, s), p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
+        if (f) atomicOr(p.err, f);
+    }
+}
+
 template <typename T, int CACHE, int PAIR>
 __global__ void __launch_bounds__(kRopeWarps * 32, sizeof(T) == 2 ? 5 : 4) rope_kernel(const __grid_constant__ RopeParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -342,28 +505,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, sizeof(T) == 2 ? 5 : 4) rope_
     pdl_wait();
     pdl_trigger();
     if (CACHE == kFp4 && (int)blockIdx.x >= p.row_ctas) {
-        // V pages: units (segment, kv head, page warp), page warps fastest
-        const long long unit = (long long)(blockIdx.x - p.row_ctas) * kRopeWarps + warp;
-        const int pw = (int)(unit % p.page_warps), h = (int)(unit / p.page_warps % p.Hkv);
-        const long long s = unit / p.page_warps / p.Hkv;
-        if (s >= p.S) return;
-        const Segment sg = load_segment(p.seq_info, (int)s);
-        if (segment_fault(sg, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window) || sg.ql == 0) return;
-        if (!new_pages_ok(p, sg, lane)) return;
-        unsigned char *codes = smem + (size_t)warp * kPage * (p.D + p.D / 16), *scales = codes + kPage * p.D;
-        const int p1 = (sg.kend + kPage - 1) / kPage;
-        for (int pb = (sg.kend - sg.ql) / kPage + pw; pb < p1; pb += p.page_warps) {
-            if (p.D == 64) write_v4_page<64>(p, sg, h, pb, codes, scales, lane);
-            else if (p.D == 128) write_v4_page<128>(p, sg, h, pb, codes, scales, lane);
-            else write_v4_page<256>(p, sg, h, pb, codes, scales, lane);
-        }
+        write_v4_pages(p, (long long)(blockIdx.x - p.row_ctas) * kRopeWarps + warp, smem + (size_t)warp * kPage * (p.D + p.D / 16), lane);
         return;
     }
-    if (CACHE != kNoCache && blockIdx.x == 0)  // the refused segments
-        for (int s = threadIdx.x; s < p.S; s += blockDim.x) {
-            const unsigned f = segment_fault(load_segment(p.seq_info, s), p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
-            if (f) atomicOr(p.err, f);
-        }
+    if (CACHE != kNoCache && blockIdx.x == 0) report_segments(p);
     // Few rows: `slices` warps share a row's heads.  Many: a warp takes rows of
     // its own, one after the other, and looks their segment up once.
     const long long w = (long long)blockIdx.x * kRopeWarps + warp;
@@ -371,103 +516,25 @@ __global__ void __launch_bounds__(kRopeWarps * 32, sizeof(T) == 2 ? 5 : 4) rope_
     const long long warps = (long long)p.row_ctas * kRopeWarps / p.slices, wr = w / p.slices;
     if (wr >= warps) return;
     const int row0 = (int)(wr * p.rows / warps), row1 = (int)((wr + 1) * p.rows / warps);
-    const int per = 1 << p.lanes_log2, c = lane & (per - 1), half = p.rot_dim / 2, heads = 32 >> p.lanes_log2;
     float2 *angles = reinterpret_cast<float2 *>(smem) + warp * 128;                       // cosine and sine of each pair
     float *stage = reinterpret_cast<float *>(smem) + kRopeWarps * 256 + warp * 256;
-    int partner = lane;
-    if (PAIR == kByShuffle && c < half / 4) partner = lane + (c < half / 8 ? half / 8 : -(half / 8));  // the halves are whole lanes
-    const int left = p.rot_dim - c * 8;  // rotated columns from this lane's first on
-    const unsigned turned = left >= 8 ? 0xffu : left <= 0 ? 0u : (1u << left) - 1u;
-    // The row's groups of `heads` heads, q then k then v, cut evenly into the slices.
-    const int nq = p.q ? (p.Hq + heads - 1) / heads : 0, nk = p.k ? (p.Hkv + heads - 1) / heads : 0;
-    const int all = nq + nk + (CACHE == kSameType ? (p.Hkv + heads - 1) / heads : 0);
-    const int f0 = (int)((long long)all * slice / p.slices), f1 = (int)((long long)all * (slice + 1) / p.slices);
+    const RopeWork work = rope_work<CACHE, PAIR>(p, slice, p.slices, lane);
     Segment sg{0, 0, 0, 0};
     bool pages_ok = false;
 #pragma unroll 1
     for (int row = row0; row < row1; ++row) {
         RopeSlot slot{0, 0};
         long long place = 0;
-        if (CACHE != kNoCache) {
-            if (!(sg.q0 <= row && (long long)row < (long long)sg.q0 + sg.ql)) {
-                const int s = segment_of_row(p, row, lane);
-                if (s < 0) {
-                    sg.ql = 0;
-                    continue;
-                }
-                sg = load_segment(p.seq_info, s);
-                pages_ok = new_pages_ok(p, sg, lane);
-                if (!pages_ok && lane == 0) atomicOr(p.err, PKV_ERR_BLOCK);
-            }
-            if (!pages_ok) continue;
-            place = (long long)sg.kend - sg.ql + (row - sg.q0);
-            slot.block = p.block_table[(long long)sg.col * p.mbps + table_page((int)(place / kPage), p.ring_rows)];
-            slot.token = (int)(place % kPage);
-        }
-        if (p.rot_dim) {  // the row's angles, each once
+        if (CACHE != kNoCache && !place_row(p, row, sg, pages_ok, slot, place, lane)) continue;
+        if (p.rot_dim) {
+            __syncwarp();
             const unsigned pos = (unsigned)(p.positions ? p.positions[row] : (int)place);
-            __syncwarp();
-            for (int i = lane; i < half; i += 32) {
-                const unsigned long long turn = p.turns[i];
-                const unsigned f = pos * (unsigned)(turn >> 32) + __umulhi(pos, (unsigned)turn) -
-                                   ((int)pos < 0 ? (unsigned)turn : 0u);  // (pos mod 2^64) * turn, bits 32..63
-                float si, co;
-                sincospif((float)(int)f * 4.656612873077393e-10f, &si, &co);  // 2^-31: half turns in [-1, 1]
-                angles[i] = make_float2(co * p.mscale, si * p.mscale);
-            }
+            for (int i = lane; i < p.rot_dim / 2; i += 32) angles[i] = angle_of(pos, p.turns[i], p.mscale);
             __syncwarp();
         }
-        int first = 0;
-#pragma unroll 1
-        for (int kind = 0; kind < (CACHE == kSameType ? 3 : 2); ++kind) {  // q, k, v
-            const int H = kind == 0 ? p.Hq : p.Hkv, groups = kind == 0 ? nq : kind == 1 ? nk : all - nq - nk;
-            const int h0 = max(f0 - first, 0) * heads, h1 = min(max(f1 - first, 0) * heads, H);
-            first += groups;
-            if (groups == 0 || h0 >= h1) continue;
-            const T *src = reinterpret_cast<const T *>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
-                           row * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride);
-            T *dst = reinterpret_cast<T *>(kind == 0 ? p.q_out : kind == 1 ? p.k_out : p.v_out);
-            if (dst) dst += row * (kind == 0 ? p.q_out_stride : kind == 1 ? p.k_out_stride : p.v_out_stride);
-            unsigned char *pool = reinterpret_cast<unsigned char *>(kind == 0 ? nullptr : kind == 1 ? p.k_pool : p.v_pool);
-            const T *weight = reinterpret_cast<const T *>(kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr);
-            // this lane's columns: cosine and signed sine, then the head weights
-            const bool turn = kind < 2 && p.rot_dim > 0;
-            float ca[8], sb[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ca[e] = 1.f;
-                sb[e] = 0.f;
-            }
-            if (turn) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int d = c * 8 + e, i = PAIR == kInLane ? d / 2 : d < half ? d : d - half;
-                    if (turned >> e & 1u) {
-                        const float2 t = angles[i];
-                        ca[e] = t.x;
-                        sb[e] = (PAIR == kInLane ? e & 1 : d >= half) ? t.y : -t.y;
-                    }
-                }
-            }
-            if (weight && c * 8 < p.D) {
-                Raw8<T> r;
-                r.load(weight + c * 8);
-                float wt[8];
-                r.get(wt);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ca[e] *= wt[e];
-                    const int d = c * 8 + e, o = PAIR == kInLane ? d ^ 1 : d < half ? d + half : d - half;
-                    if (turned >> e & 1u) {  // the partner column's weight
-                        if constexpr (PAIR == kInLane) sb[e] *= wt[e ^ 1];
-                        else if constexpr (sizeof(T) == 2) sb[e] *= __bfloat162float(weight[o]);
-                        else sb[e] *= weight[o];
-                    }
-                }
-            }
-            rope_heads<T, CACHE, PAIR>(p, src, dst, pool, slot, h0, h1, ca, sb, weight != nullptr, turn, turned, partner,
-                                       stage, lane);
-        }
+        const T *const rows[3] = {reinterpret_cast<const T *>(p.q) + row * p.q_stride, reinterpret_cast<const T *>(p.k) + row * p.k_stride,
+                                  reinterpret_cast<const T *>(p.v) + row * p.v_stride};
+        rope_row<T, CACHE, PAIR>(p, row, slot, angles, rows, work, stage, lane);
     }
 }
 

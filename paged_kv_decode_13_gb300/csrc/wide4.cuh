@@ -44,7 +44,7 @@ struct Wide4 {
     static constexpr unsigned kQHalf = 128 * 128;
     static constexpr size_t kRawBytes = (size_t)PG * NR * kRaw;
     // registers a thread: at launch, of the softmax warps and of the others while the roles run
-    static constexpr int kRegs = 96, kRegsSoftmax = 136, kRegsOthers = 64;
+    static constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsOthers = 72;
     static constexpr int kBars = 2 * NK + 2 * NV + 3 * NB + 2 + 2 * NR, kPieces = 16;
     static constexpr size_t kSmem = 1024 + (size_t)(NK + NV) * kTile + 2 * kQHalf + kRawBytes + 6 * R * 4 + kBars * 8 + 256;
     static constexpr unsigned kColO = 64 * NB;                      // O_h at kColO + 128 h
@@ -63,24 +63,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// Two fp32 numbers in one 64-bit register: one instruction for both.
-__device__ __forceinline__ uint64_t f32x2(float a, float b) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};\n" : "=l"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ void f32x2_split(uint64_t d, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(d)); }
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // kind::f16 with fp16 A and B, fp32 D, both K-major.
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -128,10 +110,10 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
     __syncthreads();
     tc_fence_after();
     const unsigned tmem = *tslot, lane_off = (unsigned)(32 * quad) << 16;
+    depend4(p, false);
     Share4 share;
     share.find<C::kThreads>(p, R, reinterpret_cast<long long *>(sQm));
-    pdl_wait();
-    pdl_trigger();
+    depend4(p, true);
 
     // Bounded wait of a whole warp on one phase; false on a timeout, here or in
     // another role.

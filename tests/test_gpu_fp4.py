@@ -700,3 +700,41 @@ def test_shares_scales_and_magnitudes(pkv, q_heads):
     got, l2 = go(base, 0.0)
     for s, (_, _, col, kend) in enumerate(w.seq_info.tolist()):
         assert torch.allclose(l2[s], torch.full_like(l2[s], float(np.log(kend))), rtol=1e-5)
+
+
+# ---------------------------------------------------------------- appends of many rows
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rotate", [False, True])
+def test_append_many_rows(pkv, D, rotate):
+    lengths = [700, 300, 17, 900, 64, 333]
+    w = workloads.batched(S=6, max_len=1024, lengths=lengths, q_heads=4, kv_heads=2, head_dim=D, seed=1)
+    w.block_table[4, 1] = -3
+    rows = 2300
+    g = torch.Generator().manual_seed(3)
+    w.q, w.k_new, w.v_new = [[torch.randn(rows, h, D, generator=g).bfloat16()] for h in (4, 2, 2)]
+    good = [[1000, 700, 0, 700], [5, 299, 1, 300], [400, 10, 2, 17], [1701, 500, 3, 900]]
+    w.seq_info = torch.tensor(good + [[420, 40, 4, 64], [900, 50, 5, 40]], dtype=torch.int32)
+    f = Fp4(pkv, w)
+    q, kn, vn, err = w.q[0].cuda(), w.k_new[0].cuda(), w.v_new[0].cuda(), pkv.new_err_flags()
+    qo, ko, vo = torch.full_like(q, 9), torch.full_like(kn, 9), torch.full_like(vn, 9)
+    freq, m = pkv.rope_inv_freq(D)
+    rope = pkv.Rope(freq, device="cuda") if rotate else None
+    pkv.norm_rope_append(f.cache, 0, rope, q, kn, vn, w.seq_info.cuda(), qo, err, k_out=ko, v_out=vo)
+    assert int(err.item()) == 1 | 8
+    w.seq_info = torch.tensor(good, dtype=torch.int32)
+    live, k2 = torch.zeros(rows, dtype=torch.bool), kn.clone()
+    pos = torch.zeros(rows, dtype=torch.int32)
+    for q0, n, _, kend in good:
+        live[q0:q0 + n] = True
+        pos[q0:q0 + n] = torch.arange(kend - n, kend, dtype=torch.int32)
+    q2 = q.clone()
+    if rotate:
+        pkv.norm_rope(rope, q2, k2, pos.cuda())
+    want, e = f.oracle_bytes(k2.cpu(), w.v_new[0])
+    assert e == 0
+    for i in (0, 1):
+        assert f.host(i).tobytes() == want[i].tobytes(), "KV"[i]
+    for got, x in ((qo, q2), (ko, torch.from_numpy(R.values(*R.quantise(U.f64(k2)))).bfloat16().cuda()),
+                   (vo, torch.from_numpy(R.values(*R.quantise(U.f64(vn)))).bfloat16().cuda())):
+        assert torch.equal(got[live.cuda()], x[live.cuda()]) and (got[~live.cuda()] == 9).all()

@@ -255,3 +255,45 @@ def test_many_rows_and_unsorted_segments(pkv):
     assert err == 0
     pos, live = cache_positions(w)
     check_append(w, cache, qo, ko, vo, wq, wk, True, freq, pos, 1.0, False, live)
+
+
+# ---------------------------------------------------------------- many rows: through shared memory
+
+@pytest.mark.parametrize("dtype,D,rot,interleaved,hq,hkv", [
+    (torch.bfloat16, 128, 128, False, 8, 2), (torch.bfloat16, 128, 64, True, 7, 3), (torch.bfloat16, 72, 24, False, 5, 1),
+    (torch.float32, 64, 64, False, 4, 2), (torch.float32, 80, 18, False, 3, 1), (torch.bfloat16, 256, 256, False, 64, 8),
+])
+@pytest.mark.parametrize("norm", [False, True])
+def test_many_rows(pkv, dtype, D, rot, interleaved, hq, hkv, norm):
+    rows = 1501
+    g = torch.Generator().manual_seed(rows + D)
+    q, k, v, wq, wk = make(D, rows, hq, hkv, D, dtype)
+    freq, m = pkv.rope_inv_freq(rot, scaling="yarn", factor=4.0, trained_len=512)
+    rope = pkv.Rope(freq, interleaved, mscale=m, q_weight=wq if norm else None, k_weight=wk if norm else None, eps=1e-6, device="cuda")
+    pos = torch.randint(0, 1 << 20, (rows,), generator=g, dtype=torch.int32)
+    qo, ko = torch.empty_like(q), torch.empty_like(k)
+    pkv.norm_rope(rope, q, k, pos.cuda(), qo, ko)
+    check_rows(qo, q, wq if norm else None, 1e-6, freq, pos.numpy(), m, interleaved, dtype)
+    check_rows(ko, k, wk if norm else None, 1e-6, freq, pos.numpy(), m, interleaved, dtype)
+    pkv.norm_rope(rope, q, k, pos.cuda())       # in place, through the stages
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+
+
+@pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 128), (torch.float32, 64)])
+def test_many_rows_append(pkv, dtype, D):
+    """Ragged prompts with gaps, a refused segment and a bad page among them."""
+    lengths = [700, 300, 17, 900, 64, 333]
+    w = workloads.batched(S=6, max_len=1024, lengths=lengths, q_heads=6, kv_heads=2, head_dim=D, dtype=dtype, seed=1)
+    w.block_table[4, 1] = -3
+    rows = 2300
+    g = torch.Generator().manual_seed(3)
+    w.q, w.k_new, w.v_new = [[torch.randn(rows, h, D, generator=g).to(dtype)] for h in (6, 2, 2)]
+    w.seq_info = torch.tensor([[1000, 700, 0, 700], [5, 299, 1, 300], [400, 10, 2, 17], [1701, 500, 3, 900], [420, 40, 4, 64], [900, 50, 5, 40]],
+                              dtype=torch.int32)
+    freq, m = pkv.rope_inv_freq(D)
+    _, cache, qo, ko, vo, err, wq, wk = run_append(pkv, w, {}, freq, True)
+    assert err == 1 | 8
+    w.seq_info = w.seq_info[:4]
+    pos, live = cache_positions(w)
+    assert (qo[~live] == 9).all() and (ko[~live] == 9).all() and (vo[~live] == 9).all()
+    check_append(w, cache, qo, ko, vo, wq, wk, True, freq, pos, 1.0, False, live)
