@@ -460,12 +460,18 @@ __device__ __forceinline__ void write_v4_page(const RopeParams &p, const Segment
             uint4 w = make_uint4(__byte_perm(x.x, y.x, 0x5140), __byte_perm(x.x, y.x, 0x7362),
                                  __byte_perm(x.y, y.y, 0x5140), __byte_perm(x.y, y.y, 0x7362));
             uint4 *d = reinterpret_cast<uint4 *>(out + pl * 512 + lane * 16);
-            if (mask != 0xffffffffu) {
-                const uint4 o = *d;
-                w = make_uint4((w.x & mask) | (o.x & ~mask), (w.y & mask) | (o.y & ~mask), (w.z & mask) | (o.z & ~mask),
-                               (w.w & mask) | (o.w & ~mask));
+            if (mask == 0xffffffffu) {
+                *d = w;
+            } else {
+                // Other tokens of the page may be written at the same time (a
+                // ring's last page is its first one too, another segment goes
+                // on in the page): flip just the bits of these tokens that change.
+                const uint4 o = __ldcg(d);
+                atomicXor(&d->x, (w.x ^ o.x) & mask);
+                atomicXor(&d->y, (w.y ^ o.y) & mask);
+                atomicXor(&d->z, (w.z ^ o.z) & mask);
+                atomicXor(&d->w, (w.w ^ o.w) & mask);
             }
-            *d = w;
         }
     }
     for (int i = lane; i < (b - a) * (D / 16); i += 32) {

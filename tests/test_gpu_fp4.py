@@ -738,3 +738,62 @@ def test_append_many_rows(pkv, D, rotate):
     for got, x in ((qo, q2), (ko, torch.from_numpy(R.values(*R.quantise(U.f64(k2)))).bfloat16().cuda()),
                    (vo, torch.from_numpy(R.values(*R.quantise(U.f64(vn)))).bfloat16().cuda())):
         assert torch.equal(got[live.cuda()], x[live.cuda()]) and (got[~live.cuda()] == 9).all()
+
+
+# ---------------------------------------------------------------- appends that meet in a page
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kend", [1000, 1003, 77, 128])
+def test_append_a_whole_ring(pkv, D, kend):
+    """As many rows as the ring holds: its last new page is also its first one, cut between two tokens of a byte."""
+    w = workloads.long_context(S=1, kv_len=kend, window=1, ring_rows=64, q_heads=3, kv_heads=3, head_dim=D)
+    g = torch.Generator().manual_seed(kend)
+    w.q, w.k_new, w.v_new = [[torch.randn(64, 3, D, generator=g).bfloat16()] for _ in range(3)]
+    w.seq_info, w.window = torch.tensor([[0, 64, 0, kend]], dtype=torch.int32), 1
+    want = None
+    for _ in range(5):
+        f, err = Fp4(pkv, w), pkv.new_err_flags()
+        pkv.append(f.cache, 0, w.k_new[0].cuda(), w.v_new[0].cuda(), w.seq_info.cuda(), err, window=1)
+        if want is None:
+            want, e = f.oracle_bytes(w.k_new[0], w.v_new[0])
+        assert e == 0 and int(err.item()) == 0
+        for i in (0, 1):
+            assert f.host(i).tobytes() == want[i].tobytes(), "KV"[i]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_segments_that_share_a_page(pkv, D):
+    """Consecutive pieces of one sequence in one call, and tails of two sequences in a shared page."""
+    w = workloads.batched(S=2, max_len=64, lengths=[64, 64], q_heads=2, kv_heads=2, head_dim=D)
+    g = torch.Generator().manual_seed(D)
+    w.q, w.k_new, w.v_new = [[torch.randn(40, 2, D, generator=g).bfloat16()] for _ in range(3)]
+    w.block_table[1, 0] = w.block_table[0, 3]
+    w.seq_info = torch.tensor([[0, 7, 0, 20], [7, 1, 0, 21], [8, 2, 0, 23], [10, 20, 0, 43], [30, 5, 1, 5], [35, 5, 0, 58]], dtype=torch.int32)
+    for _ in range(5):
+        f, err = Fp4(pkv, w), pkv.new_err_flags()
+        pkv.append(f.cache, 0, w.k_new[0].cuda(), w.v_new[0].cuda(), w.seq_info.cuda(), err)
+        want, e = f.oracle_bytes(w.k_new[0], w.v_new[0])
+        assert e == 0 and int(err.item()) == 0
+        for i in (0, 1):
+            assert f.host(i).tobytes() == want[i].tobytes(), "KV"[i]
+
+
+def test_shares_on_a_given_stream(pkv):
+    """stream= takes the call and its workspace to that stream: nothing on the current one is disturbed."""
+    w = workloads.batched(S=4, max_len=4000, seed=3, q_heads=16, kv_heads=4)
+    f = Fp4(pkv, w)
+    q, si, err = w.q[0].cuda(), w.seq_info.cuda(), pkv.new_err_flags()
+    want, want_lse, _ = attend(pkv, f, max_kv=BIG)
+    n = pkv.attend_workspace_bytes(f.cache, 16, 4, 1, BIG)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    bufs = []
+    for i in range(20):
+        out, lse = torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:2], device="cuda")
+        st.wait_stream(torch.cuda.current_stream())
+        pkv.attend_varlen(f.cache, 0, q, si, out, err, 1, BIG, w.scale, lse=lse, stream=st)
+        bufs.append((out, lse, torch.full((n,), i, dtype=torch.uint8, device="cuda")))   # the current stream's own use of such a block
+    torch.cuda.synchronize()
+    for i, (out, lse, b) in enumerate(bufs):
+        assert torch.equal(out, want) and torch.equal(lse, want_lse) and bool((b == i).all())
+    assert int(err.item()) == 0
