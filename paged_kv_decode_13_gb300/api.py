@@ -350,10 +350,10 @@ def _fp4_workspace(cache, hq, segments, max_q_len, max_kv, window, flags, stream
     n = attend_workspace_bytes(cache, hq, segments, max_q_len, max_kv, 0, flags)
     if n <= 0:
         return None
-    ws = torch.empty(n, dtype=torch.uint8, device=cache.k[0].device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=cache.k[0].device)
+    with torch.cuda.stream(stream):  # the allocator orders a block's users by the stream it was taken on
+        return torch.empty(n, dtype=torch.uint8, device=cache.k[0].device)
 
 
 def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max_q_len, max_kv, scale, causal,
@@ -362,6 +362,11 @@ def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max
     max_q_len, max_kv, window = int(max_q_len), int(max_kv), int(window)
     if out.dtype is torch.bfloat16:
         flags |= _lib.FLAG_OUT_BF16
+    dev = cache._device
+    if dev >= 0 and dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max_q_len, max_kv, scale, causal,
+                           window, num_splits, flags, stream, workspace)
     if cache._fp4 and workspace is None and num_splits == 0:
         workspace = _fp4_workspace(cache, shape[1], segments, max_q_len, max_kv, window, flags, stream)
     new = ()

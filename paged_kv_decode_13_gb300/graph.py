@@ -13,12 +13,13 @@ per runner grew device memory without bound in the page's measurement.
 from __future__ import annotations
 
 import math
-from typing import Dict, List, Optional, Tuple
+from typing import Dict, List, Optional, Sequence, Tuple, Union
 
 import torch
 
 from . import _lib
-from .api import PagedKVCache, append, append_attend, attend_varlen, new_err_flags, new_workspace
+from .api import (PagedKVCache, Rope, append, append_attend, attend_varlen, new_err_flags, new_workspace,
+                  norm_rope_append)
 from .api import advance as advance_lengths
 
 _SHARED_POOL = None
@@ -57,13 +58,22 @@ class DecodeStep:
     leaves the segment table ready for the next step and the host writes it
     only once: per step it copies q, k_new and v_new (`step_inputs`) and
     keeps its own copy of the lengths in step (advance_host).
+
+    rope (a Rope for every layer, or one per layer) makes q and k_new the rows
+    as the projections give them: each layer is then norm_rope_append, which
+    leaves the turned queries in `q_rot`, and the attention over them, two
+    launches (fused does not apply).  The angles are those of the rows'
+    positions in the cache.  A cache held in 4 bits takes two launches a layer
+    as well, three where large bounds share the key ranges; its outputs may be
+    bf16 (out_dtype).
     """
 
     def __init__(self, cache: PagedKVCache, num_q_heads: int, rows: int = 1, num_segments: int = 1,
                  max_q_len: int = 1, max_kv: Optional[int] = None, scale: Optional[float] = None,
                  causal: bool = False, window: int = 0, fused: bool = True, pdl: bool = True,
                  flags: int = 0, num_splits: int = 0, with_lse: bool = False, prefetch_next: bool = True,
-                 workspace: bool = False, advance: bool = False):
+                 workspace: bool = False, advance: bool = False,
+                 rope: Union[Rope, Sequence[Rope], None] = None, out_dtype: torch.dtype = torch.float32):
         dev = cache.k[0].device
         L, Hkv, D = cache.num_layers, cache.kv_heads, cache.head_dim
         self.cache = cache
@@ -74,7 +84,13 @@ class DecodeStep:
         self.causal, self.window = causal, window
         self.fused, self.pdl, self.flags, self.num_splits = fused, pdl, flags, num_splits
         self.prefetch_next = prefetch_next
-        spec_in = ([((rows, num_q_heads, D), cache.dtype)] * L + [((rows, Hkv, D), cache.dtype)] * (2 * L)
+        if out_dtype != torch.float32 and not (out_dtype == torch.bfloat16 and cache.dtype == torch.uint8):
+            raise ValueError("out_dtype is float32, or bfloat16 over a 4-bit cache")
+        self.rope = None if rope is None else [rope] * L if isinstance(rope, Rope) else list(rope)
+        if self.rope is not None and len(self.rope) != L:
+            raise ValueError("rope needs one entry per layer")
+        row = cache.row_dtype
+        spec_in = ([((rows, num_q_heads, D), row)] * L + [((rows, Hkv, D), row)] * (2 * L)
                    + [((num_segments, 4), torch.int32)])
         self.inputs, views = _carve(spec_in, dev)
         self.q, self.k_new, self.v_new = views[:L], views[L:2 * L], views[2 * L:3 * L]
@@ -83,7 +99,8 @@ class DecodeStep:
         # segment table sits after it
         self.step_inputs = self.inputs[:self.seq_info.data_ptr() - self.inputs.data_ptr()]
         self.advance = advance
-        spec_out = [((rows, num_q_heads, D), torch.float32)] * L
+        self.q_rot = None if self.rope is None else [torch.zeros(rows, num_q_heads, D, dtype=row, device=dev) for _ in range(L)]
+        spec_out = [((rows, num_q_heads, D), out_dtype)] * L
         if with_lse:
             spec_out += [((rows, num_q_heads), torch.float32)] * L
         self.outputs, views = _carve(spec_out, dev)
@@ -102,7 +119,9 @@ class DecodeStep:
                                     self.max_kv, self.num_splits, self.flags)
 
     def launch_count(self) -> int:
-        return self.cache.num_layers * (1 if self.fused else 2) + (1 if self.advance else 0)
+        """Kernels of one run (a 4-bit cache's merge launches, which its bounds decide, not counted)."""
+        one = self.fused and self.rope is None and self.cache.dtype != torch.uint8
+        return self.cache.num_layers * (1 if one else 2) + (1 if self.advance else 0)
 
     def run(self, stream=None, advance: Optional[bool] = None) -> None:
         """Enqueue every layer's append + attention on the current stream,
@@ -115,7 +134,15 @@ class DecodeStep:
                 flags |= _lib.FLAG_PDL
             if self.prefetch_next and layer + 1 < c.num_layers:
                 flags |= _lib.FLAG_PREFETCH_NEXT  # the next call attends layer + 1 over the same segments
-            if self.fused:
+            if self.rope is not None:
+                norm_rope_append(c, layer, self.rope[layer], self.q[layer], self.k_new[layer], self.v_new[layer],
+                                 self.seq_info, self.q_rot[layer], self.err, window=self.window, stream=stream)
+                # the kernel before it writes only this step's slots and q_rot: an early start is safe
+                attend_varlen(c, layer, self.q_rot[layer], self.seq_info, self.out[layer], self.err, self.max_q_len,
+                              self.max_kv, self.scale, self.causal, self.window, lse=self.lse[layer],
+                              num_splits=self.num_splits, flags=flags | (_lib.FLAG_PDL if self.pdl else 0),
+                              stream=stream, workspace=self.ws)
+            elif self.fused:
                 append_attend(c, layer, self.q[layer], self.k_new[layer], self.v_new[layer], self.seq_info,
                               self.out[layer], self.err, self.max_q_len, self.max_kv, self.scale, self.causal,
                               self.window, lse=self.lse[layer], num_splits=self.num_splits, flags=flags,
