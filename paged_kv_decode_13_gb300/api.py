@@ -334,7 +334,7 @@ def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Te
 
 # Bounds (segments x kv heads x row tiles x keys) from which a launch over a 4-bit cache
 # may use a workspace; pkv_attend_workspace_bytes decides.
-_FP4_WORKSPACE_FROM = 16 * 6144
+_FP4_WORKSPACE_FROM = 1 << 18
 
 
 def _fp4_workspace(cache, hq, segments, max_q_len, max_kv, window, flags, stream):

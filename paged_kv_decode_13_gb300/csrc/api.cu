@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <mutex>
 
 #include <math.h>
@@ -361,24 +362,26 @@ int encode_pool_pages(CUtensorMap *map, const void *pool, const pkv_cache *c) {
 
 struct Plan4 {
     Attend4Kernel k4;
-    AttnKernel k;  // the same kernel for the shared cluster queries
     int G, row_tiles, ncta;
-    long long units;
+    long long units, pages;  // ranges, and the pages of the longest
     Attend4Kernel ks;  // the kernel of equal shares
     int shares;        // its CTAs, 0: not for these bounds
 };
 
-// Equal shares cost a second launch (about 3 us) and balance the SMs: worth
-// it from about this many 16-token pages of one kv head on (about 8 us of
-// reading at head_dim 128; one sequence of 8192 keys and 8 heads, 4096 pages, is
-// faster in clusters).  Every CTA sums the segment table's pages, so the
-// table has to be short; long ones have ranges enough for one CTA each.
-constexpr long long kSharesFrom = 6144;
+// Equal shares are taken up to this many percent above what the clusters cost at equal
+// lengths: they balance lengths that differ, which the bounds do not tell.
+// (16 ranges' worth, 8 kv heads, head_dim 128: of 8192 keys each 42 us in shares
+// against 35, of random lengths up to that 32 against 32; up to 16384 65
+// against 60 and 37 against 47; one sequence of 131072 keys 42 against 59.)
+// Every CTA sums the segment table's pages, so the table has to be short.
+constexpr int kSharesEdge = 15;
 constexpr int kSharesSegments = 512;
 constexpr int kSharesTiles = 16;  // each tile's range is taken as long as its segment's: not for long causal chunks
 constexpr int kPieceWide = 36;  // the same for the tcgen05 kernel, in pages
-// Rows a kv head from which the tcgen05 kernel (tiles of 128) is faster than mma.sync tiles of 32.
-constexpr int kWideFrom = 17;
+// Rows a kv head from which the tcgen05 kernel (tiles of 128) is faster than mma.sync tiles
+// of 32: as shares of 8 sequences of 4096 keys and 8 heads, 32 rows 43 us
+// against 34, 36 rows 43 against 51, 128 rows 51 against 89.
+constexpr int kWideFrom = 33;
 constexpr int kPieceBytes = 56 << 10;  // what a piece costs, as bytes that one CTA reads meanwhile
 
 // Whether the kernel was compiled to the register count its warps hand around
@@ -399,6 +402,110 @@ bool regs_ok(const Attend4Kernel &k) {
         fn = k.balance;
     }
     return ok;
+}
+
+Attend4Kernel pick4_rows(int head_dim, int rows, bool few) {
+    return head_dim == 64 ? pick4_64(rows, few) : head_dim == 128 ? pick4_128(rows, few) : pick4_256(rows, few);
+}
+
+// Clusters of n CTAs that the device holds at once with at most l of the
+// kernel's CTAs an SM: held[l][n], l up to the CTAs that fit.  Asked once a
+// kernel (with more shared memory for the smaller l).
+struct Fit4 {
+    const void *fn;
+    int held[5][kMaxCluster + 1];
+};
+const Fit4 &fit4(const Attend4Kernel &k) {
+    static std::mutex mu;
+    static Fit4 known[16];  // eleven kernels
+    static int n = 0;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < n; ++i)
+        if (known[i].fn == k.fn) return known[i];
+    Fit4 &f = known[n < 15 ? n++ : 15];
+    f.fn = k.fn;
+    const bool asks = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) == cudaSuccess &&
+                      cudaFuncSetAttribute(k.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    for (int l = 1; l <= k.ctas; ++l)
+        for (int c = 1; c <= kMaxCluster; ++c) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)c, 1, 1);
+            cfg.blockDim = dim3((unsigned)k.threads);
+            cfg.dynamicSmemBytes = l == k.ctas ? k.smem : std::max<size_t>(k.smem, 233472 / (l + 1));
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = (unsigned)c;
+            attr.val.clusterDim.y = 1;
+            attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if (!asks || cudaOccupancyMaxActiveClusters(&f.held[l][c], k.fn, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                f.held[l][c] = l * kDefaultSms / c;  // no device answers
+            }
+        }
+    return f;
+}
+
+// What a launch of `units` clusters of n CTAs over `pages` pages each takes
+// besides a constant, in ns.  Measured over 1 to 256 ranges of 256 to 16384
+// keys at every head_dim and row class: CTAs that share an SM slow each other
+// (kSlow, in 1 / 20, by the CTAs an SM may hold and holds), each adds about 0.6 us to
+// the launch, a further wave 5 us, and the merge of a cluster 1 us.  Clusters
+// start only where a GPC has room for all their CTAs, so the CTAs an SM gets come
+// from the occupancy of clusters (32 ranges of 8192 keys: 8 CTAs each, two an SM at
+// most, 14.8 us; 9, three an SM, 19.5; 48 ranges: 11 each 18.7 us, 12, a
+// second wave, 27.4; 96: 6 each 27.4, 7 each 40.6).  Large clusters, and kernels of
+// one or two CTAs an SM, need some room to spare (16 ranges, 32 rows, 8192 keys:
+// 12 CTAs each, 23 clusters fit, 24.3 us; 13, 19 fit, 32.5).
+// few: the kernel with eight warps, for ranges that leave it alone on its SM: it is
+// through a page sooner, and its merge takes longer (one range of 256 keys
+// 5.3 us against 5.9, of 4096 7.4 against 6.9, of 8192 7.5 against 8.7).
+constexpr int kSlow[5][5] = {{0}, {0, 20}, {0, 20, 27}, {0, 20, 32, 33}, {0, 20, 28, 42, 42}};
+long long cost4(const Attend4Kernel &k, const Fit4 &f, bool few, long long units, long long pages, int n) {
+    const int held = f.held[k.ctas][n];
+    if (held <= 0) return LLONG_MAX;
+    const long long time = (pages + n - 1) / n * k.page_ns;
+    const long long room = n >= 12 ? units + units / 4 : n >= 8 || (n >= 3 && k.ctas <= 2) ? units + units / 16 : units;
+    int l = 1;
+    while (l < k.ctas && f.held[l][n] < room) ++l;
+    const long long waves = held >= room ? 1 : std::max<long long>(2, (units + units / 8 + held - 1) / held);
+    if (few) {
+        if (l > 1 || waves > 1) return LLONG_MAX;
+        return n == 1 ? time - 1100 : std::max<long long>(time - 100, 1700);
+    }
+    return waves * kSlow[k.ctas][l] * time / 20 + 600 * (l - 1) + 5000 * (waves - 1) - (n == 1 ? 1000 : 0);
+}
+
+// CTAs of a range (num_splits, or the cheapest number), their kernel and the cost.
+long long split4(Attend4Kernel *k4, int head_dim, int rows, long long units, long long pages, int num_splits, int *ncta) {
+    long long best = LLONG_MAX;
+    const Attend4Kernel cand[2] = {*k4, pick4_rows(head_dim, rows, true)};
+    *ncta = 1;
+    for (int few = 0; few < (cand[1].fn == cand[0].fn ? 1 : 2); ++few) {
+        const Attend4Kernel &k = cand[few];
+        const Fit4 &f = fit4(k);
+        // no more CTAs than leave each of its warps four pages
+        const int top = (int)std::max<long long>(1, std::min<long long>(kMaxCluster, pages / (4 * k.warps)));
+        for (int n = num_splits ? num_splits : 1; n <= (num_splits ? num_splits : top); ++n) {
+            const long long cost = cost4(k, f, few, units, pages, n);
+            if (cost < best) {
+                best = cost;
+                *k4 = k;
+                *ncta = n;
+            }
+        }
+    }
+    return best;
+}
+
+// The same of equal shares: `units` ranges (by this kernel's row tiles) of `pages`
+// pages each, read by all SMs at 1.1 times what full SMs take.  The second launch, the
+// scan of the segment table and the merge cost 10 us (the tcgen05 kernel: 14.5),
+// a range about 8 ns (35).
+long long cost4_shares(const Attend4Kernel &k, long long units, long long pages) {
+    const bool wide = k.rows == 128;
+    return (wide ? 14500 : 10000) + units * (wide ? 35 : 8) + units * pages * k.page_ns * kSlow[k.ctas][k.ctas] * 11 / (200LL * k.ctas * device_sms());
 }
 
 struct Ws4Layout {
@@ -422,35 +529,20 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     pl->G = Hq / c->kv_heads;
     const long long rows = (long long)pl->G * max_q_len;
     if (rows > (1 << 20)) return PKV_EINVAL;
-    auto pick4 = [&](bool few) {
-        return c->head_dim == 64 ? pick4_64((int)rows, few) : c->head_dim == 128 ? pick4_128((int)rows, few) : pick4_256((int)rows, few);
-    };
-    pl->k4 = pick4(false);
-    const Attend4Kernel small = pl->k4;  // of equal shares
-    // Few ranges: CTAs of eight warps, each with fewer pages to wait for.
-    if ((long long)std::max(S, 1) * c->kv_heads * 8 <= device_sms()) pl->k4 = pick4(true);
-    pl->k = AttnKernel{pl->k4.fn, pl->k4.threads, pl->k4.smem, pl->k4.rows, c->head_dim, true, false};
+    pl->k4 = pick4_rows(c->head_dim, (int)rows, false);
     pl->row_tiles = (int)((rows + pl->k4.rows - 1) / pl->k4.rows);
     if ((long long)c->kv_heads * pl->row_tiles > 65535) return PKV_EINVAL;
     pl->units = (long long)std::max(S, 1) * c->kv_heads * pl->row_tiles;
-    const long long max_pages = (max_kv + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE + 1;
-    long long n = num_splits;
-    if (n == 0) {
-        const long long want = ((long long)kTargetWaves * device_sms() * pl->k4.ctas + pl->units - 1) / pl->units;
-        n = 1;
-        while (n < want && n < kMaxCluster) n *= 2;
-        // no more CTAs than leave each warp a few pages
-        while (n > 1 && n * pl->k4.warps * 2 > max_pages) n /= 2;
-    }
-    pl->ncta = (int)std::max<long long>(1, std::min<long long>(n, max_pages));
+    const long long keys = window > 0 ? std::min<long long>(max_kv, (long long)window + max_q_len) : max_kv;
+    pl->pages = (keys + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE;
     pl->shares = 0;
+    pl->ks = pl->k4;
+    const long long cost = split4(&pl->k4, c->head_dim, (int)rows, pl->units, pl->pages, num_splits, &pl->ncta);
     if (num_splits == 0 && S > 0 && S <= kSharesSegments) {
-        pl->ks = small;
         if (c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide())) pl->ks = pick4_wide();
         const long long tiles = (rows + pl->ks.rows - 1) / pl->ks.rows;
-        const long long keys = window > 0 ? std::min<long long>(max_kv, (long long)window + max_q_len) : max_kv;
-        const long long pages = (long long)S * c->kv_heads * tiles * ((keys + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE);
-        if (tiles <= kSharesTiles && pages >= (pl->ks.rows == 8 ? kSharesFrom : pl->ks.rows == 128 ? kSharesFrom / 6 : kSharesFrom / 2))
+        const long long shares = cost4_shares(pl->ks, (long long)S * c->kv_heads * tiles, pl->pages);
+        if (tiles <= kSharesTiles && shares < cost + cost * kSharesEdge / 100)
             pl->shares = std::min(device_sms() * pl->ks.ctas, kMerge4Slots);
     }
     return PKV_OK;
@@ -473,10 +565,11 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     const Ws4Layout wl = ws4_layout(pl.shares, pl.ks.rows, c->head_dim);
     if (shares && workspace_bytes < (long long)wl.total) return PKV_EINVAL;
     if (check_only) return PKV_OK;
-    if (shares) pl.k = AttnKernel{pl.ks.balance, pl.ks.threads, pl.ks.smem, pl.ks.rows, c->head_dim, true, pl.ks.rows == 128};
-    if ((st = prepare_kernel(pl.k))) return st;
-    int ncta = S == 0 || shares ? 1 : schedulable_cluster(pl.k, pl.ncta);
-    if (S > 0 && !shares && num_splits == 0) ncta = wave_cluster(pl.k, pl.units, ncta);
+    const Attend4Kernel &k4 = shares ? pl.ks : pl.k4;
+    const void *fn = shares ? k4.balance : k4.fn;
+    const AttnKernel prep{fn, k4.threads, k4.smem, k4.rows, c->head_dim, true, shares && k4.rows == 128};
+    if ((st = prepare_kernel(prep))) return st;
+    const int ncta = S == 0 || shares ? 1 : schedulable_cluster(prep, pl.ncta);
     Attend4Params p;
     p.k = reinterpret_cast<const unsigned char *>(c->k[layer]);
     p.v = reinterpret_cast<const unsigned char *>(c->v[layer]);
@@ -498,7 +591,7 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     p.ring_rows = c->ring_rows;
     p.max_q_len = max_q_len;
     p.row_tiles = pl.row_tiles;
-    p.min_pages = 4 * (shares ? pl.ks.warps : pl.k4.warps);  // four a warp
+    p.min_pages = 4 * k4.warps;  // four a warp
     p.causal = causal;
     p.window = window;
     p.out_bf16 = (flags & PKV_FLAG_OUT_BF16) ? 1 : 0;
@@ -517,8 +610,8 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = S == 0 ? dim3(1, 1, 1) : dim3((unsigned)ncta, (unsigned)(c->kv_heads * pl.row_tiles), (unsigned)S);
     if (shares) cfg.gridDim = dim3((unsigned)pl.shares, 1, 1);
-    cfg.blockDim = dim3((unsigned)pl.k.threads);
-    cfg.dynamicSmemBytes = pl.k.smem;
+    cfg.blockDim = dim3((unsigned)k4.threads);
+    cfg.dynamicSmemBytes = k4.smem;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     int na = 0;
@@ -537,7 +630,7 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     cfg.attrs = na ? attr : nullptr;
     cfg.numAttrs = (unsigned)na;
     void *args[] = {&p};
-    if ((st = launch_status(cudaLaunchKernelExC(&cfg, pl.k.fn, args))) || !shares) return st;
+    if ((st = launch_status(cudaLaunchKernelExC(&cfg, fn, args))) || !shares) return st;
     cudaLaunchConfig_t mc = {};
     const int merge_rows = pl.ks.rows == 8 ? 1 : kMerge4Threads / 32;  // a CTA's
     mc.gridDim = dim3((unsigned)pl.shares, (unsigned)((std::min(pl.ks.rows, pl.G * max_q_len) + merge_rows - 1) / merge_rows), 1);

@@ -797,3 +797,45 @@ def test_shares_on_a_given_stream(pkv):
     for i, (out, lse, b) in enumerate(bufs):
         assert torch.equal(out, want) and torch.equal(lse, want_lse) and bool((b == i).all())
     assert int(err.item()) == 0
+
+
+# ---------------------------------------------------------------- equal shares with a window: the window bounds the work, so many (empty) segments
+
+def with_empty_segments(w, n):
+    w.seq_info = torch.cat([w.seq_info, torch.zeros(n - w.num_segments, 4, dtype=torch.int32)])
+    return w
+
+
+def attend_in_shares(pkv, f, max_q, window):
+    """Attention with a workspace, which must have been used."""
+    w = f.w
+    n = pkv.attend_workspace_bytes(f.cache, w.q_heads, w.num_segments, max_q, BIG)
+    assert n > 0
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse, err = torch.empty(w.q[0].shape, device="cuda"), torch.empty(w.q[0].shape[:2], device="cuda"), pkv.new_err_flags()
+    pkv.attend_varlen(f.cache, 0, w.q[0].cuda(), w.seq_info.cuda(), out, err, max_q, BIG, w.scale, w.causal, window, lse=lse, workspace=ws)
+    assert int(err.item()) == 0 and not bool((ws == 0xA5).all()), "not run as shares"
+    return out, lse
+
+
+@pytest.mark.parametrize("q_heads,max_q", [(8, 1), (16, 4), (32, 4), (64, 9)])
+@pytest.mark.parametrize("window", [300, 700])
+@pytest.mark.parametrize("padded", [False, True])
+def test_shares_with_windows(pkv, q_heads, max_q, window, padded):
+    w = workloads.spec_verify(S=7, max_q=max_q, len_lo=max_q, len_hi=2000, seed=q_heads + window, q_heads=q_heads, kv_heads=8)
+    ends = w.seq_info[:, 3].tolist()
+    fv = np.array([0, 17, ends[2] - 1, ends[3] + 5, max(ends[4] - 5, 0), 3, 0], np.int32) if padded else None
+    f = Fp4(pkv, w, first_valid=fv)
+    with_empty_segments(w, 500)
+    out, lse = attend_in_shares(pkv, f, max_q, window)
+    check(f, out, lse, window=window)
+
+
+@pytest.mark.parametrize("D,window,ring,kv", [(128, 700, 720, 5000), (64, 700, 704, 3000), (256, 512, 512, 3001)])
+@pytest.mark.parametrize("q_heads", [8, 288])
+def test_shares_with_rings(pkv, D, window, ring, kv, q_heads):
+    w = workloads.long_context(S=3, kv_len=kv, window=window, ring_rows=ring, q_heads=q_heads, kv_heads=8, head_dim=D)
+    f = Fp4(pkv, w, garbage=False, first_valid=np.array([0, kv - 100, kv + 5], np.int32))
+    with_empty_segments(w, 500)
+    out, lse = attend_in_shares(pkv, f, 1, window)
+    check(f, out, lse, window=window)
