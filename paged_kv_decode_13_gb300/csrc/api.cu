@@ -450,7 +450,7 @@ const Fit4 &fit4(const Attend4Kernel &k) {
 // What a launch of `units` clusters of n CTAs over `pages` pages each takes
 // besides a constant, in ns.  Measured over 1 to 256 ranges of 256 to 16384
 // keys at every head_dim and row class: CTAs that share an SM slow each other
-// (kSlow, in 1 / 20, by the CTAs an SM may hold and holds), each adds about 0.6 us to
+// (k.full; two where four fit by 3 / 8 of that), each adds about 0.6 us to
 // the launch, a further wave 5 us, and the merge of a cluster 1 us.  Clusters
 // start only where a GPC has room for all their CTAs, so the CTAs an SM gets come
 // from the occupancy of clusters (32 ranges of 8192 keys: 8 CTAs each, two an SM at
@@ -461,7 +461,6 @@ const Fit4 &fit4(const Attend4Kernel &k) {
 // few: the kernel with eight warps, for ranges that leave it alone on its SM: it is
 // through a page sooner, and its merge takes longer (one range of 256 keys
 // 5.3 us against 5.9, of 4096 7.4 against 6.9, of 8192 7.5 against 8.7).
-constexpr int kSlow[5][5] = {{0}, {0, 20}, {0, 20, 27}, {0, 20, 32, 33}, {0, 20, 28, 42, 42}};
 long long cost4(const Attend4Kernel &k, const Fit4 &f, bool few, long long units, long long pages, int n) {
     const int held = f.held[k.ctas][n];
     if (held <= 0) return LLONG_MAX;
@@ -474,7 +473,8 @@ long long cost4(const Attend4Kernel &k, const Fit4 &f, bool few, long long units
         if (l > 1 || waves > 1) return LLONG_MAX;
         return n == 1 ? time - 1100 : std::max<long long>(time - 100, 1700);
     }
-    return waves * kSlow[k.ctas][l] * time / 20 + 600 * (l - 1) + 5000 * (waves - 1) - (n == 1 ? 1000 : 0);
+    const int slow = l == 1 ? 20 : k.ctas == 4 && l == 2 ? 20 + (k.full - 20) * 3 / 8 : k.full;
+    return waves * slow * time / 20 + 600 * (l - 1) + 5000 * (waves - 1) - (n == 1 ? 1000 : 0);
 }
 
 // CTAs of a range (num_splits, or the cheapest number), their kernel and the cost.
@@ -502,10 +502,10 @@ long long split4(Attend4Kernel *k4, int head_dim, int rows, long long units, lon
 // The same of equal shares: `units` ranges (by this kernel's row tiles) of `pages`
 // pages each, read by all SMs at 1.1 times what full SMs take.  The second launch, the
 // scan of the segment table and the merge cost 10 us (the tcgen05 kernel: 14.5),
-// a range about 8 ns (35).
+// a range about 12 ns (35).
 long long cost4_shares(const Attend4Kernel &k, long long units, long long pages) {
     const bool wide = k.rows == 128;
-    return (wide ? 14500 : 10000) + units * (wide ? 35 : 8) + units * pages * k.page_ns * kSlow[k.ctas][k.ctas] * 11 / (200LL * k.ctas * device_sms());
+    return (wide ? 14500 : 10000) + units * (wide ? 35 : 12) + units * pages * k.page_ns * k.full * 11 / (200LL * k.ctas * device_sms());
 }
 
 struct Ws4Layout {

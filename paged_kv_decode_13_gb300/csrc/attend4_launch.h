@@ -45,7 +45,8 @@ struct Attend4Kernel {
     int rows;   // query rows of a CTA
     int warps;
     int ctas;   // CTAs an SM holds
-    int page_ns;  // what a CTA alone on its SM takes for a page of its range (measured)
+    int page_ns;  // what a CTA alone on its SM takes for a page of its range, and
+    int full;     // what it takes on a full one, in 1 / 20 of that (both measured)
     int regs;   // registers a thread the kernel has to be launched with (it hands them between its warps), or 0
 };
 
