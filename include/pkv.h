@@ -176,7 +176,9 @@ const char *pkv_status_str(int status);
  * err_flags: device uint32, OR-ed, never cleared by the library.
  *
  * On a PKV_FP4 cache the rows are bf16 and are quantised on the way (this is
- * pkv_norm_rope_append without a pkv_rope and without q).
+ * pkv_norm_rope_append without a pkv_rope and without q).  A byte of its V
+ * pages holds two tokens; calls and segments that write different slots of
+ * one page at the same time do not disturb each other.
  */
 int pkv_append(const pkv_cache *cache, int32_t layer,
                const void *k_new, const void *v_new, int32_t total_rows,
@@ -334,7 +336,10 @@ int pkv_norm_rope_append(const pkv_cache *cache, int32_t layer, const pkv_rope *
  * pkv_attend_workspace_bytes).  PKV_FLAG_SIMT, PKV_FLAG_MMA_SYNC and
  * PKV_FLAG_PREFETCH_NEXT have no effect.  PKV_FLAG_PDL: pages wholly below
  * position kv_end - q_len may be read before the previous kernel has
- * finished, so it may be the append of this step.
+ * finished, so it may be the append of this step.  (Most 4-bit attention
+ * launches, and pkv_norm_rope and pkv_norm_rope_append, are programmatic
+ * dependent launches without the flag too, which wait for the previous
+ * kernel first thing.)
  *
  * Device pointers must be 16-byte aligned (out and lse: 4-byte; with a
  * PKV_FP4 cache out: 16-byte).
@@ -383,11 +388,15 @@ int pkv_append_attend(const pkv_cache *cache, int32_t layer,
  * concurrently need their own.  A workspace smaller than this size is rejected with
  * PKV_EINVAL.  Returns a negative pkv_status for invalid bounds.
  *
- * With a PKV_FP4 cache: launches with num_splits 0, at most 8 query rows per
- * kv head, at most 512 segments and bounds of about 100,000 (key, kv head)
- * pairs or more.  Given a workspace, they run as one wave of CTAs with equal shares of all
+ * With a PKV_FP4 cache: launches with num_splits 0, at most 512 segments and
+ * at most 16 row tiles a kv head, whose bounds make it worth while (at 8 query rows per kv
+ * head and head_dim 128, from about half a million (key, kv head) pairs for one
+ * sequence and twice that for several; with more rows from fewer).
+ * Given a workspace, they run as one wave of CTAs with equal shares of all
  * key ranges and a second launch that merges the shared ones, instead of as a
- * cluster per range.  It need not be zeroed, and may be shared by calls that
+ * cluster per range; more than 32 rows per kv head at head_dim 128 then take
+ * the tcgen05 tile.  The size does not grow with the lengths and is below 25 MB.
+ * It need not be zeroed, and may be shared by calls that
  * follow one another on one stream.
  */
 int64_t pkv_attend_workspace_bytes(const pkv_cache *cache, int32_t num_q_heads,

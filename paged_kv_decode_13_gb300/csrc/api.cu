@@ -377,12 +377,11 @@ struct Plan4 {
 constexpr int kSharesEdge = 15;
 constexpr int kSharesSegments = 512;
 constexpr int kSharesTiles = 16;  // each tile's range is taken as long as its segment's: not for long causal chunks
-constexpr int kPieceWide = 36;  // the same for the tcgen05 kernel, in pages
+constexpr int kPieceTile = 50;  // (tiles of 16 and 32 rows; 30 and 80 are slower for uneven lengths at every head_dim)
 // Rows a kv head from which the tcgen05 kernel (tiles of 128) is faster than mma.sync tiles
 // of 32: as shares of 8 sequences of 4096 keys and 8 heads, 32 rows 43 us
 // against 34, 36 rows 43 against 51, 128 rows 51 against 89.
 constexpr int kWideFrom = 33;
-constexpr int kPieceBytes = 56 << 10;  // what a piece costs, as bytes that one CTA reads meanwhile
 
 // Whether the kernel was compiled to the register count its warps hand around
 // (setmaxnreg waits for registers the launch must have brought).
@@ -499,13 +498,21 @@ long long split4(Attend4Kernel *k4, int head_dim, int rows, long long units, lon
     return best;
 }
 
+// What a piece of a range costs a CTA of equal shares besides its pages (query rows in,
+// first pages, partials out), in pages: CTAs are dealt equal sums of both.
+// The batch of 32 uneven sequences (8 rows, head_dim 128) took 60 us with 24
+// pages, uneven 16-row tiles of head_dim 256 (16 sequences up to 4096 keys) 67 us
+// with 12, the tcgen05 kernel's drafts of 16 sequences 82, 72, 73 us with 10, 36, 24.
+int piece_pages4(const Attend4Kernel &k, int head_dim) {
+    return k.rows == 128 ? 36 : k.rows == 8 ? (56 << 10) / (2 * block4_bytes(head_dim)) : kPieceTile;
+}
+
 // The same of equal shares: `units` ranges (by this kernel's row tiles) of `pages`
-// pages each, read by all SMs at 1.1 times what full SMs take.  The second launch, the
-// scan of the segment table and the merge cost 10 us (the tcgen05 kernel: 14.5),
-// a range about 12 ns (35).
-long long cost4_shares(const Attend4Kernel &k, long long units, long long pages) {
-    const bool wide = k.rows == 128;
-    return (wide ? 14500 : 10000) + units * (wide ? 35 : 12) + units * pages * k.page_ns * k.full * 11 / (200LL * k.ctas * device_sms());
+// pages each, pieces and pages read by all SMs at 1.1 times what full SMs take;
+// the second launch and the scan of the segment table cost 10 us (the tcgen05 kernel: 14.5).
+long long cost4_shares(const Attend4Kernel &k, int head_dim, long long units, long long pages) {
+    return (k.rows == 128 ? 14500 : 10000) +
+           units * (pages + piece_pages4(k, head_dim)) * k.page_ns * k.full * 11 / (200LL * k.ctas * device_sms());
 }
 
 struct Ws4Layout {
@@ -541,7 +548,7 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     if (num_splits == 0 && S > 0 && S <= kSharesSegments) {
         if (c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide())) pl->ks = pick4_wide();
         const long long tiles = (rows + pl->ks.rows - 1) / pl->ks.rows;
-        const long long shares = cost4_shares(pl->ks, (long long)S * c->kv_heads * tiles, pl->pages);
+        const long long shares = cost4_shares(pl->ks, c->head_dim, (long long)S * c->kv_heads * tiles, pl->pages);
         if (tiles <= kSharesTiles && shares < cost + cost * kSharesEdge / 100)
             pl->shares = std::min(device_sms() * pl->ks.ctas, kMerge4Slots);
     }
@@ -597,7 +604,7 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     p.out_bf16 = (flags & PKV_FLAG_OUT_BF16) ? 1 : 0;
     p.early = (flags & PKV_FLAG_PDL) ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.piece_pages = shares && pl.ks.rows == 128 ? kPieceWide : kPieceBytes / (2 * block4_bytes(c->head_dim));
+    p.piece_pages = piece_pages4(k4, c->head_dim);
     p.ws_head = nullptr;
     p.ws_stat = nullptr;
     p.ws_part = nullptr;

@@ -819,10 +819,10 @@ def attend_in_shares(pkv, f, max_q, window):
 
 
 @pytest.mark.parametrize("q_heads,max_q", [(8, 1), (16, 4), (32, 4), (64, 9)])
-@pytest.mark.parametrize("window", [300, 700])
+@pytest.mark.parametrize("window", [1000, 3000])
 @pytest.mark.parametrize("padded", [False, True])
 def test_shares_with_windows(pkv, q_heads, max_q, window, padded):
-    w = workloads.spec_verify(S=7, max_q=max_q, len_lo=max_q, len_hi=2000, seed=q_heads + window, q_heads=q_heads, kv_heads=8)
+    w = workloads.spec_verify(S=7, max_q=max_q, len_lo=max_q, len_hi=6000, seed=q_heads + window, q_heads=q_heads, kv_heads=8)
     ends = w.seq_info[:, 3].tolist()
     fv = np.array([0, 17, ends[2] - 1, ends[3] + 5, max(ends[4] - 5, 0), 3, 0], np.int32) if padded else None
     f = Fp4(pkv, w, first_valid=fv)
@@ -831,7 +831,7 @@ def test_shares_with_windows(pkv, q_heads, max_q, window, padded):
     check(f, out, lse, window=window)
 
 
-@pytest.mark.parametrize("D,window,ring,kv", [(128, 700, 720, 5000), (64, 700, 704, 3000), (256, 512, 512, 3001)])
+@pytest.mark.parametrize("D,window,ring,kv", [(128, 3000, 3024, 5000), (64, 2000, 2000, 3000), (256, 2000, 2000, 3001)])
 @pytest.mark.parametrize("q_heads", [8, 288])
 def test_shares_with_rings(pkv, D, window, ring, kv, q_heads):
     w = workloads.long_context(S=3, kv_len=kv, window=window, ring_rows=ring, q_heads=q_heads, kv_heads=8, head_dim=D)
