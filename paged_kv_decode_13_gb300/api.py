@@ -367,6 +367,11 @@ def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max
         with torch.cuda.device(dev):
             return _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max_q_len, max_kv, scale, causal,
                            window, num_splits, flags, stream, workspace)
+    if cache._fp4:
+        if q.dtype is not torch.bfloat16 or (out.dtype is not torch.float32 and out.dtype is not torch.bfloat16) or out.shape != shape:
+            raise ValueError("over a 4-bit cache q is bf16 (rows, heads, head_dim) and out fp32 or bf16 of the same shape")
+        if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != shape[0] * shape[1]):
+            raise ValueError("lse is fp32 (rows, heads)")
     if cache._fp4 and workspace is None and num_splits == 0:
         workspace = _fp4_workspace(cache, shape[1], segments, max_q_len, max_kv, window, flags, stream)
     new = ()

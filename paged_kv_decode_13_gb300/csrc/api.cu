@@ -8,7 +8,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <climits>
 #include <mutex>
 
 #include <math.h>
@@ -460,25 +459,26 @@ const Fit4 &fit4(const Attend4Kernel &k) {
 // few: the kernel with eight warps, for ranges that leave it alone on its SM: it is
 // through a page sooner, and its merge takes longer (one range of 256 keys
 // 5.3 us against 5.9, of 4096 7.4 against 6.9, of 8192 7.5 against 8.7).
-long long cost4(const Attend4Kernel &k, const Fit4 &f, bool few, long long units, long long pages, int n) {
+constexpr double kNever = 1e30;
+double cost4(const Attend4Kernel &k, const Fit4 &f, bool few, long long units, long long pages, int n) {
     const int held = f.held[k.ctas][n];
-    if (held <= 0) return LLONG_MAX;
-    const long long time = (pages + n - 1) / n * k.page_ns;
+    if (held <= 0) return kNever;
+    const double time = (double)((pages + n - 1) / n) * k.page_ns;
     const long long room = n >= 12 ? units + units / 4 : n >= 8 || (n >= 3 && k.ctas <= 2) ? units + units / 16 : units;
     int l = 1;
     while (l < k.ctas && f.held[l][n] < room) ++l;
     const long long waves = held >= room ? 1 : std::max<long long>(2, (units + units / 8 + held - 1) / held);
     if (few) {
-        if (l > 1 || waves > 1) return LLONG_MAX;
-        return n == 1 ? time - 1100 : std::max<long long>(time - 100, 1700);
+        if (l > 1 || waves > 1) return kNever;
+        return n == 1 ? time - 1100 : std::max(time - 100, 1700.0);
     }
     const int slow = l == 1 ? 20 : k.ctas == 4 && l == 2 ? 20 + (k.full - 20) * 3 / 8 : k.full;
-    return waves * slow * time / 20 + 600 * (l - 1) + 5000 * (waves - 1) - (n == 1 ? 1000 : 0);
+    return waves * time * slow / 20 + 600 * (l - 1) + 5000.0 * (waves - 1) - (n == 1 ? 1000 : 0);
 }
 
 // CTAs of a range (num_splits, or the cheapest number), their kernel and the cost.
-long long split4(Attend4Kernel *k4, int head_dim, int rows, long long units, long long pages, int num_splits, int *ncta) {
-    long long best = LLONG_MAX;
+double split4(Attend4Kernel *k4, int head_dim, int rows, long long units, long long pages, int num_splits, int *ncta) {
+    double best = kNever;
     const Attend4Kernel cand[2] = {*k4, pick4_rows(head_dim, rows, true)};
     *ncta = 1;
     for (int few = 0; few < (cand[1].fn == cand[0].fn ? 1 : 2); ++few) {
@@ -487,7 +487,7 @@ long long split4(Attend4Kernel *k4, int head_dim, int rows, long long units, lon
         // no more CTAs than leave each of its warps four pages
         const int top = (int)std::max<long long>(1, std::min<long long>(kMaxCluster, pages / (4 * k.warps)));
         for (int n = num_splits ? num_splits : 1; n <= (num_splits ? num_splits : top); ++n) {
-            const long long cost = cost4(k, f, few, units, pages, n);
+            const double cost = cost4(k, f, few, units, pages, n);
             if (cost < best) {
                 best = cost;
                 *k4 = k;
@@ -495,6 +495,7 @@ long long split4(Attend4Kernel *k4, int head_dim, int rows, long long units, lon
             }
         }
     }
+    if (best == kNever && num_splits) *ncta = num_splits;  // (the launch takes the largest that fits)
     return best;
 }
 
@@ -510,9 +511,9 @@ int piece_pages4(const Attend4Kernel &k, int head_dim) {
 // The same of equal shares: `units` ranges (by this kernel's row tiles) of `pages`
 // pages each, pieces and pages read by all SMs at 1.1 times what full SMs take;
 // the second launch and the scan of the segment table cost 10 us (the tcgen05 kernel: 14.5).
-long long cost4_shares(const Attend4Kernel &k, int head_dim, long long units, long long pages) {
+double cost4_shares(const Attend4Kernel &k, int head_dim, long long units, long long pages) {
     return (k.rows == 128 ? 14500 : 10000) +
-           units * (pages + piece_pages4(k, head_dim)) * k.page_ns * k.full * 11 / (200LL * k.ctas * device_sms());
+           (double)units * (pages + piece_pages4(k, head_dim)) * k.page_ns * k.full * 11 / (200.0 * k.ctas * device_sms());
 }
 
 struct Ws4Layout {
@@ -544,12 +545,12 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     pl->pages = (keys + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE;
     pl->shares = 0;
     pl->ks = pl->k4;
-    const long long cost = split4(&pl->k4, c->head_dim, (int)rows, pl->units, pl->pages, num_splits, &pl->ncta);
+    const double cost = split4(&pl->k4, c->head_dim, (int)rows, pl->units, pl->pages, num_splits, &pl->ncta);
     if (num_splits == 0 && S > 0 && S <= kSharesSegments) {
         if (c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide())) pl->ks = pick4_wide();
         const long long tiles = (rows + pl->ks.rows - 1) / pl->ks.rows;
-        const long long shares = cost4_shares(pl->ks, c->head_dim, (long long)S * c->kv_heads * tiles, pl->pages);
-        if (tiles <= kSharesTiles && shares < cost + cost * kSharesEdge / 100)
+        const double shares = cost4_shares(pl->ks, c->head_dim, (long long)S * c->kv_heads * tiles, pl->pages);
+        if (tiles <= kSharesTiles && shares < cost * (100 + kSharesEdge) / 100)
             pl->shares = std::min(device_sms() * pl->ks.ctas, kMerge4Slots);
     }
     return PKV_OK;

@@ -277,3 +277,26 @@ def test_binding_refusals(pkv):
             a["q_out"] = kn.float()
         with pytest.raises(ValueError):
             pkv.norm_rope_append(c, 0, **a)
+
+
+@pytest.mark.parametrize("q,out,lse", [
+    (torch.float32, (torch.float32, (2, 4, 64)), None), (torch.bfloat16, (torch.float16, (2, 4, 64)), None),
+    (torch.bfloat16, (torch.float32, (1, 4, 64)), None), (torch.bfloat16, (torch.bfloat16, (2, 4, 128)), None),
+    (torch.bfloat16, (torch.float32, (2, 4, 64)), (torch.float32, (2, 3))), (torch.bfloat16, (torch.float32, (2, 4, 64)), (torch.bfloat16, (2, 4))),
+])
+def test_attention_over_fp4_checks_its_tensors(q, out, lse):
+    import paged_kv_decode_13_gb300 as pkv
+    cache = pkv.PagedKVCache.allocate(1, 2, 64, 512, dtype=torch.uint8, device="cpu")
+    si, err = torch.tensor([[0, 2, 0, 2]], dtype=torch.int32), pkv.new_err_flags("cpu")
+    lse = None if lse is None else torch.empty(lse[1], dtype=lse[0])
+    with pytest.raises(ValueError):
+        pkv.attend_varlen(cache, 0, torch.zeros(2, 4, 64, dtype=q), si, torch.empty(out[1], dtype=out[0]), err, 2, 512, 0.125, lse=lse)
+
+
+def test_workspace_bounds_do_not_overflow(lib):
+    """Any bounds give a size or a refusal, the largest ones a size that does not grow with them."""
+    d, keep = _desc(lib, kv_heads=64)
+    size = lib.lib.pkv_attend_workspace_bytes(ctypes.byref(d), 512, 512, 1, 1 << 20, 0, 0)
+    assert 0 < size < 25 << 20
+    assert lib.lib.pkv_attend_workspace_bytes(ctypes.byref(d), 512, 512, 1, (1 << 62), 0, 0) == size
+    assert lib.lib.pkv_attend_workspace_bytes(ctypes.byref(d), 512, 512, 1, 16, 0, 0) == 0
