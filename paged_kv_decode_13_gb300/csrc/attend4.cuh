@@ -132,11 +132,10 @@ __device__ __forceinline__ void zero_row4(const Attend4Params &p, long long row,
 // Rows of no segment read zero, rows of two set PKV_ERR_OVERLAP: the grid's
 // CTAs share the rows, a warp a row at a time, lanes over the segments.
 template <int D>
-__device__ __noinline__ void coverage4(const Attend4Params &p) {
+__device__ __noinline__ void cover_rows4(const Attend4Params &p, long long row) {
     const int lane = threadIdx.x & 31;
-    const long long cta = blockIdx.x + (long long)gridDim.x * (blockIdx.y + (long long)gridDim.y * blockIdx.z);
     const long long warps = (long long)gridDim.x * gridDim.y * gridDim.z * (blockDim.x >> 5);
-    for (long long row = cta * (blockDim.x >> 5) + (threadIdx.x >> 5); row < p.total_rows; row += warps) {
+    for (; row < p.total_rows; row += warps) {
         int n = 0;
         for (int s = lane; s < p.S; s += 32) {
             const int4 v = p.seq_info[s];
@@ -146,6 +145,12 @@ __device__ __noinline__ void coverage4(const Attend4Params &p) {
         if (n == 0) zero_row4(p, row, 0, p.Hq, D, lane, 32);
         if (n > 1 && lane == 0) atomicOr(p.err, PKV_ERR_OVERLAP);
     }
+}
+template <int D>
+__device__ __forceinline__ void coverage4(const Attend4Params &p) {
+    const long long cta = blockIdx.x + (long long)gridDim.x * (blockIdx.y + (long long)gridDim.y * blockIdx.z);
+    const long long row = cta * (blockDim.x >> 5) + (threadIdx.x >> 5);  // the warp's first
+    if (row < p.total_rows) cover_rows4<D>(p, row);
 }
 
 // The dependency wait.  Every launch is a programmatic dependent one, so that
@@ -236,6 +241,8 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
     uint64_t *wbars = sm.bars + kw * NST;
     unsigned char *wstage = pipe + (size_t)kw * NST * C::kStage;
     const int *bt_row = p.block_table + (long long)sg.col * p.mbps;
+    // ids of the warp's first 32 pages (lane l: page l), on their way while the bounds are formed
+    const int id_first = kw + lane * KW < nb ? bt_row[table_page(cb0 + kw + lane * KW, p.ring_rows)] : -1;
     if (tid == 0) sFlag[0] = 0;
     if (tid < R) {
         int lo = 0, hi = 0;  // padding rows see no key
@@ -249,7 +256,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
     // ---- page ids and copies.  The warp's j-th stage is its pages j PP .. (j + 1) PP - 1;
     // lane l holds the id of its page window + l.
     const int stages = (n_mine + PP - 1) / PP, base = ring;
-    int id_reg = -1, id_window = -1;
+    int id_reg = id_first, id_window = 0;
     bool bad = false, timed_out = false;
     const unsigned char *copy_base = ((lane & 1) ? p.v : p.k) + (size_t)h * C::kBlock;
     const size_t block_stride = (size_t)p.Hkv * C::kBlock;
@@ -750,7 +757,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
 // them splits long and short ranges alike; shares have neither limit.
 
 // A CTA's share, and a walk over its pieces.
+// FAST: two paths for each division (a CTA of 640 threads, five roles of which
+// walk their pieces, is faster with less code: 72 us against 75).
+template <bool FAST>
 struct Share4 {
+    // a / b for a >= 0, b > 0; short where both fit 32 bits, as they mostly do.
+    __device__ __forceinline__ static long long div4(long long a, long long b) {
+        return !FAST || ((unsigned long long)(a | b) >> 32) ? a / b : (long long)((unsigned)a / (unsigned)b);
+    }
     long long T;       // length of all ranges
     int N;             // CTAs that share them
     long long at, b;   // what is left of this CTA's share
@@ -796,14 +810,14 @@ struct Share4 {
             if (k < tid >> 5) upto += scratch[k];
             T += scratch[k];
         }
-        N = (int)max(1ll, min((long long)gridDim.x, T / p.min_pages));
-        at = cta * T / N;
-        b = cta < N ? (cta + 1) * T / N : at;
+        N = (int)max(1ll, min((long long)gridDim.x, div4(T, p.min_pages)));
+        at = div4(cta * T, N);
+        b = cta < N ? div4((cta + 1) * T, N) : at;
         if (at < b && upto - mine <= at && at < upto) {
             long long x = upto - mine;
             int i = s_lo;
 #pragma unroll 1
-            for (; i < s_hi; ++i) {
+            for (; i + 1 < s_hi; ++i) {  // (the last one, where none before it does)
                 Piece4 w;
                 segment(p, i, w);
                 const long long n = length(p, w, R);
@@ -832,7 +846,7 @@ struct Share4 {
                 ++s;
                 continue;
             }
-            const int range = (int)((at - begin) / len), tiles = (w.rows + R - 1) / R;
+            const int range = (int)div4(at - begin, len), tiles = (w.rows + R - 1) / R;
             tile = range % tiles;
             const long long first = begin + (long long)range * len, end = min(b, first + len);
             // the pages come after the piece's cost
@@ -848,7 +862,7 @@ struct Share4 {
             w.page0 = page;
             w.pages = n;
             whole = n == nblk;
-            last = (int)(((first + len) * N - 1) / T);
+            last = (int)div4((first + len) * N - 1, T);
             return true;
         }
         return false;
@@ -867,7 +881,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) balance4_kernel(const _
     const int tid = threadIdx.x, cta = blockIdx.x;
     init_bars4<C>(sm);
     depend4(p, false);
-    Share4 share;
+    Share4<true> share;
     share.find<NTHR>(p, R, reinterpret_cast<long long *>(sm.recv));
     int ring = 0, left = 0;  // left: bit i, a piece in slot 2 cta + i
     bool waited = false;

@@ -119,7 +119,7 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
     tc_fence_after();
     const unsigned tmem = *tslot, lane_off = (unsigned)(32 * quad) << 16;
     depend4(p, false);
-    Share4 share;
+    Share4<false> share;
     share.find<C::kThreads>(p, R, reinterpret_cast<long long *>(sQm));
     depend4(p, true);
 
