@@ -21,15 +21,15 @@
 // and a few narrow shared loads a lane, a conversion (two values) and one fp16
 // multiply by the scale for each fragment register, and no shuffles.
 //
-// A page of one kv head (2,304 bytes at D = 128) costs a warp about 250 issue slots, a
+// A page of one kv head (2,304 bytes at D = 128) costs a warp about 300 issue slots, a
 // quarter of them conversions (two a value pair at half rate), so four
 // or five warps an SM sub-partition are needed to keep up with HBM: CTAs of four
 // warps, four an SM for 8 rows.  Sequences of equal length stream at 0.8 to
 // 0.9 of the rate of a copy once a CTA has some 100 pages; short calls are a chain of
 // launch (2.5 us), tables and first pages (2 us), and the merge (1 to 2 us).
 // Eight warps a CTA double the pages in flight for few ranges.  At most 8 rows,
-// head_dim 128: 300 keys 6.4 us, 8192 keys 9.3 us (the launch, the
-// merge), 32 sequences of up to 16384 keys 60 us (37 at the rate of a copy; HBM 57 %
+// head_dim 128: 300 keys 6.4 us, 8192 keys 9.1 us (the launch, the
+// merge), 32 sequences of up to 16384 keys 58 us (37 at the rate of a copy; HBM 57 %
 // busy: starts and ends of 1,000 pieces); head_dim 256, 4 x 131072 keys 107
 // us (89; HBM 73 %).  More splits, one large CTA an SM, sixteen warps and
 // integer unpacking (2.2 times the conversion's time) were slower.
