@@ -20,8 +20,8 @@
 // 77 us, 4.3 TB/s, against 49 us at the rate of a copy; 2,800 instructions a token
 // (convert, square, scale, rotate, round: about 10 a value pair with packed
 // fp32) keep the schedulers 52 % busy, at 20 warps an SM (96 registers).  Three
-// heads' loads in flight or six, more warps with fewer registers, prefetches
-// and a version fed by bulk copies through shared memory (95 us) were slower.
+// heads' loads in flight or six, more warps with fewer registers, prefetches,
+// loads rolling from row to row (85 us) and a version fed by bulk copies through shared memory (95 us) were slower.
 //
 // Angles: turn_i = frequency / 2 pi as a 64-bit fraction of a turn.  position *
 // turn_i, taken modulo 2^64, is the exact fractional turn to 2^-33 at any
