@@ -324,9 +324,26 @@ def norm_rope_append(cache: PagedKVCache, layer: int, rope: Optional[Rope], q: O
             dev, stream)
 
 
+def _check_new(k_new: torch.Tensor, v_new: torch.Tensor) -> None:
+    if k_new.dtype is not torch.bfloat16 or v_new.dtype is not torch.bfloat16 or k_new.shape != v_new.shape:
+        raise ValueError("rows for a 4-bit cache are bf16, k_new and v_new of one shape")
+
+
+def _check_fp4(q, k_new, v_new, out, lse) -> None:
+    """The tensors of an attention call over a 4-bit cache."""
+    if q.dtype is not torch.bfloat16 or (out.dtype is not torch.float32 and out.dtype is not torch.bfloat16) or out.shape != q.shape:
+        raise ValueError("over a 4-bit cache q is bf16 (rows, heads, head_dim) and out fp32 or bf16 of the same shape")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != q.shape[0] * q.shape[1]):
+        raise ValueError("lse is fp32 (rows, heads)")
+    if k_new is not None:
+        _check_new(k_new, v_new)
+
+
 def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, seq_info: torch.Tensor,
            err: torch.Tensor, window: int = 0, stream=None) -> None:
     rows = int(k_new.shape[0])
+    if cache._fp4:
+        _check_new(k_new, v_new)
     _lib.check("pkv_append", lib.pkv_append(
         cache.ref(), layer, _ptr(_contig(k_new, "k_new")), _ptr(_contig(v_new, "v_new")), rows,
         _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(window), _ptr(err), _stream(stream)))
@@ -368,10 +385,7 @@ def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max
             return _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max_q_len, max_kv, scale, causal,
                            window, num_splits, flags, stream, workspace)
     if cache._fp4:
-        if q.dtype is not torch.bfloat16 or (out.dtype is not torch.float32 and out.dtype is not torch.bfloat16) or out.shape != shape:
-            raise ValueError("over a 4-bit cache q is bf16 (rows, heads, head_dim) and out fp32 or bf16 of the same shape")
-        if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != shape[0] * shape[1]):
-            raise ValueError("lse is fp32 (rows, heads)")
+        _check_fp4(q, k_new, v_new, out, lse)
     if cache._fp4 and workspace is None and num_splits == 0:
         workspace = _fp4_workspace(cache, shape[1], segments, max_q_len, max_kv, window, flags, stream)
     new = ()
@@ -409,6 +423,8 @@ def append_attend_noalloc(cache: PagedKVCache, layer: int, q: torch.Tensor, k_ne
                           stream=None) -> None:
     """pkv_append_attend_noalloc: append_attend merging its splits in the library's fixed scratch."""
     rows, hq = int(q.shape[0]), int(q.shape[1])
+    if cache._fp4:
+        _check_fp4(q, k_new, v_new, out, lse)
     if out.dtype == torch.bfloat16:
         flags |= _lib.FLAG_OUT_BF16
     _lib.check("pkv_append_attend_noalloc", lib.pkv_append_attend_noalloc(

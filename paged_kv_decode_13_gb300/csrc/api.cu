@@ -369,7 +369,7 @@ struct Plan4 {
 
 // Equal shares are taken up to this many percent above what the clusters cost at equal
 // lengths: they balance lengths that differ, which the bounds do not tell.
-// (16 ranges' worth, 8 kv heads, head_dim 128: of 8192 keys each 42 us in shares
+// (16 sequences, 8 kv heads, head_dim 128: of 8192 keys each 42 us in shares
 // against 35, of random lengths up to that 32 against 32; up to 16384 65
 // against 60 and 37 against 47; one sequence of 131072 keys 42 against 59.)
 // Every CTA sums the segment table's pages, so the table has to be short.

@@ -293,6 +293,22 @@ def test_attention_over_fp4_checks_its_tensors(q, out, lse):
         pkv.attend_varlen(cache, 0, torch.zeros(2, 4, 64, dtype=q), si, torch.empty(out[1], dtype=out[0]), err, 2, 512, 0.125, lse=lse)
 
 
+def test_rows_for_fp4_are_bf16():
+    import paged_kv_decode_13_gb300 as pkv
+    cache = pkv.PagedKVCache.allocate(1, 2, 64, 512, dtype=torch.uint8, device="cpu")
+    si, err = torch.tensor([[0, 2, 0, 2]], dtype=torch.int32), pkv.new_err_flags("cpu")
+    q, out = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.empty(2, 4, 64)
+    good = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    for k, v in ((good.float(), good), (good, good.half()), (good, good[:1])):
+        with pytest.raises(ValueError):
+            pkv.append(cache, 0, k, v, si, err)
+        for fn in (pkv.append_attend, pkv.append_attend_noalloc):
+            with pytest.raises(ValueError):
+                fn(cache, 0, q, k, v, si, out, err, 2, 512, 0.125)
+    with pytest.raises(ValueError):
+        pkv.append_attend_noalloc(cache, 0, q, good, good, si, out.half(), err, 2, 512, 0.125)
+
+
 def test_workspace_bounds_do_not_overflow(lib):
     """Any bounds give a size or a refusal, the largest ones a size that does not grow with them."""
     d, keep = _desc(lib, kv_heads=64)
