@@ -379,7 +379,7 @@ def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max
     max_q_len, max_kv, window = int(max_q_len), int(max_kv), int(window)
     if out.dtype is torch.bfloat16:
         flags |= _lib.FLAG_OUT_BF16
-    dev = cache._device
+    dev = cache._device  # -1 on the host (a call that is refused)
     if dev >= 0 and dev != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             return _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max_q_len, max_kv, scale, causal,
@@ -392,10 +392,11 @@ def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max
     if fn_name == "pkv_append_attend":
         new = (_contig(k_new, "k_new").data_ptr(), _contig(v_new, "v_new").data_ptr())
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None and dev >= 0 else _stream(stream)
     st = getattr(lib, fn_name)(
         cache._ref, layer, _contig(q, "q").data_ptr(), *new, shape[1], shape[0], _contig(seq_info, "seq_info").data_ptr(), segments,
         max_q_len, max_kv, int(num_splits), float(scale), 1 if causal else 0, window, _contig(out, "out").data_ptr(),
-        None if lse is None else lse.data_ptr(), ws, ws_bytes, err.data_ptr(), int(flags), _stream(stream))
+        None if lse is None else lse.data_ptr(), ws, ws_bytes, err.data_ptr(), int(flags), handle)
     if st:
         _lib.check(fn_name, st)
 
