@@ -357,8 +357,10 @@ _FP4_WORKSPACE_FROM = 1 << 18
 def _fp4_workspace(cache, hq, segments, max_q_len, max_kv, window, flags, stream):
     """A workspace for one call over a 4-bit cache, or None: a large launch merges its shared ranges through it.
 
-    Each call takes its own from torch's allocator, so calls on several
-    streams, and captured graphs, share nothing.
+    Each call takes its own from torch's allocator, so eager calls on several
+    streams share nothing.  A captured call's comes from the graph's memory pool:
+    graphs captured into one pool must not run at the same time, unless their
+    calls were given workspaces of their own (DecodeStep keeps one).
     """
     keys = min(max_kv, window + max_q_len) if window > 0 else max_kv
     tiles = -(-hq * max_q_len // (8 * cache._kv_heads))  # of 8 query rows, at most

@@ -18,7 +18,7 @@ from typing import Dict, List, Optional, Sequence, Tuple, Union
 import torch
 
 from . import _lib
-from .api import (PagedKVCache, Rope, append, append_attend, attend_varlen, new_err_flags, new_workspace,
+from .api import (PagedKVCache, Rope, append, append_attend, attend_varlen, attend_workspace_bytes, new_err_flags,
                   norm_rope_append)
 from .api import advance as advance_lengths
 
@@ -65,7 +65,8 @@ class DecodeStep:
     launches (fused does not apply).  The angles are those of the rows'
     positions in the cache.  A cache held in 4 bits takes two launches a layer
     as well, three where large bounds share the key ranges; its outputs may be
-    bf16 (out_dtype).
+    bf16 (out_dtype).  The workspace of that merge belongs to the step: a
+    capture allocates nothing, and captured steps share no memory.
     """
 
     def __init__(self, cache: PagedKVCache, num_q_heads: int, rows: int = 1, num_segments: int = 1,
@@ -112,11 +113,16 @@ class DecodeStep:
         self.size_workspace()
 
     def size_workspace(self) -> None:
-        """(Re)allocate the split-merge workspace for the current cache and bounds (None when not needed)."""
-        self.ws = None
-        if self.use_workspace:
-            self.ws = new_workspace(self.cache, self.num_q_heads, int(self.seq_info.shape[0]), self.max_q_len,
-                                    self.max_kv, self.num_splits, self.flags)
+        """(Re)allocate the split-merge workspace where the current cache and bounds need another size (None: they need none)."""
+        fp4, n = self.cache.dtype == torch.uint8, 0
+        if self.use_workspace or (fp4 and self.num_splits == 0):
+            n = attend_workspace_bytes(self.cache, self.num_q_heads, int(self.seq_info.shape[0]), self.max_q_len, self.max_kv,
+                                       self.num_splits, self.flags)
+        if n <= 0:
+            self.ws = None
+        elif self.ws is None or self.ws.numel() != n:
+            make = torch.empty if fp4 else torch.zeros  # (a 4-bit cache's need not be zeroed)
+            self.ws = make(n, dtype=torch.uint8, device=self.cache.k[0].device)
 
     def launch_count(self) -> int:
         """Kernels of one run (a 4-bit cache's merge launches, which its bounds decide, not counted)."""
@@ -190,7 +196,11 @@ class DecodeGraphRunner:
         st = self.step_bufs
         st.cache = cache
         st.max_kv = cache.bucket
+        ws = st.ws
         st.size_workspace()
+        if ws is not None and st.ws is not ws:  # every capture holds the old one
+            ws.record_stream(torch.cuda.current_stream(ws.device))  # (a replay of theirs may still run)
+            self._graphs = {}
         self._graphs = {k: g for k, g in self._graphs.items() if k == (cache.bucket, cache.generation)}
 
     def graph_for(self) -> torch.cuda.CUDAGraph:
