@@ -265,10 +265,12 @@ int pkv_norm_rope(const pkv_rope *rope, int32_t dtype, int32_t head_dim, int32_t
  * those are the quantised values (k is rounded to bf16 before it is
  * quantised).  Rows are of the cache's dtype (PKV_FP4: bf16).
  *
- * A row belongs to one segment at most (in two it is unspecified which of
- * them places it).  Rows no segment covers, and rows of segments that
- * pkv_append would refuse (the same PKV_ERR_* bits), are not written, in
- * none of the outputs.  A later attention call may be launched with
+ * On a bf16 or fp32 cache a row belongs to one segment at most (in two it is
+ * unspecified which of them places it).  On a PKV_FP4 cache it goes to its slot
+ * in every segment that holds it, turned by positions[row] or by its position
+ * in the lowest of them (v_out must not be v then).  Rows no segment covers, and
+ * rows of segments that pkv_append would refuse (the same PKV_ERR_* bits), are
+ * not written, in none of the outputs.  A later attention call may be launched with
  * PKV_FLAG_PDL behind this one.
  */
 int pkv_norm_rope_append(const pkv_cache *cache, int32_t layer, const pkv_rope *rope, const pkv_rows *rows,

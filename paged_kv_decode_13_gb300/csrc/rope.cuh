@@ -89,17 +89,33 @@ __device__ __forceinline__ bool holds_row(const RopeParams &p, const Segment &sg
            !segment_fault(sg, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
 }
 
-// Lowest valid segment that holds `row`, or -1 (the whole warp asks).  A decode
-// step's table has segment i at row i: looked at first.
-__device__ __forceinline__ int segment_of_row(const RopeParams &p, int row, int lane) {
-    if (row < p.S && holds_row(p, load_segment(p.seq_info, row), row)) return row;
-    for (int s0 = 0; s0 < p.S; s0 += 32) {
+// Lowest valid segment from `from` on that holds `row`, or -1 (the whole warp asks).
+__device__ __forceinline__ int next_segment(const RopeParams &p, int row, int from, int lane) {
+    for (int s0 = from; s0 < p.S; s0 += 32) {
         const int s = s0 + lane;
         const bool hit = s < p.S && holds_row(p, load_segment(p.seq_info, min(s, p.S - 1)), row);
         const unsigned m = __ballot_sync(0xffffffffu, hit);
         if (m) return s0 + __ffs(m) - 1;
     }
     return -1;
+}
+
+// A valid segment that holds `row`, or -1 (the whole warp asks): the lowest, but
+// segment i for row i, as a decode step's table has it, is looked at first.
+__device__ __forceinline__ int segment_of_row(const RopeParams &p, int row, int lane) {
+    if (row < p.S && holds_row(p, load_segment(p.seq_info, row), row)) return row;
+    return next_segment(p, row, 0, lane);
+}
+
+// Whether a segment but s has a row of sg, segment s (the whole warp asks).
+__device__ __forceinline__ bool shares_rows(const RopeParams &p, const Segment &sg, int s, int lane) {
+    bool any = false;
+#pragma unroll 4
+    for (int t = lane; t < p.S; t += 32) {
+        const Segment o = load_segment(p.seq_info, t);
+        any |= t != s && o.q0 < (long long)sg.q0 + sg.ql && sg.q0 < (long long)o.q0 + o.ql;
+    }
+    return __any_sync(0xffffffffu, any);
 }
 
 // Eight elements of a row as they are in memory.
@@ -295,24 +311,53 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T 
     }
 }
 
-// Where a row goes; false where it goes nowhere (no valid segment, or a bad
-// page).  sg: the segment of the row before, looked up again when the row is
-// past it.  The whole warp asks.
-__device__ __forceinline__ bool place_row(const RopeParams &p, int row, Segment &sg, bool &pages_ok, RopeSlot &slot, long long &place, int lane) {
-    if (!(sg.q0 <= row && (long long)row < (long long)sg.q0 + sg.ql)) {
-        const int s = segment_of_row(p, row, lane);
-        if (s < 0) {
-            sg.ql = 0;
-            return false;
-        }
-        sg = load_segment(p.seq_info, s);
-        pages_ok = new_pages_ok(p, sg, lane);
-        if (!pages_ok && lane == 0) atomicOr(p.err, PKV_ERR_BLOCK);
-    }
-    if (!pages_ok) return false;
+// What a row warp knows of the segment of its last row.
+struct RowSegment {
+    Segment sg{0, 0, 0, 0};
+    int s = 0;             // its index, where `shared`
+    bool pages_ok = false;
+    bool shared = false;   // 4-bit caches: other segments have some of its rows
+};
+__device__ __forceinline__ void locate_row(const RopeParams &p, const Segment &sg, int row, RopeSlot &slot, long long &place) {
     place = (long long)sg.kend - sg.ql + (row - sg.q0);
     slot.block = p.block_table[(long long)sg.col * p.mbps + table_page((int)(place / kPage), p.ring_rows)];
     slot.token = (int)(place % kPage);
+}
+__device__ __forceinline__ bool ask_pages(const RopeParams &p, const Segment &sg, int lane) {
+    const bool ok = new_pages_ok(p, sg, lane);
+    if (!ok && lane == 0) atomicOr(p.err, PKV_ERR_BLOCK);
+    return ok;
+}
+// Where a row goes; false where it goes nowhere (no valid segment, or a bad
+// page).  c: the segment of the row before, looked up again when the row is
+// past it.  The whole warp asks.  The V pages of a 4-bit cache are written for every
+// segment of a row, and so is its K: the lowest segment that takes the row places it
+// here, copy_k4_to_others the rest.
+template <int CACHE>
+__device__ __forceinline__ bool place_row(const RopeParams &p, int row, RowSegment &c, RopeSlot &slot, long long &place, int lane) {
+    if (c.shared || !(c.sg.q0 <= row && (long long)row < (long long)c.sg.q0 + c.sg.ql)) {
+        const int s = segment_of_row(p, row, lane);
+        c.shared = false;
+        if (s < 0) {
+            c.sg.ql = 0;
+            return false;
+        }
+        c.sg = load_segment(p.seq_info, s);
+        if (CACHE == kFp4 && p.S > 1) c.shared = shares_rows(p, c.sg, s, lane);
+        if (c.shared) {
+            c.pages_ok = false;
+#pragma unroll 1
+            for (c.s = next_segment(p, row, 0, lane); c.s >= 0 && !c.pages_ok;) {
+                c.sg = load_segment(p.seq_info, c.s);
+                c.pages_ok = ask_pages(p, c.sg, lane);
+                if (!c.pages_ok) c.s = next_segment(p, row, c.s + 1, lane);
+            }
+        } else {
+            c.pages_ok = ask_pages(p, c.sg, lane);
+        }
+    }
+    if (!c.pages_ok) return false;
+    locate_row(p, c.sg, row, slot, place);
     return true;
 }
 
@@ -416,6 +461,27 @@ __device__ __forceinline__ RopeWork rope_work(const RopeParams &p, int slice, in
     w.f0 = (int)((long long)w.all * slice / slices);
     w.f1 = (int)((long long)w.all * (slice + 1) / slices);
     return w;
+}
+
+// The K heads of this warp's part of a row, as they are in the slot `from` of
+// segment s, to the row's slots in the segments after it.  (A lane copies what it wrote.)
+static __device__ __noinline__ void copy_k4_to_others(const RopeParams &p, int row, int s, RopeSlot from, int f0, int f1, int nq, int lane) {
+    const int per = 1 << p.lanes_log2, sub = lane >> p.lanes_log2, c = lane & (per - 1), heads = 32 >> p.lanes_log2, block = block4_bytes(p.D);
+    const int h0 = max(f0 - nq, 0) * heads, h1 = min(max(f1 - nq, 0) * heads, p.Hkv);
+    unsigned char *pool = reinterpret_cast<unsigned char *>(p.k_pool);
+    for (s = next_segment(p, row, s + 1, lane); s >= 0; s = next_segment(p, row, s + 1, lane)) {
+        const Segment sg = load_segment(p.seq_info, s);
+        if (!ask_pages(p, sg, lane)) continue;
+        RopeSlot to;
+        long long place;
+        locate_row(p, sg, row, to, place);
+        for (int h = h0 + sub; h < h1; h += heads) {  // D is a power of two: every lane has columns
+            const unsigned char *a = pool + (from.block * p.Hkv + h) * block;
+            unsigned char *b = pool + (to.block * p.Hkv + h) * block;
+            *reinterpret_cast<unsigned *>(b + to.token * (p.D / 2) + c * 4) = *reinterpret_cast<const unsigned *>(a + from.token * (p.D / 2) + c * 4);
+            if ((c & 1) == 0) b[8 * p.D + to.token * (p.D / 16) + c / 2] = a[8 * p.D + from.token * (p.D / 16) + c / 2];
+        }
+    }
 }
 
 // Write the 4-bit V page `pb` of kv head h from the segment's new rows.
@@ -540,13 +606,12 @@ __global__ void __launch_bounds__(kRopeWarps * 32, sizeof(T) == 2 ? 5 : 4) rope_
     float2 *angles = reinterpret_cast<float2 *>(smem) + warp * 128;                       // cosine and sine of each pair
     float *stage = reinterpret_cast<float *>(smem) + kRopeWarps * 256 + warp * 256;
     const RopeWork work = rope_work<CACHE, PAIR>(p, slice, p.slices, lane);
-    Segment sg{0, 0, 0, 0};
-    bool pages_ok = false;
+    RowSegment seg;
 #pragma unroll 1
     for (int row = row0; row < row1; ++row) {
         RopeSlot slot{0, 0};
         long long place = 0;
-        if (CACHE != kNoCache && !place_row(p, row, sg, pages_ok, slot, place, lane)) continue;
+        if (CACHE != kNoCache && !place_row<CACHE>(p, row, seg, slot, place, lane)) continue;
         if (p.rot_dim) {
             __syncwarp();
             const unsigned pos = (unsigned)(p.positions ? p.positions[row] : (int)place);
@@ -556,6 +621,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, sizeof(T) == 2 ? 5 : 4) rope_
         const T *const rows[3] = {reinterpret_cast<const T *>(p.q) + row * p.q_stride, reinterpret_cast<const T *>(p.k) + row * p.k_stride,
                                   reinterpret_cast<const T *>(p.v) + row * p.v_stride};
         rope_row<T, CACHE, PAIR>(p, row, slot, angles, rows, work, stage, lane);
+        if (CACHE == kFp4 && seg.shared) copy_k4_to_others(p, row, seg.s, slot, work.f0, work.f1, work.nq, lane);
     }
 }
 
