@@ -178,7 +178,8 @@ const char *pkv_status_str(int status);
  * On a PKV_FP4 cache the rows are bf16 and are quantised on the way (this is
  * pkv_norm_rope_append without a pkv_rope and without q).  A byte of its V
  * pages holds two tokens; calls and segments that write different slots of
- * one page at the same time do not disturb each other.
+ * one page, or the same row to one slot, at the same time do not disturb each
+ * other.
  */
 int pkv_append(const pkv_cache *cache, int32_t layer,
                const void *k_new, const void *v_new, int32_t total_rows,

@@ -546,12 +546,12 @@ __device__ __forceinline__ void write_v4_page(const RopeParams &p, const Segment
             } else {
                 // Other tokens of the page may be written at the same time (a
                 // ring's last page is its first one too, another segment goes
-                // on in the page): flip just the bits of these tokens that change.
-                const uint4 o = __ldcg(d);
-                atomicXor(&d->x, (w.x ^ o.x) & mask);
-                atomicXor(&d->y, (w.y ^ o.y) & mask);
-                atomicXor(&d->z, (w.z ^ o.z) & mask);
-                atomicXor(&d->w, (w.w ^ o.w) & mask);
+                // on in the page): only these tokens' bits are cleared and set.  The same
+                // segment twice, as padded batches have it, still leaves its values.
+                atomicAnd(&d->x, ~mask); atomicOr(&d->x, w.x & mask);
+                atomicAnd(&d->y, ~mask); atomicOr(&d->y, w.y & mask);
+                atomicAnd(&d->z, ~mask); atomicOr(&d->z, w.z & mask);
+                atomicAnd(&d->w, ~mask); atomicOr(&d->w, w.w & mask);
             }
         }
     }

@@ -52,6 +52,24 @@ def test_each_segment_gets_k_and_v(pkv, D, segments):
     f.check_guards()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("segments", [
+    [[0, 1, 0, 20]] * 2, [[3, 1, 1, 33], [0, 1, 0, 20]] + [[1, 1, 2, 50]] * 6,    # a padded decode step
+    [[0, 7, 0, 40]] * 3 + [[10, 60, 2, 71]] * 2, [[5, 31, 1, 39], [10, 20, 1, 33], [0, 3, 0, 3]],   # and a piece of a segment again
+])
+def test_the_same_slot_twice_with_the_same_row(pkv, D, segments):
+    w = workload(D, segments, 100)
+    want = None
+    for _ in range(10):
+        f, err = Fp4(pkv, w), pkv.new_err_flags()
+        pkv.append(f.cache, 0, w.k_new[0].cuda(), w.v_new[0].cuda(), w.seq_info.cuda(), err)
+        if want is None:
+            want, e = f.oracle_bytes(w.k_new[0], w.v_new[0])
+        assert int(err.item()) == e == 0
+        for i in (0, 1):
+            assert f.host(i).tobytes() == want[i].tobytes(), "KV"[i]
+
+
 @pytest.mark.parametrize("segments", SEGMENTS)
 @pytest.mark.parametrize("given", [False, True])
 def test_rotated_and_in_place(pkv, segments, given):
