@@ -271,8 +271,9 @@ int pkv_norm_rope(const pkv_rope *rope, int32_t dtype, int32_t head_dim, int32_t
  * in every segment that holds it, turned by positions[row] or by its position
  * in the lowest of them (v_out must not be v then).  Rows no segment covers, and
  * rows of segments that pkv_append would refuse (the same PKV_ERR_* bits), are
- * not written, in none of the outputs.  A later attention call may be launched with
- * PKV_FLAG_PDL behind this one.
+ * not written, in none of the outputs.  A later attention call may be launched
+ * with PKV_FLAG_PDL behind this one, unless one segment's rows are older keys
+ * of another (two pieces of one sequence in a call).
  */
 int pkv_norm_rope_append(const pkv_cache *cache, int32_t layer, const pkv_rope *rope, const pkv_rows *rows,
                          const int32_t *seq_info, int32_t num_segments, int32_t window,
@@ -339,7 +340,8 @@ int pkv_norm_rope_append(const pkv_cache *cache, int32_t layer, const pkv_rope *
  * pkv_attend_workspace_bytes).  PKV_FLAG_SIMT, PKV_FLAG_MMA_SYNC and
  * PKV_FLAG_PREFETCH_NEXT have no effect.  PKV_FLAG_PDL: pages wholly below
  * position kv_end - q_len may be read before the previous kernel has
- * finished, so it may be the append of this step.  (Most 4-bit attention
+ * finished, so it may be the append of this step, unless two segments are
+ * pieces of one sequence.  (Most 4-bit attention
  * launches, and pkv_norm_rope and pkv_norm_rope_append, are programmatic
  * dependent launches without the flag too, which wait for the previous
  * kernel first thing.)

@@ -67,11 +67,18 @@ class DecodeStep:
     as well, three where large bounds share the key ranges; its outputs may be
     bf16 (out_dtype).  The workspace of that merge belongs to the step: a
     capture allocates nothing, and captured steps share no memory.
+
+    pdl lets a layer's attention start before the launch in front of it has
+    finished, and read the sequences' older pages: fused steps (append_attend, no
+    two segments of which may name one column) always do.  With a rope two
+    segments may be pieces of one sequence, and the older pages of one are
+    then written in the same step: by default (None) only a step of one segment
+    starts early; True promises that no segment's rows are older keys of another.
     """
 
     def __init__(self, cache: PagedKVCache, num_q_heads: int, rows: int = 1, num_segments: int = 1,
                  max_q_len: int = 1, max_kv: Optional[int] = None, scale: Optional[float] = None,
-                 causal: bool = False, window: int = 0, fused: bool = True, pdl: bool = True,
+                 causal: bool = False, window: int = 0, fused: bool = True, pdl: Optional[bool] = None,
                  flags: int = 0, num_splits: int = 0, with_lse: bool = False, prefetch_next: bool = True,
                  workspace: bool = False, advance: bool = False,
                  rope: Union[Rope, Sequence[Rope], None] = None, out_dtype: torch.dtype = torch.float32):
@@ -83,7 +90,8 @@ class DecodeStep:
         self.max_kv = int(max_kv if max_kv is not None else cache.bucket)
         self.scale = scale if scale is not None else 1.0 / math.sqrt(D)
         self.causal, self.window = causal, window
-        self.fused, self.pdl, self.flags, self.num_splits = fused, pdl, flags, num_splits
+        self.fused, self.pdl, self.flags, self.num_splits = fused, pdl is None or pdl, flags, num_splits
+        self.rope_pdl = num_segments == 1 if pdl is None else pdl
         self.prefetch_next = prefetch_next
         if out_dtype != torch.float32 and not (out_dtype == torch.bfloat16 and cache.dtype == torch.uint8):
             raise ValueError("out_dtype is float32, or bfloat16 over a 4-bit cache")
@@ -136,18 +144,16 @@ class DecodeStep:
         c = self.cache
         for layer in range(c.num_layers):
             flags = self.flags
-            if self.pdl and layer > 0 and self.fused:
+            if self.rope_pdl if self.rope is not None else self.pdl and layer > 0 and self.fused:
                 flags |= _lib.FLAG_PDL
             if self.prefetch_next and layer + 1 < c.num_layers:
                 flags |= _lib.FLAG_PREFETCH_NEXT  # the next call attends layer + 1 over the same segments
             if self.rope is not None:
                 norm_rope_append(c, layer, self.rope[layer], self.q[layer], self.k_new[layer], self.v_new[layer],
                                  self.seq_info, self.q_rot[layer], self.err, window=self.window, stream=stream)
-                # the kernel before it writes only this step's slots and q_rot: an early start is safe
                 attend_varlen(c, layer, self.q_rot[layer], self.seq_info, self.out[layer], self.err, self.max_q_len,
                               self.max_kv, self.scale, self.causal, self.window, lse=self.lse[layer],
-                              num_splits=self.num_splits, flags=flags | (_lib.FLAG_PDL if self.pdl else 0),
-                              stream=stream, workspace=self.ws)
+                              num_splits=self.num_splits, flags=flags, stream=stream, workspace=self.ws)
             elif self.fused:
                 append_attend(c, layer, self.q[layer], self.k_new[layer], self.v_new[layer], self.seq_info,
                               self.out[layer], self.err, self.max_q_len, self.max_kv, self.scale, self.causal,
