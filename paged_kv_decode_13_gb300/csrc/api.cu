@@ -1,7 +1,7 @@
 // C-ABI entry points of libpkv: argument checks, launch planning and launches.
 // Every entry point validates on the host first and returns a negative
 // pkv_status before launching anything; nothing here allocates memory,
-// synchronises the host or keeps state beyond per-process kernel attributes.
+// synchronises the host or keeps state beyond kernel attributes and occupancy, per device.
 #include <cuda_runtime.h>
 
 #include <cudaTypedefs.h>
@@ -13,6 +13,7 @@
 #include <math.h>
 
 #include "attend4_launch.h"
+#include "kernel_table.h"
 #include "launch.h"
 #include "misc_kernels.cuh"
 #include "rope_launch.h"
@@ -64,20 +65,29 @@ struct Plan {
 
 constexpr int kMaxSplitsGm = 64;  // splits per key range when merging through global memory
 
-// SMs of the current device (GB300's count when no device answers).
-int device_sms() {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
+constexpr int kKernelRoom = 512;  // (kernel, device) pairs whose state is kept
+
+// The current device, or -1 when none answers.
+int current_device() {
+    int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
-        return kDefaultSms;
+        return -1;
     }
-    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    return dev;
+}
+
+// SMs of a device (GB300's count when no device answers).
+int device_sms(int dev) {
+    static std::atomic<int> known[64];
+    int n = 0;
+    if (dev < 0) return kDefaultSms;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         cudaGetLastError();
         return kDefaultSms;
     }
-    if (dev >= 0 && dev < 64 && n > 0) known[dev].store(n, std::memory_order_relaxed);
+    if (dev < 64 && n > 0) known[dev].store(n, std::memory_order_relaxed);
     return n > 0 ? n : kDefaultSms;
 }
 
@@ -113,33 +123,26 @@ AttnKernel pick(int variant, int dp, int rc) {
     return AttnKernel{nullptr, 0, 0, 0, 0, false, false};
 }
 
-// Clusters of c CTAs of this kernel that the device holds at once (c = 1:
-// resident CTAs); cached per kernel and size, 0 when none fits or no device
-// answers the query.
-int active_clusters(const AttnKernel &k, int c) {
+// Clusters of c CTAs of this kernel that the current device `dev` holds at once
+// (c = 1: resident CTAs); kept per kernel, device and size, 0 when none fits or no
+// device answers the query (which is not kept).
+int active_clusters(const AttnKernel &k, int c, int dev) {
+    struct Counts {
+        int n[kMaxCluster + 1];  // one more than the count, 0: not asked
+    };
     static std::mutex mu;
-    static const void *fns[64];
-    static int count[64][kMaxCluster + 1];
-    static int n = 0;
-    if (c < 1 || c > kMaxCluster) return 0;
+    static KernelTable<Counts, kKernelRoom> known;
+    if (c < 1 || c > kMaxCluster || dev < 0) return 0;
     std::lock_guard<std::mutex> lock(mu);
-    int slot = -1;
-    for (int i = 0; i < n; ++i)
-        if (fns[i] == k.fn) slot = i;
-    if (slot < 0 && n < 64) {
-        slot = n++;
-        fns[slot] = k.fn;
-        for (int i = 0; i <= kMaxCluster; ++i) count[slot][i] = -1;
-    }
-    if (slot >= 0 && count[slot][c] >= 0) return count[slot][c];
+    Counts *kept = known.find(k.fn, dev);
+    if (!kept) kept = known.add(k.fn, dev, Counts{});
+    if (kept && kept->n[c]) return kept->n[c] - 1;
     int clusters = 0;
+    cudaError_t e;
     if (c == 1) {
         int per_sm = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.fn, k.threads, k.smem) != cudaSuccess) {
-            cudaGetLastError();
-            per_sm = 0;
-        }
-        clusters = per_sm * device_sms();
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k.fn, k.threads, k.smem);
+        clusters = per_sm * device_sms(dev);
     } else {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)c, 1, 1);
@@ -152,21 +155,22 @@ int active_clusters(const AttnKernel &k, int c) {
         attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&clusters, k.fn, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            clusters = 0;
-        }
+        e = cudaOccupancyMaxActiveClusters(&clusters, k.fn, &cfg);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
     }
     clusters = std::max(clusters, 0);
-    if (slot >= 0) count[slot][c] = clusters;
+    if (kept) kept->n[c] = clusters + 1;
     return clusters;
 }
 
 // Largest cluster size <= want that the device can schedule for this kernel
 // (1 when no device answers the query).
-int schedulable_cluster(const AttnKernel &k, int want) {
+int schedulable_cluster(const AttnKernel &k, int want, int dev) {
     for (int c = want; c > 1; --c)
-        if (active_clusters(k, c) > 0) return c;
+        if (active_clusters(k, c, dev) > 0) return c;
     return 1;
 }
 
@@ -183,11 +187,11 @@ int schedulable_cluster(const AttnKernel &k, int want) {
 // those launches keep `want`.  Kernels that fit twice per SM keep it too:
 // there the second slot holds the next layer's CTAs (programmatic launch),
 // which the wave count does not see.
-int wave_cluster(const AttnKernel &k, long long units, int want) {
-    const int resident = active_clusters(k, 1);
-    if (want <= 1 || units <= 0 || resident > device_sms() || 2 * units > resident) return want;
+int wave_cluster(const AttnKernel &k, long long units, int want, int dev) {
+    const int resident = active_clusters(k, 1, dev);
+    if (want <= 1 || units <= 0 || resident > device_sms(dev) || 2 * units > resident) return want;
     auto waves = [&](int c) {
-        const long long a = active_clusters(k, c);
+        const long long a = active_clusters(k, c, dev);
         return a > 0 ? (units + a - 1) / a : (long long)1 << 40;
     };
     int best = want;
@@ -205,7 +209,7 @@ int wave_cluster(const AttnKernel &k, long long units, int want) {
 }
 
 int make_plan(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_kv, int num_splits,
-              unsigned flags, bool want_gm, Plan *pl) {
+              unsigned flags, bool want_gm, int dev, Plan *pl) {
     int st = check_cache(c);
     if (st) return st;
     if (Hq <= 0 || Hq % c->kv_heads != 0) return PKV_EINVAL;
@@ -241,7 +245,7 @@ int make_plan(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_kv
     if (pl->gm) {
         // independent CTAs: one per SM across the launch (the next layer's
         // CTAs take the second slot of each SM), at least 4 pages each
-        if (n == 0) n = std::min<long long>({(device_sms() + units - 1) / units, std::max<long long>(1, max_pages / 4),
+        if (n == 0) n = std::min<long long>({(device_sms(dev) + units - 1) / units, std::max<long long>(1, max_pages / 4),
                                              (long long)kMaxSplitsGm});
         pl->ncta = (int)std::max<long long>(1, std::min<long long>(n, max_pages));
         return PKV_OK;
@@ -252,7 +256,7 @@ int make_plan(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_kv
         // loads, cluster merge) is worth about 15 groups of 64 keys, and it
         // orders ranges longest first and runs short ones alone instead.
         const long long per_sm = std::max<long long>(1, 232448 / ((long long)pl->k.smem + 1024));
-        const long long target = (long long)(pl->k.tc ? 1 : kTargetWaves) * device_sms() * per_sm;
+        const long long target = (long long)(pl->k.tc ? 1 : kTargetWaves) * device_sms(dev) * per_sm;
         const long long want = (target + units - 1) / units;
         n = 1;
         while (n < want && n < kMaxCluster) n *= 2;
@@ -268,14 +272,13 @@ int make_plan(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_kv
     return PKV_OK;
 }
 
-// Opt a kernel into its dynamic shared memory size and cluster sizes once per process.
-int prepare_kernel(const AttnKernel &k) {
+// Opt a kernel into its dynamic shared memory size and cluster sizes, once per
+// device (the current one, `dev`).
+int prepare_kernel(const AttnKernel &k, int dev) {
     static std::mutex mu;
-    static const void *done[64];
-    static int ndone = 0;
+    static KernelTable<bool, kKernelRoom> done;
     std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < ndone; ++i)
-        if (done[i] == k.fn) return PKV_OK;
+    if (done.find(k.fn, dev)) return PKV_OK;
     // Ask for the largest shared-memory carveout so two CTAs fit on an SM:
     // with programmatic dependent launch the next layer's CTAs can then start
     // streaming their pages beside this layer's.
@@ -286,7 +289,7 @@ int prepare_kernel(const AttnKernel &k) {
         cudaGetLastError();
         return PKV_ECUDA;
     }
-    if (ndone < 64) done[ndone++] = k.fn;
+    done.add(k.fn, dev, true);
     return PKV_OK;
 }
 
@@ -384,46 +387,41 @@ constexpr int kWideFrom = 33;
 
 // Whether the kernel was compiled to the register count its warps hand around
 // (setmaxnreg waits for registers the launch must have brought).
-bool regs_ok(const Attend4Kernel &k) {
+bool regs_ok(const Attend4Kernel &k, int dev) {
     static std::mutex mu;
-    static const void *fn = nullptr;
-    static bool ok = false;
+    static KernelTable<int, 64> known;
     if (!k.regs) return true;
     std::lock_guard<std::mutex> lock(mu);
-    if (fn != k.balance) {
-        cudaFuncAttributes a;
-        if (cudaFuncGetAttributes(&a, k.balance) != cudaSuccess) {
-            cudaGetLastError();
-            return false;
-        }
-        ok = a.numRegs == k.regs;
-        fn = k.balance;
+    if (const int *regs = known.find(k.balance, dev)) return *regs == k.regs;
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, k.balance) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
     }
-    return ok;
+    known.add(k.balance, dev, a.numRegs);
+    return a.numRegs == k.regs;
 }
 
 Attend4Kernel pick4_rows(int head_dim, int rows, bool few) {
     return head_dim == 64 ? pick4_64(rows, few) : head_dim == 128 ? pick4_128(rows, few) : pick4_256(rows, few);
 }
 
-// Clusters of n CTAs that the device holds at once with at most l of the
+// Clusters of n CTAs that the current device `dev` holds at once with at most l of the
 // kernel's CTAs an SM: held[l][n], l up to the CTAs that fit.  Asked once a
-// kernel (with more shared memory for the smaller l).
+// kernel and device (with more shared memory for the smaller l); a guess where no
+// device answers.
 struct Fit4 {
-    const void *fn;
     int held[5][kMaxCluster + 1];
 };
-const Fit4 &fit4(const Attend4Kernel &k) {
+const Fit4 &fit4(const Attend4Kernel &k, int dev) {
     static std::mutex mu;
-    static Fit4 known[16];  // eleven kernels
-    static int n = 0;
+    static KernelTable<Fit4, 256> known;  // eleven kernels
+    static thread_local Fit4 f;
     std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < n; ++i)
-        if (known[i].fn == k.fn) return known[i];
-    Fit4 &f = known[n < 15 ? n++ : 15];
-    f.fn = k.fn;
-    const bool asks = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) == cudaSuccess &&
-                      cudaFuncSetAttribute(k.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    if (const Fit4 *kept = known.find(k.fn, dev)) return *kept;
+    bool all = dev >= 0 && cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) == cudaSuccess &&
+               cudaFuncSetAttribute(k.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    const bool asks = all;
     for (int l = 1; l <= k.ctas; ++l)
         for (int c = 1; c <= kMaxCluster; ++c) {
             cudaLaunchConfig_t cfg = {};
@@ -438,11 +436,13 @@ const Fit4 &fit4(const Attend4Kernel &k) {
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
             if (!asks || cudaOccupancyMaxActiveClusters(&f.held[l][c], k.fn, &cfg) != cudaSuccess) {
-                cudaGetLastError();
-                f.held[l][c] = l * kDefaultSms / c;  // no device answers
+                f.held[l][c] = l * kDefaultSms / c;
+                all = false;
             }
         }
-    return f;
+    if (!all) cudaGetLastError();
+    const Fit4 *kept = all ? known.add(k.fn, dev, f) : nullptr;
+    return kept ? *kept : f;
 }
 
 // What a launch of `units` clusters of n CTAs over `pages` pages each takes
@@ -477,13 +477,13 @@ double cost4(const Attend4Kernel &k, const Fit4 &f, bool few, long long units, l
 }
 
 // CTAs of a range (num_splits, or the cheapest number), their kernel and the cost.
-double split4(Attend4Kernel *k4, int head_dim, int rows, long long units, long long pages, int num_splits, int *ncta) {
+double split4(Attend4Kernel *k4, int head_dim, int rows, long long units, long long pages, int num_splits, int dev, int *ncta) {
     double best = kNever;
     const Attend4Kernel cand[2] = {*k4, pick4_rows(head_dim, rows, true)};
     *ncta = 1;
     for (int few = 0; few < (cand[1].fn == cand[0].fn ? 1 : 2); ++few) {
         const Attend4Kernel &k = cand[few];
-        const Fit4 &f = fit4(k);
+        const Fit4 &f = fit4(k, dev);
         // no more CTAs than leave each of its warps four pages
         const int top = (int)std::max<long long>(1, std::min<long long>(kMaxCluster, pages / (4 * k.warps)));
         for (int n = num_splits ? num_splits : 1; n <= (num_splits ? num_splits : top); ++n) {
@@ -511,9 +511,9 @@ int piece_pages4(const Attend4Kernel &k, int head_dim) {
 // The same of equal shares: `units` ranges (by this kernel's row tiles) of `pages`
 // pages each, pieces and pages read by all SMs at 1.1 times what full SMs take;
 // the second launch and the scan of the segment table cost 10 us (the tcgen05 kernel: 14.5).
-double cost4_shares(const Attend4Kernel &k, int head_dim, long long units, long long pages) {
+double cost4_shares(const Attend4Kernel &k, int head_dim, long long units, long long pages, int dev) {
     return (k.rows == 128 ? 14500 : 10000) +
-           (double)units * (pages + piece_pages4(k, head_dim)) * k.page_ns * k.full * 11 / (200.0 * k.ctas * device_sms());
+           (double)units * (pages + piece_pages4(k, head_dim)) * k.page_ns * k.full * 11 / (200.0 * k.ctas * device_sms(dev));
 }
 
 struct Ws4Layout {
@@ -529,7 +529,7 @@ Ws4Layout ws4_layout(int shares, int rows, int head_dim) {
     return w;
 }
 
-int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_kv, int window, int num_splits, Plan4 *pl) {
+int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_kv, int window, int num_splits, int dev, Plan4 *pl) {
     const int st = check_cache(c, true);
     if (st) return st;
     if (Hq <= 0 || Hq % c->kv_heads != 0) return PKV_EINVAL;
@@ -545,13 +545,13 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     pl->pages = (keys + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE;
     pl->shares = 0;
     pl->ks = pl->k4;
-    const double cost = split4(&pl->k4, c->head_dim, (int)rows, pl->units, pl->pages, num_splits, &pl->ncta);
+    const double cost = split4(&pl->k4, c->head_dim, (int)rows, pl->units, pl->pages, num_splits, dev, &pl->ncta);
     if (num_splits == 0 && S > 0 && S <= kSharesSegments) {
-        if (c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide())) pl->ks = pick4_wide();
+        if (c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide(), dev)) pl->ks = pick4_wide();
         const long long tiles = (rows + pl->ks.rows - 1) / pl->ks.rows;
-        const double shares = cost4_shares(pl->ks, c->head_dim, (long long)S * c->kv_heads * tiles, pl->pages);
+        const double shares = cost4_shares(pl->ks, c->head_dim, (long long)S * c->kv_heads * tiles, pl->pages, dev);
         if (tiles <= kSharesTiles && shares < cost * (100 + kSharesEdge) / 100)
-            pl->shares = std::min(device_sms() * pl->ks.ctas, kMerge4Slots);
+            pl->shares = std::min(device_sms(dev) * pl->ks.ctas, kMerge4Slots);
     }
     return PKV_OK;
 }
@@ -560,7 +560,8 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
             long long max_kv, int num_splits, float scale, int causal, int window, void *out, float *lse, void *workspace,
             long long workspace_bytes, unsigned *err, unsigned flags, void *stream, bool check_only = false) {
     Plan4 pl;
-    int st = make_plan4(c, Hq, S, max_q_len, max_kv, window, num_splits, &pl);
+    const int dev = current_device();
+    int st = make_plan4(c, Hq, S, max_q_len, max_kv, window, num_splits, dev, &pl);
     if (st) return st;
     if ((st = check_layer(c, layer))) return st;
     if (total_rows < 0 || window < 0 || (causal != 0 && causal != 1)) return PKV_EINVAL;
@@ -576,8 +577,8 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     const Attend4Kernel &k4 = shares ? pl.ks : pl.k4;
     const void *fn = shares ? k4.balance : k4.fn;
     const AttnKernel prep{fn, k4.threads, k4.smem, k4.rows, c->head_dim, true, shares && k4.rows == 128};
-    if ((st = prepare_kernel(prep))) return st;
-    const int ncta = S == 0 || shares ? 1 : schedulable_cluster(prep, pl.ncta);
+    if ((st = prepare_kernel(prep, dev))) return st;
+    const int ncta = S == 0 || shares ? 1 : schedulable_cluster(prep, pl.ncta, dev);
     Attend4Params p;
     p.k = reinterpret_cast<const unsigned char *>(c->k[layer]);
     p.v = reinterpret_cast<const unsigned char *>(c->v[layer]);
@@ -717,7 +718,8 @@ int attend_common(const pkv_cache *c, int layer, const void *q, const void *k_ne
                   int *counters = nullptr) {
     if (flags & PKV_FLAG_OUT_BF16) return PKV_EUNSUPPORTED;  // 4-bit caches only
     Plan pl;
-    int st = make_plan(c, Hq, S, max_q_len, max_kv, num_splits, flags, workspace != nullptr, &pl);
+    const int dev = current_device();
+    int st = make_plan(c, Hq, S, max_q_len, max_kv, num_splits, flags, workspace != nullptr, dev, &pl);
     if (st) return st;
     if (workspace && (!aligned16(workspace) || workspace_bytes < 0)) return PKV_EINVAL;
     if ((st = check_layer(c, layer))) return st;
@@ -731,9 +733,9 @@ int attend_common(const pkv_cache *c, int layer, const void *q, const void *k_ne
     const bool gm = pl.gm && S > 0 && pl.ncta > 1;
     const WsLayout wl = ws_layout((long long)S * c->kv_heads * pl.row_tiles, pl.ncta, pl.k.dp);
     if (gm && workspace_bytes < (long long)wl.total) return PKV_EINVAL;
-    if ((st = prepare_kernel(pl.k))) return st;
-    int ncta = S == 0 ? 1 : pl.gm ? pl.ncta : schedulable_cluster(pl.k, pl.ncta);
-    if (S > 0 && !pl.gm && num_splits == 0) ncta = wave_cluster(pl.k, pl.units, ncta);
+    if ((st = prepare_kernel(pl.k, dev))) return st;
+    int ncta = S == 0 ? 1 : pl.gm ? pl.ncta : schedulable_cluster(pl.k, pl.ncta, dev);
+    if (S > 0 && !pl.gm && num_splits == 0) ncta = wave_cluster(pl.k, pl.units, ncta, dev);
 
     AttendParams p;
     // bf16 page tiles come in one box when head_dim fills its padded width
@@ -981,7 +983,7 @@ int pkv_norm_rope(const pkv_rope *rope, int32_t dtype, int32_t head_dim, int32_t
     const int st = rope_params(rope, rows, dtype, head_dim, kv_heads, false, &p);
     if (st) return st;
     if (p.rows == 0) return PKV_OK;
-    return launch_status(launch_rope(p, kNoCache, dtype == PKV_F32, device_sms(), reinterpret_cast<cudaStream_t>(stream)));
+    return launch_status(launch_rope(p, kNoCache, dtype == PKV_F32, device_sms(current_device()), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int pkv_norm_rope_append(const pkv_cache *c, int32_t layer, const pkv_rope *rope, const pkv_rows *rows, const int32_t *seq_info,
@@ -1005,7 +1007,7 @@ int pkv_norm_rope_append(const pkv_cache *c, int32_t layer, const pkv_rope *rope
     p.mbps = c->max_blocks_per_seq;
     p.ring_rows = c->ring_rows;
     p.window = window;
-    return launch_status(launch_rope(p, is_fp4(c) ? kFp4 : kSameType, c->dtype == PKV_F32, device_sms(),
+    return launch_status(launch_rope(p, is_fp4(c) ? kFp4 : kSameType, c->dtype == PKV_F32, device_sms(current_device()),
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1056,7 +1058,7 @@ int pkv_append_attend_noalloc(const pkv_cache *c, int32_t layer, const void *q, 
         // One arrival counter per (segment, kv head, row tile) range: the
         // same count the kernel indexes them by.
         Plan pl;
-        const int st = make_plan(c, Hq, S, max_q_len, max_kv, num_splits, flags, true, &pl);
+        const int st = make_plan(c, Hq, S, max_q_len, max_kv, num_splits, flags, true, current_device(), &pl);
         if (st) return st;
         if (need > kStaticScratchBytes || (long long)S * c->kv_heads * pl.row_tiles > kStaticUnits)
             return PKV_ECAPACITY;  // rejected before any launch
@@ -1074,11 +1076,11 @@ int64_t pkv_attend_workspace_bytes(const pkv_cache *c, int32_t Hq, int32_t S, in
                                    int32_t num_splits, uint32_t flags) {
     if (is_fp4(c)) {  // 4-bit caches merge in the cluster
         Plan4 pl4;
-        const int st = make_plan4(c, Hq, S, max_q_len, max_kv, 0, num_splits, &pl4);
+        const int st = make_plan4(c, Hq, S, max_q_len, max_kv, 0, num_splits, current_device(), &pl4);
         return st ? st : pl4.shares ? (int64_t)ws4_layout(pl4.shares, pl4.ks.rows, c->head_dim).total : 0;
     }
     Plan pl;
-    const int st = make_plan(c, Hq, S, max_q_len, max_kv, num_splits, flags, true, &pl);
+    const int st = make_plan(c, Hq, S, max_q_len, max_kv, num_splits, flags, true, current_device(), &pl);
     if (st) return st;
     if (!pl.gm || S == 0 || pl.ncta <= 1) return 0;
     return (int64_t)ws_layout((long long)S * c->kv_heads * pl.row_tiles, pl.ncta, pl.k.dp).total;
@@ -1114,7 +1116,7 @@ int pkv_seq_clone(const pkv_cache *c, int32_t src_col, int32_t dst_col, int64_t 
         p.src = src_col;
         p.dst = dst_col;
         const long long total = 2LL * p.layers * (n - lo) * row_chunks;
-        const long long blocks = std::max<long long>(1, std::min<long long>((total + 255) / 256, (long long)device_sms() * 8));
+        const long long blocks = std::max<long long>(1, std::min<long long>((total + 255) / 256, (long long)device_sms(current_device()) * 8));
         seq_clone_kernel<<<(unsigned)blocks, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
         if ((st = launch_status(cudaSuccess))) return st;
     }
