@@ -402,7 +402,10 @@ int pkv_append_attend(const pkv_cache *cache, int32_t layer,
  * cluster per range; more than 32 rows per kv head at head_dim 128 then take
  * the tcgen05 tile.  The size does not grow with the lengths and is below 25 MB.
  * It need not be zeroed, and may be shared by calls that
- * follow one another on one stream.
+ * follow one another on one stream.  A call with a window counts
+ * min(max_kv, window + max_q_len) keys in place of max_kv: it uses a workspace where
+ * the query for that many keys asks for one, of the same size, and takes any where the
+ * query for max_kv asks for none.
  */
 int64_t pkv_attend_workspace_bytes(const pkv_cache *cache, int32_t num_q_heads,
                                    int32_t num_segments, int32_t max_q_len,

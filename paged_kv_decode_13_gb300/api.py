@@ -354,6 +354,11 @@ def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Te
 _FP4_WORKSPACE_FROM = 1 << 18
 
 
+def fp4_keys(max_kv: int, max_q_len: int, window: int) -> int:
+    """Keys of a segment at most: the bound that decides how a launch over a 4-bit cache is cut."""
+    return min(max_kv, window + max_q_len) if window > 0 else max_kv
+
+
 def _fp4_workspace(cache, hq, segments, max_q_len, max_kv, window, flags, stream):
     """A workspace for one call over a 4-bit cache, or None: a large launch merges its shared ranges through it.
 
@@ -362,11 +367,11 @@ def _fp4_workspace(cache, hq, segments, max_q_len, max_kv, window, flags, stream
     graphs captured into one pool must not run at the same time, unless their
     calls were given workspaces of their own (DecodeStep keeps one).
     """
-    keys = min(max_kv, window + max_q_len) if window > 0 else max_kv
+    keys = fp4_keys(max_kv, max_q_len, window)
     tiles = -(-hq * max_q_len // (8 * cache._kv_heads))  # of 8 query rows, at most
     if segments * cache._kv_heads * tiles * keys < _FP4_WORKSPACE_FROM:
         return None
-    n = attend_workspace_bytes(cache, hq, segments, max_q_len, max_kv, 0, flags)
+    n = attend_workspace_bytes(cache, hq, segments, max_q_len, keys, 0, flags)
     if n <= 0:
         return None
     if stream is None:

@@ -570,9 +570,15 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     if (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)) return PKV_EINVAL;
     if (S == 0 && total_rows == 0) return PKV_OK;
     if (workspace && (!aligned16(workspace) || workspace_bytes < 0)) return PKV_EINVAL;
-    const bool shares = pl.shares > 0 && workspace;
+    bool shares = pl.shares > 0 && workspace;
     const Ws4Layout wl = ws4_layout(pl.shares, pl.ks.rows, c->head_dim);
-    if (shares && workspace_bytes < (long long)wl.total) return PKV_EINVAL;
+    if (shares && workspace_bytes < (long long)wl.total) {
+        // The size query knows no window.  Where it asks for nothing, any workspace will
+        // do, though shares would pay for the keys that the window leaves.
+        Plan4 whole;
+        if (window == 0 || (st = make_plan4(c, Hq, S, max_q_len, max_kv, 0, num_splits, dev, &whole)) || whole.shares) return PKV_EINVAL;
+        shares = false;
+    }
     if (check_only) return PKV_OK;
     const Attend4Kernel &k4 = shares ? pl.ks : pl.k4;
     const void *fn = shares ? k4.balance : k4.fn;

@@ -18,8 +18,8 @@ from typing import Dict, List, Optional, Sequence, Tuple, Union
 import torch
 
 from . import _lib
-from .api import (PagedKVCache, Rope, append, append_attend, attend_varlen, attend_workspace_bytes, new_err_flags,
-                  norm_rope_append)
+from .api import (PagedKVCache, Rope, append, append_attend, attend_varlen, attend_workspace_bytes, fp4_keys,
+                  new_err_flags, norm_rope_append)
 from .api import advance as advance_lengths
 
 _SHARED_POOL = None
@@ -124,7 +124,8 @@ class DecodeStep:
         """(Re)allocate the split-merge workspace where the current cache and bounds need another size (None: they need none)."""
         fp4, n = self.cache.dtype == torch.uint8, 0
         if self.use_workspace or (fp4 and self.num_splits == 0):
-            n = attend_workspace_bytes(self.cache, self.num_q_heads, int(self.seq_info.shape[0]), self.max_q_len, self.max_kv,
+            keys = fp4_keys(self.max_kv, self.max_q_len, self.window) if fp4 else self.max_kv
+            n = attend_workspace_bytes(self.cache, self.num_q_heads, int(self.seq_info.shape[0]), self.max_q_len, keys,
                                        self.num_splits, self.flags)
         if n <= 0:
             self.ws = None
