@@ -66,6 +66,8 @@ class PagedKVCache:
             if len(shape) != 3 or shape[2] % 9:
                 raise ValueError("4-bit pools are uint8 (num_blocks, kv_heads, 9 * head_dim)")
             kv_heads, head_dim = int(shape[1]), int(shape[2]) // 9
+            if any(t.get_device() != k[0].get_device() for t in [*k, *v, block_table] + ([] if first_valid is None else [first_valid])):
+                raise ValueError("the pools and tables of a 4-bit cache are on one device")
         else:
             if len(shape) != 4 or shape[1] != _lib.BLOCK_SIZE:
                 raise ValueError("pools are (num_blocks, 16, kv_heads, head_dim)")
@@ -315,35 +317,51 @@ def norm_rope_append(cache: PagedKVCache, layer: int, rope: Optional[Rope], q: O
     dev, dtype, dim = cache._device, cache.row_dtype, cache._head_dim
     if rope is not None:
         rope.check(dtype, dim, dev)
-    si = seq_info.shape
-    if seq_info.dtype is not torch.int32 or len(si) != 2 or si[1] != 4 or seq_info.get_device() != dev:
-        raise ValueError(f"seq_info is int32 (segments, 4) on device {dev}")
+    segments = _check_segments(cache, seq_info, err)
     d = _rows_desc(q, k_new, v_new, q if q_out is None else q_out, k_out, v_out, positions, cache._kv_heads, dim, dtype, dev)
     _launch("pkv_norm_rope_append", lib.pkv_norm_rope_append,
-            (cache._ref, layer, None if rope is None else rope._ref, d, _contig(seq_info, "seq_info").data_ptr(), si[0], window, err.data_ptr()),
+            (cache._ref, layer, None if rope is None else rope._ref, d, _contig(seq_info, "seq_info").data_ptr(), segments, window, err.data_ptr()),
             dev, stream)
 
 
-def _check_new(k_new: torch.Tensor, v_new: torch.Tensor) -> None:
-    if k_new.dtype is not torch.bfloat16 or v_new.dtype is not torch.bfloat16 or k_new.shape != v_new.shape:
-        raise ValueError("rows for a 4-bit cache are bf16, k_new and v_new of one shape")
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32  # (short calls are bound by what the host looks up)
 
 
-def _check_fp4(q, k_new, v_new, out, lse) -> None:
+def _check_new(cache: PagedKVCache, rows: int, k_new: torch.Tensor, v_new: torch.Tensor) -> None:
+    """New rows for a 4-bit cache, heads and columns of a row apart or as one dimension."""
+    shape, heads, dim, dev = k_new.shape, cache._kv_heads, cache._head_dim, cache._device
+    if (k_new.dtype is not _BF16 or v_new.dtype is not _BF16 or v_new.shape != shape
+            or (shape != (rows, heads, dim) and shape != (rows, heads * dim)) or k_new.get_device() != dev or v_new.get_device() != dev):
+        raise ValueError(f"rows for a 4-bit cache are bf16, k_new and v_new ({rows}, {heads}, {dim}) on the cache's device")
+
+
+def _check_segments(cache: PagedKVCache, seq_info: torch.Tensor, err: torch.Tensor) -> int:
+    """The segment table and error flags of a call: the number of segments."""
+    shape, dev = seq_info.shape, cache._device
+    if seq_info.dtype is not _I32 or len(shape) != 2 or shape[1] != 4 or seq_info.get_device() != dev or err.get_device() != dev:
+        raise ValueError("seq_info is int32 (segments, 4), and err with it on the cache's device")
+    return shape[0]
+
+
+def _check_fp4(cache: PagedKVCache, q, k_new, v_new, seq_info, out, lse, err) -> None:
     """The tensors of an attention call over a 4-bit cache."""
-    if q.dtype is not torch.bfloat16 or (out.dtype is not torch.float32 and out.dtype is not torch.bfloat16) or out.shape != q.shape:
-        raise ValueError("over a 4-bit cache q is bf16 (rows, heads, head_dim) and out fp32 or bf16 of the same shape")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.numel() != q.shape[0] * q.shape[1]):
-        raise ValueError("lse is fp32 (rows, heads)")
+    shape, kind, dev = q.shape, out.dtype, cache._device
+    if (len(shape) != 3 or shape[2] != cache._head_dim or q.dtype is not _BF16 or (kind is not _F32 and kind is not _BF16) or out.shape != shape
+            or q.get_device() != dev or out.get_device() != dev):
+        raise ValueError(f"over a 4-bit cache q is bf16 (rows, heads, {cache._head_dim}) and out fp32 or bf16 of the same shape, on its device")
+    if lse is not None and (lse.dtype is not _F32 or lse.numel() != shape[0] * shape[1] or not lse.is_contiguous() or lse.get_device() != dev):
+        raise ValueError("lse is fp32 (rows, heads), contiguous, on the cache's device")
+    _check_segments(cache, seq_info, err)
     if k_new is not None:
-        _check_new(k_new, v_new)
+        _check_new(cache, shape[0], k_new, v_new)
 
 
 def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, seq_info: torch.Tensor,
            err: torch.Tensor, window: int = 0, stream=None) -> None:
     rows = int(k_new.shape[0])
     if cache._fp4:
-        _check_new(k_new, v_new)
+        _check_new(cache, rows, k_new, v_new)
+        _check_segments(cache, seq_info, err)
     _lib.check("pkv_append", lib.pkv_append(
         cache.ref(), layer, _ptr(_contig(k_new, "k_new")), _ptr(_contig(v_new, "v_new")), rows,
         _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(window), _ptr(err), _stream(stream)))
@@ -367,7 +385,7 @@ def _fp4_workspace(cache, hq, segments, max_q_len, max_kv, window, flags, stream
     graphs captured into one pool must not run at the same time, unless their
     calls were given workspaces of their own (DecodeStep keeps one).
     """
-    keys = fp4_keys(max_kv, max_q_len, window)
+    keys = max_kv if window <= 0 else fp4_keys(max_kv, max_q_len, window)
     tiles = -(-hq * max_q_len // (8 * cache._kv_heads))  # of 8 query rows, at most
     if segments * cache._kv_heads * tiles * keys < _FP4_WORKSPACE_FROM:
         return None
@@ -384,7 +402,7 @@ def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max
             window, num_splits, flags, stream, workspace):
     shape, segments = q.shape, seq_info.shape[0]
     max_q_len, max_kv, window = int(max_q_len), int(max_kv), int(window)
-    if out.dtype is torch.bfloat16:
+    if out.dtype is _BF16:
         flags |= _lib.FLAG_OUT_BF16
     dev = cache._device  # -1 on the host (a call that is refused)
     if dev >= 0 and dev != torch._C._cuda_getDevice():
@@ -392,9 +410,9 @@ def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max
             return _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max_q_len, max_kv, scale, causal,
                            window, num_splits, flags, stream, workspace)
     if cache._fp4:
-        _check_fp4(q, k_new, v_new, out, lse)
-    if cache._fp4 and workspace is None and num_splits == 0:
-        workspace = _fp4_workspace(cache, shape[1], segments, max_q_len, max_kv, window, flags, stream)
+        _check_fp4(cache, q, k_new, v_new, seq_info, out, lse, err)
+        if workspace is None and num_splits == 0:
+            workspace = _fp4_workspace(cache, shape[1], segments, max_q_len, max_kv, window, flags, stream)
     new = ()
     if fn_name == "pkv_append_attend":
         new = (_contig(k_new, "k_new").data_ptr(), _contig(v_new, "v_new").data_ptr())
@@ -432,7 +450,7 @@ def append_attend_noalloc(cache: PagedKVCache, layer: int, q: torch.Tensor, k_ne
     """pkv_append_attend_noalloc: append_attend merging its splits in the library's fixed scratch."""
     rows, hq = int(q.shape[0]), int(q.shape[1])
     if cache._fp4:
-        _check_fp4(q, k_new, v_new, out, lse)
+        _check_fp4(cache, q, k_new, v_new, seq_info, out, lse, err)
     if out.dtype == torch.bfloat16:
         flags |= _lib.FLAG_OUT_BF16
     _lib.check("pkv_append_attend_noalloc", lib.pkv_append_attend_noalloc(
