@@ -281,6 +281,14 @@ def _launch(name: str, fn, args, device: int, stream) -> None:
         _lib.check(name, st)
 
 
+def _on_device(device: int, name: str, fn, args, stream, allowed=(_lib.OK,)) -> int:
+    """The status of fn(*args, stream) with `device` current; with the current one where it is -1 (host memory)."""
+    if device < 0 or device == torch._C._cuda_getDevice():
+        return _lib.check(name, fn(*args, _stream(stream)), allowed)
+    with torch.cuda.device(device):
+        return _lib.check(name, fn(*args, _stream(stream)), allowed)
+
+
 def norm_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
               q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None) -> None:
     """pkv_norm_rope: norm and rotation of rows that go to no cache.
@@ -362,9 +370,9 @@ def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Te
     if cache._fp4:
         _check_new(cache, rows, k_new, v_new)
         _check_segments(cache, seq_info, err)
-    _lib.check("pkv_append", lib.pkv_append(
+    _on_device(cache._device, "pkv_append", lib.pkv_append, (
         cache.ref(), layer, _ptr(_contig(k_new, "k_new")), _ptr(_contig(v_new, "v_new")), rows,
-        _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(window), _ptr(err), _stream(stream)))
+        _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(window), _ptr(err)), stream)
 
 
 # Bounds (segments x kv heads x row tiles x keys) from which a launch over a 4-bit cache
@@ -453,18 +461,22 @@ def append_attend_noalloc(cache: PagedKVCache, layer: int, q: torch.Tensor, k_ne
         _check_fp4(cache, q, k_new, v_new, seq_info, out, lse, err)
     if out.dtype == torch.bfloat16:
         flags |= _lib.FLAG_OUT_BF16
-    _lib.check("pkv_append_attend_noalloc", lib.pkv_append_attend_noalloc(
+    _on_device(cache._device, "pkv_append_attend_noalloc", lib.pkv_append_attend_noalloc, (
         cache.ref(), layer, _ptr(_contig(q, "q")), _ptr(_contig(k_new, "k_new")), _ptr(_contig(v_new, "v_new")),
         hq, rows, _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(max_q_len), int(max_kv),
         int(num_splits), float(scale), int(bool(causal)), int(window), _ptr(_contig(out, "out")), _ptr(lse),
-        _ptr(err), int(flags), _stream(stream)))
+        _ptr(err), int(flags)), stream)
 
 
 def attend_workspace_bytes(cache: PagedKVCache, num_q_heads: int, num_segments: int, max_q_len: int, max_kv: int,
                            num_splits: int = 0, flags: int = 0) -> int:
     """pkv_attend_workspace_bytes: workspace the attention calls need for these bounds (0: none)."""
-    n = int(lib.pkv_attend_workspace_bytes(cache.ref(), int(num_q_heads), int(num_segments), int(max_q_len),
-                                           int(max_kv), int(num_splits), int(flags)))
+    args = (cache.ref(), int(num_q_heads), int(num_segments), int(max_q_len), int(max_kv), int(num_splits), int(flags))
+    if cache._device < 0 or cache._device == torch._C._cuda_getDevice():
+        n = int(lib.pkv_attend_workspace_bytes(*args))
+    else:
+        with torch.cuda.device(cache._device):
+            n = int(lib.pkv_attend_workspace_bytes(*args))
     if n < 0:
         _lib.check("pkv_attend_workspace_bytes", n)
     return n
@@ -479,33 +491,31 @@ def new_workspace(cache: PagedKVCache, num_q_heads: int, num_segments: int, max_
 
 def seq_clone(cache: PagedKVCache, src_col: int, dst_col: int, n: int, err: torch.Tensor, stream=None) -> None:
     """pkv_seq_clone: copy positions 0..n-1 of block-table row src_col to dst_col in every layer."""
-    _lib.check("pkv_seq_clone", lib.pkv_seq_clone(cache.ref(), int(src_col), int(dst_col), int(n), _ptr(err),
-                                                  _stream(stream)))
+    _on_device(cache._device, "pkv_seq_clone", lib.pkv_seq_clone, (cache.ref(), int(src_col), int(dst_col), int(n), _ptr(err)), stream)
 
 
 def rewind(cache: PagedKVCache, seq_info: torch.Tensor, amount: torch.Tensor, err: torch.Tensor, window: int = 0,
            stream=None) -> None:
     """pkv_rewind: kv_end -= amount per segment on the device, bounded by the ring floor."""
-    _lib.check("pkv_rewind", lib.pkv_rewind(cache.ref(), _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]),
-                                            _ptr(_contig(amount, "amount")), int(window), _ptr(err),
-                                            _stream(stream)))
+    _on_device(cache._device, "pkv_rewind", lib.pkv_rewind, (cache.ref(), _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]),
+                                                            _ptr(_contig(amount, "amount")), int(window), _ptr(err)), stream)
 
 
 def seqinfo_from_seqused(cu_seqlens_q: torch.Tensor, seqused_k: torch.Tensor, out: torch.Tensor,
                          stream=None) -> None:
     n = int(seqused_k.shape[0])
-    _lib.check("pkv_seqinfo_from_seqused", lib.pkv_seqinfo_from_seqused(
-        _ptr(cu_seqlens_q), _ptr(seqused_k), n, _ptr(out), _stream(stream)))
+    _on_device(out.get_device(), "pkv_seqinfo_from_seqused", lib.pkv_seqinfo_from_seqused,
+               (_ptr(cu_seqlens_q), _ptr(seqused_k), n, _ptr(out)), stream)
 
 
 def advance(seq_info: torch.Tensor, stream=None) -> None:
-    _lib.check("pkv_advance", lib.pkv_advance(_ptr(seq_info), int(seq_info.shape[0]), _stream(stream)))
+    _on_device(seq_info.get_device(), "pkv_advance", lib.pkv_advance, (_ptr(seq_info), int(seq_info.shape[0])), stream)
 
 
 def resize_bucket(old: PagedKVCache, new: PagedKVCache, old_len: int, stream=None) -> int:
     """Copy the first old_len tokens of every layer; bumps new.generation on success."""
-    st = _lib.check("pkv_resize_bucket", lib.pkv_resize_bucket(old.ref(), new.ref(), int(old_len),
-                                                                 _stream(stream)), (_lib.OK, _lib.SAME_BUCKET))
+    st = _on_device(new._device, "pkv_resize_bucket", lib.pkv_resize_bucket, (old.ref(), new.ref(), int(old_len)), stream,
+                    (_lib.OK, _lib.SAME_BUCKET))
     new.generation = int(new.desc.generation)
     return st
 
@@ -524,13 +534,13 @@ def load_prefix(cache: PagedKVCache, keys: Sequence[torch.Tensor], values: Seque
             raise ValueError("all prefix tensors need the same shape, strides and dtype")
     kp = (ctypes.c_void_p * len(keys))(*[t.data_ptr() for t in keys])
     vp = (ctypes.c_void_p * len(values))(*[t.data_ptr() for t in values])
-    st = lib.pkv_load_prefix(cache.ref(), ctypes.cast(kp, ctypes.c_void_p), ctypes.cast(vp, ctypes.c_void_p), n,
-                             ss, sh, _stream(stream))
-    return _lib.check("pkv_load_prefix", st, (_lib.OK, _lib.EMPTY)) == _lib.OK
+    st = _on_device(cache._device, "pkv_load_prefix", lib.pkv_load_prefix,
+                    (cache.ref(), ctypes.cast(kp, ctypes.c_void_p), ctypes.cast(vp, ctypes.c_void_p), n, ss, sh), stream, (_lib.OK, _lib.EMPTY))
+    return st == _lib.OK
 
 
 def to_contiguous(cache: PagedKVCache, layer: int, n: int, keys_out: torch.Tensor, values_out: torch.Tensor,
                   stream=None) -> None:
     """keys_out / values_out: contiguous [kv_heads, n, head_dim]."""
-    _lib.check("pkv_to_contiguous", lib.pkv_to_contiguous(cache.ref(), layer, int(n), _ptr(keys_out),
-                                                          _ptr(values_out), _stream(stream)))
+    _on_device(cache._device, "pkv_to_contiguous", lib.pkv_to_contiguous, (cache.ref(), layer, int(n), _ptr(keys_out), _ptr(values_out)),
+               stream)
