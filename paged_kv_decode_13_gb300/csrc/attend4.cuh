@@ -14,8 +14,9 @@
 // with fp16 mma.sync and fp32 accumulation.  K and V values are exact in fp16
 // (fp4.cuh), and a bf16 query row, scaled by the power of two that brings its
 // largest value to [2^14, 2^15), is exact in fp16 down to 2^-31 of that value, so the
-// scores are those of the stored values to fp32.  P is rounded to fp16 (2^-11
-// relative at most, an eighth of the rounding of a bf16 output).
+// scores are those of the stored values to fp32.  P is rounded to fp16: by
+// at most 2^-11 of itself (an eighth of the rounding of a bf16 output), or, where it is
+// below 2^-21 of its row's largest weight, by at most 2^-32 of that.
 //
 // The lanes read codes in fragment order (fp4.cuh), so a page costs four 16-byte
 // and a few narrow shared loads a lane, a conversion (two values) and one fp16
@@ -50,7 +51,12 @@ namespace pkv {
 
 constexpr int kWaitProbes4 = 1 << 20;  // probes of one barrier phase before PKV_ERR_TIMEOUT
 constexpr float kNoMax = -1e30f;       // reference maximum of a row that has seen no key
-constexpr float kLazy4 = 8.f;          // a row's reference maximum moves when a score passes it by 2^8
+// Weights are 2^(score - reference).  A row's reference is set 7 below the score
+// that moves it, and moves again when a score passes it by 15: the largest weight
+// is then between 2^7 and 2^15, within fp16, and weights down to 2^-21 of 2^7 are normal
+// numbers of it (set at the score itself, those below 2^-25 of the largest would vanish from
+// the product with V while the sum still counts them).
+constexpr float kLift4 = 7.f, kLazy4 = 15.f;
 
 template <int D_, int NT_, int KW_, int NST_, int PP_, int CTAS_, bool QSH_>
 struct Cfg4 {
@@ -87,7 +93,7 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], unsigned a0, unsign
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// 2^x for x <= about 8; results below fp32's normal range are zero.
+// 2^x for x <= about 15; results below fp32's normal range are zero.
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -416,7 +422,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
         }
         // Online softmax (base 2) with a lazy maximum: this lane has tokens g,
         // g + 8 of rows 2t, 2t + 1.  x = score - reference; the reference moves
-        // only when some x passes 2^kLazy4.
+        // only when some x passes kLazy4.
         const bool inside = pages == PP && pos_first >= lo_in && pos_first + (PP - 1) * KW * kPage + kPage <= hi_in;
         unsigned pb[PP][NT][2];
 #pragma unroll
@@ -445,7 +451,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                     for (int e = 0; e < PP; ++e)
 #pragma unroll
                         for (int o = 0; o < 4; o += 2)
-                            if (x[e][i + o] != -CUDART_INF_F) mx = fmaxf(mx, sa[e][nt][i + o] * sc[nt][i]);
+                            if (x[e][i + o] != -CUDART_INF_F) mx = fmaxf(mx, fmaf(sa[e][nt][i + o], sc[nt][i], -kLift4));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                     const float al = ex2(m_r[nt][i] - mx);

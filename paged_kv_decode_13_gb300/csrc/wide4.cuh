@@ -418,7 +418,7 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
                 }
                 const bool grow = mx > m + kLazy4;
                 if (__any_sync(0xffffffffu, grow)) {
-                    const float m_new = grow ? mx : m, alpha = ex2(m - m_new);
+                    const float m_new = grow ? mx - kLift4 : m, alpha = ex2(m - m_new);
                     if (j > 0 && __any_sync(0xffffffffu, grow && m != kNoMax)) {
                         // O_half holds P V up to the group before against the old reference
                         if (!wait_bar(pv_done + (J - 1) % NB, ((J - 1) / NB) & 1)) { timed_out = true; break; }
