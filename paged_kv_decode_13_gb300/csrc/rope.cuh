@@ -107,13 +107,29 @@ __device__ __forceinline__ int segment_of_row(const RopeParams &p, int row, int 
     return next_segment(p, row, 0, lane);
 }
 
+// Whether segments may share rows (the whole CTA asks): not where each begins at or past the end of the one
+// before it, with empty ones only at the table's end, as steps mostly have
+// them.  Asked once a CTA of a long table (place_row knows of a short one): a warp that asks for
+// each segment (shares_rows) took 8 us of 53 for 4096 tokens of as many sequences.
+__device__ __forceinline__ bool may_share_rows(const RopeParams &p) {
+    if (p.S <= 32) return false;
+    bool odd = false;
+#pragma unroll 4
+    for (int t = threadIdx.x + 1; t < p.S; t += kRopeWarps * 32) {
+        const Segment a = load_segment(p.seq_info, t - 1), b = load_segment(p.seq_info, t);
+        odd |= b.ql > 0 && (a.ql <= 0 || b.q0 < (long long)a.q0 + a.ql);
+    }
+    return __syncthreads_or(odd);
+}
+__device__ __forceinline__ bool overlap(const Segment &a, const Segment &b) {
+    return a.q0 < (long long)b.q0 + b.ql && b.q0 < (long long)a.q0 + a.ql;
+}
 // Whether a segment but s has a row of sg, segment s (the whole warp asks).
 __device__ __forceinline__ bool shares_rows(const RopeParams &p, const Segment &sg, int s, int lane) {
     bool any = false;
 #pragma unroll 4
     for (int t = lane; t < p.S; t += 32) {
-        const Segment o = load_segment(p.seq_info, t);
-        any |= t != s && o.q0 < (long long)sg.q0 + sg.ql && sg.q0 < (long long)o.q0 + o.ql;
+        any |= t != s && overlap(load_segment(p.seq_info, t), sg);
     }
     return __any_sync(0xffffffffu, any);
 }
@@ -316,7 +332,8 @@ struct RowSegment {
     Segment sg{0, 0, 0, 0};
     int s = 0;             // its index, where `shared`
     bool pages_ok = false;
-    bool shared = false;   // 4-bit caches: other segments have some of its rows
+    bool may_share = false;  // 4-bit caches: segments of this table may share rows
+    bool shared = false;     // and others have some of this one's
 };
 __device__ __forceinline__ void locate_row(const RopeParams &p, const Segment &sg, int row, RopeSlot &slot, long long &place) {
     place = (long long)sg.kend - sg.ql + (row - sg.q0);
@@ -336,14 +353,29 @@ __device__ __forceinline__ bool ask_pages(const RopeParams &p, const Segment &sg
 template <int CACHE>
 __device__ __forceinline__ bool place_row(const RopeParams &p, int row, RowSegment &c, RopeSlot &slot, long long &place, int lane) {
     if (c.shared || !(c.sg.q0 <= row && (long long)row < (long long)c.sg.q0 + c.sg.ql)) {
-        const int s = segment_of_row(p, row, lane);
         c.shared = false;
-        if (s < 0) {
-            c.sg.ql = 0;
-            return false;
+        if (CACHE == kFp4 && p.S <= 32) {  // a lane has a segment: one load answers both questions
+            const Segment o = load_segment(p.seq_info, min(lane, p.S - 1));
+            const unsigned m = __ballot_sync(0xffffffffu, lane < p.S && holds_row(p, o, row));
+            if (!m) {
+                c.sg.ql = 0;
+                return false;
+            }
+            const int s = __ffs(m) - 1;
+            c.sg.q0 = __shfl_sync(0xffffffffu, o.q0, s);
+            c.sg.ql = __shfl_sync(0xffffffffu, o.ql, s);
+            c.sg.col = __shfl_sync(0xffffffffu, o.col, s);
+            c.sg.kend = __shfl_sync(0xffffffffu, o.kend, s);
+            c.shared = __any_sync(0xffffffffu, lane < p.S && lane != s && overlap(o, c.sg));
+        } else {
+            const int s = segment_of_row(p, row, lane);
+            if (s < 0) {
+                c.sg.ql = 0;
+                return false;
+            }
+            c.sg = load_segment(p.seq_info, s);
+            if (CACHE == kFp4 && c.may_share) c.shared = shares_rows(p, c.sg, s, lane);
         }
-        c.sg = load_segment(p.seq_info, s);
-        if (CACHE == kFp4 && p.S > 1) c.shared = shares_rows(p, c.sg, s, lane);
         if (c.shared) {
             c.pages_ok = false;
 #pragma unroll 1
@@ -595,6 +627,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, sizeof(T) == 2 ? 5 : 4) rope_
         write_v4_pages(p, (long long)(blockIdx.x - p.row_ctas) * kRopeWarps + warp, smem + (size_t)warp * kPage * (p.D + p.D / 16), lane);
         return;
     }
+    RowSegment seg;
+    if (CACHE == kFp4) seg.may_share = may_share_rows(p);
     if (CACHE != kNoCache && blockIdx.x == 0) report_segments(p);
     // Few rows: `slices` warps share a row's heads.  Many: a warp takes rows of
     // its own, one after the other, and looks their segment up once.
@@ -606,7 +640,6 @@ __global__ void __launch_bounds__(kRopeWarps * 32, sizeof(T) == 2 ? 5 : 4) rope_
     float2 *angles = reinterpret_cast<float2 *>(smem) + warp * 128;                       // cosine and sine of each pair
     float *stage = reinterpret_cast<float *>(smem) + kRopeWarps * 256 + warp * 256;
     const RopeWork work = rope_work<CACHE, PAIR>(p, slice, p.slices, lane);
-    RowSegment seg;
 #pragma unroll 1
     for (int row = row0; row < row1; ++row) {
         RopeSlot slot{0, 0};

@@ -70,6 +70,28 @@ def test_the_same_slot_twice_with_the_same_row(pkv, D, segments):
             assert f.host(i).tobytes() == want[i].tobytes(), "KV"[i]
 
 
+ONE_EACH = [[2 * i, 2, i % 5, 10 + 3 * i] for i in range(45)]
+LONG_TABLES = [
+    ONE_EACH, ONE_EACH[::-1], ONE_EACH + [[0, 0, 0, 0]] * 60,                  # in order, backwards, padded behind
+    [[0, 0, 0, 0]] * 3 + ONE_EACH, ONE_EACH + [[0, 0, 0, 0], [20, 2, 4, 3]],  # empty ones in front of others, one of which shares
+    ONE_EACH[:40] + [[79, 3, 4, 6]], [[0, 90, 3, 95]] + ONE_EACH[:3] + ONE_EACH[4::5],   # the last row again; one segment over all
+    [[-1, 2, 0, 9], [5, -3, 1, 9]] + ONE_EACH + [[2, 99, 1, 120], [88, 4, 3, 150]],   # refused ones
+]
+
+
+@pytest.mark.parametrize("segments", LONG_TABLES)
+def test_long_tables(pkv, segments):
+    """More segments than a warp has lanes, sharing rows or not, in any order."""
+    w = workload(64, segments, 100)
+    f, err = Fp4(pkv, w), pkv.new_err_flags()
+    pkv.append(f.cache, 0, w.k_new[0].cuda(), w.v_new[0].cuda(), w.seq_info.cuda(), err)
+    want, e = f.oracle_bytes(w.k_new[0], w.v_new[0])
+    assert int(err.item()) == e >> 1
+    for i in (0, 1):
+        assert f.host(i).tobytes() == want[i].tobytes(), "KV"[i]
+    f.check_guards()
+
+
 @pytest.mark.parametrize("segments", SEGMENTS)
 @pytest.mark.parametrize("given", [False, True])
 def test_rotated_and_in_place(pkv, segments, given):
