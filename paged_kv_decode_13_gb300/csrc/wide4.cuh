@@ -398,13 +398,14 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
                 tc_fence_after();
                 float x[32];
                 tmem_ld32(tmem + lane_off + b * 64 + half * 32, x);
-                const int pos0 = (w.page0 + j * PG) * kPage + half * 32;
+                // (unsigned: a group's missing last pages may lie past 2^31)
+                const unsigned pos0 = (unsigned)(w.page0 + j * PG) * kPage + half * 32, lo_u = lo_r, hi_u = hi_k;
                 // Key bounds per score only where some real row of the warp does not see all 32.
-                if (!__all_sync(0xffffffffu, !real || (pos0 >= lo_r && pos0 + 32 <= hi_k))) {
+                if (!__all_sync(0xffffffffu, !real || (pos0 >= lo_u && pos0 + 32 <= hi_u))) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        const int pos = pos0 + (k & 16) + 2 * ((k & 15) >> 2) + (k & 1) + 8 * ((k >> 1) & 1);  // the token at column k
-                        if (pos < lo_r || pos >= hi_k) x[k] = -CUDART_INF_F;
+                        const unsigned pos = pos0 + (k & 16) + 2 * ((k & 15) >> 2) + (k & 1) + 8 * ((k >> 1) & 1);  // the token at column k
+                        if (pos < lo_u || pos >= hi_u) x[k] = -CUDART_INF_F;
                     }
                 }
                 float mx;
