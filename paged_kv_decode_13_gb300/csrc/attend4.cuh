@@ -301,7 +301,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
         // Pages wholly below this step's rows are in the cache already, whatever
         // the kernel before this one still writes.
 #pragma unroll 1
-        for (; issued < NST && issued < stages && (cb0 + kw + (issued * PP + PP - 1) * KW + 1) * kPage <= new_start; ++issued) issue(issued);
+        for (; issued < NST && issued < stages && cb0 + kw + (issued * PP + PP - 1) * KW < new_start / kPage; ++issued) issue(issued);
         depend4(p, true);
     }
 #pragma unroll 1
