@@ -686,17 +686,18 @@ __global__ void __launch_bounds__(C::kThreads, 1) verify_kernel(const __grid_con
             tc_fence_after();
             float x[32];
             tmem_ld32(tmem + lane_off + b * 64 + half * 32, x);
-            const int pos0 = lo_pos + j * PG * kPage + half * 32;
+            // (unsigned: a group's missing last pages may lie past 2^31)
+            const unsigned pos0 = (unsigned)lo_pos + j * PG * kPage + half * 32, row_lo = lo_r, row_hi = hi_r;
             // Key bounds per score only where some real row of the warp
             // does not see all 32 keys (padding rows are never written out).
-            if (__all_sync(0xffffffffu, r >= rows_here || (pos0 >= lo_r && pos0 + 32 <= hi_r))) {
+            if (__all_sync(0xffffffffu, r >= rows_here || (pos0 >= row_lo && pos0 + 32 <= row_hi))) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k] *= p.scale_log2;
             } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
-                    const int pos = pos0 + k;
-                    x[k] = (pos >= lo_r && pos < hi_r) ? x[k] * p.scale_log2 : -CUDART_INF_F;
+                    const unsigned pos = pos0 + k;
+                    x[k] = (pos >= row_lo && pos < row_hi) ? x[k] * p.scale_log2 : -CUDART_INF_F;
                 }
             }
             float mx;
