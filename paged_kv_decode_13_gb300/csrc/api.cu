@@ -501,9 +501,10 @@ double split4(Attend4Kernel *k4, int head_dim, int rows, long long units, long l
 
 // What a piece of a range costs a CTA of equal shares besides its pages (query rows in,
 // first pages, partials out), in pages: CTAs are dealt equal sums of both.
-// The batch of 32 uneven sequences (8 rows, head_dim 128) took 60 us with 24
-// pages, uneven 16-row tiles of head_dim 256 (16 sequences up to 4096 keys) 67 us
-// with 12, the tcgen05 kernel's drafts of 16 sequences 82, 72, 73 us with 10, 36, 24.
+// The batch of 32 uneven sequences (8 rows, head_dim 128) takes 77, 63, 58 us with
+// 0, 12, 24 pages; uneven 16-row tiles of head_dim 256 (16 sequences up to 4096 keys) took 67 us
+// with 12 and 43 with 50, the tcgen05 kernel's drafts of 16 sequences 82, 72, 73 us with 10, 36, 24
+// (69 now).
 int piece_pages4(const Attend4Kernel &k, int head_dim) {
     return k.rows == 128 ? 36 : k.rows == 8 ? (56 << 10) / (2 * block4_bytes(head_dim)) : kPieceTile;
 }
@@ -1080,7 +1081,7 @@ int pkv_append_attend_noalloc(const pkv_cache *c, int32_t layer, const void *q, 
 
 int64_t pkv_attend_workspace_bytes(const pkv_cache *c, int32_t Hq, int32_t S, int32_t max_q_len, int64_t max_kv,
                                    int32_t num_splits, uint32_t flags) {
-    if (is_fp4(c)) {  // 4-bit caches merge in the cluster
+    if (is_fp4(c)) {  // equal shares merge through it, clusters need none
         Plan4 pl4;
         const int st = make_plan4(c, Hq, S, max_q_len, max_kv, 0, num_splits, current_device(), &pl4);
         return st ? st : pl4.shares ? (int64_t)ws4_layout(pl4.shares, pl4.ks.rows, c->head_dim).total : 0;

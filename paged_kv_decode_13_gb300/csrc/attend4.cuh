@@ -753,7 +753,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas) attend4_kernel(const __
 // With a workspace the ranges (one (kv head, row tile) each) are laid end to end, each
 // as long as its pages and a few more for what a piece costs besides them (its
 // first loads and its merge, about 4 us: short ranges would else make the
-// CTAs that hold many of them late, 73 us against 50 on 32 sequences of up to
+// CTAs that hold many of them late, 77 us against 58 on 32 sequences of up to
 // 16384 keys).  The one wave of CTAs the device holds takes equal shares of
 // the total T: CTA i [i T / N, (i + 1) T / N).  A range that one CTA holds whole is
 // written at once; of a range that several share, each leaves its rows and

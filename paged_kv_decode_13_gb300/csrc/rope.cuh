@@ -17,22 +17,25 @@
 // Small calls are a launch: one token of 32 + 8 + 8 heads 4.1 us, 256 tokens 7.0 us.
 // Long ones should be bound by HBM and are bound by issue and latency: 16,400
 // tokens of 32 + 8 + 8 heads of 128 (330 MB), norm and half the head rotated,
-// 77 us, 4.3 TB/s, against 49 us at the rate of a copy; 2,800 instructions a token
-// (convert, square, scale, rotate, round: about 10 a value pair with packed
-// fp32) keep the schedulers 52 % busy, at 20 warps an SM (96 registers).  Three
+// 76 us, 4.3 TB/s, against 49 us at the rate of a copy; 2,800 instructions a token
+// keep the schedulers 52 % busy, at 20 warps an SM (96 registers): four heads are
+// loaded together but handled one behind the other, each a chain of a sum, shuffles and a
+// root.  Three
 // heads' loads in flight or six, more warps with fewer registers, prefetches,
 // loads rolling from row to row (85 us) and a version fed by bulk copies through shared memory (95 us) were slower.
 //
-// Angles: turn_i = frequency / 2 pi as a 64-bit fraction of a turn.  position *
-// turn_i, taken modulo 2^64, is the exact fractional turn to 2^-33 at any
-// 32-bit position; sinpif / cospif of its top 32 bits need no range reduction.
+// Angles: turn_i = frequency / 2 pi as a 64-bit fraction of a turn, formed in
+// double: off by at most 2^-55 of a turn a position for frequencies up to 1.  position *
+// turn_i modulo 2^64 is its exact product, whose top 32 bits (2^-32) become a
+// float of half turns (2^-26 of a turn) that sinpif / cospif take as it is: the angle
+// is off by |position| 2^-55 + 2^-25.9 of a turn.
 // (A float product pos * freq is off by 0.008 rad at position 131072.)
 //
 // The 4-bit cache stores V by token pairs, two tokens to a byte, so its V pages
 // are written by page: a warp takes one (segment, kv head, page), gathers the
 // page's new rows and merges their nibbles into the old ones.  K needs no
 // merge (a byte is two columns of one token) and is quantised by the row warps.
-// 16,600 tokens of 8 heads of 128: 50 us, 24 at the rate of a copy: the quantiser's
+// 16,600 tokens of 8 heads of 128: 49 us, 24 at the rate of a copy: the quantiser's
 // instructions (maximum, scale, eight products rounded to codes, the byte
 // exchange; 46 % of issue slots) and its shuffles' latency bound it.  A page's
 // rows are loaded together first (loads one by one behind the stores: 98 us).
@@ -177,10 +180,11 @@ struct Raw8 {
 // hold one).  Returns the codes; stored: x becomes the stored values.
 //
 // x / s: s has 4 significant bits and x 8, so the quotient is either exactly
-// on a border between two codes (a multiple of 1/4) or at least 2^-8 of it
-// away.  x * (1 / s), whose error is below 2^-21, rounded to a multiple of
-// 2^-11 by adding and taking off 3 * 2^11, is therefore on the same side, and
-// exactly on the border where x / s is: the code is that of the exact quotient.
+// on a border b between two codes (a multiple of 1/4) or at least b 2^-8 away from
+// it, 2^-10 at the lowest, 1/4.  x * (1 / s), whose error is below 2^-21 of it, is rounded to a
+// multiple of 2^-11 by adding and taking off 3 * 2^11, which moves it by at most 2^-12: it
+// stays on the same side, and is exactly on the border where x / s is.  The code
+// is that of the exact quotient.
 __device__ __forceinline__ unsigned quantise8(Raw8<__nv_bfloat16> &x, unsigned &scale, bool stored) {
     __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&x.w[0]));
 #pragma unroll
