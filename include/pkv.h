@@ -219,7 +219,15 @@ int pkv_rope_turns(const double *inv_freq, int32_t n, uint64_t *turns);
  *   (u, w) -> mscale * (u cos a_i - w sin a_i, w cos a_i + u sin a_i)
  * for column pairs (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved.
  * All in fp32, rounded once at the end.  Host struct, device pointers.
+ *
+ * num_axes > 1: a row has a position on each of several axes (time, height
+ * and width of images and video; at most PKV_ROPE_AXES), positions is
+ * [total_rows][num_axes], and pair i is turned by the position on axis[i]
+ * (axis: device, values below num_axes; a larger one counts as the last axis).
+ * A row without positions, in norm + append, has its cache position on all of them.
+ * num_axes 0 or 1 with axis NULL: one axis.
  */
+#define PKV_ROPE_AXES 8
 typedef struct pkv_rope {
     const uint64_t *turns;      /* device [rot_dim / 2], from pkv_rope_turns; unread if rot_dim is 0 */
     int32_t rot_dim;            /* even, 0 (no rotation) .. head_dim */
@@ -228,6 +236,9 @@ typedef struct pkv_rope {
     float eps;
     const void *q_weight;       /* device [head_dim] of the rows' type (16-byte aligned), or NULL: q is not normalised */
     const void *k_weight;       /* the same for k */
+    const uint8_t *axis;        /* device [rot_dim / 2], or NULL: one axis */
+    int32_t num_axes;           /* positions of a row; 0 counts as 1 */
+    int32_t reserved0;
 } pkv_rope;
 
 /*
@@ -244,7 +255,7 @@ typedef struct pkv_rows {
     int64_t q_out_stride, k_out_stride, v_out_stride;
     int32_t q_heads;
     int32_t total_rows;
-    const int32_t *positions;   /* device [total_rows], the angles' positions, or NULL */
+    const int32_t *positions;   /* device [total_rows][num_axes], the angles' positions, or NULL */
 } pkv_rows;
 
 /*

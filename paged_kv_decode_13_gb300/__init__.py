@@ -10,5 +10,5 @@ from ._lib import (BF16, BLOCK_SIZE, ERR_BLOCK, ERR_CAPACITY, ERR_OVERLAP, ERR_Q
 from .api import (PagedKVCache, Rope, advance, append, append_attend, append_attend_noalloc,  # noqa: F401
                   attend_varlen, attend_workspace_bytes,
                   bucket_for, load_prefix, new_err_flags, new_workspace, norm_rope, norm_rope_append,
-                  resize_bucket, rewind, rope_inv_freq, seq_clone,
+                  resize_bucket, rewind, rope_axes, rope_inv_freq, seq_clone,
                   seqinfo_from_seqused, to_contiguous)

@@ -23,6 +23,7 @@ ERR_SEGMENT, ERR_CAPACITY, ERR_RING, ERR_BLOCK, ERR_QLEN, ERR_OVERLAP, ERR_TIMEO
 # attention flags
 FLAG_SIMT, FLAG_PDL, FLAG_PREFETCH_NEXT, FLAG_MMA_SYNC, FLAG_OUT_BF16 = 1, 2, 4, 8, 16
 BLOCK_SIZE = 16
+ROPE_AXES = 8
 
 
 class CacheDesc(ctypes.Structure):
@@ -58,6 +59,9 @@ class RopeDesc(ctypes.Structure):
         ("eps", ctypes.c_float),
         ("q_weight", ctypes.c_void_p),
         ("k_weight", ctypes.c_void_p),
+        ("axis", ctypes.c_void_p),
+        ("num_axes", ctypes.c_int32),
+        ("reserved0", ctypes.c_int32),
     ]
 
 

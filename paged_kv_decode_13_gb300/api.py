@@ -161,6 +161,27 @@ def rope_inv_freq(rot_dim: int, theta: float = 10000.0, scaling: str = "none", f
     return freq, float(mscale.value)
 
 
+def rope_axes(sections: Sequence[int], dealt: bool = False) -> List[int]:
+    """The axis of every column pair, for Rope's axes, from the number of pairs each axis turns.
+
+    Axis after axis (the first sections[0] pairs turn with axis 0, ...), or
+    dealt: to the axes in turn, passing over those that have all their pairs
+    (0, 1, 2, 0, 1, 2, ..).
+    """
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= _lib.ROPE_AXES or min(left) < 0 or sum(left) == 0:
+        raise ValueError(f"sections are the pairs of 1 to {_lib.ROPE_AXES} axes, none negative")
+    if not dealt:
+        return [a for a, n in enumerate(left) for _ in range(n)]
+    out: List[int] = []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                left[a] -= 1
+                out.append(a)
+    return out
+
+
 class Rope:
     """What norm_rope and norm_rope_append do to a head: RMSNorm by a weight, then a rotation.
 
@@ -170,12 +191,17 @@ class Rope:
     rot_dim / 2).  mscale multiplies the rotated columns.  q_weight /
     k_weight: (head_dim,) of the rows' type, or None for no norm of that
     side.  Made once per model or layer; it keeps its tensors.
+
+    axes: for rows with a position on each of several axes (time, height and
+    width of images and video), the axis of every pair, as from rope_axes;
+    positions are then (rows, number of axes), the highest of `axes` and one.
     """
 
     def __init__(self, inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False, mscale: float = 1.0,
                  q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
-                 device=None):
-        self.turns = None
+                 device=None, axes: Optional[Sequence[int]] = None):
+        self.turns = self.axis = None
+        self.num_axes = 1
         n = 0
         if inv_freq is not None:
             if inv_freq.dim() != 1 or inv_freq.numel() == 0:
@@ -187,6 +213,13 @@ class Rope:
             if device is None:
                 device = inv_freq.device if inv_freq.is_cuda else "cuda"
             self.turns = turns.to(device)
+        if axes is not None:
+            axes = [int(a) for a in axes]
+            if len(axes) != n or n == 0 or min(axes) < 0 or max(axes) >= _lib.ROPE_AXES:
+                raise ValueError(f"axes names an axis below {_lib.ROPE_AXES} for each of the {n} pairs")
+            self.num_axes = max(axes) + 1
+            if self.num_axes > 1:
+                self.axis = torch.tensor(axes, dtype=torch.uint8).to(device)
         for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
             if w is not None and (w.dim() != 1 or w.dtype not in (torch.bfloat16, torch.float32)):
                 raise ValueError(f"{name} is (head_dim,) of bf16 or fp32")
@@ -195,7 +228,7 @@ class Rope:
         self.rot_dim, self.interleaved, self.mscale, self.eps = 2 * n, bool(interleaved), float(mscale), float(eps)
         self.desc = _lib.RopeDesc(turns=_ptr(self.turns), rot_dim=self.rot_dim, interleaved=int(self.interleaved),
                                   mscale=self.mscale, eps=self.eps, q_weight=_ptr(self.q_weight),
-                                  k_weight=_ptr(self.k_weight))
+                                  k_weight=_ptr(self.k_weight), axis=_ptr(self.axis), num_axes=self.num_axes, reserved0=0)
 
         given = [t for t in (self.turns, self.q_weight, self.k_weight) if t is not None]
         weights = [w for w in (self.q_weight, self.k_weight) if w is not None]
@@ -232,7 +265,7 @@ def _row_stride(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: i
     return s0 if rows > 1 else heads * dim
 
 
-def _rows_desc(q, k, v, q_out, k_out, v_out, positions, kv_heads, head_dim, dtype, device) -> bytes:
+def _rows_desc(q, k, v, q_out, k_out, v_out, positions, kv_heads, head_dim, dtype, device, axes=1) -> bytes:
     shape = (q if q is not None else k).shape
     if len(shape) != 3:
         raise ValueError("rows are (rows, heads, head_dim)")
@@ -256,8 +289,9 @@ def _rows_desc(q, k, v, q_out, k_out, v_out, positions, kv_heads, head_dim, dtyp
     if v_out is not None:
         vos, vop = _row_stride(v_out, "v_out", kv, dtype, device), v_out.data_ptr()
     if positions is not None:
-        if positions.shape != (rows,) or positions.dtype is not torch.int32 or positions.get_device() != device:
-            raise ValueError(f"positions is int32 ({rows},) on device {device}")
+        want = (rows,) if axes == 1 else (rows, axes)
+        if positions.shape != want or positions.dtype is not torch.int32 or positions.get_device() != device:
+            raise ValueError(f"positions is int32 {want} on device {device}")
         pos = _contig(positions, "positions").data_ptr()
     return _ROWS.pack(qp, kp, vp, qop, kop, vop, qs, ks, vs, qos, kos, vos, hq, rows, pos)
 
@@ -295,6 +329,7 @@ def norm_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
 
     q (rows, q_heads, head_dim) and k (rows, kv_heads, head_dim), bf16 or fp32,
     either may be None; rows may be strided (a slice of a projection's output).
+    positions: int32 (rows,), or (rows, axes) with a Rope of several axes.
     Without q_out / k_out the rows are changed in place.
     """
     some = q if q is not None else k
@@ -308,7 +343,7 @@ def norm_rope(rope: Rope, q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
     rope.check(dtype, dim, dev)
     kv = int(k.shape[1]) if k is not None and k.dim() == 3 else 0
     d = _rows_desc(q, k, None, q_out if q_out is not None else q, k_out if k_out is not None else k, None, positions, kv, dim,
-                   dtype, dev)
+                   dtype, dev, rope.num_axes)
     _launch("pkv_norm_rope", lib.pkv_norm_rope, (rope._ref, _DTYPES[dtype], dim, kv, d), dev, stream)
 
 
@@ -318,15 +353,17 @@ def norm_rope_append(cache: PagedKVCache, layer: int, rope: Optional[Rope], q: O
                      v_out: Optional[torch.Tensor] = None, stream=None) -> None:
     """pkv_norm_rope_append: norm and rotation of q and k, and the append of k and v, in one pass.
 
-    q goes to q_out (None: in place).  positions (rows,) int32 overrides the
-    angles' positions; by default a row's position in the cache.  k_out / v_out
+    q goes to q_out (None: in place).  positions (rows,) int32, or (rows, axes)
+    with a Rope of several axes, overrides the angles' positions; by default a
+    row's position in the cache, on every axis.  k_out / v_out
     get the rows as the cache holds them.  Rows may be strided.
     """
     dev, dtype, dim = cache._device, cache.row_dtype, cache._head_dim
     if rope is not None:
         rope.check(dtype, dim, dev)
     segments = _check_segments(cache, seq_info, err)
-    d = _rows_desc(q, k_new, v_new, q if q_out is None else q_out, k_out, v_out, positions, cache._kv_heads, dim, dtype, dev)
+    d = _rows_desc(q, k_new, v_new, q if q_out is None else q_out, k_out, v_out, positions, cache._kv_heads, dim, dtype, dev,
+                   1 if rope is None else rope.num_axes)
     _launch("pkv_norm_rope_append", lib.pkv_norm_rope_append,
             (cache._ref, layer, None if rope is None else rope._ref, d, _contig(seq_info, "seq_info").data_ptr(), segments, window, err.data_ptr()),
             dev, stream)

@@ -690,7 +690,10 @@ int rope_params(const pkv_rope *rope, const pkv_rows *r, int dtype, int head_dim
         if (rope->rot_dim > 0 && (!rope->turns || (reinterpret_cast<uintptr_t>(rope->turns) & 7u))) return PKV_EINVAL;
         if (!aligned16(rope->q_weight) || !aligned16(rope->k_weight)) return PKV_EINVAL;
         if (!append && rope->rot_dim > 0 && r->total_rows > 0 && !r->positions) return PKV_EINVAL;
+        if (rope->num_axes < 0 || rope->num_axes > PKV_ROPE_AXES || (rope->num_axes > 1) != (rope->axis != nullptr)) return PKV_EINVAL;
         p->turns = reinterpret_cast<const unsigned long long *>(rope->turns);
+        p->axis = rope->axis;
+        p->axes = rope->num_axes > 1 ? rope->num_axes : 1;
         p->rot_dim = rope->rot_dim;
         p->interleaved = rope->interleaved;
         p->mscale = rope->mscale;

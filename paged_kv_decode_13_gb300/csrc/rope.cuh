@@ -55,7 +55,9 @@ struct RopeParams {
     const void *q, *k, *v;            // rows; q may be null (no query heads), k and v null without a cache or k rows
     void *q_out, *k_out, *v_out;      // q_out null without q; k_out / v_out optional with a cache
     long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride, v_out_stride;  // elements between rows
-    const int *positions;             // [rows] or null: the row's cache position
+    const int *positions;             // [rows][axes] or null: the row's cache position, on every axis
+    const unsigned char *axis;        // [rot_dim / 2] the pair's axis, or null: one axis
+    int axes;
     const unsigned long long *turns;  // [rot_dim / 2]
     const void *q_weight, *k_weight;  // [D] or null
     float eps, mscale;
@@ -406,6 +408,19 @@ __device__ __forceinline__ float2 angle_of(unsigned pos, unsigned long long turn
     return make_float2(co * mscale, si * mscale);
 }
 
+// Angles of a row's pairs, shared among `threads` threads.  With several axes a pair's position is that of its
+// axis (clamped into the row's own positions, whatever the array holds).
+__device__ __forceinline__ void row_angles(const RopeParams &p, int row, int place, float2 *angles, int t, int threads) {
+    if (p.positions && p.axis) {
+        const int *pos = p.positions + (long long)row * p.axes;
+        for (int i = t; i < p.rot_dim / 2; i += threads)
+            angles[i] = angle_of((unsigned)pos[min((int)p.axis[i], p.axes - 1)], p.turns[i], p.mscale);
+    } else {
+        const unsigned pos = (unsigned)(p.positions ? p.positions[row] : place);
+        for (int i = t; i < p.rot_dim / 2; i += threads) angles[i] = angle_of(pos, p.turns[i], p.mscale);
+    }
+}
+
 // The heads of one row that groups [f0, f1) name (q, then k, then v), from
 // `rows[kind]` (global or shared memory); angles: the row's pairs.
 struct RopeWork {
@@ -651,8 +666,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, sizeof(T) == 2 ? 5 : 4) rope_
         if (CACHE != kNoCache && !place_row<CACHE>(p, row, seg, slot, place, lane)) continue;
         if (p.rot_dim) {
             __syncwarp();
-            const unsigned pos = (unsigned)(p.positions ? p.positions[row] : (int)place);
-            for (int i = lane; i < p.rot_dim / 2; i += 32) angles[i] = angle_of(pos, p.turns[i], p.mscale);
+            row_angles(p, row, (int)place, angles, lane, 32);
             __syncwarp();
         }
         const T *const rows[3] = {reinterpret_cast<const T *>(p.q) + row * p.q_stride, reinterpret_cast<const T *>(p.k) + row * p.k_stride,
