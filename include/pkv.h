@@ -63,7 +63,18 @@ typedef enum pkv_status {
  * s is 0, the sign kept).  A group that holds a NaN reads back as NaN, an
  * infinity as its scale's largest value.  Rows (q, k_new, v_new) are bf16.
  */
-typedef enum pkv_dtype { PKV_BF16 = 0, PKV_F32 = 1, PKV_FP4 = 2 } pkv_dtype;
+/*
+ * PKV_FP8 is another: values are e4m3 numbers (the finite ones, up to 448) times
+ * a scale 2^e shared by the 16 tokens of a page and kv head.  e is the smallest by which
+ * every value fits, -126 to 119; the code is the nearest e4m3 number to x / 2^e, ties to
+ * even.  A page is filled as tokens come: those that are in it keep e from
+ * getting smaller, and where a new one makes it larger, their codes are rounded to the larger one
+ * (exact down to 2^-6 times the scale, by at most 2^-10 times it below).  A
+ * page whose new rows begin at its first slot starts afresh (with ring
+ * storage: one whose slots are all new).  A token of a kv head that holds a NaN
+ * reads back as NaN, all of it, and an infinity as 448 * 2^119.  Rows are bf16.
+ */
+typedef enum pkv_dtype { PKV_BF16 = 0, PKV_F32 = 1, PKV_FP4 = 2, PKV_FP8 = 8 } pkv_dtype;
 
 /* Device-side error bits, OR-ed into *err_flags. */
 #define PKV_ERR_SEGMENT  (1u << 0)  /* q_start/q_len/col/kv_end out of range, or kv_end < q_len */
@@ -79,7 +90,7 @@ typedef enum pkv_dtype { PKV_BF16 = 0, PKV_F32 = 1, PKV_FP4 = 2 } pkv_dtype;
 #define PKV_FLAG_PDL   (1u << 1)  /* launch with programmatic dependent launch; see pkv_attend_varlen */
 #define PKV_FLAG_PREFETCH_NEXT (1u << 2)  /* warm L2 with layer + 1's pages; see pkv_attend_varlen */
 #define PKV_FLAG_MMA_SYNC (1u << 3)  /* bf16, head_dim 128, > 8 rows per kv head: mma.sync tile instead of tcgen05 */
-#define PKV_FLAG_OUT_BF16 (1u << 4)  /* PKV_FP4 caches: out is bf16 (it is fp32 otherwise) */
+#define PKV_FLAG_OUT_BF16 (1u << 4)  /* PKV_FP4 and PKV_FP8 caches: out is bf16 (it is fp32 otherwise) */
 
 /*
  * One paged K/V cache: per layer, a K pool and a V pool, each
@@ -103,10 +114,19 @@ typedef enum pkv_dtype { PKV_BF16 = 0, PKV_F32 = 1, PKV_FP4 = 2 } pkv_dtype;
  * 8 * D + token * D / 16 + column / 16.  In a V block, with token = 8 * hi +
  * 2 * t + n and column = g * D / 8 + 8 * p + i, it is in byte 512 * p +
  * 16 * (4 * g + t) + 2 * i + hi, nibble n, and its scale at 8 * D +
- * 4 * (4 * (column / 16) + t) + 2 * hi + n.  The append and attention calls,
- * pkv_rewind, pkv_advance and pkv_seqinfo_from_seqused take such caches; the
- * copying calls (pkv_seq_clone, pkv_resize_bucket, pkv_load_prefix,
- * pkv_to_contiguous) return PKV_EUNSUPPORTED for them.
+ * 4 * (4 * (column / 16) + t) + 2 * hi + n.
+ *
+ * A PKV_FP8 cache has the same head_dims, and pools of (num_blocks, kv_heads,
+ * 16 * D + 16) bytes: 16 rows of D codes, then 16 bytes: e + 127 (0: no
+ * scale yet, every value zero), 0, a 16-bit mask (low byte first) of the tokens that hold a NaN,
+ * whose NaN codes are 0, and twelve bytes that are not used.  The
+ * 16 codes from column 16 * c on of token t are in place c ^ (((t & 6) ^ (t & 1) << 2)
+ * % (D / 16)) of its row.  Pools are zero-filled before their first use.
+ *
+ * The append and attention calls, pkv_rewind, pkv_advance and
+ * pkv_seqinfo_from_seqused take quantised caches (PKV_FP4, PKV_FP8), and
+ * pkv_to_contiguous takes PKV_FP8; the other copying calls (pkv_seq_clone,
+ * pkv_resize_bucket, pkv_load_prefix) return PKV_EUNSUPPORTED for them.
  *
  * The descriptor is host memory owned by the caller; k and v are host arrays
  * of num_layers device pointers (16-byte aligned).  bucket is the token
@@ -180,6 +200,12 @@ const char *pkv_status_str(int status);
  * pages holds two tokens; calls and segments that write different slots of
  * one page, or the same row to one slot, at the same time do not disturb each
  * other.
+ *
+ * On a PKV_FP8 cache they are quantised as well, and the page's scale is shared:
+ * the segments of one call may write different slots of a page in the same column (the
+ * lowest of them writes the page; of rows for one slot the highest segment's counts),
+ * and a segment may be in the table twice, but columns whose tables name one page must
+ * not both write it, in one call or in two at a time.
  */
 int pkv_append(const pkv_cache *cache, int32_t layer,
                const void *k_new, const void *v_new, int32_t total_rows,
@@ -275,12 +301,15 @@ int pkv_norm_rope(const pkv_rope *rope, int32_t dtype, int32_t head_dim, int32_t
  * row's position in the cache (kv_end - q_len + i).  k_out and v_out
  * (optional) get the rows as the cache now holds them; with a PKV_FP4 cache
  * those are the quantised values (k is rounded to bf16 before it is
- * quantised).  Rows are of the cache's dtype (PKV_FP4: bf16).
+ * quantised), with PKV_FP8 under the scale that the whole call leaves.  Rows are of
+ * the cache's dtype (PKV_FP4, PKV_FP8: bf16).
  *
  * On a bf16 or fp32 cache a row belongs to one segment at most (in two it is
  * unspecified which of them places it).  On a PKV_FP4 cache it goes to its slot
  * in every segment that holds it, turned by positions[row] or by its position
- * in the lowest of them (v_out must not be v then).  Rows no segment covers, and
+ * in the lowest of them (v_out must not be v then).  On a PKV_FP8 cache it goes to
+ * all of them too; its q_out, k_out and v_out are then unspecified (and must not be q,
+ * k and v).  Rows no segment covers, and
  * rows of segments that pkv_append would refuse (the same PKV_ERR_* bits), are
  * not written, in none of the outputs.  A later attention call may be launched
  * with PKV_FLAG_PDL behind this one, unless one segment's rows are older keys
@@ -343,23 +372,25 @@ int pkv_norm_rope_append(const pkv_cache *cache, int32_t layer, const pkv_rope *
  * segments (one decode step): a hint only, it changes no result.  The
  * prefetch is capped at about 48 MB per call.
  *
- * On a PKV_FP4 cache q is bf16 and out is fp32, or bf16 with
+ * On a PKV_FP4 or PKV_FP8 cache q is bf16 and out is fp32, or bf16 with
  * PKV_FLAG_OUT_BF16.  Scores are those of the stored values to fp32; the
  * softmax weights are rounded to fp16 for the product with V (each by at most
- * 2^-11 of itself or 2^-32 of its row's largest, whichever is more).  A NaN in V
+ * 2^-11 of itself or 2^-32 of its row's largest, whichever is more; with PKV_FP8
+ * that is said of a weight times its page's V scale, and sums of such products above
+ * 2^100 may overflow).  A NaN in V
  * reaches only the rows that see its key.  Without a workspace the splits form
  * a cluster (num_splits 0..16); large launches are faster with one (see
  * pkv_attend_workspace_bytes).  PKV_FLAG_SIMT, PKV_FLAG_MMA_SYNC and
  * PKV_FLAG_PREFETCH_NEXT have no effect.  PKV_FLAG_PDL: pages wholly below
  * position kv_end - q_len may be read before the previous kernel has
  * finished, so it may be the append of this step, unless two segments are
- * pieces of one sequence.  (Most 4-bit attention
- * launches, and pkv_norm_rope and pkv_norm_rope_append, are programmatic
+ * pieces of one sequence.  (Most attention launches over quantised caches, and
+ * pkv_norm_rope and pkv_norm_rope_append, are programmatic
  * dependent launches without the flag too, which wait for the previous
  * kernel first thing.)
  *
  * Device pointers must be 16-byte aligned (out and lse: 4-byte; with a
- * PKV_FP4 cache out: 16-byte).
+ * quantised cache out: 16-byte).
  */
 int pkv_attend_varlen(const pkv_cache *cache, int32_t layer,
                       const void *q, int32_t num_q_heads, int32_t total_rows,
@@ -375,7 +406,7 @@ int pkv_attend_varlen(const pkv_cache *cache, int32_t layer,
  * step are written into the cache and attended to from k_new / v_new
  * directly.  Same arguments and results as the two calls in sequence, with
  * one extra condition: no two segments of the call may name the same `col`
- * (the two-call sequence has no such limit).  On a PKV_FP4 cache it is the two
+ * (the two-call sequence has no such limit).  On a quantised cache it is the two
  * calls, one launch each.
  */
 int pkv_append_attend(const pkv_cache *cache, int32_t layer,
@@ -405,13 +436,13 @@ int pkv_append_attend(const pkv_cache *cache, int32_t layer,
  * concurrently need their own.  A workspace smaller than this size is rejected with
  * PKV_EINVAL.  Returns a negative pkv_status for invalid bounds.
  *
- * With a PKV_FP4 cache: launches with num_splits 0, at most 512 segments and
+ * With a quantised cache: launches with num_splits 0, at most 512 segments and
  * at most 16 row tiles a kv head, whose bounds make it worth while (at 8 query rows per kv
  * head and head_dim 128, from about half a million (key, kv head) pairs for one
  * sequence and twice that for several; with more rows from fewer).
  * Given a workspace, they run as one wave of CTAs with equal shares of all
  * key ranges and a second launch that merges the shared ones, instead of as a
- * cluster per range; more than 32 rows per kv head at head_dim 128 then take
+ * cluster per range; with PKV_FP4 more than 32 rows per kv head at head_dim 128 then take
  * the tcgen05 tile.  The size does not grow with the lengths and is below 25 MB.
  * It need not be zeroed, and may be shared by calls that
  * follow one another on one stream.  A call with a window counts
@@ -536,7 +567,8 @@ int pkv_load_prefix(const pkv_cache *cache, const void *const *keys,
  * Write-back for a stage that reads an ordinary cache
  * ([vllm-omni paged_decode.py] PagedDecodeCache.to_dynamic_cache): copy the
  * first n flat rows of layer `layer` into keys_out / values_out laid out
- * [kv_heads][n][head_dim] (device, contiguous).
+ * [kv_heads][n][head_dim] (device, contiguous).  Of a PKV_FP8 cache the rows are
+ * bf16, the stored values (exact).
  */
 int pkv_to_contiguous(const pkv_cache *cache, int32_t layer, int64_t n,
                       void *keys_out, void *values_out, void *stream);

@@ -15,7 +15,7 @@ LIB_PATH = os.path.join(HERE, "libpkv.so")
 OK, EMPTY, SAME_BUCKET = 0, 1, 2
 EINVAL, EUNSUPPORTED, ECUDA, ECAPACITY, ESTALE = -1, -2, -3, -4, -5
 # pkv_dtype
-BF16, F32, FP4 = 0, 1, 2
+BF16, F32, FP4, FP8 = 0, 1, 2, 8
 # frequency scalings
 ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
 # device error bits

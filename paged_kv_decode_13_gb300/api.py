@@ -15,7 +15,8 @@ import torch
 from . import _lib
 from ._lib import lib
 
-_DTYPES = {torch.bfloat16: _lib.BF16, torch.float32: _lib.F32, torch.uint8: _lib.FP4}
+_DTYPES = {torch.bfloat16: _lib.BF16, torch.float32: _lib.F32, torch.uint8: _lib.FP4, torch.float8_e4m3fn: _lib.FP8}
+_QUANTISED = (torch.uint8, torch.float8_e4m3fn)  # caches held in 4 and in 8 bits
 
 
 def _stream(stream=None) -> int:
@@ -42,8 +43,9 @@ class PagedKVCache:
 
     Pools are (num_blocks, 16, kv_heads, head_dim) tensors of bf16 or fp32
     (the layout of vLLM-Omni's SenseNova-U1 PagedDecodeCache), or, for a cache
-    held in 4 bits, uint8 (num_blocks, kv_heads, 9 * head_dim) with head_dim
-    64, 128 or 256 (the page format is in include/pkv.h); the block
+    held in 4 bits, uint8 (num_blocks, kv_heads, 9 * head_dim), or, in 8 bits,
+    float8_e4m3fn (num_blocks, kv_heads, 16 * head_dim + 16), with head_dim
+    64, 128 or 256 (the page formats are in include/pkv.h; 8-bit pools start zeroed); the block
     table is int32 (max_seqs, max_blocks_per_seq).  first_valid, optional
     int32 (max_seqs,), is each sequence's first non-padding position for
     left-padded batches (tiny-llm kv_cache.py, SlotKVCache): the attention
@@ -62,12 +64,17 @@ class PagedKVCache:
         for t in list(k) + list(v):
             if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError("every pool must be contiguous with the same shape and dtype")
-        if dtype == torch.uint8:
-            if len(shape) != 3 or shape[2] % 9:
-                raise ValueError("4-bit pools are uint8 (num_blocks, kv_heads, 9 * head_dim)")
-            kv_heads, head_dim = int(shape[1]), int(shape[2]) // 9
+        if dtype in _QUANTISED:
+            if dtype == torch.uint8:
+                if len(shape) != 3 or shape[2] % 9:
+                    raise ValueError("4-bit pools are uint8 (num_blocks, kv_heads, 9 * head_dim)")
+                kv_heads, head_dim = int(shape[1]), int(shape[2]) // 9
+            else:
+                if len(shape) != 3 or shape[2] % 16 or shape[2] < 32:
+                    raise ValueError("8-bit pools are float8_e4m3fn (num_blocks, kv_heads, 16 * head_dim + 16)")
+                kv_heads, head_dim = int(shape[1]), int(shape[2]) // 16 - 1
             if any(t.get_device() != k[0].get_device() for t in [*k, *v, block_table] + ([] if first_valid is None else [first_valid])):
-                raise ValueError("the pools and tables of a 4-bit cache are on one device")
+                raise ValueError("the pools and tables of a quantised cache are on one device")
         else:
             if len(shape) != 4 or shape[1] != _lib.BLOCK_SIZE:
                 raise ValueError("pools are (num_blocks, 16, kv_heads, head_dim)")
@@ -94,17 +101,17 @@ class PagedKVCache:
             block_table=block_table.data_ptr(), bucket=self.bucket, generation=self.generation,
             first_valid=_ptr(self.first_valid))
         self._ref = ctypes.byref(self.desc)
-        self._fp4 = dtype == torch.uint8
+        self._quantised = dtype in _QUANTISED
         self._kv_heads, self._head_dim, self._device = kv_heads, head_dim, k[0].get_device()
-        # the type of q, k_new and v_new rows: the cache's, bf16 for a 4-bit cache
-        self.row_dtype = torch.bfloat16 if self._fp4 else dtype
+        # the type of q, k_new and v_new rows: the cache's, bf16 for a quantised cache
+        self.row_dtype = torch.bfloat16 if self._quantised else dtype
 
     @classmethod
     def allocate(cls, num_layers: int, kv_heads: int, head_dim: int, bucket: int, dtype=torch.bfloat16,
                  device="cuda", generation: int = 0) -> "PagedKVCache":
-        """Zeroed single-sequence cache behind an identity table (one bucket); dtype torch.uint8: held in 4 bits."""
+        """Zeroed single-sequence cache behind an identity table (one bucket); dtype torch.uint8: held in 4 bits, torch.float8_e4m3fn: in 8."""
         nb = (bucket + _lib.BLOCK_SIZE - 1) // _lib.BLOCK_SIZE
-        shape = (nb, kv_heads, 9 * head_dim) if dtype == torch.uint8 else (nb, _lib.BLOCK_SIZE, kv_heads, head_dim)
+        shape = (nb, kv_heads, 9 * head_dim if dtype == torch.uint8 else 16 * head_dim + 16) if dtype in _QUANTISED else (nb, _lib.BLOCK_SIZE, kv_heads, head_dim)
         k = [torch.zeros(shape, dtype=dtype, device=device) for _ in range(num_layers)]
         v = [torch.zeros(shape, dtype=dtype, device=device) for _ in range(num_layers)]
         bt = torch.arange(nb, dtype=torch.int32, device=device).unsqueeze(0)
@@ -373,11 +380,11 @@ _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32  # (short calls a
 
 
 def _check_new(cache: PagedKVCache, rows: int, k_new: torch.Tensor, v_new: torch.Tensor) -> None:
-    """New rows for a 4-bit cache, heads and columns of a row apart or as one dimension."""
+    """New rows for a quantised cache, heads and columns of a row apart or as one dimension."""
     shape, heads, dim, dev = k_new.shape, cache._kv_heads, cache._head_dim, cache._device
     if (k_new.dtype is not _BF16 or v_new.dtype is not _BF16 or v_new.shape != shape
             or (shape != (rows, heads, dim) and shape != (rows, heads * dim)) or k_new.get_device() != dev or v_new.get_device() != dev):
-        raise ValueError(f"rows for a 4-bit cache are bf16, k_new and v_new ({rows}, {heads}, {dim}) on the cache's device")
+        raise ValueError(f"rows for a quantised cache are bf16, k_new and v_new ({rows}, {heads}, {dim}) on the cache's device")
 
 
 def _check_segments(cache: PagedKVCache, seq_info: torch.Tensor, err: torch.Tensor) -> int:
@@ -389,11 +396,11 @@ def _check_segments(cache: PagedKVCache, seq_info: torch.Tensor, err: torch.Tens
 
 
 def _check_fp4(cache: PagedKVCache, q, k_new, v_new, seq_info, out, lse, err) -> None:
-    """The tensors of an attention call over a 4-bit cache."""
+    """The tensors of an attention call over a quantised cache."""
     shape, kind, dev = q.shape, out.dtype, cache._device
     if (len(shape) != 3 or shape[2] != cache._head_dim or q.dtype is not _BF16 or (kind is not _F32 and kind is not _BF16) or out.shape != shape
             or q.get_device() != dev or out.get_device() != dev):
-        raise ValueError(f"over a 4-bit cache q is bf16 (rows, heads, {cache._head_dim}) and out fp32 or bf16 of the same shape, on its device")
+        raise ValueError(f"over a quantised cache q is bf16 (rows, heads, {cache._head_dim}) and out fp32 or bf16 of the same shape, on its device")
     if lse is not None and (lse.dtype is not _F32 or lse.numel() != shape[0] * shape[1] or not lse.is_contiguous() or lse.get_device() != dev):
         raise ValueError("lse is fp32 (rows, heads), contiguous, on the cache's device")
     _check_segments(cache, seq_info, err)
@@ -404,7 +411,7 @@ def _check_fp4(cache: PagedKVCache, q, k_new, v_new, seq_info, out, lse, err) ->
 def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, seq_info: torch.Tensor,
            err: torch.Tensor, window: int = 0, stream=None) -> None:
     rows = int(k_new.shape[0])
-    if cache._fp4:
+    if cache._quantised:
         _check_new(cache, rows, k_new, v_new)
         _check_segments(cache, seq_info, err)
     _on_device(cache._device, "pkv_append", lib.pkv_append, (
@@ -412,18 +419,18 @@ def append(cache: PagedKVCache, layer: int, k_new: torch.Tensor, v_new: torch.Te
         _ptr(_contig(seq_info, "seq_info")), int(seq_info.shape[0]), int(window), _ptr(err)), stream)
 
 
-# Bounds (segments x kv heads x row tiles x keys) from which a launch over a 4-bit cache
+# Bounds (segments x kv heads x row tiles x keys) from which a launch over a quantised cache
 # may use a workspace; pkv_attend_workspace_bytes decides.
 _FP4_WORKSPACE_FROM = 1 << 18
 
 
 def fp4_keys(max_kv: int, max_q_len: int, window: int) -> int:
-    """Keys of a segment at most: the bound that decides how a launch over a 4-bit cache is cut."""
+    """Keys of a segment at most: the bound that decides how a launch over a quantised cache is cut."""
     return min(max_kv, window + max_q_len) if window > 0 else max_kv
 
 
 def _fp4_workspace(cache, hq, segments, max_q_len, max_kv, window, flags, stream):
-    """A workspace for one call over a 4-bit cache, or None: a large launch merges its shared ranges through it.
+    """A workspace for one call over a quantised cache, or None: a large launch merges its shared ranges through it.
 
     Each call takes its own from torch's allocator, so eager calls on several
     streams share nothing.  A captured call's comes from the graph's memory pool:
@@ -454,7 +461,7 @@ def _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max
         with torch.cuda.device(dev):
             return _attend(fn_name, cache, layer, q, k_new, v_new, seq_info, out, lse, err, max_q_len, max_kv, scale, causal,
                            window, num_splits, flags, stream, workspace)
-    if cache._fp4:
+    if cache._quantised:
         _check_fp4(cache, q, k_new, v_new, seq_info, out, lse, err)
         if workspace is None and num_splits == 0:
             workspace = _fp4_workspace(cache, shape[1], segments, max_q_len, max_kv, window, flags, stream)
@@ -494,7 +501,7 @@ def append_attend_noalloc(cache: PagedKVCache, layer: int, q: torch.Tensor, k_ne
                           stream=None) -> None:
     """pkv_append_attend_noalloc: append_attend merging its splits in the library's fixed scratch."""
     rows, hq = int(q.shape[0]), int(q.shape[1])
-    if cache._fp4:
+    if cache._quantised:
         _check_fp4(cache, q, k_new, v_new, seq_info, out, lse, err)
     if out.dtype == torch.bfloat16:
         flags |= _lib.FLAG_OUT_BF16
@@ -578,6 +585,11 @@ def load_prefix(cache: PagedKVCache, keys: Sequence[torch.Tensor], values: Seque
 
 def to_contiguous(cache: PagedKVCache, layer: int, n: int, keys_out: torch.Tensor, values_out: torch.Tensor,
                   stream=None) -> None:
-    """keys_out / values_out: contiguous [kv_heads, n, head_dim]."""
+    """keys_out / values_out: contiguous [kv_heads, n, head_dim] of the cache's row_dtype (an 8-bit cache's stored values)."""
+    if cache.dtype == torch.float8_e4m3fn:
+        want = (cache._kv_heads, int(n), cache._head_dim)
+        for t in (keys_out, values_out):
+            if t.shape != want or t.dtype is not _BF16 or not t.is_contiguous() or t.get_device() != cache._device:
+                raise ValueError(f"keys_out and values_out are bf16 {want}, contiguous, on the cache's device")
     _on_device(cache._device, "pkv_to_contiguous", lib.pkv_to_contiguous, (cache.ref(), layer, int(n), _ptr(keys_out), _ptr(values_out)),
                stream)

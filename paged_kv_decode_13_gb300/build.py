@@ -37,8 +37,10 @@ def _sources():
             units.append((os.path.join(CSRC, "attend_inst.cu"), f"attend_{variant}_{dp}.o",
                           [f"-DPKV_INST_VARIANT={variant}", f"-DPKV_INST_DP={dp}"]))
     for d in (64, 128, 256):
-        units.append((os.path.join(CSRC, "attend4_inst.cu"), f"attend4_{d}.o", [f"-DPKV_INST_D={d}"]))
+        for bits in (4, 8):
+            units.append((os.path.join(CSRC, "attend4_inst.cu"), f"attend{bits}_{d}.o", [f"-DPKV_INST_D={d}", f"-DPKV_INST_BITS={bits}"]))
     units.append((os.path.join(CSRC, "rope.cu"), "rope.o", []))
+    units.append((os.path.join(CSRC, "append8.cu"), "append8.o", []))
     units.append((os.path.join(CSRC, "api.cu"), "api.o", []))
     return units
 

@@ -30,15 +30,18 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 int elem_bytes(int dtype) { return dtype == PKV_BF16 ? 2 : dtype == PKV_F32 ? 4 : 0; }
 
-bool is_fp4(const pkv_cache *c) { return c && c->dtype == PKV_FP4; }
+// A cache held in 4 or 8 bits.
+bool is_quantised(const pkv_cache *c) { return c && (c->dtype == PKV_FP4 || c->dtype == PKV_FP8); }
+// Bytes of its page block of one kv head.
+int block_bytes(const pkv_cache *c) { return c->dtype == PKV_FP4 ? 9 * c->head_dim : 16 * c->head_dim + 16; }
 
-// fp4: whether the call takes 4-bit caches.
-int check_cache(const pkv_cache *c, bool fp4 = false) {
+// quantised: whether the call takes such caches.
+int check_cache(const pkv_cache *c, bool quantised = false) {
     if (!c) return PKV_EINVAL;
-    if (c->dtype != PKV_BF16 && c->dtype != PKV_F32 && !(fp4 && is_fp4(c))) return PKV_EUNSUPPORTED;
+    if (c->dtype != PKV_BF16 && c->dtype != PKV_F32 && !(quantised && is_quantised(c))) return PKV_EUNSUPPORTED;
     // vLLM-Omni paged_decode_supported: head_dim a multiple of 8, at most 256.
     if (c->head_dim <= 0 || c->head_dim % 8 != 0 || c->head_dim > 256) return PKV_EUNSUPPORTED;
-    if (is_fp4(c) && c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return PKV_EUNSUPPORTED;
+    if (is_quantised(c) && c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return PKV_EUNSUPPORTED;
     if (c->num_layers <= 0 || c->kv_heads <= 0 || c->num_blocks <= 0) return PKV_EINVAL;
     if (c->num_blocks > INT32_MAX || c->kv_heads > 65535) return PKV_EINVAL;
     if (c->max_seqs <= 0 || c->max_blocks_per_seq <= 0) return PKV_EINVAL;
@@ -360,7 +363,7 @@ int encode_pool_pages(CUtensorMap *map, const void *pool, const pkv_cache *c) {
     return r == CUDA_SUCCESS ? PKV_OK : PKV_ECUDA;
 }
 
-// ---- 4-bit caches
+// ---- quantised caches
 
 struct Plan4 {
     Attend4Kernel k4;
@@ -402,7 +405,8 @@ bool regs_ok(const Attend4Kernel &k, int dev) {
     return a.numRegs == k.regs;
 }
 
-Attend4Kernel pick4_rows(int head_dim, int rows, bool few) {
+Attend4Kernel pick4_rows(int dtype, int head_dim, int rows, bool few) {
+    if (dtype == PKV_FP8) return head_dim == 64 ? pick8_64(rows, few) : head_dim == 128 ? pick8_128(rows, few) : pick8_256(rows, few);
     return head_dim == 64 ? pick4_64(rows, few) : head_dim == 128 ? pick4_128(rows, few) : pick4_256(rows, few);
 }
 
@@ -415,7 +419,7 @@ struct Fit4 {
 };
 const Fit4 &fit4(const Attend4Kernel &k, int dev) {
     static std::mutex mu;
-    static KernelTable<Fit4, 256> known;  // eleven kernels
+    static KernelTable<Fit4, 512> known;  // 22 kernels
     static thread_local Fit4 f;
     std::lock_guard<std::mutex> lock(mu);
     if (const Fit4 *kept = known.find(k.fn, dev)) return *kept;
@@ -477,9 +481,9 @@ double cost4(const Attend4Kernel &k, const Fit4 &f, bool few, long long units, l
 }
 
 // CTAs of a range (num_splits, or the cheapest number), their kernel and the cost.
-double split4(Attend4Kernel *k4, int head_dim, int rows, long long units, long long pages, int num_splits, int dev, int *ncta) {
+double split4(Attend4Kernel *k4, int dtype, int head_dim, int rows, long long units, long long pages, int num_splits, int dev, int *ncta) {
     double best = kNever;
-    const Attend4Kernel cand[2] = {*k4, pick4_rows(head_dim, rows, true)};
+    const Attend4Kernel cand[2] = {*k4, pick4_rows(dtype, head_dim, rows, true)};
     *ncta = 1;
     for (int few = 0; few < (cand[1].fn == cand[0].fn ? 1 : 2); ++few) {
         const Attend4Kernel &k = cand[few];
@@ -505,16 +509,16 @@ double split4(Attend4Kernel *k4, int head_dim, int rows, long long units, long l
 // 0, 12, 24 pages; uneven 16-row tiles of head_dim 256 (16 sequences up to 4096 keys) took 67 us
 // with 12 and 43 with 50, the tcgen05 kernel's drafts of 16 sequences 82, 72, 73 us with 10, 36, 24
 // (69 now).
-int piece_pages4(const Attend4Kernel &k, int head_dim) {
-    return k.rows == 128 ? 36 : k.rows == 8 ? (56 << 10) / (2 * block4_bytes(head_dim)) : kPieceTile;
+int piece_pages4(const Attend4Kernel &k, int block) {
+    return k.rows == 128 ? 36 : k.rows == 8 ? (56 << 10) / (2 * block) : kPieceTile;
 }
 
 // The same of equal shares: `units` ranges (by this kernel's row tiles) of `pages`
 // pages each, pieces and pages read by all SMs at 1.1 times what full SMs take;
 // the second launch and the scan of the segment table cost 10 us (the tcgen05 kernel: 14.5).
-double cost4_shares(const Attend4Kernel &k, int head_dim, long long units, long long pages, int dev) {
+double cost4_shares(const Attend4Kernel &k, int block, long long units, long long pages, int dev) {
     return (k.rows == 128 ? 14500 : 10000) +
-           (double)units * (pages + piece_pages4(k, head_dim)) * k.page_ns * k.full * 11 / (200.0 * k.ctas * device_sms(dev));
+           (double)units * (pages + piece_pages4(k, block)) * k.page_ns * k.full * 11 / (200.0 * k.ctas * device_sms(dev));
 }
 
 struct Ws4Layout {
@@ -538,7 +542,7 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     pl->G = Hq / c->kv_heads;
     const long long rows = (long long)pl->G * max_q_len;
     if (rows > (1 << 20)) return PKV_EINVAL;
-    pl->k4 = pick4_rows(c->head_dim, (int)rows, false);
+    pl->k4 = pick4_rows(c->dtype, c->head_dim, (int)rows, false);
     pl->row_tiles = (int)((rows + pl->k4.rows - 1) / pl->k4.rows);
     if ((long long)c->kv_heads * pl->row_tiles > 65535) return PKV_EINVAL;
     pl->units = (long long)std::max(S, 1) * c->kv_heads * pl->row_tiles;
@@ -546,11 +550,11 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     pl->pages = (keys + PKV_BLOCK_SIZE - 1) / PKV_BLOCK_SIZE;
     pl->shares = 0;
     pl->ks = pl->k4;
-    const double cost = split4(&pl->k4, c->head_dim, (int)rows, pl->units, pl->pages, num_splits, dev, &pl->ncta);
+    const double cost = split4(&pl->k4, c->dtype, c->head_dim, (int)rows, pl->units, pl->pages, num_splits, dev, &pl->ncta);
     if (num_splits == 0 && S > 0 && S <= kSharesSegments) {
-        if (c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide(), dev)) pl->ks = pick4_wide();
+        if (c->dtype == PKV_FP4 && c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide(), dev)) pl->ks = pick4_wide();
         const long long tiles = (rows + pl->ks.rows - 1) / pl->ks.rows;
-        const double shares = cost4_shares(pl->ks, c->head_dim, (long long)S * c->kv_heads * tiles, pl->pages, dev);
+        const double shares = cost4_shares(pl->ks, block_bytes(c), (long long)S * c->kv_heads * tiles, pl->pages, dev);
         if (tiles <= kSharesTiles && shares < cost * (100 + kSharesEdge) / 100)
             pl->shares = std::min(device_sms(dev) * pl->ks.ctas, kMerge4Slots);
     }
@@ -613,7 +617,7 @@ int attend4(const pkv_cache *c, int layer, const void *q, int Hq, int total_rows
     p.out_bf16 = (flags & PKV_FLAG_OUT_BF16) ? 1 : 0;
     p.early = (flags & PKV_FLAG_PDL) ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.piece_pages = piece_pages4(k4, c->head_dim);
+    p.piece_pages = piece_pages4(k4, block_bytes(c));
     p.ws_head = nullptr;
     p.ws_stat = nullptr;
     p.ws_part = nullptr;
@@ -906,7 +910,7 @@ int pkv_append(const pkv_cache *c, int32_t layer, const void *k_new, const void 
                const int32_t *seq_info, int32_t S, int32_t window, uint32_t *err, void *stream) {
     int st = check_cache(c, true);
     if (st) return st;
-    if (is_fp4(c)) {
+    if (is_quantised(c)) {
         const int64_t n = (int64_t)c->kv_heads * c->head_dim;
         pkv_rows r = {};
         r.k = k_new;
@@ -1017,7 +1021,9 @@ int pkv_norm_rope_append(const pkv_cache *c, int32_t layer, const pkv_rope *rope
     p.mbps = c->max_blocks_per_seq;
     p.ring_rows = c->ring_rows;
     p.window = window;
-    return launch_status(launch_rope(p, is_fp4(c) ? kFp4 : kSameType, c->dtype == PKV_F32, device_sms(current_device()),
+    if (c->dtype == PKV_FP8)
+        return launch_status(launch_append8(p, device_sms(current_device()), reinterpret_cast<cudaStream_t>(stream)));
+    return launch_status(launch_rope(p, c->dtype == PKV_FP4 ? kFp4 : kSameType, c->dtype == PKV_F32, device_sms(current_device()),
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1025,7 +1031,7 @@ int pkv_attend_varlen(const pkv_cache *c, int32_t layer, const void *q, int32_t 
                       const int32_t *seq_info, int32_t S, int32_t max_q_len, int64_t max_kv, int32_t num_splits,
                       float scale, int32_t causal, int32_t window, float *out, float *lse, void *workspace,
                       int64_t workspace_bytes, uint32_t *err, uint32_t flags, void *stream) {
-    if (is_fp4(c))
+    if (is_quantised(c))
         return attend4(c, layer, q, Hq, total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale, causal, window, out, lse,
                        workspace, workspace_bytes, err, flags, stream);
     return attend_common(c, layer, q, nullptr, nullptr, Hq, total_rows, seq_info, S, max_q_len, max_kv,
@@ -1039,7 +1045,7 @@ int pkv_append_attend(const pkv_cache *c, int32_t layer, const void *q, const vo
                       float *out, float *lse, void *workspace, int64_t workspace_bytes, uint32_t *err,
                       uint32_t flags, void *stream) {
     if (total_rows > 0 && (!k_new || !v_new)) return PKV_EINVAL;
-    if (is_fp4(c)) {
+    if (is_quantised(c)) {
         // The attention's arguments are checked first, so that a refused call writes nothing.
         auto attend = [&](bool check_only) {
             return attend4(c, layer, q, Hq, total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale, causal, window, out, lse,
@@ -1059,7 +1065,7 @@ int pkv_append_attend_noalloc(const pkv_cache *c, int32_t layer, const void *q, 
                               const void *v_new, int32_t Hq, int32_t total_rows, const int32_t *seq_info, int32_t S,
                               int32_t max_q_len, int64_t max_kv, int32_t num_splits, float scale, int32_t causal,
                               int32_t window, float *out, float *lse, uint32_t *err, uint32_t flags, void *stream) {
-    if (is_fp4(c))  // needs no scratch
+    if (is_quantised(c))  // needs no scratch
         return pkv_append_attend(c, layer, q, k_new, v_new, Hq, total_rows, seq_info, S, max_q_len, max_kv, num_splits, scale,
                                  causal, window, out, lse, nullptr, 0, err, flags, stream);
     const int64_t need = pkv_attend_workspace_bytes(c, Hq, S, max_q_len, max_kv, num_splits, flags);
@@ -1084,7 +1090,7 @@ int pkv_append_attend_noalloc(const pkv_cache *c, int32_t layer, const void *q, 
 
 int64_t pkv_attend_workspace_bytes(const pkv_cache *c, int32_t Hq, int32_t S, int32_t max_q_len, int64_t max_kv,
                                    int32_t num_splits, uint32_t flags) {
-    if (is_fp4(c)) {  // equal shares merge through it, clusters need none
+    if (is_quantised(c)) {  // equal shares merge through it, clusters need none
         Plan4 pl4;
         const int st = make_plan4(c, Hq, S, max_q_len, max_kv, 0, num_splits, current_device(), &pl4);
         return st ? st : pl4.shares ? (int64_t)ws4_layout(pl4.shares, pl4.ks.rows, c->head_dim).total : 0;
@@ -1212,12 +1218,16 @@ int pkv_load_prefix(const pkv_cache *c, const void *const *keys, const void *con
 
 int pkv_to_contiguous(const pkv_cache *c, int32_t layer, int64_t n, void *keys_out, void *values_out,
                       void *stream) {
-    int st = check_cache(c);
+    const bool fp8 = c && c->dtype == PKV_FP8;
+    int st = check_cache(c, fp8);
     if (st) return st;
     if ((st = check_layer(c, layer))) return st;
     if (n < 0 || n > c->num_blocks * PKV_BLOCK_SIZE) return PKV_ECAPACITY;
     if (n == 0) return PKV_OK;
     if (!keys_out || !values_out || !aligned16(keys_out) || !aligned16(values_out)) return PKV_EINVAL;
+    if (fp8)
+        return launch_status(launch_read8(c->k[layer], c->v[layer], keys_out, values_out, n, c->kv_heads, c->head_dim, device_sms(current_device()),
+                                          reinterpret_cast<cudaStream_t>(stream)));
     const int row = c->head_dim * elem_bytes(c->dtype);
     const long long tok = (long long)c->kv_heads * row;
     return copy_rows(c->k[layer], c->v[layer], keys_out, values_out, n, c->kv_heads, row, tok, row, row,

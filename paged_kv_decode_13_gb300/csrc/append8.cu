@@ -1,0 +1,59 @@
+// Instantiations and launch of the append to an 8-bit cache.
+#include <algorithm>
+
+#include "append8.cuh"
+#include "rope_launch.h"
+
+namespace pkv {
+
+template <int D>
+static const void *pick_pair8(int pair) {
+    switch (pair) {
+        case kInLane: return reinterpret_cast<const void *>(&append8_kernel<D, kInLane>);
+        case kByShuffle: return reinterpret_cast<const void *>(&append8_kernel<D, kByShuffle>);
+        default: return reinterpret_cast<const void *>(&append8_kernel<D, kByShared>);
+    }
+}
+
+cudaError_t launch_append8(const RopeParams &r, int sms, cudaStream_t stream) {
+    Append8Params a;
+    a.r = r;
+    const int pair = r.rot_dim == 0 || r.interleaved ? kInLane : r.rot_dim % 16 == 0 ? kByShuffle : kByShared;
+    // A CTA a page where there are few enough (one segment may hold all rows: its
+    // pages bound the others'); the heads of a page are spread over CTAs until
+    // each SM has kAppend8Fill of them.
+    const long long pages = ((long long)r.rows + kPage - 2) / kPage + 1, most = (long long)sms * kAppend8Most;
+    const int items = (r.q ? r.Hq : 0) + 2 * r.Hkv;
+    a.page_ctas = (int)std::max<long long>(1, std::min(pages, most / r.S));
+    const long long active = std::max<long long>(1, std::min<long long>((long long)r.S * a.page_ctas, r.S + r.rows / kPage));  // CTAs with a page, about
+    a.head_ctas = (int)std::max<long long>(1, std::min<long long>((items + kAppend8Warps - 1) / kAppend8Warps, (long long)sms * kAppend8Fill / active));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)r.S * a.page_ctas * a.head_ctas));
+    cfg.blockDim = dim3(kAppend8Warps * 32);
+    cfg.dynamicSmemBytes = (size_t)kPage * (r.rot_dim / 2) * 8 + (pair == kByShared ? kAppend8Warps * 1024 : 0);
+    cfg.stream = stream;
+    cudaLaunchAttribute after;  // waits for the kernel before it first thing; only the start overlaps that one's end
+    after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    after.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &after;
+    cfg.numAttrs = 1;
+    void *args[] = {&a};
+    const void *fn = r.D == 64 ? pick_pair8<64>(pair) : r.D == 128 ? pick_pair8<128>(pair) : pick_pair8<256>(pair);
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+cudaError_t launch_read8(const void *k, const void *v, void *k_out, void *v_out, long long n, int kv_heads, int head_dim, int sms, cudaStream_t stream) {
+    Read8Params p;
+    p.pool[0] = reinterpret_cast<const unsigned char *>(k);
+    p.pool[1] = reinterpret_cast<const unsigned char *>(v);
+    p.out[0] = reinterpret_cast<__nv_bfloat16 *>(k_out);
+    p.out[1] = reinterpret_cast<__nv_bfloat16 *>(v_out);
+    p.n = n;
+    p.Hkv = kv_heads;
+    p.D = head_dim;
+    const long long ctas = std::min<long long>((2 * n * kv_heads * (head_dim / 8) + 255) / 256, (long long)sms * 16);
+    read8_kernel<<<(unsigned)ctas, 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace pkv

@@ -46,6 +46,7 @@
 
 #include "attend4_launch.h"
 #include "fp4.cuh"
+#include "fp8.cuh"
 
 namespace pkv {
 
@@ -58,13 +59,14 @@ constexpr float kNoMax = -1e30f;       // reference maximum of a row that has se
 // the product with V while the sum still counts them).
 constexpr float kLift4 = 7.f, kLazy4 = 15.f;
 
-template <int D_, int NT_, int KW_, int NST_, int PP_, int CTAS_, bool QSH_>
+template <int D_, int NT_, int KW_, int NST_, int PP_, int CTAS_, bool QSH_, int BITS_ = 4>
 struct Cfg4 {
+    static constexpr int BITS = BITS_;               // of the cache's values
     static constexpr int D = D_, NT = NT_, KW = KW_, NST = NST_, kCtas = CTAS_;
     static constexpr int PP = PP_;                   // pages of a stage
     static constexpr int kThreads = KW * 32;
     static constexpr int R = 8 * NT;                 // query rows of a CTA
-    static constexpr int kBlock = block4_bytes(D);   // K or V bytes of a page
+    static constexpr int kBlock = BITS == 4 ? block4_bytes(D) : block8_bytes(D);  // K or V bytes of a page
     static constexpr int kPageBytes = 2 * kBlock;    // a page's K block, then its V block
     static constexpr int kStage = PP * kPageBytes;
     static constexpr int KS = D / 16;                // 16-wide steps of S, 16-row tiles of O
@@ -228,6 +230,13 @@ __device__ __forceinline__ void refuse4(const Attend4Params &p, const Segment &s
             zero_row4(p, r, h0 * p.G, (h1 - h0) * p.G, D, threadIdx.x, blockDim.x);
 }
 
+// The lane's output columns of accumulator tile i: column_of and the one after it.
+template <class C>
+__device__ __forceinline__ int column_of(int gq, int i) {
+    if constexpr (C::BITS == 8 && C::D == 256) return (i >> 3) * 128 + gq * 16 + 2 * (i & 7);  // two chunks of 16 columns
+    return gq * (C::D / 8) + 2 * i;
+}
+
 // Attend one piece: every warp takes every KW-th of its pages and leaves its
 // partial rows and (max, sum) in shared memory.  ring: stages this warp has
 // used so far.  dep: the dependency wait happens in here, after the first
@@ -299,26 +308,29 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
     int issued = 0;
     if (dep) {
         // Pages wholly below this step's rows are in the cache already, whatever
-        // the kernel before this one still writes.
+        // the kernel before this one still writes.  (An 8-bit ring's append also moves the
+        // older tokens of its page to a larger scale: no early start where that page is in the range.)
+        const bool early = C::BITS == 4 || !p.ring_rows || cb0 > (kend - 1) / kPage - p.ring_rows / kPage;
 #pragma unroll 1
-        for (; issued < NST && issued < stages && cb0 + kw + (issued * PP + PP - 1) * KW < new_start / kPage; ++issued) issue(issued);
+        for (; early && issued < NST && issued < stages && cb0 + kw + (issued * PP + PP - 1) * KW < new_start / kPage; ++issued) issue(issued);
         depend4(p, true);
     }
 #pragma unroll 1
     for (; issued < NST && issued < stages; ++issued) issue(issued);
     if (dep) coverage4<D>(p);  // while the copies are on their way
 
-    // ---- Q^T fragments of one 8-row tile: lane (g, t) holds row g, columns t D/4 ..
+    // ---- Q^T fragments of one 8-row tile: lane (g, t) holds row g, columns t D/4 .. (4 bits)
+    // or the 16-column chunks t + 4 i (8 bits)
     auto load_q = [&](int nt, unsigned (&f)[KS][2]) {
         const int r = nt * 8 + gq;
         const bool real = r < rows_here;
         const int i = (row0 + (real ? r : 0)) / p.G, jh = (row0 + (real ? r : 0)) % p.G;
         const unsigned char *src = reinterpret_cast<const unsigned char *>(
-            p.q + (((long long)sg.q0 + i) * p.Hq + (long long)h * p.G + jh) * D + tq * (D / 4));
+            p.q + (((long long)sg.q0 + i) * p.Hq + (long long)h * p.G + jh) * D + tq * (C::BITS == 4 ? D / 4 : 16));
         unsigned w[D / 8];
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-            const uint4 v = real ? *reinterpret_cast<const uint4 *>(src + 16 * c) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 v = real ? *reinterpret_cast<const uint4 *>(src + (C::BITS == 4 ? 16 * c : (c >> 1) * 128 + (c & 1) * 16)) : make_uint4(0u, 0u, 0u, 0u);
             w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
         }
         unsigned mx = 0;
@@ -359,6 +371,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
     // ---- the warp's pages
     float acc[NT][KS][4];
     float m_r[NT][2], l_r[NT][2];
+    unsigned vref = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         m_r[nt][0] = m_r[nt][1] = kNoMax;
@@ -375,9 +388,16 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
         // S^T: lane (g, t) holds tokens g and g + 8, columns t D/4 ..  (A stage's
         // missing last page holds whatever was there: its scores and scales are masked.)
         float sa[PP][NT][4];
+        float sp[PP][NT][2];  // factors of the pages' scores
 #pragma unroll
         for (int e = 0; e < PP; ++e) {
             const unsigned char *st = stage + e * C::kPageBytes;
+            unsigned kt = 0;  // 8 bits: the page's scale, and its tokens that hold a NaN
+            if constexpr (C::BITS == 8) kt = e < pages ? *reinterpret_cast<const unsigned *>(st + 16 * D) : 0u;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) sp[e][nt][i] = C::BITS == 8 ? sc[nt][i] * scale8_value(kt & 0xffu) : sc[nt][i];
             // One accumulation chain a page and tile; a lone one is split in two.
             constexpr bool kTwo = PP * NT == 1;
             float sb[4] = {0.f, 0.f, 0.f, 0.f};
@@ -385,6 +405,35 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sa[e][nt][i] = 0.f;
+            if constexpr (C::BITS == 8) {
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    unsigned ka[4], kb[4];
+                    lds_words<4>(ka, st + gq * D + 16 * place8(gq, tq + 4 * i, D));
+                    lds_words<4>(kb, st + (gq + 8) * D + 16 * place8(gq, tq + 4 * i, D));
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        unsigned a0, a1, b0, b1;
+                        unpack_e4m3x4(a0, a1, ka[w]);
+                        unpack_e4m3x4(b0, b1, kb[w]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            uint2 q;
+                            if constexpr (C::kQShared) q = sQ[(nt * KS + 4 * i + w) * 32 + lane];
+                            else q = make_uint2(qf[4 * i + w][0], qf[4 * i + w][1]);
+                            if (kTwo && (w & 1)) mma_f16_16816(sb, a0, b0, a1, b1, q.x, q.y);
+                            else mma_f16_16816(sa[e][nt], a0, b0, a1, b1, q.x, q.y);
+                        }
+                    }
+                }
+                if (kt >> 16) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (kt >> (16 + gq + (i >> 1) * 8) & 1u) sa[e][nt][i] = CUDART_NAN_F;
+                }
+            } else {
             constexpr int W = D / 32;  // code words of a token and lane
             unsigned ka[W], kb[W];
             lds_words<W>(ka, st + gq * (D / 2) + tq * (D / 8));
@@ -416,9 +465,35 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                     else mma_f16_16816(sa[e][nt], a[2], b[2], a[3], b[3], q1.x, q1.y);
                 }
             }
+            }
             if constexpr (kTwo)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sa[e][0][i] += sb[i];
+        }
+        // 8 bits: a page's V scale goes into the weights of the product, relative to the
+        // largest one met so far (`vref`, its exponent); the sum of weights stays as it is.
+        unsigned vt[PP];
+        float fv[PP];
+        if constexpr (C::BITS == 8) {
+            unsigned most = 0;
+#pragma unroll
+            for (int e = 0; e < PP; ++e) {
+                vt[e] = e < pages ? *reinterpret_cast<const unsigned *>(stage + e * C::kPageBytes + C::kBlock + 16 * D) : 0u;
+                most = max(most, vt[e] & 0xffu);
+            }
+            auto power = [](int d) { return d > -127 ? __uint_as_float((unsigned)(127 + d) << 23) : 0.f; };
+            if (most > vref) {
+                const float f = power((int)vref - (int)most);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[nt][k][i] *= f;
+                vref = most;
+            }
+#pragma unroll
+            for (int e = 0; e < PP; ++e) fv[e] = (vt[e] & 0xffu) ? power((int)(vt[e] & 0xffu) - (int)vref) : 0.f;
         }
         // Online softmax (base 2) with a lazy maximum: this lane has tokens g,
         // g + 8 of rows 2t, 2t + 1.  x = score - reference; the reference moves
@@ -431,7 +506,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
 #pragma unroll
             for (int e = 0; e < PP; ++e)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[e][i] = fmaf(sa[e][nt][i], sc[nt][i & 1], -m_r[nt][i & 1]);
+                for (int i = 0; i < 4; ++i) x[e][i] = fmaf(sa[e][nt][i], sp[e][nt][i & 1], -m_r[nt][i & 1]);
             if (!inside) {
 #pragma unroll
                 for (int e = 0; e < PP; ++e)
@@ -451,7 +526,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                     for (int e = 0; e < PP; ++e)
 #pragma unroll
                         for (int o = 0; o < 4; o += 2)
-                            if (x[e][i + o] != -CUDART_INF_F) mx = fmaxf(mx, fmaf(sa[e][nt][i + o], sc[nt][i], -kLift4));
+                            if (x[e][i + o] != -CUDART_INF_F) mx = fmaxf(mx, fmaf(sa[e][nt][i + o], sp[e][nt][i], -kLift4));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                     const float al = ex2(m_r[nt][i] - mx);
@@ -466,7 +541,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                     for (int e = 0; e < PP; ++e)
 #pragma unroll
                         for (int o = 0; o < 4; o += 2)
-                            if (x[e][i + o] != -CUDART_INF_F) x[e][i + o] = fmaf(sa[e][nt][i + o], sc[nt][i], -mx);
+                            if (x[e][i + o] != -CUDART_INF_F) x[e][i + o] = fmaf(sa[e][nt][i + o], sp[e][nt][i], -mx);
                 }
             }
 #pragma unroll
@@ -474,8 +549,13 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                 const float p00 = ex2(x[e][0]), p01 = ex2(x[e][1]), p10 = ex2(x[e][2]), p11 = ex2(x[e][3]);
                 l_r[nt][0] += p00 + p10;
                 l_r[nt][1] += p01 + p11;
-                pb[e][nt][0] = transpose8x8(pack_f16x2(p00, p01));
-                pb[e][nt][1] = transpose8x8(pack_f16x2(p10, p11));
+                if constexpr (C::BITS == 8) {
+                    pb[e][nt][0] = transpose8x8(pack_f16x2(p00 * fv[e], p01 * fv[e]));
+                    pb[e][nt][1] = transpose8x8(pack_f16x2(p10 * fv[e], p11 * fv[e]));
+                } else {
+                    pb[e][nt][0] = transpose8x8(pack_f16x2(p00, p01));
+                    pb[e][nt][1] = transpose8x8(pack_f16x2(p10, p11));
+                }
             }
         }
         // O^T += V^T P^T: lane (g, t) holds columns g D/8 .., tokens 2t, 2t + 1, 2t + 8, 2t + 9
@@ -483,6 +563,48 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
         for (int e = 0; e < PP; ++e) {
             const int pos0 = pos_first + e * KW * kPage;
             const unsigned char *sv = stage + e * C::kPageBytes + C::kBlock;
+            if constexpr (C::BITS == 8) {
+                constexpr int VW = D == 64 ? 2 : 4;  // words of a token, chunk and lane
+#pragma unroll
+                for (int c = 0; c < (D + 127) / 128; ++c) {
+                    unsigned v[4][VW];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int tok = 2 * tq + (i >> 1) * 8 + (i & 1);
+                        if constexpr (D == 64) lds_words<VW>(v[i], sv + tok * D + 16 * place8(tok, gq >> 1, D) + 8 * (gq & 1));
+                        else lds_words<VW>(v[i], sv + tok * D + 16 * place8(tok, gq + 8 * c, D));
+                        // keys that no row sees may hold anything
+                        if (!inside && (e >= pages || pos0 + tok < lo_u || pos0 + tok >= hi_u))
+#pragma unroll
+                            for (int w = 0; w < VW; ++w) v[i][w] = 0u;
+                    }
+#pragma unroll
+                    for (int w = 0; w < VW; ++w)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {  // columns 4 w + 2 k and the next
+                            unsigned a0, a1, a2, a3;
+                            unpack_e4m3x4(a0, a1, __byte_perm(v[0][w], v[1][w], k ? 0x7362 : 0x5140));
+                            unpack_e4m3x4(a2, a3, __byte_perm(v[2][w], v[3][w], k ? 0x7362 : 0x5140));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma_f16_16816(acc[nt][8 * c + 2 * w + k], a0, a1, a2, a3, pb[e][nt][0], pb[e][nt][1]);
+                        }
+                }
+                if (vt[e] >> 16) {  // tokens that hold a NaN: the rows that see them are NaN
+#pragma unroll 1
+                    for (int o = 0; o < kPage; ++o)
+                        if (vt[e] >> (16 + o) & 1u)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const int r = nt * 8 + 2 * tq + i;
+                                    if (pos0 + o >= sLo[r] && pos0 + o < sHi[r])
+#pragma unroll
+                                        for (int k = 0; k < KS; ++k) acc[nt][k][i] = acc[nt][k][i + 2] = CUDART_NAN_F;
+                                }
+                }
+            } else {
             unsigned fa = 0, fb = 0;
 #pragma unroll
             for (int pl = 0; pl < D / 64; ++pl) {
@@ -536,6 +658,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                     for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[nt][pl * 4 + k], a0, a1, a2, a3, pb[e][nt][0], pb[e][nt][1]);
                 }
             }
+            }
         }
         __syncwarp();  // every lane is done with the stage
         if (j + NST < stages) issue(j + NST);
@@ -571,11 +694,13 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
         float *part = reinterpret_cast<float *>(pipe) + (size_t)kw * C::kPartFloats;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float *r0 = part + (nt * 8 + 2 * tq) * LD + gq * (D / 8), *r1 = r0 + LD;
+            float *r0 = part + (nt * 8 + 2 * tq) * LD, *r1 = r0 + LD;
+            const float unit = C::BITS == 8 ? scale8_value(vref) : 1.f;  // what the sums count in
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
-                *reinterpret_cast<float2 *>(r0 + 2 * i) = make_float2(acc[nt][i][0], acc[nt][i][2]);
-                *reinterpret_cast<float2 *>(r1 + 2 * i) = make_float2(acc[nt][i][1], acc[nt][i][3]);
+                const int col = column_of<C>(gq, i);
+                *reinterpret_cast<float2 *>(r0 + col) = make_float2(acc[nt][i][0] * unit, acc[nt][i][2] * unit);
+                *reinterpret_cast<float2 *>(r1 + col) = make_float2(acc[nt][i][1] * unit, acc[nt][i][3] * unit);
             }
             if (gq == 0) {
                 float *st = part + R * LD + nt * 8 + 2 * tq;

@@ -1,10 +1,14 @@
-// Instantiates the 4-bit attention kernel for one head_dim (-DPKV_INST_D=<64|128|256>).
+// Instantiates the attention over quantised caches for one head_dim (-DPKV_INST_D=<64|128|256>) and
+// format (-DPKV_INST_BITS=<4|8>).
 #include "attend4.cuh"
 
 #ifndef PKV_INST_D
 #error "PKV_INST_D not set"
 #endif
-#if PKV_INST_D == 128
+#ifndef PKV_INST_BITS
+#error "PKV_INST_BITS not set"
+#endif
+#if PKV_INST_D == 128 && PKV_INST_BITS == 4
 #include "wide4.cuh"
 #endif
 
@@ -16,11 +20,27 @@ static Attend4Kernel info4(int page_ns, int full) {
                          reinterpret_cast<const void *>(&merge4_kernel<C::D, C::R, C::R == 8 ? kMerge4Threads : 32>), C::kThreads, C::kSmem, C::R, C::KW, C::kCtas, page_ns, full, 0};
 }
 
-#define PICK4_NAME2(D) pick4_##D
-#define PICK4_NAME(D) PICK4_NAME2(D)
+#define PICK4_NAME2(B, D) pick##B##_##D
+#define PICK4_NAME(B, D) PICK4_NAME2(B, D)
 
-Attend4Kernel PICK4_NAME(PKV_INST_D)(int rows, bool few) {
+Attend4Kernel PICK4_NAME(PKV_INST_BITS, PKV_INST_D)(int rows, bool few) {
+#if PKV_INST_BITS == 8
 #if PKV_INST_D == 64
+    if (rows <= 8 && few) return info4<Cfg4<64, 1, 8, 2, 2, 2, false, 8>>(46, 20);
+    if (rows <= 8) return info4<Cfg4<64, 1, 4, 3, 2, 3, false, 8>>(78, 34);
+    if (rows <= 16) return info4<Cfg4<64, 2, 8, 4, 1, 2, true, 8>>(78, 27);
+    return info4<Cfg4<64, 4, 8, 4, 1, 1, true, 8>>(107, 20);
+#elif PKV_INST_D == 128
+    if (rows <= 8 && few) return info4<Cfg4<128, 1, 8, 2, 2, 1, false, 8>>(67, 20);
+    if (rows <= 8) return info4<Cfg4<128, 1, 4, 2, 2, 3, false, 8>>(100, 42);
+    if (rows <= 16) return info4<Cfg4<128, 2, 8, 4, 1, 1, true, 8>>(100, 20);
+    return info4<Cfg4<128, 4, 4, 4, 1, 2, true, 8>>(228, 27);
+#else
+    if (rows <= 8 && few) return info4<Cfg4<256, 1, 8, 3, 1, 1, true, 8>>(110, 20);
+    if (rows <= 8) return info4<Cfg4<256, 1, 4, 2, 1, 2, true, 8>>(180, 33);
+    return info4<Cfg4<256, 2, 8, 2, 1, 1, true, 8>>(153, 20);
+#endif
+#elif PKV_INST_D == 64
     if (rows <= 8 && few) return info4<Cfg4<64, 1, 8, 2, 2, 2, false>>(46, 20);
     if (rows <= 8) return info4<Cfg4<64, 1, 4, 4, 2, 4, false>>(78, 34);
     if (rows <= 16) return info4<Cfg4<64, 2, 8, 4, 1, 2, true>>(78, 27);
@@ -37,7 +57,7 @@ Attend4Kernel PICK4_NAME(PKV_INST_D)(int rows, bool few) {
 #endif
 }
 
-#if PKV_INST_D == 128
+#if PKV_INST_D == 128 && PKV_INST_BITS == 4
 Attend4Kernel pick4_wide() {
     return Attend4Kernel{nullptr, reinterpret_cast<const void *>(&wide4_kernel), reinterpret_cast<const void *>(&merge4_kernel<128, 128, 32>),
                          Wide4::kThreads, Wide4::kSmem, Wide4::R, 8, 1, 235, 20, Wide4::kRegs};

@@ -1,4 +1,4 @@
-// Host-side view of the 4-bit attention kernels.
+// Host-side view of the kernels that attend over quantised caches (4 and 8 bits).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -10,7 +10,7 @@ namespace pkv {
 
 // Everything one launch reads; passed by value as a grid constant.
 struct Attend4Params {
-    const unsigned char *k, *v;   // this layer's pools, [num_blocks][Hkv][9 D]
+    const unsigned char *k, *v;   // this layer's pools, [num_blocks][Hkv] blocks
     const __nv_bfloat16 *q;       // [rows][Hq][D]
     const int *block_table;       // [max_seqs][mbps]
     const int4 *seq_info;         // [S]
@@ -55,6 +55,10 @@ struct Attend4Kernel {
 Attend4Kernel pick4_64(int rows, bool few);
 Attend4Kernel pick4_128(int rows, bool few);
 Attend4Kernel pick4_256(int rows, bool few);
+// The same over an 8-bit cache.
+Attend4Kernel pick8_64(int rows, bool few);
+Attend4Kernel pick8_128(int rows, bool few);
+Attend4Kernel pick8_256(int rows, bool few);
 // The tcgen05 kernel of wide groups (head_dim 128, equal shares only: fn is null).
 Attend4Kernel pick4_wide();
 

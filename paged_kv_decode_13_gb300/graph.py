@@ -63,7 +63,7 @@ class DecodeStep:
     as the projections give them: each layer is then norm_rope_append, which
     leaves the turned queries in `q_rot`, and the attention over them, two
     launches (fused does not apply).  The angles are those of the rows'
-    positions in the cache.  A cache held in 4 bits takes two launches a layer
+    positions in the cache.  A cache held in 4 or 8 bits takes two launches a layer
     as well, three where large bounds share the key ranges; its outputs may be
     bf16 (out_dtype).  The workspace of that merge belongs to the step: a
     capture allocates nothing, and captured steps share no memory.
@@ -93,8 +93,8 @@ class DecodeStep:
         self.fused, self.pdl, self.flags, self.num_splits = fused, pdl is None or pdl, flags, num_splits
         self.rope_pdl = num_segments == 1 if pdl is None else pdl
         self.prefetch_next = prefetch_next
-        if out_dtype != torch.float32 and not (out_dtype == torch.bfloat16 and cache.dtype == torch.uint8):
-            raise ValueError("out_dtype is float32, or bfloat16 over a 4-bit cache")
+        if out_dtype != torch.float32 and not (out_dtype == torch.bfloat16 and cache._quantised):
+            raise ValueError("out_dtype is float32, or bfloat16 over a quantised cache")
         self.rope = None if rope is None else [rope] * L if isinstance(rope, Rope) else list(rope)
         if self.rope is not None and len(self.rope) != L:
             raise ValueError("rope needs one entry per layer")
@@ -122,20 +122,20 @@ class DecodeStep:
 
     def size_workspace(self) -> None:
         """(Re)allocate the split-merge workspace where the current cache and bounds need another size (None: they need none)."""
-        fp4, n = self.cache.dtype == torch.uint8, 0
-        if self.use_workspace or (fp4 and self.num_splits == 0):
-            keys = fp4_keys(self.max_kv, self.max_q_len, self.window) if fp4 else self.max_kv
+        quantised, n = self.cache._quantised, 0
+        if self.use_workspace or (quantised and self.num_splits == 0):
+            keys = fp4_keys(self.max_kv, self.max_q_len, self.window) if quantised else self.max_kv
             n = attend_workspace_bytes(self.cache, self.num_q_heads, int(self.seq_info.shape[0]), self.max_q_len, keys,
                                        self.num_splits, self.flags)
         if n <= 0:
             self.ws = None
         elif self.ws is None or self.ws.numel() != n:
-            make = torch.empty if fp4 else torch.zeros  # (a 4-bit cache's need not be zeroed)
+            make = torch.empty if quantised else torch.zeros  # (a quantised cache's need not be zeroed)
             self.ws = make(n, dtype=torch.uint8, device=self.cache.k[0].device)
 
     def launch_count(self) -> int:
-        """Kernels of one run (a 4-bit cache's merge launches, which its bounds decide, not counted)."""
-        one = self.fused and self.rope is None and self.cache.dtype != torch.uint8
+        """Kernels of one run (a quantised cache's merge launches, which its bounds decide, not counted)."""
+        one = self.fused and self.rope is None and not self.cache._quantised
         return self.cache.num_layers * (1 if one else 2) + (1 if self.advance else 0)
 
     def run(self, stream=None, advance: Optional[bool] = None) -> None:
