@@ -177,6 +177,7 @@ __device__ __forceinline__ void append8_head(const RopeParams &p, int kind, int 
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] *= rinv;
             x[it].set(y);
+            if (rows[it * TPI + sub] < 0) x[it].clear();  // (a slot without a new row has no angles, and 1 / sqrt(eps) may be infinite)
         }
     }
     if (kind == 0) {

@@ -282,6 +282,23 @@ def test_norm_rope_into_fp8(pkv, D, rot, interleaved, norm):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+def test_single_rows_beside_empty_slots(pkv, D):
+    """A page's slots without a new row take no part, whatever a norm with eps 0 makes of nothing."""
+    w = workloads.batched(S=3, max_len=64, lengths=[64, 40, 17], q_heads=4, kv_heads=2, head_dim=D)
+    f = Fp8(pkv, w)
+    freq, _ = pkv.rope_inv_freq(D)
+    wq, wk = [(1 + 0.2 * torch.randn(D)).bfloat16().cuda() for _ in range(2)]
+    rope = pkv.Rope(freq, q_weight=wq, k_weight=wk, eps=0.0, device="cuda")
+    q, kn, vn, si, err = w.q[0].cuda(), w.k_new[0].cuda(), w.v_new[0].cuda(), w.seq_info.cuda(), pkv.new_err_flags()
+    qo, ko, vo = torch.empty_like(q), torch.empty_like(kn), torch.empty_like(vn)
+    pkv.norm_rope_append(f.cache, 0, rope, q, kn, vn, si, qo, err, k_out=ko, v_out=vo)
+    q2, k2 = q.clone(), kn.clone()
+    pkv.norm_rope(rope, q2, k2, (w.seq_info[:, 3] - 1).cuda())
+    assert int(err.item()) == 0 and torch.equal(q2, qo)
+    check_append(f, f.bytes, k2, vn, ko, vo)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_append_many_rows(pkv, D):
     """Ragged prompts with gaps, a refused segment and a bad page among them."""
     w = workloads.batched(S=6, max_len=1024, lengths=[700, 300, 17, 900, 64, 333], q_heads=4, kv_heads=2, head_dim=D, seed=1)
