@@ -402,6 +402,33 @@ int pkv_attend_varlen(const pkv_cache *cache, int32_t layer,
                       uint32_t *err_flags, uint32_t flags, void *stream);
 
 /*
+ * Attention of whole prompts over their own rows, which are packed one after the
+ * other: rows->q [total_rows][q_heads][head_dim], rows->k and rows->v
+ * [total_rows][kv_heads][head_dim], bf16, rows apart as their strides say (slices of
+ * one projection output); the other pointers of rows are NULL.  No cache is read or
+ * written: the step's append (of the same rows and table) and this call may come in either order.
+ *
+ * seq_info as for pkv_append.  A segment's rows are its sequence from the first
+ * position on, so kv_end has to be q_len (else PKV_ERR_SEGMENT: keys before the rows
+ * would be in a cache, which pkv_attend_varlen reads); col is not looked at.
+ * max_len bounds every segment's q_len (PKV_ERR_QLEN) and sizes the launch.  Which
+ * keys a row sees, out, lse, uncovered rows, refused segments and overlaps
+ * (PKV_ERR_OVERLAP) are as in pkv_attend_varlen, without padding.  softmax_scale is
+ * positive and finite; head_dim a multiple of 8, at most 256; q_heads / kv_heads at most 128.
+ *
+ * Scores are fp32 sums of exact products; softmax weights are rounded to bf16 (each
+ * by at most 2^-8 of itself) for the product with V, whose sums are fp32.  A NaN or
+ * infinity in k or v reaches the rows that see its key and no others (a
+ * call that meets one takes longer).  out: fp32, or bf16 with PKV_FLAG_OUT_BF16, 16-byte
+ * aligned, [total_rows][q_heads][head_dim].  The launch is a programmatic dependent one,
+ * which waits for the kernel before it first thing; PKV_FLAG_PDL has no effect.
+ */
+int pkv_attend_prompt(int32_t head_dim, int32_t kv_heads, const pkv_rows *rows,
+                      const int32_t *seq_info, int32_t num_segments, int32_t max_len,
+                      float softmax_scale, int32_t causal, int32_t window,
+                      void *out, float *lse, uint32_t *err_flags, uint32_t flags, void *stream);
+
+/*
  * pkv_append followed by pkv_attend_varlen in one launch: the rows of this
  * step are written into the cache and attended to from k_new / v_new
  * directly.  Same arguments and results as the two calls in sequence, with

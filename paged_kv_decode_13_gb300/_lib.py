@@ -105,6 +105,7 @@ def _declare(lib):
         "pkv_rope_turns": (ctypes.c_int, [p, i32, p]),
         "pkv_norm_rope": (ctypes.c_int, [rp, i32, i32, i32, wp, p]),
         "pkv_norm_rope_append": (ctypes.c_int, [cp, i32, rp, wp, p, i32, i32, p, p]),
+        "pkv_attend_prompt": (ctypes.c_int, [i32, i32, wp, p, i32, i32, f32, i32, i32, p, p, p, u32, p]),
         "pkv_attend_workspace_bytes": (i64, [cp, i32, i32, i32, i64, i32, u32]),
         "pkv_append_attend_noalloc": (ctypes.c_int, [cp, i32, p, p, p, i32, i32, p, i32, i32, i64, i32, f32, i32,
                                                      i32, p, p, p, u32, p]),

@@ -486,6 +486,32 @@ def attend_varlen(cache: PagedKVCache, layer: int, q: torch.Tensor, seq_info: to
             causal, window, num_splits, flags, stream, workspace)
 
 
+def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_info: torch.Tensor, out: torch.Tensor, err: torch.Tensor,
+                  max_len: int, scale: float, causal: bool = True, window: int = 0, lse: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """pkv_attend_prompt: attention of packed whole prompts over their own rows.
+
+    q (rows, q_heads, head_dim), k and v (rows, kv_heads, head_dim), bf16; rows
+    may be strided (slices of a projection's output).  out: fp32 or bf16, like
+    q.  seq_info's segments have kv_end == q_len; max_len bounds it.
+    """
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v are (rows, heads, head_dim)")
+    (rows, hq, dim), hkv, dev = q.shape, int(k.shape[1]), q.get_device()
+    qs = _row_stride(q, "q", (rows, hq, dim), _BF16, dev)
+    ks, vs = [_row_stride(t, name, (rows, hkv, dim), _BF16, dev) for t, name in ((k, "k"), (v, "v"))]
+    if out.shape != q.shape or (out.dtype is not _F32 and out.dtype is not _BF16) or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError("out is fp32 or bf16 of q's shape, contiguous, on its device")
+    if lse is not None and (lse.dtype is not _F32 or lse.shape != (rows, hq) or not lse.is_contiguous() or lse.get_device() != dev):
+        raise ValueError("lse is fp32 (rows, heads), contiguous, on q's device")
+    if seq_info.dtype is not _I32 or seq_info.dim() != 2 or seq_info.shape[1] != 4 or seq_info.get_device() != dev or err.get_device() != dev:
+        raise ValueError("seq_info is int32 (segments, 4), and err with it on q's device")
+    d = _ROWS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), 0, 0, 0, qs, ks, vs, 0, 0, 0, hq, rows, 0)
+    _launch("pkv_attend_prompt", lib.pkv_attend_prompt,
+            (dim, hkv, d, _contig(seq_info, "seq_info").data_ptr(), seq_info.shape[0], int(max_len), float(scale), 1 if causal else 0, int(window),
+             out.data_ptr(), _ptr(lse), err.data_ptr(), _lib.FLAG_OUT_BF16 if out.dtype is _BF16 else 0), dev, stream)
+
+
 def append_attend(cache: PagedKVCache, layer: int, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                   seq_info: torch.Tensor, out: torch.Tensor, err: torch.Tensor, max_q_len: int, max_kv: int,
                   scale: float, causal: bool = False, window: int = 0, lse: Optional[torch.Tensor] = None,

@@ -41,6 +41,7 @@ def _sources():
             units.append((os.path.join(CSRC, "attend4_inst.cu"), f"attend{bits}_{d}.o", [f"-DPKV_INST_D={d}", f"-DPKV_INST_BITS={bits}"]))
     units.append((os.path.join(CSRC, "rope.cu"), "rope.o", []))
     units.append((os.path.join(CSRC, "append8.cu"), "append8.o", []))
+    units.append((os.path.join(CSRC, "prompt.cu"), "prompt.o", []))
     units.append((os.path.join(CSRC, "api.cu"), "api.o", []))
     return units
 

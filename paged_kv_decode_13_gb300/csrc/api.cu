@@ -16,6 +16,7 @@
 #include "kernel_table.h"
 #include "launch.h"
 #include "misc_kernels.cuh"
+#include "prompt_launch.h"
 #include "rope_launch.h"
 
 using namespace pkv;
@@ -1037,6 +1038,76 @@ int pkv_attend_varlen(const pkv_cache *c, int32_t layer, const void *q, int32_t 
     return attend_common(c, layer, q, nullptr, nullptr, Hq, total_rows, seq_info, S, max_q_len, max_kv,
                          num_splits, scale, causal, window, out, lse, workspace, workspace_bytes, err, flags,
                          stream);
+}
+
+int pkv_attend_prompt(int32_t head_dim, int32_t kv_heads, const pkv_rows *r, const int32_t *seq_info, int32_t S, int32_t max_len,
+                      float scale, int32_t causal, int32_t window, void *out, float *lse, uint32_t *err, uint32_t flags, void *stream) {
+    if (head_dim <= 0 || head_dim % 8 != 0 || head_dim > 256) return PKV_EUNSUPPORTED;
+    if (!r || r->total_rows < 0 || kv_heads <= 0 || r->q_heads <= 0 || r->q_heads % kv_heads != 0) return PKV_EINVAL;
+    if (r->q_heads / kv_heads > 128) return PKV_EUNSUPPORTED;  // a token's heads fill more than a tile
+    if (r->q_out || r->k_out || r->v_out || r->positions || (flags & ~(PKV_FLAG_OUT_BF16 | PKV_FLAG_PDL))) return PKV_EINVAL;
+    if (S < 0 || S > 65535 || max_len <= 0 || window < 0 || (causal != 0 && causal != 1) || !(scale > 0.f) || !isfinite(scale)) return PKV_EINVAL;
+    const long long nq = (long long)r->q_heads * head_dim, nk = (long long)kv_heads * head_dim;
+    if (!err || !out || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return PKV_EINVAL;
+    if (S > 0 && (!seq_info || !aligned16(seq_info))) return PKV_EINVAL;
+    if (r->total_rows == 0) return PKV_OK;
+    if (!rows_ok(r->q, r->q_stride, nq, 2) || !rows_ok(r->k, r->k_stride, nk, 2) || !rows_ok(r->v, r->v_stride, nk, 2)) return PKV_EINVAL;
+    const PromptKernel k = pick_prompt(head_dim);
+    PromptParams p;
+    p.G = r->q_heads / kv_heads;
+    p.tokens = 128 / p.G;
+    const int group = k.tiles * p.tokens;  // tokens of a CTA
+    p.items = S > 0 ? (int)(((long long)std::min(max_len, r->total_rows) + group - 1) / group) : 1;
+    const long long ctas = (long long)p.items * std::max(S, 1) * kv_heads;
+    if (ctas > INT32_MAX) return PKV_EINVAL;
+    auto fn = encode_fn();
+    if (!fn) return PKV_ECUDA;
+    // (head_dim, heads, rows); a box is 64 columns of the given heads and rows, with 128-byte swizzling
+    auto encode = [&](CUtensorMap *map, const void *base, int heads, int64_t stride, int box_heads, int box_rows) {
+        cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)heads, (cuuint64_t)r->total_rows};
+        cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, (cuuint64_t)stride * 2};
+        cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, estr[3] = {1, 1, 1};
+        return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (!encode(&p.tmap_q, r->q, r->q_heads, r->q_stride, p.G, p.tokens) || !encode(&p.tmap_k, r->k, kv_heads, r->k_stride, 1, 128) ||
+        !encode(&p.tmap_v, r->v, kv_heads, r->v_stride, 1, 128))
+        return PKV_ECUDA;
+    p.q = reinterpret_cast<const __nv_bfloat16 *>(r->q);
+    p.k = reinterpret_cast<const __nv_bfloat16 *>(r->k);
+    p.v = reinterpret_cast<const __nv_bfloat16 *>(r->v);
+    p.q_stride = r->q_stride;
+    p.k_stride = r->k_stride;
+    p.v_stride = r->v_stride;
+    p.seq_info = reinterpret_cast<const int4 *>(seq_info);
+    p.out = out;
+    p.lse = lse;
+    p.err = err;
+    p.Hq = r->q_heads;
+    p.Hkv = kv_heads;
+    p.D = head_dim;
+    p.total_rows = r->total_rows;
+    p.S = S;
+    p.max_len = max_len;
+    p.causal = causal;
+    p.window = window;
+    p.out_bf16 = (flags & PKV_FLAG_OUT_BF16) ? 1 : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const int dev = current_device();
+    int st = prepare_kernel(AttnKernel{k.fn, k.threads, k.smem, 128, head_dim, true, true}, dev);
+    if (st) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)k.threads);
+    cfg.dynamicSmemBytes = k.smem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute after;  // waits for the kernel before it first thing; only the start overlaps that one's end
+    after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    after.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &after;
+    cfg.numAttrs = 1;
+    void *args[] = {&p};
+    return launch_status(cudaLaunchKernelExC(&cfg, k.fn, args));
 }
 
 int pkv_append_attend(const pkv_cache *c, int32_t layer, const void *q, const void *k_new, const void *v_new,
