@@ -391,19 +391,19 @@ constexpr int kWideFrom = 33;
 
 // Whether the kernel was compiled to the register count its warps hand around
 // (setmaxnreg waits for registers the launch must have brought).
-bool regs_ok(const Attend4Kernel &k, int dev) {
+bool regs_ok(const void *fn, int want, int dev) {
     static std::mutex mu;
     static KernelTable<int, 64> known;
-    if (!k.regs) return true;
+    if (!want) return true;
     std::lock_guard<std::mutex> lock(mu);
-    if (const int *regs = known.find(k.balance, dev)) return *regs == k.regs;
+    if (const int *regs = known.find(fn, dev)) return *regs == want;
     cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, k.balance) != cudaSuccess) {
+    if (cudaFuncGetAttributes(&a, fn) != cudaSuccess) {
         cudaGetLastError();
         return false;
     }
-    known.add(k.balance, dev, a.numRegs);
-    return a.numRegs == k.regs;
+    known.add(fn, dev, a.numRegs);
+    return a.numRegs == want;
 }
 
 Attend4Kernel pick4_rows(int dtype, int head_dim, int rows, bool few) {
@@ -553,7 +553,7 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     pl->ks = pl->k4;
     const double cost = split4(&pl->k4, c->dtype, c->head_dim, (int)rows, pl->units, pl->pages, num_splits, dev, &pl->ncta);
     if (num_splits == 0 && S > 0 && S <= kSharesSegments) {
-        if (c->dtype == PKV_FP4 && c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide(), dev)) pl->ks = pick4_wide();
+        if (c->dtype == PKV_FP4 && c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide().balance, pick4_wide().regs, dev)) pl->ks = pick4_wide();
         const long long tiles = (rows + pl->ks.rows - 1) / pl->ks.rows;
         const double shares = cost4_shares(pl->ks, block_bytes(c), (long long)S * c->kv_heads * tiles, pl->pages, dev);
         if (tiles <= kSharesTiles && shares < cost * (100 + kSharesEdge) / 100)
@@ -1094,6 +1094,7 @@ int pkv_attend_prompt(int32_t head_dim, int32_t kv_heads, const pkv_rows *r, con
     p.out_bf16 = (flags & PKV_FLAG_OUT_BF16) ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     const int dev = current_device();
+    if (!regs_ok(k.fn, k.regs, dev)) return PKV_ECUDA;  // (never so as built: its warps would wait for registers)
     int st = prepare_kernel(AttnKernel{k.fn, k.threads, k.smem, 128, head_dim, true, true}, dev);
     if (st) return st;
     cudaLaunchConfig_t cfg = {};

@@ -6,7 +6,7 @@ namespace pkv {
 template <int DP>
 static PromptKernel info_prompt() {
     using C = PromptCfg<DP>;
-    return PromptKernel{reinterpret_cast<const void *>(&prompt_kernel<C>), C::kThreads, C::kSmem, C::NT};
+    return PromptKernel{reinterpret_cast<const void *>(&prompt_kernel<C>), C::kThreads, C::kSmem, C::NT, C::kRegs};
 }
 
 PromptKernel pick_prompt(int head_dim) {

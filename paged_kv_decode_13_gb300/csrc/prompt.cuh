@@ -9,15 +9,21 @@
 // prompts fill tiles and the causal edge of a tile is 128 / G tokens wide.  It walks over
 // the keys that some row sees in blocks of 128.
 //
-// Roles, meeting on mbarriers:
+// The grid has a CTA for every such item, the longest first, but a CTA that runs
+// takes the items of CTAs that have not started (cluster launch control) instead of ending: one
+// CTA an SM stays, dynamic balance without a counter in memory, and the next
+// item's copies and products start while the rows of this one are written.
+//
+// Roles, meeting on mbarriers only, each walking through the items by itself:
 //   softmax warps (four a tile; thread = row)  read S from TMEM, mask, take the
 //       maximum, write P = 2^(S - reference) as bf16 over the S columns read,
 //       and at the end the normalised rows out.  The reference moves only when a score
 //       passes it by 2^8 (then O is rescaled in TMEM; no product is in flight on it then);
 //   MMA warp    S = Q K^T (M 128, N 128; Q and K in shared memory) and O += P V (P
 //       from TMEM, V as an MN-major tile);
-//   copy warp   Q once, then K and V blocks through a ring of stages (TMA, 128-byte
-//       swizzle; rows past the tensor and columns past head_dim come as zeros).
+//   copy warp   asks for the next item; Q, then K and V blocks through a ring of stages
+//       (TMA, 128-byte swizzle; rows past the tensor and columns past head_dim come as zeros);
+//   cover warp  rows of no segment, rows of two, refused segments.
 // TMEM (512 columns): two S / P slots of 128, then O.  Up to head_dim 128 the two
 // slots are the CTA's two tiles, whose softmax and products alternate: each tile's
 // next S waits for its own P V, and the tensor core works on the other's meanwhile.
@@ -28,11 +34,11 @@
 // taken from the unrounded ones in fp32.
 //
 // Keys that a row does not see have weight zero, and zero times a NaN or an
-// infinity of such a key's V is NaN.  That shows in the row: a CTA that finds a row
-// not finite runs its item once more, carefully: V blocks that not every row sees have their
+// infinity of such a key's V is NaN.  That shows in the row: items in which a row is
+// not finite are kept in a list and run once more, carefully: V blocks that not every row sees have their
 // non-finite values zeroed in shared memory, and the rows that do see
 // such a key get its products at the end.  All waits are bounded; a
-// timeout ends every role, the rows read zero and PKV_ERR_TIMEOUT is set.
+// timeout ends every role, rows not written yet read zero and PKV_ERR_TIMEOUT is set.
 #pragma once
 
 #include <math_constants.h>
@@ -54,9 +60,14 @@ struct PromptCfg {
     static constexpr unsigned kQTile = DP / 64 * kPart;
     static constexpr int NST = DP == 64 ? 8 : 5;
     static constexpr int kSoftmaxWarps = 4 * NT;
-    static constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
-    static constexpr int kBars = 2 * NST + 1 + 2 + 2 + 2 + 1;
-    static constexpr size_t kSmem = 1024 + (size_t)NT * kQTile + (size_t)NST * kStage + kBars * 8 + 64;
+    static constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
+    // registers a thread: at launch, and of the softmax warps and of the others while the roles run (one tile leaves enough for all)
+    static constexpr int kRegs = NT == 2 ? 168 : 0, kRegsSoftmax = NT == 2 ? 200 : 0, kRegsOthers = 104;
+    static_assert(kSoftmaxWarps * 32 * kRegsSoftmax + 128 * kRegsOthers <= kThreads * kRegs || NT == 1, "the roles' registers fit the launch's");
+    static constexpr int kSched = 4;                                // items on their way through the roles
+    static constexpr int kOdd = 64;                                 // items to run again, at most before they are
+    static constexpr int kBars = 2 * NST + 2 + 2 + 4 + 2 + 1 + 2 * kSched + 1;
+    static constexpr size_t kSmem = 1024 + (size_t)NT * kQTile + (size_t)NST * kStage + 16 + kBars * 8 + (kSched + kOdd) * 4 + 64;
     static constexpr unsigned kColO = 256;                          // O of tile t at kColO + t * DP
     static_assert(kSmem <= 232448, "exceeds the per-CTA shared memory limit");
 };
@@ -106,9 +117,9 @@ __device__ __forceinline__ void prompt_zero(const PromptParams &p, long long row
     if (p.lse)
         for (int e = t; e < heads; e += threads) p.lse[row * p.Hq + h0 + e] = -CUDART_INF_F;
 }
-// Rows of no segment read zero, rows of two set PKV_ERR_OVERLAP: one warp of every CTA takes its share of the rows.
-__device__ __noinline__ void prompt_coverage(const PromptParams &p, int lane) {
-    for (long long row = blockIdx.x; row < p.total_rows; row += gridDim.x) {
+// Rows of no segment read zero, rows of two set PKV_ERR_OVERLAP: one warp takes the rows of item id's share.
+__device__ __noinline__ void prompt_coverage(const PromptParams &p, int id, int lane) {
+    for (long long row = id; row < p.total_rows; row += gridDim.x) {
         int n = 0;
         for (int s = lane; s < p.S; s += 32) {
             const int4 v = p.seq_info[s];
@@ -148,62 +159,113 @@ __device__ __noinline__ void prompt_add_key(const PromptParams &p, long long key
     }
 }
 
+// One item: 2 (or 1) x 128 query rows of one (segment, kv head), and the blocks of keys they see.
+template <int NT>
+struct PromptItem {
+    Segment sg;
+    unsigned fault;
+    int s, h, index;         // segment, kv head, item of the segment
+    int token0, tokens;      // tokens of the segment; none: nothing to do
+    int first[NT], last[NT]; // blocks of each tile
+    int in_lo, in_hi;        // keys that every row sees
+    int b0, b1;              // blocks of the item
+    __device__ __forceinline__ void load(const PromptParams &p, int id) {
+        const int per = max(p.S, 1) * p.Hkv;
+        s = id % per / p.Hkv;
+        h = id % p.Hkv;
+        index = p.items - 1 - id / per;
+        sg = p.S ? load_segment(p.seq_info, s) : Segment{0, 0, 0, 0};
+        fault = p.S ? prompt_fault(p, sg) : 0u;
+        token0 = index * NT * p.tokens;
+        tokens = fault ? 0 : max(0, min(NT * p.tokens, sg.ql - token0));
+        if (tokens == 0) return;
+        int lo, hi, x;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int a = token0 + t * p.tokens, b = min(a + p.tokens, sg.ql) - 1;  // tokens of the tile
+            first[t] = last[t] = 0;
+            if (b >= a) {
+                row_key_bounds(a, sg.ql, p.causal, p.window, 0, lo, x);
+                row_key_bounds(b, sg.ql, p.causal, p.window, 0, x, hi);
+                first[t] = lo / 128;
+                last[t] = (hi + 127) / 128;
+            }
+        }
+        row_key_bounds(token0, sg.ql, p.causal, p.window, 0, lo, in_hi);
+        row_key_bounds(token0 + tokens - 1, sg.ql, p.causal, p.window, 0, in_lo, hi);
+        b0 = lo / 128;
+        b1 = (hi + 127) / 128;
+    }
+};
+
+// Ask for the item of a CTA that has not started: 16 bytes at `at`, completing on `bar`.
+__device__ __forceinline__ void ask_next(uint4 *at, uint64_t *bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(smem_u32(at)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The answer: the CTA's number, or -1 where none was left.
+__device__ __forceinline__ int next_of(const uint4 *at) {
+    unsigned got, x;
+    asm volatile(
+        "{\n .reg .b128 r;\n .reg .pred p;\n ld.shared.b128 r, [%2];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_u32(at))
+        : "memory");
+    return got ? (int)x : -1;
+}
+// Eight 32-bit words to global memory: one 32-byte store where the address allows it.
+__device__ __forceinline__ void store32(void *at, const unsigned (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                     "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+// 16 32-bit columns into this thread's TMEM lane; the caller waits (tmem_wait_st).
+__device__ __forceinline__ void tmem_st16_async(unsigned taddr, const unsigned (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]),
+        "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
-    constexpr int DP = C::DP, NT = C::NT, NST = C::NST, SPB = C::SPB;
-    constexpr int kWarpMma = C::kSoftmaxWarps, kWarpTma = kWarpMma + 1;
+    constexpr int DP = C::DP, NT = C::NT, NST = C::NST, SPB = C::SPB, SCHED = C::kSched;
+    constexpr int kWarpMma = C::kSoftmaxWarps, kWarpTma = kWarpMma + 1, kWarpCover = kWarpTma + 1;
+    using Item = PromptItem<NT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sQ = smem_raw + (-smem_u32(smem_raw) & 1023u);  // pointer arithmetic keeps the shared address space
     unsigned char *ring = sQ + NT * C::kQTile;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + (size_t)NST * C::kStage);
-    uint64_t *full = bars, *empty = full + NST, *q_full = empty + NST, *s_full = q_full + 1, *p_full = s_full + 2, *pv_done = p_full + 2, *drain = pv_done + 2;
-    unsigned *tslot = reinterpret_cast<unsigned *>(bars + C::kBars);
-    volatile int *sAbort = reinterpret_cast<volatile int *>(tslot + 1), *sOdd = sAbort + 1;  // a wait ran out; a row is not finite
+    uint4 *answer = reinterpret_cast<uint4 *>(ring + (size_t)NST * C::kStage);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(answer + 1);
+    uint64_t *full = bars, *empty = full + NST, *q_full = empty + NST, *q_empty = q_full + 1, *s_full = q_empty + 1;
+    uint64_t *p_half = s_full + 2, *p_full = p_half + 2, *pv_done = p_full + 2, *drain = pv_done + 2;  // P of keys 0-63 and 64-127
+    uint64_t *sched_full = drain + 1, *sched_empty = sched_full + SCHED, *asked = sched_empty + SCHED;
+    int *sItem = reinterpret_cast<int *>(bars + C::kBars), *sOdd = sItem + SCHED;
+    unsigned *tslot = reinterpret_cast<unsigned *>(sOdd + C::kOdd);
+    volatile int *sAbort = reinterpret_cast<volatile int *>(tslot + 1), *sCount = sAbort + 1, *sNext = sAbort + 2;  // items to run again; the item after them
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-    // ---- this CTA's item: the longest (the last tiles) first
-    const int per = max(p.S, 1) * p.Hkv, order = blockIdx.x / per, s = blockIdx.x % per / p.Hkv, h = blockIdx.x % p.Hkv;
-    const int item = p.items - 1 - order;
-    pdl_wait();
-    pdl_trigger();
-    const Segment sg = p.S ? load_segment(p.seq_info, s) : Segment{0, 0, 0, 0};
-    const unsigned fault = p.S ? prompt_fault(p, sg) : 0u;
-    const int token0 = item * NT * p.tokens, tokens = min(NT * p.tokens, sg.ql - token0);  // of this item
-    if (fault || tokens <= 0) {
-        if (fault && item == 0) {
-            if (tid == 0) atomicOr(p.err, fault);
-            if (sg.q0 >= 0)  // a negative q_start covers nothing
-                for (long long r = sg.q0; r < min((long long)sg.q0 + sg.ql, (long long)p.total_rows); ++r)
-                    prompt_zero(p, r, h * p.G, p.G, tid, C::kThreads);
-        }
-        if (warp == kWarpTma) prompt_coverage(p, lane);
-        return;
-    }
-    // keys of each tile: [lo, hi) that some row sees; of the item: [in_lo, in_hi) that every row does
-    int first[NT], last[NT];  // blocks of each tile
-    int in_lo, in_hi, lo, hi;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int a = token0 + t * p.tokens, b = min(a + p.tokens, sg.ql) - 1;  // tokens of the tile
-        first[t] = last[t] = 0;
-        if (b >= a) {
-            int x;
-            row_key_bounds(a, sg.ql, p.causal, p.window, 0, lo, x);
-            row_key_bounds(b, sg.ql, p.causal, p.window, 0, x, hi);
-            first[t] = lo / C::kKeys;
-            last[t] = (hi + C::kKeys - 1) / C::kKeys;
-        }
-    }
-    row_key_bounds(token0, sg.ql, p.causal, p.window, 0, lo, in_hi);
-    row_key_bounds(token0 + tokens - 1, sg.ql, p.causal, p.window, 0, in_lo, hi);
-    const int b0 = lo / C::kKeys, b1 = (hi + C::kKeys - 1) / C::kKeys;
 
     if (tid == 0) {
 #pragma unroll 1
-        for (int i = 0; i < C::kBars; ++i) mbar_init(bars + i, bars + i >= p_full && bars + i < p_full + 2 ? 4 : 1);
+        for (int i = 0; i < C::kBars; ++i) {
+            uint64_t *b = bars + i;
+            // P: every warp of the tile; an item is released by every warp but the one that copies
+            mbar_init(b, b >= p_half && b < pv_done ? 4 : b >= sched_empty && b < asked ? 3 + C::kSoftmaxWarps : 1);
+        }
         fence_barrier_init();
         *sAbort = 0;
-        *sOdd = 0;
+        *sCount = 0;
+        *sNext = blockIdx.x;
     }
     if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(tslot)), "r"(512) : "memory");
@@ -213,352 +275,513 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     const unsigned tmem = *tslot;
+    pdl_wait();
+    pdl_trigger();
 
-    // Bounded wait of a whole warp on one phase; false on a timeout, here or in another role.
-    auto wait_bar = [&](uint64_t *bar, unsigned parity) -> bool {
-        bool ok = mbar_try_wait(bar, parity);
-        if (!ok) {
-            const unsigned long long t0 = global_ns();
+    // Bounded wait of one thread on one phase; false on a timeout, here or in another role.
+    auto wait_one = [&](uint64_t *bar, unsigned parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        const unsigned long long t0 = global_ns();
 #pragma unroll 1
-            while (!ok) {
-                ok = mbar_try_wait(bar, parity);
-                if (!ok && (*sAbort || global_ns() - t0 > kWaitNs)) break;
+        while (!mbar_try_wait(bar, parity))
+            if (*sAbort || global_ns() - t0 > kWaitNs) {
+                *sAbort = 1;
+                return false;
             }
-        }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) *sAbort = 1;
-        return ok;
+        return true;
     };
+    // The same of a whole warp.
+    auto wait_bar = [&](uint64_t *bar, unsigned parity) -> bool { return __all_sync(0xffffffffu, wait_one(bar, parity)); };
 
     int stages = 0;             // stages used so far
     unsigned uses[2] = {0, 0};  // S / P slots: blocks so far
-    bool covered = false;
+    unsigned queries = 0;       // items with rows so far
+    int nth = 0;                // items taken from the scheduler so far
+    bool ok = true;
+    unsigned answers = 0;
+
+    // The copies of one item (one thread).
+    auto copy_item = [&](const Item &w) {
+        if (queries > 0) ok = ok && wait_one(q_empty, (queries - 1) & 1);
+        if (!ok) return;
+        unsigned bytes = 0;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) bytes += w.last[t] > w.first[t] ? DP / 64 * p.tokens * p.G * 128 : 0;
+        mbar_expect_tx(q_full, bytes);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            if (w.last[t] > w.first[t])
 #pragma unroll 1
-    for (int careful = 0; careful < 2; ++careful) {
-        const int begin = stages;
-        if (warp == kWarpTma) {
-            // ---------------- copies
-            if (!careful && lane == 0) {
-                unsigned bytes = 0;
+                for (int c = 0; c < DP / 64; ++c)
+                    tma_load_3d(sQ + t * C::kQTile + c * C::kPart, &p.tmap_q, q_full, c * 64, w.h * p.G, w.sg.q0 + w.token0 + t * p.tokens);
+        ++queries;
+        auto load = [&](const CUtensorMap *map, int block) {
+#pragma unroll 1
+            for (int c = 0; ok && c < SPB; ++c) {
+                const int st = stages % NST;
+                if (stages >= NST) ok = wait_one(empty + st, ((stages / NST) - 1) & 1);
+                if (!ok) break;
+                mbar_expect_tx(full + st, C::kStage);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) bytes += last[t] > first[t] ? DP / 64 * p.tokens * p.G * 128 : 0;
-                mbar_expect_tx(q_full, bytes);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    if (last[t] > first[t])
-                        for (int c = 0; c < DP / 64; ++c)
-                            tma_load_3d(sQ + t * C::kQTile + c * C::kPart, &p.tmap_q, q_full, c * 64, h * p.G, sg.q0 + token0 + t * p.tokens);
+                for (int x = 0; x < C::kCols / 64; ++x)
+                    tma_load_3d(ring + (size_t)st * C::kStage + x * C::kPart, map, full + st, c * C::kCols + x * 64, w.h, w.sg.q0 + block * C::kKeys);
+                ++stages;
             }
-            __syncwarp();
-            bool ok = true;
-            auto load = [&](const CUtensorMap *map, int block) {
+        };
+        load(&p.tmap_k, w.b0);
 #pragma unroll 1
-                for (int c = 0; ok && c < SPB; ++c) {
-                    const int st = stages % NST;
-                    if (stages >= NST) ok = wait_bar(empty + st, ((stages / NST) - 1) & 1);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        mbar_expect_tx(full + st, C::kStage);
+        for (int j = w.b0; ok && j < w.b1; ++j) {
+            // the order in which the products take them
+            if (NT == 1 && j + 1 < w.b1) load(&p.tmap_k, j + 1);
+            load(&p.tmap_v, j);
+            if (NT == 2 && j + 1 < w.b1) load(&p.tmap_k, j + 1);
+        }
+    };
+    // The products of one item (one thread).
+    const unsigned q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
+    auto multiply_item = [&](const Item &w) {
+        const uint32_t id_s = umma_idesc_bf16(128, 128, 0), id_o = umma_idesc_bf16(128, C::kCols, 1);
+        auto block_ready = [&](int i) {
+            bool r = true;
 #pragma unroll
-                        for (int x = 0; x < C::kCols / 64; ++x)
-                            tma_load_3d(ring + (size_t)st * C::kStage + x * C::kPart, map, full + st, c * C::kCols + x * 64, h, sg.q0 + block * C::kKeys);
-                    }
-                    __syncwarp();
-                    ++stages;
+            for (int c = 0; c < SPB; ++c) r = r && wait_one(full + (i + c) % NST, ((i + c) / NST) & 1);
+            return r;
+        };
+        auto release = [&](int i) {  // once what has been issued so far is done
+#pragma unroll
+            for (int c = 0; c < SPB; ++c) umma_commit(empty + (i + c) % NST);
+        };
+        // S of tile t and the block whose stages begin at i, into slot; P that was there has been read
+        auto issue_s = [&](int t, int i, int slot) {
+            if (uses[slot] > 0 && !wait_one(pv_done + slot, (uses[slot] - 1) & 1)) return false;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < SPB; ++c) {
+                const uint64_t qd = umma_desc(q_addr + t * C::kQTile + c * (C::kCols / 64) * C::kPart, 16, 1024);
+                const uint64_t kd = umma_desc(ring_addr + (unsigned)((i + c) % NST) * C::kStage, 16, 1024);
+#pragma unroll
+                for (int k = 0; k < C::kCols / 16; ++k) {  // (an address moves in units of 16 bytes)
+                    const unsigned off = ((k >> 2) * C::kPart + (k & 3) * 32) >> 4;
+                    umma_bf16(tmem + slot * 128, qd + off, kd + off, id_s, c > 0 || k > 0 ? 1 : 0);
                 }
-            };
-            load(&p.tmap_k, b0);
-#pragma unroll 1
-            for (int j = b0; ok && j < b1; ++j) {
-                // the order in which the products take them
-                if (NT == 1 && j + 1 < b1) load(&p.tmap_k, j + 1);
-                load(&p.tmap_v, j);
-                if (NT == 2 && j + 1 < b1) load(&p.tmap_k, j + 1);
             }
-            if (!ok) {  // copies in flight get a bounded chance to land
-                if (lane == 0)
-#pragma unroll 1
-                    for (int i = max(0, stages - NST); i < stages; ++i)
-                        if (!mbar_wait_ns(full + i % NST, (i / NST) & 1)) break;
-                __syncwarp();
-            }
-            if (!covered) prompt_coverage(p, lane);
-            covered = true;
-        } else if (warp == kWarpMma) {
-            // ---------------- products
-            const uint32_t id_s = umma_idesc_bf16(128, 128, 0), id_o = umma_idesc_bf16(128, C::kCols, 1);
-            const unsigned q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
-            bool ok = careful || wait_bar(q_full, 0);
-            auto stage_ready = [&](int i) { return wait_bar(full + i % NST, (i / NST) & 1); };
-            // S of tile t and the block whose stages begin at i, into slot
-            auto issue_s = [&](int t, int i, int slot) {
+            umma_commit(s_full + slot);
+            return true;
+        };
+        // O of tile t += P in slot times the V block whose stages begin at i
+        auto issue_pv = [&](int t, int i, int slot, bool fresh) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (!wait_one((half ? p_full : p_half) + slot, uses[slot] & 1)) return false;
                 tc_fence_after();
-                if (lane == 0) {
 #pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        const unsigned k_addr = ring_addr + (unsigned)((i + k / (C::kCols / 16)) % NST) * C::kStage;
-                        umma_bf16(tmem + slot * 128, umma_desc(q_addr + t * C::kQTile + (k >> 2) * C::kPart + (k & 3) * 32, 16, 1024),
-                                  umma_desc(k_addr + (k % (C::kCols / 16) >> 2) * C::kPart + (k & 3) * 32, 16, 1024), id_s, k > 0 ? 1 : 0);
-                    }
-                    umma_commit(s_full + slot);
+                for (int c = 0; c < SPB; ++c) {
+                    const uint64_t vd = umma_desc(ring_addr + (unsigned)((i + c) % NST) * C::kStage, C::kPart, 1024);
+#pragma unroll
+                    for (int u = 4 * half; u < 4 * half + 4; ++u)
+                        umma_bf16_ts(tmem + C::kColO + t * DP + c * C::kCols, tmem + slot * 128 + u * 8, vd + (u * 2048 >> 4), id_o, (!fresh || u > 0) ? 1 : 0);
                 }
-                __syncwarp();
-            };
-            // O of tile t += P in slot times the V block whose stages begin at i
-            auto issue_pv = [&](int t, int i, int slot, bool fresh) {
-                tc_fence_after();
-                if (lane == 0) {
-#pragma unroll
-                    for (int c = 0; c < SPB; ++c) {
-                        const unsigned v_addr = ring_addr + (unsigned)((i + c) % NST) * C::kStage;
-#pragma unroll
-                        for (int u = 0; u < C::kKeys / 16; ++u)
-                            umma_bf16_ts(tmem + C::kColO + t * DP + c * C::kCols, tmem + slot * 128 + u * 8, umma_desc(v_addr + u * 2048, C::kPart, 1024),
-                                         id_o, (!fresh || u > 0) ? 1 : 0);
-                    }
-                    umma_commit(pv_done + slot);
-                }
-                __syncwarp();
-                ++uses[slot];
-            };
-            auto release = [&](int i) {  // once what has been issued so far is done
-                if (lane == 0)
-#pragma unroll
-                    for (int c = 0; c < SPB; ++c) umma_commit(empty + (i + c) % NST);
-                __syncwarp();
-            };
-            auto block_ready = [&](int i) {
-                bool r = true;
-                for (int c = 0; r && c < SPB; ++c) r = stage_ready(i + c);
-                return r;
-            };
-            ok = ok && block_ready(stages);
-            if (ok) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    if (b0 >= first[t] && b0 < last[t]) issue_s(t, stages, t);
-                release(stages);
             }
-            stages += SPB;
-#pragma unroll 1
-            for (int j = b0; ok && j < b1; ++j) {
-                const bool more = j + 1 < b1;
-                if constexpr (NT == 2) {
-                    const int v = stages, k = stages + SPB;
-                    ok = block_ready(v);
-                    bool k_ready = false;
+            umma_commit(pv_done + slot);
+            ++uses[slot];
+            return true;
+        };
+        ok = ok && wait_one(q_full, queries & 1) && block_ready(stages);
+        ++queries;
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const bool here = j >= first[t] && j < last[t], next = more && j + 1 >= first[t] && j + 1 < last[t];
-                        if (ok && here) {
-                            ok = wait_bar(p_full + t, uses[t] & 1);
-                            if (ok) issue_pv(t, v, t, j == first[t]);
-                        }
-                        if (ok && next) {
-                            if (!k_ready) ok = block_ready(k);
-                            k_ready = true;
-                            if (ok && here) ok = wait_bar(pv_done + t, (uses[t] - 1) & 1);  // P is read: S may go over it
-                            if (ok) issue_s(t, k, t);
-                        }
+        for (int t = 0; t < NT; ++t)
+            if (ok && w.b0 >= w.first[t] && w.b0 < w.last[t]) ok = issue_s(t, stages, t);
+        if (ok) {
+            release(stages);
+            if (w.b0 + 1 == w.b1) umma_commit(q_empty);
+        }
+        stages += SPB;
+#pragma unroll 1
+        for (int j = w.b0; ok && j < w.b1; ++j) {
+            const bool more = j + 1 < w.b1;
+            if constexpr (NT == 2) {
+                const int v = stages, k = stages + SPB;
+                bool k_ready = false;
+                ok = block_ready(v);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    if (ok && j >= w.first[t] && j < w.last[t]) ok = issue_pv(t, v, t, j == w.first[t]);
+                    if (ok && more && j + 1 >= w.first[t] && j + 1 < w.last[t]) {
+                        if (!k_ready) ok = block_ready(k);
+                        k_ready = true;
+                        ok = ok && issue_s(t, k, t);
                     }
-                    if (ok) {
-                        release(v);
-                        if (more) release(k);
-                    }
-                    stages += more ? 2 * SPB : SPB;
-                } else {
-                    const int slot = (j - b0) & 1;
+                }
+                if (ok) {
+                    release(v);
                     if (more) {
-                        ok = block_ready(stages);
-                        if (ok && j > b0) ok = wait_bar(pv_done + (slot ^ 1), (uses[slot ^ 1] - 1) & 1);
-                        if (ok) {
-                            issue_s(0, stages, slot ^ 1);
-                            release(stages);
-                        }
-                        stages += SPB;
+                        release(k);
+                        if (j + 2 == w.b1) umma_commit(q_empty);
                     }
-                    ok = ok && block_ready(stages) && wait_bar(p_full + slot, uses[slot] & 1);
+                }
+                stages += more ? 2 * SPB : SPB;
+            } else {
+                const int slot = (j - w.b0) & 1;
+                if (more) {
+                    ok = block_ready(stages) && issue_s(0, stages, slot ^ 1);
                     if (ok) {
-                        issue_pv(0, stages, slot, j == b0);
                         release(stages);
+                        if (j + 2 == w.b1) umma_commit(q_empty);
                     }
                     stages += SPB;
                 }
+                ok = ok && block_ready(stages) && issue_pv(0, stages, slot, j == w.b0);
+                if (ok) release(stages);
+                stages += SPB;
             }
-            if (!ok && lane == 0) {  // every product issued has completed before TMEM is freed
-                umma_commit(drain);
-                mbar_wait_ns(drain, 0);
-            }
-            __syncwarp();
-        } else {
-            // ---------------- softmax
-            const int t = warp >> 2, r = tid & 127;  // tile, row of it
-            const unsigned lane_off = (unsigned)(32 * (warp & 3)) << 16;
-            const int token = token0 + t * p.tokens + r / p.G;
-            const bool real = r < p.tokens * p.G && token < sg.ql;
-            int lo_r = 0, hi_r = 0;
-            if (real) row_key_bounds(token, sg.ql, p.causal, p.window, 0, lo_r, hi_r);
-            const float sc = p.scale_log2;
-            float m = kNoScore, l = 0.f;
-            bool ok = true;
-            const int f = NT == 2 ? first[t] : b0, e = NT == 2 ? last[t] : b1;
+        }
+    };
+    // The rows of one item (a softmax warp).
+    auto rows_of_item = [&](const Item &w, int id, bool careful) {
+        const int t = warp >> 2, r = tid & 127;  // tile, row of it
+        const unsigned lane_off = (unsigned)(32 * (warp & 3)) << 16;
+        const int token = w.token0 + t * p.tokens + r / p.G, begin = stages;
+        const bool real = r < p.tokens * p.G && token < w.sg.ql;
+        stages += 2 * SPB * (w.b1 - w.b0);
+        int lo_r = 0, hi_r = 0;
+        if (real) row_key_bounds(token, w.sg.ql, p.causal, p.window, 0, lo_r, hi_r);
+        const float sc = p.scale_log2;
+        float m = kNoScore, l = 0.f;
+        const int f = NT == 2 ? w.first[t] : w.b0, e = NT == 2 ? w.last[t] : w.b1;
+        if (e <= f) return;
 #pragma unroll 1
-            for (int j = f; ok && j < e; ++j) {
-                const int slot = NT == 2 ? t : (j - b0) & 1;
-                const unsigned s_addr = tmem + lane_off + slot * 128;
-                if (!(ok = wait_bar(s_full + slot, uses[slot] & 1))) break;
-                tc_fence_after();
-                unsigned x[4][32];
+        for (int j = f; ok && j < e; ++j) {
+            const int slot = NT == 2 ? t : (j - w.b0) & 1;
+            const unsigned s_addr = tmem + lane_off + slot * 128;
+            if (!(ok = wait_bar(s_full + slot, uses[slot] & 1))) break;
+            tc_fence_after();
+            unsigned x[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32_async(s_addr + 32 * c, x[c]);
-                tmem_wait_ld();
-                const int pos0 = j * C::kKeys;
-                if (!__all_sync(0xffffffffu, !real || (pos0 >= lo_r && pos0 + C::kKeys <= hi_r))) {
-                    const int a = lo_r - pos0, b = hi_r - pos0;
+            for (int c = 0; c < 4; ++c) tmem_ld32_async(s_addr + 32 * c, x[c]);
+            tmem_wait_ld();
+            const int pos0 = j * C::kKeys;
+            if (!__all_sync(0xffffffffu, !real || (pos0 >= lo_r && pos0 + C::kKeys <= hi_r))) {
+                const int a = lo_r - pos0, b = hi_r - pos0;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (32 * c + k < a || 32 * c + k >= b) x[c][k] = 0xff800000u;
-                }
-                float mx = -CUDART_INF_F;
+                    for (int k = 0; k < 32; ++k)
+                        if (32 * c + k < a || 32 * c + k >= b) x[c][k] = 0xff800000u;
+            }
+            float mx;
+            {   // row maximum as a tree of three-way maxima
+                float y[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    float y[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+                    float z[11];
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) y[i] = fmaxf(y[i], __uint_as_float(x[c][k + i]));
-                    mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+                    for (int k = 0; k < 10; ++k)
+                        z[k] = max3(__uint_as_float(x[c][3 * k]), __uint_as_float(x[c][3 * k + 1]), __uint_as_float(x[c][3 * k + 2]));
+                    z[10] = fmaxf(__uint_as_float(x[c][30]), __uint_as_float(x[c][31]));
+                    y[c] = max3(max3(max3(z[0], z[1], z[2]), max3(z[3], z[4], z[5]), max3(z[6], z[7], z[8])), z[9], z[10]);
                 }
-                mx *= sc;
-                const bool grow = mx > m + kPromptLazy;
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float m_new = grow ? mx : m, alpha = exp2_fast(m - m_new);
-                    if (j > f && __any_sync(0xffffffffu, grow && m != kNoScore)) {
-                        // the product before is done: with two tiles S came after it, with two slots it is waited for
-                        if (NT == 1 && !(ok = wait_bar(pv_done + (slot ^ 1), (uses[slot ^ 1] - 1) & 1))) break;
-                        tc_fence_after();
+                mx = fmaxf(max3(y[0], y[1], y[2]), y[3]) * sc;
+            }
+            const bool grow = mx > m + kPromptLazy;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float m_new = grow ? mx : m, alpha = exp2_fast(m - m_new);
+                if (j > f && __any_sync(0xffffffffu, grow && m != kNoScore)) {
+                    // the product before is done: with two tiles S came after it, with two slots it is waited for
+                    if (NT == 1 && !(ok = wait_bar(pv_done + (slot ^ 1), (uses[slot ^ 1] - 1) & 1))) break;
+                    tc_fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < DP; c0 += 32) {
-                            float o[32];
-                            tmem_ld32(tmem + lane_off + C::kColO + t * DP + c0, o);
+                    for (int c0 = 0; c0 < DP; c0 += 32) {
+                        float o[32];
+                        tmem_ld32(tmem + lane_off + C::kColO + t * DP + c0, o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= alpha;
-                            tmem_st32(tmem + lane_off + C::kColO + t * DP + c0, o);
-                        }
+                        for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                        tmem_st32(tmem + lane_off + C::kColO + t * DP + c0, o);
                     }
-                    l *= alpha;
-                    m = m_new;
                 }
-                const uint64_t sc2 = f32x2(sc, sc), m2 = f32x2(-m, -m);
-                uint64_t la = 0, lb = 0;
+                l *= alpha;
+                m = m_new;
+            }
+            const uint64_t sc2 = f32x2(sc, sc), m2 = f32x2(-m, -m);
+            uint64_t la = 0, lb = 0;
+            const bool zero_v = careful && !(pos0 >= w.in_lo && pos0 + C::kKeys <= w.in_hi);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    unsigned pk[16];
+            for (int c = 0; c < 4; ++c) {
+                unsigned pk[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        float e0, e1;
-                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c][2 * k]), __uint_as_float(x[c][2 * k + 1])), sc2, m2), e0, e1);
-                        e0 = exp2_fast(e0);
-                        e1 = exp2_fast(e1);
-                        if (k & 1) lb = add_f32x2(lb, f32x2(e0, e1));
-                        else la = add_f32x2(la, f32x2(e0, e1));
-                        pk[k] = pack_bf16x2(e0, e1);
-                    }
-                    tmem_st16(s_addr + 16 * c, pk);
+                for (int k = 0; k < 16; ++k) {
+                    float e0, e1;
+                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(x[c][2 * k]), __uint_as_float(x[c][2 * k + 1])), sc2, m2), e0, e1);
+                    e0 = exp2_fast(e0);
+                    e1 = exp2_fast(e1);
+                    if (k & 1) lb = add_f32x2(lb, f32x2(e0, e1));
+                    else la = add_f32x2(la, f32x2(e0, e1));
+                    pk[k] = pack_bf16x2(e0, e1);
                 }
-                {
-                    float l0, l1;
-                    f32x2_split(add_f32x2(la, lb), l0, l1);
-                    l += l0 + l1;
-                }
-                if (careful && !(pos0 >= in_lo && pos0 + C::kKeys <= in_hi)) {
-                    // V rows that not every row of the item sees: what is not finite reads zero
-                    const int i0 = begin + SPB * (NT == 2 ? 2 * (j - b0) + 1 : (min(j + 1, b1 - 1) - b0 + 1) + (j - b0));
-                    const int key = pos0 + r;
-#pragma unroll 1
-                    for (int c = 0; ok && c < SPB; ++c) {
-                        ok = wait_bar(full + (i0 + c) % NST, ((i0 + c) / NST) & 1);
-                        if (!ok || (key >= in_lo && key < in_hi)) continue;
-#pragma unroll 1
-                        for (int x8 = 0; x8 < C::kCols / 8; ++x8) {
-                            uint4 *at = reinterpret_cast<uint4 *>(ring + (size_t)((i0 + c) % NST) * C::kStage + (x8 >> 3) * C::kPart + r * 128 + (x8 & 7) * 16);
-                            uint4 v = *at;
-                            unsigned u[4] = {v.x, v.y, v.z, v.w};
-                            bool odd = false;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (!not_finite(u[i])) continue;
-                                odd = true;
-                                if ((u[i] & 0x7f80u) == 0x7f80u) u[i] &= 0xffff0000u;
-                                if ((u[i] & 0x7f800000u) == 0x7f800000u) u[i] &= 0xffffu;
-                            }
-                            if (odd) *at = make_uint4(u[0], u[1], u[2], u[3]);
-                        }
-                    }
+                tmem_st16_async(s_addr + 16 * c, pk);
+                if (c == 1 && !zero_v) {  // the first keys' weights are there: their products may start
+                    tmem_wait_st();
+                    tc_fence_before();
                     __syncwarp();
-                    fence_proxy_async();
-                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(p_half + slot);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + slot);
-                ++uses[slot];
             }
-            // ---- the rows' ends: the last product has landed
-            if (e > f) {
-                const int slot = NT == 2 ? t : (e - 1 - b0) & 1;
-                if (ok) ok = wait_bar(pv_done + slot, (uses[slot] - 1) & 1);
-                tc_fence_after();
-                const long long row = (long long)sg.q0 + (real ? token : 0);
-                const int hq = h * p.G + (real ? r % p.G : 0);
-                const bool zero = !ok || l == 0.f;
-                const float inv = 1.f / l;
-                bool odd = false;
+            {
+                float l0, l1;
+                f32x2_split(add_f32x2(la, lb), l0, l1);
+                l += l0 + l1;
+            }
+            if (zero_v) {
+                // V rows that not every row of the item sees: what is not finite reads zero
+                const int i0 = begin + SPB * (NT == 2 ? 2 * (j - w.b0) + 1 : (min(j + 1, w.b1 - 1) - w.b0 + 1) + (j - w.b0));
+                const int key = pos0 + r;
 #pragma unroll 1
-                for (int c0 = 0; c0 < DP; c0 += 32) {
-                    float o[32];
-                    tmem_ld32(tmem + lane_off + C::kColO + t * DP + c0, o);
-                    if (!real) continue;
-                    if (careful) {
-                        float y[32];
+                for (int c = 0; ok && c < SPB; ++c) {
+                    ok = wait_bar(full + (i0 + c) % NST, ((i0 + c) / NST) & 1);
+                    if (!ok || (key >= w.in_lo && key < w.in_hi)) continue;
+#pragma unroll 1
+                    for (int x8 = 0; x8 < C::kCols / 8; ++x8) {
+                        uint4 *at = reinterpret_cast<uint4 *>(ring + (size_t)((i0 + c) % NST) * C::kStage + (x8 >> 3) * C::kPart + r * 128 + (x8 & 7) * 16);
+                        uint4 v = *at;
+                        unsigned u[4] = {v.x, v.y, v.z, v.w};
+                        bool odd = false;
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k] = o[k];
-#pragma unroll 1
-                        for (int key = lo_r; key < hi_r; ++key) {
-                            if (key >= in_lo && key < in_hi) key = in_hi;  // (those every row sees were not touched)
-                            if (key < hi_r) prompt_add_key(p, (long long)sg.q0 + key, row, h, hq, c0, m, y);
+                        for (int i = 0; i < 4; ++i) {
+                            if (!not_finite(u[i])) continue;
+                            odd = true;
+                            if ((u[i] & 0x7f80u) == 0x7f80u) u[i] &= 0xffff0000u;
+                            if ((u[i] & 0x7f800000u) == 0x7f800000u) u[i] &= 0xffffu;
                         }
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = y[k];
+                        if (odd) *at = make_uint4(u[0], u[1], u[2], u[3]);
                     }
-                    float sum = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) sum += o[k] * 0.f;  // NaN where one is not finite
-                    odd |= sum != 0.f;
-#pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        if (c0 + k < p.D)
-                            prompt_store4(p, (row * p.Hq + hq) * p.D + c0 + k,
-                                          zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o[k] * inv, o[k + 1] * inv, o[k + 2] * inv, o[k + 3] * inv));
                 }
-                if (real && p.lse) p.lse[row * p.Hq + hq] = zero ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
-                if (odd && l == l) *sOdd = 1;  // (a NaN sum: its own scores hold one)
-                tc_fence_before();
+                __syncwarp();
+                fence_proxy_async();
+                if (!ok) break;
             }
-            stages += 2 * SPB * (b1 - b0);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (zero_v) mbar_arrive(p_half + slot);
+                mbar_arrive(p_full + slot);
+            }
+            ++uses[slot];
+        }
+        // ---- the rows' ends: the last product has landed
+        const int slot = NT == 2 ? t : (e - 1 - w.b0) & 1;
+        if (ok) ok = wait_bar(pv_done + slot, (uses[slot] - 1) & 1);
+        tc_fence_after();
+        const long long row = (long long)w.sg.q0 + (real ? token : 0);
+        const int hq = w.h * p.G + (real ? r % p.G : 0);
+        const bool zero = !ok || l == 0.f;
+        const float inv = zero ? 0.f : 1.f / l;
+        const long long at = (row * p.Hq + hq) * p.D;
+        bool odd = false;
+#pragma unroll 1
+        for (int c0 = 0; c0 < DP; c0 += 32) {
+            unsigned x[32];
+            tmem_ld32_async(tmem + lane_off + C::kColO + t * DP + c0, x);
+            tmem_wait_ld();
+            float o[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __uint_as_float(x[k]);
+            if (!real) continue;
+            if (careful) {
+                float y[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) y[k] = o[k];
+#pragma unroll 1
+                for (int key = lo_r; key < hi_r; ++key) {
+                    if (key >= w.in_lo && key < w.in_hi) key = w.in_hi;  // (those every row sees were not touched)
+                    if (key < hi_r) prompt_add_key(p, (long long)w.sg.q0 + key, row, w.h, hq, c0, m, y);
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = y[k];
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+                sum = fmaf(o[k], 0.f, sum);  // NaN where one is not finite
+                o[k] = zero ? 0.f : o[k] * inv;
+            }
+            odd |= sum != 0.f;
+            if (p.out_bf16) {
+                __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(p.out) + at + c0;
+                if (c0 + 32 <= p.D) {
+                    const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 16) {
+                        unsigned v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = pack_bf16x2(o[k + 2 * i], o[k + 2 * i + 1]);
+                        store32(dst + k, v, wide);
+                    }
+                    continue;
+                }
+            } else if (c0 + 32 <= p.D) {
+                float *dst = reinterpret_cast<float *>(p.out) + at + c0;
+                const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    unsigned v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(o[k + i]);
+                    store32(dst + k, v, wide);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+                if (c0 + k < p.D) prompt_store4(p, at + c0 + k, make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
+        }
+        if (real && p.lse) p.lse[row * p.Hq + hq] = zero ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
+        // (a row with a NaN sum has one among its own scores)
+        if (!careful && ok && __any_sync(0xffffffffu, odd && l == l) && lane == 0) {
+            const int n = atomicAdd(const_cast<int *>(sCount), 1);
+            sOdd[n % C::kOdd] = id;  // (never that many: see below)
+        }
+        __syncwarp();
+        tc_fence_before();
+    };
+
+    // What a CTA does: items until none is left, or until the list of those to run again is nearly
+    // full (the items on their way may each add one a softmax warp); then that list.
+    constexpr int kListRoom = C::kOdd - (SCHED + 1) * C::kSoftmaxWarps;
+    static_assert(kListRoom > 0, "the list holds what the items on their way may add");
+    // Waits on the scheduler last as long as an item may take, and end whatever has happened to the others.
+    auto wait_long = [&](uint64_t *bar, unsigned parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        const unsigned long long t0 = global_ns();
+#pragma unroll 1
+        while (!mbar_try_wait(bar, parity))
+            if (global_ns() - t0 > 100 * kWaitNs) {
+                *sAbort = 1;
+                return false;
+            }
+        return true;
+    };
+    // The next item of a role but the copies', or -1 (a whole warp).
+    auto take = [&]() -> int {
+        const int i = nth++ % SCHED;
+        const bool got = __all_sync(0xffffffffu, wait_long(sched_full + i, ((nth - 1) / SCHED) & 1));
+        const int id = got ? sItem[i] : -1;
+        __syncwarp();
+        if (got && lane == 0) mbar_arrive(sched_empty + i);
+        ok = ok && got;
+        return id;
+    };
+    // The end of a phase, which all roles come to: items of the list once more; true where none is left after it.
+    auto phase_over = [&](auto &&again) -> bool {
+        __syncthreads();
+        const int n = min(*sCount, C::kOdd);
+#pragma unroll 1
+        for (int i = 0; i < n && !*sAbort; ++i) {
+            bool twice = false;  // (each warp of an item may have put it there)
+            for (int k = 0; k < i; ++k) twice |= sOdd[k] == sOdd[i];
+            if (!twice) again(sOdd[i]);
+            __syncwarp();
         }
         __syncthreads();
-        if (careful || *sAbort || !*sOdd) break;
+        const bool done = *sNext < 0 || *sAbort;
+        __syncthreads();
+        if (tid == 0) *sCount = 0;
+        return done;
+    };
+    Item w;
+    if (warp < C::kSoftmaxWarps) {
+        if constexpr (C::kRegsSoftmax > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kRegsSoftmax));
+        do {
+#pragma unroll 1
+            for (int id = take(); id >= 0; id = take()) {
+                w.load(p, id);
+                if (w.tokens > 0) rows_of_item(w, id, false);
+            }
+        } while (!phase_over([&](int id) {
+            w.load(p, id);
+            rows_of_item(w, id, true);
+        }));
+    } else {
+        if constexpr (C::kRegsSoftmax > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsOthers));
+        if (warp == kWarpMma) {
+            do {
+#pragma unroll 1
+                for (int id = take(); id >= 0; id = take()) {
+                    w.load(p, id);
+                    if (w.tokens > 0 && lane == 0) multiply_item(w);
+                    __syncwarp();
+                }
+            } while (!phase_over([&](int id) {
+                w.load(p, id);
+                if (lane == 0) multiply_item(w);
+            }));
+        } else if (warp == kWarpTma) {
+            do {
+                if (lane == 0) {
+                    int id = *sNext;
+#pragma unroll 1
+                    for (;;) {
+                        const int i = nth % SCHED;
+                        if (nth >= SCHED) ok = wait_long(sched_empty + i, ((nth / SCHED) - 1) & 1) && ok;
+                        const bool rest = ok && *sCount >= kListRoom;
+                        sItem[i] = rest ? -1 : id;
+                        mbar_arrive(sched_full + i);
+                        ++nth;
+                        if (rest || id < 0) break;
+                        const bool ask = ok && !*sAbort;  // (after a timeout the others still write this item's zeros)
+                        if (ask) {
+                            fence_proxy_async();  // the answer before has been read
+                            mbar_expect_tx(asked, 16);
+                            ask_next(answer, asked);
+                        }
+                        w.load(p, id);
+                        if (w.tokens > 0 && ok) copy_item(w);
+                        id = -1;
+                        if (ask) {
+                            if (wait_long(asked, answers & 1)) id = next_of(answer);
+                            else ok = false;
+                            ++answers;
+                        }
+                    }
+                    *sNext = id;
+                }
+                __syncwarp();
+            } while (!phase_over([&](int id) {
+                w.load(p, id);
+                if (lane == 0) copy_item(w);
+            }));
+        } else {
+            do {
+#pragma unroll 1
+                for (int id = take(); id >= 0; id = take()) {
+                    if (warp != kWarpCover) continue;
+                    w.load(p, id);
+                    prompt_coverage(p, id, lane);
+                    if (w.fault && w.index == 0) {  // (one warp writes its rows)
+                        if (lane == 0) atomicOr(p.err, w.fault);
+                        if (w.sg.q0 >= 0)           // a negative q_start covers nothing
+                            for (long long r = w.sg.q0; r < min((long long)w.sg.q0 + w.sg.ql, (long long)p.total_rows); ++r)
+                                prompt_zero(p, r, w.h * p.G, p.G, lane, 32);
+                    }
+                }
+            } while (!phase_over([](int) {}));
+        }
+    }
+    if (*sAbort) {
+        // what is on its way gets a bounded chance to land: copies, then products, before TMEM is freed
+        if (warp == kWarpTma && lane == 0)
+#pragma unroll 1
+            for (int i = max(0, stages - NST); i < stages; ++i)
+                if (!mbar_wait_ns(full + i % NST, (i / NST) & 1)) break;
+        if (warp == kWarpMma && lane == 0) {
+            umma_commit(drain);
+            mbar_wait_ns(drain, 0);
+        }
+        if (tid == 0) atomicOr(p.err, PKV_ERR_TIMEOUT);
+        __syncthreads();
     }
     if (warp == kWarpMma) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512) : "memory");
-    }
-    if (*sAbort) {  // every row of the item reads zero
-        for (int i = warp; i < tokens; i += C::kThreads / 32) prompt_zero(p, (long long)sg.q0 + token0 + i, h * p.G, p.G, lane, 32);
-        if (tid == 0) atomicOr(p.err, PKV_ERR_TIMEOUT);
     }
 }
 

@@ -27,6 +27,7 @@ struct PromptKernel {
     int threads;
     size_t smem;
     int tiles;  // query tiles of a CTA
+    int regs;   // registers a thread the kernel has to be launched with (it hands them between its warps), or 0
 };
 // The kernel for head_dim D (a multiple of 8, at most 256).
 PromptKernel pick_prompt(int head_dim);

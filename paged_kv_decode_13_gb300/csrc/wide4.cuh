@@ -66,11 +66,6 @@ struct Wide4 {
 // four neighbouring groups differ where the swizzle's low bit does not.
 __device__ __forceinline__ int v_turn(int g) { return ((g << 1) & 6) | (g >> 2); }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
 // kind::f16 with fp16 A and B, fp32 D, both K-major.
 __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
