@@ -19,8 +19,8 @@
 //       maximum, write P = 2^(S - reference) as bf16 over the S columns read,
 //       and at the end the normalised rows out.  The reference moves only when a score
 //       passes it by 2^8 (then O is rescaled in TMEM; no product is in flight on it then);
-//   MMA warp    S = Q K^T (M 128, N 128; Q and K in shared memory) and O += P V (P
-//       from TMEM, V as an MN-major tile);
+//   MMA warps   S = Q K^T (M 128, N 128; Q and K in shared memory) and O += P V (P
+//       from TMEM, V as an MN-major tile), two warps: a tile each, or S and P V;
 //   copy warp   asks for the next item; Q, then K and V blocks through a ring of stages
 //       (TMA, 128-byte swizzle; rows past the tensor and columns past head_dim come as zeros);
 //   cover warp  rows of no segment, rows of two, refused segments.
@@ -66,7 +66,7 @@ struct PromptCfg {
     static_assert(kSoftmaxWarps * 32 * kRegsSoftmax + 128 * kRegsOthers <= kThreads * kRegs || NT == 1, "the roles' registers fit the launch's");
     static constexpr int kSched = 4;                                // items on their way through the roles
     static constexpr int kOdd = 64;                                 // items to run again, at most before they are
-    static constexpr int kBars = 2 * NST + 2 + 2 + 4 + 2 + 1 + 2 * kSched + 1;
+    static constexpr int kBars = 2 * NST + 2 + 2 + 4 + 2 + 2 + 2 * kSched + 1;
     static constexpr size_t kSmem = 1024 + (size_t)NT * kQTile + (size_t)NST * kStage + 16 + kBars * 8 + (kSched + kOdd) * 4 + 64;
     static constexpr unsigned kColO = 256;                          // O of tile t at kColO + t * DP
     static_assert(kSmem <= 232448, "exceeds the per-CTA shared memory limit");
@@ -132,30 +132,23 @@ __device__ __noinline__ void prompt_coverage(const PromptParams &p, int id, int 
 }
 __device__ __forceinline__ bool not_finite(unsigned bf16_pair) { return (bf16_pair & 0x7f80u) == 0x7f80u || (bf16_pair & 0x7f800000u) == 0x7f800000u; }
 
-// Products of the non-finite V values of one key that were zeroed, added to columns c0 .. c0 + 31 of a row.
-__device__ __noinline__ void prompt_add_key(const PromptParams &p, long long key_row, long long q_row, int h, int hq, int c0, float m, float (&o)[32]) {
+// Products of the non-finite V values of one key that were zeroed, added to columns c0 .. c0 + 31 of a row.  (Rare, and short.)
+__device__ __noinline__ void prompt_add_key(const PromptParams &p, long long key_row, long long q_row, int h, int hq, int c0, float m, float *o) {
     const __nv_bfloat16 *v = p.v + key_row * p.v_stride + (long long)h * p.D + c0;
-    float w = 0.f;
-    bool known = false;
-#pragma unroll
-    for (int c = 0; c < 32; c += 8) {
-        if (c0 + c >= p.D) break;
-        const uint4 x = *reinterpret_cast<const uint4 *>(v + c);
-        const unsigned u[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (!not_finite(u[e])) continue;
-            if (!known) {
-                float s = 0.f;
-                for (int d = 0; d < p.D; ++d)
-                    s = fmaf(__bfloat162float(p.q[q_row * p.q_stride + (long long)hq * p.D + d]), __bfloat162float(p.k[key_row * p.k_stride + (long long)h * p.D + d]), s);
-                w = exp2_fast(fmaf(s, p.scale_log2, -m));
-                known = true;
-            }
-            const float lo = __uint_as_float(u[e] << 16), hi = __uint_as_float(u[e] & 0xffff0000u);
-            if (!isfinite(lo)) o[c + 2 * e] = fmaf(w, lo, o[c + 2 * e]);
-            if (!isfinite(hi)) o[c + 2 * e + 1] = fmaf(w, hi, o[c + 2 * e + 1]);
-        }
+    const int n = min(32, p.D - c0);
+    bool some = false;
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) some |= !isfinite(__bfloat162float(v[c]));
+    if (!some) return;
+    const __nv_bfloat16 *q = p.q + q_row * p.q_stride + (long long)hq * p.D, *k = p.k + key_row * p.k_stride + (long long)h * p.D;
+    float s = 0.f;
+#pragma unroll 1
+    for (int d = 0; d < p.D; ++d) s = fmaf(__bfloat162float(q[d]), __bfloat162float(k[d]), s);
+    const float w = exp2_fast(fmaf(s, p.scale_log2, -m));
+#pragma unroll 1
+    for (int c = 0; c < n; ++c) {
+        const float x = __bfloat162float(v[c]);
+        if (!isfinite(x)) o[c] = fmaf(w, x, o[c]);
     }
 }
 
@@ -198,6 +191,35 @@ struct PromptItem {
     }
 };
 
+// The products below are issued by the whole warp with one lane's predicate: no branch, so that
+// descriptors stay in uniform registers (moved there one by one, a product took twice its time).
+// A descriptor is its low word, which the address and leading offset are in, and a constant high word.
+struct UmmaDesc {
+    unsigned lo;
+    __device__ __forceinline__ UmmaDesc(unsigned addr, unsigned lbo) : lo((addr >> 4) & 0x3FFFu | (lbo >> 4) << 16) {}
+};
+constexpr unsigned kUmmaHigh = (1024u >> 4) | 1u << 14 | 2u << 29;  // stride of 8 rows, version, 128-byte swizzle
+__device__ __forceinline__ void umma_ss(unsigned lead, unsigned d_tmem, unsigned a, unsigned b, uint32_t idesc, unsigned accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n mov.b64 x, {%1, %6};\n mov.b64 y, {%2, %6};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(lead), "r"(kUmmaHigh)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts(unsigned lead, unsigned d_tmem, unsigned a_tmem, unsigned b, uint32_t idesc, unsigned accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n mov.b64 y, {%2, %6};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(lead), "r"(kUmmaHigh)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit_by(unsigned lead, uint64_t *bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+
 // Ask for the item of a CTA that has not started: 16 bytes at `at`, completing on `bar`.
 __device__ __forceinline__ void ask_next(uint4 *at, uint64_t *bar) {
     asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(smem_u32(at)),
@@ -237,10 +259,12 @@ __device__ __forceinline__ void tmem_st16_async(unsigned taddr, const unsigned (
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
+constexpr int kPromptProbes = 1 << 20;  // of one barrier phase before a wait is given up (a probe sleeps for a while)
+
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
     constexpr int DP = C::DP, NT = C::NT, NST = C::NST, SPB = C::SPB, SCHED = C::kSched;
-    constexpr int kWarpMma = C::kSoftmaxWarps, kWarpTma = kWarpMma + 1, kWarpCover = kWarpTma + 1;
+    constexpr int kWarpMma = C::kSoftmaxWarps, kWarpTma = kWarpMma + 2;  // then the cover warp
     using Item = PromptItem<NT>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sQ = smem_raw + (-smem_u32(smem_raw) & 1023u);  // pointer arithmetic keeps the shared address space
@@ -249,7 +273,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
     uint64_t *bars = reinterpret_cast<uint64_t *>(answer + 1);
     uint64_t *full = bars, *empty = full + NST, *q_full = empty + NST, *q_empty = q_full + 1, *s_full = q_empty + 1;
     uint64_t *p_half = s_full + 2, *p_full = p_half + 2, *pv_done = p_full + 2, *drain = pv_done + 2;  // P of keys 0-63 and 64-127
-    uint64_t *sched_full = drain + 1, *sched_empty = sched_full + SCHED, *asked = sched_empty + SCHED;
+    uint64_t *sched_full = drain + 2, *sched_empty = sched_full + SCHED, *asked = sched_empty + SCHED;
     int *sItem = reinterpret_cast<int *>(bars + C::kBars), *sOdd = sItem + SCHED;
     unsigned *tslot = reinterpret_cast<unsigned *>(sOdd + C::kOdd);
     volatile int *sAbort = reinterpret_cast<volatile int *>(tslot + 1), *sCount = sAbort + 1, *sNext = sAbort + 2;  // items to run again; the item after them
@@ -259,8 +283,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll 1
         for (int i = 0; i < C::kBars; ++i) {
             uint64_t *b = bars + i;
-            // P: every warp of the tile; an item is released by every warp but the one that copies
-            mbar_init(b, b >= p_half && b < pv_done ? 4 : b >= sched_empty && b < asked ? 3 + C::kSoftmaxWarps : 1);
+            // P: every warp of the tile; an item is released by every warp but the one that copies, a stage and the queries by each tile's products
+            mbar_init(b, b >= p_half && b < pv_done ? 4 : b >= sched_empty && b < asked ? 3 + C::kSoftmaxWarps : (b >= empty && b < q_full) || b == q_empty ? NT : 1);
         }
         fence_barrier_init();
         *sAbort = 0;
@@ -278,13 +302,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
     pdl_wait();
     pdl_trigger();
 
-    // Bounded wait of one thread on one phase; false on a timeout, here or in another role.
+    // Bounded wait of one thread on one phase; false on a timeout, here or in another role.  (The code of what
+    // runs all the time has to stay small: with 250 KB of it the products' warp waited for instructions half its time.)
     auto wait_one = [&](uint64_t *bar, unsigned parity) -> bool {
-        if (mbar_try_wait(bar, parity)) return true;
-        const unsigned long long t0 = global_ns();
+        int left = kPromptProbes;
 #pragma unroll 1
         while (!mbar_try_wait(bar, parity))
-            if (*sAbort || global_ns() - t0 > kWaitNs) {
+            if (--left == 0 || *sAbort) {
                 *sAbort = 1;
                 return false;
             }
@@ -294,7 +318,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
     auto wait_bar = [&](uint64_t *bar, unsigned parity) -> bool { return __all_sync(0xffffffffu, wait_one(bar, parity)); };
 
     int stages = 0;             // stages used so far
-    unsigned uses[2] = {0, 0};  // S / P slots: blocks so far
+    unsigned used = 0, phase = 0;  // bit slot: an S / P slot has been used; how often, modulo two
     unsigned queries = 0;       // items with rows so far
     int nth = 0;                // items taken from the scheduler so far
     bool ok = true;
@@ -337,102 +361,133 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             if (NT == 2 && j + 1 < w.b1) load(&p.tmap_k, j + 1);
         }
     };
-    // The products of one item (one thread).
-    const unsigned q_addr = smem_u32(sQ), ring_addr = smem_u32(ring);
-    auto multiply_item = [&](const Item &w) {
-        const uint32_t id_s = umma_idesc_bf16(128, 128, 0), id_o = umma_idesc_bf16(128, C::kCols, 1);
-        auto block_ready = [&](int i) {
-            bool r = true;
+    // The products, two warps of them (one lane of each issues): with two tiles a warp has a tile, with one the first
+    // has S and the second P V.  A look at an mbarrier takes 110 cycles even if it is open, a commit 60, and an issuing warp
+    // waits behind its products: one warp for all of it left the tensor core idle half the time (4700 cycles for the
+    // blocks of two tiles, 2050 of them products).
+    const unsigned lead = lane == 0;
+    unsigned ring_at = 0, ring_phase = 0;    // the stage to be read next
+    // The stages of the next block, and the way over blocks that are the other warp's.
+    auto next_block = [&](unsigned (&at)[SPB], unsigned (&ph)[SPB]) {
 #pragma unroll
-            for (int c = 0; c < SPB; ++c) r = r && wait_one(full + (i + c) % NST, ((i + c) / NST) & 1);
-            return r;
-        };
-        auto release = [&](int i) {  // once what has been issued so far is done
+        for (int c = 0; c < SPB; ++c) {
+            at[c] = ring_at;
+            ph[c] = ring_phase;
+            if (++ring_at == NST) {
+                ring_at = 0;
+                ring_phase ^= 1;
+            }
+        }
+    };
+    auto block_ready = [&](const unsigned (&at)[SPB], const unsigned (&ph)[SPB]) {
+        bool r = true;
 #pragma unroll
-            for (int c = 0; c < SPB; ++c) umma_commit(empty + (i + c) % NST);
-        };
-        // S of tile t and the block whose stages begin at i, into slot; P that was there has been read
-        auto issue_s = [&](int t, int i, int slot) {
-            if (uses[slot] > 0 && !wait_one(pv_done + slot, (uses[slot] - 1) & 1)) return false;
+        for (int c = 0; c < SPB; ++c) r = r && wait_bar(full + at[c], ph[c]);
+        return r;
+    };
+    auto release = [&](const unsigned (&at)[SPB]) {  // once what has been issued so far is done
+#pragma unroll
+        for (int c = 0; c < SPB; ++c) umma_commit_by(lead, empty + at[c]);
+    };
+    // S of tile t and the block in stages `at`, into slot; P that was there has been read
+    auto issue_s = [&](int t, const unsigned (&at)[SPB], int slot) {
+        const unsigned q_lo = UmmaDesc(smem_u32(sQ), 16).lo + t * (C::kQTile >> 4), k_lo = UmmaDesc(smem_u32(ring), 16).lo;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < SPB; ++c) {
+            const unsigned qd = q_lo + (c * (C::kCols / 64) * C::kPart >> 4), kd = k_lo + at[c] * (C::kStage >> 4);
+#pragma unroll
+            for (int k = 0; k < C::kCols / 16; ++k) {
+                const unsigned off = ((k >> 2) * C::kPart + (k & 3) * 32) >> 4;
+                umma_ss(lead, tmem + slot * 128, qd + off, kd + off, umma_idesc_bf16(128, 128, 0), c > 0 || k > 0);
+            }
+        }
+        umma_commit_by(lead, s_full + slot);
+        release(at);
+    };
+    // O of tile t += P in slot times the V block in stages `at`
+    auto issue_pv = [&](int t, const unsigned (&at)[SPB], int slot, bool fresh) {
+        const unsigned v_lo = UmmaDesc(smem_u32(ring), C::kPart).lo;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (!wait_bar((half ? p_full : p_half) + slot, phase >> slot & 1)) return false;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < SPB; ++c) {
-                const uint64_t qd = umma_desc(q_addr + t * C::kQTile + c * (C::kCols / 64) * C::kPart, 16, 1024);
-                const uint64_t kd = umma_desc(ring_addr + (unsigned)((i + c) % NST) * C::kStage, 16, 1024);
+                const unsigned vd = v_lo + at[c] * (C::kStage >> 4);
 #pragma unroll
-                for (int k = 0; k < C::kCols / 16; ++k) {  // (an address moves in units of 16 bytes)
-                    const unsigned off = ((k >> 2) * C::kPart + (k & 3) * 32) >> 4;
-                    umma_bf16(tmem + slot * 128, qd + off, kd + off, id_s, c > 0 || k > 0 ? 1 : 0);
-                }
+                for (int u = 4 * half; u < 4 * half + 4; ++u)
+                    umma_ts(lead, tmem + C::kColO + t * DP + c * C::kCols, tmem + slot * 128 + u * 8, vd + (u * 2048 >> 4), umma_idesc_bf16(128, C::kCols, 1),
+                            !fresh || u > 0);
             }
-            umma_commit(s_full + slot);
-            return true;
-        };
-        // O of tile t += P in slot times the V block whose stages begin at i
-        auto issue_pv = [&](int t, int i, int slot, bool fresh) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (!wait_one((half ? p_full : p_half) + slot, uses[slot] & 1)) return false;
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < SPB; ++c) {
-                    const uint64_t vd = umma_desc(ring_addr + (unsigned)((i + c) % NST) * C::kStage, C::kPart, 1024);
-#pragma unroll
-                    for (int u = 4 * half; u < 4 * half + 4; ++u)
-                        umma_bf16_ts(tmem + C::kColO + t * DP + c * C::kCols, tmem + slot * 128 + u * 8, vd + (u * 2048 >> 4), id_o, (!fresh || u > 0) ? 1 : 0);
-                }
-            }
-            umma_commit(pv_done + slot);
-            ++uses[slot];
-            return true;
-        };
-        ok = ok && wait_one(q_full, queries & 1) && block_ready(stages);
-        ++queries;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-            if (ok && w.b0 >= w.first[t] && w.b0 < w.last[t]) ok = issue_s(t, stages, t);
-        if (ok) {
-            release(stages);
-            if (w.b0 + 1 == w.b1) umma_commit(q_empty);
         }
-        stages += SPB;
-#pragma unroll 1
-        for (int j = w.b0; ok && j < w.b1; ++j) {
-            const bool more = j + 1 < w.b1;
-            if constexpr (NT == 2) {
-                const int v = stages, k = stages + SPB;
-                bool k_ready = false;
-                ok = block_ready(v);
+        umma_commit_by(lead, pv_done + slot);
+        release(at);
+        phase ^= 1u << slot;
+        return true;
+    };
+    auto multiply_item = [&](const Item &w) {
+        const int which = warp - kWarpMma;
+        unsigned at[SPB], ph[SPB];
+        if constexpr (NT == 2) {
+            const int f = which ? w.first[NT - 1] : w.first[0], e = which ? w.last[NT - 1] : w.last[0];
+            // The other warp's blocks are released by this one too, so that both are done with a stage: not before its
+            // copies are there, or it would be released twice.
+            auto pass = [&]() {
+                if (!block_ready(at, ph)) return false;
+                if (lane == 0)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (ok && j >= w.first[t] && j < w.last[t]) ok = issue_pv(t, v, t, j == w.first[t]);
-                    if (ok && more && j + 1 >= w.first[t] && j + 1 < w.last[t]) {
-                        if (!k_ready) ok = block_ready(k);
-                        k_ready = true;
-                        ok = ok && issue_s(t, k, t);
-                    }
-                }
-                if (ok) {
-                    release(v);
-                    if (more) {
-                        release(k);
-                        if (j + 2 == w.b1) umma_commit(q_empty);
-                    }
-                }
-                stages += more ? 2 * SPB : SPB;
-            } else {
+                    for (int c = 0; c < SPB; ++c) mbar_arrive(empty + at[c]);
+                __syncwarp();
+                return true;
+            };
+            auto scores = [&](int j) {
+                next_block(at, ph);
+                if (j < f || j >= e) return pass();
+                if (!block_ready(at, ph) || ((used >> which & 1) && !wait_bar(pv_done + which, (phase >> which & 1) ^ 1))) return false;
+                issue_s(which, at, which);
+                used |= 1u << which;
+                if (j + 1 == e) umma_commit_by(lead, q_empty);
+                return true;
+            };
+            ok = ok && wait_bar(q_full, queries & 1);
+            ++queries;
+            if (ok && e <= f && lane == 0) mbar_arrive(q_empty);
+            ok = ok && scores(w.b0);
+#pragma unroll 1
+            for (int j = w.b0; ok && j < w.b1; ++j) {
+                next_block(at, ph);
+                ok = j >= f && j < e ? block_ready(at, ph) && issue_pv(which, at, which, j == f) : pass();
+                if (ok && j + 1 < w.b1) ok = scores(j + 1);
+            }
+        } else {
+            if (which == 0) {
+                ok = ok && wait_bar(q_full, queries & 1);
+                ++queries;
+            }
+#pragma unroll 1
+            for (int j = w.b0; ok && j < w.b1; ++j) {
+                // copied in this order: K(b0), K(b0 + 1), V(b0), K(b0 + 2), V(b0 + 1), ..
                 const int slot = (j - w.b0) & 1;
-                if (more) {
-                    ok = block_ready(stages) && issue_s(0, stages, slot ^ 1);
-                    if (ok) {
-                        release(stages);
-                        if (j + 2 == w.b1) umma_commit(q_empty);
+                if (which == 0) {
+                    if (j > w.b0 + 1) next_block(at, ph);  // V(j - 2)
+                    next_block(at, ph);
+                    ok = block_ready(at, ph) && (!(used >> slot & 1) || wait_bar(pv_done + slot, (phase >> slot & 1) ^ 1));
+                    if (!ok) break;
+                    issue_s(0, at, slot);
+                    used |= 1u << slot;
+                    phase ^= 1u << slot;
+                    if (j + 1 == w.b1) {
+                        umma_commit_by(lead, q_empty);
+                        if (j > w.b0) next_block(at, ph);  // V(j - 1), V(j)
+                        next_block(at, ph);
                     }
-                    stages += SPB;
+                } else {
+                    if (j == w.b0) next_block(at, ph);         // K(b0)
+                    if (j + 1 < w.b1) next_block(at, ph);      // K(j + 1)
+                    next_block(at, ph);
+                    ok = block_ready(at, ph) && issue_pv(0, at, slot, j == w.b0);
                 }
-                ok = ok && block_ready(stages) && issue_pv(0, stages, slot, j == w.b0);
-                if (ok) release(stages);
-                stages += SPB;
             }
         }
     };
@@ -447,13 +502,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         if (real) row_key_bounds(token, w.sg.ql, p.causal, p.window, 0, lo_r, hi_r);
         const float sc = p.scale_log2;
         float m = kNoScore, l = 0.f;
-        const int f = NT == 2 ? w.first[t] : w.b0, e = NT == 2 ? w.last[t] : w.b1;
+        // (no index of a run-time value: the item would live in local memory, 500 cycles a look where the products' warp asks between two of them)
+        const int f = NT == 1 ? w.b0 : t ? w.first[NT - 1] : w.first[0], e = NT == 1 ? w.b1 : t ? w.last[NT - 1] : w.last[0];
         if (e <= f) return;
 #pragma unroll 1
         for (int j = f; ok && j < e; ++j) {
             const int slot = NT == 2 ? t : (j - w.b0) & 1;
             const unsigned s_addr = tmem + lane_off + slot * 128;
-            if (!(ok = wait_bar(s_full + slot, uses[slot] & 1))) break;
+            if (!(ok = wait_bar(s_full + slot, phase >> slot & 1))) break;
             tc_fence_after();
             unsigned x[4][32];
 #pragma unroll
@@ -461,12 +517,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             tmem_wait_ld();
             const int pos0 = j * C::kKeys;
             if (!__all_sync(0xffffffffu, !real || (pos0 >= lo_r && pos0 + C::kKeys <= hi_r))) {
-                const int a = lo_r - pos0, b = hi_r - pos0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < 4; ++c) {
+                    // bits of the chunk's keys that the row sees
+                    const int a = lo_r - pos0 - 32 * c, b = hi_r - pos0 - 32 * c;
+                    const unsigned see = (b >= 32 ? ~0u : b <= 0 ? 0u : (1u << b) - 1u) & (a <= 0 ? ~0u : a >= 32 ? 0u : ~0u << a);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (32 * c + k < a || 32 * c + k >= b) x[c][k] = 0xff800000u;
+                    for (int k = 0; k < 32; ++k) x[c][k] = see & (1u << k) ? x[c][k] : 0xff800000u;
+                }
             }
             float mx;
             {   // row maximum as a tree of three-way maxima
@@ -487,7 +545,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
                 const float m_new = grow ? mx : m, alpha = exp2_fast(m - m_new);
                 if (j > f && __any_sync(0xffffffffu, grow && m != kNoScore)) {
                     // the product before is done: with two tiles S came after it, with two slots it is waited for
-                    if (NT == 1 && !(ok = wait_bar(pv_done + (slot ^ 1), (uses[slot ^ 1] - 1) & 1))) break;
+                    if (NT == 1 && !(ok = wait_bar(pv_done + (slot ^ 1), (phase >> (slot ^ 1) & 1) ^ 1))) break;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c0 = 0; c0 < DP; c0 += 32) {
@@ -565,11 +623,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
                 if (zero_v) mbar_arrive(p_half + slot);
                 mbar_arrive(p_full + slot);
             }
-            ++uses[slot];
+            phase ^= 1u << slot;
         }
         // ---- the rows' ends: the last product has landed
         const int slot = NT == 2 ? t : (e - 1 - w.b0) & 1;
-        if (ok) ok = wait_bar(pv_done + slot, (uses[slot] - 1) & 1);
+        if (ok) ok = wait_bar(pv_done + slot, (phase >> slot & 1) ^ 1);
         tc_fence_after();
         const long long row = (long long)w.sg.q0 + (real ? token : 0);
         const int hq = w.h * p.G + (real ? r % p.G : 0);
@@ -650,11 +708,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
     static_assert(kListRoom > 0, "the list holds what the items on their way may add");
     // Waits on the scheduler last as long as an item may take, and end whatever has happened to the others.
     auto wait_long = [&](uint64_t *bar, unsigned parity) -> bool {
-        if (mbar_try_wait(bar, parity)) return true;
-        const unsigned long long t0 = global_ns();
+        int left = 64 * kPromptProbes;
 #pragma unroll 1
         while (!mbar_try_wait(bar, parity))
-            if (global_ns() - t0 > 100 * kWaitNs) {
+            if (--left == 0) {
                 *sAbort = 1;
                 return false;
             }
@@ -670,100 +727,112 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         ok = ok && got;
         return id;
     };
-    // The end of a phase, which all roles come to: items of the list once more; true where none is left after it.
-    auto phase_over = [&](auto &&again) -> bool {
-        __syncthreads();
-        const int n = min(*sCount, C::kOdd);
-#pragma unroll 1
-        for (int i = 0; i < n && !*sAbort; ++i) {
-            bool twice = false;  // (each warp of an item may have put it there)
-            for (int k = 0; k < i; ++k) twice |= sOdd[k] == sOdd[i];
-            if (!twice) again(sOdd[i]);
-            __syncwarp();
-        }
-        __syncthreads();
-        const bool done = *sNext < 0 || *sAbort;
-        __syncthreads();
-        if (tid == 0) *sCount = 0;
-        return done;
-    };
+    // A role's items: those of the scheduler (`next`), then, where all roles have come to the end of
+    // it, those of the list, and so on until none is left.
     Item w;
+    auto all_items = [&](auto &&next, auto &&run) {
+        bool careful = false;
+        int i = 0, n = 0;
+#pragma unroll 1
+        for (;;) {
+            int id = -1;
+            if (!careful) {
+                id = next();
+            } else {
+#pragma unroll 1
+                for (bool twice = true; twice && i < n; ++i) {  // (each warp of an item may have put it there)
+                    id = sOdd[i];
+                    twice = false;
+                    for (int k = 0; k < i; ++k) twice |= sOdd[k] == id;
+                    if (twice) id = -1;
+                }
+                if (*sAbort) id = -1;
+            }
+            if (id >= 0) {
+                run(id, careful);
+                __syncwarp();
+                continue;
+            }
+            __syncthreads();
+            if (!careful) {
+                n = min(*sCount, C::kOdd);
+                i = 0;
+                careful = true;
+                if (n > 0) continue;
+                __syncthreads();
+            }
+            const bool done = *sNext < 0 || *sAbort;
+            if (tid == 0) *sCount = 0;
+            __syncthreads();
+            if (done) return;
+            careful = false;
+        }
+    };
     if (warp < C::kSoftmaxWarps) {
         if constexpr (C::kRegsSoftmax > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kRegsSoftmax));
-        do {
-#pragma unroll 1
-            for (int id = take(); id >= 0; id = take()) {
-                w.load(p, id);
-                if (w.tokens > 0) rows_of_item(w, id, false);
-            }
-        } while (!phase_over([&](int id) {
+        all_items(take, [&](int id, bool careful) {
             w.load(p, id);
-            rows_of_item(w, id, true);
-        }));
+            if (w.tokens > 0) rows_of_item(w, id, careful);
+        });
     } else {
         if constexpr (C::kRegsSoftmax > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsOthers));
-        if (warp == kWarpMma) {
-            do {
-#pragma unroll 1
-                for (int id = take(); id >= 0; id = take()) {
-                    w.load(p, id);
-                    if (w.tokens > 0 && lane == 0) multiply_item(w);
-                    __syncwarp();
-                }
-            } while (!phase_over([&](int id) {
+        if (warp < kWarpTma) {
+            all_items(take, [&](int id, bool) {
                 w.load(p, id);
-                if (lane == 0) multiply_item(w);
-            }));
+                if (w.tokens > 0) multiply_item(w);
+            });
         } else if (warp == kWarpTma) {
-            do {
+            // The first lane copies, and asks for the item after the one it copies; the answer is there when the copies are on their way.
+            int id = blockIdx.x;
+            bool asking = false;
+            all_items([&]() -> int {
+                int now = -1;
                 if (lane == 0) {
-                    int id = *sNext;
-#pragma unroll 1
-                    for (;;) {
-                        const int i = nth % SCHED;
-                        if (nth >= SCHED) ok = wait_long(sched_empty + i, ((nth / SCHED) - 1) & 1) && ok;
-                        const bool rest = ok && *sCount >= kListRoom;
-                        sItem[i] = rest ? -1 : id;
-                        mbar_arrive(sched_full + i);
-                        ++nth;
-                        if (rest || id < 0) break;
-                        const bool ask = ok && !*sAbort;  // (after a timeout the others still write this item's zeros)
-                        if (ask) {
+                    if (asking) {  // the item after the last one
+                        id = -1;
+                        if (wait_long(asked, answers & 1)) id = next_of(answer);
+                        else ok = false;
+                        ++answers;
+                        asking = false;
+                    }
+                    const int i = nth % SCHED;
+                    if (nth >= SCHED) ok = wait_long(sched_empty + i, ((nth / SCHED) - 1) & 1) && ok;
+                    const bool rest = ok && *sCount >= kListRoom;
+                    *sNext = id;
+                    if (!rest) now = id;
+                    sItem[i] = now;
+                    mbar_arrive(sched_full + i);
+                    ++nth;
+                    if (now >= 0) {
+                        if (ok && !*sAbort) {  // (after a timeout the others still write this item's zeros)
                             fence_proxy_async();  // the answer before has been read
                             mbar_expect_tx(asked, 16);
                             ask_next(answer, asked);
-                        }
-                        w.load(p, id);
-                        if (w.tokens > 0 && ok) copy_item(w);
-                        id = -1;
-                        if (ask) {
-                            if (wait_long(asked, answers & 1)) id = next_of(answer);
-                            else ok = false;
-                            ++answers;
+                            asking = true;
+                        } else {
+                            id = -1;
                         }
                     }
-                    *sNext = id;
                 }
-                __syncwarp();
-            } while (!phase_over([&](int id) {
-                w.load(p, id);
-                if (lane == 0) copy_item(w);
-            }));
+                return __shfl_sync(0xffffffffu, now, 0);
+            }, [&](int item, bool) {
+                if (lane == 0) {
+                    w.load(p, item);
+                    if (w.tokens > 0 && ok) copy_item(w);
+                }
+            });
         } else {
-            do {
-#pragma unroll 1
-                for (int id = take(); id >= 0; id = take()) {
-                    if (warp != kWarpCover) continue;
-                    w.load(p, id);
-                    prompt_coverage(p, id, lane);
-                    if (w.fault && w.index == 0) {  // (one warp writes its rows)
-                        if (lane == 0) atomicOr(p.err, w.fault);
-                        if (w.sg.q0 >= 0)           // a negative q_start covers nothing
-                            for (long long r = w.sg.q0; r < min((long long)w.sg.q0 + w.sg.ql, (long long)p.total_rows); ++r)
-                                prompt_zero(p, r, w.h * p.G, p.G, lane, 32);
-                    }
+            all_items(take, [&](int id, bool careful) {
+                if (careful) return;
+                w.load(p, id);
+                prompt_coverage(p, id, lane);
+                if (w.fault && w.index == 0) {  // (one warp writes its rows)
+                    if (lane == 0) atomicOr(p.err, w.fault);
+                    if (w.sg.q0 >= 0)           // a negative q_start covers nothing
+                        for (long long r = w.sg.q0; r < min((long long)w.sg.q0 + w.sg.ql, (long long)p.total_rows); ++r)
+                            prompt_zero(p, r, w.h * p.G, p.G, lane, 32);
                 }
-            } while (!phase_over([](int) {}));
+            });
         }
     }
     if (*sAbort) {
@@ -772,9 +841,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll 1
             for (int i = max(0, stages - NST); i < stages; ++i)
                 if (!mbar_wait_ns(full + i % NST, (i / NST) & 1)) break;
-        if (warp == kWarpMma && lane == 0) {
-            umma_commit(drain);
-            mbar_wait_ns(drain, 0);
+        if ((warp == kWarpMma || warp == kWarpMma + 1) && lane == 0) {
+            umma_commit(drain + (warp - kWarpMma));
+            mbar_wait_ns(drain + (warp - kWarpMma), 0);
         }
         if (tid == 0) atomicOr(p.err, PKV_ERR_TIMEOUT);
         __syncthreads();
