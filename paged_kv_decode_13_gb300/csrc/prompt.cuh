@@ -16,18 +16,19 @@
 //
 // Roles, meeting on mbarriers only, each walking through the items by itself:
 //   softmax warps (four a tile; thread = row)  read S from TMEM, mask, take the
-//       maximum, write P = 2^(S - reference) as bf16 over the S columns read,
+//       maximum, write P = 2^(S - reference) as bf16 to TMEM,
 //       and at the end the normalised rows out.  The reference moves only when a score
 //       passes it by 2^8 (then O is rescaled in TMEM; no product is in flight on it then);
 //   MMA warps   S = Q K^T (M 128, N 128; Q and K in shared memory) and O += P V (P
-//       from TMEM, V as an MN-major tile), two warps: a tile each, or S and P V;
+//       from TMEM, V as an MN-major tile), a warp each;
 //   copy warp   asks for the next item; Q, then K and V blocks through a ring of stages
 //       (TMA, 128-byte swizzle; rows past the tensor and columns past head_dim come as zeros);
 //   cover warp  rows of no segment, rows of two, refused segments.
-// TMEM (512 columns): two S / P slots of 128, then O.  Up to head_dim 128 the two
-// slots are the CTA's two tiles, whose softmax and products alternate: each tile's
-// next S waits for its own P V, and the tensor core works on the other's meanwhile.
-// Above, O of one tile takes 256 columns and the slots are two blocks in turn.
+// TMEM (512 columns): one S of 128, two P of 64, then O (256: two tiles up to head_dim 128,
+// one above).  S is in registers some 200 cycles after it is there, and the next one is computed in its
+// place: with two tiles that of the other tile, so that one tile's softmax runs beside the other's
+// products; with one the next block's.  (S and P in one place for each tile, 2 x 128 columns, let the tiles fall into
+// step, softmax and products in turn: 462 us against NEWTIME for one prompt of 8192 rows.)
 //
 // P is rounded to bf16, as V is: half a step, 2^-8 of a weight, on sums
 // whose result is rounded the same way or averaged over many keys; the sum of weights is
@@ -66,9 +67,9 @@ struct PromptCfg {
     static_assert(kSoftmaxWarps * 32 * kRegsSoftmax + 128 * kRegsOthers <= kThreads * kRegs || NT == 1, "the roles' registers fit the launch's");
     static constexpr int kSched = 4;                                // items on their way through the roles
     static constexpr int kOdd = 64;                                 // items to run again, at most before they are
-    static constexpr int kBars = 2 * NST + 2 + 2 + 4 + 2 + 2 + 2 * kSched + 1;
+    static constexpr int kBars = 2 * NST + 3 + 2 + 4 + 2 + 2 + 2 * kSched + 1;
     static constexpr size_t kSmem = 1024 + (size_t)NT * kQTile + (size_t)NST * kStage + 16 + kBars * 8 + (kSched + kOdd) * 4 + 64;
-    static constexpr unsigned kColO = 256;                          // O of tile t at kColO + t * DP
+    static constexpr unsigned kColP = 128, kColO = 256;             // S at 0; two slots of P; O of tile t at kColO + t * DP
     static_assert(kSmem <= 232448, "exceeds the per-CTA shared memory limit");
 };
 
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
     unsigned char *ring = sQ + NT * C::kQTile;
     uint4 *answer = reinterpret_cast<uint4 *>(ring + (size_t)NST * C::kStage);
     uint64_t *bars = reinterpret_cast<uint64_t *>(answer + 1);
-    uint64_t *full = bars, *empty = full + NST, *q_full = empty + NST, *q_empty = q_full + 1, *s_full = q_empty + 1;
+    uint64_t *full = bars, *empty = full + NST, *q_full = empty + NST, *q_empty = q_full + 1, *s_free = q_empty + 1, *s_full = s_free + 1;
     uint64_t *p_half = s_full + 2, *p_full = p_half + 2, *pv_done = p_full + 2, *drain = pv_done + 2;  // P of keys 0-63 and 64-127
     uint64_t *sched_full = drain + 2, *sched_empty = sched_full + SCHED, *asked = sched_empty + SCHED;
     int *sItem = reinterpret_cast<int *>(bars + C::kBars), *sOdd = sItem + SCHED;
@@ -283,8 +284,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll 1
         for (int i = 0; i < C::kBars; ++i) {
             uint64_t *b = bars + i;
-            // P: every warp of the tile; an item is released by every warp but the one that copies, a stage and the queries by each tile's products
-            mbar_init(b, b >= p_half && b < pv_done ? 4 : b >= sched_empty && b < asked ? 3 + C::kSoftmaxWarps : (b >= empty && b < q_full) || b == q_empty ? NT : 1);
+            // P, and S once it is read: every warp of a tile; an item is released by every warp but the one that copies
+            mbar_init(b, (b >= p_half && b < pv_done) || b == s_free ? 4 : b >= sched_empty && b < asked ? 3 + C::kSoftmaxWarps : 1);
         }
         fence_barrier_init();
         *sAbort = 0;
@@ -318,7 +319,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
     auto wait_bar = [&](uint64_t *bar, unsigned parity) -> bool { return __all_sync(0xffffffffu, wait_one(bar, parity)); };
 
     int stages = 0;             // stages used so far
-    unsigned used = 0, phase = 0;  // bit slot: an S / P slot has been used; how often, modulo two
+    unsigned used = 0, phase = 0;  // bit slot: a P slot has been used; how often, modulo two (S products: of S itself)
+    unsigned s_phase = 0;          // softmax: blocks of the tile so far, modulo two
     unsigned queries = 0;       // items with rows so far
     int nth = 0;                // items taken from the scheduler so far
     bool ok = true;
@@ -355,16 +357,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         load(&p.tmap_k, w.b0);
 #pragma unroll 1
         for (int j = w.b0; ok && j < w.b1; ++j) {
-            // the order in which the products take them
-            if (NT == 1 && j + 1 < w.b1) load(&p.tmap_k, j + 1);
+            if (j + 1 < w.b1) load(&p.tmap_k, j + 1);  // (S is a block ahead)
             load(&p.tmap_v, j);
-            if (NT == 2 && j + 1 < w.b1) load(&p.tmap_k, j + 1);
         }
     };
-    // The products, two warps of them (one lane of each issues): with two tiles a warp has a tile, with one the first
-    // has S and the second P V.  A look at an mbarrier takes 110 cycles even if it is open, a commit 60, and an issuing warp
-    // waits behind its products: one warp for all of it left the tensor core idle half the time (4700 cycles for the
-    // blocks of two tiles, 2050 of them products).
+    // The products: one warp has S, one P V (one lane of each issues).  A look at an mbarrier takes 110 cycles even if
+    // it is open, a commit 60, and an issuing warp waits behind its products: one warp for all of them left the tensor core
+    // idle half the time (4700 cycles for the blocks of two tiles, 2050 of them products).
     const unsigned lead = lane == 0;
     unsigned ring_at = 0, ring_phase = 0;    // the stage to be read next
     // The stages of the next block, and the way over blocks that are the other warp's.
@@ -389,8 +388,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll
         for (int c = 0; c < SPB; ++c) umma_commit_by(lead, empty + at[c]);
     };
-    // S of tile t and the block in stages `at`, into slot; P that was there has been read
-    auto issue_s = [&](int t, const unsigned (&at)[SPB], int slot) {
+    // S of tile t and the block in stages `at`; what was there has been read
+    auto issue_s = [&](int t, const unsigned (&at)[SPB]) {
         const unsigned q_lo = UmmaDesc(smem_u32(sQ), 16).lo + t * (C::kQTile >> 4), k_lo = UmmaDesc(smem_u32(ring), 16).lo;
         tc_fence_after();
 #pragma unroll
@@ -399,11 +398,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll
             for (int k = 0; k < C::kCols / 16; ++k) {
                 const unsigned off = ((k >> 2) * C::kPart + (k & 3) * 32) >> 4;
-                umma_ss(lead, tmem + slot * 128, qd + off, kd + off, umma_idesc_bf16(128, 128, 0), c > 0 || k > 0);
+                umma_ss(lead, tmem, qd + off, kd + off, umma_idesc_bf16(128, 128, 0), c > 0 || k > 0);
             }
         }
-        umma_commit_by(lead, s_full + slot);
-        release(at);
+        umma_commit_by(lead, s_full + t);
     };
     // O of tile t += P in slot times the V block in stages `at`
     auto issue_pv = [&](int t, const unsigned (&at)[SPB], int slot, bool fresh) {
@@ -417,78 +415,52 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
                 const unsigned vd = v_lo + at[c] * (C::kStage >> 4);
 #pragma unroll
                 for (int u = 4 * half; u < 4 * half + 4; ++u)
-                    umma_ts(lead, tmem + C::kColO + t * DP + c * C::kCols, tmem + slot * 128 + u * 8, vd + (u * 2048 >> 4), umma_idesc_bf16(128, C::kCols, 1),
+                    umma_ts(lead, tmem + C::kColO + t * DP + c * C::kCols, tmem + C::kColP + slot * 64 + u * 8, vd + (u * 2048 >> 4), umma_idesc_bf16(128, C::kCols, 1),
                             !fresh || u > 0);
             }
         }
         umma_commit_by(lead, pv_done + slot);
-        release(at);
         phase ^= 1u << slot;
         return true;
     };
-    auto multiply_item = [&](const Item &w) {
-        const int which = warp - kWarpMma;
+    // (copied in this order: K(b0), K(b0 + 1), V(b0), K(b0 + 2), V(b0 + 1), ..)
+    auto scores_of_item = [&](const Item &w) {
         unsigned at[SPB], ph[SPB];
-        if constexpr (NT == 2) {
-            const int f = which ? w.first[NT - 1] : w.first[0], e = which ? w.last[NT - 1] : w.last[0];
-            // The other warp's blocks are released by this one too, so that both are done with a stage: not before its
-            // copies are there, or it would be released twice.
-            auto pass = [&]() {
-                if (!block_ready(at, ph)) return false;
-                if (lane == 0)
+        ok = ok && wait_bar(q_full, queries & 1);
+        ++queries;
+#pragma unroll 1
+        for (int j = w.b0; ok && j < w.b1; ++j) {
+            if (j > w.b0 + 1) next_block(at, ph);  // V(j - 2)
+            next_block(at, ph);
+            ok = block_ready(at, ph);
 #pragma unroll
-                    for (int c = 0; c < SPB; ++c) mbar_arrive(empty + at[c]);
-                __syncwarp();
-                return true;
-            };
-            auto scores = [&](int j) {
-                next_block(at, ph);
-                if (j < f || j >= e) return pass();
-                if (!block_ready(at, ph) || ((used >> which & 1) && !wait_bar(pv_done + which, (phase >> which & 1) ^ 1))) return false;
-                issue_s(which, at, which);
-                used |= 1u << which;
-                if (j + 1 == e) umma_commit_by(lead, q_empty);
-                return true;
-            };
-            ok = ok && wait_bar(q_full, queries & 1);
-            ++queries;
-            if (ok && e <= f && lane == 0) mbar_arrive(q_empty);
-            ok = ok && scores(w.b0);
-#pragma unroll 1
-            for (int j = w.b0; ok && j < w.b1; ++j) {
-                next_block(at, ph);
-                ok = j >= f && j < e ? block_ready(at, ph) && issue_pv(which, at, which, j == f) : pass();
-                if (ok && j + 1 < w.b1) ok = scores(j + 1);
-            }
-        } else {
-            if (which == 0) {
-                ok = ok && wait_bar(q_full, queries & 1);
-                ++queries;
-            }
-#pragma unroll 1
-            for (int j = w.b0; ok && j < w.b1; ++j) {
-                // copied in this order: K(b0), K(b0 + 1), V(b0), K(b0 + 2), V(b0 + 1), ..
-                const int slot = (j - w.b0) & 1;
-                if (which == 0) {
-                    if (j > w.b0 + 1) next_block(at, ph);  // V(j - 2)
-                    next_block(at, ph);
-                    ok = block_ready(at, ph) && (!(used >> slot & 1) || wait_bar(pv_done + slot, (phase >> slot & 1) ^ 1));
+            for (int t = 0; t < NT; ++t)
+                if (ok && j >= w.first[t] && j < w.last[t]) {
+                    if (used) ok = wait_bar(s_free, phase);  // the S before has been read
                     if (!ok) break;
-                    issue_s(0, at, slot);
-                    used |= 1u << slot;
-                    phase ^= 1u << slot;
-                    if (j + 1 == w.b1) {
-                        umma_commit_by(lead, q_empty);
-                        if (j > w.b0) next_block(at, ph);  // V(j - 1), V(j)
-                        next_block(at, ph);
-                    }
-                } else {
-                    if (j == w.b0) next_block(at, ph);         // K(b0)
-                    if (j + 1 < w.b1) next_block(at, ph);      // K(j + 1)
-                    next_block(at, ph);
-                    ok = block_ready(at, ph) && issue_pv(0, at, slot, j == w.b0);
+                    phase ^= used;
+                    used = 1;
+                    issue_s(t, at);
                 }
-            }
+            if (ok) release(at);
+        }
+        if (!ok) return;
+        umma_commit_by(lead, q_empty);
+        if (w.b1 - w.b0 > 1) next_block(at, ph);  // the last two V
+        next_block(at, ph);
+    };
+    auto sums_of_item = [&](const Item &w) {
+        unsigned at[SPB], ph[SPB];
+#pragma unroll 1
+        for (int j = w.b0; ok && j < w.b1; ++j) {
+            if (j == w.b0) next_block(at, ph);     // K(b0)
+            if (j + 1 < w.b1) next_block(at, ph);  // K(j + 1)
+            next_block(at, ph);
+            ok = block_ready(at, ph);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (ok && j >= w.first[t] && j < w.last[t]) ok = issue_pv(t, at, NT == 2 ? t : (j - w.b0) & 1, j == w.first[t]);
+            if (ok) release(at);
         }
     };
     // The rows of one item (a softmax warp).
@@ -508,13 +480,20 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll 1
         for (int j = f; ok && j < e; ++j) {
             const int slot = NT == 2 ? t : (j - w.b0) & 1;
-            const unsigned s_addr = tmem + lane_off + slot * 128;
-            if (!(ok = wait_bar(s_full + slot, phase >> slot & 1))) break;
+            const unsigned p_addr = tmem + lane_off + C::kColP + slot * 64;
+            if (!(ok = wait_bar(s_full + t, s_phase))) break;
+            s_phase ^= 1;
             tc_fence_after();
             unsigned x[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_async(s_addr + 32 * c, x[c]);
+            for (int c = 0; c < 4; ++c) tmem_ld32_async(tmem + lane_off + 32 * c, x[c]);
+            // the product that read P's slot before is done (asked while S is on its way)
+            if ((used >> slot & 1) && !(ok = wait_bar(pv_done + slot, (phase >> slot & 1) ^ 1))) break;
+            used |= 1u << slot;
             tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_free);  // S is in registers: the next one may go over it
             const int pos0 = j * C::kKeys;
             if (!__all_sync(0xffffffffu, !real || (pos0 >= lo_r && pos0 + C::kKeys <= hi_r))) {
 #pragma unroll
@@ -544,7 +523,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             if (__any_sync(0xffffffffu, grow)) {
                 const float m_new = grow ? mx : m, alpha = exp2_fast(m - m_new);
                 if (j > f && __any_sync(0xffffffffu, grow && m != kNoScore)) {
-                    // the product before is done: with two tiles S came after it, with two slots it is waited for
+                    // (no product is in flight on O: with one tile the last one was in the other slot)
                     if (NT == 1 && !(ok = wait_bar(pv_done + (slot ^ 1), (phase >> (slot ^ 1) & 1) ^ 1))) break;
                     tc_fence_after();
 #pragma unroll 1
@@ -575,7 +554,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
                     else la = add_f32x2(la, f32x2(e0, e1));
                     pk[k] = pack_bf16x2(e0, e1);
                 }
-                tmem_st16_async(s_addr + 16 * c, pk);
+                tmem_st16_async(p_addr + 16 * c, pk);
                 if (c == 1 && !zero_v) {  // the first keys' weights are there: their products may start
                     tmem_wait_st();
                     tc_fence_before();
@@ -590,7 +569,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             }
             if (zero_v) {
                 // V rows that not every row of the item sees: what is not finite reads zero
-                const int i0 = begin + SPB * (NT == 2 ? 2 * (j - w.b0) + 1 : (min(j + 1, w.b1 - 1) - w.b0 + 1) + (j - w.b0));
+                const int i0 = begin + SPB * ((min(j + 1, w.b1 - 1) - w.b0 + 1) + (j - w.b0));
                 const int key = pos0 + r;
 #pragma unroll 1
                 for (int c = 0; ok && c < SPB; ++c) {
@@ -779,7 +758,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         if (warp < kWarpTma) {
             all_items(take, [&](int id, bool) {
                 w.load(p, id);
-                if (w.tokens > 0) multiply_item(w);
+                if (w.tokens == 0) return;
+                if (warp == kWarpMma) scores_of_item(w);
+                else sums_of_item(w);
             });
         } else if (warp == kWarpTma) {
             // The first lane copies, and asks for the item after the one it copies; the answer is there when the copies are on their way.
