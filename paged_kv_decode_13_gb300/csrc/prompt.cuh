@@ -487,9 +487,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             unsigned x[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32_async(tmem + lane_off + 32 * c, x[c]);
-            // the product that read P's slot before is done (asked while S is on its way)
-            if ((used >> slot & 1) && !(ok = wait_bar(pv_done + slot, (phase >> slot & 1) ^ 1))) break;
-            used |= 1u << slot;
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
@@ -519,6 +516,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
                 }
                 mx = fmaxf(max3(y[0], y[1], y[2]), y[3]) * sc;
             }
+            // P's slot: the product that read it is done
+            if ((used >> slot & 1) && !(ok = wait_bar(pv_done + slot, (phase >> slot & 1) ^ 1))) break;
+            used |= 1u << slot;
             const bool grow = mx > m + kPromptLazy;
             if (__any_sync(0xffffffffu, grow)) {
                 const float m_new = grow ? mx : m, alpha = exp2_fast(m - m_new);
