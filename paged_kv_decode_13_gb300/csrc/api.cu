@@ -553,7 +553,8 @@ int make_plan4(const pkv_cache *c, int Hq, int S, int max_q_len, long long max_k
     pl->ks = pl->k4;
     const double cost = split4(&pl->k4, c->dtype, c->head_dim, (int)rows, pl->units, pl->pages, num_splits, dev, &pl->ncta);
     if (num_splits == 0 && S > 0 && S <= kSharesSegments) {
-        if (c->dtype == PKV_FP4 && c->head_dim == 128 && rows >= kWideFrom && regs_ok(pick4_wide().balance, pick4_wide().regs, dev)) pl->ks = pick4_wide();
+        const Attend4Kernel wide = c->dtype == PKV_FP8 ? pick8_wide() : pick4_wide();
+        if (c->head_dim == 128 && rows >= kWideFrom && regs_ok(wide.balance, wide.regs, dev)) pl->ks = wide;
         const long long tiles = (rows + pl->ks.rows - 1) / pl->ks.rows;
         const double shares = cost4_shares(pl->ks, block_bytes(c), (long long)S * c->kv_heads * tiles, pl->pages, dev);
         if (tiles <= kSharesTiles && shares < cost * (100 + kSharesEdge) / 100)

@@ -9,6 +9,7 @@ namespace pkv {
 template <int D>
 static const void *pick_pair8(int pair) {
     switch (pair) {
+        case kPlainRows: return reinterpret_cast<const void *>(&append8_kernel<D, kPlainRows>);
         case kInLane: return reinterpret_cast<const void *>(&append8_kernel<D, kInLane>);
         case kByShuffle: return reinterpret_cast<const void *>(&append8_kernel<D, kByShuffle>);
         default: return reinterpret_cast<const void *>(&append8_kernel<D, kByShared>);
@@ -18,17 +19,17 @@ static const void *pick_pair8(int pair) {
 cudaError_t launch_append8(const RopeParams &r, int sms, cudaStream_t stream) {
     Append8Params a;
     a.r = r;
-    const int pair = r.rot_dim == 0 || r.interleaved ? kInLane : r.rot_dim % 16 == 0 ? kByShuffle : kByShared;
-    // A CTA a page where there are few enough (one segment may hold all rows: its
-    // pages bound the others'); the heads of a page are spread over CTAs until
-    // each SM has kAppend8Fill of them.
-    const long long pages = ((long long)r.rows + kPage - 2) / kPage + 1, most = (long long)sms * kAppend8Most;
+    const bool plain = !r.q && r.rot_dim == 0 && !r.k_weight;
+    const int pair = plain ? kPlainRows : r.rot_dim == 0 || r.interleaved ? kInLane : r.rot_dim % 16 == 0 ? kByShuffle : kByShared;
+    // A CTA a page that the rows can have at most, up to kAppend8Most an SM (which then take
+    // several); with few, a page's heads are spread over CTAs until an SM has kAppend8Fill.
+    const long long pages = r.S + ((long long)r.rows + 14ll * std::min(r.S, r.rows)) / kPage + 1;
+    a.page_ctas = (int)std::max<long long>(1, std::min(pages, (long long)sms * kAppend8Most));
     const int items = (r.q ? r.Hq : 0) + 2 * r.Hkv;
-    a.page_ctas = (int)std::max<long long>(1, std::min(pages, most / r.S));
-    const long long active = std::max<long long>(1, std::min<long long>((long long)r.S * a.page_ctas, r.S + r.rows / kPage));  // CTAs with a page, about
-    a.head_ctas = (int)std::max<long long>(1, std::min<long long>((items + kAppend8Warps - 1) / kAppend8Warps, (long long)sms * kAppend8Fill / active));
+    const long long active = std::min<long long>(a.page_ctas, r.S + r.rows / kPage);  // CTAs with a page, about
+    a.head_ctas = (int)std::max<long long>(1, std::min<long long>((items + kAppend8Warps - 1) / kAppend8Warps, (long long)sms * kAppend8Fill / std::max(active, 1ll)));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)r.S * a.page_ctas * a.head_ctas));
+    cfg.gridDim = dim3((unsigned)((long long)a.page_ctas * a.head_ctas));
     cfg.blockDim = dim3(kAppend8Warps * 32);
     cfg.dynamicSmemBytes = (size_t)kPage * (r.rot_dim / 2) * 8 + (pair == kByShared ? kAppend8Warps * 1024 : 0);
     cfg.stream = stream;

@@ -11,8 +11,12 @@
 //
 // The tokens of one page may come from several segments of a call (pieces of one
 // sequence, a padded batch that holds a segment twice).  The scale is theirs in
-// common, so the lowest of them writes the page for all; where no other valid segment
-// names the same column, which is one look at the table, none of that is asked.
+// common, so the lowest of them writes the page for all; where the table's columns
+// ascend, as a step's mostly do, or no other valid segment names the same one, none of that is asked.
+//
+// How many pages there are only the table says: every CTA sums it (a thread some
+// segments) and takes every n-th page of all segments end to end.  (A CTA for each page that a
+// segment could have at most was 13,000 CTAs for a step of 256 sequences, 18.6 us.)
 #pragma once
 
 #include "fp8.cuh"
@@ -20,13 +24,21 @@
 
 namespace pkv {
 
-constexpr int kAppend8Warps = 4;
+constexpr int kAppend8Warps = 4, kAppend8Threads = kAppend8Warps * 32;
+constexpr int kPlainRows = 3;  // beside RopePair: rows that are neither normalised nor turned, and no queries
 
 struct Append8Params {
     RopeParams r;     // rows, rope, cache (lanes_log2, slices, row_ctas and page_warps unused)
-    int page_ctas;    // CTAs that share a segment's pages
+    int page_ctas;    // CTAs that share the pages
     int head_ctas;    // and those that share a page's heads
 };
+
+// Pages that a segment's new rows go to; none for an empty or refused one.
+__device__ __forceinline__ int new_pages(const RopeParams &p, const Segment &sg) {
+    if (sg.ql <= 0 || segment_fault(sg, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window)) return 0;
+    const int n = (sg.kend + kPage - 1) / kPage - (sg.kend - sg.ql) / kPage;
+    return p.ring_rows ? min(n, p.ring_rows / kPage) : n;  // (a step as long as the ring: its last page is its first one too)
+}
 
 // Row and position of slot `slot` (of the table's columns laid end to end) in segment o, or row -1.
 __device__ __forceinline__ int row_of_slot(const Segment &o, int slot, int ring_rows, int &pos) {
@@ -84,6 +96,11 @@ __device__ __forceinline__ void append8_head(const RopeParams &p, int kind, int 
     if (dst) dst += h * D + c * 8;
     const unsigned fresh = __ballot_sync(0xffffffffu, lane < kPage && rows[lane & 15] >= 0);  // bit j: slot j has a new row
     auto some = [&](int it) { return (fresh >> (it * TPI)) & ((1u << TPI) - 1u); };
+    unsigned char *out = reinterpret_cast<unsigned char *>(kind == 1 ? p.k_pool : p.v_pool) + (block * p.Hkv + h) * block8_bytes(D);
+    unsigned kept = ~fresh & 0xffffu;  // a ring's page holds older tokens behind the new ones too
+    if (!p.ring_rows) kept &= (1u << (31 - __clz(fresh))) - 1u;
+    unsigned word = 0;  // the page's scale and NaN tokens, on their way with the rows
+    if (kind && kept) word = *reinterpret_cast<const unsigned *>(out + 16 * D);
     Raw8<T> x[IT];
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
@@ -94,7 +111,7 @@ __device__ __forceinline__ void append8_head(const RopeParams &p, int kind, int 
     }
     const T *weight = reinterpret_cast<const T *>(kind == 0 ? p.q_weight : kind == 1 ? p.k_weight : nullptr);
     const bool turn = kind < 2 && p.rot_dim > 0;
-    if (weight || turn) {
+    if (PAIR != kPlainRows && (weight || turn)) {
         const int left = p.rot_dim - c * 8;  // rotated columns from this lane's first on
         const unsigned turned = !turn ? 0u : left >= 8 ? 0xffu : left <= 0 ? 0u : (1u << left) - 1u;
         int partner = lane;
@@ -219,12 +236,9 @@ __device__ __forceinline__ void append8_head(const RopeParams &p, int kind, int 
         }
     }
     // ---- the page's scale: that of the tokens it keeps, or more
-    unsigned char *out = reinterpret_cast<unsigned char *>(kind == 1 ? p.k_pool : p.v_pool) + (block * p.Hkv + h) * block8_bytes(D);
-    unsigned kept = ~fresh & 0xffffu;  // a ring's page holds older tokens behind the new ones too
-    if (!p.ring_rows) kept &= (1u << (31 - __clz(fresh))) - 1u;
     unsigned b = scale8_of(amax);
     if (kept) {
-        const unsigned word = *reinterpret_cast<const unsigned *>(out + 16 * D), b0 = min(word & 0xffu, kScaleMax8);
+        const unsigned b0 = min(word & 0xffu, kScaleMax8);
         nan |= (word >> 16) & kept;
         if (b > b0 && b0) {
             const float down = b - b0 < 32 ? __uint_as_float((127u + b0 - b) << 23) : 0.f;  // (what is 2^-18 of 2^-9 or less reads zero anyway)
@@ -298,43 +312,96 @@ static __global__ void __launch_bounds__(256) read8_kernel(const __grid_constant
 }
 
 template <int D, int PAIR>
-__global__ void __launch_bounds__(kAppend8Warps * 32) append8_kernel(const __grid_constant__ Append8Params a) {
+__global__ void __launch_bounds__(kAppend8Threads, PAIR == kPlainRows ? (D == 256 ? 3 : 5) : D == 256 ? 3 : 4) append8_kernel(const __grid_constant__ Append8Params a) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int sRow[2][kPage], sPos[2][kPage], sOwner;  // own rows; those of every segment
+    __shared__ long long sSum[kAppend8Warps], sFirst;
+    __shared__ int sSegment;
     const RopeParams &p = a.r;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pairs = p.rot_dim / 2;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, pairs = PAIR == kPlainRows ? 0 : p.rot_dim / 2;
     float *stage = reinterpret_cast<float *>(smem) + warp * 256;                                                    // (kByShared)
     float2 *angles = reinterpret_cast<float2 *>(smem + (PAIR == kByShared ? kAppend8Warps * 1024 : 0));             // [16][pairs]
-    const int hc = blockIdx.x % a.head_ctas, pc = blockIdx.x / a.head_ctas % a.page_ctas, s = blockIdx.x / a.head_ctas / a.page_ctas;
+    const int hc = blockIdx.x % a.head_ctas, pc = blockIdx.x / a.head_ctas, ring_pages = p.ring_rows / kPage;
     pdl_wait();
     pdl_trigger();
-    const Segment sg = load_segment(p.seq_info, s);
-    const unsigned fault = segment_fault(sg, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
-    if (fault) {
-        if (hc == 0 && pc == 0 && tid == 0) atomicOr(p.err, fault);
-        return;
-    }
-    if (sg.ql == 0) return;
-    const int p0 = (sg.kend - sg.ql) / kPage, ring_pages = p.ring_rows / kPage;
-    int units = (sg.kend + kPage - 1) / kPage - p0;
-    if (ring_pages) units = min(units, ring_pages);  // (a step as long as the ring: its last page is its first one too)
-    if (pc >= units) return;
-    if (!new_pages_ok(p, sg, lane)) {  // (every warp sees the same)
-        if (hc == 0 && pc == 0 && tid == 0) atomicOr(p.err, PKV_ERR_BLOCK);
-        return;
-    }
-    bool shared = false;  // another segment writes this column
+    // ---- the pages of all segments: thread t sums segments t per .. (a table of one needs no sum)
+    const int per = (p.S + kAppend8Threads - 1) / kAppend8Threads, s_lo = min(tid * per, p.S), s_hi = min(s_lo + per, p.S);
+    long long mine = 0, upto, total;
+    bool may_share = false;  // columns that do not ascend
+    Segment sg{0, 0, 0, 0};
     if (p.S > 1) {
+        int last = s_lo > 0 && s_lo < s_hi ? load_segment(p.seq_info, s_lo - 1).col : -1;
 #pragma unroll 4
-        for (int t = tid; t < p.S; t += kAppend8Warps * 32) {
-            const Segment o = load_segment(p.seq_info, t);
-            shared |= t != s && o.col == sg.col && o.ql > 0 && !segment_fault(o, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
+        for (int i = s_lo; i < s_hi; ++i) {
+            const Segment o = load_segment(p.seq_info, i);
+            mine += new_pages(p, o);
+            may_share |= o.col <= last;
+            last = o.col;
+            const unsigned fault = segment_fault(o, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
+            if (fault && blockIdx.x == 0) atomicOr(p.err, fault);
         }
-        shared = __syncthreads_or(shared);
+        upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+        if (lane == 31) sSum[warp] = upto;
+        may_share = __syncthreads_or(may_share);
+        total = 0;
+#pragma unroll
+        for (int k = 0; k < kAppend8Warps; ++k) {
+            if (k < warp) upto += sSum[k];
+            total += sSum[k];
+        }
+    } else {
+        sg = load_segment(p.seq_info, 0);
+        total = new_pages(p, sg);
+        const unsigned fault = segment_fault(sg, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
+        if (fault && blockIdx.x == 0 && tid == 0) atomicOr(p.err, fault);
     }
     const int nq = p.q ? p.Hq : 0, items = nq + 2 * p.Hkv;
+    long long end = 0, first = 0;  // pages before the segment's end, and before it
+    int s = 0, p0 = 0;
+    bool fine = false, shared = false;
 #pragma unroll 1
-    for (int u = pc; u < units; u += a.page_ctas) {
+    for (long long at = pc; at < total; at += a.page_ctas) {
+        if (at >= end) {  // another segment
+            if (p.S > 1) {
+                __syncthreads();
+                if (upto - mine <= at && at < upto) {
+                    long long x = upto - mine;
+                    int i = s_lo;
+#pragma unroll 1
+                    for (;; ++i) {
+                        const int n = new_pages(p, load_segment(p.seq_info, i));
+                        if (at < x + n) break;
+                        x += n;
+                    }
+                    sSegment = i;
+                    sFirst = x;
+                }
+                __syncthreads();
+                s = sSegment;
+                first = sFirst;
+                sg = load_segment(p.seq_info, s);
+            }
+            end = first + new_pages(p, sg);
+            p0 = (sg.kend - sg.ql) / kPage;
+            fine = new_pages_ok(p, sg, lane);  // (every warp sees the same)
+            if (!fine && hc == 0 && tid == 0) atomicOr(p.err, PKV_ERR_BLOCK);
+            shared = false;  // another segment writes this column
+            if (may_share) {
+#pragma unroll 4
+                for (int t = tid; t < p.S; t += kAppend8Threads) {
+                    const Segment o = load_segment(p.seq_info, t);
+                    shared |= t != s && o.col == sg.col && new_pages(p, o) > 0;
+                }
+                shared = __syncthreads_or(shared);
+            }
+        }
+        if (!fine) continue;
+        const int u = (int)(at - first);
         const int tp = ring_pages ? (p0 + u) % ring_pages : p0 + u;
         const long long block = p.block_table[(long long)sg.col * p.mbps + tp];
         __syncthreads();
@@ -354,19 +421,21 @@ __global__ void __launch_bounds__(kAppend8Warps * 32) append8_kernel(const __gri
         // Own rows serve q, those of every segment k and v; they are the same but where segments share a column.
 #pragma unroll 1
         for (int pass = 0; pass < (shared ? 2 : 1); ++pass) {
-            const int first = pass ? nq : 0, last = shared && !pass ? nq : items;
+            const int i0 = pass ? nq : 0, i1 = shared && !pass ? nq : items;
             __syncthreads();
             if (pass && sOwner != s) break;
-            for (int i = tid; i < kPage * pairs; i += kAppend8Warps * 32) {
-                const int j = i / pairs, e = i % pairs, row = sRow[pass][j];
-                if (row < 0) continue;
-                unsigned pos = (unsigned)sPos[pass][j];
-                if (p.positions) pos = (unsigned)p.positions[p.axis ? (long long)row * p.axes + min((int)p.axis[e], p.axes - 1) : row];
-                angles[i] = angle_of(pos, p.turns[e], p.mscale);
+            if constexpr (PAIR != kPlainRows) {
+                for (int i = tid; i < kPage * pairs; i += kAppend8Threads) {
+                    const int j = i / pairs, e = i % pairs, row = sRow[pass][j];
+                    if (row < 0) continue;
+                    unsigned pos = (unsigned)sPos[pass][j];
+                    if (p.positions) pos = (unsigned)p.positions[p.axis ? (long long)row * p.axes + min((int)p.axis[e], p.axes - 1) : row];
+                    angles[i] = angle_of(pos, p.turns[e], p.mscale);
+                }
+                __syncthreads();
             }
-            __syncthreads();
 #pragma unroll 1
-            for (int it = first + hc * kAppend8Warps + warp; it < last; it += a.head_ctas * kAppend8Warps) {
+            for (int it = i0 + hc * kAppend8Warps + warp; it < i1; it += a.head_ctas * kAppend8Warps) {
                 const int kind = it < nq ? 0 : it < nq + p.Hkv ? 1 : 2;
                 append8_head<D, PAIR>(p, kind, kind == 0 ? it : kind == 1 ? it - nq : it - nq - p.Hkv, sRow[pass], angles, block, stage, lane);
             }

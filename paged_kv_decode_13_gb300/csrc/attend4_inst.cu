@@ -8,7 +8,7 @@
 #ifndef PKV_INST_BITS
 #error "PKV_INST_BITS not set"
 #endif
-#if PKV_INST_D == 128 && PKV_INST_BITS == 4
+#if PKV_INST_D == 128
 #include "wide4.cuh"
 #endif
 
@@ -57,10 +57,13 @@ Attend4Kernel PICK4_NAME(PKV_INST_BITS, PKV_INST_D)(int rows, bool few) {
 #endif
 }
 
-#if PKV_INST_D == 128 && PKV_INST_BITS == 4
-Attend4Kernel pick4_wide() {
-    return Attend4Kernel{nullptr, reinterpret_cast<const void *>(&wide4_kernel), reinterpret_cast<const void *>(&merge4_kernel<128, 128, 32>),
-                         Wide4::kThreads, Wide4::kSmem, Wide4::R, 8, 1, 235, 20, Wide4::kRegs};
+#if PKV_INST_D == 128
+#define WIDE4_NAME2(B) pick##B##_wide
+#define WIDE4_NAME(B) WIDE4_NAME2(B)
+Attend4Kernel WIDE4_NAME(PKV_INST_BITS)() {
+    using C = Wide4<PKV_INST_BITS>;
+    return Attend4Kernel{nullptr, reinterpret_cast<const void *>(&wide4_kernel<C>), reinterpret_cast<const void *>(&merge4_kernel<128, 128, 32>),
+                         C::kThreads, C::kSmem, C::R, 8, 1, 235, 20, C::kRegs};
 }
 #endif
 

@@ -61,5 +61,6 @@ Attend4Kernel pick8_128(int rows, bool few);
 Attend4Kernel pick8_256(int rows, bool few);
 // The tcgen05 kernel of wide groups (head_dim 128, equal shares only: fn is null).
 Attend4Kernel pick4_wide();
+Attend4Kernel pick8_wide();
 
 }  // namespace pkv

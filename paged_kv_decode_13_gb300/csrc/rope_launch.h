@@ -14,8 +14,8 @@ constexpr int kRopeSpread = 20;
 // cache: RopeCache; f32: the rows' type (bf16 otherwise; 4-bit caches take bf16 rows).
 cudaError_t launch_rope(RopeParams &p, int cache, bool f32, int sms, cudaStream_t stream);
 
-// CTAs an SM is given, at most, before the pages of a segment share one, and before the heads of a page do.
-constexpr int kAppend8Most = 64;
+// CTAs an SM is given, at most, before pages share one, and before the heads of a page do.
+constexpr int kAppend8Most = 16;
 constexpr int kAppend8Fill = 6;
 
 // The append to an 8-bit cache (bf16 rows; head_dim 64, 128 or 256, S > 0).

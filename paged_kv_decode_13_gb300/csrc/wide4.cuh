@@ -1,5 +1,5 @@
-// Tensor-core (tcgen05) attention over a 4-bit cache for wide query groups
-// (sm_103a, head_dim 128).
+// Tensor-core (tcgen05) attention over a quantised cache (4 or 8 bits) for wide
+// query groups (sm_103a, head_dim 128).
 //
 // The row class of draft verification and chunked steps: 128 query rows of
 // one (segment, kv head) against its pages, as equal shares of all ranges
@@ -44,21 +44,23 @@
 
 namespace pkv {
 
+template <int BITS_>
 struct Wide4 {
-    static constexpr int D = 128, R = 128, kThreads = 640, PG = 4;
-    static constexpr int NK = 3, NV = 3, NB = 3, NR = 6;           // K, V tiles; S / P buffers; raw groups
-    static constexpr int kBlock = block4_bytes(D), kRaw = 2 * kBlock;
+    static constexpr int BITS = BITS_, D = 128, R = 128, kThreads = 640, PG = 4;
+    static constexpr int NK = 3, NV = 3, NB = 3, NR = BITS == 4 ? 6 : 5;  // K, V tiles; S / P buffers; raw groups
+    static constexpr int NS = 8;                                    // 8 bits: groups whose pages' scales are kept (the copies are 6 ahead of the softmax at most)
+    static constexpr int kBlock = BITS == 4 ? block4_bytes(D) : block8_bytes(D), kRaw = 2 * kBlock;
     static constexpr unsigned kTile = 64 * 256;                     // K: two halves of 64 tokens x 64 columns; V^T: 128 columns x 64 tokens
     static constexpr unsigned kQHalf = 128 * 128;
     static constexpr size_t kRawBytes = (size_t)PG * NR * kRaw;
     // registers a thread: at launch, of the softmax warps and of the others while the roles run
     static constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsOthers = 72;
-    static constexpr int kBars = 2 * NK + 2 * NV + 3 * NB + 2 + 2 * NR, kPieces = 16;
-    static constexpr size_t kSmem = 1024 + (size_t)(NK + NV) * kTile + 2 * kQHalf + kRawBytes + 6 * R * 4 + kBars * 8 + 256;
+    static constexpr int kBars = 2 * NK + 2 * NV + 3 * NB + 2 + 2 * NR + (BITS == 8 ? NS : 0), kPieces = 16;
+    static constexpr size_t kSmem = 1024 + (size_t)(NK + NV) * kTile + 2 * kQHalf + kRawBytes + 6 * R * 4 + kBars * 8 + (BITS == 8 ? 2 * NS * PG * 4 : 0) + 256;
     static constexpr unsigned kColO = 64 * NB;                      // O_h at kColO + 128 h
     static_assert(kSmem <= 232448, "exceeds the per-CTA shared memory limit");
     static_assert(256 * kRegsSoftmax + 384 * kRegsOthers <= kThreads * kRegs, "the roles' registers fit the launch's");
-    static_assert(kRaw % 128 == 0, "raw stages stay 128-byte aligned");
+    static_assert(kBlock % 16 == 0, "copies stay 16-byte aligned");
     static_assert(NR + NV < kPieces, "the copies are ahead of the softmax by fewer pieces than there are flag words");
 };
 
@@ -71,8 +73,9 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const __grid_constant__ Attend4Params p) {
-    using C = Wide4;
+template <class C>
+__global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_constant__ Attend4Params p) {
+    constexpr bool k8 = C::BITS == 8;
     constexpr int D = C::D, R = C::R, PG = C::PG, NK = C::NK, NV = C::NV, NB = C::NB, NR = C::NR;
     constexpr int kWarpS = 16, kWarpPv = 17, kWarpRaw = 18;
     extern __shared__ unsigned char smem_raw[];
@@ -86,8 +89,11 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
     uint64_t *k_full = bars, *k_empty = k_full + NK, *v_full = k_empty + NK, *v_empty = v_full + NV;
     uint64_t *s_full = v_empty + NV, *p_full = s_full + NB, *pv_done = p_full + NB;
     uint64_t *q_full = pv_done + NB, *drain = q_full + 1, *raw_full = drain + 1, *raw_empty = raw_full + NR;
-    unsigned *tslot = reinterpret_cast<unsigned *>(bars + C::kBars);
+    uint64_t *sc_full = raw_empty + NR;                             // 8 bits: the scales of group J are in slot J % NS
+    unsigned *sWord = reinterpret_cast<unsigned *>(bars + C::kBars);  // [K, V][NS][PG] scale and NaN tokens of the pages
+    unsigned *tslot = sWord + (k8 ? 2 * C::NS * PG : 0);
     volatile int *sAbort = reinterpret_cast<volatile int *>(tslot + 1);
+    float *sUnit = reinterpret_cast<float *>(tslot + 2 + C::kPieces);  // 8 bits: [2] what O of each half counts in
     int *sPiece = reinterpret_cast<int *>(tslot + 2);               // [kPieces] flags of piece i % kPieces: 1 bad page, 2 NaN in an edge page's V
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3, cta = blockIdx.x;
@@ -98,7 +104,7 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
         for (int i = 0; i < C::kBars; ++i) {
             const bool four = (i < NK) || (i >= 2 * NK && i < 2 * NK + NV) ;                                     // k_full, v_full: the dequantising warps
             const bool eight = (bars + i >= p_full && bars + i < p_full + NB) || bars + i == q_full;           // every softmax warp
-            mbar_init(bars + i, four ? 4 : eight || bars + i >= raw_full ? 8 : 1);                             // raw_full: two copies a page; raw_empty: both of its readers
+            mbar_init(bars + i, four ? 4 : eight || bars + i >= raw_full ? 8 : 1);                             // raw_full: two copies a page; raw_empty: both of its readers; sc_full: K and V of each page
         }
         fence_barrier_init();
         *sAbort = 0;
@@ -153,7 +159,52 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
                 const bool mine = li < w.pages;
                 const unsigned char *st = raw + (size_t)(rs * PG + u) * C::kRaw;
                 if (!wait_bar(raw_full + rs, (J / NR) & 1)) { timed_out = true; break; }
-                if (!is_v) {
+                if constexpr (k8) {
+                    // Tokens l / 8 + 4 i, chunk l % 8 of 16 columns (K and V alike: both tiles have a token's columns side by side).
+                    // Lanes of the second column half store their two 16-byte pieces the other way round: the writes meet no bank twice.
+                    const unsigned char *src = st + (is_v ? C::kBlock : 0);
+                    uint4 cw[4];
+                    unsigned word = 0;
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int tok = (lane >> 3) + 4 * i;
+                            cw[i] = *reinterpret_cast<const uint4 *>(src + tok * D + 16 * place8(tok, lane & 7, D));
+                        }
+                        word = *reinterpret_cast<const unsigned *>(src + 16 * D);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(raw_empty + rs);
+                    // (slot J % NS is free: its group's P V is done before the tile of group J - 3 is)
+                    if (is_v ? J >= NV && !wait_bar(v_empty + vs, ((J / NV) - 1) & 1) : J >= NK && !wait_bar(k_empty + ks, ((J / NK) - 1) & 1)) { timed_out = true; break; }
+                    if (lane == 0) {
+                        sWord[((is_v ? C::NS : 0) + J % C::NS) * PG + u] = word;
+                        if (is_v && word >> 16) atomicOr(sPiece + piece % C::kPieces, 2);
+                        mbar_arrive(sc_full + J % C::NS);
+                    }
+                    const int pos0 = (w.page0 + li) * kPage, half64 = (lane >> 2) & 1;
+                    unsigned char *tile64 = (is_v ? sV + (size_t)vs * C::kTile : sK + (size_t)ks * C::kTile) + half64 * (64 * 128);
+                    if (mine || is_v) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int tok = (lane >> 3) + 4 * i, row = u * 16 + tok;
+                            const bool some = mine && (!is_v || (pos0 + tok >= w.lo_u && pos0 + tok < w.hi_u));  // keys that no row sees may hold anything
+                            unsigned x[8];
+                            unpack_e4m3x4(x[0], x[1], cw[i].x);
+                            unpack_e4m3x4(x[2], x[3], cw[i].y);
+                            unpack_e4m3x4(x[4], x[5], cw[i].z);
+                            unpack_e4m3x4(x[6], x[7], cw[i].w);
+                            const uint4 a = some ? make_uint4(x[0], x[1], x[2], x[3]) : make_uint4(0u, 0u, 0u, 0u);
+                            const uint4 b = some ? make_uint4(x[4], x[5], x[6], x[7]) : make_uint4(0u, 0u, 0u, 0u);
+                            const int c = 2 * (lane & 3);
+                            *reinterpret_cast<uint4 *>(tile64 + swz_row(row, c + half64)) = half64 ? b : a;
+                            *reinterpret_cast<uint4 *>(tile64 + swz_row(row, c + (half64 ^ 1))) = half64 ? a : b;
+                        }
+                    }
+                    fence_proxy_async();  // the tensor core reads through the async proxy
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(is_v ? v_full + vs : k_full + ks);
+                } else if (!is_v) {
                     // K: two tokens a lane, 32 columns each.  The block goes to registers
                     // first: the stores then wait for no load, and the slot is free early.
                     const int swap = (tq >> 1) * 8;  // lanes of the second column half go the other way round: the writes meet no bank twice
@@ -310,7 +361,7 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
             __syncwarp();
         } else if (warp == kWarpPv) {
             // ---------------- P V products
-            const uint32_t idesc = umma_idesc_f16(128, 128);
+            const uint32_t idesc = umma_idesc_f16(128, 128) | (k8 ? 1u << 16 : 0u);  // 8 bits: V with its columns side by side (MN-major)
             int done = -1;
 #pragma unroll 1
             while (!timed_out && share.next(p, R, w, tile, from, whole, last)) {
@@ -326,7 +377,7 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
 #pragma unroll
                         for (int k = 0; k < PG; ++k) {
                             const int h = k >> 1;  // keys 0-31 -> O_0 (P of half 0), 32-63 -> O_1
-                            umma_bf16_ts(tmem + C::kColO + h * 128, tmem + b * 64 + h * 32 + (k & 1) * 8, umma_desc(v_addr + k * 32, 16, 1024), idesc,
+                            umma_bf16_ts(tmem + C::kColO + h * 128, tmem + b * 64 + h * 32 + (k & 1) * 8, k8 ? umma_desc(v_addr + k * 2048, 64 * 128, 1024) : umma_desc(v_addr + k * 32, 16, 1024), idesc,
                                          (j > 0 || (k & 1)) ? 1 : 0);
                         }
                         umma_commit(v_empty + vs);
@@ -386,6 +437,7 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
             if (real) row_key_bounds(w.sg.kend - w.sg.ql + (w.row0 + r) / p.G, w.sg.kend, p.causal, p.window, first, lo_r, hi_r);
             const int hi_k = min(hi_r, (w.page0 + w.pages) * kPage);  // of this piece
             float m = kNoMax, l = 0.f;
+            unsigned vref = 0;  // 8 bits: the largest exponent of a V page so far, which O_half counts in
 #pragma unroll 1
             for (int j = 0; j < ngr && !timed_out; ++j) {
                 const int J = gbase + j, b = J % NB;
@@ -393,18 +445,43 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
                 tc_fence_after();
                 float x[32];
                 tmem_ld32(tmem + lane_off + b * 64 + half * 32, x);
+                float f[2] = {sc, sc};           // of the scores of each of the half's two pages
+                unsigned vw[2] = {0, 0}, most = 0;
+                if constexpr (k8) {
+                    if (!wait_bar(sc_full + J % C::NS, (J / C::NS) & 1)) { timed_out = true; break; }
+                    const unsigned *kw = sWord + (J % C::NS) * PG + half * 2;
+                    vw[0] = kw[C::NS * PG];
+                    vw[1] = kw[C::NS * PG + 1];
+                    most = max(vw[0] & 0xffu, vw[1] & 0xffu);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) f[i] = fmaxf(sc * scale8_value(kw[i] & 0xffu), 1e-38f);
+                    if ((kw[0] | kw[1]) >> 16) {  // tokens that hold a NaN
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (kw[k >> 4] >> (16 + (k & 15)) & 1u) x[k] = CUDART_NAN_F;
+                    }
+                }
                 // (unsigned: a group's missing last pages may lie past 2^31)
                 const unsigned pos0 = (unsigned)(w.page0 + j * PG) * kPage + half * 32, lo_u = lo_r, hi_u = hi_k;
                 // Key bounds per score only where some real row of the warp does not see all 32.
                 if (!__all_sync(0xffffffffu, !real || (pos0 >= lo_u && pos0 + 32 <= hi_u))) {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) {
-                        const unsigned pos = pos0 + (k & 16) + 2 * ((k & 15) >> 2) + (k & 1) + 8 * ((k >> 1) & 1);  // the token at column k
+                        const unsigned pos = k8 ? pos0 + k : pos0 + (k & 16) + 2 * ((k & 15) >> 2) + (k & 1) + 8 * ((k >> 1) & 1);  // the token at column k
                         if (pos < lo_u || pos >= hi_u) x[k] = -CUDART_INF_F;
                     }
                 }
                 float mx;
-                {   // row maximum of the 32 scores as a tree of three-way maxima
+                if constexpr (k8) {  // the pages' maxima each as a tree of three-way maxima
+                    float t[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float *y = x + 16 * i;
+                        const float a = max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), max3(y[6], y[7], y[8]));
+                        t[i] = fmaxf(max3(a, max3(y[9], y[10], y[11]), max3(y[12], y[13], y[14])), y[15]) * f[i];
+                    }
+                    mx = fmaxf(t[0], t[1]);
+                } else {  // row maximum of the 32 scores as a tree of three-way maxima
                     float t[11];
 #pragma unroll
                     for (int k = 0; k < 10; ++k) t[k] = max3(x[3 * k], x[3 * k + 1], x[3 * k + 2]);
@@ -413,9 +490,12 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
                     mx = max3(max3(a, b3, c3), t[9], t[10]) * sc;
                 }
                 const bool grow = mx > m + kLazy4;
-                if (__any_sync(0xffffffffu, grow)) {
+                auto power = [](int d) { return d > -127 ? __uint_as_float((unsigned)(127 + d) << 23) : 0.f; };
+                if (__any_sync(0xffffffffu, grow) || (k8 && most > vref)) {
                     const float m_new = grow ? mx - kLift4 : m, alpha = ex2(m - m_new);
-                    if (j > 0 && __any_sync(0xffffffffu, grow && m != kNoMax)) {
+                    const bool raised = k8 && most > vref && vref > 0;
+                    const float all = raised ? alpha * power((int)vref - (int)most) : alpha;
+                    if (j > 0 && (raised || __any_sync(0xffffffffu, grow && m != kNoMax))) {
                         // O_half holds P V up to the group before against the old reference
                         if (!wait_bar(pv_done + (J - 1) % NB, ((J - 1) / NB) & 1)) { timed_out = true; break; }
                         tc_fence_after();
@@ -424,24 +504,32 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
                             float o[32];
                             tmem_ld32(tmem + lane_off + C::kColO + half * 128 + c0, o);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                            for (int k = 0; k < 32; ++k) o[k] *= all;
                             tmem_st32(tmem + lane_off + C::kColO + half * 128 + c0, o);
                         }
                     }
                     l *= alpha;
                     m = m_new;
+                    if (k8) vref = max(vref, most);
                 }
                 unsigned pk[16];
-                const uint64_t sc2 = f32x2(sc, sc), mm2 = f32x2(-m, -m);
+                const uint64_t mm2 = f32x2(-m, -m);
+                uint64_t fv[2];  // 8 bits: the V page's scale goes into the weights of the product
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float v = (vw[i] & 0xffu) ? power((int)(vw[i] & 0xffu) - (int)vref) : 0.f;
+                    fv[i] = f32x2(v, v);
+                }
                 uint64_t la = 0, lb = 0;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     float e0, e1;
-                    f32x2_split(fma_f32x2(f32x2(x[2 * k], x[2 * k + 1]), sc2, mm2), e0, e1);
+                    f32x2_split(fma_f32x2(f32x2(x[2 * k], x[2 * k + 1]), f32x2(f[k >> 3], f[k >> 3]), mm2), e0, e1);
                     e0 = ex2(e0);
                     e1 = ex2(e1);
                     if (k & 1) lb = add_f32x2(lb, f32x2(e0, e1));
                     else la = add_f32x2(la, f32x2(e0, e1));
+                    if constexpr (k8) f32x2_split(mul_f32x2(f32x2(e0, e1), fv[k >> 3]), e0, e1);
                     pk[k] = pack_f16x2(e0, e1);
                 }
                 {
@@ -461,6 +549,7 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
             tc_fence_after();
             sXm[half * R + r] = m == kNoMax ? (l != l ? 0.f : -CUDART_INF_F) : m;  // a row of NaN scores keeps its NaN sum
             sXl[half * R + r] = l;
+            if (k8 && r == 0) sUnit[half] = scale8_value(vref);  // (the same for all rows)
             const int flags = *reinterpret_cast<volatile int *>(sPiece + piece % C::kPieces);
             named_barrier(1, 256);
             if (timed_out) continue;
@@ -470,14 +559,21 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
             const float m0 = sXm[r], m1 = sXm[R + r], M = fmaxf(m0, m1);
             const float w0 = m0 == -CUDART_INF_F ? 0.f : ex2(m0 - M), w1 = m1 == -CUDART_INF_F ? 0.f : ex2(m1 - M);
             const float L = w0 * sXl[r] + w1 * sXl[R + r];
-            // A NaN in V on a page that not every row sees was left out: the rows that see it get it here.
+            const float v0 = k8 ? w0 * sUnit[0] : w0, v1 = k8 ? w1 * sUnit[1] : w1;  // of the halves' columns
+            // A NaN in V (4 bits: on a page that not every row sees) was left out: the rows that see it get it here.
             unsigned nan = 0;  // bit g: columns 16 g ..
             if (flags & 2)
 #pragma unroll 1
                 for (int li = 0; li < w.pages; ++li) {
                     const int pos0 = (w.page0 + li) * kPage;
                     const int bid = p.block_table[(long long)w.sg.col * p.mbps + table_page(w.page0 + li, p.ring_rows)];
-                    if ((pos0 >= w.lo_in && pos0 + kPage <= w.hi_in) || (unsigned)bid >= (unsigned)p.num_blocks) continue;
+                    if ((!k8 && pos0 >= w.lo_in && pos0 + kPage <= w.hi_in) || (unsigned)bid >= (unsigned)p.num_blocks) continue;
+                    if constexpr (k8) {  // the whole token
+                        const unsigned odd = *reinterpret_cast<const unsigned *>(p.v + ((size_t)bid * p.Hkv + w.h) * C::kBlock + 16 * D) >> 16;
+                        for (int k = max(lo_r - pos0, 0); k < min(hi_r - pos0, kPage); ++k)
+                            if (odd >> k & 1u) nan = 0xffu;
+                        continue;
+                    }
                     const unsigned char *ss = p.v + ((size_t)bid * p.Hkv + w.h) * C::kBlock + 8 * D;
                     for (int k = max(lo_r - pos0, 0); k < min(hi_r - pos0, kPage); ++k)
                         for (int g = 0; g < 8; ++g)
@@ -493,14 +589,14 @@ static __global__ void __launch_bounds__(Wide4::kThreads, 1) wide4_kernel(const 
                 tmem_ld32(tmem + lane_off + C::kColO + half * 64 + c0, o);
                 tmem_ld32(tmem + lane_off + C::kColO + 128 + half * 64 + c0, o1);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = (w0 != 0.f ? w0 * o[e] : 0.f) + (w1 != 0.f ? w1 * o1[e] : 0.f);
+                for (int e = 0; e < 32; ++e) o[e] = (w0 != 0.f ? v0 * o[e] : 0.f) + (w1 != 0.f ? v1 * o1[e] : 0.f);
                 if (real)
 #pragma unroll
-                    for (int g = 0; g < 8; ++g) {  // O's column 8 i + turn(g) is V's column 16 g + i
+                    for (int g = 0; g < 8; ++g) {  // 4 bits: O's column 8 i + turn(g) is V's column 16 g + i
                         const int tg = v_turn(g);
-                        float4 v = make_float4(o[tg], o[8 + tg], o[16 + tg], o[24 + tg]);
+                        float4 v = k8 ? make_float4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]) : make_float4(o[tg], o[8 + tg], o[16 + tg], o[24 + tg]);
                         if (nan >> g & 1u) v = make_float4(CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F, CUDART_NAN_F);
-                        const int d = g * 16 + half * 8 + c0 / 8;
+                        const int d = k8 ? half * 64 + c0 + 4 * g : g * 16 + half * 8 + c0 / 8;
                         if (whole)
                             store_out4(p, row * D + d, zero ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
                         else
