@@ -149,6 +149,34 @@ __device__ __forceinline__ void umma_commit(uint64_t *bar) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 
+// Products issued by a whole warp with one lane's predicate (lead), without a branch, and descriptors that are
+// their low word (address, leading offset) and a constant high one: an addition from product to product.
+struct UmmaDesc {
+    unsigned lo;
+    __device__ __forceinline__ UmmaDesc(unsigned addr, unsigned lbo) : lo((addr >> 4) & 0x3FFFu | (lbo >> 4) << 16) {}
+};
+constexpr unsigned kUmmaHigh = (1024u >> 4) | 1u << 14 | 2u << 29;  // stride of 8 rows, version, 128-byte swizzle
+__device__ __forceinline__ void umma_ss(unsigned lead, unsigned d_tmem, unsigned a, unsigned b, uint32_t idesc, unsigned accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n mov.b64 x, {%1, %6};\n mov.b64 y, {%2, %6};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(lead), "r"(kUmmaHigh)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts(unsigned lead, unsigned d_tmem, unsigned a_tmem, unsigned b, uint32_t idesc, unsigned accumulate) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n mov.b64 y, {%2, %6};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(idesc), "r"(accumulate), "r"(lead), "r"(kUmmaHigh)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit_by(unsigned lead, uint64_t *bar) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+
 // 32 consecutive fp32 columns of this thread's TMEM lane (warp-collective).
 __device__ __forceinline__ void tmem_ld32(unsigned taddr, float (&v)[32]) {
     unsigned r[32];

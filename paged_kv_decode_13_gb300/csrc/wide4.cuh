@@ -73,6 +73,21 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// A place in a ring of N, and the parity of its phase: carried along, as a division between two waits is on the groups' critical path.
+template <int N>
+struct RingAt {
+    int i = 0;
+    unsigned phase = 0;
+    bool again = false;  // not the first time round
+    __device__ __forceinline__ void next() {
+        if (++i == N) {
+            i = 0;
+            phase ^= 1;
+            again = true;
+        }
+    }
+};
+
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_constant__ Attend4Params p) {
     constexpr bool k8 = C::BITS == 8;
@@ -145,6 +160,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
     int tile, from, last, left = 0;
     bool whole, timed_out = false;
     int gbase = 0, issued = 0;  // groups before this piece; of them, copied
+    static_assert(NK == NV && NV == NB, "one place serves the tiles and the buffers");
+    RingAt<NK> tile3;           // group gbase + j's tiles and buffer
+    RingAt<NR> raws;            // and its raw pages
     if (warp >= 8 && warp < 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsOthers));
         // ---------------- raw pages to operand tiles
@@ -154,11 +172,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
         for (int piece = 0; !timed_out && share.next(p, R, w, tile, from, whole, last); ++piece) {
             const int ngr = (w.pages + PG - 1) / PG;
 #pragma unroll 1
-            for (int j = 0; j < ngr; ++j) {
-                const int J = gbase + j, ks = J % NK, vs = J % NV, rs = J % NR, li = j * PG + u;
+            for (int j = 0; j < ngr; ++j, tile3.next(), raws.next()) {
+                const int J = gbase + j, ks = tile3.i, vs = tile3.i, rs = raws.i, li = j * PG + u;
                 const bool mine = li < w.pages;
                 const unsigned char *st = raw + (size_t)(rs * PG + u) * C::kRaw;
-                if (!wait_bar(raw_full + rs, (J / NR) & 1)) { timed_out = true; break; }
+                const bool free_now = !tile3.again || mbar_try_wait((is_v ? v_empty : k_empty) + tile3.i, tile3.phase ^ 1);  // (asked before it is needed: an answer takes 110 cycles)
+                if (!wait_bar(raw_full + rs, raws.phase)) { timed_out = true; break; }
+                auto tile_free = [&] { return __all_sync(0xffffffffu, free_now) || wait_bar((is_v ? v_empty : k_empty) + tile3.i, tile3.phase ^ 1); };
                 if constexpr (k8) {
                     // Tokens l / 8 + 4 i, chunk l % 8 of 16 columns (K and V alike: both tiles have a token's columns side by side).
                     // Lanes of the second column half store their two 16-byte pieces the other way round: the writes meet no bank twice.
@@ -176,7 +196,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                     __syncwarp();
                     if (lane == 0) mbar_arrive(raw_empty + rs);
                     // (slot J % NS is free: its group's P V is done before the tile of group J - 3 is)
-                    if (is_v ? J >= NV && !wait_bar(v_empty + vs, ((J / NV) - 1) & 1) : J >= NK && !wait_bar(k_empty + ks, ((J / NK) - 1) & 1)) { timed_out = true; break; }
+                    if (!tile_free()) { timed_out = true; break; }
                     if (lane == 0) {
                         sWord[((is_v ? C::NS : 0) + J % C::NS) * PG + u] = word;
                         if (is_v && word >> 16) atomicOr(sPiece + piece % C::kPieces, 2);
@@ -219,7 +239,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(raw_empty + rs);
-                    if (J >= NK && !wait_bar(k_empty + ks, ((J / NK) - 1) & 1)) { timed_out = true; break; }
+                    if (!tile_free()) { timed_out = true; break; }
                     if (mine) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
@@ -267,7 +287,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                         sw &= keep;
                         if (__any_sync(0xffffffffu, nan != 0) && lane == 0) atomicOr(sPiece + piece % C::kPieces, 2);
                     }
-                    if (J >= NV && !wait_bar(v_empty + vs, ((J / NV) - 1) & 1)) { timed_out = true; break; }
+                    if (!tile_free()) { timed_out = true; break; }
                     const unsigned fa = scale4_pair(sw, 0), fb = scale4_pair(sw, 2);
                     unsigned char *dst = sV + (size_t)vs * C::kTile + v_turn(gq) * 128 + (((u * 2 + (tq >> 1)) ^ v_turn(gq)) << 4) + (tq & 1) * 8;
 #pragma unroll
@@ -300,11 +320,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                 const size_t block_stride = (size_t)p.Hkv * C::kBlock;
                 int id_reg = -1;  // page j0 + lane of the window of 32 pages
 #pragma unroll 1
-                for (int j = 0; j < ngr; ++j) {
-                    const int J = gbase + j, rs = J % NR, j0 = j * PG;
+                for (int j = 0; j < ngr; ++j, raws.next()) {
+                    const int J = gbase + j, rs = raws.i, j0 = j * PG;
                     if ((j0 & 31) == 0) id_reg = j0 + lane < w.pages ? bt_row[table_page(w.page0 + j0 + lane, p.ring_rows)] : -1;
                     const int bid = __shfl_sync(0xffffffffu, id_reg, (j0 + (lane >> 1)) & 31);
-                    if (J >= NR && !wait_bar(raw_empty + rs, ((J / NR) - 1) & 1)) { timed_out = true; break; }
+                    if (raws.again && !wait_bar(raw_empty + rs, raws.phase ^ 1)) { timed_out = true; break; }
                     if (lane < 2 * PG) {
                         const bool some = j0 + (lane >> 1) < w.pages, ok = (unsigned)bid < (unsigned)p.num_blocks;
                         if (some && ok) {
@@ -329,28 +349,26 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
         } else if (warp == kWarpS) {
             // ---------------- S products
             const uint32_t idesc = umma_idesc_f16(128, 64);
+            const unsigned lead = lane == 0, k_first = UmmaDesc(smem_u32(sK), 16).lo, q_first = UmmaDesc(smem_u32(sQ), 16).lo;
             int piece = 0;
 #pragma unroll 1
             for (; !timed_out && share.next(p, R, w, tile, from, whole, last); ++piece) {
                 const int ngr = (w.pages + PG - 1) / PG;
                 if (!wait_bar(q_full, piece & 1)) { timed_out = true; break; }
 #pragma unroll 1
-                for (int j = 0; j < ngr; ++j) {
-                    const int J = gbase + j, ks = J % NK, b = J % NB;
-                    if (!wait_bar(k_full + ks, (J / NK) & 1)) { timed_out = true; break; }
+                for (int j = 0; j < ngr; ++j, tile3.next()) {
+                    const int ks = tile3.i, b = tile3.i;
+                    const bool read = !tile3.again || mbar_try_wait(pv_done + b, tile3.phase ^ 1);
+                    if (!wait_bar(k_full + ks, tile3.phase)) { timed_out = true; break; }
                     // S(J) goes over buffer b, which P V(J - NB) reads P(J - NB) from
-                    if (J >= NB && !wait_bar(pv_done + b, ((J / NB) - 1) & 1)) { timed_out = true; break; }
+                    if (!__all_sync(0xffffffffu, read) && !wait_bar(pv_done + b, tile3.phase ^ 1)) { timed_out = true; break; }
                     tc_fence_after();
-                    if (lane == 0) {
-                        const unsigned k_addr = smem_u32(sK + (size_t)ks * C::kTile), q_addr = smem_u32(sQ);
+                    const unsigned k_lo = k_first + ks * (C::kTile >> 4);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k)
-                            umma_bf16(tmem + b * 64, umma_desc(q_addr + (k >> 2) * C::kQHalf + (k & 3) * 32, 16, 1024),
-                                      umma_desc(k_addr + (k >> 2) * (64 * 128) + (k & 3) * 32, 16, 1024), idesc, k > 0 ? 1 : 0);
-                        umma_commit(s_full + b);
-                        umma_commit(k_empty + ks);
-                    }
-                    __syncwarp();
+                    for (int k = 0; k < D / 16; ++k)
+                        umma_ss(lead, tmem + b * 64, q_first + (((k >> 2) * C::kQHalf + (k & 3) * 32) >> 4), k_lo + (((k >> 2) * (64 * 128) + (k & 3) * 32) >> 4), idesc, k > 0);
+                    umma_commit_by(lead, s_full + b);
+                    umma_commit_by(lead, k_empty + ks);
                 }
                 gbase += ngr;
             }
@@ -362,28 +380,26 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
         } else if (warp == kWarpPv) {
             // ---------------- P V products
             const uint32_t idesc = umma_idesc_f16(128, 128) | (k8 ? 1u << 16 : 0u);  // 8 bits: V with its columns side by side (MN-major)
+            const unsigned lead = lane == 0, v_first = UmmaDesc(smem_u32(sV), k8 ? 64 * 128 : 16).lo;
             int done = -1;
 #pragma unroll 1
             while (!timed_out && share.next(p, R, w, tile, from, whole, last)) {
                 const int ngr = (w.pages + PG - 1) / PG;
 #pragma unroll 1
-                for (int j = 0; j < ngr; ++j) {
-                    const int J = gbase + j, vs = J % NV, b = J % NB;
-                    if (!wait_bar(v_full + vs, (J / NV) & 1)) { timed_out = true; break; }
-                    if (!wait_bar(p_full + b, (J / NB) & 1)) { timed_out = true; break; }
+                for (int j = 0; j < ngr; ++j, tile3.next()) {
+                    const int J = gbase + j, vs = tile3.i, b = tile3.i;
+                    const bool weights = mbar_try_wait(p_full + b, tile3.phase);
+                    if (!wait_bar(v_full + vs, tile3.phase)) { timed_out = true; break; }
+                    if (!__all_sync(0xffffffffu, weights) && !wait_bar(p_full + b, tile3.phase)) { timed_out = true; break; }
                     tc_fence_after();
-                    if (lane == 0) {
-                        const unsigned v_addr = smem_u32(sV + (size_t)vs * C::kTile);
+                    const unsigned v_lo = v_first + vs * (C::kTile >> 4);
 #pragma unroll
-                        for (int k = 0; k < PG; ++k) {
-                            const int h = k >> 1;  // keys 0-31 -> O_0 (P of half 0), 32-63 -> O_1
-                            umma_bf16_ts(tmem + C::kColO + h * 128, tmem + b * 64 + h * 32 + (k & 1) * 8, k8 ? umma_desc(v_addr + k * 2048, 64 * 128, 1024) : umma_desc(v_addr + k * 32, 16, 1024), idesc,
-                                         (j > 0 || (k & 1)) ? 1 : 0);
-                        }
-                        umma_commit(v_empty + vs);
-                        umma_commit(pv_done + b);
+                    for (int k = 0; k < PG; ++k) {
+                        const int h = k >> 1;  // keys 0-31 -> O_0 (P of half 0), 32-63 -> O_1
+                        umma_ts(lead, tmem + C::kColO + h * 128, tmem + b * 64 + h * 32 + (k & 1) * 8, v_lo + (k * (k8 ? 2048 : 32) >> 4), idesc, j > 0 || (k & 1));
                     }
-                    __syncwarp();
+                    umma_commit_by(lead, v_empty + vs);
+                    umma_commit_by(lead, pv_done + b);
                     done = J;
                 }
                 gbase += ngr;
@@ -439,16 +455,18 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
             float m = kNoMax, l = 0.f;
             unsigned vref = 0;  // 8 bits: the largest exponent of a V page so far, which O_half counts in
 #pragma unroll 1
-            for (int j = 0; j < ngr && !timed_out; ++j) {
-                const int J = gbase + j, b = J % NB;
-                if (!wait_bar(s_full + b, (J / NB) & 1)) { timed_out = true; break; }
+            for (int j = 0; j < ngr && !timed_out; ++j, tile3.next()) {
+                const int J = gbase + j, b = tile3.i;
+                // (an mbarrier's answer takes 110 cycles: both are asked before either is looked at)
+                const bool scaled = !k8 || mbar_try_wait(sc_full + J % C::NS, (J / C::NS) & 1), there = mbar_try_wait(s_full + b, tile3.phase);
+                if (!__all_sync(0xffffffffu, scaled && there) &&
+                    ((k8 && !wait_bar(sc_full + J % C::NS, (J / C::NS) & 1)) || !wait_bar(s_full + b, tile3.phase))) { timed_out = true; break; }
                 tc_fence_after();
                 float x[32];
                 tmem_ld32(tmem + lane_off + b * 64 + half * 32, x);
                 float f[2] = {sc, sc};           // of the scores of each of the half's two pages
                 unsigned vw[2] = {0, 0}, most = 0;
                 if constexpr (k8) {
-                    if (!wait_bar(sc_full + J % C::NS, (J / C::NS) & 1)) { timed_out = true; break; }
                     const unsigned *kw = sWord + (J % C::NS) * PG + half * 2;
                     vw[0] = kw[C::NS * PG];
                     vw[1] = kw[C::NS * PG + 1];
@@ -494,10 +512,10 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                 if (__any_sync(0xffffffffu, grow) || (k8 && most > vref)) {
                     const float m_new = grow ? mx - kLift4 : m, alpha = ex2(m - m_new);
                     const bool raised = k8 && most > vref && vref > 0;
-                    const float all = raised ? alpha * power((int)vref - (int)most) : alpha;
+                    const float all = raised ? alpha * power((int)vref - (int)(most + 1)) : alpha;  // (a step above the largest: it moves less often)
                     if (j > 0 && (raised || __any_sync(0xffffffffu, grow && m != kNoMax))) {
                         // O_half holds P V up to the group before against the old reference
-                        if (!wait_bar(pv_done + (J - 1) % NB, ((J - 1) / NB) & 1)) { timed_out = true; break; }
+                        if (!wait_bar(pv_done + (b ? b - 1 : NB - 1), b ? tile3.phase : tile3.phase ^ 1)) { timed_out = true; break; }
                         tc_fence_after();
 #pragma unroll 1
                         for (int c0 = 0; c0 < 128; c0 += 32) {
@@ -510,7 +528,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                     }
                     l *= alpha;
                     m = m_new;
-                    if (k8) vref = max(vref, most);
+                    if (k8 && most > vref) vref = most + 1;
                 }
                 unsigned pk[16];
                 const uint64_t mm2 = f32x2(-m, -m);
@@ -545,7 +563,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
             }
             gbase += ngr;
             // ---- the piece's end: the last product has landed
-            if (!timed_out && !wait_bar(pv_done + (gbase - 1) % NB, ((gbase - 1) / NB) & 1)) timed_out = true;
+            if (!timed_out && !wait_bar(pv_done + (tile3.i ? tile3.i - 1 : NB - 1), tile3.i ? tile3.phase : tile3.phase ^ 1)) timed_out = true;
             tc_fence_after();
             sXm[half * R + r] = m == kNoMax ? (l != l ? 0.f : -CUDART_INF_F) : m;  // a row of NaN scores keeps its NaN sum
             sXl[half * R + r] = l;
