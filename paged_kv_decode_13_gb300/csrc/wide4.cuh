@@ -19,8 +19,9 @@
 //               writes wide and off each other's banks: token 8 hi + 2 t + n
 //               of a page sits at 4 t + 2 hi + n, V column 16 g + i at row
 //               8 i + turn(g);
-//   warp 16     S(j) = Q K_j^T (M 128, N 64, K 128), Q and K in shared memory,
-//               into one of NB buffers of TMEM;
+//   warp 16     S(j) = Q K_j^T (M 128, N 64, K 128), Q from TMEM (from shared memory its
+//               reads met the dequantising warps' traffic: 89 us of 8-bit drafts
+//               against 86), K from shared memory, into one of NB buffers of TMEM;
 //   warps 0-7   softmax: row t belongs to warps t / 32 and t / 32 + 4, each with
 //               32 of a group's 64 keys, its own running maximum and sum and
 //               its own O, as in the bf16 tile; P (fp16) over the S columns read;
@@ -47,17 +48,17 @@ namespace pkv {
 template <int BITS_>
 struct Wide4 {
     static constexpr int BITS = BITS_, D = 128, R = 128, kThreads = 640, PG = 4;
-    static constexpr int NK = 3, NV = 3, NB = 3, NR = BITS == 4 ? 6 : 5;  // K, V tiles; S / P buffers; raw groups
+    static constexpr int NK = 3, NV = 3, NB = 3, NR = BITS == 4 ? 8 : 7;  // K, V tiles; S / P buffers; raw groups
     static constexpr int NS = 8;                                    // 8 bits: groups whose pages' scales are kept (the copies are 6 ahead of the softmax at most)
     static constexpr int kBlock = BITS == 4 ? block4_bytes(D) : block8_bytes(D), kRaw = 2 * kBlock;
     static constexpr unsigned kTile = 64 * 256;                     // K: two halves of 64 tokens x 64 columns; V^T: 128 columns x 64 tokens
-    static constexpr unsigned kQHalf = 128 * 128;
     static constexpr size_t kRawBytes = (size_t)PG * NR * kRaw;
     // registers a thread: at launch, of the softmax warps and of the others while the roles run
     static constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsOthers = 72;
     static constexpr int kBars = 2 * NK + 2 * NV + 3 * NB + 2 + 2 * NR + (BITS == 8 ? NS : 0), kPieces = 16;
-    static constexpr size_t kSmem = 1024 + (size_t)(NK + NV) * kTile + 2 * kQHalf + kRawBytes + 6 * R * 4 + kBars * 8 + (BITS == 8 ? 2 * NS * PG * 4 : 0) + 256;
-    static constexpr unsigned kColO = 64 * NB;                      // O_h at kColO + 128 h
+    static constexpr size_t kSmem = 1024 + (size_t)(NK + NV) * kTile + kRawBytes + 6 * R * 4 + kBars * 8 + (BITS == 8 ? 2 * NS * PG * 4 : 0) + 256;
+    static constexpr unsigned kColO = 64 * NB, kColQ = kColO + 256; // O_h at kColO + 128 h; Q as fp16 pairs
+    static_assert(kColQ + 64 <= 512, "the columns of TMEM");
     static_assert(kSmem <= 232448, "exceeds the per-CTA shared memory limit");
     static_assert(256 * kRegsSoftmax + 384 * kRegsOthers <= kThreads * kRegs, "the roles' registers fit the launch's");
     static_assert(kBlock % 16 == 0, "copies stay 16-byte aligned");
@@ -96,8 +97,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sK = smem_raw + (-smem_u32(smem_raw) & 1023u);  // pointer arithmetic keeps the shared address space (a cast would lose it)
     unsigned char *sV = sK + (size_t)NK * C::kTile;
-    unsigned char *sQ = sV + (size_t)NV * C::kTile;
-    unsigned char *raw = sQ + 2 * C::kQHalf;                        // [NR][PG] raw pages
+    unsigned char *raw = sV + (size_t)NV * C::kTile;                // [NR][PG] raw pages
     float *sQm = reinterpret_cast<float *>(raw + C::kRawBytes);     // [2][R] largest query magnitude of each half
     float *sXm = sQm + 2 * R, *sXl = sXm + 2 * R;                   // [2][R] each half's maximum and sum
     uint64_t *bars = reinterpret_cast<uint64_t *>(sXl + 2 * R);
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
         } else if (warp == kWarpS) {
             // ---------------- S products
             const uint32_t idesc = umma_idesc_f16(128, 64);
-            const unsigned lead = lane == 0, k_first = UmmaDesc(smem_u32(sK), 16).lo, q_first = UmmaDesc(smem_u32(sQ), 16).lo;
+            const unsigned lead = lane == 0, k_first = UmmaDesc(smem_u32(sK), 16).lo;
             int piece = 0;
 #pragma unroll 1
             for (; !timed_out && share.next(p, R, w, tile, from, whole, last); ++piece) {
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                     const unsigned k_lo = k_first + ks * (C::kTile >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        umma_ss(lead, tmem + b * 64, q_first + (((k >> 2) * C::kQHalf + (k & 3) * 32) >> 4), k_lo + (((k >> 2) * (64 * 128) + (k & 3) * 32) >> 4), idesc, k > 0);
+                        umma_ts(lead, tmem + b * 64, tmem + C::kColQ + k * 8, k_lo + (((k >> 2) * (64 * 128) + (k & 3) * 32) >> 4), idesc, k > 0);
                     umma_commit_by(lead, s_full + b);
                     umma_commit_by(lead, k_empty + ks);
                 }
@@ -439,13 +439,17 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                 // (never 0: a masked score times it has to stay -inf)
                 sc = fmaxf(fabsf(p.scale_log2) * __uint_as_float((unsigned)(127 - k2) << 23), 1e-38f);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    unsigned v[4] = {qv[c].x, qv[c].y, qv[c].z, qv[c].w};
+                for (int c = 0; c < 8; c += 4) {  // (the products of the piece before are done: its last S has been read)
+                    unsigned v[16];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = pack_f16x2(__uint_as_float(v[k] << 16) * up, __uint_as_float(v[k] & 0xffff0000u) * up);
-                    *reinterpret_cast<uint4 *>(sQ + half * C::kQHalf + swz_row(r, c)) = make_uint4(v[0], v[1], v[2], v[3]);
+                    for (int k = 0; k < 16; ++k) {
+                        const uint4 &y = qv[c + (k >> 2)];
+                        const unsigned x = (k & 3) == 0 ? y.x : (k & 3) == 1 ? y.y : (k & 3) == 2 ? y.z : y.w;
+                        v[k] = pack_f16x2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+                    }
+                    tmem_st16(tmem + lane_off + C::kColQ + half * 32 + c * 4, v);
                 }
-                fence_proxy_async();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_full);
             }
