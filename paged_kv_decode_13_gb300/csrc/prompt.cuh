@@ -42,6 +42,7 @@
 // timeout ends every role, rows not written yet read zero and PKV_ERR_TIMEOUT is set.
 #pragma once
 
+#include <limits.h>
 #include <math_constants.h>
 
 #include "prompt_launch.h"
@@ -448,6 +449,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         // (no index of a run-time value: the item would live in local memory, 500 cycles a look where the products' warp asks between two of them)
         const int f = NT == 1 ? w.b0 : t ? w.first[NT - 1] : w.first[0], e = NT == 1 ? w.b1 : t ? w.last[NT - 1] : w.last[0];
         if (e <= f) return;
+        // blocks that every row of the warp sees whole (rows that are none do not matter)
+        const int in0 = __reduce_max_sync(0xffffffffu, real ? (lo_r + C::kKeys - 1) / C::kKeys : 0);
+        const int in1 = __reduce_min_sync(0xffffffffu, real ? hi_r / C::kKeys : INT_MAX);
 #pragma unroll 1
         for (int j = f; ok && j < e; ++j) {
             const int slot = NT == 2 ? t : (j - w.b0) & 1;
@@ -462,8 +466,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_free);  // S is in registers: the next one may go over it
+            // (P's slot: whether the product that read it is done, asked before it is needed; an answer takes 110 cycles)
+            const bool p_free = !(used >> slot & 1) || mbar_try_wait(pv_done + slot, (phase >> slot & 1) ^ 1);
+            used |= 1u << slot;
             const int pos0 = j * C::kKeys;
-            if (!__all_sync(0xffffffffu, !real || (pos0 >= lo_r && pos0 + C::kKeys <= hi_r))) {
+            if (j < in0 || j >= in1) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     // bits of the chunk's keys that the row sees
@@ -487,9 +494,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
                 }
                 mx = fmaxf(max3(y[0], y[1], y[2]), y[3]) * sc;
             }
-            // P's slot: the product that read it is done
-            if ((used >> slot & 1) && !(ok = wait_bar(pv_done + slot, (phase >> slot & 1) ^ 1))) break;
-            used |= 1u << slot;
+            if (!__all_sync(0xffffffffu, p_free) && !(ok = wait_bar(pv_done + slot, (phase >> slot & 1) ^ 1))) break;
             const bool grow = mx > m + kPromptLazy;
             if (__any_sync(0xffffffffu, grow)) {
                 const float m_new = grow ? mx : m, alpha = exp2_fast(m - m_new);
@@ -606,13 +611,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = y[k];
             }
-            float sum = 0.f;
+            float test[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
-                sum = fmaf(o[k], 0.f, sum);  // NaN where one is not finite
+                test[k & 3] = fmaf(o[k], 0.f, test[k & 3]);  // NaN where one is not finite
                 o[k] = zero ? 0.f : o[k] * inv;
             }
-            odd |= sum != 0.f;
+            odd |= (test[0] + test[1]) + (test[2] + test[3]) != 0.f;
             if (p.out_bf16) {
                 __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(p.out) + at + c0;
                 if (c0 + 32 <= p.D) {
