@@ -15,12 +15,12 @@
 // turn.
 //
 // Small calls are a launch: one token of 32 + 8 + 8 heads 4.1 us, 256 tokens 7.0 us.
-// Long ones should be bound by HBM and are bound by issue and latency: 16,400
-// tokens of 32 + 8 + 8 heads of 128 (330 MB), norm and half the head rotated,
-// 76 us, 4.3 TB/s, against 49 us at the rate of a copy; 2,800 instructions a token
-// keep the schedulers 52 % busy, at 20 warps an SM (96 registers): four heads are
-// loaded together but handled one behind the other, each a chain of a sum, shuffles and a
-// root.  Three
+// Long ones should be bound by HBM and are bound by issue and latency: 13,033
+// tokens of 32 + 8 + 8 heads of 128 (320 MB), norm and the whole head rotated by three axes,
+// 81 us, 4.0 TB/s, against 47 us at the rate of a copy (norm_rope alone, without cache and v,
+// 62 us); some 2,800 instructions a token at 20 warps an SM (96 registers): four heads are
+// loaded together, each a chain of a sum, shuffles and a root, two chains beside each other
+// (one behind the other: 84 and 71 us).  Three
 // heads' loads in flight or six, more warps with fewer registers, prefetches,
 // loads rolling from row to row (85 us) and a version fed by bulk copies through shared memory (95 us) were slower.
 //
@@ -226,6 +226,69 @@ struct RopeSlot {
     int token;        // slot in the page
 };
 
+// kRopeUnroll groups of heads whose rows are in `raw`, with what is done to them known when it is
+// compiled: no branch lies between the groups, so that their chains of a sum, shuffles and
+// a root run beside each other, two at a time (four take too many registers).
+template <typename T, int PAIR, bool NORM, bool TURN>
+__device__ __forceinline__ void rope_groups(Raw8<T> (&raw)[kRopeUnroll], float inv_d, float eps, int per, const float (&ca)[8], const float (&sb)[8],
+                                            unsigned turned, int partner) {
+    constexpr int B = 2;
+#pragma unroll
+    for (int u0 = 0; u0 < kRopeUnroll; u0 += B) {
+        float x[B][8], rinv[B];
+#pragma unroll
+        for (int u = 0; u < B; ++u) raw[u0 + u].get(x[u]);
+        if constexpr (NORM) {
+            float ss[B];
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                uint64_t s2 = 0;
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) s2 = fma_f32x2(f32x2(x[u][e], x[u][e + 1]), f32x2(x[u][e], x[u][e + 1]), s2);
+                float st;
+                f32x2_split(s2, ss[u], st);
+                ss[u] += st;
+            }
+            for (int o = per >> 1; o; o >>= 1)
+#pragma unroll
+                for (int u = 0; u < B; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+#pragma unroll
+            for (int u = 0; u < B; ++u) rinv[u] = rsqrtf(fmaf(ss[u], inv_d, eps));
+        }
+        Raw8<T> o[B];
+        if constexpr (TURN && PAIR == kByShuffle)
+#pragma unroll
+            for (int u = 0; u < B; ++u)
+#pragma unroll
+                for (int e = 0; e < 2 * (int)sizeof(T); ++e) o[u].w[e] = __shfl_sync(0xffffffffu, raw[u0 + u].w[e], partner);
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+            float y[8], z[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) f32x2_split(mul_f32x2(f32x2(x[u][e], x[u][e + 1]), f32x2(ca[e], ca[e + 1])), y[e], y[e + 1]);
+            if constexpr (TURN) {
+                if constexpr (PAIR == kInLane) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] = x[u][e ^ 1];
+                } else {
+                    o[u].get(z);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {  // (columns that are not rotated never meet a partner's infinity)
+                    float a, b;
+                    f32x2_split(fma_f32x2(f32x2(z[e], z[e + 1]), f32x2(sb[e], sb[e + 1]), f32x2(y[e], y[e + 1])), a, b);
+                    y[e] = turned ? a : y[e];
+                    y[e + 1] = turned ? b : y[e + 1];
+                }
+            }
+            if constexpr (NORM)
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) f32x2_split(mul_f32x2(f32x2(y[e], y[e + 1]), f32x2(rinv[u], rinv[u])), y[e], y[e + 1]);
+            raw[u0 + u].set(y);
+        }
+    }
+}
+
 // The heads [h0, h1) of one kind (q, k or v) of a row.  ca, sb: this lane's
 // factors of its own and its partner's columns; norm, turn: what is done to
 // them; turned: bit e set where column e of the lane is rotated.
@@ -251,6 +314,21 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, const T *src, T 
         for (int u = 0; u < kRopeUnroll; ++u) {
             raw[u].clear();
             if (col_ok && hb + u * heads < h1) raw[u].load(src + u * step);
+        }
+        if (CACHE != kFp4 && PAIR != kByShared && whole && hb - sub + kRopeUnroll * heads <= h1) {  // (uniform) every group is whole
+            if (norm && turn) rope_groups<T, PAIR, true, true>(raw, inv_d, p.eps, per, ca, sb, turned, partner);
+            else if (turn) rope_groups<T, PAIR, false, true>(raw, inv_d, p.eps, per, ca, sb, turned, partner);
+            else if (norm) rope_groups<T, PAIR, true, false>(raw, inv_d, p.eps, per, ca, sb, turned, partner);
+#pragma unroll
+            for (int u = 0; u < kRopeUnroll; ++u) {
+                if (!col_ok) continue;
+                if (CACHE == kSameType && pool) raw[u].store(reinterpret_cast<T *>(pool + u * pool_step));
+                if (dst) raw[u].store(dst + u * step);
+            }
+            src += kRopeUnroll * step;
+            if (dst) dst += kRopeUnroll * step;
+            if (CACHE != kNoCache && pool) pool += kRopeUnroll * pool_step;
+            continue;
         }
 #pragma unroll
         for (int u = 0; u < kRopeUnroll; ++u) {
