@@ -1023,8 +1023,21 @@ int pkv_norm_rope_append(const pkv_cache *c, int32_t layer, const pkv_rope *rope
     p.mbps = c->max_blocks_per_seq;
     p.ring_rows = c->ring_rows;
     p.window = window;
-    if (c->dtype == PKV_FP8)
-        return launch_status(launch_append8(p, device_sms(current_device()), reinterpret_cast<cudaStream_t>(stream)));
+    if (c->dtype == PKV_FP8) {
+        const int sms = device_sms(current_device());
+        if (p.q && p.rows >= kAppend8OwnQ) {
+            RopeParams q = p;  // no heads of k and v
+            q.k = q.v = nullptr;
+            q.k_out = q.v_out = nullptr;
+            q.k_pool = q.v_pool = nullptr;
+            q.Hkv = 0;
+            const cudaError_t e = launch_rope(q, kSameType, false, sms, reinterpret_cast<cudaStream_t>(stream));
+            if (e != cudaSuccess) return launch_status(e);
+            p.q = nullptr;
+            p.q_out = nullptr;
+        }
+        return launch_status(launch_append8(p, sms, reinterpret_cast<cudaStream_t>(stream)));
+    }
     return launch_status(launch_rope(p, c->dtype == PKV_FP4 ? kFp4 : kSameType, c->dtype == PKV_F32, device_sms(current_device()),
                                      reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -5,7 +5,7 @@
 // warps take heads (of q, then k, then v).  A warp holds the page's new rows of a head
 // in registers, 16-byte loads all in flight together, turns them as the row kernel
 // does (rope.cuh: same order of operations, so k is the row that a bf16 cache would
-// hold), takes the largest magnitude of all of them, and writes codes, the scale and
+// hold; the queries of a long step go through that kernel itself), takes the largest magnitude of all of them, and writes codes, the scale and
 // the rows as they are held.  Tokens that are in the page already keep the scale
 // from shrinking; where it grows, their codes are brought to it.
 //
@@ -425,12 +425,19 @@ __global__ void __launch_bounds__(kAppend8Threads, PAIR == kPlainRows ? (D == 25
             __syncthreads();
             if (pass && sOwner != s) break;
             if constexpr (PAIR != kPlainRows) {
-                for (int i = tid; i < kPage * pairs; i += kAppend8Threads) {
-                    const int j = i / pairs, e = i % pairs, row = sRow[pass][j];
-                    if (row < 0) continue;
-                    unsigned pos = (unsigned)sPos[pass][j];
-                    if (p.positions) pos = (unsigned)p.positions[p.axis ? (long long)row * p.axes + min((int)p.axis[e], p.axes - 1) : row];
-                    angles[i] = angle_of(pos, p.turns[e], p.mscale);
+                // a thread keeps to one pair, and takes every n-th slot
+                const int width = pairs <= 32 ? 32 : pairs <= 64 ? 64 : 128, e = tid & (width - 1);
+                if (e < pairs) {
+                    const unsigned long long turn = p.turns[e];
+                    const int axis = p.axis ? min((int)p.axis[e], p.axes - 1) : 0;
+#pragma unroll 4
+                    for (int j = tid / width; j < kPage; j += kAppend8Threads / width) {
+                        const int row = sRow[pass][j];
+                        if (row < 0) continue;
+                        unsigned pos = (unsigned)sPos[pass][j];
+                        if (p.positions) pos = (unsigned)p.positions[p.axis ? (long long)row * p.axes + axis : row];
+                        angles[j * pairs + e] = angle_of(pos, turn, p.mscale);
+                    }
                 }
                 __syncthreads();
             }

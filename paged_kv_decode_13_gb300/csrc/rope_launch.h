@@ -17,6 +17,11 @@ cudaError_t launch_rope(RopeParams &p, int cache, bool f32, int sms, cudaStream_
 // CTAs an SM is given, at most, before pages share one, and before the heads of a page do.
 constexpr int kAppend8Most = 16;
 constexpr int kAppend8Fill = 6;
+// Rows from which the queries of such a step go through the row kernel, in a launch of their own.  A page's
+// CTA reads every angle again for each head, which is soon slower than the second launch: 32 + 8 heads of 128,
+// one launch against two: 512 rows of one prompt 12.9 / 21.2 us, 1024 rows 23.6 / 23.9, 4096 rows 67 / 51;
+// a row for each of 256 sequences 20.8 / 20.4, 1024 sequences 52 / 38, 4096 228 / 151.
+constexpr int kAppend8OwnQ = 1024;
 
 // The append to an 8-bit cache (bf16 rows; head_dim 64, 128 or 256, S > 0).
 cudaError_t launch_append8(const RopeParams &p, int sms, cudaStream_t stream);

@@ -639,6 +639,41 @@ def test_side_stream_and_graph(pkv):
         check(f, out, lse, q=qo.cpu())
 
 
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("rows", [1023, 1024, 2600])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_queries_of_long_steps(pkv, D, rows, in_place):
+    """The queries of many rows: as norm_rope turns them; rows of no segment and of refused ones stay as they were."""
+    g = torch.Generator().manual_seed(rows)
+    ql = [1, 700, 0, 33, rows - 764, 20]
+    w = workloads.batched(S=6, max_len=2000, lengths=[n + 5 for n in ql], q_heads=4, kv_heads=1, head_dim=D)
+    q0 = [sum(ql[:i]) for i in range(6)]
+    w.seq_info = torch.tensor([[a, n, i, n + 5] for i, (a, n) in enumerate(zip(q0, ql))], dtype=torch.int32)
+    w.seq_info[3, 2] = 6          # no such sequence
+    w.block_table[5, 1] = 1 << 20   # no such page
+    valid = [s for i, s in enumerate(w.seq_info.tolist()) if i not in (3, 5)]
+    total = rows                  # the last ten belong to none
+    kn, vn = [torch.randn(total, 1, D, generator=g).bfloat16() for _ in range(2)]
+    q = torch.randn(total, 4, D, generator=g).bfloat16().cuda()
+    wq, wk = [(1 + 0.2 * torch.randn(D, generator=g)).bfloat16().cuda() for _ in range(2)]
+    rope = pkv.Rope(pkv.rope_inv_freq(D)[0], q_weight=wq, k_weight=wk, device="cuda")
+    f, err = Fp8(pkv, w), pkv.new_err_flags()
+    pos, new = np.zeros(total, np.int32), np.zeros(total, bool)
+    for a, n, _, kend in valid:
+        pos[a:a + n], new[a:a + n] = np.arange(kend - n, kend), True
+    q2, k2 = q.clone(), kn.cuda()
+    pkv.norm_rope(rope, q2, k2, torch.from_numpy(pos).cuda())
+    new = torch.from_numpy(new).cuda()
+    qo = q.clone() if in_place else torch.full_like(q, 9)
+    want = torch.where(new[:, None, None], q2, qo)
+    ko, vo = torch.full_like(k2, 9), torch.full_like(k2, 9)
+    pkv.norm_rope_append(f.cache, 0, rope, qo if in_place else q, kn.cuda(), vn.cuda(), w.seq_info.cuda(), None if in_place else qo, err, k_out=ko, v_out=vo)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 1 | 8 and torch.equal(qo, want)
+    f.check_guards()
+    check_append(f, f.bytes, k2, vn, ko, vo, si=valid)
+
+
 @pytest.mark.parametrize("with_rope", [False, True])
 @pytest.mark.parametrize("S", [1, 6])
 def test_decode_step(pkv, with_rope, S):
