@@ -1071,9 +1071,11 @@ int pkv_attend_prompt(int32_t head_dim, int32_t kv_heads, const pkv_rows *r, con
     p.G = r->q_heads / kv_heads;
     p.tokens = 128 / p.G;
     const int group = k.tiles * p.tokens;  // tokens of a CTA
-    p.items = S > 0 ? (int)(((long long)std::min(max_len, r->total_rows) + group - 1) / group) : 1;
-    const long long ctas = (long long)p.items * std::max(S, 1) * kv_heads;
-    if (ctas > INT32_MAX) return PKV_EINVAL;
+    // tile groups that segments without a row in common can have: each has one that its rows do not fill
+    const long long each = ((long long)std::min(max_len, r->total_rows) + group - 1) / group;
+    const long long units = std::max(std::min(each * S, (long long)r->total_rows / group + S), 1ll), ctas = units * kv_heads;
+    if (ctas > INT32_MAX || each * kv_heads > INT32_MAX) return PKV_EINVAL;
+    p.units = (int)units;
     auto fn = encode_fn();
     if (!fn) return PKV_ECUDA;
     // (head_dim, heads, rows); a box is 64 columns of the given heads and rows, with 128-byte swizzling

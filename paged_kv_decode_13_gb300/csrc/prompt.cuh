@@ -9,10 +9,12 @@
 // prompts fill tiles and the causal edge of a tile is 128 / G tokens wide.  It walks over
 // the keys that some row sees in blocks of 128.
 //
-// The grid has a CTA for every such item, the longest first, but a CTA that runs
+// The grid has a CTA for every such item that the rows can make (the longest of 32 segments first), but a CTA that runs
 // takes the items of CTAs that have not started (cluster launch control) instead of ending: one
 // CTA an SM stays, dynamic balance without a counter in memory, and the next
-// item's copies and products start while the rows of this one are written.
+// item's copies and products start while the rows of this one are written.  Which item a number is, one
+// warp finds in the table as it goes along it.  (A CTA for each item that a segment could have at most: 128 prompts
+// of 30 rows where 2048 were allowed 205 us, now 47; one of 4096 beside 63 of 30 rows 308, now 128.)
 //
 // Roles, meeting on mbarriers only, each walking through the items by itself:
 //   softmax warps (four a tile; thread = row)  read S from TMEM, mask, take the
@@ -20,15 +22,20 @@
 //       and at the end the normalised rows out.  The reference moves only when a score
 //       passes it by 2^8 (then O is rescaled in TMEM; no product is in flight on it then);
 //   MMA warps   S = Q K^T (M 128, N 128; Q and K in shared memory) and O += P V (P
-//       from TMEM, V as an MN-major tile), a warp each;
-//   copy warp   asks for the next item; Q, then K and V blocks through a ring of stages
+//       from TMEM, V as an MN-major tile), a warp each; the second one then looks after rows of no
+//       segment or of two, and refused segments;
+//   copy warp   Q, then K and V blocks through a ring of stages
 //       (TMA, 128-byte swizzle; rows past the tensor and columns past head_dim come as zeros);
-//   cover warp  rows of no segment, rows of two, refused segments.
+//   dealer warp   asks for the next item, finds it in the table and works out its blocks for all.
+// Where items are short a role's code is cold each time, some ten cycles an instruction: the kernel has to
+// stay small (88 KB), what an item needs is worked out once, and the steps are spread over warps that
+// wait anyway.  (Every role working items out for itself, 120 KB: 16 prompts of up to 301 rows 33 us, now 29;
+// sliding windows at head_dim 256 248, now 210.)
 // TMEM (512 columns): one S of 128, two P of 64, then O (256: two tiles up to head_dim 128,
 // one above).  S is in registers some 200 cycles after it is there, and the next one is computed in its
 // place: with two tiles that of the other tile, so that one tile's softmax runs beside the other's
 // products; with one the next block's.  (S and P in one place for each tile, 2 x 128 columns, let the tiles fall into
-// step, softmax and products in turn: 462 us against NEWTIME for one prompt of 8192 rows.)
+// step, softmax and products in turn: 462 us for one prompt of 8192 rows, now 377.)
 //
 // P is rounded to bf16, as V is: half a step, 2^-8 of a weight, on sums
 // whose result is rounded the same way or averaged over many keys; the sum of weights is
@@ -66,10 +73,10 @@ struct PromptCfg {
     // registers a thread: at launch, and of the softmax warps and of the others while the roles run (one tile leaves enough for all)
     static constexpr int kRegs = NT == 2 ? 168 : 0, kRegsSoftmax = NT == 2 ? 200 : 0, kRegsOthers = 104;
     static_assert(kSoftmaxWarps * 32 * kRegsSoftmax + 128 * kRegsOthers <= kThreads * kRegs || NT == 1, "the roles' registers fit the launch's");
-    static constexpr int kSched = 4;                                // items on their way through the roles
+    static constexpr int kSched = 1;                                // items dealt out and not taken by all roles (two: 4096 rows beside short ones 138 us, not 128)
     static constexpr int kOdd = 64;                                 // items to run again, at most before they are
     static constexpr int kBars = 2 * NST + 3 + 2 + 4 + 2 + 2 + 2 * kSched + 1;
-    static constexpr size_t kSmem = 1024 + (size_t)NT * kQTile + (size_t)NST * kStage + 16 + kBars * 8 + (kSched + kOdd) * 4 + 64;
+    static constexpr size_t kSmem = 1024 + (size_t)NT * kQTile + (size_t)NST * kStage + 16 + kSched * 80 + kBars * 8 + kOdd * 8 + 64;
     static constexpr unsigned kColP = 128, kColO = 256;             // S at 0; two slots of P; O of tile t at kColO + t * DP
     static_assert(kSmem <= 232448, "exceeds the per-CTA shared memory limit");
 };
@@ -119,17 +126,30 @@ __device__ __forceinline__ void prompt_zero(const PromptParams &p, long long row
     if (p.lse)
         for (int e = t; e < heads; e += threads) p.lse[row * p.Hq + h0 + e] = -CUDART_INF_F;
 }
-// Rows of no segment read zero, rows of two set PKV_ERR_OVERLAP: one warp takes the rows of item id's share.
+// Rows of no segment read zero, rows of two set PKV_ERR_OVERLAP: one warp takes the share of CTA number id.
+// (Eight rows at a look at the table: row by row it held up everything else, 128 prompts of 30 rows took 42 us.)
 __device__ __noinline__ void prompt_coverage(const PromptParams &p, int id, int lane) {
-    for (long long row = id; row < p.total_rows; row += gridDim.x) {
-        int n = 0;
+    const int end = (int)((long long)(id + 1) * p.total_rows / gridDim.x);
+#pragma unroll 1
+    for (int row = (int)((long long)id * p.total_rows / gridDim.x); row < end; row += 8) {
+        int n[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 2
         for (int s = lane; s < p.S; s += 32) {
             const int4 v = p.seq_info[s];
-            n += v.x >= 0 && v.x <= row && row < (long long)v.x + v.y;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) n[i] += v.x >= 0 && v.x <= row + i && (long long)row + i < (long long)v.x + v.y;
         }
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (n == 0) prompt_zero(p, row, 0, p.Hq, lane, 32);
-        if (n > 1 && lane == 0) atomicOr(p.err, PKV_ERR_OVERLAP);
+        unsigned none = 0, two = 0;  // rows of no segment, and of two
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = __reduce_add_sync(0xffffffffu, n[i]);
+            none |= (k == 0) << i;
+            two |= (k > 1) << i;
+        }
+        const unsigned rows = (1u << min(end - row, 8)) - 1u;
+        if ((two & rows) && lane == 0) atomicOr(p.err, PKV_ERR_OVERLAP);
+#pragma unroll 1
+        for (none &= rows; none; none &= none - 1) prompt_zero(p, row + __ffs(none) - 1, 0, p.Hq, lane, 32);
     }
 }
 __device__ __forceinline__ bool not_finite(unsigned bf16_pair) { return (bf16_pair & 0x7f80u) == 0x7f80u || (bf16_pair & 0x7f800000u) == 0x7f800000u; }
@@ -154,44 +174,69 @@ __device__ __noinline__ void prompt_add_key(const PromptParams &p, long long key
     }
 }
 
-// One item: 2 (or 1) x 128 query rows of one (segment, kv head), and the blocks of keys they see.
-template <int NT>
+// One item: 2 (or 1) x 128 query rows of one (segment, kv head), and the blocks of keys they see.  One
+// warp works it out, the others read it in shared memory (as each of them did that, the divisions' code alone was 50 KB).
 struct PromptItem {
-    Segment sg;
-    unsigned fault;
-    int s, h, index;         // segment, kv head, item of the segment
+    int q0, ql;              // the segment's rows
     int token0, tokens;      // tokens of the segment; none: nothing to do
-    int first[NT], last[NT]; // blocks of each tile
+    int first[2], last[2];   // blocks of each tile
     int in_lo, in_hi;        // keys that every row sees
     int b0, b1;              // blocks of the item
-    __device__ __forceinline__ void load(const PromptParams &p, int id) {
-        const int per = max(p.S, 1) * p.Hkv;
-        s = id % per / p.Hkv;
-        h = id % p.Hkv;
-        index = p.items - 1 - id / per;
-        sg = p.S ? load_segment(p.seq_info, s) : Segment{0, 0, 0, 0};
-        fault = p.S ? prompt_fault(p, sg) : 0u;
-        token0 = index * NT * p.tokens;
-        tokens = fault ? 0 : max(0, min(NT * p.tokens, sg.ql - token0));
-        if (tokens == 0) return;
-        int lo, hi, x;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int a = token0 + t * p.tokens, b = min(a + p.tokens, sg.ql) - 1;  // tokens of the tile
-            first[t] = last[t] = 0;
-            if (b >= a) {
-                row_key_bounds(a, sg.ql, p.causal, p.window, 0, lo, x);
-                row_key_bounds(b, sg.ql, p.causal, p.window, 0, x, hi);
-                first[t] = lo / 128;
-                last[t] = (hi + 127) / 128;
-            }
-        }
-        row_key_bounds(token0, sg.ql, p.causal, p.window, 0, lo, in_hi);
-        row_key_bounds(token0 + tokens - 1, sg.ql, p.causal, p.window, 0, in_lo, hi);
-        b0 = lo / 128;
-        b1 = (hi + 127) / 128;
+    int kind, rows_of;       // kNoItem ..; the CTA number whose rows are looked after, or -1
+    int s, place;            // segment (-1: none); item of the segment * Hkv + kv head
+    int h, fault;            // kv head; why the segment is refused
+
+    __device__ __forceinline__ void to(int4 *at) const {
+        at[0] = make_int4(q0, ql, token0, tokens);
+        at[1] = make_int4(first[0], last[0], first[1], last[1]);
+        at[2] = make_int4(in_lo, in_hi, b0, b1);
+        at[3] = make_int4(kind, rows_of, s, place);
+        at[4] = make_int4(h, fault, 0, 0);
+    }
+    __device__ __forceinline__ void from(const int4 *at) {
+        const int4 a = at[0], b = at[1], c = at[2], d = at[3], e = at[4];
+        q0 = a.x; ql = a.y; token0 = a.z; tokens = a.w;
+        first[0] = b.x; last[0] = b.y; first[1] = b.z; last[1] = b.w;
+        in_lo = c.x; in_hi = c.y; b0 = c.z; b1 = c.w;
+        kind = d.x; rows_of = d.y; s = d.z; place = d.w;
+        h = e.x; fault = e.y;
     }
 };
+enum { kNoItem = 0, kItem = 1, kCarefulItem = 2 };
+
+// Items of a segment for a kv head (a refused one has its rows to clear).
+__device__ __forceinline__ int prompt_items(const PromptParams &p, const Segment &o, int tiles) {
+    return prompt_fault(p, o) ? 1 : (o.ql + tiles * p.tokens - 1) / (tiles * p.tokens);
+}
+// Item `index` of segment s, which is sg, for kv head h.
+template <int NT>
+__device__ __forceinline__ void prompt_item(const PromptParams &p, PromptItem &w, const Segment &sg, int s, int index, int h) {
+    w.q0 = sg.q0;
+    w.ql = sg.ql;
+    w.s = s;
+    w.h = h;
+    w.place = index * p.Hkv + h;
+    w.fault = s >= 0 ? prompt_fault(p, sg) : 0u;
+    w.token0 = index * NT * p.tokens;
+    w.tokens = w.fault || s < 0 ? 0 : max(0, min(NT * p.tokens, sg.ql - w.token0));
+    if (w.tokens == 0) return;
+    int lo, hi, x;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int a = w.token0 + t * p.tokens, b = min(a + p.tokens, sg.ql) - 1;  // tokens of the tile
+        w.first[t] = w.last[t] = 0;
+        if (b >= a) {
+            row_key_bounds(a, sg.ql, p.causal, p.window, 0, lo, x);
+            row_key_bounds(b, sg.ql, p.causal, p.window, 0, x, hi);
+            w.first[t] = lo / 128;
+            w.last[t] = (hi + 127) / 128;
+        }
+    }
+    row_key_bounds(w.token0, sg.ql, p.causal, p.window, 0, lo, w.in_hi);
+    row_key_bounds(w.token0 + w.tokens - 1, sg.ql, p.causal, p.window, 0, w.in_lo, hi);
+    w.b0 = lo / 128;
+    w.b1 = (hi + 127) / 128;
+}
 
 // Ask for the item of a CTA that has not started: 16 bytes at `at`, completing on `bar`.
 __device__ __forceinline__ void ask_next(uint4 *at, uint64_t *bar) {
@@ -237,17 +282,18 @@ constexpr int kPromptProbes = 1 << 20;  // of one barrier phase before a wait is
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
     constexpr int DP = C::DP, NT = C::NT, NST = C::NST, SPB = C::SPB, SCHED = C::kSched;
-    constexpr int kWarpMma = C::kSoftmaxWarps, kWarpTma = kWarpMma + 2;  // then the cover warp
-    using Item = PromptItem<NT>;
+    constexpr int kWarpMma = C::kSoftmaxWarps, kWarpTma = kWarpMma + 2;  // then the warp that deals items out
+    using Item = PromptItem;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sQ = smem_raw + (-smem_u32(smem_raw) & 1023u);  // pointer arithmetic keeps the shared address space
     unsigned char *ring = sQ + NT * C::kQTile;
     uint4 *answer = reinterpret_cast<uint4 *>(ring + (size_t)NST * C::kStage);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(answer + 1);
+    int4 *sItem = reinterpret_cast<int4 *>(answer + 1);  // [SCHED] items
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sItem + 5 * SCHED);
     uint64_t *full = bars, *empty = full + NST, *q_full = empty + NST, *q_empty = q_full + 1, *s_free = q_empty + 1, *s_full = s_free + 1;
     uint64_t *p_half = s_full + 2, *p_full = p_half + 2, *pv_done = p_full + 2, *drain = pv_done + 2;  // P of keys 0-63 and 64-127
     uint64_t *sched_full = drain + 2, *sched_empty = sched_full + SCHED, *asked = sched_empty + SCHED;
-    int *sItem = reinterpret_cast<int *>(bars + C::kBars), *sOdd = sItem + SCHED;
+    int2 *sOdd = reinterpret_cast<int2 *>(bars + C::kBars);  // segment's number, item's place in it
     unsigned *tslot = reinterpret_cast<unsigned *>(sOdd + C::kOdd);
     volatile int *sAbort = reinterpret_cast<volatile int *>(tslot + 1), *sCount = sAbort + 1, *sNext = sAbort + 2;  // items to run again; the item after them
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -256,7 +302,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll 1
         for (int i = 0; i < C::kBars; ++i) {
             uint64_t *b = bars + i;
-            // P, and S once it is read: every warp of a tile; an item is released by every warp but the one that copies
+            // P, and S once it is read: every warp of a tile; an item is released by every warp but the one that deals it out
             mbar_init(b, (b >= p_half && b < pv_done) || b == s_free ? 4 : b >= sched_empty && b < asked ? 3 + C::kSoftmaxWarps : 1);
         }
         fence_barrier_init();
@@ -311,9 +357,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             if (w.last[t] > w.first[t])
 #pragma unroll 1
                 for (int c = 0; c < DP / 64; ++c)
-                    tma_load_3d(sQ + t * C::kQTile + c * C::kPart, &p.tmap_q, q_full, c * 64, w.h * p.G, w.sg.q0 + w.token0 + t * p.tokens);
+                    tma_load_3d(sQ + t * C::kQTile + c * C::kPart, &p.tmap_q, q_full, c * 64, w.h * p.G, w.q0 + w.token0 + t * p.tokens);
         ++queries;
-        auto load = [&](const CUtensorMap *map, int block) {
+        // K(b0), K(b0 + 1), V(b0), K(b0 + 2), V(b0 + 1), ..: S is a block ahead
+        const int n = w.b1 - w.b0;
+#pragma unroll 1
+        for (int i = 0; ok && i < 2 * n; ++i) {
+            const bool k = i == 0 || ((i & 1) && i < 2 * n - 1);
+            const int block = w.b0 + (k ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1);
 #pragma unroll 1
             for (int c = 0; ok && c < SPB; ++c) {
                 const int st = stages % NST;
@@ -322,15 +373,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
                 mbar_expect_tx(full + st, C::kStage);
 #pragma unroll
                 for (int x = 0; x < C::kCols / 64; ++x)
-                    tma_load_3d(ring + (size_t)st * C::kStage + x * C::kPart, map, full + st, c * C::kCols + x * 64, w.h, w.sg.q0 + block * C::kKeys);
+                    tma_load_3d(ring + (size_t)st * C::kStage + x * C::kPart, k ? &p.tmap_k : &p.tmap_v, full + st, c * C::kCols + x * 64, w.h, w.q0 + block * C::kKeys);
                 ++stages;
             }
-        };
-        load(&p.tmap_k, w.b0);
-#pragma unroll 1
-        for (int j = w.b0; ok && j < w.b1; ++j) {
-            if (j + 1 < w.b1) load(&p.tmap_k, j + 1);  // (S is a block ahead)
-            load(&p.tmap_v, j);
         }
     };
     // The products: one warp has S, one P V (one lane of each issues).  A look at an mbarrier takes 110 cycles even if
@@ -436,14 +481,14 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         }
     };
     // The rows of one item (a softmax warp).
-    auto rows_of_item = [&](const Item &w, int id, bool careful) {
+    auto rows_of_item = [&](const Item &w, bool careful) {
         const int t = warp >> 2, r = tid & 127;  // tile, row of it
         const unsigned lane_off = (unsigned)(32 * (warp & 3)) << 16;
         const int token = w.token0 + t * p.tokens + r / p.G, begin = stages;
-        const bool real = r < p.tokens * p.G && token < w.sg.ql;
+        const bool real = r < p.tokens * p.G && token < w.ql;
         stages += 2 * SPB * (w.b1 - w.b0);
         int lo_r = 0, hi_r = 0;
-        if (real) row_key_bounds(token, w.sg.ql, p.causal, p.window, 0, lo_r, hi_r);
+        if (real) row_key_bounds(token, w.ql, p.causal, p.window, 0, lo_r, hi_r);
         const float sc = p.scale_log2;
         float m = kNoScore, l = 0.f;
         // (no index of a run-time value: the item would live in local memory, 500 cycles a look where the products' warp asks between two of them)
@@ -584,7 +629,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         const int slot = NT == 2 ? t : (e - 1 - w.b0) & 1;
         if (ok) ok = wait_bar(pv_done + slot, (phase >> slot & 1) ^ 1);
         tc_fence_after();
-        const long long row = (long long)w.sg.q0 + (real ? token : 0);
+        const long long row = (long long)w.q0 + (real ? token : 0);
         const int hq = w.h * p.G + (real ? r % p.G : 0);
         const bool zero = !ok || l == 0.f;
         const float inv = zero ? 0.f : 1.f / l;
@@ -606,7 +651,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll 1
                 for (int key = lo_r; key < hi_r; ++key) {
                     if (key >= w.in_lo && key < w.in_hi) key = w.in_hi;  // (those every row sees were not touched)
-                    if (key < hi_r) prompt_add_key(p, (long long)w.sg.q0 + key, row, w.h, hq, c0, m, y);
+                    if (key < hi_r) prompt_add_key(p, (long long)w.q0 + key, row, w.h, hq, c0, m, y);
                 }
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = y[k];
@@ -651,7 +696,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         // (a row with a NaN sum has one among its own scores)
         if (!careful && ok && __any_sync(0xffffffffu, odd && l == l) && lane == 0) {
             const int n = atomicAdd(const_cast<int *>(sCount), 1);
-            sOdd[n % C::kOdd] = id;  // (never that many: see below)
+            sOdd[n % C::kOdd] = make_int2(w.s, w.place);  // (never that many: see below)
         }
         __syncwarp();
         tc_fence_before();
@@ -672,124 +717,193 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             }
         return true;
     };
-    // The next item of a role but the copies', or -1 (a whole warp).
-    auto take = [&]() -> int {
+    // The next item of a role, into w (a whole warp); false where there is none.
+    Item w;
+    auto take = [&](bool) -> bool {
         const int i = nth++ % SCHED;
         const bool got = __all_sync(0xffffffffu, wait_long(sched_full + i, ((nth - 1) / SCHED) & 1));
-        const int id = got ? sItem[i] : -1;
+        w.from(sItem + 5 * i);
         __syncwarp();
         if (got && lane == 0) mbar_arrive(sched_empty + i);
         ok = ok && got;
-        return id;
+        return got && w.kind != kNoItem;
     };
-    // A role's items: those of the scheduler (`next`), then, where all roles have come to the end of
-    // it, those of the list, and so on until none is left.
-    Item w;
+    // A role's items: those of the grid, then, where all roles have come to the end of
+    // them, those of the list, and so on until none is left.
     auto all_items = [&](auto &&next, auto &&run) {
         bool careful = false;
-        int i = 0, n = 0;
 #pragma unroll 1
         for (;;) {
-            int id = -1;
-            if (!careful) {
-                id = next();
-            } else {
-#pragma unroll 1
-                for (bool twice = true; twice && i < n; ++i) {  // (each warp of an item may have put it there)
-                    id = sOdd[i];
-                    twice = false;
-                    for (int k = 0; k < i; ++k) twice |= sOdd[k] == id;
-                    if (twice) id = -1;
-                }
-                if (*sAbort) id = -1;
-            }
-            if (id >= 0) {
-                run(id, careful);
+            if (next(careful)) {
+                run();
                 __syncwarp();
                 continue;
             }
             __syncthreads();
-            if (!careful) {
-                n = min(*sCount, C::kOdd);
-                i = 0;
-                careful = true;
-                if (n > 0) continue;
-                __syncthreads();
-            }
+            careful = !careful && *sCount > 0;
+            if (careful) continue;
             const bool done = *sNext < 0 || *sAbort;
+            __syncthreads();
             if (tid == 0) *sCount = 0;
             __syncthreads();
             if (done) return;
-            careful = false;
         }
     };
     if (warp < C::kSoftmaxWarps) {
         if constexpr (C::kRegsSoftmax > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kRegsSoftmax));
-        all_items(take, [&](int id, bool careful) {
-            w.load(p, id);
-            if (w.tokens > 0) rows_of_item(w, id, careful);
+        all_items(take, [&]() {
+            if (w.tokens > 0) rows_of_item(w, w.kind == kCarefulItem);
         });
     } else {
         if constexpr (C::kRegsSoftmax > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kRegsOthers));
         if (warp < kWarpTma) {
-            all_items(take, [&](int id, bool) {
-                w.load(p, id);
-                if (w.tokens == 0) return;
-                if (warp == kWarpMma) scores_of_item(w);
-                else sums_of_item(w);
-            });
-        } else if (warp == kWarpTma) {
-            // The first lane copies, and asks for the item after the one it copies; the answer is there when the copies are on their way.
-            int id = blockIdx.x;
-            bool asking = false;
-            all_items([&]() -> int {
-                int now = -1;
-                if (lane == 0) {
-                    if (asking) {  // the item after the last one
-                        id = -1;
-                        if (wait_long(asked, answers & 1)) id = next_of(answer);
-                        else ok = false;
-                        ++answers;
-                        asking = false;
-                    }
-                    const int i = nth % SCHED;
-                    if (nth >= SCHED) ok = wait_long(sched_empty + i, ((nth / SCHED) - 1) & 1) && ok;
-                    const bool rest = ok && *sCount >= kListRoom;
-                    *sNext = id;
-                    if (!rest) now = id;
-                    sItem[i] = now;
-                    mbar_arrive(sched_full + i);
-                    ++nth;
-                    if (now >= 0) {
-                        if (ok && !*sAbort) {  // (after a timeout the others still write this item's zeros)
-                            fence_proxy_async();  // the answer before has been read
-                            mbar_expect_tx(asked, 16);
-                            ask_next(answer, asked);
-                            asking = true;
-                        } else {
-                            id = -1;
-                        }
-                    }
+            all_items(take, [&]() {
+                if (w.tokens > 0) {
+                    if (warp == kWarpMma) scores_of_item(w);
+                    else sums_of_item(w);
                 }
-                return __shfl_sync(0xffffffffu, now, 0);
-            }, [&](int item, bool) {
-                if (lane == 0) {
-                    w.load(p, item);
-                    if (w.tokens > 0 && ok) copy_item(w);
-                }
-            });
-        } else {
-            all_items(take, [&](int id, bool careful) {
-                if (careful) return;
-                w.load(p, id);
-                prompt_coverage(p, id, lane);
-                if (w.fault && w.index == 0) {  // (one warp writes its rows)
+                if (warp == kWarpMma) return;
+                if (w.rows_of >= 0) prompt_coverage(p, w.rows_of, lane);
+                if (w.fault && w.place < p.Hkv) {  // (one warp writes its rows)
                     if (lane == 0) atomicOr(p.err, w.fault);
-                    if (w.sg.q0 >= 0)           // a negative q_start covers nothing
-                        for (long long r = w.sg.q0; r < min((long long)w.sg.q0 + w.sg.ql, (long long)p.total_rows); ++r)
+                    if (w.q0 >= 0)           // a negative q_start covers nothing
+                        for (long long r = w.q0; r < min((long long)w.q0 + w.ql, (long long)p.total_rows); ++r)
                             prompt_zero(p, r, w.h * p.G, p.G, lane, 32);
                 }
             });
+        } else if (warp == kWarpTma) {
+            all_items(take, [&]() {
+                if (lane == 0 && w.tokens > 0 && ok) copy_item(w);
+            });
+        } else {
+            int id = blockIdx.x;
+            bool asking = false, held = true, cover = true;  // an answer is to come; the item is still to be given out; its number's rows too
+            long long unit = id / p.Hkv, units = -1;         // the item's place among those of a kv head; how many there are
+            // ---- units to items: lane i has segment s0 + i of the table and its n items; those of 32 segments come the last ones first
+            int s0 = 0, n = 0, all = 0, top = 0, passed = 0;  // items of the 32; the item of each segment looked at, and those of the 32 before it
+            long long before = 0;                             // items before s0
+            bool loaded = false;
+            Segment o{0, 0, 0, 0};
+            auto seek = [&](Segment &g, int &index) -> int {  // the segment of `unit`, or -1
+                if (unit < before + passed) {
+                    if (unit < before) {
+                        s0 = 0;
+                        before = 0;
+                    }
+                    loaded = false;
+                }
+#pragma unroll 1
+                for (;;) {
+                    if (!loaded) {
+                        o = s0 + lane < p.S ? load_segment(p.seq_info, s0 + lane) : Segment{0, 0, 0, 0};
+                        n = s0 + lane < p.S ? prompt_items(p, o, NT) : 0;
+                        all = __reduce_add_sync(0xffffffffu, n);
+                        top = __reduce_max_sync(0xffffffffu, n) - 1;
+                        passed = 0;
+                        loaded = true;
+                    }
+                    if (unit < before + all) break;
+                    if (s0 + 32 >= p.S) return -1;
+                    before += all;
+                    s0 += 32;
+                    loaded = false;
+                }
+                const int at = (int)(unit - before);
+                unsigned m;
+#pragma unroll 1
+                for (;;) {
+                    m = __ballot_sync(0xffffffffu, n > top);
+                    const int c = __popc(m);
+                    if (at - passed < c) break;
+                    // as many of a segment's items as the same segments have
+                    const int down = min((at - passed) / c, top + 1 - __reduce_max_sync(0xffffffffu, n > top ? 0 : n));
+                    passed += down * c;
+                    top -= down;
+                }
+                for (int l = at - passed; l; --l) m &= m - 1;
+                const int l = __ffs(m) - 1;  // the one of them
+                g.q0 = __shfl_sync(0xffffffffu, o.q0, l);
+                g.ql = __shfl_sync(0xffffffffu, o.ql, l);
+                g.kend = __shfl_sync(0xffffffffu, o.kend, l);
+                index = top;
+                return s0 + l;
+            };
+            int done = 0;  // of the list
+            all_items([&](bool careful) -> bool {
+                Segment g{0, 0, 0, 0};
+                int s = -1, index = 0, h = 0;
+                bool now = false;
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (careful) {
+                    const int listed = min(*sCount, C::kOdd);
+                    int2 e = make_int2(0, 0);
+#pragma unroll 1
+                    for (; !now && done < listed; ++done) {  // (each warp of an item may have put it there)
+                        e = sOdd[done];
+                        now = true;
+#pragma unroll 1
+                        for (int k = 0; k < done; ++k) now = now && !(sOdd[k].x == e.x && sOdd[k].y == e.y);
+                    }
+                    now = __shfl_sync(0xffffffffu, now && !*sAbort, 0);
+                    if (now) {
+                        s = e.x;
+                        g = load_segment(p.seq_info, s);
+                        index = e.y / p.Hkv;
+                        h = e.y % p.Hkv;
+                    }
+                } else {
+                    done = 0;
+                    if (!held) {
+                        if (units < 0) {  // (asked while the first item is on its way)
+                            units = 0;
+#pragma unroll 4
+                            for (int i = lane; i < p.S; i += 32) units += prompt_items(p, load_segment(p.seq_info, i), NT);
+#pragma unroll
+                            for (int d = 16; d; d >>= 1) units += __shfl_xor_sync(0xffffffffu, units, d);
+                        }
+                        cover = id < 0 || unit + p.units >= units;
+                        if (!cover) {  // segments that overlap may have more items than the grid
+                            unit += p.units;
+                        } else {
+                            id = -1;
+                            if (lane == 0 && asking) {  // the item after the last one
+                                if (wait_long(asked, answers & 1)) id = next_of(answer);
+                                else ok = false;
+                                ++answers;
+                            }
+                            asking = false;
+                            id = __shfl_sync(0xffffffffu, id, 0);
+                            unit = id / p.Hkv;
+                        }
+                    }
+                    held = id >= 0 && __shfl_sync(0xffffffffu, *sCount, 0) >= kListRoom;  // the list is run first
+                    now = id >= 0 && !held;
+                    if (now) {
+                        h = id % p.Hkv;
+                        s = seek(g, index);
+                    }
+                }
+                prompt_item<NT>(p, w, g, s, index, h);
+                w.kind = !now ? kNoItem : careful ? kCarefulItem : kItem;
+                w.rows_of = now && !careful && cover ? id : -1;
+                const int i = nth % SCHED;
+                if (lane == 0) {
+                    if (nth >= SCHED) ok = wait_long(sched_empty + i, ((nth / SCHED) - 1) & 1) && ok;
+                    if (!careful) *sNext = id;
+                    w.to(sItem + 5 * i);
+                    mbar_arrive(sched_full + i);
+                }
+                ++nth;
+                if (now && !careful && !asking) {  // for the item after this one: the answer is there when this one is on its way
+                    asking = __shfl_sync(0xffffffffu, ok && !*sAbort, 0);  // (after a timeout the others still write this item's zeros)
+                    if (asking && lane == 0) {
+                        fence_proxy_async();  // the answer before has been read
+                        mbar_expect_tx(asked, 16);
+                        ask_next(answer, asked);
+                    }
+                }
+                return now;
+            }, [&]() {});
         }
     }
     if (*sAbort) {

@@ -17,7 +17,7 @@ struct PromptParams {
     unsigned *err;
     int Hq, Hkv, G, D, total_rows, S, max_len;
     int tokens;                   // of a tile of 128 query rows: 128 / G
-    int items;                    // tile groups of the longest segment
+    int units;                    // of a kv head, in the grid: tile groups of all segments, at most
     int causal, window, out_bf16;
     float scale_log2;             // softmax scale * log2(e), positive
 };

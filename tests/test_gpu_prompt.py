@@ -173,6 +173,41 @@ def test_uncovered_overlapping_and_no_segments(pkv):
     assert err == 0 and bool((out == 0).all()) and bool(torch.isinf(lse).all())
 
 
+@pytest.mark.parametrize("D,hq,hkv", [(64, 4, 2), (128, 8, 1), (256, 6, 2)])
+@pytest.mark.parametrize("S", [31, 33, 100])
+def test_long_tables(pkv, D, hq, hkv, S):
+    """Prompts of all lengths side by side and in any order, empty and refused ones between them, rows of none at the end."""
+    g = torch.Generator().manual_seed(S)
+    lens = [int(x) for x in torch.randint(0, 60, (S,), generator=g)]
+    lens[S // 2], lens[S - 1], lens[0] = 700, 301, 0
+    si, rows = table(lens, gap=1)
+    rows += 40
+    si = si[torch.randperm(S, generator=g)]
+    bad = int((si[:, 1] == 301).nonzero()[0, 0])
+    q, k, v = make(5, rows, hq, hkv, D)
+    out, lse, err = run(pkv, q, k, v, si, max_len=5000)
+    assert err == 0
+    check(out, lse, q, k, v, si)
+    si[bad, 3] -= 1
+    good = torch.cat([si[:bad], si[bad + 1:]])
+    a, b, err = run(pkv, q, k, v, si, max_len=5000)
+    live = torch.zeros(rows, dtype=torch.bool)
+    for q0, n, _, _ in good.tolist():
+        live[q0:q0 + n] = True
+    assert err == 1 and torch.equal(a[live], out[live]) and torch.equal(b[live], lse[live])
+    assert bool((a[~live] == 0).all()) and bool(torch.isinf(b[~live]).all())
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(128, 8, 2), (256, 4, 1)])
+def test_the_same_rows_in_many_segments(pkv, D, hq, hkv):
+    """An error, but every row of every segment is computed all the same."""
+    q, k, v = make(6, 640, hq, hkv, D)
+    si = torch.tensor([[0, 640, 0, 640]], dtype=torch.int32)
+    one = run(pkv, q, k, v, si)
+    many = run(pkv, q, k, v, torch.cat([si] * 40 + [torch.tensor([[0, 0, 0, 0]], dtype=torch.int32)] * 3))
+    assert many[2] == 32 and torch.equal(one[0], many[0]) and torch.equal(one[1], many[1])
+
+
 @pytest.mark.parametrize("seg,bit", [((50, 10, 0, 11), 1), ((50, 10, 0, 9), 1), ((-1, 20, 0, 20), 1), ((90, 20, 0, 20), 1), ((50, -3, 0, -3), 1),
                                      ((2 ** 31 - 5, 10, 0, 10), 1), ((50, 45, 0, 45), 16)])
 @pytest.mark.parametrize("D", [128, 256])
