@@ -376,8 +376,8 @@ int pkv_norm_rope_append(const pkv_cache *cache, int32_t layer, const pkv_rope *
  * PKV_FLAG_OUT_BF16.  Scores are those of the stored values to fp32; the
  * softmax weights are rounded to fp16 for the product with V (each by at most
  * 2^-11 of itself or 2^-32 of its row's largest, whichever is more; with PKV_FP8
- * that is said of a weight times its page's V scale, and sums of such products above
- * 2^100 may overflow).  A NaN in V
+ * that is said of a weight times its page's V scale, with 2^-31, and sums of such
+ * products above 2^100 may overflow).  A NaN in V
  * reaches only the rows that see its key.  Without a workspace the splits form
  * a cluster (num_splits 0..16); large launches are faster with one (see
  * pkv_attend_workspace_bytes).  PKV_FLAG_SIMT, PKV_FLAG_MMA_SYNC and
@@ -414,7 +414,8 @@ int pkv_attend_varlen(const pkv_cache *cache, int32_t layer,
  * max_len bounds every segment's q_len (PKV_ERR_QLEN) and sizes the launch.  Which
  * keys a row sees, out, lse, uncovered rows, refused segments and overlaps
  * (PKV_ERR_OVERLAP) are as in pkv_attend_varlen, without padding.  softmax_scale is
- * positive and finite; head_dim a multiple of 8, at most 256; q_heads / kv_heads at most 128.
+ * positive and finite (times log2 e, too); head_dim a multiple of 8, at most 256; q_heads / kv_heads at most 128.  PKV_EINVAL also
+ * where num_segments prompts of min(max_len, total_rows) rows would be more than 2^31 tiles.
  *
  * Scores are fp32 sums of exact products; softmax weights are rounded to bf16 (each
  * by at most 2^-8 of itself) for the product with V, whose sums are fp32.  A NaN or
@@ -469,7 +470,7 @@ int pkv_append_attend(const pkv_cache *cache, int32_t layer,
  * sequence and twice that for several; with more rows from fewer).
  * Given a workspace, they run as one wave of CTAs with equal shares of all
  * key ranges and a second launch that merges the shared ones, instead of as a
- * cluster per range; with PKV_FP4 more than 32 rows per kv head at head_dim 128 then take
+ * cluster per range; more than 32 rows per kv head at head_dim 128 then take
  * the tcgen05 tile.  The size does not grow with the lengths and is below 25 MB.
  * It need not be zeroed, and may be shared by calls that
  * follow one another on one stream.  A call with a window counts

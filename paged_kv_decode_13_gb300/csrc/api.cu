@@ -509,7 +509,7 @@ double split4(Attend4Kernel *k4, int dtype, int head_dim, int rows, long long un
 // The batch of 32 uneven sequences (8 rows, head_dim 128) takes 77, 63, 58 us with
 // 0, 12, 24 pages; uneven 16-row tiles of head_dim 256 (16 sequences up to 4096 keys) took 67 us
 // with 12 and 43 with 50, the tcgen05 kernel's drafts of 16 sequences 82, 72, 73 us with 10, 36, 24
-// (69 now).
+// (65 now).
 int piece_pages4(const Attend4Kernel &k, int block) {
     return k.rows == 128 ? 36 : k.rows == 8 ? (56 << 10) / (2 * block) : kPieceTile;
 }
@@ -1060,7 +1060,7 @@ int pkv_attend_prompt(int32_t head_dim, int32_t kv_heads, const pkv_rows *r, con
     if (!r || r->total_rows < 0 || kv_heads <= 0 || r->q_heads <= 0 || r->q_heads % kv_heads != 0) return PKV_EINVAL;
     if (r->q_heads / kv_heads > 128) return PKV_EUNSUPPORTED;  // a token's heads fill more than a tile
     if (r->q_out || r->k_out || r->v_out || r->positions || (flags & ~(PKV_FLAG_OUT_BF16 | PKV_FLAG_PDL))) return PKV_EINVAL;
-    if (S < 0 || S > 65535 || max_len <= 0 || window < 0 || (causal != 0 && causal != 1) || !(scale > 0.f) || !isfinite(scale)) return PKV_EINVAL;
+    if (S < 0 || S > 65535 || max_len <= 0 || window < 0 || (causal != 0 && causal != 1) || !(scale > 0.f) || !isfinite(scale * 1.4426950408889634f)) return PKV_EINVAL;
     const long long nq = (long long)r->q_heads * head_dim, nk = (long long)kv_heads * head_dim;
     if (!err || !out || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return PKV_EINVAL;
     if (S > 0 && (!seq_info || !aligned16(seq_info))) return PKV_EINVAL;
@@ -1071,10 +1071,10 @@ int pkv_attend_prompt(int32_t head_dim, int32_t kv_heads, const pkv_rows *r, con
     p.G = r->q_heads / kv_heads;
     p.tokens = 128 / p.G;
     const int group = k.tiles * p.tokens;  // tokens of a CTA
-    // tile groups that segments without a row in common can have: each has one that its rows do not fill
+    // tile groups that segments without a row in common can have: each that has rows has one that they do not fill
     const long long each = ((long long)std::min(max_len, r->total_rows) + group - 1) / group;
-    const long long units = std::max(std::min(each * S, (long long)r->total_rows / group + S), 1ll), ctas = units * kv_heads;
-    if (ctas > INT32_MAX || each * kv_heads > INT32_MAX) return PKV_EINVAL;
+    const long long units = std::max(std::min(each * S, (long long)r->total_rows / group + std::min(S, r->total_rows)), 1ll), ctas = units * kv_heads;
+    if (ctas > INT32_MAX || each * std::max(S, 1) * kv_heads > INT32_MAX) return PKV_EINVAL;  // (segments that overlap may ask for the second)
     p.units = (int)units;
     auto fn = encode_fn();
     if (!fn) return PKV_ECUDA;

@@ -1,28 +1,29 @@
-// Split-K attention over a 4-bit paged cache (sm_103a).
+// Split-K attention over a paged cache held in 4 or 8 bits (sm_103a).
 //
 // The segment-table attention of the bf16 kernels (same segments, windows,
-// rings, left padding, errors) over PKV_FP4 pages.  Grid (C, kv_heads x row
+// rings, left padding, errors) over PKV_FP4 and PKV_FP8 pages.  Grid (C, kv_heads x row
 // tiles, segments), the C CTAs along x one thread-block cluster that shares a
 // key range.  A CTA holds 8 * NT query rows of one kv head's group; its KW warps
 // take every KW-th page of the CTA's range, each with its own ring of NST
 // stages: a page block of one kv head is contiguous, so a stage is two bulk
-// copies (9 D bytes of K, 9 D of V) on one mbarrier.
+// copies (9 D or 16 D + 16 bytes of K, as many of V) on one mbarrier.
 //
 //   S^T (16 tokens x 8 rows) = K (16 x D) . Q^T
 //   O^T (D x 8 rows)        += V^T (D x 16 tokens) . P^T
 //
-// with fp16 mma.sync and fp32 accumulation.  K and V values are exact in fp16
-// (fp4.cuh), and a bf16 query row, scaled by the power of two that brings its
+// with fp16 mma.sync and fp32 accumulation.  K and V values (of 8 bits: the codes without their
+// page's scale, which goes into the scores, and into the weights of the product with V) are exact in fp16
+// (fp4.cuh, fp8.cuh), and a bf16 query row, scaled by the power of two that brings its
 // largest value to [2^14, 2^15), is exact in fp16 down to 2^-31 of that value, so the
 // scores are those of the stored values to fp32.  P is rounded to fp16: by
 // at most 2^-11 of itself (an eighth of the rounding of a bf16 output), or, where it is
 // below 2^-21 of its row's largest weight, by at most 2^-32 of that.
 //
-// The lanes read codes in fragment order (fp4.cuh), so a page costs four 16-byte
+// The lanes read codes in fragment order, so a page of 4 bits costs four 16-byte
 // and a few narrow shared loads a lane, a conversion (two values) and one fp16
 // multiply by the scale for each fragment register, and no shuffles.
 //
-// A page of one kv head (2,304 bytes at D = 128) costs a warp about 300 issue slots, a
+// A 4-bit page of one kv head (2,304 bytes at D = 128) costs a warp about 300 issue slots, a
 // quarter of them conversions (two a value pair at half rate), so four
 // or five warps an SM sub-partition are needed to keep up with HBM: CTAs of four
 // warps, four an SM for 8 rows.  Sequences of equal length stream at 0.8 to
@@ -32,7 +33,8 @@
 // head_dim 128: 300 keys 6.4 us, 8192 keys 9.1 us (the launch, the
 // merge), 32 sequences of up to 16384 keys 58 us (37 at the rate of a copy; HBM 57 %
 // busy: starts and ends of 1,000 pieces); head_dim 256, 4 x 131072 keys 107
-// us (89; HBM 73 %).  More splits, one large CTA an SM, sixteen warps and
+// us (89; HBM 73 %).  8 bits: 300 keys 6.3 us, the 32 sequences 111 (93 at the rate of a
+// copy), the four long ones 166 (159).  More splits, one large CTA an SM, sixteen warps and
 // integer unpacking (2.2 times the conversion's time) were slower.
 //
 // Two ways to cut the work.  attend4_kernel: a cluster a range, its size by the

@@ -23,6 +23,8 @@ static Attend4Kernel info4(int page_ns, int full) {
 #define PICK4_NAME2(B, D) pick##B##_##D
 #define PICK4_NAME(B, D) PICK4_NAME2(B, D)
 
+// (page times of the 8-bit kernels: those of 4 bits choose as well at head_dim 64 and 128, over 336 shapes; their own ones
+// at 256, 173 and more measured, are up to a quarter better there: 16 uneven sequences up to 8192 keys 69 -> 56 us.)
 Attend4Kernel PICK4_NAME(PKV_INST_BITS, PKV_INST_D)(int rows, bool few) {
 #if PKV_INST_BITS == 8
 #if PKV_INST_D == 64
@@ -36,9 +38,9 @@ Attend4Kernel PICK4_NAME(PKV_INST_BITS, PKV_INST_D)(int rows, bool few) {
     if (rows <= 16) return info4<Cfg4<128, 2, 8, 4, 1, 1, true, 8>>(100, 20);
     return info4<Cfg4<128, 4, 4, 4, 1, 2, true, 8>>(228, 27);
 #else
-    if (rows <= 8 && few) return info4<Cfg4<256, 1, 8, 3, 1, 1, true, 8>>(110, 20);
-    if (rows <= 8) return info4<Cfg4<256, 1, 4, 2, 1, 2, true, 8>>(180, 33);
-    return info4<Cfg4<256, 2, 8, 2, 1, 1, true, 8>>(153, 20);
+    if (rows <= 8 && few) return info4<Cfg4<256, 1, 8, 3, 1, 1, true, 8>>(165, 20);
+    if (rows <= 8) return info4<Cfg4<256, 1, 4, 2, 1, 2, true, 8>>(185, 36);
+    return info4<Cfg4<256, 2, 8, 2, 1, 1, true, 8>>(162, 20);
 #endif
 #elif PKV_INST_D == 64
     if (rows <= 8 && few) return info4<Cfg4<64, 1, 8, 2, 2, 2, false>>(46, 20);

@@ -29,9 +29,9 @@
 //               or leave them for the merge;
 //   warp 17     O_h += P_h(j) V_j (A from TMEM, K-major V^T, N 128).
 //
-// 16 sequences of up to 8192 keys, 8 kv heads, up to 128 rows each: 69 us with
-// the merge (65 the kernel), where the bytes take 12 us, the products (of full tiles) at the
-// measured bf16 rate 19, and the mma.sync tiles 179.  The tensor cores are 22 %
+// 16 sequences of up to 8192 keys, 8 kv heads, up to 128 rows each: 65 us with
+// the merge, where the bytes take 12 us, the products (of full tiles) at the
+// measured bf16 rate 19, and the mma.sync tiles 179; in 8 bits 86, the bytes 22.  The tensor cores are 22 %
 // busy, the schedulers 46 %: the softmax warps' 930 issue slots a group of 64
 // keys and sub-partition (convert, maximum, exp2, pack, rescale) are the
 // longest chain.  Registers 128 / 72 (136 / 64 and 144 / 64: the same time), and a
