@@ -30,12 +30,12 @@
 // Where items are short a role's code is cold each time, some ten cycles an instruction: the kernel has to
 // stay small (88 KB), what an item needs is worked out once, and the steps are spread over warps that
 // wait anyway.  (Every role working items out for itself, 120 KB: 16 prompts of up to 301 rows 33 us, now 29;
-// sliding windows at head_dim 256 248, now 210.)
+// sliding windows at head_dim 256 248, then 209.)
 // TMEM (512 columns): one S of 128, two P of 64, then O (256: two tiles up to head_dim 128,
 // one above).  S is in registers some 200 cycles after it is there, and the next one is computed in its
 // place: with two tiles that of the other tile, so that one tile's softmax runs beside the other's
 // products; with one the next block's.  (S and P in one place for each tile, 2 x 128 columns, let the tiles fall into
-// step, softmax and products in turn: 462 us for one prompt of 8192 rows, now 377.)
+// step, softmax and products in turn: 462 us for one prompt of 8192 rows, now 375.)
 //
 // P is rounded to bf16, as V is: half a step, 2^-8 of a weight, on sums
 // whose result is rounded the same way or averaged over many keys; the sum of weights is
@@ -277,6 +277,13 @@ __device__ __forceinline__ void tmem_st16_async(unsigned taddr, const unsigned (
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
+// Whether the phase is over; does not wait.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, unsigned parity) {
+    unsigned done;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return done;
+}
+
 constexpr int kPromptProbes = 1 << 20;  // of one barrier phase before a wait is given up (a probe sleeps for a while)
 
 template <class C>
@@ -344,20 +351,22 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
     bool ok = true;
     unsigned answers = 0;
 
-    // The copies of one item (one thread).
+    // The copies of one item (a whole warp: lane c has stage c of every block; one thread for all of them takes 450 cycles a stage).
     auto copy_item = [&](const Item &w) {
-        if (queries > 0) ok = ok && wait_one(q_empty, (queries - 1) & 1);
+        if (queries > 0) ok = ok && wait_bar(q_empty, (queries - 1) & 1);
         if (!ok) return;
-        unsigned bytes = 0;
+        if (lane == 0) {
+            unsigned bytes = 0;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) bytes += w.last[t] > w.first[t] ? DP / 64 * p.tokens * p.G * 128 : 0;
-        mbar_expect_tx(q_full, bytes);
+            for (int t = 0; t < NT; ++t) bytes += w.last[t] > w.first[t] ? DP / 64 * p.tokens * p.G * 128 : 0;
+            mbar_expect_tx(q_full, bytes);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-            if (w.last[t] > w.first[t])
+            for (int t = 0; t < NT; ++t)
+                if (w.last[t] > w.first[t])
 #pragma unroll 1
-                for (int c = 0; c < DP / 64; ++c)
-                    tma_load_3d(sQ + t * C::kQTile + c * C::kPart, &p.tmap_q, q_full, c * 64, w.h * p.G, w.q0 + w.token0 + t * p.tokens);
+                    for (int c = 0; c < DP / 64; ++c)
+                        tma_load_3d(sQ + t * C::kQTile + c * C::kPart, &p.tmap_q, q_full, c * 64, w.h * p.G, w.q0 + w.token0 + t * p.tokens);
+        }
         ++queries;
         // K(b0), K(b0 + 1), V(b0), K(b0 + 2), V(b0 + 1), ..: S is a block ahead
         const int n = w.b1 - w.b0;
@@ -365,17 +374,27 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         for (int i = 0; ok && i < 2 * n; ++i) {
             const bool k = i == 0 || ((i & 1) && i < 2 * n - 1);
             const int block = w.b0 + (k ? (i + 1) / 2 : i == 2 * n - 1 ? n - 1 : i / 2 - 1);
+            const int mine = stages + lane, st = mine % NST;
+            bool todo = lane < SPB;
+            int left = 64 * kPromptProbes;
 #pragma unroll 1
-            for (int c = 0; ok && c < SPB; ++c) {
-                const int st = stages % NST;
-                if (stages >= NST) ok = wait_one(empty + st, ((stages / NST) - 1) & 1);
-                if (!ok) break;
-                mbar_expect_tx(full + st, C::kStage);
+            for (; __any_sync(0xffffffffu, todo); --left) {
+                if (todo && (mine < NST || mbar_test_wait(empty + st, ((mine / NST) - 1) & 1))) {
+                    todo = false;
+                    mbar_expect_tx(full + st, C::kStage);
+                    unsigned char *to = ring + (size_t)st * C::kStage;
 #pragma unroll
-                for (int x = 0; x < C::kCols / 64; ++x)
-                    tma_load_3d(ring + (size_t)st * C::kStage + x * C::kPart, k ? &p.tmap_k : &p.tmap_v, full + st, c * C::kCols + x * 64, w.h, w.q0 + block * C::kKeys);
-                ++stages;
+                    for (int x = 0; x < C::kCols / 64; ++x)
+                        tma_load_3d(to + x * C::kPart, k ? &p.tmap_k : &p.tmap_v, full + st, lane * C::kCols + x * 64, w.h, w.q0 + block * C::kKeys);
+                }
+                if (left == 0 || *sAbort) {
+                    *sAbort = 1;
+                    ok = false;
+                    break;
+                }
             }
+            ok = __all_sync(0xffffffffu, ok);
+            stages += SPB;  // (some of them copied, where a wait ran out)
         }
     };
     // The products: one warp has S, one P V (one lane of each issues).  A look at an mbarrier takes 110 cycles even if
@@ -395,46 +414,49 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             }
         }
     };
-    auto block_ready = [&](const unsigned (&at)[SPB], const unsigned (&ph)[SPB]) {
-        bool r = true;
-#pragma unroll
-        for (int c = 0; c < SPB; ++c) r = r && wait_bar(full + at[c], ph[c]);
-        return r;
-    };
-    auto release = [&](const unsigned (&at)[SPB]) {  // once what has been issued so far is done
-#pragma unroll
-        for (int c = 0; c < SPB; ++c) umma_commit_by(lead, empty + at[c]);
-    };
-    // S of tile t and the block in stages `at`; what was there has been read
-    auto issue_s = [&](int t, const unsigned (&at)[SPB]) {
+    auto block_ready = [&](const unsigned (&at)[SPB], const unsigned (&ph)[SPB]) { return wait_bar(full + at[0], ph[0]); };
+    auto release = [&](const unsigned (&at)[SPB]) { umma_commit_by(lead, empty + at[0]); };  // once what has been issued so far is done
+    // S of tile t and the block in stages `at`; what was there has been read.  (Above head_dim 128 a block is two stages, and
+    // the ring holds two blocks and a half: each, of K and of V, is waited for and given back by itself, so that the next one is on its
+    // way while the other half is used; both at once: 209 us of sliding windows at head_dim 256, now 198.  Four stages of
+    // 16 KB a block: 224 to 247, more waits, commits and copies than their earlier starts are worth.)
+    auto issue_s = [&](int t, const unsigned (&at)[SPB], const unsigned (&ph)[SPB]) {
         const unsigned q_lo = UmmaDesc(smem_u32(sQ), 16).lo + t * (C::kQTile >> 4), k_lo = UmmaDesc(smem_u32(ring), 16).lo;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < SPB; ++c) {
+            if (SPB > 1) {
+                if (!wait_bar(full + at[c], ph[c])) return false;
+                tc_fence_after();
+            }
             const unsigned qd = q_lo + (c * (C::kCols / 64) * C::kPart >> 4), kd = k_lo + at[c] * (C::kStage >> 4);
 #pragma unroll
             for (int k = 0; k < C::kCols / 16; ++k) {
                 const unsigned off = ((k >> 2) * C::kPart + (k & 3) * 32) >> 4;
                 umma_ss(lead, tmem, qd + off, kd + off, umma_idesc_bf16(128, 128, 0), c > 0 || k > 0);
             }
+            if (SPB > 1) umma_commit_by(lead, empty + at[c]);
         }
         umma_commit_by(lead, s_full + t);
+        return true;
     };
-    // O of tile t += P in slot times the V block in stages `at`
-    auto issue_pv = [&](int t, const unsigned (&at)[SPB], int slot, bool fresh) {
+    // O of tile t += P in slot times the V block in stages `at` (two stages: the columns of one, then those of the other)
+    auto issue_pv = [&](int t, const unsigned (&at)[SPB], const unsigned (&ph)[SPB], int slot, bool fresh) {
         const unsigned v_lo = UmmaDesc(smem_u32(ring), C::kPart).lo;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (!wait_bar((half ? p_full : p_half) + slot, phase >> slot & 1)) return false;
-            tc_fence_after();
+        for (int c = 0; c < SPB; ++c) {
+            if (SPB > 1 && !wait_bar(full + at[c], ph[c])) return false;
+            const unsigned vd = v_lo + at[c] * (C::kStage >> 4);
 #pragma unroll
-            for (int c = 0; c < SPB; ++c) {
-                const unsigned vd = v_lo + at[c] * (C::kStage >> 4);
+            for (int half = 0; half < 2; ++half) {
+                if (c == 0 && !wait_bar((half ? p_full : p_half) + slot, phase >> slot & 1)) return false;
+                tc_fence_after();
 #pragma unroll
                 for (int u = 4 * half; u < 4 * half + 4; ++u)
                     umma_ts(lead, tmem + C::kColO + t * DP + c * C::kCols, tmem + C::kColP + slot * 64 + u * 8, vd + (u * 2048 >> 4), umma_idesc_bf16(128, C::kCols, 1),
                             !fresh || u > 0);
             }
+            if (SPB > 1) umma_commit_by(lead, empty + at[c]);
         }
         umma_commit_by(lead, pv_done + slot);
         phase ^= 1u << slot;
@@ -449,7 +471,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         for (int j = w.b0; ok && j < w.b1; ++j) {
             if (j > w.b0 + 1) next_block(at, ph);  // V(j - 2)
             next_block(at, ph);
-            ok = block_ready(at, ph);
+            if (SPB == 1) ok = block_ready(at, ph);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
                 if (ok && j >= w.first[t] && j < w.last[t]) {
@@ -457,9 +479,9 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
                     if (!ok) break;
                     phase ^= used;
                     used = 1;
-                    issue_s(t, at);
+                    ok = issue_s(t, at, ph);
                 }
-            if (ok) release(at);
+            if (SPB == 1 && ok) release(at);
         }
         if (!ok) return;
         umma_commit_by(lead, q_empty);
@@ -473,11 +495,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             if (j == w.b0) next_block(at, ph);     // K(b0)
             if (j + 1 < w.b1) next_block(at, ph);  // K(j + 1)
             next_block(at, ph);
-            ok = block_ready(at, ph);
+            if (SPB == 1) ok = block_ready(at, ph);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-                if (ok && j >= w.first[t] && j < w.last[t]) ok = issue_pv(t, at, NT == 2 ? t : (j - w.b0) & 1, j == w.first[t]);
-            if (ok) release(at);
+                if (ok && j >= w.first[t] && j < w.last[t]) ok = issue_pv(t, at, ph, NT == 2 ? t : (j - w.b0) & 1, j == w.first[t]);
+            if (SPB == 1 && ok) release(at);
         }
     };
     // The rows of one item (a softmax warp).
@@ -773,7 +795,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             });
         } else if (warp == kWarpTma) {
             all_items(take, [&]() {
-                if (lane == 0 && w.tokens > 0 && ok) copy_item(w);
+                if (w.tokens > 0 && ok) copy_item(w);
             });
         } else {
             int id = blockIdx.x;
@@ -911,7 +933,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         if (warp == kWarpTma && lane == 0)
 #pragma unroll 1
             for (int i = max(0, stages - NST); i < stages; ++i)
-                if (!mbar_wait_ns(full + i % NST, (i / NST) & 1)) break;
+                mbar_wait_ns(full + i % NST, (i / NST) & 1);
         if ((warp == kWarpMma || warp == kWarpMma + 1) && lane == 0) {
             umma_commit(drain + (warp - kWarpMma));
             mbar_wait_ns(drain + (warp - kWarpMma), 0);
