@@ -421,7 +421,7 @@ int pkv_attend_varlen(const pkv_cache *cache, int32_t layer,
  * by at most 2^-8 of itself) for the product with V, whose sums are fp32.  A NaN or
  * infinity in k or v reaches the rows that see its key and no others (a
  * call that meets one takes longer).  out: fp32, or bf16 with PKV_FLAG_OUT_BF16, 16-byte
- * aligned, [total_rows][q_heads][head_dim].  The launch is a programmatic dependent one,
+ * aligned, [total_rows][q_heads][head_dim], apart from q, k and v.  The launch is a programmatic dependent one,
  * which waits for the kernel before it first thing; PKV_FLAG_PDL has no effect.
  */
 int pkv_attend_prompt(int32_t head_dim, int32_t kv_heads, const pkv_rows *rows,

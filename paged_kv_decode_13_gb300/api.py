@@ -493,7 +493,7 @@ def attend_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_info: t
 
     q (rows, q_heads, head_dim), k and v (rows, kv_heads, head_dim), bf16; rows
     may be strided (slices of a projection's output).  out: fp32 or bf16, like
-    q.  seq_info's segments have kv_end == q_len; max_len bounds it.
+    q, and apart from it.  seq_info's segments have kv_end == q_len; max_len bounds it.
     """
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k and v are (rows, heads, head_dim)")

@@ -1062,7 +1062,7 @@ int pkv_attend_prompt(int32_t head_dim, int32_t kv_heads, const pkv_rows *r, con
     if (r->q_out || r->k_out || r->v_out || r->positions || (flags & ~(PKV_FLAG_OUT_BF16 | PKV_FLAG_PDL))) return PKV_EINVAL;
     if (S < 0 || S > 65535 || max_len <= 0 || window < 0 || (causal != 0 && causal != 1) || !(scale > 0.f) || !isfinite(scale * 1.4426950408889634f)) return PKV_EINVAL;
     const long long nq = (long long)r->q_heads * head_dim, nk = (long long)kv_heads * head_dim;
-    if (!err || !out || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return PKV_EINVAL;
+    if (!err || (!out && r->total_rows > 0) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u)) return PKV_EINVAL;
     if (S > 0 && (!seq_info || !aligned16(seq_info))) return PKV_EINVAL;
     if (r->total_rows == 0) return PKV_OK;
     if (!rows_ok(r->q, r->q_stride, nq, 2) || !rows_ok(r->k, r->k_stride, nk, 2) || !rows_ok(r->v, r->v_stride, nk, 2)) return PKV_EINVAL;

@@ -726,7 +726,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 
     // What a CTA does: items until none is left, or until the list of those to run again is nearly
     // full (the items on their way may each add one a softmax warp); then that list.
-    constexpr int kListRoom = C::kOdd - (SCHED + 1) * C::kSoftmaxWarps;
+    constexpr int kListRoom = C::kOdd - (SCHED + 2) * C::kSoftmaxWarps;  // (asked before the slot is free: a slow warp may be two items behind)
     static_assert(kListRoom > 0, "the list holds what the items on their way may add");
     // Waits on the scheduler last as long as an item may take, and end whatever has happened to the others.
     auto wait_long = [&](uint64_t *bar, unsigned parity) -> bool {

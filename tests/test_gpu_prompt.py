@@ -198,6 +198,35 @@ def test_long_tables(pkv, D, hq, hkv, S):
     assert bool((a[~live] == 0).all()) and bool(torch.isinf(b[~live]).all())
 
 
+def test_no_rows(pkv):
+    q, k, v = make(7, 0, 8, 2, 128)
+    for si in (torch.zeros(0, 4, dtype=torch.int32), torch.zeros(3, 4, dtype=torch.int32)):
+        err = pkv.new_err_flags()
+        pkv.attend_prompt(q, k, v, si.cuda(), torch.empty_like(q), err, 5, 0.1)
+        assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(128, 8, 2), (256, 4, 1)])
+def test_many_bad_items(pkv, D, hq, hkv):
+    """More items to run again than the list holds, after others with a bad row in one warp only."""
+    rows, G = 160 * 190, hq // hkv
+    q, k, v = make(8, rows, hq, hkv, D)
+    si, _ = table([190] * 160)
+    clean, lse0, _ = run(pkv, q, k, v, si)
+    bad = v.clone()
+    i = torch.arange(rows, device="cuda")
+    n, at = i // 190, i % 190
+    bad[(at == 189) & (n % 7 != 0), 0, 5] = float("inf")   # seen by the last row alone
+    bad[(at == 0) & (n % 7 == 3), hkv - 1, 2] = float("nan")  # and by all
+    out, lse, err = run(pkv, q, k, bad, si)
+    last = torch.zeros_like(out, dtype=torch.bool)
+    last[(at == 189) & (n % 7 != 0), :G, 5] = True
+    every = torch.zeros_like(last)
+    every[n % 7 == 3, (hkv - 1) * G:, 2] = True
+    assert err == 0 and torch.equal(lse, lse0) and torch.equal(out[~(last | every)], clean[~(last | every)])
+    assert bool(out[every].isnan().all()) and bool((out[last & ~every] == float("inf")).all())
+
+
 @pytest.mark.parametrize("D,hq,hkv", [(128, 8, 2), (256, 4, 1)])
 def test_the_same_rows_in_many_segments(pkv, D, hq, hkv):
     """An error, but every row of every segment is computed all the same."""

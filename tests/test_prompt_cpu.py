@@ -39,6 +39,11 @@ def test_unsupported_and_empty(pkv):
     assert call(pkv, total_rows=0) == 0 and call(pkv, total_rows=0, S=0, si=None, q=None, k=None, v=None) == 0
 
 
+def test_no_rows_need_no_output(pkv):
+    assert call(pkv, total_rows=0, out=None) == 0 and call(pkv, total_rows=0, out=None, q=None, k=None, v=None) == 0
+    assert call(pkv, total_rows=0, out=0x70008) == -1 and call(pkv, total_rows=0, err=None) == -1
+
+
 def test_binding_checks(pkv):
     q, kv = torch.zeros(5, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 2, 64, dtype=torch.bfloat16)
     si, err, out = torch.tensor([[0, 5, 0, 5]], dtype=torch.int32), pkv.new_err_flags("cpu"), torch.zeros(5, 4, 64)
