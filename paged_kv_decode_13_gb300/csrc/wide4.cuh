@@ -21,7 +21,7 @@
 //               8 i + turn(g);
 //   warp 16     S(j) = Q K_j^T (M 128, N 64, K 128), Q from TMEM (from shared memory its
 //               reads met the dequantising warps' traffic: 89 us of 8-bit drafts
-//               against 86), K from shared memory, into one of NB buffers of TMEM;
+//               against 86 then), K from shared memory, into one of NB buffers of TMEM;
 //   warps 0-7   softmax: row t belongs to warps t / 32 and t / 32 + 4, each with
 //               32 of a group's 64 keys, its own running maximum and sum and
 //               its own O, as in the bf16 tile; P (fp16) over the S columns read;
@@ -31,7 +31,8 @@
 //
 // 16 sequences of up to 8192 keys, 8 kv heads, up to 128 rows each: 65 us with
 // the merge, where the bytes take 12 us, the products (of full tiles) at the
-// measured bf16 rate 19, and the mma.sync tiles 179; in 8 bits 86, the bytes 22.  The tensor cores are 22 %
+// measured bf16 rate 19, and the mma.sync tiles 179; in 8 bits 84, the bytes 22 (halves of a lane's
+// two pieces exchanged as codes and masked only in edge pages: 86.5 before).  The tensor cores are 22 %
 // busy, the schedulers 46 %: the softmax warps' 930 issue slots a group of 64
 // keys and sub-partition (convert, maximum, exp2, pack, rescale) are the
 // longest chain.  Registers 128 / 72 (136 / 64 and 144 / 64: the same time), and a
@@ -204,21 +205,24 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                     }
                     const int pos0 = (w.page0 + li) * kPage, half64 = (lane >> 2) & 1;
                     unsigned char *tile64 = (is_v ? sV + (size_t)vs * C::kTile : sK + (size_t)ks * C::kTile) + half64 * (64 * 128);
+                    if (is_v && !(mine && pos0 >= w.lo_u && pos0 + kPage <= w.hi_u)) {  // keys that no row sees may hold anything
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = pos0 + (lane >> 3) + 4 * i;
+                            if (!mine || key < w.lo_u || key >= w.hi_u) cw[i] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
                     if (mine || is_v) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int tok = (lane >> 3) + 4 * i, row = u * 16 + tok;
-                            const bool some = mine && (!is_v || (pos0 + tok >= w.lo_u && pos0 + tok < w.hi_u));  // keys that no row sees may hold anything
+                            const int row = u * 16 + (lane >> 3) + 4 * i, c = 2 * (lane & 3);
                             unsigned x[8];
-                            unpack_e4m3x4(x[0], x[1], cw[i].x);
-                            unpack_e4m3x4(x[2], x[3], cw[i].y);
-                            unpack_e4m3x4(x[4], x[5], cw[i].z);
-                            unpack_e4m3x4(x[6], x[7], cw[i].w);
-                            const uint4 a = some ? make_uint4(x[0], x[1], x[2], x[3]) : make_uint4(0u, 0u, 0u, 0u);
-                            const uint4 b = some ? make_uint4(x[4], x[5], x[6], x[7]) : make_uint4(0u, 0u, 0u, 0u);
-                            const int c = 2 * (lane & 3);
-                            *reinterpret_cast<uint4 *>(tile64 + swz_row(row, c + half64)) = half64 ? b : a;
-                            *reinterpret_cast<uint4 *>(tile64 + swz_row(row, c + (half64 ^ 1))) = half64 ? a : b;
+                            unpack_e4m3x4(x[0], x[1], half64 ? cw[i].z : cw[i].x);
+                            unpack_e4m3x4(x[2], x[3], half64 ? cw[i].w : cw[i].y);
+                            unpack_e4m3x4(x[4], x[5], half64 ? cw[i].x : cw[i].z);
+                            unpack_e4m3x4(x[6], x[7], half64 ? cw[i].y : cw[i].w);
+                            *reinterpret_cast<uint4 *>(tile64 + swz_row(row, c + half64)) = make_uint4(x[0], x[1], x[2], x[3]);
+                            *reinterpret_cast<uint4 *>(tile64 + swz_row(row, c + (half64 ^ 1))) = make_uint4(x[4], x[5], x[6], x[7]);
                         }
                     }
                     fence_proxy_async();  // the tensor core reads through the async proxy
