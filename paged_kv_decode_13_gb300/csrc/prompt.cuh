@@ -29,13 +29,13 @@
 //   dealer warp   asks for the next item, finds it in the table and works out its blocks for all.
 // Where items are short a role's code is cold each time, some ten cycles an instruction: the kernel has to
 // stay small (88 KB), what an item needs is worked out once, and the steps are spread over warps that
-// wait anyway.  (Every role working items out for itself, 120 KB: 16 prompts of up to 301 rows 33 us, now 29;
+// wait anyway.  (Every role working items out for itself, 120 KB: 16 prompts of up to 301 rows 33 us, now 27;
 // sliding windows at head_dim 256 248, then 209.)
 // TMEM (512 columns): one S of 128, two P of 64, then O (256: two tiles up to head_dim 128,
 // one above).  S is in registers some 200 cycles after it is there, and the next one is computed in its
 // place: with two tiles that of the other tile, so that one tile's softmax runs beside the other's
 // products; with one the next block's.  (S and P in one place for each tile, 2 x 128 columns, let the tiles fall into
-// step, softmax and products in turn: 462 us for one prompt of 8192 rows, now 375.)
+// step, softmax and products in turn: 462 us for one prompt of 8192 rows, now 372.)
 //
 // P is rounded to bf16, as V is: half a step, 2^-8 of a weight, on sums
 // whose result is rounded the same way or averaged over many keys; the sum of weights is
@@ -289,7 +289,7 @@ constexpr int kPromptProbes = 1 << 20;  // of one barrier phase before a wait is
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
     constexpr int DP = C::DP, NT = C::NT, NST = C::NST, SPB = C::SPB, SCHED = C::kSched;
-    constexpr int kWarpMma = C::kSoftmaxWarps, kWarpTma = kWarpMma + 2;  // then the warp that deals items out
+    constexpr int kWarpMma = C::kSoftmaxWarps, kWarpTma = kWarpMma + 2, kWarpDeal = kWarpMma + 3;
     using Item = PromptItem;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sQ = smem_raw + (-smem_u32(smem_raw) & 1023u);  // pointer arithmetic keeps the shared address space
@@ -316,6 +316,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
         *sAbort = 0;
         *sCount = 0;
         *sNext = blockIdx.x;
+    }
+    Segment seen{0, 0, 0, 0};  // dealer: segment `lane`, on its way while the barriers and TMEM are set up
+    if (warp == kWarpDeal) {
+        pdl_wait();
+        if (lane < p.S) seen = load_segment(p.seq_info, lane);
     }
     if (warp == kWarpMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(tslot)), "r"(512) : "memory");
@@ -804,8 +809,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             // ---- units to items: lane i has segment s0 + i of the table and its n items; those of 32 segments come the last ones first
             int s0 = 0, n = 0, all = 0, top = 0, passed = 0;  // items of the 32; the item of each segment looked at, and those of the 32 before it
             long long before = 0;                             // items before s0
-            bool loaded = false;
-            Segment o{0, 0, 0, 0};
+            bool loaded = false, again = false;
+            Segment o = seen;
             auto seek = [&](Segment &g, int &index) -> int {  // the segment of `unit`, or -1
                 if (unit < before + passed) {
                     if (unit < before) {
@@ -817,7 +822,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll 1
                 for (;;) {
                     if (!loaded) {
-                        o = s0 + lane < p.S ? load_segment(p.seq_info, s0 + lane) : Segment{0, 0, 0, 0};
+                        if (again) o = s0 + lane < p.S ? load_segment(p.seq_info, s0 + lane) : Segment{0, 0, 0, 0};
+                        again = true;
                         n = s0 + lane < p.S ? prompt_items(p, o, NT) : 0;
                         all = __reduce_add_sync(0xffffffffu, n);
                         top = __reduce_max_sync(0xffffffffu, n) - 1;
