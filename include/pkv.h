@@ -376,8 +376,8 @@ int pkv_norm_rope_append(const pkv_cache *cache, int32_t layer, const pkv_rope *
  * PKV_FLAG_OUT_BF16.  Scores are those of the stored values to fp32; the
  * softmax weights are rounded to fp16 for the product with V (each by at most
  * 2^-11 of itself or 2^-32 of its row's largest, whichever is more; with PKV_FP8
- * that is said of a weight times its page's V scale, with 2^-31, and sums of such
- * products above 2^100 may overflow).  A NaN in V
+ * that is said of a weight times its page's V scale, and sums of such
+ * products above 2^100 may overflow).  Weights below 2^-126 of the row's largest may count as zero.  A NaN in V
  * reaches only the rows that see its key.  Without a workspace the splits form
  * a cluster (num_splits 0..16); large launches are faster with one (see
  * pkv_attend_workspace_bytes).  PKV_FLAG_SIMT, PKV_FLAG_MMA_SYNC and

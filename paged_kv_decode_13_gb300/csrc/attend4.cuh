@@ -373,10 +373,10 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
     // ---- the warp's pages
     float acc[NT][KS][4];
     float m_r[NT][2], l_r[NT][2];
-    unsigned vref = 0;
+    float w_r[NT][2];  // 8 bits: the reference of the weights of the product with V
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        m_r[nt][0] = m_r[nt][1] = kNoMax;
+        m_r[nt][0] = m_r[nt][1] = w_r[nt][0] = w_r[nt][1] = kNoMax;
         l_r[nt][0] = l_r[nt][1] = 0.f;
 #pragma unroll
         for (int i = 0; i < KS; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
@@ -472,34 +472,21 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sa[e][0][i] += sb[i];
         }
-        // 8 bits: a page's V scale goes into the weights of the product, relative to the
-        // largest one met so far (`vref`, its exponent); the sum of weights stays as it is.
+        // 8 bits: a page's V scale goes into the weights of the product.
         unsigned vt[PP];
-        float fv[PP];
+        float ve[PP];  // log2 of the scale; -inf: every value is zero
         if constexpr (C::BITS == 8) {
-            unsigned most = 0;
 #pragma unroll
             for (int e = 0; e < PP; ++e) {
                 vt[e] = e < pages ? *reinterpret_cast<const unsigned *>(stage + e * C::kPageBytes + C::kBlock + 16 * D) : 0u;
-                most = max(most, vt[e] & 0xffu);
+                ve[e] = (vt[e] & 0xffu) ? (float)((int)(vt[e] & 0xffu) - 127) : -CUDART_INF_F;
             }
-            auto power = [](int d) { return d > -127 ? __uint_as_float((unsigned)(127 + d) << 23) : 0.f; };
-            if (most > vref) {
-                const float f = power((int)vref - (int)most);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int k = 0; k < KS; ++k)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[nt][k][i] *= f;
-                vref = most;
-            }
-#pragma unroll
-            for (int e = 0; e < PP; ++e) fv[e] = (vt[e] & 0xffu) ? power((int)(vt[e] & 0xffu) - (int)vref) : 0.f;
         }
         // Online softmax (base 2) with a lazy maximum: this lane has tokens g,
         // g + 8 of rows 2t, 2t + 1.  x = score - reference; the reference moves
-        // only when some x passes kLazy4.
+        // only when some x passes kLazy4.  8 bits: a weight of the product is
+        // 2^(score + log2 of the page's V scale), against a reference of its own (w_r, as lazy), so that it keeps its bits
+        // whatever the scales of pages that the row does not see, or sees with less weight; the sum of weights stays as it is.
         const bool inside = pages == PP && pos_first >= lo_in && pos_first + (PP - 1) * KW * kPage + kPage <= hi_in;
         unsigned pb[PP][NT][2];
 #pragma unroll
@@ -520,6 +507,16 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
             }
 #pragma unroll
             for (int e = 0; e < PP; ++e) top = fmaxf(top, fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3])));
+            float up[PP][2];  // from x to the weight's exponent
+            if constexpr (C::BITS == 8) {
+#pragma unroll
+                for (int e = 0; e < PP; ++e)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        up[e][i] = ve[e] + (m_r[nt][i] - w_r[nt][i]);
+                        top = fmaxf(top, fmaxf(x[e][i], x[e][i + 2]) + up[e][i]);
+                    }
+            }
             if (__any_sync(0xffffffffu, top > kLazy4)) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -531,9 +528,23 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                             if (x[e][i + o] != -CUDART_INF_F) mx = fmaxf(mx, fmaf(sa[e][nt][i + o], sp[e][nt][i], -kLift4));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    const float al = ex2(m_r[nt][i] - mx);
+                    float al = ex2(m_r[nt][i] - mx);
                     m_r[nt][i] = mx;
                     l_r[nt][i] *= al;
+                    if constexpr (C::BITS == 8) {
+                        float wx = w_r[nt][i];
+#pragma unroll
+                        for (int e = 0; e < PP; ++e)
+#pragma unroll
+                            for (int o = 0; o < 4; o += 2)
+                                if (x[e][i + o] != -CUDART_INF_F) wx = fmaxf(wx, fmaf(sa[e][nt][i + o], sp[e][nt][i], ve[e] - kLift4));
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) wx = fmaxf(wx, __shfl_xor_sync(0xffffffffu, wx, o));
+                        al = ex2(w_r[nt][i] - wx);
+                        w_r[nt][i] = wx;
+#pragma unroll
+                        for (int e = 0; e < PP; ++e) up[e][i] = ve[e] + (mx - wx);
+                    }
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         acc[nt][k][i] *= al;
@@ -552,8 +563,8 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                 l_r[nt][0] += p00 + p10;
                 l_r[nt][1] += p01 + p11;
                 if constexpr (C::BITS == 8) {
-                    pb[e][nt][0] = transpose8x8(pack_f16x2(p00 * fv[e], p01 * fv[e]));
-                    pb[e][nt][1] = transpose8x8(pack_f16x2(p10 * fv[e], p11 * fv[e]));
+                    pb[e][nt][0] = transpose8x8(pack_f16x2(ex2(x[e][0] + up[e][0]), ex2(x[e][1] + up[e][1])));
+                    pb[e][nt][1] = transpose8x8(pack_f16x2(ex2(x[e][2] + up[e][0]), ex2(x[e][3] + up[e][1])));
                 } else {
                     pb[e][nt][0] = transpose8x8(pack_f16x2(p00, p01));
                     pb[e][nt][1] = transpose8x8(pack_f16x2(p10, p11));
@@ -683,6 +694,11 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
             l_r[nt][0] += __shfl_xor_sync(0xffffffffu, l_r[nt][0], o);
             l_r[nt][1] += __shfl_xor_sync(0xffffffffu, l_r[nt][1], o);
         }
+    float unit[NT][2];  // what a row's columns count in (none summed: 0)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) unit[nt][e] = C::BITS == 4 ? 1.f : w_r[nt][e] == kNoMax ? 0.f : ex2(w_r[nt][e] - m_r[nt][e]);
     // A row whose scores are all NaN has no maximum: give it one, so that its
     // NaN sum and columns reach the output.
 #pragma unroll
@@ -697,12 +713,11 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float *r0 = part + (nt * 8 + 2 * tq) * LD, *r1 = r0 + LD;
-            const float unit = C::BITS == 8 ? scale8_value(vref) : 1.f;  // what the sums count in
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
                 const int col = column_of<C>(gq, i);
-                *reinterpret_cast<float2 *>(r0 + col) = make_float2(acc[nt][i][0] * unit, acc[nt][i][2] * unit);
-                *reinterpret_cast<float2 *>(r1 + col) = make_float2(acc[nt][i][1] * unit, acc[nt][i][3] * unit);
+                *reinterpret_cast<float2 *>(r0 + col) = make_float2(acc[nt][i][0] * unit[nt][0], acc[nt][i][2] * unit[nt][0]);
+                *reinterpret_cast<float2 *>(r1 + col) = make_float2(acc[nt][i][1] * unit[nt][1], acc[nt][i][3] * unit[nt][1]);
             }
             if (gq == 0) {
                 float *st = part + R * LD + nt * 8 + 2 * tq;

@@ -57,7 +57,7 @@ struct Wide4 {
     // registers a thread: at launch, of the softmax warps and of the others while the roles run
     static constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsOthers = 72;
     static constexpr int kBars = 2 * NK + 2 * NV + 3 * NB + 2 + 2 * NR + (BITS == 8 ? NS : 0), kPieces = 16;
-    static constexpr size_t kSmem = 1024 + (size_t)(NK + NV) * kTile + kRawBytes + 6 * R * 4 + kBars * 8 + (BITS == 8 ? 2 * NS * PG * 4 : 0) + 256;
+    static constexpr size_t kSmem = 1024 + (size_t)(NK + NV) * kTile + kRawBytes + (BITS == 8 ? 8 : 6) * R * 4 + kBars * 8 + (BITS == 8 ? 2 * NS * PG * 4 : 0) + 256;
     static constexpr unsigned kColO = 64 * NB, kColQ = kColO + 256; // O_h at kColO + 128 h; Q as fp16 pairs
     static_assert(kColQ + 64 <= 512, "the columns of TMEM");
     static_assert(kSmem <= 232448, "exceeds the per-CTA shared memory limit");
@@ -100,8 +100,8 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
     unsigned char *sV = sK + (size_t)NK * C::kTile;
     unsigned char *raw = sV + (size_t)NV * C::kTile;                // [NR][PG] raw pages
     float *sQm = reinterpret_cast<float *>(raw + C::kRawBytes);     // [2][R] largest query magnitude of each half
-    float *sXm = sQm + 2 * R, *sXl = sXm + 2 * R;                   // [2][R] each half's maximum and sum
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sXl + 2 * R);
+    float *sXm = sQm + 2 * R, *sXl = sXm + 2 * R, *sXu = sXl + 2 * R;  // [2][R] each half's maximum and sum; 8 bits: what its O counts in
+    uint64_t *bars = reinterpret_cast<uint64_t *>(k8 ? sXu + 2 * R : sXu);
     uint64_t *k_full = bars, *k_empty = k_full + NK, *v_full = k_empty + NK, *v_empty = v_full + NV;
     uint64_t *s_full = v_empty + NV, *p_full = s_full + NB, *pv_done = p_full + NB;
     uint64_t *q_full = pv_done + NB, *drain = q_full + 1, *raw_full = drain + 1, *raw_empty = raw_full + NR;
@@ -109,7 +109,6 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
     unsigned *sWord = reinterpret_cast<unsigned *>(bars + C::kBars);  // [K, V][NS][PG] scale and NaN tokens of the pages
     unsigned *tslot = sWord + (k8 ? 2 * C::NS * PG : 0);
     volatile int *sAbort = reinterpret_cast<volatile int *>(tslot + 1);
-    float *sUnit = reinterpret_cast<float *>(tslot + 2 + C::kPieces);  // 8 bits: [2] what O of each half counts in
     int *sPiece = reinterpret_cast<int *>(tslot + 2);               // [kPieces] flags of piece i % kPieces: 1 bad page, 2 NaN in an edge page's V
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3, cta = blockIdx.x;
@@ -461,7 +460,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
             if (real) row_key_bounds(w.sg.kend - w.sg.ql + (w.row0 + r) / p.G, w.sg.kend, p.causal, p.window, first, lo_r, hi_r);
             const int hi_k = min(hi_r, (w.page0 + w.pages) * kPage);  // of this piece
             float m = kNoMax, l = 0.f;
-            unsigned vref = 0;  // 8 bits: the largest exponent of a V page so far, which O_half counts in
+            float wref = kNoMax;  // 8 bits: the reference of the weights of the product with V, which O_half counts in (attend4.cuh)
 #pragma unroll 1
             for (int j = 0; j < ngr && !timed_out; ++j, tile3.next()) {
                 const int J = gbase + j, b = tile3.i;
@@ -473,14 +472,15 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                 float x[32];
                 tmem_ld32(tmem + lane_off + b * 64 + half * 32, x);
                 float f[2] = {sc, sc};           // of the scores of each of the half's two pages
-                unsigned vw[2] = {0, 0}, most = 0;
+                float ve[2] = {0.f, 0.f};        // 8 bits: log2 of the pages' V scales, -inf: every value is zero
                 if constexpr (k8) {
                     const unsigned *kw = sWord + (J % C::NS) * PG + half * 2;
-                    vw[0] = kw[C::NS * PG];
-                    vw[1] = kw[C::NS * PG + 1];
-                    most = max(vw[0] & 0xffu, vw[1] & 0xffu);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) f[i] = fmaxf(sc * scale8_value(kw[i] & 0xffu), 1e-38f);
+                    for (int i = 0; i < 2; ++i) {
+                        f[i] = fmaxf(sc * scale8_value(kw[i] & 0xffu), 1e-38f);
+                        const unsigned b8 = kw[C::NS * PG + i] & 0xffu;
+                        ve[i] = b8 ? (float)((int)b8 - 127) : -CUDART_INF_F;
+                    }
                     if ((kw[0] | kw[1]) >> 16) {  // tokens that hold a NaN
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                         if (pos < lo_u || pos >= hi_u) x[k] = -CUDART_INF_F;
                     }
                 }
-                float mx;
+                float mx, wx = 0.f;  // wx, 8 bits: the largest exponent of a weight of the product
                 if constexpr (k8) {  // the pages' maxima each as a tree of three-way maxima
                     float t[2];
 #pragma unroll
@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                         t[i] = fmaxf(max3(a, max3(y[9], y[10], y[11]), max3(y[12], y[13], y[14])), y[15]) * f[i];
                     }
                     mx = fmaxf(t[0], t[1]);
+                    wx = fmaxf(t[0] + ve[0], t[1] + ve[1]);
                 } else {  // row maximum of the 32 scores as a tree of three-way maxima
                     float t[11];
 #pragma unroll
@@ -515,13 +516,11 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                     const float a = max3(t[0], t[1], t[2]), b3 = max3(t[3], t[4], t[5]), c3 = max3(t[6], t[7], t[8]);
                     mx = max3(max3(a, b3, c3), t[9], t[10]) * sc;
                 }
-                const bool grow = mx > m + kLazy4;
-                auto power = [](int d) { return d > -127 ? __uint_as_float((unsigned)(127 + d) << 23) : 0.f; };
-                if (__any_sync(0xffffffffu, grow) || (k8 && most > vref)) {
-                    const float m_new = grow ? mx - kLift4 : m, alpha = ex2(m - m_new);
-                    const bool raised = k8 && most > vref && vref > 0;
-                    const float all = raised ? alpha * power((int)vref - (int)(most + 1)) : alpha;  // (a step above the largest: it moves less often)
-                    if (j > 0 && (raised || __any_sync(0xffffffffu, grow && m != kNoMax))) {
+                const bool grow = mx > m + kLazy4, raise = k8 && wx > wref + kLazy4;
+                if (__any_sync(0xffffffffu, grow || raise)) {
+                    const float m_new = grow ? mx - kLift4 : m, alpha = ex2(m - m_new), w_new = raise ? wx - kLift4 : wref;
+                    const float all = k8 ? ex2(wref - w_new) : alpha;
+                    if (j > 0 && __any_sync(0xffffffffu, k8 ? raise && wref != kNoMax : grow && m != kNoMax)) {
                         // O_half holds P V up to the group before against the old reference
                         if (!wait_bar(pv_done + (b ? b - 1 : NB - 1), b ? tile3.phase : tile3.phase ^ 1)) { timed_out = true; break; }
                         tc_fence_after();
@@ -536,16 +535,23 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                     }
                     l *= alpha;
                     m = m_new;
-                    if (k8 && most > vref) vref = most + 1;
+                    wref = w_new;
                 }
                 unsigned pk[16];
-                const uint64_t mm2 = f32x2(-m, -m);
-                uint64_t fv[2];  // 8 bits: the V page's scale goes into the weights of the product
+                // 8 bits: a weight of the product is that of the sum times 2^up of its page.  A page whose scale is 2^127 and
+                // more above the reference has small weights alone: they are raised by 2^far beforehand.
+                float far = 0.f;
+                uint64_t fv[2];
+                if constexpr (k8) {
+                    const float up[2] = {ve[0] + (m - wref), ve[1] + (m - wref)};
+                    far = fminf(fmaxf(fmaxf(up[0], up[1]) - 127.f, 0.f), 100.f);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float v = (vw[i] & 0xffu) ? power((int)(vw[i] & 0xffu) - (int)vref) : 0.f;
-                    fv[i] = f32x2(v, v);
+                    for (int i = 0; i < 2; ++i) {
+                        const float v = ex2(fminf(up[i] - far, 127.f));
+                        fv[i] = f32x2(v, v);
+                    }
                 }
+                const uint64_t mm2 = f32x2(far - m, far - m);
                 uint64_t la = 0, lb = 0;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
@@ -561,7 +567,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
                 {
                     float l0, l1;
                     f32x2_split(add_f32x2(la, lb), l0, l1);
-                    l += l0 + l1;
+                    l = k8 ? fmaf(l0 + l1, ex2(-far), l) : l + (l0 + l1);
                 }
                 // P(j) as fp16 pairs over the first 16 of this half's S columns (read above)
                 tmem_st16(tmem + lane_off + b * 64 + half * 32, pk);
@@ -575,7 +581,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
             tc_fence_after();
             sXm[half * R + r] = m == kNoMax ? (l != l ? 0.f : -CUDART_INF_F) : m;  // a row of NaN scores keeps its NaN sum
             sXl[half * R + r] = l;
-            if (k8 && r == 0) sUnit[half] = scale8_value(vref);  // (the same for all rows)
+            if (k8) sXu[half * R + r] = wref == kNoMax ? 0.f : ex2(wref - m);
             const int flags = *reinterpret_cast<volatile int *>(sPiece + piece % C::kPieces);
             named_barrier(1, 256);
             if (timed_out) continue;
@@ -585,7 +591,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
             const float m0 = sXm[r], m1 = sXm[R + r], M = fmaxf(m0, m1);
             const float w0 = m0 == -CUDART_INF_F ? 0.f : ex2(m0 - M), w1 = m1 == -CUDART_INF_F ? 0.f : ex2(m1 - M);
             const float L = w0 * sXl[r] + w1 * sXl[R + r];
-            const float v0 = k8 ? w0 * sUnit[0] : w0, v1 = k8 ? w1 * sUnit[1] : w1;  // of the halves' columns
+            const float v0 = k8 ? w0 * sXu[r] : w0, v1 = k8 ? w1 * sXu[R + r] : w1;  // of the halves' columns
             // A NaN in V (4 bits: on a page that not every row sees) was left out: the rows that see it get it here.
             unsigned nan = 0;  // bit g: columns 16 g ..
             if (flags & 2)
