@@ -70,8 +70,10 @@ typedef enum pkv_status {
  * even.  A page is filled as tokens come: those that are in it keep e from
  * getting smaller, and where a new one makes it larger, their codes are rounded to the larger one
  * (exact down to 2^-6 times the scale, by at most 2^-10 times it below).  A
- * page whose new rows begin at its first slot starts afresh (with ring
- * storage: one whose slots are all new).  A token of a kv head that holds a NaN
+ * page whose new rows begin at its first slot starts afresh.  With ring storage the slots that the
+ * sequence has not come to hold nothing, whatever an earlier one left there, and
+ * e comes down (exactly) where it is more than 6 above what the new rows need and the tokens that the window of the
+ * call's first row still reaches; tokens further back, until they are overwritten, saturate then.  A token of a kv head that holds a NaN
  * reads back as NaN, all of it, and an infinity as 448 * 2^119.  Rows are bf16.
  */
 typedef enum pkv_dtype { PKV_BF16 = 0, PKV_F32 = 1, PKV_FP4 = 2, PKV_FP8 = 8 } pkv_dtype;

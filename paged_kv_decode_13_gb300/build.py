@@ -1,8 +1,9 @@
 """Build libpkv.so in-tree with nvcc for sm_103a.
 
 Nine attention translation units (three compute variants x three padded
-head_dims), three of the 4-bit attention (one per head_dim), the norm + rotary
-+ append unit and the C-ABI unit compile in parallel, then link into one shared
+head_dims), six of the attention over quantised caches and three of the 8-bit
+append (one per head_dim and format), the norm + rotary + append unit, that of prompt
+attention and the C-ABI unit compile in parallel, then link into one shared
 library next to this file.  Objects go to ``_build/`` (git-ignored).
 """
 from __future__ import annotations
@@ -39,6 +40,7 @@ def _sources():
     for d in (64, 128, 256):
         for bits in (4, 8):
             units.append((os.path.join(CSRC, "attend4_inst.cu"), f"attend{bits}_{d}.o", [f"-DPKV_INST_D={d}", f"-DPKV_INST_BITS={bits}"]))
+        units.append((os.path.join(CSRC, "append8_inst.cu"), f"append8_{d}.o", [f"-DPKV_INST_D={d}"]))
     units.append((os.path.join(CSRC, "rope.cu"), "rope.o", []))
     units.append((os.path.join(CSRC, "append8.cu"), "append8.o", []))
     units.append((os.path.join(CSRC, "prompt.cu"), "prompt.o", []))

@@ -1,20 +1,10 @@
-// Instantiations and launch of the append to an 8-bit cache.
+// Launch of the append to an 8-bit cache, and reading it back.
 #include <algorithm>
 
 #include "append8.cuh"
 #include "rope_launch.h"
 
 namespace pkv {
-
-template <int D>
-static const void *pick_pair8(int pair) {
-    switch (pair) {
-        case kPlainRows: return reinterpret_cast<const void *>(&append8_kernel<D, kPlainRows>);
-        case kInLane: return reinterpret_cast<const void *>(&append8_kernel<D, kInLane>);
-        case kByShuffle: return reinterpret_cast<const void *>(&append8_kernel<D, kByShuffle>);
-        default: return reinterpret_cast<const void *>(&append8_kernel<D, kByShared>);
-    }
-}
 
 cudaError_t launch_append8(const RopeParams &r, int sms, cudaStream_t stream) {
     Append8Params a;
@@ -39,7 +29,7 @@ cudaError_t launch_append8(const RopeParams &r, int sms, cudaStream_t stream) {
     cfg.attrs = &after;
     cfg.numAttrs = 1;
     void *args[] = {&a};
-    const void *fn = r.D == 64 ? pick_pair8<64>(pair) : r.D == 128 ? pick_pair8<128>(pair) : pick_pair8<256>(pair);
+    const void *fn = r.D == 64 ? pick_append8_64(pair, r.ring_rows) : r.D == 128 ? pick_append8_128(pair, r.ring_rows) : pick_append8_256(pair, r.ring_rows);
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 

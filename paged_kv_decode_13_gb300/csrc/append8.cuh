@@ -9,6 +9,13 @@
 // the rows as they are held.  Tokens that are in the page already keep the scale
 // from shrinking; where it grows, their codes are brought to it.
 //
+// In a ring a scale is left over once the tokens that made it are overwritten or behind the
+// window, or are those of an earlier sequence.  Where it is far (kScaleSlack8) above what the new rows need,
+// the codes of the tokens that some row may still see are looked at, and where it is as far above theirs it comes down to the larger
+// of both, which is exact for them.  Older tokens stay until they are overwritten (a rewind may bring them back), and saturate;
+// a slot that the sequence has not come to holds nothing.  (A kernel of its own: with the look in the
+// one of flat caches, 256 sequences of a row each took 9.8 us there, not 9.3, 12.9, not 11.3, at head_dim 256.)
+//
 // The tokens of one page may come from several segments of a call (pieces of one
 // sequence, a padded batch that holds a segment twice).  The scale is theirs in
 // common, so the lowest of them writes the page for all; where the table's columns
@@ -25,6 +32,9 @@
 namespace pkv {
 
 constexpr int kAppend8Warps = 4, kAppend8Threads = kAppend8Warps * 32;
+// Doublings by which a ring's page may have too large a scale: of the 14.8 from 448 down to the first value that loses
+// bits, so that rows of less than 2^-6 of the scale's largest start it anew.  (With four, pages of ordinary rows are looked at now and then, a microsecond each.)
+constexpr unsigned kScaleSlack8 = 6;
 constexpr int kPlainRows = 3;  // beside RopePair: rows that are neither normalised nor turned, and no queries
 
 struct Append8Params {
@@ -32,6 +42,11 @@ struct Append8Params {
     int page_ctas;    // CTAs that share the pages
     int head_ctas;    // and those that share a page's heads
 };
+
+// The kernel for how column pairs meet (RopePair, kPlainRows), one unit per head_dim.
+const void *pick_append8_64(int pair, bool ring);
+const void *pick_append8_128(int pair, bool ring);
+const void *pick_append8_256(int pair, bool ring);
 
 // Pages that a segment's new rows go to; none for an empty or refused one.
 __device__ __forceinline__ int new_pages(const RopeParams &p, const Segment &sg) {
@@ -54,8 +69,9 @@ __device__ __forceinline__ int row_of_slot(const Segment &o, int slot, int ring_
 
 // Which rows the page `tp` of segment s's column gets from all segments of the table,
 // later ones before earlier ones where two write a slot, and the lowest segment that
-// writes it.  One warp; lane j < 16 has slot j's row and position.
-__device__ __noinline__ int merge_page_rows(const RopeParams &p, const Segment &sg, int tp, int lane, int &row, int &pos) {
+// writes it.  One warp; lane j < 16 has slot j's row and position.  first, kend: of all segments that
+// write this column, the lowest first position and the highest end.
+static __device__ __noinline__ int merge_page_rows(const RopeParams &p, const Segment &sg, int tp, int lane, int &row, int &pos, int &first, int &kend) {
     int owner = -1;
     row = -1;
     pos = 0;
@@ -69,6 +85,8 @@ __device__ __noinline__ int merge_page_rows(const RopeParams &p, const Segment &
             const int s = s0 + __ffs(m) - 1;
             const Segment o = load_segment(p.seq_info, s);
             if (!new_pages_ok(p, o, lane)) continue;
+            first = min(first, o.kend - o.ql);
+            kend = max(kend, o.kend);
             int at;
             const int r = row_of_slot(o, tp * kPage + (lane & 15), p.ring_rows, at);
             if (!__any_sync(0xffffffffu, r >= 0)) continue;
@@ -82,9 +100,37 @@ __device__ __noinline__ int merge_page_rows(const RopeParams &p, const Segment &
     return owner;
 }
 
-// One head of one page: kind 0 q, 1 k, 2 v.  rows: the page's new rows by slot, -1: none.  angles: [16][rot_dim / 2].
-template <int D, int PAIR>
-__device__ __forceinline__ void append8_head(const RopeParams &p, int kind, int h, const int *rows, const float2 *angles, long long block,
+// Which slots of a ring's page `tp` without a new row (`fresh`) hold a token, and, in the upper 16 bits, which of those some row may still see.
+// One warp, lane j < 16: slot j.  first, kend: of the column's new rows.
+__device__ __forceinline__ unsigned kept_tokens(const RopeParams &p, int tp, unsigned fresh, int first, int kend, int lane) {
+    // the slot's token is the last one before kend
+    const int back = (kend - 1 - (tp * kPage + (lane & 15))) % p.ring_rows;
+    const long long at = (long long)kend - 1 - (back < 0 ? back + p.ring_rows : back);
+    const bool there = lane < kPage && !(fresh >> (lane & 15) & 1u) && at >= 0;
+    const unsigned m = __ballot_sync(0xffffffffu, there);
+    return m | __ballot_sync(0xffffffffu, there && at > (long long)first - p.window) << 16;
+}
+
+// The scale that the tokens `count` of block `at` need, which are held under b0.
+template <int D>
+__device__ __noinline__ unsigned scale_needed(const unsigned char *at, unsigned count, unsigned b0, int lane) {
+    unsigned top = 0;  // largest code
+#pragma unroll 1
+    for (int i = lane; i < kPage * D / 16; i += 32) {
+        if (!(count >> (i / (D / 16)) & 1u)) continue;
+        const uint4 w = reinterpret_cast<const uint4 *>(at)[i];
+        const unsigned m = __vmaxu4(__vmaxu4(w.x & 0x7f7f7f7fu, w.y & 0x7f7f7f7fu), __vmaxu4(w.z & 0x7f7f7f7fu, w.w & 0x7f7f7f7fu));
+        top = max(top, max(max(m & 0xffu, m >> 8 & 0xffu), max(m >> 16 & 0xffu, m >> 24)));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    unsigned lo, hi;
+    unpack_e4m3x4(lo, hi, top);
+    return scale8_of(__float_as_uint(half2_floats(lo).x * scale8_value(b0)));
+}
+
+// One head of one page: kind 0 q, 1 k, 2 v.  rows: the page's new rows by slot, -1: none.  tokens: kept_tokens of a ring's page.  angles: [16][rot_dim / 2].
+template <int D, int PAIR, bool RING>
+__device__ __forceinline__ void append8_head(const RopeParams &p, int kind, int h, const int *rows, unsigned tokens, const float2 *angles, long long block,
                                              float *stage, int lane) {
     constexpr int L = D / 8, TPI = 32 / L, IT = kPage / TPI;  // lanes a row, rows at once, turns
     using T = __nv_bfloat16;
@@ -97,8 +143,7 @@ __device__ __forceinline__ void append8_head(const RopeParams &p, int kind, int 
     const unsigned fresh = __ballot_sync(0xffffffffu, lane < kPage && rows[lane & 15] >= 0);  // bit j: slot j has a new row
     auto some = [&](int it) { return (fresh >> (it * TPI)) & ((1u << TPI) - 1u); };
     unsigned char *out = reinterpret_cast<unsigned char *>(kind == 1 ? p.k_pool : p.v_pool) + (block * p.Hkv + h) * block8_bytes(D);
-    unsigned kept = ~fresh & 0xffffu;  // a ring's page holds older tokens behind the new ones too
-    if (!p.ring_rows) kept &= (1u << (31 - __clz(fresh))) - 1u;
+    const unsigned kept = RING ? tokens & 0xffffu : ~fresh & ((1u << (31 - __clz(fresh))) - 1u);
     unsigned word = 0;  // the page's scale and NaN tokens, on their way with the rows
     if (kind && kept) word = *reinterpret_cast<const unsigned *>(out + 16 * D);
     Raw8<T> x[IT];
@@ -240,18 +285,25 @@ __device__ __forceinline__ void append8_head(const RopeParams &p, int kind, int 
     if (kept) {
         const unsigned b0 = min(word & 0xffu, kScaleMax8);
         nan |= (word >> 16) & kept;
-        if (b > b0 && b0) {
-            const float down = b - b0 < 32 ? __uint_as_float((127u + b0 - b) << 23) : 0.f;  // (what is 2^-18 of 2^-9 or less reads zero anyway)
+        unsigned least = b0;
+        if (RING && b0 > b + kScaleSlack8) {
+            const unsigned theirs = scale_needed<D>(out, tokens >> 16, b0, lane);
+            if (max(theirs, b) + kScaleSlack8 < b0) least = max(theirs, 1u);
+        }
+        b = max(b, least);
+        if ((RING ? b != b0 : b > b0) && b0) {
+            // to a larger scale: what is 2^-18 of 2^-9 or less reads zero anyway; to a smaller one: what is too large saturates
+            float by = b - b0 < 32 ? __uint_as_float((127u + b0 - b) << 23) : 0.f;
+            if (RING && b < b0) by = __uint_as_float((127u + min(b0 - b, 127u)) << 23);
 #pragma unroll 1
             for (int it = 0; it < IT; ++it) {
                 const int tok = it * TPI + sub;
                 if (!(kept >> tok & 1u)) continue;
                 uint2 *a = reinterpret_cast<uint2 *>(out + tok * D + 16 * place8(tok, c >> 1, D) + 8 * (c & 1));
                 const uint2 w = *a;
-                *a = make_uint2(lower_e4m3x4(w.x, down), lower_e4m3x4(w.y, down));
+                *a = make_uint2(scale_e4m3x4(w.x, by), scale_e4m3x4(w.y, by));
             }
         }
-        b = max(b, b0);
     }
     const float inv = scale8_inverse(b), scale = scale8_value(b);
 #pragma unroll
@@ -311,10 +363,11 @@ static __global__ void __launch_bounds__(256) read8_kernel(const __grid_constant
     }
 }
 
-template <int D, int PAIR>
-__global__ void __launch_bounds__(kAppend8Threads, PAIR == kPlainRows ? (D == 256 ? 3 : 5) : D == 256 ? 3 : 4) append8_kernel(const __grid_constant__ Append8Params a) {
+template <int D, int PAIR, bool RING>
+__global__ void __launch_bounds__(kAppend8Threads, D == 256 ? 3 : PAIR == kPlainRows && !(RING && D == 128) ? 5 : 4) append8_kernel(const __grid_constant__ Append8Params a) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int sRow[2][kPage], sPos[2][kPage], sOwner;  // own rows; those of every segment
+    __shared__ unsigned sKept;  // (ring)
     __shared__ long long sSum[kAppend8Warps], sFirst;
     __shared__ int sSegment;
     const RopeParams &p = a.r;
@@ -406,17 +459,21 @@ __global__ void __launch_bounds__(kAppend8Threads, PAIR == kPlainRows ? (D == 25
         const long long block = p.block_table[(long long)sg.col * p.mbps + tp];
         __syncthreads();
         if (warp == 0) {
-            int pos, row = row_of_slot(sg, tp * kPage + (lane & 15), p.ring_rows, pos), owner = s;
+            int pos, row = row_of_slot(sg, tp * kPage + (lane & 15), p.ring_rows, pos), owner = s, from = sg.kend - sg.ql, to = sg.kend;
             if (lane < kPage) {
                 sRow[0][lane] = row;
                 sPos[0][lane] = pos;
             }
-            if (shared) owner = merge_page_rows(p, sg, tp, lane, row, pos);
+            if (shared) owner = merge_page_rows(p, sg, tp, lane, row, pos, from, to);
+            const unsigned tokens = RING ? kept_tokens(p, tp, __ballot_sync(0xffffffffu, lane < kPage && row >= 0), from, to, lane) : 0u;
             if (lane < kPage) {
                 sRow[1][lane] = row;
                 sPos[1][lane] = pos;
             }
-            if (lane == 0) sOwner = owner;
+            if (lane == 0) {
+                sOwner = owner;
+                sKept = tokens;
+            }
         }
         // Own rows serve q, those of every segment k and v; they are the same but where segments share a column.
 #pragma unroll 1
@@ -444,7 +501,7 @@ __global__ void __launch_bounds__(kAppend8Threads, PAIR == kPlainRows ? (D == 25
 #pragma unroll 1
             for (int it = i0 + hc * kAppend8Warps + warp; it < i1; it += a.head_ctas * kAppend8Warps) {
                 const int kind = it < nq ? 0 : it < nq + p.Hkv ? 1 : 2;
-                append8_head<D, PAIR>(p, kind, kind == 0 ? it : kind == 1 ? it - nq : it - nq - p.Hkv, sRow[pass], angles, block, stage, lane);
+                append8_head<D, PAIR, RING>(p, kind, kind == 0 ? it : kind == 1 ? it - nq : it - nq - p.Hkv, sRow[pass], RING ? sKept : 0u, angles, block, stage, lane);
             }
         }
     }

@@ -60,12 +60,12 @@ __device__ __forceinline__ void unpack_e4m3x4(unsigned &lo, unsigned &hi, unsign
         : "r"(w));
 }
 __device__ __forceinline__ float2 half2_floats(unsigned h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
-// The codes of a word under a scale 2^-down of the one before.
-__device__ __forceinline__ unsigned lower_e4m3x4(unsigned w, float down) {
+// The codes of a word, their values times `by` (saturating).
+__device__ __forceinline__ unsigned scale_e4m3x4(unsigned w, float by) {
     unsigned lo, hi;
     unpack_e4m3x4(lo, hi, w);
     const float2 a = half2_floats(lo), b = half2_floats(hi);
-    return pack_e4m3x4(a.x * down, a.y * down, b.x * down, b.y * down);
+    return pack_e4m3x4(a.x * by, a.y * by, b.x * by, b.y * by);
 }
 
 }  // namespace pkv
