@@ -207,7 +207,8 @@ const char *pkv_status_str(int status);
  * the segments of one call may write different slots of a page in the same column (the
  * lowest of them writes the page; of rows for one slot the highest segment's counts),
  * and a segment may be in the table twice, but columns whose tables name one page must
- * not both write it, in one call or in two at a time.
+ * not both write it, in one call or in two at a time.  An append is at its sequence's
+ * end: tokens that such a page holds at kv_end and later are not kept.
  */
 int pkv_append(const pkv_cache *cache, int32_t layer,
                const void *k_new, const void *v_new, int32_t total_rows,
@@ -545,7 +546,11 @@ int pkv_seq_clone(const pkv_cache *cache, int32_t src_col, int32_t dst_col, int6
  * rewind of the batched-sequence cache ([ExecuTorch #24073], bounded by the
  * ring floor), on the device: kv_end -= amount[s] for every segment s
  * (amount: device int32[num_segments]), e.g. the draft tokens a verify step
- * rejected; their slots are simply rewritten by the next append.  A segment
+ * rejected; their slots are simply rewritten by the next append.  On a PKV_FP8
+ * cache that does not undo the append of the rejected rows: where tokens before them are in
+ * their page, those have been rounded to the scale that the rejected rows needed too (by at most 2^-10 of it; under
+ * that of an infinity, 2^119, ordinary values are zero), and a page of a flat cache keeps that scale while it has tokens
+ * before the new rows.  In a ring the tokens that the window had passed may be saturated (see PKV_FP8).  A segment
  * keeps its kv_end and sets PKV_ERR_SEGMENT when amount < 0 or
  * amount > kv_end, and PKV_ERR_RING when the cache is a ring of R rows and
  * amount > R - window + 1 (the next step's window would need positions the
