@@ -311,8 +311,8 @@ int pkv_norm_rope(const pkv_rope *rope, int32_t dtype, int32_t head_dim, int32_t
  * unspecified which of them places it).  On a PKV_FP4 cache it goes to its slot
  * in every segment that holds it, turned by positions[row] or by its position
  * in the lowest of them (v_out must not be v then).  On a PKV_FP8 cache it goes to
- * all of them too; its q_out, k_out and v_out are then unspecified (and must not be q,
- * k and v).  Rows no segment covers, and
+ * all of them too; its queries are turned once, by positions[row] or by its position in one of them, in place
+ * or not, but its k_out and v_out are unspecified (and must not be k and v).  Rows no segment covers, and
  * rows of segments that pkv_append would refuse (the same PKV_ERR_* bits), are
  * not written, in none of the outputs.  A later attention call may be launched
  * with PKV_FLAG_PDL behind this one, unless one segment's rows are older keys

@@ -18,8 +18,9 @@
 //
 // The tokens of one page may come from several segments of a call (pieces of one
 // sequence, a padded batch that holds a segment twice).  The scale is theirs in
-// common, so the lowest of them writes the page for all; where the table's columns
-// ascend, as a step's mostly do, or no other valid segment names the same one, none of that is asked.
+// common, so the lowest of them writes the page for all.  A row's queries are turned once, for the lowest
+// segment that holds it (they may be turned in place).  Where the table's columns and rows
+// ascend, as a step's mostly do, or no other valid segment names the same ones, none of that is asked.
 //
 // How many pages there are only the table says: every CTA sums it (a thread some
 // segments) and takes every n-th page of all segments end to end.  (A CTA for each page that a
@@ -98,6 +99,23 @@ static __device__ __noinline__ int merge_page_rows(const RopeParams &p, const Se
         }
     }
     return owner;
+}
+
+// Slots whose row a segment below s, segment sg, holds as well: bit j for slot j.  One warp, lane j < 16 has slot j's row.
+static __device__ __noinline__ unsigned rows_of_lower(const RopeParams &p, const Segment &sg, int s, int row, int lane) {
+    unsigned taken = 0;
+#pragma unroll 1
+    for (int s0 = 0; s0 < s; s0 += 32) {
+        const Segment a = load_segment(p.seq_info, min(s0 + lane, s - 1));
+        unsigned m = __ballot_sync(0xffffffffu, s0 + lane < s && overlap(a, sg) && new_pages(p, a) > 0);
+#pragma unroll 1
+        for (; m; m &= m - 1) {
+            const Segment o = load_segment(p.seq_info, s0 + __ffs(m) - 1);
+            if (!new_pages_ok(p, o, lane)) continue;
+            taken |= __ballot_sync(0xffffffffu, lane < kPage && row >= o.q0 && (long long)row < (long long)o.q0 + o.ql);
+        }
+    }
+    return taken;
 }
 
 // Which slots of a ring's page `tp` without a new row (`fresh`) hold a token, and, in the upper 16 bits, which of those some row may still see.
@@ -366,7 +384,7 @@ static __global__ void __launch_bounds__(256) read8_kernel(const __grid_constant
 template <int D, int PAIR, bool RING>
 __global__ void __launch_bounds__(kAppend8Threads, D == 256 ? 3 : PAIR == kPlainRows && !(RING && D == 128) ? 5 : 4) append8_kernel(const __grid_constant__ Append8Params a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int sRow[2][kPage], sPos[2][kPage], sOwner;  // own rows; those of every segment
+    __shared__ int sRow[2][kPage], sPos[2][kPage], sOwner;  // own rows (apart: queries'); those of every segment
     __shared__ unsigned sKept;  // (ring)
     __shared__ long long sSum[kAppend8Warps], sFirst;
     __shared__ int sSegment;
@@ -380,16 +398,27 @@ __global__ void __launch_bounds__(kAppend8Threads, D == 256 ? 3 : PAIR == kPlain
     // ---- the pages of all segments: thread t sums segments t per .. (a table of one needs no sum)
     const int per = (p.S + kAppend8Threads - 1) / kAppend8Threads, s_lo = min(tid * per, p.S), s_hi = min(s_lo + per, p.S);
     long long mine = 0, upto, total;
-    bool may_share = false;  // columns that do not ascend
+    const bool queries = PAIR != kPlainRows && p.q;
+    bool may_share = false;  // columns or rows that do not ascend
     Segment sg{0, 0, 0, 0};
     if (p.S > 1) {
-        int last = s_lo > 0 && s_lo < s_hi ? load_segment(p.seq_info, s_lo - 1).col : -1;
+        int last = -1;
+        long long rows_to = INT32_MIN;  // end of the last one's rows
+        if (s_lo > 0 && s_lo < s_hi) {
+            const Segment o = load_segment(p.seq_info, s_lo - 1);
+            last = o.col;
+            rows_to = o.ql > 0 ? (long long)o.q0 + o.ql : INT32_MAX;
+        }
 #pragma unroll 4
         for (int i = s_lo; i < s_hi; ++i) {
             const Segment o = load_segment(p.seq_info, i);
             mine += new_pages(p, o);
             may_share |= o.col <= last;
             last = o.col;
+            if (PAIR != kPlainRows) {
+                may_share |= queries && o.ql > 0 && o.q0 < rows_to;
+                rows_to = o.ql > 0 ? (long long)o.q0 + o.ql : INT32_MAX;
+            }
             const unsigned fault = segment_fault(o, p.rows, p.max_seqs, p.mbps, p.ring_rows, p.window);
             if (fault && blockIdx.x == 0) atomicOr(p.err, fault);
         }
@@ -416,7 +445,7 @@ __global__ void __launch_bounds__(kAppend8Threads, D == 256 ? 3 : PAIR == kPlain
     const int nq = p.q ? p.Hq : 0, items = nq + 2 * p.Hkv;
     long long end = 0, first = 0;  // pages before the segment's end, and before it
     int s = 0, p0 = 0;
-    bool fine = false, shared = false;
+    bool fine = false, shared = false, twice = false;
 #pragma unroll 1
     for (long long at = pc; at < total; at += a.page_ctas) {
         if (at >= end) {  // another segment
@@ -443,14 +472,17 @@ __global__ void __launch_bounds__(kAppend8Threads, D == 256 ? 3 : PAIR == kPlain
             p0 = (sg.kend - sg.ql) / kPage;
             fine = new_pages_ok(p, sg, lane);  // (every warp sees the same)
             if (!fine && hc == 0 && tid == 0) atomicOr(p.err, PKV_ERR_BLOCK);
-            shared = false;  // another segment writes this column
+            shared = twice = false;  // another segment writes this column; a lower one has some of these rows
             if (may_share) {
 #pragma unroll 4
                 for (int t = tid; t < p.S; t += kAppend8Threads) {
                     const Segment o = load_segment(p.seq_info, t);
-                    shared |= t != s && o.col == sg.col && new_pages(p, o) > 0;
+                    const bool writes = t != s && new_pages(p, o) > 0;
+                    shared |= writes && o.col == sg.col;
+                    if (PAIR != kPlainRows) twice |= writes && t < s && overlap(o, sg);
                 }
                 shared = __syncthreads_or(shared);
+                if (queries) twice = __syncthreads_or(twice);
             }
         }
         if (!fine) continue;
@@ -460,8 +492,9 @@ __global__ void __launch_bounds__(kAppend8Threads, D == 256 ? 3 : PAIR == kPlain
         __syncthreads();
         if (warp == 0) {
             int pos, row = row_of_slot(sg, tp * kPage + (lane & 15), p.ring_rows, pos), owner = s, from = sg.kend - sg.ql, to = sg.kend;
+            const unsigned taken = queries && twice ? rows_of_lower(p, sg, s, row, lane) : 0u;
             if (lane < kPage) {
-                sRow[0][lane] = row;
+                sRow[0][lane] = taken >> lane & 1u ? -1 : row;
                 sPos[0][lane] = pos;
             }
             if (shared) owner = merge_page_rows(p, sg, tp, lane, row, pos, from, to);
@@ -475,10 +508,11 @@ __global__ void __launch_bounds__(kAppend8Threads, D == 256 ? 3 : PAIR == kPlain
                 sKept = tokens;
             }
         }
-        // Own rows serve q, those of every segment k and v; they are the same but where segments share a column.
+        // Own rows serve q, those of every segment k and v; they are the same but where segments share a column or rows.
+        const bool apart = shared || (queries && twice);
 #pragma unroll 1
-        for (int pass = 0; pass < (shared ? 2 : 1); ++pass) {
-            const int i0 = pass ? nq : 0, i1 = shared && !pass ? nq : items;
+        for (int pass = 0; pass < (apart ? 2 : 1); ++pass) {
+            const int i0 = pass ? nq : 0, i1 = apart && !pass ? nq : items;
             __syncthreads();
             if (pass && sOwner != s) break;
             if constexpr (PAIR != kPlainRows) {
