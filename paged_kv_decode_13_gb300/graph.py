@@ -63,7 +63,10 @@ class DecodeStep:
     as the projections give them: each layer is then norm_rope_append, which
     leaves the turned queries in `q_rot`, and the attention over them, two
     launches (fused does not apply).  The angles are those of the rows'
-    positions in the cache.  A cache held in 4 or 8 bits takes two launches a layer
+    positions in the cache, on every axis of a rope that has several: right for a text alone, not
+    after an image, whose patches take more places in the cache than the text's position moves on.
+    positions=True gives the step `positions`, int32 (rows,) or (rows, axes) as its ropes have
+    them, which the host fills like q (they are part of `step_inputs`; advance leaves them).  A cache held in 4 or 8 bits takes two launches a layer
     as well, three where large bounds share the key ranges; its outputs may be
     bf16 (out_dtype).  The workspace of that merge belongs to the step: a
     capture allocates nothing, and captured steps share no memory.
@@ -81,7 +84,8 @@ class DecodeStep:
                  causal: bool = False, window: int = 0, fused: bool = True, pdl: Optional[bool] = None,
                  flags: int = 0, num_splits: int = 0, with_lse: bool = False, prefetch_next: bool = True,
                  workspace: bool = False, advance: bool = False,
-                 rope: Union[Rope, Sequence[Rope], None] = None, out_dtype: torch.dtype = torch.float32):
+                 rope: Union[Rope, Sequence[Rope], None] = None, out_dtype: torch.dtype = torch.float32,
+                 positions: bool = False):
         dev = cache.k[0].device
         L, Hkv, D = cache.num_layers, cache.kv_heads, cache.head_dim
         self.cache = cache
@@ -98,13 +102,17 @@ class DecodeStep:
         self.rope = None if rope is None else [rope] * L if isinstance(rope, Rope) else list(rope)
         if self.rope is not None and len(self.rope) != L:
             raise ValueError("rope needs one entry per layer")
+        axes = sorted({r.num_axes for r in self.rope or []})
+        if positions and len(axes) != 1:
+            raise ValueError("positions are those of a rope, and every layer's has as many axes")
         row = cache.row_dtype
         spec_in = ([((rows, num_q_heads, D), row)] * L + [((rows, Hkv, D), row)] * (2 * L)
-                   + [((num_segments, 4), torch.int32)])
+                   + ([((rows,) if axes == [1] else (rows, axes[0]), torch.int32)] if positions else []) + [((num_segments, 4), torch.int32)])
         self.inputs, views = _carve(spec_in, dev)
         self.q, self.k_new, self.v_new = views[:L], views[L:2 * L], views[2 * L:3 * L]
-        self.seq_info = views[3 * L]
-        # the per-step part of `inputs` (q, k_new, v_new of every layer): the
+        self.positions = views[3 * L] if positions else None
+        self.seq_info = views[-1]
+        # the per-step part of `inputs` (q, k_new, v_new of every layer, positions): the
         # segment table sits after it
         self.step_inputs = self.inputs[:self.seq_info.data_ptr() - self.inputs.data_ptr()]
         self.advance = advance
@@ -151,7 +159,7 @@ class DecodeStep:
                 flags |= _lib.FLAG_PREFETCH_NEXT  # the next call attends layer + 1 over the same segments
             if self.rope is not None:
                 norm_rope_append(c, layer, self.rope[layer], self.q[layer], self.k_new[layer], self.v_new[layer],
-                                 self.seq_info, self.q_rot[layer], self.err, window=self.window, stream=stream)
+                                 self.seq_info, self.q_rot[layer], self.err, positions=self.positions, window=self.window, stream=stream)
                 attend_varlen(c, layer, self.q_rot[layer], self.seq_info, self.out[layer], self.err, self.max_q_len,
                               self.max_kv, self.scale, self.causal, self.window, lse=self.lse[layer],
                               num_splits=self.num_splits, flags=flags, stream=stream, workspace=self.ws)
