@@ -84,6 +84,10 @@ struct PromptCfg {
 constexpr float kNoScore = -3e38f;  // reference of a row that has seen no key
 constexpr float kPromptLazy = 8.f;  // a reference moves when a score passes it by this (base 2)
 
+// Arrival of the lanes with `by`, without a branch: the warp goes on to instructions that it executes as a whole.
+__device__ __forceinline__ void mbar_arrive_by(bool by, uint64_t *bar) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(smem_u32(bar)), "r"((int)by) : "memory");
+}
 // 32 columns of this thread's TMEM lane; the caller waits (tmem_wait_ld) before it uses them.
 __device__ __forceinline__ void tmem_ld32_async(unsigned taddr, unsigned (&r)[32]) {
     asm volatile(
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(s_free);  // S is in registers: the next one may go over it
+            mbar_arrive_by(lane == 0, s_free);  // S is in registers: the next one may go over it
             // (P's slot: whether the product that read it is done, asked before it is needed; an answer takes 110 cycles)
             const bool p_free = !(used >> slot & 1) || mbar_try_wait(pv_done + slot, (phase >> slot & 1) ^ 1);
             used |= 1u << slot;
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(p_half + slot);
+                    mbar_arrive_by(lane == 0, p_half + slot);
                 }
             }
             {
@@ -665,6 +669,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
 #pragma unroll 1
         for (int c0 = 0; c0 < DP; c0 += 32) {
             unsigned x[32];
+            __syncwarp();  // lanes without a row are ahead of the others' stores; the load is the whole warp's
             tmem_ld32_async(tmem + lane_off + C::kColO + t * DP + c0, x);
             tmem_wait_ld();
             float o[32];

@@ -808,6 +808,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) verify_kernel(const __grid_con
             return;
         }
         float o1[32];
+        __syncwarp();  // lanes without a row are ahead of the others' stores; the loads are the whole warp's
         tmem_ld32(tmem + lane_off + kColO + half * 64 + c0, o);
         tmem_ld32(tmem + lane_off + kColO + 128 + half * 64 + c0, o1);
 #pragma unroll

@@ -618,6 +618,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) wide4_kernel(const __grid_cons
 #pragma unroll 1
             for (int c0 = 0; c0 < 64; c0 += 32) {
                 float o[32], o1[32];
+                __syncwarp();  // lanes without a row are ahead of the others' stores; the loads are the whole warp's
                 tmem_ld32(tmem + lane_off + C::kColO + half * 64 + c0, o);
                 tmem_ld32(tmem + lane_off + C::kColO + 128 + half * 64 + c0, o1);
 #pragma unroll
