@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
             bool todo = lane < SPB;
             int left = 64 * kPromptProbes;
 #pragma unroll 1
-            for (; __any_sync(0xffffffffu, todo); --left) {
+            for (;; --left) {
                 if (todo && (mine < NST || mbar_test_wait(empty + st, ((mine / NST) - 1) & 1))) {
                     todo = false;
                     mbar_expect_tx(full + st, C::kStage);
@@ -396,13 +396,13 @@ __global__ void __launch_bounds__(C::kThreads, 1) prompt_kernel(const __grid_con
                     for (int x = 0; x < C::kCols / 64; ++x)
                         tma_load_3d(to + x * C::kPart, k ? &p.tmap_k : &p.tmap_v, full + st, lane * C::kCols + x * 64, w.h, w.q0 + block * C::kKeys);
                 }
-                if (left == 0 || *sAbort) {
+                if (!__any_sync(0xffffffffu, todo)) break;
+                if (__any_sync(0xffffffffu, left == 0 || *sAbort)) {  // (every lane leaves at the same vote)
                     *sAbort = 1;
                     ok = false;
                     break;
                 }
             }
-            ok = __all_sync(0xffffffffu, ok);
             stages += SPB;  // (some of them copied, where a wait ran out)
         }
     };
