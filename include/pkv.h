@@ -421,7 +421,8 @@ int pkv_attend_varlen(const pkv_cache *cache, int32_t layer,
  * where num_segments prompts of min(max_len, total_rows) rows would be more than 2^31 tiles.
  *
  * Scores are fp32 sums of exact products; softmax weights are rounded to bf16 (each
- * by at most 2^-8 of itself) for the product with V, whose sums are fp32.  A NaN or
+ * by at most 2^-8 of itself) for the product with V, whose sums are fp32, and not for the sum that divides it: a
+ * row that one key dominates comes out as that key's V times 1 - 2^-8 to 1 + 2^-8 at worst.  A NaN or
  * infinity in k or v reaches the rows that see its key and no others (a
  * call that meets one takes longer).  out: fp32, or bf16 with PKV_FLAG_OUT_BF16, 16-byte
  * aligned, [total_rows][q_heads][head_dim], apart from q, k and v.  The launch is a programmatic dependent one,

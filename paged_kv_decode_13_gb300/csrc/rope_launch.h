@@ -20,7 +20,8 @@ constexpr int kAppend8Fill = 6;
 // Rows from which the queries of such a step go through the row kernel, in a launch of their own.  A page's
 // CTA reads every angle again for each head, which is soon slower than the second launch: 32 + 8 heads of 128,
 // one launch against two: 512 rows of one prompt 12.9 / 21.2 us, 1024 rows 23.6 / 23.9, 4096 rows 67 / 51;
-// a row for each of 256 sequences 20.8 / 20.4, 1024 sequences 52 / 38, 4096 228 / 151.
+// a row for each of 256 sequences 20.8 / 20.4, 512 sequences 25.6 / 21.4, 1024 52 / 38, 4096 228 / 151.  (Between 256 and 1024
+// sequences of a row each two launches would be faster: the rule asks for the rows alone, where a prompt and a batch meet.)
 constexpr int kAppend8OwnQ = 1024;
 
 // The append to an 8-bit cache (bf16 rows; head_dim 64, 128 or 256, S > 0).
