@@ -14,7 +14,7 @@
 // CTA an SM stays, dynamic balance without a counter in memory, and the next
 // item's copies and products start while the rows of this one are written.  Which item a number is, one
 // warp finds in the table as it goes along it.  (A CTA for each item that a segment could have at most: 128 prompts
-// of 30 rows where 2048 were allowed 205 us, now 47; one of 4096 beside 63 of 30 rows 308, now 128.)
+// of 30 rows where 2048 were allowed 205 us, now 44; one of 4096 beside 63 of 30 rows 308, now 121.)
 //
 // Roles, meeting on mbarriers only, each walking through the items by itself:
 //   softmax warps (four a tile; thread = row)  read S from TMEM, mask, take the

@@ -32,10 +32,9 @@
 // 16 sequences of up to 8192 keys, 8 kv heads, up to 128 rows each: 65 us with
 // the merge, where the bytes take 12 us, the products (of full tiles) at the
 // measured bf16 rate 19, and the mma.sync tiles 179; in 8 bits 84, the bytes 22 (halves of a lane's
-// two pieces exchanged as codes and masked only in edge pages: 86.5 before).  The tensor cores are 22 %
-// busy, the schedulers 46 %: the softmax warps' 930 issue slots a group of 64
-// keys and sub-partition (convert, maximum, exp2, pack, rescale) are the
-// longest chain.  Registers 128 / 72 (136 / 64 and 144 / 64: the same time), and a
+// two pieces exchanged as codes and masked only in edge pages: 86.5 before).  In 8 bits the tensor cores are 21 %
+// busy, the schedulers 45 %, HBM 28 %: nothing is full, a group's chain of copy, conversion, scores,
+// softmax and product is waited for, and so is the change from piece to piece.  Registers 128 / 72 (136 / 64 and 144 / 64: the same time), and a
 // piece counted as 36 pages (10: 82 us, 24: 73) in the shares.
 // All waits are bounded (kWaitNs); a timeout ends every role, the rows not
 // written yet read zero, and PKV_ERR_TIMEOUT is set.
