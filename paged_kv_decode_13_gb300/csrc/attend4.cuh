@@ -60,6 +60,8 @@ constexpr float kNoMax = -1e30f;       // reference maximum of a row that has se
 // numbers of it (set at the score itself, those below 2^-25 of the largest would vanish from
 // the product with V while the sum still counts them).
 constexpr float kLift4 = 7.f, kLazy4 = 15.f;
+// 8 bits: factors between weights of the sum and of the product with V up to 2^kFar8 (kFactors below).
+constexpr float kFar8 = 120.f, kNoRef = 1e30f;
 
 template <int D_, int NT_, int KW_, int NST_, int PP_, int CTAS_, bool QSH_, int BITS_ = 4>
 struct Cfg4 {
@@ -373,10 +375,15 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
     // ---- the warp's pages
     float acc[NT][KS][4];
     float m_r[NT][2], l_r[NT][2];
-    float w_r[NT][2];  // 8 bits: the reference of the weights of the product with V
+    // Its weights as those of the sum times a factor of the page and row, where no factor is too large for that, or as exponentials of their
+    // own: 32 sequences of 8000 keys at head_dim 64, 8 rows, 54.4 us and 57.0; with more columns a page (one sequence of 300 keys at 128: 7.0 and
+    // 6.8) or more rows (32 of head_dim 128: 39 and 37) asking whether they are costs more than it saves.
+    constexpr bool kFactors = C::BITS == 8 && NT == 1 && D == 64;
+    float g_r[NT][2];  // 8 bits: m_r less the reference of the weights of the product with V (kNoRef: it has none yet)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        m_r[nt][0] = m_r[nt][1] = w_r[nt][0] = w_r[nt][1] = kNoMax;
+        m_r[nt][0] = m_r[nt][1] = kNoMax;
+        g_r[nt][0] = g_r[nt][1] = 0.f;
         l_r[nt][0] = l_r[nt][1] = 0.f;
 #pragma unroll
         for (int i = 0; i < KS; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
@@ -485,7 +492,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
         // Online softmax (base 2) with a lazy maximum: this lane has tokens g,
         // g + 8 of rows 2t, 2t + 1.  x = score - reference; the reference moves
         // only when some x passes kLazy4.  8 bits: a weight of the product is
-        // 2^(score + log2 of the page's V scale), against a reference of its own (w_r, as lazy), so that it keeps its bits
+        // 2^(score + log2 of the page's V scale), against a reference of the row's own (m_r - g_r, as lazy), so that it keeps its bits
         // whatever the scales of pages that the row does not see, or sees with less weight; the sum of weights stays as it is.
         const bool inside = pages == PP && pos_first >= lo_in && pos_first + (PP - 1) * KW * kPage + kPage <= hi_in;
         unsigned pb[PP][NT][2];
@@ -505,18 +512,21 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                         if (e >= pages || key < sLo[r] || key >= sHi[r]) x[e][i] = -CUDART_INF_F;
                     }
             }
-#pragma unroll
-            for (int e = 0; e < PP; ++e) top = fmaxf(top, fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3])));
             float up[PP][2];  // from x to the weight's exponent
             if constexpr (C::BITS == 8) {
 #pragma unroll
                 for (int e = 0; e < PP; ++e)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        up[e][i] = ve[e] + (m_r[nt][i] - w_r[nt][i]);
-                        top = fmaxf(top, fmaxf(x[e][i], x[e][i + 2]) + up[e][i]);
+                        up[e][i] = ve[e] + g_r[nt][i];
+                        top = fmaxf(top, fmaxf(x[e][i], x[e][i + 2]) + fmaxf(up[e][i], 0.f));
+                        if (kFactors) top = fmaxf(top, up[e][i] - (kFar8 - kLazy4));
                     }
+            } else {
+#pragma unroll
+                for (int e = 0; e < PP; ++e) top = fmaxf(top, fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3])));
             }
+            bool far = false;
             if (__any_sync(0xffffffffu, top > kLazy4)) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -528,11 +538,13 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                             if (x[e][i + o] != -CUDART_INF_F) mx = fmaxf(mx, fmaf(sa[e][nt][i + o], sp[e][nt][i], -kLift4));
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    float al = ex2(m_r[nt][i] - mx);
+                    const float m0 = m_r[nt][i];
+                    float al = ex2(m0 - mx);
                     m_r[nt][i] = mx;
                     l_r[nt][i] *= al;
                     if constexpr (C::BITS == 8) {
-                        float wx = w_r[nt][i];
+                        const float g0 = g_r[nt][i], w0 = m0 == kNoMax || g0 == kNoRef ? kNoMax : m0 - g0;
+                        float wx = w0;
 #pragma unroll
                         for (int e = 0; e < PP; ++e)
 #pragma unroll
@@ -540,10 +552,14 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                                 if (x[e][i + o] != -CUDART_INF_F) wx = fmaxf(wx, fmaf(sa[e][nt][i + o], sp[e][nt][i], ve[e] - kLift4));
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) wx = fmaxf(wx, __shfl_xor_sync(0xffffffffu, wx, o));
-                        al = ex2(w_r[nt][i] - wx);
-                        w_r[nt][i] = wx;
+                        const float g = wx != kNoMax ? mx - wx : mx != kNoMax ? kNoRef : 0.f;
+                        al = w0 == kNoMax ? 1.f : ex2((m0 - mx) - (g0 - g));  // (nothing summed yet: zeros, or the NaN of a token)
+                        g_r[nt][i] = g;
 #pragma unroll
-                        for (int e = 0; e < PP; ++e) up[e][i] = ve[e] + (mx - wx);
+                        for (int e = 0; e < PP; ++e) {
+                            up[e][i] = ve[e] + g;
+                            if (kFactors) far |= up[e][i] > kFar8;
+                        }
                     }
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
@@ -556,6 +572,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                         for (int o = 0; o < 4; o += 2)
                             if (x[e][i + o] != -CUDART_INF_F) x[e][i + o] = fmaf(sa[e][nt][i + o], sp[e][nt][i], -mx);
                 }
+                if (kFactors) far = __any_sync(0xffffffffu, far);
             }
 #pragma unroll
             for (int e = 0; e < PP; ++e) {
@@ -563,8 +580,19 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
                 l_r[nt][0] += p00 + p10;
                 l_r[nt][1] += p01 + p11;
                 if constexpr (C::BITS == 8) {
-                    pb[e][nt][0] = transpose8x8(pack_f16x2(ex2(x[e][0] + up[e][0]), ex2(x[e][1] + up[e][1])));
-                    pb[e][nt][1] = transpose8x8(pack_f16x2(ex2(x[e][2] + up[e][0]), ex2(x[e][3] + up[e][1])));
+                    float w[4];
+                    if (!kFactors || far) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = ex2(x[e][i] + up[e][i & 1]);
+                    } else {
+                        const float f0 = ex2(up[e][0]), f1 = ex2(up[e][1]);
+                        w[0] = p00 * f0;
+                        w[1] = p01 * f1;
+                        w[2] = p10 * f0;
+                        w[3] = p11 * f1;
+                    }
+                    pb[e][nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
+                    pb[e][nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
                 } else {
                     pb[e][nt][0] = transpose8x8(pack_f16x2(p00, p01));
                     pb[e][nt][1] = transpose8x8(pack_f16x2(p10, p11));
@@ -698,7 +726,7 @@ __device__ __forceinline__ int attend_piece(const Attend4Params &p, const Smem4<
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) unit[nt][e] = C::BITS == 4 ? 1.f : w_r[nt][e] == kNoMax ? 0.f : ex2(w_r[nt][e] - m_r[nt][e]);
+        for (int e = 0; e < 2; ++e) unit[nt][e] = C::BITS == 4 ? 1.f : m_r[nt][e] == kNoMax || g_r[nt][e] == kNoRef ? 0.f : ex2(-g_r[nt][e]);
     // A row whose scores are all NaN has no maximum: give it one, so that its
     // NaN sum and columns reach the output.
 #pragma unroll
